@@ -59,6 +59,7 @@ enum {
   KVQ_DEV_POS_RANGE = 2u,      /* pos + n_tokens > max_seq_len: the sequence was skipped */
   KVQ_DEV_SEQLEN_RANGE = 4u,   /* seq_lens[b] < 0 or > max_seq_len: treated as empty */
   KVQ_DEV_TIMEOUT = 8u,        /* a copy-pipeline wait gave up after ~1 s: output is incomplete */
+  KVQ_DEV_BAD_NODE = 16u,      /* a tree node's parent is not an earlier node, or a path entry is no node: skipped */
 };
 
 /* ---------------------------------------------------------------- formats */
@@ -283,6 +284,136 @@ size_t kv_prefill_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t b
 int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
                          float* out, const int32_t* pos, int32_t batch, int32_t n_tokens, void* scratch,
                          size_t scratch_bytes, void* stream);
+
+/*
+ * Queries, keys and values out of a fused projection, ready for the entry points above: per-head RMS norm of
+ * queries and keys (where weights are given), rotary position, and the [batch][heads][n_tokens][128] layout
+ * (with n_tokens == 1 that of kv_decode_attention's q).  Computed in fp32, rounded once.
+ *
+ * kv_rope_init fills a plain-data handle (host work only):
+ *   rot_dim      channels that turn, the first of each head: even, 0..128 (0: norm and layout only)
+ *   layout       KVQ_ROPE_HALF: pairs (i, i + rot_dim / 2); KVQ_ROPE_INTERLEAVED: pairs (2i, 2i + 1)
+ *   theta        base > 1; pair i turns by f_i = theta^(-2i / rot_dim) radians per position
+ *   scaling      KVQ_ROPE_PLAIN; KVQ_ROPE_LINEAR: f_i / factor; KVQ_ROPE_NTK: theta scaled by
+ *                factor^(rot_dim / (rot_dim - 2)); KVQ_ROPE_TURNS: f_i keep + f_i / factor (1 - keep) with keep =
+ *                clamp((original_len f_i / 2 pi - low) / (high - low), 0, 1), the turns a pair makes over the
+ *                trained length; KVQ_ROPE_DIMS: the same blend with keep = 1 - clamp((i - a) / max(b - a, 0.001),
+ *                0, 1), a = max(floor(d(high)), 0), b = min(ceil(d(low)), rot_dim - 1), d(r) = rot_dim
+ *                ln(original_len / (2 pi r)) / (2 ln theta)
+ *   factor, original_len, low, high   as the scaling uses them (ignored otherwise)
+ *   attn_factor  multiplies every sine and cosine (1: plain rotation)
+ * Angles are exact at any position (a 64-bit fraction of a turn per position).
+ *
+ * kv_qk_norm_rope (no cache is involved; pointers belong to the current device):
+ *   qkv          device, in_dtype: row r = b n_tokens + t at qkv + r row_stride elements holds the n_q_heads
+ *                query heads, the n_kv_heads key heads, then (when v is given) the n_kv_heads value heads, 128
+ *                channels each; row_stride * element size a multiple of 16
+ *   positions    device int32 [batch][n_tokens]; a negative position marks a padded row: its outputs are left
+ *                as they were
+ *   q_weight, k_weight   device, in_dtype [128], or NULL for no norm; y = x / sqrt(mean(x^2) + eps) * weight
+ *   q            device, in_dtype [batch][n_q_heads][n_tokens][128]; k, v likewise with n_kv_heads; v may be NULL
+ *                (values are then not copied).  Outputs must not overlap qkv.
+ */
+enum { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 };
+enum { KVQ_ROPE_PLAIN = 0, KVQ_ROPE_LINEAR = 1, KVQ_ROPE_NTK = 2, KVQ_ROPE_TURNS = 3, KVQ_ROPE_DIMS = 4 };
+typedef struct kvq_rope {
+  int32_t rot_dim;
+  int32_t layout;
+  float attn_factor;
+  uint32_t magic;       /* set by kv_rope_init */
+  uint64_t turns[64];   /* turn per position of each pair, in units of 2^-64 of a turn */
+} kvq_rope;
+int kv_rope_init(kvq_rope* rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling, double factor,
+                 double original_len, double low, double high, double attn_factor);
+int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, const int32_t* positions,
+                    const void* q_weight, const void* k_weight, float eps, void* q, void* k, void* v, int32_t batch,
+                    int32_t n_tokens, int32_t n_q_heads, int32_t n_kv_heads, int32_t in_dtype, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache: one pass over the cached positions for all nodes, what
+ * speculative decoding verifies a draft with.  Nothing is appended.  Node i of sequence b, at depth d below the
+ * cached context (children of the context have d = 0), sits at position P = seq_lens[b] + d and attends to the
+ * cached positions and to itself and its ancestors among the drafts, as its own single-token step along that
+ * path would: cached positions j <= P - window through their records, the newer ones raw from the ring; drafted
+ * tokens are always raw.
+ *   k, v         device, cfg.in_dtype [L?][batch][n_kv_heads][n_nodes][128]: the drafts' raw keys and values, within
+ *                the range that kv_quant_append takes (nodes that are not there may hold anything)
+ *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_nodes][128]
+ *   out          device, cfg.in_dtype, like q (a float cache's outputs are float, a bf16 cache's bf16: its
+ *                operands are then rounded once to fp16, below the output's own rounding)
+ *   seq_lens     device int32 [batch]: cached tokens, drafts not counted; 0 is an empty context.  Out of range:
+ *                flagged KVQ_DEV_SEQLEN_RANGE, treated as 0
+ *   parents      device int32 [batch][n_nodes]: the parent's index, smaller than the node's own; -1: a child of
+ *                the context; less than -1: the node is not there (a shorter draft in the batch).  Nodes that
+ *                are not there, and nodes below them, give zeros.  A parent >= the node's own index is flagged
+ *                KVQ_DEV_BAD_NODE and the node treated as not there
+ *   n_nodes      1..KVQ_MAX_TREE
+ *   scratch      device, >= kv_tree_scratch_bytes(cache, layer, batch, n_nodes) bytes, any contents; calls that
+ *                share it must not overlap on the GPU
+ * Results do not depend on timing.  May be captured in a CUDA graph once a call of the same cache has run
+ * outside capture.
+ */
+#define KVQ_MAX_TREE 64
+size_t kv_tree_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_nodes);
+int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                      const int32_t* seq_lens, const int32_t* parents, int32_t batch, int32_t n_nodes, void* scratch,
+                      size_t scratch_bytes, void* stream);
+
+/*
+ * Append the accepted path of each sequence's tree: nodes path[b][0 .. n_accept[b]) go to positions pos[b] ..
+ * pos[b] + n_accept[b] - 1, writing exactly the bytes (records and ring) that kv_quant_append of those vectors
+ * writes.
+ *   k, v         as given to kv_tree_attention
+ *   path         device int32 [batch][max_path]: node indices along the path (1 <= max_path <= n_nodes)
+ *   n_accept     device int32 [batch], 0..max_path; 0 (or less) and pos[b] < 0 leave the sequence untouched.  More
+ *                than max_path: flagged KVQ_DEV_BAD_NODE, the sequence untouched; pos[b] + n_accept[b] >
+ *                max_seq_len: flagged KVQ_DEV_POS_RANGE, the sequence untouched; a path entry outside
+ *                0..n_nodes-1: flagged KVQ_DEV_BAD_NODE, that token skipped
+ */
+int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v, const int32_t* path,
+                   const int32_t* n_accept, const int32_t* pos, int32_t batch, int32_t n_nodes, int32_t max_path,
+                   void* stream);
+
+/*
+ * Attention weight that each cached position receives, accumulated for eviction: the n_queries newest tokens'
+ * queries (query t of sequence b at position P = seq_lens[b] - n_queries + t, attending to positions 0..P; P < 0:
+ * the query is ignored) against the cache as it stands -- positions below seq_lens[b] - window through their
+ * records, the rest raw -- and for every position j < seq_lens[b]
+ *   weights[j] = decay weights[j] + sum over the queries and the query heads of the kv-head of softmax(...)_j.
+ * With n_queries == 1 the softmax is that of kv_decode_attention at the same lengths.
+ *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_queries][128], n_queries 1..KVQ_MAX_TREE
+ *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; positions >= seq_lens[b] are left as they were
+ *   decay        0..1; 0 writes without reading what was there
+ *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
+ *   scratch      device, >= kv_weights_scratch_bytes bytes, any contents, not shared by overlapping calls
+ */
+size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries);
+int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* weights, float decay,
+                         const int32_t* seq_lens, int32_t batch, int32_t n_queries, void* scratch, size_t scratch_bytes,
+                         void* stream);
+
+/*
+ * Eviction: cut every sequence longer than ``budget`` to its newest ``recent`` positions and, of the older ones,
+ * the budget - recent with the largest weights (ties to the lowest position; NaN counts below every other value),
+ * separately for each (layer, kv-head), in place.  Kept positions stay in order: position kept[s] moves to slot s,
+ * its record as it is, and the ring is turned to match, so that every entry point above goes on at length budget
+ * (new keys keep their true rotary positions: those are the caller's, see kv_qk_norm_rope).
+ *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; compacted like the records, entries at and
+ *                after ``budget`` left as they were
+ *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
+ *   kept         device int32 [L?][batch][n_kv_heads][budget] (out): the position each slot held; -1 past the end of
+ *                a sequence of fewer than ``budget`` tokens (which is left as it is)
+ *   new_lens     device int32 [batch] (out): min(seq_lens[b], budget); not the same buffer as seq_lens
+ *   budget, recent   window <= recent <= budget <= max_seq_len
+ *   scratch      device, >= kv_evict_scratch_bytes bytes (a copy of the kept records), any contents
+ * All layers of a sequence have to be cut together (layer == -1, or each layer in turn) before its new length is
+ * used.  A page must not be shared by several sequences, or by positions of one, when it is evicted from.  A
+ * block-table entry outside [0, n_pages) is flagged KVQ_DEV_BAD_PAGE: records in it count as zeros, and slots in
+ * it are not written.
+ */
+size_t kv_evict_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget);
+int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
+             int32_t batch, int32_t budget, int32_t recent, void* scratch, size_t scratch_bytes, void* stream);
 
 /*
  * Block codecs next to the cache: the TurboQuant MSE quantiser ([TQ] "key idea" row: random

@@ -13,7 +13,8 @@ from . import lib
 from .lib import (KVQ_IN_BF16, KVQ_IN_F32, KVQ_Q4G32, KVQ_Q8G32, KVQ_TQ3_QJL, kv_cache_bytes,  # noqa: F401
                   kv_cache_init,
                   kv_calibrate, kv_calibrate_scratch_bytes, kv_decode_attention,
-                  kv_decode_scratch_bytes, kv_quant_append, kv_status, kv_strerror, make_config)
+                  kv_decode_scratch_bytes, kv_qk_norm_rope, kv_quant_append, kv_rope_init, kv_status, kv_strerror,
+                  make_config)
 
 
 class QuantKVCache:
@@ -68,6 +69,53 @@ class QuantKVCache:
             self._scratch[key] = t
         lib.kv_prefill_attention(self.handle, layer, k, v, q, out, pos, t, stream)
         return out
+
+    def _kept_scratch(self, key: tuple, size, *args) -> torch.Tensor:
+        """Scratch of size(handle, *args) bytes (at least one), kept per key and reused across calls."""
+        t = self._scratch.get(key)
+        if t is None:
+            t = torch.empty(max(1, size(self.handle, *args)), dtype=torch.uint8, device=self.buffer.device)
+            self._scratch[key] = t
+        return t
+
+    def tree_decode(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor,
+                    parents: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of a tree of drafted tokens (k, v, q; parents [B][N]) over the cache: [L?][B][Hq][N][128]."""
+        if out is None:
+            out = torch.empty_like(q)
+        key = ("tree", layer == -1, q.shape[-4], q.shape[-2])
+        scratch = self._kept_scratch(key, lib.kv_tree_scratch_bytes, layer, q.shape[-4], q.shape[-2])
+        lib.kv_tree_attention(self.handle, layer, k, v, q, out, seq_lens, parents, scratch, stream)
+        return out
+
+    def commit(self, layer: int, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor, n_accept: torch.Tensor,
+               pos: torch.Tensor, stream=None):
+        """Append the accepted path of each sequence's tree at pos (see lib.kv_tree_commit)."""
+        lib.kv_tree_commit(self.handle, layer, k, v, path, n_accept, pos, stream)
+
+    def attention_weights(self, layer: int, q: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
+                          decay: float = 1.0, stream=None) -> torch.Tensor:
+        """Add the attention weight that cached positions receive from the newest tokens' queries to ``weights``."""
+        key = ("weights", layer == -1, q.shape[-4], q.shape[-2])
+        scratch = self._kept_scratch(key, lib.kv_weights_scratch_bytes, layer, q.shape[-4], q.shape[-2])
+        lib.kv_attention_weights(self.handle, layer, q, weights, decay, seq_lens, scratch, stream)
+        return weights
+
+    def evict(self, layer: int, weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, recent: int,
+              kept: torch.Tensor | None = None, new_lens: torch.Tensor | None = None, stream=None):
+        """Cut every sequence to ``budget`` positions by weight; returns (kept, new_lens)."""
+        if kept is None:
+            kept = torch.empty(tuple(weights.shape[:-1]) + (budget,), dtype=torch.int32, device=weights.device)
+        if new_lens is None:
+            new_lens = torch.empty_like(seq_lens)
+        batch = seq_lens.shape[0]
+        # a copy of the kept records: one buffer, as large as the largest call so far
+        need = lib.kv_evict_scratch_bytes(self.handle, layer, batch, budget)
+        scratch = self._scratch.get("evict")
+        if scratch is None or scratch.numel() < need:
+            scratch = self._scratch["evict"] = torch.empty(max(1, need), dtype=torch.uint8, device=self.buffer.device)
+        lib.kv_evict(self.handle, layer, weights, seq_lens, kept, new_lens, budget, recent, scratch, stream)
+        return kept, new_lens
 
     def status(self) -> int:
         return kv_status(self.handle)

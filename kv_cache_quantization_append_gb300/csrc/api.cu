@@ -427,6 +427,178 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
   return cuda_err(launch_prefill(a, ap, static_cast<cudaStream_t>(stream)));
 }
 
+int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v, const int32_t* path,
+                   const int32_t* n_accept, const int32_t* pos, int32_t batch, int32_t n_nodes, int32_t max_path,
+                   void* stream) {
+  Layout L;
+  int rc = check_cache(cache, &L);
+  if (rc != KVQ_OK) return rc;
+  if (!k || !v || !path || !n_accept || !pos) return KVQ_ERR_INVALID_ARG;
+  if (batch < 1 || batch > cache->cfg.max_batch || n_nodes < 1 || n_nodes > KVQ_MAX_TREE) return KVQ_ERR_INVALID_ARG;
+  if (max_path < 1 || max_path > n_nodes) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(path) || !aligned16(n_accept) || !aligned16(pos)) return KVQ_ERR_ALIGN;
+  int l0, nl;
+  if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  AppendArgs a;
+  a.p = dev_ptrs(*cache, L);
+  a.L = L;
+  a.block_table = cache->block_table;
+  a.k = k;
+  a.v = v;
+  a.pos = pos;
+  a.layer0 = l0;
+  a.n_layers_call = nl;
+  a.batch = batch;
+  a.Hkv = cache->cfg.n_kv_heads;
+  a.W = cache->cfg.window;
+  a.max_seq_len = cache->cfg.max_seq_len;
+  a.k_format = cache->cfg.k_format;
+  a.sinkhorn = cache->cfg.sinkhorn;
+  a.in_bf16 = cache->cfg.in_dtype == KVQ_IN_BF16;
+  a.max_batch = cache->cfg.max_batch;
+  CommitArgs c;
+  c.path = path;
+  c.n_accept = n_accept;
+  c.n_nodes = n_nodes;
+  c.max_path = max_path;
+  return cuda_err(launch_commit(a, c, static_cast<cudaStream_t>(stream)));
+}
+
+// what kv_tree_attention and kv_attention_weights share: the cache, the queries' shape and the layers of the call
+static int multi_args(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n, MultiArgs* a) {
+  Layout L;
+  int rc = check_cache(cache, &L);
+  if (rc != KVQ_OK) return rc;
+  if (batch < 1 || batch > cache->cfg.max_batch || n < 1 || n > KVQ_MAX_TREE) return KVQ_ERR_INVALID_ARG;
+  int l0, nl;
+  if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
+  *a = MultiArgs{};
+  a->p = dev_ptrs(*cache, L);
+  a->L = L;
+  a->block_table = cache->block_table;
+  a->layer0 = l0;
+  a->n_layers_call = nl;
+  a->batch = batch;
+  a->max_batch = cache->cfg.max_batch;
+  a->Hkv = cache->cfg.n_kv_heads;
+  a->g = cache->cfg.n_q_heads / cache->cfg.n_kv_heads;
+  a->W = cache->cfg.window;
+  a->n = n;
+  a->k_format = cache->cfg.k_format;
+  a->sinkhorn = cache->cfg.sinkhorn;
+  a->in_bf16 = cache->cfg.in_dtype == KVQ_IN_BF16;
+  a->max_pages_per_seq = cache->max_pages_per_seq;
+  a->max_seq_len = cache->cfg.max_seq_len;
+  return KVQ_OK;
+}
+
+size_t kv_tree_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_nodes) {
+  MultiArgs a;
+  if (multi_args(cache, layer, batch, n_nodes, &a) != KVQ_OK) return 0;
+  return std::max<size_t>(256, tree_scratch_bytes(a));
+}
+
+int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                      const int32_t* seq_lens, const int32_t* parents, int32_t batch, int32_t n_nodes, void* scratch,
+                      size_t scratch_bytes, void* stream) {
+  MultiArgs a;
+  int rc = multi_args(cache, layer, batch, n_nodes, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!k || !v || !q || !out || !seq_lens || !parents || !scratch) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(out) || !aligned16(seq_lens) || !aligned16(parents) ||
+      !aligned16(scratch))
+    return KVQ_ERR_ALIGN;
+  if (scratch_bytes < kv_tree_scratch_bytes(cache, layer, batch, n_nodes)) return KVQ_ERR_CAPACITY;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.out = out;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.scratch = static_cast<uint8_t*>(scratch);
+  return cuda_err(launch_tree(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries) {
+  MultiArgs a;
+  if (multi_args(cache, layer, batch, n_queries, &a) != KVQ_OK) return 0;
+  return std::max<size_t>(256, weights_scratch_bytes(a));
+}
+
+int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* weights, float decay,
+                         const int32_t* seq_lens, int32_t batch, int32_t n_queries, void* scratch, size_t scratch_bytes,
+                         void* stream) {
+  MultiArgs a;
+  int rc = multi_args(cache, layer, batch, n_queries, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!q || !weights || !seq_lens || !scratch) return KVQ_ERR_INVALID_ARG;
+  if (!(decay >= 0.f) || !(decay <= 1.f)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(weights) || !aligned16(seq_lens) || !aligned16(scratch)) return KVQ_ERR_ALIGN;
+  if (scratch_bytes < kv_weights_scratch_bytes(cache, layer, batch, n_queries)) return KVQ_ERR_CAPACITY;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.q = q;
+  a.weights = weights;
+  a.decay = decay;
+  a.seq_lens = seq_lens;
+  a.scratch = static_cast<uint8_t*>(scratch);
+  return cuda_err(launch_weights(a, static_cast<cudaStream_t>(stream)));
+}
+
+static int evict_args(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget, EvictArgs* a) {
+  Layout L;
+  int rc = check_cache(cache, &L);
+  if (rc != KVQ_OK) return rc;
+  if (batch < 1 || batch > cache->cfg.max_batch || budget < 1 || budget > cache->cfg.max_seq_len) return KVQ_ERR_INVALID_ARG;
+  int l0, nl;
+  if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
+  const long long units = (long long)nl * batch * cache->cfg.n_kv_heads;
+  if (units > 0x7fffffffLL / 32) return KVQ_ERR_UNSUPPORTED;
+  *a = EvictArgs{};
+  a->p = dev_ptrs(*cache, L);
+  a->L = L;
+  a->block_table = cache->block_table;
+  a->layer0 = l0;
+  a->batch = batch;
+  a->max_batch = cache->cfg.max_batch;
+  a->Hkv = cache->cfg.n_kv_heads;
+  a->W = cache->cfg.window;
+  a->k_format = cache->cfg.k_format;
+  a->max_pages_per_seq = cache->max_pages_per_seq;
+  a->max_seq_len = cache->cfg.max_seq_len;
+  a->budget = budget;
+  a->n_units = (int)units;
+  a->n_halves = (budget + HALF - 1) / HALF;
+  return KVQ_OK;
+}
+
+size_t kv_evict_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget) {
+  EvictArgs a;
+  if (evict_args(cache, layer, batch, budget, &a) != KVQ_OK) return 0;
+  return std::max<size_t>(256, evict_scratch_bytes(a.n_units, budget, a.L.half_bytes));
+}
+
+int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
+             int32_t batch, int32_t budget, int32_t recent, void* scratch, size_t scratch_bytes, void* stream) {
+  EvictArgs a;
+  int rc = evict_args(cache, layer, batch, budget, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!weights || !seq_lens || !kept || !new_lens || !scratch || new_lens == seq_lens) return KVQ_ERR_INVALID_ARG;
+  if (recent < 0 || recent < cache->cfg.window || recent > budget) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(weights) || !aligned16(seq_lens) || !aligned16(kept) || !aligned16(new_lens) || !aligned16(scratch))
+    return KVQ_ERR_ALIGN;
+  if (scratch_bytes < kv_evict_scratch_bytes(cache, layer, batch, budget)) return KVQ_ERR_CAPACITY;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.weights = weights;
+  a.seq_lens = seq_lens;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.images = static_cast<uint8_t*>(scratch);
+  a.recent = recent;
+  return cuda_err(launch_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream) {
   Layout L;
   int rc = check_cache(cache, &L);

@@ -99,12 +99,12 @@ __device__ __forceinline__ void q8_encode_key(const float (&y)[4], int lane, int
 
 constexpr int VPW = 4;  // vectors (consecutive tokens) per warp: their loads are issued together
 
-// encode one vector (lane holds channels 4*lane..+3 of the raw input) into its page and ring slot
+// encode one vector (lane holds channels 4*lane..+3 of the raw input) into its page and, where `raw`
+// (the last `window` tokens of the sequence's share of the call), its ring slot
 __device__ __forceinline__ void encode_vector(const AppendArgs& a, int lane, int kv, int layer, int b, int h,
-                                              int t, int p, float4 xin) {
+                                              bool raw, int p, float4 xin) {
   const int H = a.Hkv;
-  // raw copy into the window ring for the last `window` tokens of this call
-  if (a.W > 0 && t >= a.T - a.W) {
+  if (raw) {
     float* ring = kv ? a.p.ringv : a.p.ringk;
     const size_t slot = (size_t)(p % a.W);
     float* dst = ring + ((((size_t)layer * a.max_batch + b) * H + h) * a.W + slot) * D + 4 * lane;
@@ -192,7 +192,7 @@ __device__ __forceinline__ void append_warps_body(const AppendArgs& a) {
     if (j < nv) x[j] = load4_in(kv ? a.v : a.k, (vec0 + j) * D + 4 * lane, a.in_bf16);
 #pragma unroll
   for (int j = 0; j < VPW; ++j)
-    if (j < nv) encode_vector(a, lane, kv, layer, b, h, t0 + j, p0 + t0 + j, x[j]);
+    if (j < nv) encode_vector(a, lane, kv, layer, b, h, a.W > 0 && t0 + j >= a.T - a.W, p0 + t0 + j, x[j]);
 }
 
 // As append_bulk_kernel: launched for the values of a TurboQuant-key append (AFTER_KEYS) as a
@@ -225,11 +225,11 @@ struct TqKey {
 
 // Ring copy, page lookup, rotation, norm, codes and residual of one key vector; the residual
 // (channels 4 lane .. +3) goes to rs[4 lane ..].
-__device__ __forceinline__ TqKey tq_key_prepare(const AppendArgs& a, int lane, int layer, int b, int h, int t, int p,
+__device__ __forceinline__ TqKey tq_key_prepare(const AppendArgs& a, int lane, int layer, int b, int h, bool raw, int p,
                                                 float4 xin, float* rs) {
   TqKey k{nullptr, p % HALF, 0u, 0.f, 0.f};
   const int H = a.Hkv;
-  if (a.W > 0 && t >= a.T - a.W) {
+  if (raw) {
     float* dst = a.p.ringk + ((((size_t)layer * a.max_batch + b) * H + h) * a.W + (size_t)(p % a.W)) * D + 4 * lane;
     *reinterpret_cast<float4*>(dst) = xin;
   }
@@ -264,8 +264,29 @@ __device__ __forceinline__ TqKey tq_key_prepare(const AppendArgs& a, int lane, i
   return k;
 }
 
-template <int VPW>
-__global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const AppendArgs a) {
+// The token range of sequence b in a commit of accepted tree nodes: n nodes path[b][0 .. n) go to positions
+// p0 .. p0 + n - 1; false (nothing to do, or flagged by the warp with `flag`) leaves the sequence alone.
+__device__ __forceinline__ bool commit_range(const AppendArgs& a, const CommitArgs& c, int b, bool flag, int& p0, int& n) {
+  p0 = a.pos[b];
+  n = c.n_accept[b];
+  if (p0 < 0 || n <= 0) return false;
+  if (n > c.max_path || (long long)p0 + n > a.max_seq_len) {
+    if (flag) atomicOr(a.p.status, n > c.max_path ? KVQ_DEV_BAD_NODE : KVQ_DEV_POS_RANGE);
+    return false;
+  }
+  return true;
+}
+__device__ __forceinline__ int commit_node(const AppendArgs& a, const CommitArgs& c, int b, int t, bool flag) {
+  const int node = c.path[(size_t)b * c.max_path + t];
+  if (node >= 0 && node < c.n_nodes) return node;
+  if (flag) atomicOr(a.p.status, KVQ_DEV_BAD_NODE);
+  return -1;
+}
+
+// COMMIT: the vectors are accepted tree nodes (one per warp), read through the path and ranged per sequence
+template <int VPW, bool COMMIT>
+__global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const AppendArgs a, const CommitArgs c) {
+  static_assert(!COMMIT || VPW == 1, "a node's position in the path is its own");
   extern __shared__ __align__(16) float tq_smem[];
   const float* sT = tq_smem;  // [j][i] = S[i][j]
   const int lane = threadIdx.x & 31, wl = threadIdx.x >> 5;
@@ -296,15 +317,21 @@ __global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const App
     const int b = (int)(rest % a.batch);
     const int ll = (int)(rest / a.batch);
     const int layer = a.layer0 + ll;
-    const int p0 = a.pos[b];
-    if (p0 < 0) continue;  // sequence not part of this append
-    if ((long long)p0 + a.T > a.max_seq_len) {
-      if (lane == 0 && tq == 0 && h == 0) atomicOr(a.p.status, KVQ_DEV_POS_RANGE);
-      continue;
-    }
     const int t0 = tq * VPW;
-    const int nv = min(VPW, a.T - t0);
-    const size_t vec0 = (((size_t)ll * a.batch + b) * a.Hkv + h) * a.T + t0;
+    int p0, T = a.T, node = t0;
+    if (COMMIT) {
+      if (!commit_range(a, c, b, lane == 0 && tq == 0 && h == 0, p0, T) || t0 >= T) continue;
+      if ((node = commit_node(a, c, b, t0, lane == 0 && h == 0)) < 0) continue;
+    } else {
+      p0 = a.pos[b];
+      if (p0 < 0) continue;  // sequence not part of this append
+      if ((long long)p0 + a.T > a.max_seq_len) {
+        if (lane == 0 && tq == 0 && h == 0) atomicOr(a.p.status, KVQ_DEV_POS_RANGE);
+        continue;
+      }
+    }
+    const int nv = COMMIT ? 1 : min(VPW, a.T - t0);
+    const size_t vec0 = (((size_t)ll * a.batch + b) * a.Hkv + h) * (COMMIT ? c.n_nodes : a.T) + node;
     float4 x[VPW];
 #pragma unroll
     for (int v = 0; v < VPW; ++v)
@@ -313,7 +340,7 @@ __global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const App
 #pragma unroll
     for (int v = 0; v < VPW; ++v) {
       if (v < nv) {
-        key[v] = tq_key_prepare(a, lane, layer, b, h, t0 + v, p0 + t0 + v, x[v], rs + v * D);
+        key[v] = tq_key_prepare(a, lane, layer, b, h, a.W > 0 && t0 + v >= T - a.W, p0 + t0 + v, x[v], rs + v * D);
       } else {
         key[v] = TqKey{nullptr, 0, 0u, 0.f, 0.f};
         *reinterpret_cast<float4*>(rs + v * D + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -376,6 +403,32 @@ __global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const App
   }
 }
 
+// Commit of accepted tree nodes: append_kernel with the vector's source read through the path and the token
+// range of each sequence its own; one vector per warp (paths are a few nodes, so what counts is how soon all
+// vectors are under way).  Same encoding, same bytes.
+__global__ void __launch_bounds__(WARPS * 32) commit_kernel(const AppendArgs a, const CommitArgs c) {
+  const int lane = threadIdx.x & 31;
+  const unsigned total = (unsigned)a.n_layers_call * a.batch * a.Hkv * c.max_path * a.kv_n;
+  const unsigned wid = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  if (wid >= total) return;
+  const int kv = a.kv_lo + (int)(wid % a.kv_n);
+  unsigned rest = wid / a.kv_n;
+  const int t = (int)(rest % c.max_path);
+  rest /= c.max_path;
+  const int h = (int)(rest % a.Hkv);
+  rest /= a.Hkv;
+  const int b = (int)(rest % a.batch);
+  const int ll = (int)(rest / a.batch);
+  int p0, n;
+  const bool flag = lane == 0 && h == 0 && kv == a.kv_lo;
+  if (!commit_range(a, c, b, flag && t == 0, p0, n) || t >= n) return;
+  const int node = commit_node(a, c, b, t, flag);
+  if (node < 0) return;
+  const size_t vec = (((size_t)ll * a.batch + b) * a.Hkv + h) * c.n_nodes + node;
+  encode_vector(a, lane, kv, a.layer0 + ll, b, h, a.W > 0 && t >= n - a.W, p0 + t,
+                load4_in(kv ? a.v : a.k, vec * D + 4 * lane, a.in_bf16));
+}
+
 }  // namespace
 
 cudaError_t launch_append_warps(const AppendArgs& a, cudaStream_t s, bool after_keys) {
@@ -395,10 +448,10 @@ cudaError_t launch_append_warps(const AppendArgs& a, cudaStream_t s, bool after_
   return after_keys ? cudaLaunchKernelEx(&cfg, append_kernel<true>, a) : cudaLaunchKernelEx(&cfg, append_kernel<false>, a);
 }
 
-cudaError_t launch_append_tq_keys(const AppendArgs& a, cudaStream_t s) {
+cudaError_t launch_append_tq_keys(const AppendArgs& a, cudaStream_t s, const CommitArgs* commit = nullptr) {
   // a warp projects TQ_VPW vectors of a sequence at a time; appends of fewer tokens per sequence
   // (the decode step's one token) one vector per warp, so that no lane computes empty slots
-  const int vpw = a.T >= TQ_VPW ? TQ_VPW : 1;
+  const int vpw = a.T >= TQ_VPW && !commit ? TQ_VPW : 1;
   const long long warps = (long long)a.n_layers_call * a.batch * a.Hkv * ((a.T + vpw - 1) / vpw);
   if (warps <= 0) return cudaSuccess;
   if (warps > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -406,15 +459,35 @@ cudaError_t launch_append_tq_keys(const AppendArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(vpw == TQ_VPW ? (const void*)append_tq_keys_kernel<TQ_VPW> : (const void*)append_tq_keys_kernel<1>,
+    e = cudaFuncSetAttribute(commit          ? (const void*)append_tq_keys_kernel<1, true>
+                             : vpw == TQ_VPW ? (const void*)append_tq_keys_kernel<TQ_VPW, false>
+                                             : (const void*)append_tq_keys_kernel<1, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TQ_SMEM);
   if (e != cudaSuccess) return e;
   // the projection is loaded once per CTA: at most two CTAs per SM, each looping over warp groups
   const long long want = (warps + TQ_WARPS - 1) / TQ_WARPS;
   const long long cap = 2LL * (sms > 0 ? sms : 1);
   const unsigned grid = (unsigned)(want < cap ? want : cap);
-  if (vpw == TQ_VPW) append_tq_keys_kernel<TQ_VPW><<<grid, TQ_WARPS * 32, TQ_SMEM, s>>>(a);
-  else append_tq_keys_kernel<1><<<grid, TQ_WARPS * 32, TQ_SMEM, s>>>(a);
+  if (commit) append_tq_keys_kernel<1, true><<<grid, TQ_WARPS * 32, TQ_SMEM, s>>>(a, *commit);
+  else if (vpw == TQ_VPW) append_tq_keys_kernel<TQ_VPW, false><<<grid, TQ_WARPS * 32, TQ_SMEM, s>>>(a, CommitArgs{});
+  else append_tq_keys_kernel<1, false><<<grid, TQ_WARPS * 32, TQ_SMEM, s>>>(a, CommitArgs{});
+  return cudaGetLastError();
+}
+
+cudaError_t launch_commit(const AppendArgs& a0, const CommitArgs& c, cudaStream_t s) {
+  AppendArgs a = a0;
+  a.T = c.max_path;
+  a.kv_lo = 0;
+  a.kv_n = 2;
+  if (a.k_format == KVQ_TQ3_QJL) {
+    const cudaError_t e = launch_append_tq_keys(a, s, &c);
+    if (e != cudaSuccess) return e;
+    a.kv_lo = 1;
+    a.kv_n = 1;
+  }
+  const long long warps = (long long)a.n_layers_call * a.batch * a.Hkv * c.max_path * a.kv_n;
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidValue;
+  commit_kernel<<<(unsigned)((warps + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(a, c);
   return cudaGetLastError();
 }
 

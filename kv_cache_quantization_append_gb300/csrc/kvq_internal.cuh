@@ -76,6 +76,12 @@ struct AppendArgs {
   int kv_lo, kv_n;  // vectors handled by one launch: K (0) and/or V (1), kv_lo .. kv_lo + kv_n - 1
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+struct CommitArgs {         // accepted nodes of drafted trees: AppendArgs::k, v are [L?][batch][Hkv][n_nodes][128]
+  const int32_t* path;      // [batch][max_path] node of each step
+  const int32_t* n_accept;  // [batch]
+  int n_nodes, max_path;
+};
+cudaError_t launch_commit(const AppendArgs& a, const CommitArgs& c, cudaStream_t s);
 // after_keys: the values of a TurboQuant-key append, launched right after the keys kernel as its
 // programmatic dependent (the two overlap; the values grid ends after the keys grid)
 cudaError_t launch_append_bulk(const AppendArgs& a, cudaStream_t s, bool after_keys = false);
@@ -126,6 +132,44 @@ struct PrefillArgs {
 };
 size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W);
 cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStream_t s);
+
+struct EvictArgs {
+  DevPtrs p;
+  Layout L;
+  const int32_t* block_table;
+  float* weights;           // [L?][batch][Hkv][max_seq_len]
+  const int32_t* seq_lens;
+  int32_t* kept;            // [L?][batch][Hkv][budget]
+  int32_t* new_lens;        // [batch]
+  uint8_t* images;          // scratch: [n_units][n_halves][half_bytes]
+  int layer0, batch, max_batch, Hkv, W, k_format, max_pages_per_seq, max_seq_len;
+  int budget, recent, n_units, n_halves;
+};
+size_t evict_scratch_bytes(int n_units, int budget, int half_bytes);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
+// Attention of several queries per sequence over the cache as it stands: the nodes of drafted trees (their
+// own raw keys and values behind the cached ones) or the newest tokens' queries (weights only)
+struct MultiArgs {
+  DevPtrs p;
+  Layout L;
+  const int32_t* block_table;
+  const void* k;            // tree: [L?][batch][Hkv][n][128] cfg.in_dtype, the drafts' raw keys
+  const void* v;
+  const void* q;            // [L?][batch][Hq][n][128]
+  void* out;                // tree: like q
+  float* weights;           // weights: [L?][batch][Hkv][max_seq_len]
+  float decay;
+  const int32_t* seq_lens;
+  const int32_t* parents;   // tree: [batch][n]
+  uint8_t* scratch;
+  int layer0, n_layers_call, batch, max_batch, Hkv, g, W, n, k_format, sinkhorn, in_bf16;
+  int max_pages_per_seq, max_seq_len;
+};
+size_t tree_scratch_bytes(const MultiArgs& a);
+cudaError_t launch_tree(const MultiArgs& a, cudaStream_t s);
+size_t weights_scratch_bytes(const MultiArgs& a);
+cudaError_t launch_weights(const MultiArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__

@@ -28,13 +28,20 @@ DEV_BAD_PAGE = 1
 DEV_POS_RANGE = 2
 DEV_SEQLEN_RANGE = 4
 DEV_TIMEOUT = 8
+DEV_BAD_NODE = 16
+
+MAX_TREE = 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_TURNS, ROPE_DIMS = range(5)
 
 EXPORTS = ("kv_cache_bytes", "kv_cache_init", "kv_calibrate_scratch_bytes", "kv_calibrate",
            "kv_quant_append", "kv_decode_scratch_bytes", "kv_decode_attention",
            "kv_decode_attention_noalloc", "kv_prefill_scratch_bytes", "kv_prefill_attention",
            "kv_tbq_block_bytes", "kv_tbq_encode", "kv_tbq_decode", "kv_split_record_bytes",
            "kv_split_outliers", "kv_split_encode", "kv_split_decode", "kv_status", "kv_set_wait_limit_ns",
-           "kv_strerror")
+           "kv_strerror", "kv_rope_init", "kv_qk_norm_rope", "kv_tree_scratch_bytes", "kv_tree_attention",
+           "kv_tree_commit", "kv_weights_scratch_bytes", "kv_attention_weights", "kv_evict_scratch_bytes",
+           "kv_evict")
 NOALLOC_SCRATCH_MAX = 32 * 1024 * 1024
 
 
@@ -55,6 +62,11 @@ class kvq_cache(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("device", ctypes.c_int32), ("magic", ctypes.c_uint32)]
 
 
+class kvq_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("attn_factor", ctypes.c_float),
+                ("magic", ctypes.c_uint32), ("turns", ctypes.c_uint64 * 64)]
+
+
 class KVQError(RuntimeError):
     pass
 
@@ -72,6 +84,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I32, SZ, U32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint32)
     cfgp, cachep = ctypes.POINTER(kvq_config), ctypes.POINTER(kvq_cache)
+    ropep, I64, F32, F64 = ctypes.POINTER(kvq_rope), ctypes.c_int64, ctypes.c_float, ctypes.c_double
     sig = {
         "kv_cache_bytes": (SZ, [cfgp]),
         "kv_cache_init": (ctypes.c_int, [cachep, cfgp, P, SZ, P, P, P]),
@@ -93,6 +106,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kv_status": (ctypes.c_int, [cachep, U32P, P]),
         "kv_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
         "kv_strerror": (ctypes.c_char_p, [ctypes.c_int]),
+        "kv_rope_init": (ctypes.c_int, [ropep, I32, I32, F64, I32, F64, F64, F64, F64, F64]),
+        "kv_qk_norm_rope": (ctypes.c_int, [ropep, P, I64, P, P, P, F32, P, P, P, I32, I32, I32, I32, I32, P]),
+        "kv_tree_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
+        "kv_tree_attention": (ctypes.c_int, [cachep, I32, P, P, P, P, P, P, I32, I32, P, SZ, P]),
+        "kv_tree_commit": (ctypes.c_int, [cachep, I32, P, P, P, P, P, I32, I32, I32, P]),
+        "kv_weights_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
+        "kv_attention_weights": (ctypes.c_int, [cachep, I32, P, P, F32, P, I32, I32, P, SZ, P]),
+        "kv_evict_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
+        "kv_evict": (ctypes.c_int, [cachep, I32, P, P, P, P, I32, I32, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -266,6 +288,137 @@ def kv_prefill_attention(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch
     _check(load().kv_prefill_attention(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(q), _ptr(out),
                                        _ptr(pos), B, T, _ptr(scratch), scratch.numel() * scratch.element_size(),
                                        _stream(stream)))
+
+
+def kv_rope_init(rot_dim: int, layout: int = ROPE_HALF, theta: float = 10000.0, scaling: int = ROPE_PLAIN,
+                 factor: float = 1.0, original_len: float = 0.0, low: float = 0.0, high: float = 0.0,
+                 attn_factor: float = 1.0) -> kvq_rope:
+    """The rotary positions' handle (host data; see include/kvq.h for the scalings)."""
+    rope = kvq_rope()
+    _check(load().kv_rope_init(ctypes.byref(rope), rot_dim, layout, theta, scaling, factor, original_len, low, high,
+                               attn_factor))
+    return rope
+
+
+def kv_qk_norm_rope(rope: kvq_rope, qkv: torch.Tensor, positions: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                    v: torch.Tensor | None, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                    eps: float = 1e-6, stream=None):
+    """qkv: [B][T][>= (Hq + 2 Hkv) * 128] (rows of one stride; Hkv once less where v is None); positions: int32 [B][T];
+    q: [B][Hq][T][128], k, v: [B][Hkv][T][128] (written; without the T axis where T is 1, as kv_decode_attention takes
+    q); weights [128], all of qkv's dtype."""
+    dt = _in_dtype_of(qkv)
+    if qkv.dim() != 3 or positions.dtype != torch.int32:
+        raise KVQError("qkv must be [B][T][row] and positions int32")
+    B, T, row = qkv.shape
+    sb, st, s1 = qkv.stride()
+    if row > 1 and s1 != 1 or T > 1 and B > 1 and sb != T * st:
+        raise KVQError("qkv's rows must be contiguous and of one stride")
+    st = st if T > 1 else sb if B > 1 else row
+    if q.dim() != 4 and not (T == 1 and q.dim() == 3) or k.dim() != q.dim():
+        raise KVQError(f"q and k must be [B][heads][T][128], got {tuple(q.shape)} and {tuple(k.shape)}")
+    hq, hkv = q.shape[1], k.shape[1]
+    tail = (T, 128) if q.dim() == 4 else (128,)
+    _check_shape("q", q, (B, hq) + tail)
+    _check_shape("k", k, (B, hkv) + tail)
+    _check_shape("positions", positions, (B, T))
+    if v is not None:
+        _check_shape("v", v, tuple(k.shape))
+    if row < (hq + (1 if v is None else 2) * hkv) * 128:
+        raise KVQError(f"qkv rows hold {row} values, fewer than their heads")
+    for w in (q_weight, k_weight):
+        if w is not None:
+            _check_shape("weight", w, (128,))
+    for x in (q, k, v, q_weight, k_weight):
+        if x is not None and x.dtype != qkv.dtype:
+            raise KVQError(f"dtype {x.dtype} does not match qkv's ({qkv.dtype})")
+    if not qkv.is_cuda:
+        raise KVQError("device tensor expected")
+    _check(load().kv_qk_norm_rope(ctypes.byref(rope), ctypes.c_void_p(qkv.data_ptr()), st, _ptr(positions), _ptr(q_weight),
+                                  _ptr(k_weight), eps, _ptr(q), _ptr(k), _ptr(v), B, T, hq, hkv, dt, _stream(stream)))
+
+
+def kv_tree_scratch_bytes(cache: kvq_cache, layer: int, batch: int, n_nodes: int) -> int:
+    return int(load().kv_tree_scratch_bytes(ctypes.byref(cache), layer, batch, n_nodes))
+
+
+def kv_tree_attention(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
+                      out: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, scratch: torch.Tensor,
+                      stream=None):
+    """k, v: [L?][B][Hkv][N][128]; q: [L?][B][Hq][N][128]; out like q, in the cache's input dtype; seq_lens: int32 [B];
+    parents: int32 [B][N]; scratch: device bytes, at least kv_tree_scratch_bytes."""
+    if seq_lens.dtype != torch.int32 or parents.dtype != torch.int32:
+        raise KVQError("seq_lens and parents must be int32")
+    _check_in_dtype(cache, k, v, q, out)
+    B, N = _check_append_shapes(cache, layer, k, v, seq_lens)
+    lead = (_layers_in_call(cache, layer),) if layer == -1 else ()
+    _check_shape("q", q, lead + (B, cache.cfg.n_q_heads, N, 128))
+    _check_shape("out", out, tuple(q.shape))
+    _check_shape("parents", parents, (B, N))
+    _check(load().kv_tree_attention(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(q), _ptr(out), _ptr(seq_lens),
+                                    _ptr(parents), B, N, _ptr(scratch), scratch.numel() * scratch.element_size(),
+                                    _stream(stream)))
+
+
+def kv_tree_commit(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor,
+                   n_accept: torch.Tensor, pos: torch.Tensor, stream=None):
+    """k, v: [L?][B][Hkv][N][128] (the tree's); path: int32 [B][P] node indices; n_accept, pos: int32 [B]."""
+    if path.dtype != torch.int32 or n_accept.dtype != torch.int32 or pos.dtype != torch.int32:
+        raise KVQError("path, n_accept and pos must be int32")
+    _check_in_dtype(cache, k, v)
+    B, N = _check_append_shapes(cache, layer, k, v, pos)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise KVQError(f"path must be [{B}][max_path], got {tuple(path.shape)}")
+    _check_shape("n_accept", n_accept, (B,))
+    _check(load().kv_tree_commit(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(path), _ptr(n_accept), _ptr(pos), B, N,
+                                 path.shape[1], _stream(stream)))
+
+
+def kv_weights_scratch_bytes(cache: kvq_cache, layer: int, batch: int, n_queries: int) -> int:
+    return int(load().kv_weights_scratch_bytes(ctypes.byref(cache), layer, batch, n_queries))
+
+
+def _check_weights(cache: kvq_cache, layer: int, batch: int, weights: torch.Tensor):
+    lead = (_layers_in_call(cache, layer),) if layer == -1 else ()
+    if weights.dtype != torch.float32:
+        raise KVQError("weights must be float32")
+    _check_shape("weights", weights, lead + (batch, cache.cfg.n_kv_heads, cache.cfg.max_seq_len))
+
+
+def kv_attention_weights(cache: kvq_cache, layer: int, q: torch.Tensor, weights: torch.Tensor, decay: float,
+                         seq_lens: torch.Tensor, scratch: torch.Tensor, stream=None):
+    """q: [L?][B][Hq][T][128], the newest T tokens' queries; weights: float32 [L?][B][Hkv][max_seq_len] (updated);
+    seq_lens: int32 [B]; scratch: device bytes, at least kv_weights_scratch_bytes."""
+    if seq_lens.dtype != torch.int32:
+        raise KVQError("seq_lens must be int32")
+    _check_in_dtype(cache, q)
+    if q.dim() != (5 if layer == -1 else 4):
+        raise KVQError(f"q must be {'[L][B][Hq][T][128]' if layer == -1 else '[B][Hq][T][128]'}, got {tuple(q.shape)}")
+    B, T = q.shape[-4], q.shape[-2]
+    lead = (_layers_in_call(cache, layer),) if layer == -1 else ()
+    _check_shape("q", q, lead + (B, cache.cfg.n_q_heads, T, 128))
+    _check_shape("seq_lens", seq_lens, (B,))
+    _check_weights(cache, layer, B, weights)
+    _check(load().kv_attention_weights(ctypes.byref(cache), layer, _ptr(q), _ptr(weights), decay, _ptr(seq_lens), B, T,
+                                       _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
+
+
+def kv_evict_scratch_bytes(cache: kvq_cache, layer: int, batch: int, budget: int) -> int:
+    return int(load().kv_evict_scratch_bytes(ctypes.byref(cache), layer, batch, budget))
+
+
+def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torch.Tensor, kept: torch.Tensor,
+             new_lens: torch.Tensor, budget: int, recent: int, scratch: torch.Tensor, stream=None):
+    """weights: float32 [L?][B][Hkv][max_seq_len] (compacted); seq_lens: int32 [B]; kept: int32 [L?][B][Hkv][budget] and
+    new_lens: int32 [B] (written); scratch: device bytes, at least kv_evict_scratch_bytes."""
+    if seq_lens.dtype != torch.int32 or kept.dtype != torch.int32 or new_lens.dtype != torch.int32:
+        raise KVQError("seq_lens, kept and new_lens must be int32")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _check_shape("seq_lens", seq_lens, (B,))
+    _check_shape("new_lens", new_lens, (B,))
+    _check_weights(cache, layer, B, weights)
+    _check_shape("kept", kept, tuple(weights.shape[:-1]) + (budget,))
+    _check(load().kv_evict(ctypes.byref(cache), layer, _ptr(weights), _ptr(seq_lens), _ptr(kept), _ptr(new_lens), B, budget,
+                           recent, _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
 def _in_dtype_of(t: torch.Tensor) -> int:
