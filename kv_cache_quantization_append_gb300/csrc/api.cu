@@ -496,7 +496,7 @@ static int multi_args(const kvq_cache* cache, int32_t layer, int32_t batch, int3
 size_t kv_tree_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_nodes) {
   MultiArgs a;
   if (multi_args(cache, layer, batch, n_nodes, &a) != KVQ_OK) return 0;
-  return std::max<size_t>(256, tree_scratch_bytes(a));
+  return std::max<size_t>(256, tree_scratch_bytes(a, decode_ctas(cache->device)));
 }
 
 int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q, void* out,
@@ -518,7 +518,9 @@ int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void
   a.seq_lens = seq_lens;
   a.parents = parents;
   a.scratch = static_cast<uint8_t*>(scratch);
-  return cuda_err(launch_tree(a, static_cast<cudaStream_t>(stream)));
+  const int sms = decode_ctas(cache->device);
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  return cuda_err(launch_tree(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries) {

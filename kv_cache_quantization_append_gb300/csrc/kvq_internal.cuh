@@ -166,8 +166,8 @@ struct MultiArgs {
   int layer0, n_layers_call, batch, max_batch, Hkv, g, W, n, k_format, sinkhorn, in_bf16;
   int max_pages_per_seq, max_seq_len;
 };
-size_t tree_scratch_bytes(const MultiArgs& a);
-cudaError_t launch_tree(const MultiArgs& a, cudaStream_t s);
+size_t tree_scratch_bytes(const MultiArgs& a, int sms);
+cudaError_t launch_tree(const MultiArgs& a, int sms, cudaStream_t s);
 size_t weights_scratch_bytes(const MultiArgs& a);
 cudaError_t launch_weights(const MultiArgs& a, cudaStream_t s);
 

@@ -306,11 +306,20 @@ cudaError_t launch_tree_kf(const MultiArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t tree_scratch_bytes(const MultiArgs&) { return 256; }
-cudaError_t launch_tree(const MultiArgs& a, cudaStream_t s) {
-  return a.k_format == KVQ_TQ3_QJL ? launch_tree_kf<KVQ_TQ3_QJL>(a, s)
-         : a.k_format == KVQ_Q8G32 ? launch_tree_kf<KVQ_Q8G32>(a, s)
-                                   : launch_tree_kf<KVQ_Q4G32>(a, s);
+size_t tree_scratch_q4(const MultiArgs& a, int sms);
+size_t tree_scratch_q8(const MultiArgs& a, int sms);
+size_t tree_scratch_tq3(const MultiArgs& a, int sms);
+cudaError_t launch_tree_q4(const MultiArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_tree_q8(const MultiArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_tree_tq3(const MultiArgs& a, int sms, cudaStream_t s);
+
+size_t tree_scratch_bytes(const MultiArgs& a, int sms) {
+  return a.k_format == KVQ_TQ3_QJL ? tree_scratch_tq3(a, sms) : a.k_format == KVQ_Q8G32 ? tree_scratch_q8(a, sms) : tree_scratch_q4(a, sms);
+}
+cudaError_t launch_tree(const MultiArgs& a, int sms, cudaStream_t s) {
+  return a.k_format == KVQ_TQ3_QJL ? launch_tree_tq3(a, sms, s)
+         : a.k_format == KVQ_Q8G32 ? launch_tree_q8(a, sms, s)
+                                   : launch_tree_q4(a, sms, s);
 }
 size_t weights_scratch_bytes(const MultiArgs& a) {
   return align256((size_t)a.n_layers_call * a.batch * a.Hkv * a.n * a.g * sizeof(float));
