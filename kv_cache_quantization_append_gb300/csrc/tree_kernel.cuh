@@ -3,21 +3,23 @@
 // A unit's rows (query heads of its nodes, node-major: row = node * g + head) are the N side of the products and
 // its positions the M side, so that the tensor cores do work for the rows there are (16 to 64 a CTA, more rows in
 // further CTAs) and a position's scales and norms belong to one thread:
-//   S^T [128 positions x N rows]  = K~ [128 x 128] Q~^T         (tcgen05.mma, both operands in shared memory)
-//   O^T [128 channels x N rows] += V~^T [128 x 128] P^T
-// in the quantised records' space (rotated, balanced), where K~ and V~ are the dequantised records, or the window's
-// and the drafts' raw vectors taken there once by the first kernel.  The softmax runs in base 2 down a thread's own
-// columns against a reference per row that moves only when a logit passes it by 8 (weights stay below 2^8 in fp16):
-// no exchange between threads but one vote per tile.
+//   S^T [128 positions x N rows]  = K~ [128 x 128] Q~^T         (tcgen05.mma, K~ in tensor memory, Q~ in shared)
+//   O^T [128 channels x N rows] += V~^T [128 x 128] P^T         (both in shared memory)
+// where K~ and V~ are the dequantised records and Q~ the queries in the records' space (rotated, balanced), or the
+// window's and the drafts' raw vectors and the queries as they are.  The softmax runs in base 2 down a thread's own columns against a
+// reference per row that moves only when a logit passes it by 8 (weights stay below 2^8 in fp16): no exchange between
+// threads but one vote per tile.
 //
-// Three launches, each the programmatic dependent of the one before:
-//  1. tree_prep_kernel: rotated queries (and their QJL projections) as operand images, the raw tiles' images, and
-//     every node's ancestors and depth.
-//  2. tree_kernel: the tiles of all units in one list, cut into equal ranges, one per CTA (stream-K).  All warps of a
+// Two launches:
+//  1. tree_kernel: the tiles of all units in one list, cut into equal ranges, one per CTA (stream-K).  Eight warps of a
 //     CTA dequantise K~, then V~ while the tensor cores run the logits, then take the softmax, then go on to the next
-//     K~ while the tensor cores run P V: the CUDA cores never wait for the products, and two CTAs an SM fill each
-//     other's barriers.  A range's part of a unit ends as one partial record (reference, sum, O).
-//  3. tree_merge_kernel: joins a row's records in a fixed order, undoes the balancing and the rotation.
+//     K~ while the tensor cores run P V; a ninth issues the products (issuing them costs a warp about as long as they
+//     take, which the others would all wait for).  Two CTAs an SM fill each other's waits.  A range's part of a unit's
+//     records, and of its raw positions, ends as one partial record (reference, sum, O).
+//  2. tree_merge_kernel (a programmatic dependent): joins a row's records in a fixed order, undoes the balancing and
+//     the rotation.
+// Rotating the queries and following the parents is done again by every CTA that needs them: a kernel in front that did
+// it once cost 6 us of latency.
 //
 // Operands: bf16 caches take each of K~, V~, Q~ and P rounded once to fp16 (2^-11, an eighth of the bf16 output's own
 // rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys need
@@ -32,8 +34,10 @@ namespace tree {
 
 using namespace tc;
 
-constexpr int TILE = 128;     // positions per tile = MMA M
-constexpr int THREADS = 256;
+constexpr int TILE = 128;  // positions per tile = MMA M
+constexpr int WORKERS = 256;   // two threads to a position
+constexpr int WARPS = WORKERS / 32;
+constexpr int THREADS = WORKERS + 32;  // and the warp that issues the products
 constexpr int MAX_ROWS = 64;  // rows per CTA
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
@@ -41,12 +45,8 @@ constexpr float NO_REF = -1e30f;  // reference of a row that has met no position
 // what the launches share: sizes from the host, pointers into the caller's scratch
 struct Plan {
   MultiArgs a;
-  int rb, N, n_units, G, raw_tiles;  // row blocks of N rows per unit, units (with row blocks), CTAs, raw tiles at most
-  int q_image, raw_image;            // bytes: of a row block's queries, of one raw tile (K then V)
-  unsigned long long* anc;           // [batch][n] ancestors-or-self, 0: not there
-  uint8_t* q_images;                 // [n_units][q_image]
-  uint8_t* raw_images;               // [n_units / rb][raw_tiles][raw_image]
-  float* records;                    // [n_units + G][2 N + 128 N]
+  int rb, N, n_units, G;  // row blocks of N rows per unit, units (with row blocks), CTAs
+  float* records;         // [2 n_units + G][2 N + 128 N]: range c's part of unit u's records (+ 0) or raw positions (+ 1) at 2 u + c
 };
 
 __host__ __device__ inline int raw_count(int L, int W, int n) { return (W > 0 ? (L < W - 1 ? L : W - 1) : 0) + n; }
@@ -56,19 +56,23 @@ __host__ __device__ inline int quant_end(int L, int W, int n) {
   const int e = L - W + n;
   return e < 0 ? 0 : e > L ? L : e;
 }
-__device__ __forceinline__ int seq_len(const MultiArgs& a, int b) {
-  const int L = a.seq_lens[b];
-  return L < 0 || L > a.max_seq_len ? 0 : L;
-}
 __device__ __forceinline__ int seq_tiles(const MultiArgs& a, int L) {
   return (quant_end(L, a.W, a.n) + TILE - 1) / TILE + (raw_count(L, a.W, a.n) + TILE - 1) / TILE;
 }
-// warp 0: exclusive prefix of the sequences' tiles, [batch + 1]
-__device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* pre) {
+// warp 0: the sequences' lengths (0 where out of range) and the exclusive prefix of their tiles, [batch + 1]
+__device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* lens, int* pre, bool flag) {
   const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
   const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
   int s = 0;
-  for (int b = b0; b < b1; ++b) s += seq_tiles(a, seq_len(a, b));
+  for (int b = b0; b < b1; ++b) {
+    int L = a.seq_lens[b];
+    if (L < 0 || L > a.max_seq_len) {
+      if (flag) atomicOr(a.p.status, KVQ_DEV_SEQLEN_RANGE);
+      L = 0;
+    }
+    lens[b] = L;
+    s += seq_tiles(a, L);
+  }
   int incl = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -78,9 +82,13 @@ __device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* pre) {
   int run = incl - s;
   for (int b = b0; b < b1; ++b) {
     pre[b] = run;
-    run += seq_tiles(a, seq_len(a, b));
+    run += seq_tiles(a, lens[b]);
   }
   if (lane == 31) pre[a.batch] = incl;
+}
+// n / d of numbers that usually fit 32 bits
+__device__ __forceinline__ long long quick_div(long long n, long long d) {
+  return ((unsigned long long)n | (unsigned long long)d) < 0x80000000ull ? (long long)((unsigned)n / (unsigned)d) : n / d;
 }
 
 template <int KF, bool F32>
@@ -89,162 +97,43 @@ struct Cfg {
   static constexpr int PL = F32 ? 2 : 1;            // fp16 planes per value
   static constexpr int KD = TQ ? 256 : 128;         // width of a query image: [q~] or [q~, S q~]
   static constexpr uint32_t PLANE = TILE * D * 2;   // 32 KB
-  // place of channel c within its group of eight, for the key side (values: always nibble_place)
-  __host__ __device__ static constexpr int k_place(int c) { return KF == KVQ_Q4G32 ? nibble_place(c) : c; }
 };
 
 // byte offset of (row, k) in a K-major operand of R rows
 __host__ __device__ constexpr uint32_t km_off(int row, int k, int R) {
   return (uint32_t)((k >> 3) * (R >> 3) * 128 + (row >> 3) * 128 + (row & 7) * 16 + (k & 7) * 2);
 }
-// byte offset of (m, k) in an M-major operand of 128 m
-__host__ __device__ constexpr uint32_t mm_off(int m, int k) {
-  return (uint32_t)((k >> 3) * 2048 + (m >> 3) * 128 + (k & 7) * 16 + (m & 7) * 2);
+// byte offset of (n, k) in an N-major (or M-major) operand of R n, and of (m, k) where they are 128
+__host__ __device__ constexpr uint32_t mn_off(int n, int k, int R) {
+  return (uint32_t)((k >> 3) * (R >> 3) * 128 + (n >> 3) * 128 + (k & 7) * 16 + (n & 7) * 2);
 }
+__host__ __device__ constexpr uint32_t mm_off(int m, int k) { return mn_off(m, k, D); }
 
-// ------------------------------------------------------------------ 1. prep
-template <int KF, bool F32>
-__global__ void __launch_bounds__(THREADS) tree_prep_kernel(const __grid_constant__ Plan p) {
-  using C = Cfg<KF, F32>;
-  constexpr int RPW = C::TQ ? 4 : 1;  // query rows per warp: a pass over the projection serves four
-  const MultiArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;");
-  if ((int)blockIdx.x < a.batch) {
-    // ancestors of every node of one sequence
-    __shared__ int par[KVQ_MAX_TREE];
-    const int b = blockIdx.x, i = threadIdx.x;
-    if (i < a.n) par[i] = a.parents[(size_t)b * a.n + i];
-    if (i == 0) {
-      const int L = a.seq_lens[b];
-      if (L < 0 || L > a.max_seq_len) atomicOr(a.p.status, KVQ_DEV_SEQLEN_RANGE);
-    }
-    __syncthreads();
-    if (i < a.n) {
-      unsigned long long m = 0;
-      for (int j = i; j >= 0;) {
-        m |= 1ull << j;
-        const int q = par[j];
-        if (q < -1 || q >= j) {
-          if (q >= j) atomicOr(a.p.status, KVQ_DEV_BAD_NODE);
-          m = 0;
-          break;
-        }
-        j = q;
-      }
-      p.anc[(size_t)b * a.n + i] = m;
-    }
-    return;
-  }
-  const long long item = (long long)(blockIdx.x - a.batch) * (THREADS / 32) + warp;
-  const int H = a.Hkv, B = a.batch, rows = a.n * a.g;
-  const long long q_items = (long long)p.n_units * (p.N / RPW);
-  const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
-  // is node i of sequence b there? (its chain of parents, two to a lane, walked by the whole warp)
-  auto there = [&](int b, int i) {
-    const int* par = a.parents + (size_t)b * a.n;
-    const int lo = lane < a.n ? par[lane] : -2, hi = lane + 32 < a.n ? par[lane + 32] : -2;
-    for (int j = i; j >= 0;) {
-      const int x = __shfl_sync(FULL, lo, j & 31), y = __shfl_sync(FULL, hi, j & 31);
-      const int q = j < 32 ? x : y;
-      if (q < -1 || q >= j) return false;
-      j = q;
-    }
-    return true;
-  };
-  if (item < q_items) {
-    const int u = (int)(item / (p.N / RPW)), r0 = (int)(item % (p.N / RPW)) * RPW;
-    const int rbi = u % p.rb, h = (u / p.rb) % H, b = (u / (p.rb * H)) % B, ll = u / (p.rb * H * B);
-    uint8_t* img = p.q_images + (size_t)u * p.q_image;
-    float y[RPW][4];
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-      const int row = rbi * p.N + r0 + r, node = row / a.g;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < rows && there(b, node))  // a node that is not there may hold anything
-        x = load4_in(a.q, ((((size_t)ll * B + b) * H * a.g + (size_t)h * a.g + row % a.g) * a.n + node) * D + 4 * lane, a.in_bf16);
-      y[r][0] = x.x * sg.x;
-      y[r][1] = x.y * sg.y;
-      y[r][2] = x.z * sg.z;
-      y[r][3] = x.w * sg.w;
-      hadamard_warp(y[r][0], y[r][1], y[r][2], y[r][3], lane);
-      const __half* sig = a.p.sigk + ((size_t)(a.layer0 + ll) * H + h) * D + 4 * lane;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[r][e] *= C_WHT * LOGIT_SCALE;
-        if (a.sinkhorn) y[r][e] *= __half2float(sig[e]);
-      }
-    }
-    const auto put = [&](int r, int c, float v) {
-      const __half hi = __float2half_rn(v);
-      const uint32_t off = km_off(r, (c & ~7) + C::k_place(c & 7), p.N);
-      *reinterpret_cast<__half*>(img + off) = hi;
-      if (F32) *reinterpret_cast<__half*>(img + p.N * C::KD * 2 + off) = __float2half_rn(v - __half2float(hi));
-    };
-#pragma unroll
-    for (int r = 0; r < RPW; ++r)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) put(r0 + r, 4 * lane + e, y[r][e]);
-    if (C::TQ) {
-      // projections 4 lane .. + 3 of S q~ (the stored projection is transposed: row j is column j of S)
-      float acc[RPW][4] = {};
-#pragma unroll 4
-      for (int j = 0; j < D; j += 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 s4 = *reinterpret_cast<const float4*>(a.p.qjl_t + (j + e) * D + 4 * lane);
-#pragma unroll
-          for (int r = 0; r < RPW; ++r) {
-            const float qj = __shfl_sync(FULL, y[r][e], j >> 2);
-            acc[r][0] += s4.x * qj;
-            acc[r][1] += s4.y * qj;
-            acc[r][2] += s4.z * qj;
-            acc[r][3] += s4.w * qj;
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < RPW; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) put(r0 + r, D + 4 * lane + e, acc[r][e]);
-    }
-    return;
-  }
-  // raw vectors: x = 0 .. 128 raw_tiles - 1 of each unit's list, K and V
-  const long long rest = item - q_items;
-  const int per_unit = p.raw_tiles * TILE;
-  const long long vec = rest >> 1;
-  if (vec >= (long long)(p.n_units / p.rb) * per_unit) return;
-  const int kv = (int)(rest & 1), x = (int)(vec % per_unit), u = (int)(vec / per_unit);
-  const int h = u % H, b = (u / H) % B, ll = u / (H * B), layer = a.layer0 + ll;
-  const int L = seq_len(a, b), nraw = raw_count(L, a.W, a.n), nring = nraw - a.n;
-  if (x >= (nraw + TILE - 1) / TILE * TILE) return;  // a tile that this sequence does not have
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (x < nring) {
-    const float* ring = kv ? a.p.ringv : a.p.ringk;
-    w = *reinterpret_cast<const float4*>(ring + ((((size_t)layer * a.max_batch + b) * H + h) * a.W + (L - nring + x) % a.W) * D + 4 * lane);
-  } else if (x < nraw && there(b, x - nring)) {
-    w = load4_in(kv ? a.v : a.k, ((((size_t)ll * B + b) * H + h) * a.n + x - nring) * D + 4 * lane, a.in_bf16);
-  }
-  float y[4] = {w.x * sg.x, w.y * sg.y, w.z * sg.z, w.w * sg.w};
-  hadamard_warp(y[0], y[1], y[2], y[3], lane);
-  const __half* sig = (kv ? a.p.sigv : a.p.sigk) + ((size_t)layer * H + h) * D + 4 * lane;
-  uint8_t* img = p.raw_images + ((size_t)u * p.raw_tiles + x / TILE) * p.raw_image + (kv ? C::PL * C::PLANE : 0);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float v = y[e] * C_WHT;
-    if (a.sinkhorn) v = __fdiv_rn(v, __half2float(sig[e]));
-    const int c = 4 * lane + e, t = x % TILE;
-    const uint32_t off = kv ? mm_off((c & ~7) + nibble_place(c & 7), t) : km_off(t, (c & ~7) + C::k_place(c & 7), TILE);
-    const __half hi = __float2half_rn(v);
-    *reinterpret_cast<__half*>(img + off) = hi;
-    if (F32) *reinterpret_cast<__half*>(img + C::PLANE + off) = __float2half_rn(v - __half2float(hi));
-  }
+// Four channels (4 lane .. + 3) of a vector held by a warp, as the 8 bytes that belong at 8 (lane & 1) of their
+// 16-byte group: in order, or in the order in which nibbles() leaves eight codes
+template <bool NIBBLE_ORDER>
+__device__ __forceinline__ uint2 pack4(float y0, float y1, float y2, float y3, int lane) {
+  const uint32_t a = h2u(__floats2half2_rn(y0, y1)), b = h2u(__floats2half2_rn(y2, y3));
+  if (!NIBBLE_ORDER) return make_uint2(a, b);
+  const bool odd = lane & 1;
+  const uint32_t r = __shfl_xor_sync(FULL, odd ? a : b, 1);
+  // even: (c0 c4)(c1 c5), odd: (c2 c6)(c3 c7)
+  return odd ? make_uint2(__byte_perm(r, b, 0x5410), __byte_perm(r, b, 0x7632))
+             : make_uint2(__byte_perm(a, r, 0x5410), __byte_perm(a, r, 0x7632));
+}
+__device__ __forceinline__ float lo_part(float v) { return v - __half2float(__float2half_rn(v)); }
+// store the four channels to a plane and, with F32, their lo parts to the next
+template <bool NIBBLE_ORDER, bool F32>
+__device__ __forceinline__ void put4(uint8_t* dst, uint32_t plane, const float (&y)[4], int lane) {
+  *reinterpret_cast<uint2*>(dst) = pack4<NIBBLE_ORDER>(y[0], y[1], y[2], y[3], lane);
+  if (F32)
+    *reinterpret_cast<uint2*>(dst + plane) =
+        pack4<NIBBLE_ORDER>(lo_part(y[0]), lo_part(y[1]), lo_part(y[2]), lo_part(y[3]), lane);
 }
 
 // ------------------------------------------------------------------ dequantising
-// one tile's words of this thread: keys of position t = tid & 127 (half tid >> 7 of its record), values of the
-// position pair vp and rows 2 vr, 2 vr + 1
+// one tile's words of this thread: keys of position t = tid & 127 (half hf of its record), values of the position pair
+// vp and rows 2 vr, 2 vr + 1
 template <int KF>
 struct Words {
   uint4 k[KF == KVQ_Q8G32 ? 4 : 2];
@@ -260,18 +149,22 @@ struct Lane {
 __device__ __forceinline__ Lane lane_of(int tid) {
   // values: 8 consecutive lanes write 8 distinct 16-byte slots of their core matrices (the odd rows' lanes take the odd
   // position of the pair first)
-  return {tid & 127, tid >> 7, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3};
+  return {tid & 127, (tid >> 7) & 1, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3};
 }
 
-// physical pages of a tile (-1: out of range or past the end)
+// physical pages of a tile, as the block table has them (-1: past the end)
 struct Pages {
   int p[2];
+  __device__ __forceinline__ int of(bool second, int n_pages) const {
+    const int x = second ? p[1] : p[0];
+    return x < n_pages ? x : -1;
+  }
 };
 
 template <int KF>
 __device__ __forceinline__ void load_k(const MultiArgs& a, const uint8_t* unit_pages, size_t page_stride, const Pages& pg,
                                        const Lane& ln, Words<KF>& w) {
-  const int tt = ln.t & 31, phys = ln.t & 64 ? pg.p[1] : pg.p[0];
+  const int tt = ln.t & 31, phys = pg.of(ln.t & 64, a.L.n_pages);
 #pragma unroll
   for (int i = 0; i < (KF == KVQ_Q8G32 ? 4 : 2); ++i) w.k[i] = make_uint4(0u, 0u, 0u, 0u);
   w.km = make_uint4(0u, 0u, 0u, 0u);
@@ -297,7 +190,7 @@ __device__ __forceinline__ void load_k(const MultiArgs& a, const uint8_t* unit_p
 template <int KF>
 __device__ __forceinline__ void load_v(const MultiArgs& a, const uint8_t* unit_pages, size_t page_stride, const Pages& pg,
                                        const Lane& ln, Words<KF>& w) {
-  const int phys = ln.vp & 32 ? pg.p[1] : pg.p[0], pp = ln.vp & 15;
+  const int phys = pg.of(ln.vp & 32, a.L.n_pages), pp = ln.vp & 15;
 #pragma unroll
   for (int i = 0; i < 2; ++i) w.v[i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -318,12 +211,11 @@ __device__ __forceinline__ void load_v(const MultiArgs& a, const uint8_t* unit_p
 __device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
 
-// eight codes of a word times scale plus zero, as one 16-byte chunk (and its lo part)
+// eight codes of a word times scale plus zero (and, with F32, their lo parts)
 template <bool F32>
-__device__ __forceinline__ void put_nibbles(uint8_t* dst, uint32_t plane, uint32_t word, uint32_t s2, uint32_t z2) {
+__device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2, uint4& o, uint4& l) {
   __half2 c[4];
   nibbles(word, c);
-  uint4 o, l;
   if (!F32) {
     o.x = h2u(__hfma2(c[0], u2h(s2), u2h(z2)));
     o.y = h2u(__hfma2(c[1], u2h(s2), u2h(z2)));
@@ -336,35 +228,32 @@ __device__ __forceinline__ void put_nibbles(uint8_t* dst, uint32_t plane, uint32
     split2(z + s * f1.x, z + s * f1.y, o.y, l.y);
     split2(z + s * f2.x, z + s * f2.y, o.z, l.z);
     split2(z + s * f3.x, z + s * f3.y, o.w, l.w);
-    *reinterpret_cast<uint4*>(dst + plane) = l;
   }
-  *reinterpret_cast<uint4*>(dst) = o;
 }
 
-// keys of the thread's position (TQ3: the exact centroids)
+// keys of the thread's position to its tensor-memory lane, 64 columns a plane (TQ3: the exact centroids)
 template <int KF, bool F32>
-__device__ __forceinline__ void put_k(uint8_t* kb, const Lane& ln, const Words<KF>& w, const uint4& cent) {
-  constexpr uint32_t PLANE = Cfg<KF, F32>::PLANE;
-  uint8_t* dst = kb + km_off(ln.t, 0, TILE);
+__device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const Words<KF>& w, const uint4& cent) {
   if (KF == KVQ_Q4G32) {
     const uint32_t sc[2] = {w.km.x, w.km.y}, zr[2] = {w.km.z, w.km.w};
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
       const uint32_t s2 = G & 1 ? dup_hi(sc[G >> 1]) : dup_lo(sc[G >> 1]), z2 = G & 1 ? dup_hi(zr[G >> 1]) : dup_lo(zr[G >> 1]);
+      uint4 o[2], l[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t word = G == 0 ? w.k[i].x : G == 1 ? w.k[i].y : G == 2 ? w.k[i].z : w.k[i].w;
-        put_nibbles<F32>(dst + (4 * G + 2 * ln.hf + i) * 2048, PLANE, word, s2, z2);
-      }
+      for (int i = 0; i < 2; ++i)
+        dequant8<F32>(G == 0 ? w.k[i].x : G == 1 ? w.k[i].y : G == 2 ? w.k[i].z : w.k[i].w, s2, z2, o[i], l[i]);
+      tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
+      if (F32) tm_st8(col + 64 + 16 * G + 8 * ln.hf, l[0], l[1]);
     }
   } else if (KF == KVQ_Q8G32) {
     const __half2 off = u2h(0x64806480u);  // 1024 + 128
 #pragma unroll
     for (int wi = 0; wi < 4; ++wi) {
       const uint32_t s2 = wi & 2 ? dup_hi(w.kx) : dup_lo(w.kx);
+      uint32_t o[8], l[8];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        uint32_t o[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t word = wi == 0 ? w.k[i].x : wi == 1 ? w.k[i].y : wi == 2 ? w.k[i].z : w.k[i].w;
@@ -372,50 +261,57 @@ __device__ __forceinline__ void put_k(uint8_t* kb, const Lane& ln, const Words<K
           if (F32) {
             const float d = __low2float(u2h(s2));
             const float2 f = __half22float2(c);
-            split2(d * f.x, d * f.y, o[i], l[i]);
+            split2(d * f.x, d * f.y, o[4 * x + i], l[4 * x + i]);
           } else {
-            o[i] = h2u(__hmul2(c, u2h(s2)));
+            o[4 * x + i] = h2u(__hmul2(c, u2h(s2)));
           }
         }
-        uint8_t* at = dst + (2 * (4 * ln.hf + wi) + x) * 2048;
-        *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
-        if (F32) *reinterpret_cast<uint4*>(at + PLANE) = make_uint4(l[0], l[1], l[2], l[3]);
       }
+      const uint32_t at = col + 32 * ln.hf + 8 * wi;
+      tm_st8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
+      if (F32) tm_st8(at + 64, make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]));
     }
   } else {
     // the eight centroids' bytes in two register pairs (low bytes: cent.x, .y; high bytes: cent.z, .w), picked by
     // byte permutes with the codes as selectors
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4& q = w.k[i >> 2];
-      const uint32_t word = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-      const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
-      const uint32_t l0 = __byte_perm(cent.x, cent.y, sel), h0 = __byte_perm(cent.z, cent.w, sel);
-      const uint32_t l1 = __byte_perm(cent.x, cent.y, sel >> 16), h1 = __byte_perm(cent.z, cent.w, sel >> 16);
-      *reinterpret_cast<uint4*>(dst + (8 * ln.hf + i) * 2048) =
-          make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140), __byte_perm(l1, h1, 0x7362));
+    for (int i = 0; i < 8; i += 2) {
+      uint4 o[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint4& q = w.k[i >> 2];
+        const uint32_t word = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
+        const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
+        const uint32_t l0 = __byte_perm(cent.x, cent.y, sel), h0 = __byte_perm(cent.z, cent.w, sel);
+        const uint32_t l1 = __byte_perm(cent.x, cent.y, sel >> 16), h1 = __byte_perm(cent.z, cent.w, sel >> 16);
+        o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                          __byte_perm(l1, h1, 0x7362));
+      }
+      tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
     }
   }
 }
 
 // TQ3: the signs of the residual's projections, exactly +-1 (bit 6: projection 2j, bit 7: 2j + 1; set: +1)
-__device__ __forceinline__ void put_signs(uint8_t* kb, const Lane& ln, const Words<KVQ_TQ3_QJL>& w) {
-  uint8_t* dst = kb + km_off(ln.t, 0, TILE);
+__device__ __forceinline__ void put_signs(uint32_t col, const Lane& ln, const Words<KVQ_TQ3_QJL>& w) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4& q = w.k[i >> 2];
-    const uint32_t hi = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    const uint32_t lo = hi << 1;  // bit 6 of each byte to its top
-    uint32_t o[4];
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t o[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // bytes 1 and 3: all ones where the bit is set (a permute that spreads the sign bit)
-      const uint32_t sel = (uint32_t)((8 + k) << 4) | (uint32_t)((12 + k) << 12);
-      uint32_t m;
-      asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(lo), "r"(hi), "r"(sel));
-      o[k] = 0xBC00BC00u ^ (m & 0x80008000u);
+    for (int x = 0; x < 2; ++x) {
+      const uint4& q = w.k[i >> 2];
+      const uint32_t hi = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
+      const uint32_t lo = hi << 1;  // bit 6 of each byte to its top
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // bytes 1 and 3: all ones where the bit is set (a permute that spreads the sign bit)
+        const uint32_t sel = (uint32_t)((8 + k) << 4) | (uint32_t)((12 + k) << 12);
+        uint32_t m;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(lo), "r"(hi), "r"(sel));
+        o[4 * x + k] = 0xBC00BC00u ^ (m & 0x80008000u);
+      }
     }
-    *reinterpret_cast<uint4*>(dst + (8 * ln.hf + i) * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+    tm_st8(col + 32 * ln.hf + 4 * i, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
   }
 }
 
@@ -424,97 +320,120 @@ template <int KF, bool F32>
 __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const Words<KF>& w, int left) {
   constexpr uint32_t PLANE = Cfg<KF, F32>::PLANE;
   const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;  // (records there may hold anything)
+  uint8_t* base = vb + mm_off(8 * ln.vr, 2 * ln.vp);
 #pragma unroll
-  for (int G = 0; G < 4; ++G) {
-    const uint32_t w0 = G == 0 ? w.v[0].x : G == 1 ? w.v[0].y : G == 2 ? w.v[0].z : w.v[0].w;
-    const uint32_t w1 = G == 0 ? w.v[1].x : G == 1 ? w.v[1].y : G == 2 ? w.v[1].z : w.v[1].w;
-    const uint32_t vs = w.vs[G] & keep, vz = w.vz[G] & keep;
+  for (int i = 0; i < 2; ++i) {
+    const bool e = (i ^ ln.vr) & 1;  // which position of the pair
+    const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
+    uint8_t* dst = base + (e ? 16 : 0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = i ^ (ln.vr & 1);
-      const uint32_t word = __byte_perm(w0, w1, e ? 0x7531 : 0x6420);
-      put_nibbles<F32>(vb + mm_off(32 * G + 8 * ln.vr, 2 * ln.vp + e), PLANE, word, e ? dup_hi(vs) : dup_lo(vs),
-                       e ? dup_hi(vz) : dup_lo(vz));
+    for (int G = 0; G < 4; ++G) {
+      const uint32_t w0 = G == 0 ? w.v[0].x : G == 1 ? w.v[0].y : G == 2 ? w.v[0].z : w.v[0].w;
+      const uint32_t w1 = G == 0 ? w.v[1].x : G == 1 ? w.v[1].y : G == 2 ? w.v[1].z : w.v[1].w;
+      const uint32_t vs = w.vs[G] & keep, vz = w.vz[G] & keep;
+      uint4 o, l;
+      dequant8<F32>(__byte_perm(w0, w1, pick), __byte_perm(vs, vs, dup), __byte_perm(vz, vz, dup), o, l);
+      *reinterpret_cast<uint4*>(dst + 512 * G) = o;
+      if (F32) *reinterpret_cast<uint4*>(dst + 512 * G + PLANE) = l;
     }
   }
 }
 
-// ------------------------------------------------------------------ 2. the tiles
-// dynamic shared memory: K planes | V planes | query image | P planes | small state.  TQ3 keys, whose query image is
-// twice as wide, take the weights P into the key buffer (free once the logits are done), so that two CTAs of 64 rows fit
-// an SM; their next keys then wait for P V.
+// ------------------------------------------------------------------ 1. the tiles
+// dynamic shared memory: V planes | query image | P planes | prefix of the sequences' tiles
 template <int KF, bool F32>
 struct Smem {
   using C = Cfg<KF, F32>;
-  static constexpr bool P_IN_K = C::TQ;
-  static constexpr uint32_t K = 0, V = C::PL * C::PLANE, Q = 2 * C::PL * C::PLANE;
-  static __host__ __device__ constexpr uint32_t P(int N) { return P_IN_K ? K : Q + N * C::KD * 2 * C::PL; }
-  static __host__ __device__ constexpr uint32_t total(int N) {
-    return Q + N * C::KD * 2 * C::PL + (P_IN_K ? 0 : N * TILE * 2 * C::PL);
-  }
+  static constexpr uint32_t V = 0, Q = C::PL * C::PLANE;
+  static __host__ __device__ constexpr uint32_t P(int N) { return Q + N * C::KD * 2 * C::PL; }
+  static __host__ __device__ constexpr uint32_t total(int N) { return P(N) + N * TILE * 2 * C::PL; }
 };
 
-template <int KF, int NH, bool F32>
+template <int KF, int NC, bool F32>
 __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF, F32>;
   using SM = Smem<KF, F32>;
-  constexpr int N = 2 * NH;
-  constexpr bool TQ = C::TQ;
-  constexpr uint32_t S_COLS = TQ ? 2 * N : N, C_O = S_COLS;
-  constexpr uint32_t TM_COLS = S_COLS + N <= 32 ? 32 : S_COLS + N <= 64 ? 64 : S_COLS + N <= 128 ? 128 : 256;
+  constexpr int N = 2 * NC;  // rows, NC of them to a thread, CH at a time
+  constexpr int CH = 8;
+  constexpr bool TQ = C::TQ, NIB = KF == KVQ_Q4G32;
+  // tensor memory: K (one or two planes of 64 columns) | S (TQ3: two) | O
+  constexpr uint32_t C_S = 64 * C::PL, C_O = C_S + (TQ ? 2 * N : N), COLS = C_O + N;
+  constexpr uint32_t TM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  constexpr uint32_t ID_S = idesc(TILE, N, false, false), ID_O = idesc(D, N, true, true);
+  constexpr uint64_t LO_Q = (N * C::KD * 2) >> 4, LO_V = C::PLANE >> 4, LO_P = (N * TILE * 2) >> 4;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t qk_bar, pv_bar, load_bar;
+  // k_bar: the keys of a tile are in place (one arrival a worker warp); p_bar: its values and weights are
+  __shared__ __align__(8) uint64_t k_bar, p_bar, qk_bar, pv_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ float mref[N], wmax[4][N];
-  __shared__ int lim[N];
-  __shared__ unsigned long long anc[N];
+  __shared__ __align__(16) float mref[N], fac[N];
+  __shared__ float wmax[4][N];
+  __shared__ unsigned long long nodes[KVQ_MAX_TREE];  // ancestors-or-self of each node (0: not there)
+  // columns (rows of the unit) that are there and at depth at most i; that have node i among their ancestors-or-self
+  __shared__ unsigned long long shallow[KVQ_MAX_TREE], below[KVQ_MAX_TREE];
+  __shared__ int par[KVQ_MAX_TREE];
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem + SM::total(N));
+  int* lens = pre + a.batch + 1;
 
   if (tid == 0) {
+    bar_init(&k_bar, WARPS);
+    bar_init(&p_bar, 1);
     bar_init(&qk_bar, 1);
     bar_init(&pv_bar, 1);
-    bar_init(&load_bar, 1);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) tile_prefix(a, pre);
+  if (warp == 0) tile_prefix(a, lens, pre, blockIdx.x == 0);
   if (warp == 1) tm_alloc(&tmem_sh, TM_COLS);
   fence_before();
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_sh;
-  const uint32_t sbase = smem_u32(smem);
+  const uint32_t tmem = tmem_sh, sbase = smem_u32(smem);
 
   // this CTA's range of the list of tiles
   const long long per_layer = (long long)pre[a.batch] * a.Hkv * p.rb, total = per_layer * a.n_layers_call;
   const long long G = min((long long)p.G, total);  // no range is empty: the merge reads every range between a unit's ends
-  long long t = blockIdx.x < G ? total * blockIdx.x / G : 0;
-  const long long t_end = blockIdx.x < G ? total * (blockIdx.x + 1) / G : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
+  const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
 
   const Lane ln = lane_of(tid);
   const size_t page_stride = (size_t)a.Hkv * a.L.page_bytes;
+  const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
   uint4 cent = make_uint4(0u, 0u, 0u, 0u);
   if (TQ) {
     const uint4 c = *reinterpret_cast<const uint4*>(a.p.cb->cent);
-    cent.x = __byte_perm(c.x, c.y, 0x6420);
-    cent.y = __byte_perm(c.z, c.w, 0x6420);
-    cent.z = __byte_perm(c.x, c.y, 0x7531);
-    cent.w = __byte_perm(c.z, c.w, 0x7531);
+    cent = make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.x, c.y, 0x7531),
+                      __byte_perm(c.z, c.w, 0x7531));
   }
-  uint32_t qk_phase = 0, pv_phase = 0, load_phase = 0;
+  uint32_t k_phase = 0, p_phase = 0, qk_phase = 0, pv_phase = 0;
   bool pv_pending = false;
-  const int col0 = (warp >> 2) * NH;                                  // this thread's columns (rows of the unit)
-  const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // its tensor-memory lane: position ln.t, channel ln.t
+  const auto wait = [&](uint64_t* bar, uint32_t& phase) {
+    bar_wait(bar, phase, &abort_sh, a.p.status);
+    phase ^= 1;
+  };
+  const auto wait_pv = [&] {
+    if (pv_pending) {
+      wait(&pv_bar, pv_phase);
+      pv_pending = false;
+    }
+  };
+  // this warp's part of the keys is in tensor memory
+  const auto k_done = [&] {
+    tm_wait_st();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&k_bar);
+  };
+  const int col0 = (warp >> 2) * NC;                                      // this thread's columns (rows of the unit)
+  const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // its lane: position ln.t, channel ln.t
   bool ok = true;
 
   while (t < t_end && ok) {
     // ---- the next unit: its sequence, head and row block, and this CTA's tiles of it
-    const int ll = (int)(t / per_layer);
+    const int ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
     const long long in_layer = t - ll * per_layer;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
@@ -524,306 +443,429 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     }
     const int b = lo, tiles = pre[b + 1] - pre[b];
     const long long r = in_layer - (long long)pre[b] * a.Hkv * p.rb;
-    const int hr = (int)(r / tiles), it0 = (int)(r - (long long)hr * tiles);
-    const int h = hr / p.rb, rbi = hr - h * p.rb;
-    const int it1 = (int)min((long long)tiles, it0 + (t_end - t));
+    const int hr = (int)quick_div(r, tiles), it0 = (int)(r - (long long)hr * tiles);
+    const int h = hr / p.rb, rbi = hr - h * p.rb, layer = a.layer0 + ll;
     const int u = ((ll * a.batch + b) * a.Hkv + h) * p.rb + rbi;
-    const int L = seq_len(a, b), qend = quant_end(L, a.W, a.n), nq = (qend + TILE - 1) / TILE;
-    const int nraw = raw_count(L, a.W, a.n), nring = nraw - a.n;
+    const int L = lens[b], qend = quant_end(L, a.W, a.n), nq = (qend + TILE - 1) / TILE;
+    // tiles of records come first, then those of raw positions; a part is of one kind
+    const bool raw = it0 >= nq;
+    const int it1 = (int)min((long long)(raw ? tiles : nq), it0 + (t_end - t));
+    t += it1 - it0;
+
+    if (warp == WARPS) {
+      // ================================================================ the products
+      if (TQ && !raw) {
+        // S q~ of every row: the projection lies in the values' place
+        wait(&k_bar, k_phase);
+        fence_after();
+        uint64_t sa = sdesc(sbase + SM::V, 2048, 128), qa = sdesc(sbase + SM::Q, N * 16, 128);
+#pragma unroll 1
+        for (int ks = 0; ks < D / 16; ++ks, sa += 256, qa += 2 * N) {
+          mma_ss(tmem + C_S, sa, qa, ID_S, ks > 0);
+          if (F32) {
+            mma_ss(tmem + C_S, sa + LO_V, qa, ID_S, 1);
+            mma_ss(tmem + C_S, sa, qa + LO_Q, ID_S, 1);
+          }
+        }
+        mma_commit(&qk_bar);
+      }
+      for (int it = it0; it < it1; ++it) {
+        // logits: a k-step of 16 channels is 8 columns of K and 32 N bytes of the queries; TQ3 records come twice, the
+        // centroids and then, in their place, the signs
+        for (int part = 0; part < (TQ && !raw ? 2 : 1); ++part) {
+          wait(&k_bar, k_phase);
+          fence_after();
+          uint64_t qa = sdesc(sbase + SM::Q + (part ? N * 256 : 0), N * 16, 128);
+          uint32_t ka = tmem;
+          const uint32_t d = tmem + C_S + (part ? N : 0);
+#pragma unroll 1
+          for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
+            mma_ts(d, ka, qa, ID_S, ks > 0);
+            if (F32) {
+              mma_ts(d, ka, qa + LO_Q, ID_S, 1);
+              if (!TQ || raw) mma_ts(d, ka + 64, qa, ID_S, 1);
+            }
+          }
+          mma_commit(&qk_bar);
+        }
+        // O += V^T P: a k-step of 16 positions is 4096 bytes of V and 32 N of P
+        wait(&p_bar, p_phase);
+        if (*(volatile int*)&abort_sh) break;
+        fence_after();
+        uint64_t va = sdesc(sbase + SM::V, 2048, 128), pa = sdesc(sbase + SM::P(N), N * 16, 128);
+#pragma unroll 1
+        for (int ks = 0; ks < TILE / 16; ++ks, va += 256, pa += 2 * N) {
+          mma_ss(tmem + C_O, va, pa, ID_O, it > it0 || ks > 0);
+          if (F32) {
+            mma_ss(tmem + C_O, va + LO_V, pa, ID_O, 1);
+            mma_ss(tmem + C_O, va, pa + LO_P, ID_O, 1);
+          }
+        }
+        mma_commit(&pv_bar);
+      }
+      ok = !*(volatile int*)&abort_sh;
+      continue;
+    }
+
+    // ================================================================ the workers
+    const int nraw = raw_count(L, a.W, a.n), nring = nraw - a.n, rows = a.n * a.g;
     const int full_end = a.W > 0 ? L - a.W + 1 : L;  // positions below are read through records by every node
-    const uint8_t* unit_pages = a.p.pages + ((size_t)(a.layer0 + ll) * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
+    const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
     const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
     const auto pages_of = [&](int it) {
       Pages g;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = it * TILE + i * PAGE;
-        const int x = it < nq && j < qend ? __ldg(bt + j / PAGE) : -1;
-        g.p[i] = x < a.L.n_pages ? x : -1;
-        if (it < nq && j < qend && (x < 0 || x >= a.L.n_pages) && tid == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
+        g.p[i] = it < nq && j < qend ? __ldg(bt + j / PAGE) : -1;  // (checked where it is used, a tile later)
       }
       return g;
     };
+    // ---- its queries (to the values' place), the parents and the first pages are requested together
+    constexpr int ESZ = F32 ? 4 : 2, Q_CHUNKS = D * ESZ / 16;
+    const size_t q_unit = ((size_t)(ll * a.batch + b) * a.Hkv + h) * a.g * a.n;
+#pragma unroll 1
+    for (int i = tid; i < N * Q_CHUNKS; i += WORKERS) {
+      const int row = rbi * N + i / Q_CHUNKS;
+      if (row < rows)
+        cp16(smem + SM::V + 16 * i, static_cast<const uint8_t*>(a.q) + ((q_unit + (size_t)(row % a.g) * a.n + row / a.g) * Q_CHUNKS + i % Q_CHUNKS) * 16);
+    }
+    const bool masked = raw || it1 * TILE > full_end;  // some position is not for every node
+    if (masked && tid < a.n) par[tid] = a.parents[(size_t)b * a.n + tid];
     Words<KF> w;
     Pages pg = pages_of(it0), pg1 = pages_of(it0 + 1);
     load_k<KF>(a, unit_pages, page_stride, pg, ln, w);
     load_v<KF>(a, unit_pages, page_stride, pg, ln, w);
-    if (tid == 0) {
-      bar_expect(&load_bar, (uint32_t)p.q_image);
-      bulk_g2s(smem + SM::Q, p.q_images + (size_t)u * p.q_image, (uint32_t)p.q_image, &load_bar);
-    }
-    if (tid < N) {
-      const int row = rbi * N + tid, node = row / a.g;
-      const unsigned long long m = row < a.n * a.g ? p.anc[(size_t)b * a.n + node] : 0ull;
-      anc[tid] = m;
-      mref[tid] = NO_REF;
-      lim[tid] = m ? (a.W > 0 ? min(L - 1, L + __popcll(m) - 1 - a.W) : L - 1) : -1;
-    }
-    float l[NH];
+    if (tid < N) mref[tid] = NO_REF;
+    cp_wait();
+    part_sync(1, WORKERS);
+    // ---- queries in base-2 units, for records rotated and balanced
+#pragma unroll 1
+    for (int r1 = warp; r1 < N; r1 += WARPS) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rbi * N + r1 < rows) x = load4_in(smem + SM::V, (size_t)r1 * D + 4 * lane, !F32);
+      float y[4] = {x.x, x.y, x.z, x.w};
+      if (!raw) {
+        y[0] *= sg.x, y[1] *= sg.y, y[2] *= sg.z, y[3] *= sg.w;
+        hadamard_warp(y[0], y[1], y[2], y[3], lane);
+      }
 #pragma unroll
-    for (int c = 0; c < NH; ++c) l[c] = 0.f;
-    bar_wait(&load_bar, load_phase, &abort_sh, a.p.status);
-    load_phase ^= 1;
+      for (int e = 0; e < 4; ++e) {
+        y[e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+        if (a.sinkhorn && !raw) y[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
+      }
+      put4<NIB, F32>(smem + SM::Q + km_off(r1, 4 * lane & ~7, N) + 8 * (lane & 1), N * C::KD * 2, y, lane);
+    }
+    if (masked) {
+      // ---- the nodes' ancestors, and what they are to this block's columns
+      if (tid < a.n) {
+        unsigned long long m = 0;
+        for (int j = tid; j >= 0;) {
+          m |= 1ull << j;
+          const int q = par[j];
+          if (q < -1 || q >= j) {
+            if (q >= j) atomicOr(a.p.status, KVQ_DEV_BAD_NODE);
+            m = 0;
+            break;
+          }
+          j = q;
+        }
+        nodes[tid] = m;
+      }
+      part_sync(1, WORKERS);
+      unsigned long long anc[2];
+      int depth[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = lane + 32 * i, row = rbi * N + c;
+        anc[i] = c < N && row < rows ? nodes[row / a.g] : 0ull;
+        depth[i] = anc[i] ? __popcll(anc[i]) - 1 : KVQ_MAX_TREE;
+      }
+#pragma unroll 1
+      for (int x = warp; x < KVQ_MAX_TREE; x += WARPS) {
+        const uint32_t s0 = __ballot_sync(FULL, depth[0] <= x), s1 = __ballot_sync(FULL, depth[1] <= x);
+        const uint32_t b0 = __ballot_sync(FULL, (anc[0] >> x) & 1), b1 = __ballot_sync(FULL, (anc[1] >> x) & 1);
+        if (lane == 0) {
+          shallow[x] = s0 | (unsigned long long)s1 << 32;
+          below[x] = b0 | (unsigned long long)b1 << 32;
+        }
+      }
+    }
+    if (TQ && !raw) part_sync(1, WORKERS);  // the queries have left the values' place
+    if (TQ && !raw) {
+      // S q~ of every row by the tensor cores: the projection as an operand in the values' place
+      const int i = tid & 127;
+#pragma unroll 1
+      for (int kg = tid >> 7; kg < D / 8; kg += 2) {
+        float s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __ldg(a.p.qjl_t + (8 * kg + e) * D + i);
+        uint4 o, l;
+        split2(s[0], s[1], o.x, l.x);
+        split2(s[2], s[3], o.y, l.y);
+        split2(s[4], s[5], o.z, l.z);
+        split2(s[6], s[7], o.w, l.w);
+        *reinterpret_cast<uint4*>(smem + SM::V + km_off(i, 8 * kg, D)) = o;
+        if (F32) *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + km_off(i, 8 * kg, D)) = l;
+      }
+      fence_async_smem();
+      k_done();
+      wait(&qk_bar, qk_phase);
+      fence_after();
+#pragma unroll 1
+      for (int c = 0; c < NC; c += CH) {
+        float x[CH];
+        tm_ld(lane_addr + C_S + col0 + c, x);
+        tm_wait_ld();
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+          uint8_t* dst = smem + SM::Q + km_off(col0 + c + e, D + i, N);
+          *reinterpret_cast<__half*>(dst) = __float2half_rn(x[e]);
+          if (F32) *reinterpret_cast<__half*>(dst + N * C::KD * 2) = __float2half_rn(lo_part(x[e]));
+        }
+      }
+    }
+    fence_async_smem();
+    part_sync(1, WORKERS);  // the columns' masks and references
+    float l[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) l[c] = 0.f;
 
     for (int it = it0; it < it1; ++it) {
-      const bool raw = it >= nq;
-      const auto wait_pv = [&] {
-        if (pv_pending) {
-          bar_wait(&pv_bar, pv_phase, &abort_sh, a.p.status);
-          pv_phase ^= 1;
-          pv_pending = false;
+      // raw tiles: this thread's position in the list of ring positions and drafts, its vector (null: none; nodes that are
+      // not there may hold anything) and the vector's eight channels of a group in nibble order
+      const int x = (it - nq) * TILE + ln.t;
+      const auto raw_row = [&](int kv) -> const void* {
+        if (x < nring)
+          return (kv ? a.p.ringv : a.p.ringk) +
+                 ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (unsigned)(L - nring + x) % (unsigned)a.W) * D;
+        if (x < nraw && nodes[x - nring])
+          return static_cast<const uint8_t*>(kv ? a.v : a.k) + ((((size_t)ll * a.batch + b) * a.Hkv + h) * a.n + x - nring) * D * ESZ;
+        return nullptr;
+      };
+      const auto raw_group = [&](const void* row, int kg, bool places, uint4& o, uint4& l) {
+        float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
+        if (row) {
+          f0 = load4_in(row, 8 * kg, !F32 && x >= nring);
+          f1 = load4_in(row, 8 * kg + 4, !F32 && x >= nring);
+        }
+        if (places) {  // 0 4 1 5 2 6 3 7
+          split2(f0.x, f1.x, o.x, l.x);
+          split2(f0.y, f1.y, o.y, l.y);
+          split2(f0.z, f1.z, o.z, l.z);
+          split2(f0.w, f1.w, o.w, l.w);
+        } else {
+          split2(f0.x, f0.y, o.x, l.x);
+          split2(f0.z, f0.w, o.y, l.y);
+          split2(f1.x, f1.y, o.z, l.z);
+          split2(f1.z, f1.w, o.w, l.w);
         }
       };
       // ---- keys (the previous tile's logits are done: its softmax has read them)
-      if (SM::P_IN_K) wait_pv();
       uint32_t ng = 0;  // TQ3: norm and residual norm of this thread's position
       bool valid = true;
       if (!raw) {
-        put_k<KF, F32>(smem + SM::K, ln, w, cent);
+        put_k<KF, F32>(lane_addr, ln, w, cent);
         ng = w.kx;
-        valid = (ln.t & 64 ? pg.p[1] : pg.p[0]) >= 0;
-        fence_async_smem();
+        valid = pg.of(ln.t & 64, a.L.n_pages) >= 0;
+        if (!valid && it * TILE + (ln.t & 64) < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
       } else {
-        const uint8_t* img = p.raw_images + ((size_t)(u / p.rb) * p.raw_tiles + (it - nq)) * p.raw_image;
-        if (tid == 0) {
-          bar_expect(&load_bar, C::PL * C::PLANE);
-          bulk_g2s(smem + SM::K, img, C::PL * C::PLANE, &load_bar);
+        const void* row = raw_row(0);
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          uint4 o, l;
+          raw_group(row, 8 * ln.hf + i, NIB, o, l);
+          tm_st4(lane_addr + 32 * ln.hf + 4 * i, o);
+          if (F32) tm_st4(lane_addr + 64 + 32 * ln.hf + 4 * i, l);
         }
-        bar_wait(&load_bar, load_phase, &abort_sh, a.p.status);
-        load_phase ^= 1;
       }
-      fence_before();
-      __syncthreads();
-      if (warp == 0) {
-        fence_after();
-        // logits: k-step of 16 channels = 4096 bytes of K, 32 N of the queries
-        uint64_t ka = sdesc(sbase + SM::K, 2048, 128), qa = sdesc(sbase + SM::Q, N * 16, 128);
-        const uint64_t lo_k = C::PLANE >> 4, lo_q = (N * C::KD * 2) >> 4;
-#pragma unroll 1
-        for (int ks = 0; ks < D / 16; ++ks, ka += 256, qa += 2 * N) {
-          mma_ss(tmem, ka, qa, idesc(TILE, N, false, false), ks > 0);
-          if (F32) {
-            mma_ss(tmem, ka, qa + lo_q, idesc(TILE, N, false, false), 1);
-            if (!TQ || raw) mma_ss(tmem, ka + lo_k, qa, idesc(TILE, N, false, false), 1);
-          }
-        }
-        mma_commit(&qk_bar);
-      }
-      // ---- values, while the logits run (the previous tile's P V must be done with the buffer)
+      k_done();
+      // ---- values, while the logits run (the previous tile's P V must be done with their place)
       wait_pv();
       if (!raw) {
         put_v<KF, F32>(smem + SM::V, ln, w, qend - it * TILE - 2 * ln.vp);
-      } else if (tid == 0) {
-        const uint8_t* img = p.raw_images + ((size_t)(u / p.rb) * p.raw_tiles + (it - nq)) * p.raw_image + C::PL * C::PLANE;
-        bar_expect(&load_bar, C::PL * C::PLANE);
-        bulk_g2s(smem + SM::V, img, C::PL * C::PLANE, &load_bar);
+      } else {
+        const void* row = raw_row(1);
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          const int kg = 8 * ln.hf + i;
+          uint4 o, l;
+          raw_group(row, kg, true, o, l);
+          *reinterpret_cast<uint4*>(smem + SM::V + mm_off(8 * kg, ln.t)) = o;
+          if (F32) *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + mm_off(8 * kg, ln.t)) = l;
+        }
       }
       if (TQ && !raw) {
         // the projections' signs take the centroids' place
-        bar_wait(&qk_bar, qk_phase, &abort_sh, a.p.status);
-        qk_phase ^= 1;
-        if constexpr (TQ) put_signs(smem + SM::K, ln, w);
-        fence_async_smem();
-        __syncthreads();
-        if (warp == 0) {
-          fence_after();
-          uint64_t ka = sdesc(sbase + SM::K, 2048, 128), qa = sdesc(sbase + SM::Q + N * 256, N * 16, 128);
-          const uint64_t lo_q = (N * C::KD * 2) >> 4;
-#pragma unroll 1
-          for (int ks = 0; ks < D / 16; ++ks, ka += 256, qa += 2 * N) {
-            mma_ss(tmem + N, ka, qa, idesc(TILE, N, false, false), ks > 0);
-            if (F32) mma_ss(tmem + N, ka, qa + lo_q, idesc(TILE, N, false, false), 1);
-          }
-          mma_commit(&qk_bar);
-        }
+        wait(&qk_bar, qk_phase);
+        fence_after();
+        if constexpr (TQ) put_signs(lane_addr, ln, w);
+        k_done();
       }
       // the next tile's words (its page numbers were read a tile earlier)
-      if (it + 1 < it1) {
+      if (it + 1 < it1 && !raw) {
         load_k<KF>(a, unit_pages, page_stride, pg1, ln, w);
         load_v<KF>(a, unit_pages, page_stride, pg1, ln, w);
         pg = pg1;
-        pg1 = it + 2 < it1 ? pages_of(it + 2) : pg1;
+        pg1 = pages_of(it + 2);
       }
+      // ---- which of the thread's columns attend to its position: by records a node at depth d reads j <= L + d - W,
+      // raw ones the rest, drafts its ancestors and itself
+      uint32_t bits = 0xffffffffu;
+      if (raw || (it + 1) * TILE > full_end || !valid) {
+        const int j = raw ? L - nring + x : it * TILE + ln.t, d = j - L + a.W - 1;  // the deepest node that reads j raw
+        unsigned long long on = 0ull;
+        if (!raw) {
+          if (valid && j < full_end) on = ~0ull;
+          else if (valid && j < L) on = shallow[KVQ_MAX_TREE - 1] & ~(a.W > 0 ? shallow[min(d, KVQ_MAX_TREE - 1)] : 0ull);
+        } else if (x < nring) {
+          on = d >= 0 ? shallow[min(d, KVQ_MAX_TREE - 1)] : 0ull;
+        } else if (x < nraw) {
+          on = below[x - nring];
+        }
+        bits = (uint32_t)(on >> col0);
+      }
+      constexpr uint32_t ALL = NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1;
+      const bool all = __all_sync(FULL, (bits & ALL) == ALL);
       // ---- softmax down the thread's columns
-      bar_wait(&qk_bar, qk_phase, &abort_sh, a.p.status);
-      qk_phase ^= 1;
+      wait(&qk_bar, qk_phase);
       fence_after();
-      const int j = (raw ? it - nq : it) * TILE + ln.t;  // position, or place in the raw list
-      const bool no_mask = !raw && (it + 1) * TILE <= full_end && valid;
       const float nn = TQ && !raw ? __low2float(u2h(ng)) : 1.f;
       const float nw = TQ && !raw ? nn * QJL_CONST * __high2float(u2h(ng)) : 0.f;
-      uint8_t* pbuf = smem + SM::P(N) + (ln.t >> 3) * (N * 16) + (ln.t & 7) * 16 + col0 * 16;
-      // logits of eight columns from tensor memory
-      const auto logits = [&](int c, float (&x)[8]) {
-        tm_ld8(lane_addr + col0 + c, x);
+      // CH columns' logits less `ref` from tensor memory
+      const auto logits = [&](int c, float (&x)[CH], const float (&ref)[CH]) {
+        tm_ld(lane_addr + C_S + col0 + c, x);
         if (TQ && !raw) {
-          float y[8];
-          tm_ld8(lane_addr + N + col0 + c, y);
+          float y[CH];
+          tm_ld(lane_addr + C_S + N + col0 + c, y);
           tm_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * nn + y[i] * nw;
+          for (int i = 0; i < CH; ++i) x[i] = fmaf(y[i], nw, fmaf(x[i], nn, -ref[i]));
         } else {
           tm_wait_ld();
-        }
-        if (!no_mask) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int cc = col0 + c + i;
-            bool on;
-            if (!raw) on = valid && j <= lim[cc];
-            else if (j < nring) on = anc[cc] != 0 && L - nring + j > lim[cc];
-            else on = j < nraw && ((anc[cc] >> (j - nring)) & 1ull);
-            if (!on) x[i] = -INFINITY;
-          }
+          for (int i = 0; i < CH; ++i) x[i] -= ref[i];
+        }
+        if (!all) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            if (!((bits >> (c + i)) & 1)) x[i] = -INFINITY;
         }
       };
-      uint32_t over = 0;  // by groups of eight columns: some lane of the warp passed a reference; those are not summed yet
+      uint32_t summed = 0;  // by groups of CH columns, warp-uniform: the weights are in the sums
+      for (int raises = it == it0 ? 0 : -1;; ++raises) {
+        if (raises >= 0) {
+          // ---- raise the references of the rows that passed theirs (all of them at first) to the tile's maxima, and
+          // rescale what has been summed; then the weights are taken (again)
+#pragma unroll 1
+          for (int c = 0; c < NC; c += CH) {
+            float x[CH];
+            const float zero[CH] = {};
+            logits(c, x, zero);
 #pragma unroll
-      for (int c = 0; c < NH; c += 8) {
-        float x[8];
-        logits(c, x);
-        uint32_t ph[4], pl[4];
-        float top = -INFINITY;
+            for (int i = 0; i < CH; ++i) {
+              const int v = __float_as_int(x[i]);
+              const int m = __reduce_max_sync(FULL, v ^ ((v >> 31) & 0x7fffffff));
+              if (lane == 0) wmax[warp & 3][col0 + c + i] = __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+            }
+          }
+          part_sync(1, WORKERS);
+          if (tid < N) {
+            const float top = fmaxf(fmaxf(wmax[0][tid], wmax[1][tid]), fmaxf(wmax[2][tid], wmax[3][tid]));
+            const float m0 = mref[tid], m1 = top > m0 + 8.f ? top : m0;
+            fac[tid] = ex2(m0 - m1);
+            mref[tid] = m1;
+          }
+          part_sync(1, WORKERS);
+          if (it > it0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] -= mref[col0 + c + i];
-          top = fmaxf(top, x[i]);
-          x[i] = ex2(x[i]);
-        }
+            for (int c = 0; c < NC; ++c) l[c] *= fac[col0 + c];
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 4) {
+              float o[4];
+              tm_ld(lane_addr + C_O + col0 + c, o);
+              tm_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (F32) split2(x[2 * i], x[2 * i + 1], ph[i], pl[i]);
-          else ph[i] = h2u(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
-        }
-        *reinterpret_cast<uint4*>(pbuf + c * 16) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-        if (F32) *reinterpret_cast<uint4*>(pbuf + N * TILE * 2 + c * 16) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-        if (__any_sync(FULL, top > 8.f)) {
-          over |= 1u << (c / 8);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) l[c + i] += x[i];
-        }
-      }
-      if (raw) {  // the raw values have landed before their product
-        bar_wait(&load_bar, load_phase, &abort_sh, a.p.status);
-        load_phase ^= 1;
-      }
-      fence_async_smem();
-      fence_before();
-      if (__syncthreads_or(over)) {
-        // ---- a row's logit passed its reference by more than 8 (its first ones do): raise the references to the
-        // tile's maxima, rescale what has been summed, and take the weights again
-#pragma unroll
-        for (int c = 0; c < NH; c += 8) {
-          float x[8];
-          logits(c, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (!(over >> (c / 8) & 1)) l[c + i] -= ex2(x[i] - mref[col0 + c + i]);
-            float m = x[i];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-            if (lane == 0) wmax[warp & 3][col0 + c + i] = m;
+              for (int i = 0; i < 4; ++i) o[i] *= fac[col0 + c + i];
+              tm_st4(lane_addr + C_O + col0 + c,
+                     make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])));
+            }
+            tm_wait_st();
           }
         }
-        __syncthreads();
+        bool over = false;
 #pragma unroll
-        for (int c = 0; c < NH; c += 8) {
-          float x[8], f[8];
-          logits(c, x);
-          uint32_t ph[4], pl[4];
+        for (int c = 0; c < NC; c += CH) {
+          float x[CH], ref[CH];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int cc = col0 + c + i;
-            const float top = fmaxf(fmaxf(wmax[0][cc], wmax[1][cc]), fmaxf(wmax[2][cc], wmax[3][cc]));
-            const float m0 = mref[cc], m1 = top > m0 + 8.f ? top : m0;
-            f[i] = ex2(m0 - m1);
-            x[i] = ex2(x[i] - m1);
-            l[c + i] = l[c + i] * f[i] + x[i];
+          for (int i = 0; i < CH; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(mref + col0 + c + i);
+            ref[i] = m.x, ref[i + 1] = m.y, ref[i + 2] = m.z, ref[i + 3] = m.w;
           }
+          logits(c, x, ref);
+          uint32_t ph[CH / 2], pl[CH / 2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < CH; ++i) x[i] = ex2(x[i]);
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) {
             if (F32) split2(x[2 * i], x[2 * i + 1], ph[i], pl[i]);
             else ph[i] = h2u(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
           }
-          *reinterpret_cast<uint4*>(pbuf + c * 16) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          if (F32) *reinterpret_cast<uint4*>(pbuf + N * TILE * 2 + c * 16) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-          if (it > it0) {
-            float o[8];
-            tm_ld8(lane_addr + C_O + col0 + c, o);
-            tm_wait_ld();
+          uint8_t* dst = smem + SM::P(N) + mn_off(col0 + c, ln.t, N);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+          if (F32) *reinterpret_cast<uint4*>(dst + N * TILE * 2) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          const __half2 top = __hmax2(__hmax2(u2h(ph[0]), u2h(ph[1])), __hmax2(u2h(ph[2]), u2h(ph[3])));
+          // a weight over 2^8 (infinity among them) waits for a higher reference
+          if (__any_sync(FULL, __hgt(__hmax(__low2half(top), __high2half(top)), __ushort_as_half(0x5C00)))) {
+            over = true;
+          } else if (!((summed >> (c / CH)) & 1)) {
+            summed |= 1u << (c / CH);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= f[i];
-            tm_st8(lane_addr + C_O + col0 + c, o);
+            for (int i = 0; i < CH; ++i) l[c + i] += x[i];
           }
         }
-        tm_wait_st();
         fence_async_smem();
         fence_before();
-        __syncthreads();
-        if (tid < N) {
-          const float top = fmaxf(fmaxf(wmax[0][tid], wmax[1][tid]), fmaxf(wmax[2][tid], wmax[3][tid]));
-          if (top > mref[tid] + 8.f) mref[tid] = top;
-        }
+        // (one raise puts every weight at or below 2^8; only an infinity or NaN is still over it then)
+        if (!part_or(1, WORKERS, over) || raises >= 0) break;
       }
-      if (abort_sh) {  // raised before the barrier above by whoever gave up: the whole CTA leaves together
+      if (*(volatile int*)&abort_sh) {  // raised before the barrier above by whoever gave up: the workers leave together
         ok = false;
         break;
       }
-      if (warp == 0) {
-        fence_after();
-        // O += V^T P: k-step of 16 positions = 4096 bytes of V, 32 N of P
-        uint64_t va = sdesc(sbase + SM::V, 2048, 128), pa = sdesc(sbase + SM::P(N), N * 16, 128);
-        const uint64_t lo_v = C::PLANE >> 4, lo_p = (N * TILE * 2) >> 4;
-#pragma unroll 1
-        for (int ks = 0; ks < TILE / 16; ++ks, va += 256, pa += 2 * N) {
-          mma_ss(tmem + C_O, va, pa, idesc(D, N, true, true), it > it0 || ks > 0);
-          if (F32) {
-            mma_ss(tmem + C_O, va + lo_v, pa, idesc(D, N, true, true), 1);
-            mma_ss(tmem + C_O, va, pa + lo_p, idesc(D, N, true, true), 1);
-          }
-        }
-        mma_commit(&pv_bar);
-      }
+      if (tid == 0) bar_arrive(&p_bar);
       pv_pending = true;
     }
     if (!ok) break;
     // ---- the range's part of the unit: reference, sum and O of every row
-    bar_wait(&pv_bar, pv_phase, &abort_sh, a.p.status);
-    pv_phase ^= 1;
-    pv_pending = false;
+    wait_pv();
     fence_after();
-    float* rec = p.records + (size_t)(u + blockIdx.x) * (2 * N + D * N);
-    __syncthreads();  // the last tile's references are up to date, and their maxima read
+    float* rec = p.records + (size_t)(2 * u + raw + blockIdx.x) * (2 * N + D * N);
 #pragma unroll
-    for (int c = 0; c < NH; ++c) {
+    for (int c = 0; c < NC; ++c) {
       float s = l[c];
 #pragma unroll
       for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
       if (lane == 0) wmax[warp & 3][col0 + c] = s;
     }
-#pragma unroll
-    for (int c = 0; c < NH; c += 8) {
-      float o[8];
-      tm_ld8(lane_addr + C_O + col0 + c, o);
+    const int ch = (ln.t & ~7) + nibble_channel(ln.t & 7);  // tensor-memory lane = place of the channel
+#pragma unroll 1
+    for (int c = 0; c < NC; c += CH) {
+      float o[CH];
+      tm_ld(lane_addr + C_O + col0 + c, o);
       tm_wait_ld();
-      // tensor-memory lane = place of the channel: back to its own
-      const int ch = (ln.t & ~7) + nibble_channel(ln.t & 7);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rec[2 * N + (col0 + c + i) * D + ch] = o[i];
+      for (int i = 0; i < CH; ++i) rec[2 * N + (col0 + c + i) * D + ch] = o[i];
     }
     fence_before();
-    __syncthreads();
-    fence_after();
+    part_sync(1, WORKERS);
     if (tid < N) {
       rec[tid] = mref[tid];
       rec[N + tid] = wmax[0][tid] + wmax[1][tid] + wmax[2][tid] + wmax[3][tid];
     }
-    __syncthreads();
-    t += it1 - it0;
   }
   // products still running (a CTA that gave up) land before the columns are freed; the wait is bounded
-  if (warp == 0 && !ok) {
+  if (warp == WARPS && !ok) {
     mma_commit(&pv_bar);
     const unsigned long long t0 = gtimer();
     while (!bar_try(&pv_bar, pv_phase) && gtimer() - t0 < WAIT_NS) {
@@ -837,15 +879,16 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   }
 }
 
-// ------------------------------------------------------------------ 3. merge
+// ------------------------------------------------------------------ 2. merge
 // WIDE: a CTA per row, its warps on slices of the row's records; else a warp per row
 template <bool WIDE>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __grid_constant__ Plan p) {
-  __shared__ float part[MERGE_WARPS][D + 2];
+  __shared__ float part[WIDE ? MERGE_WARPS : 1][2 * D + 2];
   extern __shared__ int pre[];
   const MultiArgs& a = p.a;
+  int* lens = pre + a.batch + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) tile_prefix(a, pre);
+  if (warp == 0) tile_prefix(a, lens, pre, false);
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = a.n * a.g;
@@ -855,55 +898,81 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
   const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.batch, ll = unit / (a.Hkv * a.batch);
   const int u = unit * p.rb + row / p.N, col = row % p.N, node = row / a.g;
   const long long per_layer = (long long)pre[a.batch] * a.Hkv * p.rb, total = per_layer * a.n_layers_call;
-  const int tiles = pre[b + 1] - pre[b];
+  const int tiles = pre[b + 1] - pre[b], nq = (quant_end(lens[b], a.W, a.n) + TILE - 1) / TILE;
   const long long first = ll * per_layer + (long long)pre[b] * a.Hkv * p.rb + (long long)(h * p.rb + row / p.N) * tiles;
-  // range c holds tile x for c = floor(((x + 1) G - 1) / total)
   const long long G = min((long long)p.G, total);
-  const int c0 = (int)(((first + 1) * G - 1) / total), c1 = (int)(((first + tiles) * G - 1) / total);
   const size_t rec_floats = 2 * p.N + (size_t)D * p.N;
-  float M = NO_REF, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  // the row's parts: first those of the records (o[0]), then those of the raw positions (o[1]), each kind in the order of
+  // the ranges; range c holds tile x for c = floor(((x + 1) G - 1) / total)
+  float M = NO_REF, l = 0.f, o[2][4] = {};
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const long long x0 = first + (kind ? nq : 0), x1 = first + (kind ? tiles : nq);
+    if (x0 == x1) continue;
+    const int c0 = (int)quick_div((x0 + 1) * G - 1, total), c1 = (int)quick_div(x1 * G - 1, total);
 #pragma unroll 4
-  for (int c = c0 + (WIDE ? warp : 0); c <= c1; c += WIDE ? MERGE_WARPS : 1) {
-    const float* rec = p.records + (size_t)(u + c) * rec_floats;
-    const float m = rec[col], s = rec[p.N + col];
-    const float4 x = *reinterpret_cast<const float4*>(rec + 2 * p.N + (size_t)col * D + 4 * lane);
-    const float mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
-    M = mn;
-    l = l * f0 + s * f1;
-    o[0] = o[0] * f0 + x.x * f1;
-    o[1] = o[1] * f0 + x.y * f1;
-    o[2] = o[2] * f0 + x.z * f1;
-    o[3] = o[3] * f0 + x.w * f1;
+    for (int c = c0 + (WIDE ? warp : 0); c <= c1; c += WIDE ? MERGE_WARPS : 1) {
+      const float* rec = p.records + (size_t)(2 * u + kind + c) * rec_floats;
+      const float m = rec[col], s = rec[p.N + col];
+      const float4 x = *reinterpret_cast<const float4*>(rec + 2 * p.N + (size_t)col * D + 4 * lane);
+      const float mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
+      M = mn;
+      l = l * f0 + s * f1;
+      if (kind) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][e] *= f0;
+      }
+      o[kind][0] = o[kind][0] * f0 + x.x * f1;
+      o[kind][1] = o[kind][1] * f0 + x.y * f1;
+      o[kind][2] = o[kind][2] * f0 + x.z * f1;
+      o[kind][3] = o[kind][3] * f0 + x.w * f1;
+    }
   }
   if (WIDE) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][4 * lane + e] = o[e];
+    for (int e = 0; e < 4; ++e) {
+      part[warp][4 * lane + e] = o[0][e];
+      part[warp][D + 4 * lane + e] = o[1][e];
+    }
     if (lane == 0) {
-      part[warp][D] = M;
-      part[warp][D + 1] = l;
+      part[warp][2 * D] = M;
+      part[warp][2 * D + 1] = l;
     }
     __syncthreads();
     if (warp != 0) return;
-    const int nw = min(MERGE_WARPS, c1 - c0 + 1);
-    for (int k = 1; k < nw; ++k) {
-      const float m = part[k][D], mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
+    for (int k = 1; k < MERGE_WARPS; ++k) {  // (a warp without parts has weight zero)
+      const float m = part[k][2 * D], mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
       M = mn;
-      l = l * f0 + part[k][D + 1] * f1;
+      l = l * f0 + part[k][2 * D + 1] * f1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * f0 + part[k][4 * lane + e] * f1;
+      for (int e = 0; e < 4; ++e) {
+        o[0][e] = o[0][e] * f0 + part[k][4 * lane + e] * f1;
+        o[1][e] = o[1][e] * f0 + part[k][D + 4 * lane + e] * f1;
+      }
     }
   }
-  const bool there = p.anc[(size_t)b * a.n + node] != 0;
+  // is the node there? (its chain of parents, two of them to a lane)
+  const int* par = a.parents + (size_t)b * a.n;
+  const int par_lo = lane < a.n ? par[lane] : -2, par_hi = lane + 32 < a.n ? par[lane + 32] : -2;
+  bool there = true;
+  for (int j = node; j >= 0;) {
+    const int x = __shfl_sync(FULL, par_lo, j & 31), y = __shfl_sync(FULL, par_hi, j & 31);
+    const int q = j < 32 ? x : y;
+    there = there && q >= -1 && q < j;
+    j = there ? q : -1;
+  }
   const float inv = there && l > 0.f ? 1.f / l : 0.f;
   const __half* sig = a.p.sigv + ((size_t)(a.layer0 + ll) * a.Hkv + h) * D + 4 * lane;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    o[e] = there ? o[e] * inv : 0.f;
-    if (a.sinkhorn) o[e] *= __half2float(sig[e]);
+    o[0][e] = there ? o[0][e] * inv : 0.f;
+    o[1][e] = there ? o[1][e] * inv : 0.f;
+    if (a.sinkhorn) o[0][e] *= __half2float(sig[e]);
   }
-  hadamard_warp(o[0], o[1], o[2], o[3], lane);
+  hadamard_warp(o[0][0], o[0][1], o[0][2], o[0][3], lane);
   const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
-  const float y[4] = {o[0] * C_WHT * sg.x, o[1] * C_WHT * sg.y, o[2] * C_WHT * sg.z, o[3] * C_WHT * sg.w};
+  const float y[4] = {o[0][0] * C_WHT * sg.x + o[1][0], o[0][1] * C_WHT * sg.y + o[1][1], o[0][2] * C_WHT * sg.z + o[1][2],
+                      o[0][3] * C_WHT * sg.w + o[1][3]};
   const size_t at = ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + node) * D + 4 * lane;
   if (a.in_bf16) {
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(y[0], y[1]), y1 = __floats2bfloat162_rn(y[2], y[3]);
@@ -933,52 +1002,32 @@ cudaError_t go(void (*kernel)(A...), unsigned grid, unsigned threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// sizes of a call, and its pointers into scratch (base may be null: sizes only); returns the scratch bytes
+// sizes of a call, and its records in scratch (which may be null: sizes only); returns the scratch bytes
 template <int KF, bool F32>
 size_t make_plan(const MultiArgs& a, int sms, Plan* p) {
-  using C = Cfg<KF, F32>;
   const int rows = a.n * a.g;
   p->a = a;
   p->rb = (rows + MAX_ROWS - 1) / MAX_ROWS;
   p->N = ((rows + p->rb - 1) / p->rb + 15) / 16 * 16;
   p->n_units = a.n_layers_call * a.batch * a.Hkv * p->rb;
-  // two CTAs an SM where their shared memory allows (1 KB each is the system's)
-  const size_t smem = Smem<KF, F32>::total(p->N) + (size_t)(a.batch + 1) * 4 + 2048;
-  p->G = sms * (!F32 && 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1);
-  p->raw_tiles = (raw_count(a.max_seq_len, a.W, a.n) + TILE - 1) / TILE;
-  p->q_image = p->N * C::KD * 2 * C::PL;
-  p->raw_image = 2 * C::PL * C::PLANE;
-  size_t o = 0;
-  const auto take = [&](size_t bytes) {
-    const size_t at = o;
-    o += align256(bytes);
-    return a.scratch ? a.scratch + at : nullptr;
-  };
-  p->anc = reinterpret_cast<unsigned long long*>(take((size_t)a.batch * a.n * 8));
-  p->q_images = take((size_t)p->n_units * p->q_image);
-  p->raw_images = take((size_t)(p->n_units / p->rb) * p->raw_tiles * p->raw_image);
-  p->records = reinterpret_cast<float*>(take((size_t)(p->n_units + p->G) * (2 * p->N + D * p->N) * 4));
-  return o;
+  p->G = sms * (F32 ? 1 : 2);  // two CTAs an SM (at most 80 KB of shared memory and 256 tensor-memory columns each)
+  p->records = reinterpret_cast<float*>(a.scratch);
+  return (size_t)(2 * p->n_units + p->G) * (2 * p->N + D * p->N) * 4;
 }
 
 template <int KF, bool F32>
 cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
-  constexpr int RPW = Cfg<KF, F32>::TQ ? 4 : 1;
   Plan p;
   make_plan<KF, F32>(a, sms, &p);
-  const long long items = (long long)p.n_units * (p.N / RPW) + 2LL * (p.n_units / p.rb) * p.raw_tiles * TILE;
-  const long long blocks = a.batch + (items + 7) / 8, out_rows = (long long)(p.n_units / p.rb) * a.n * a.g;
-  if (blocks > 0x7fffffffLL || out_rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = go(tree_prep_kernel<KF, F32>, (unsigned)blocks, THREADS, 0, false, s, p);
-  if (e != cudaSuccess) return e;
-  const size_t smem = Smem<KF, F32>::total(p.N) + (size_t)(a.batch + 1) * 4;
-  e = p.N == 16   ? go(tree_kernel<KF, 8, F32>, (unsigned)p.G, THREADS, smem, true, s, p)
-      : p.N == 32 ? go(tree_kernel<KF, 16, F32>, (unsigned)p.G, THREADS, smem, true, s, p)
-      : p.N == 48 ? go(tree_kernel<KF, 24, F32>, (unsigned)p.G, THREADS, smem, true, s, p)
-                  : go(tree_kernel<KF, 32, F32>, (unsigned)p.G, THREADS, smem, true, s, p);
+  const long long out_rows = (long long)(p.n_units / p.rb) * a.n * a.g;
+  if (out_rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const size_t pre = (size_t)(2 * a.batch + 1) * 4, smem = Smem<KF, F32>::total(p.N) + pre;
+  const cudaError_t e = p.N == 16   ? go(tree_kernel<KF, 8, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
+                        : p.N == 32 ? go(tree_kernel<KF, 16, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
+                        : p.N == 48 ? go(tree_kernel<KF, 24, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
+                                    : go(tree_kernel<KF, 32, F32>, (unsigned)p.G, THREADS, smem, false, s, p);
   if (e != cudaSuccess) return e;
   // many records a row (few units over all CTAs): a CTA per row, else a warp per row
-  const size_t pre = (size_t)(a.batch + 1) * 4;
   if (p.G > 8 * p.n_units) return go(tree_merge_kernel<true>, (unsigned)out_rows, MERGE_WARPS * 32, pre, true, s, p);
   return go(tree_merge_kernel<false>, (unsigned)((out_rows + MERGE_WARPS - 1) / MERGE_WARPS), MERGE_WARPS * 32, pre, true, s, p);
 }
