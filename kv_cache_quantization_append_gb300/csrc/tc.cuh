@@ -37,12 +37,21 @@ __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatil
   if (bar_try(bar, parity)) return;
   const unsigned long long t0 = gtimer();
   while (!bar_try(bar, parity)) {
+    if (*abort_flag) return;
     if (gtimer() - t0 > WAIT_NS) {
       atomicOr(status, KVQ_DEV_TIMEOUT);
       *abort_flag = 1;
       return;
     }
   }
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void cp16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");

@@ -14,7 +14,8 @@
 //  1. tree_kernel: the tiles of all units in one list, cut into equal ranges, one per CTA (stream-K).  Eight warps of a
 //     CTA dequantise K~, then V~ while the tensor cores run the logits, then take the softmax, then go on to the next
 //     K~ while the tensor cores run P V; a ninth issues the products (issuing them costs a warp about as long as they
-//     take, which the others would all wait for).  Two CTAs an SM fill each other's waits.  A range's part of a unit's
+//     take, which the others would all wait for) and the copies of the next tile's records, whose keys and values
+//     have one place each in shared memory (held in registers until used they spilled).  Two CTAs an SM fill each other's waits.  A range's part of a unit's
 //     records, and of its raw positions, ends as one partial record (reference, sum, O).
 //  2. tree_merge_kernel (a programmatic dependent): joins a row's records in a fixed order, undoes the balancing and
 //     the rotation.
@@ -40,6 +41,9 @@ constexpr int WARPS = WORKERS / 32;
 constexpr int THREADS = WORKERS + 32;  // and the warp that issues the products
 constexpr int MAX_ROWS = 64;  // rows per CTA
 constexpr int MERGE_WARPS = 8;
+// Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
+// a tile ahead), and belongs to the range that holds its first place.
+constexpr int RAW_PLACES = 3;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
 
 // what the launches share: sizes from the host, pointers into the caller's scratch
@@ -57,7 +61,7 @@ __host__ __device__ inline int quant_end(int L, int W, int n) {
   return e < 0 ? 0 : e > L ? L : e;
 }
 __device__ __forceinline__ int seq_tiles(const MultiArgs& a, int L) {
-  return (quant_end(L, a.W, a.n) + TILE - 1) / TILE + (raw_count(L, a.W, a.n) + TILE - 1) / TILE;
+  return (quant_end(L, a.W, a.n) + TILE - 1) / TILE + (raw_count(L, a.W, a.n) + TILE - 1) / TILE * RAW_PLACES;
 }
 // warp 0: the sequences' lengths (0 where out of range) and the exclusive prefix of their tiles, [batch + 1]
 __device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* lens, int* pre, bool flag) {
@@ -121,6 +125,11 @@ __device__ __forceinline__ uint2 pack4(float y0, float y1, float y2, float y3, i
   return odd ? make_uint2(__byte_perm(r, b, 0x5410), __byte_perm(r, b, 0x7632))
              : make_uint2(__byte_perm(a, r, 0x5410), __byte_perm(a, r, 0x7632));
 }
+__device__ __forceinline__ float2 load2_in(const void* base, int off, bool bf16) {
+  if (!bf16) return *reinterpret_cast<const float2*>(static_cast<const float*>(base) + off);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(base) + off);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ float lo_part(float v) { return v - __half2float(__float2half_rn(v)); }
 // store the four channels to a plane and, with F32, their lo parts to the next
 template <bool NIBBLE_ORDER, bool F32>
@@ -131,18 +140,27 @@ __device__ __forceinline__ void put4(uint8_t* dst, uint32_t plane, const float (
         pack4<NIBBLE_ORDER>(lo_part(y[0]), lo_part(y[1]), lo_part(y[2]), lo_part(y[3]), lane);
 }
 
-// ------------------------------------------------------------------ dequantising
-// one tile's words of this thread: keys of position t = tid & 127 (half hf of its record), values of the position pair
-// vp and rows 2 vr, 2 vr + 1
-template <int KF>
-struct Words {
-  uint4 k[KF == KVQ_Q8G32 ? 4 : 2];
-  uint4 km;         // Q4: scales and zeros
-  uint32_t kx;      // Q8: two scales; TQ: (norm, residual norm)
-  uint4 v[2];
-  uint32_t vs[4], vz[4];
-};
+// channels 4 lane .. + 3 of row r of a query image, in the order in which put_k leaves the keys' channels
+template <int KF, bool F32>
+__device__ __forceinline__ void put_q(uint8_t* img, int r, int N, uint32_t plane, const float (&y)[4], int lane) {
+  if (KF != KVQ_Q8G32) {
+    put4<KF == KVQ_Q4G32, F32>(img + km_off(r, 4 * lane & ~7, N) + 8 * (lane & 1), plane, y, lane);
+    return;
+  }
+  const int kk = lane >> 2, i0 = 2 * (lane & 1), at = 4 * (kk & 3) + (lane & 2);  // channels 16 kk + 4 (lane & 3) + e
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint32_t hi, lo;
+    split2(y[2 * p], y[2 * p + 1], hi, lo);
+    uint8_t* dst = img + km_off(r, 16 * (2 * (i0 + p) + (kk >> 2)) + at, N);
+    *reinterpret_cast<uint32_t*>(dst) = hi;
+    if (F32) *reinterpret_cast<uint32_t*>(dst + plane) = lo;
+  }
+}
 
+// ------------------------------------------------------------------ dequantising
+// A thread's part of a tile: keys of position t = tid & 127 (half hf of its record), values of the position pair vp and
+// rows 2 vr, 2 vr + 1.
 struct Lane {
   int t, hf, vp, vr;
 };
@@ -152,61 +170,17 @@ __device__ __forceinline__ Lane lane_of(int tid) {
   return {tid & 127, (tid >> 7) & 1, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3};
 }
 
-// physical pages of a tile, as the block table has them (-1: past the end)
-struct Pages {
-  int p[2];
-  __device__ __forceinline__ int of(bool second, int n_pages) const {
-    const int x = second ? p[1] : p[0];
-    return x < n_pages ? x : -1;
-  }
+// The records of a tile in shared memory: four half-pages' keys (main, metadata), then their values.
+template <int KF>
+struct Rec {
+  static constexpr int K_MAIN = KF == KVQ_Q8G32 ? 128 * HALF : 64 * HALF, V_MAIN = 64 * HALF;
+  static constexpr int K_META = (KF == KVQ_Q8G32 ? 8 : KF == KVQ_TQ3_QJL ? 4 : 16) * HALF, V_META = 16 * HALF;
+  static constexpr int KH = K_MAIN + K_META, VH = V_MAIN + V_META;  // of one half-page
+  static constexpr int V0 = 4 * KH, BYTES = 4 * (KH + VH);
 };
 
-template <int KF>
-__device__ __forceinline__ void load_k(const MultiArgs& a, const uint8_t* unit_pages, size_t page_stride, const Pages& pg,
-                                       const Lane& ln, Words<KF>& w) {
-  const int tt = ln.t & 31, phys = pg.of(ln.t & 64, a.L.n_pages);
-#pragma unroll
-  for (int i = 0; i < (KF == KVQ_Q8G32 ? 4 : 2); ++i) w.k[i] = make_uint4(0u, 0u, 0u, 0u);
-  w.km = make_uint4(0u, 0u, 0u, 0u);
-  w.kx = 0u;
-  if (phys < 0) return;
-  const uint8_t* hb = unit_pages + (size_t)phys * page_stride + (size_t)((ln.t >> 5) & 1) * a.L.half_bytes;
-  if (KF == KVQ_Q8G32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w.k[i] = __ldg(reinterpret_cast<const uint4*>(hb + tt * 128 + 16 * ((2 * i + ln.hf) ^ (tt & 1))));
-    w.kx = __ldg(reinterpret_cast<const uint32_t*>(hb + a.L.off_kmeta + tt * 8) + ln.hf);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) w.k[i] = __ldg(reinterpret_cast<const uint4*>(hb + tt * 64 + 32 * ln.hf) + i);
-    if (KF == KVQ_Q4G32) {
-      w.km = __ldg(reinterpret_cast<const uint4*>(hb + a.L.off_kmeta + tt * 16));
-    } else {
-      const unsigned short* m = reinterpret_cast<const unsigned short*>(hb + a.L.off_kmeta);
-      w.kx = (uint32_t)__ldg(m + tt) | ((uint32_t)__ldg(m + HALF + tt) << 16);
-    }
-  }
-}
-
-template <int KF>
-__device__ __forceinline__ void load_v(const MultiArgs& a, const uint8_t* unit_pages, size_t page_stride, const Pages& pg,
-                                       const Lane& ln, Words<KF>& w) {
-  const int phys = pg.of(ln.vp & 32, a.L.n_pages), pp = ln.vp & 15;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) w.v[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w.vs[i] = w.vz[i] = 0u;
-  if (phys < 0) return;
-  const uint8_t* hb = unit_pages + (size_t)phys * page_stride + (size_t)((ln.vp >> 4) & 1) * a.L.half_bytes;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w.v[i] = __ldg(reinterpret_cast<const uint4*>(hb + a.L.off_vmain + 128 * pp + 16 * ((2 * ln.vr + i + 2 * (pp & 3)) & 7)));
-  const uint32_t* m = reinterpret_cast<const uint32_t*>(hb + a.L.off_vmeta) + pp;
-#pragma unroll
-  for (int G = 0; G < 4; ++G) {
-    w.vs[G] = __ldg(m + 16 * G);
-    w.vz[G] = __ldg(m + 64 + 16 * G);
-  }
-}
+// physical page of position j of a sequence (-1: out of range)
+__device__ __forceinline__ int checked(int phys, int n_pages) { return phys < n_pages ? phys : -1; }
 
 __device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
@@ -231,122 +205,139 @@ __device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2
   }
 }
 
-// keys of the thread's position to its tensor-memory lane, 64 columns a plane (TQ3: the exact centroids)
-template <int KF, bool F32>
-__device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const Words<KF>& w, const uint4& cent) {
+// the 32 bytes at `at` as two words, the order in which they are read alternating over the lanes (fewer bank conflicts)
+__device__ __forceinline__ void lds32(const uint8_t* at, bool swap, uint4& a, uint4& b) {
+  const uint4 x = *reinterpret_cast<const uint4*>(at + (swap ? 16 : 0)), y = *reinterpret_cast<const uint4*>(at + (swap ? 0 : 16));
+  a = make_uint4(swap ? y.x : x.x, swap ? y.y : x.y, swap ? y.z : x.z, swap ? y.w : x.w);
+  b = make_uint4(swap ? x.x : y.x, swap ? x.y : y.y, swap ? x.z : y.z, swap ? x.w : y.w);
+}
+
+// keys of the thread's position to its tensor-memory lane, 64 columns a plane (TQ3: the exact centroids, or with
+// SIGNS the signs of the residual's projections as exact +-1)
+template <int KF, bool F32, bool SIGNS>
+__device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
+  using R = Rec<KF>;
+  const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
+  const int tt = ln.t & 31;
   if (KF == KVQ_Q4G32) {
-    const uint32_t sc[2] = {w.km.x, w.km.y}, zr[2] = {w.km.z, w.km.w};
+    uint4 k[2];
+    lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+    const uint4 km = *reinterpret_cast<const uint4*>(hb + R::K_MAIN + tt * 16);
+    const uint32_t sc[2] = {km.x, km.y}, zr[2] = {km.z, km.w};
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
       const uint32_t s2 = G & 1 ? dup_hi(sc[G >> 1]) : dup_lo(sc[G >> 1]), z2 = G & 1 ? dup_hi(zr[G >> 1]) : dup_lo(zr[G >> 1]);
       uint4 o[2], l[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        dequant8<F32>(G == 0 ? w.k[i].x : G == 1 ? w.k[i].y : G == 2 ? w.k[i].z : w.k[i].w, s2, z2, o[i], l[i]);
+      for (int i = 0; i < 2; ++i) dequant8<F32>(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, s2, z2, o[i], l[i]);
       tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
       if (F32) tm_st8(col + 64 + 16 * G + 8 * ln.hf, l[0], l[1]);
     }
   } else if (KF == KVQ_Q8G32) {
+    // in the order of the record: 16-byte chunk m = 2 i + h, its word w the channels 16 (4 h + w) + 2 i + {0, 1, 8, 9};
+    // chunk m lies at m ^ (t & 1)
     const __half2 off = u2h(0x64806480u);  // 1024 + 128
+    const uint2 sc = *reinterpret_cast<const uint2*>(hb + R::K_MAIN + tt * 8);
 #pragma unroll
-    for (int wi = 0; wi < 4; ++wi) {
-      const uint32_t s2 = wi & 2 ? dup_hi(w.kx) : dup_lo(w.kx);
+    for (int c = 0; c < 4; ++c) {
+      const uint4 q = *reinterpret_cast<const uint4*>(hb + tt * 128 + 64 * ln.hf + 16 * (c ^ (tt & 1)));
+      const uint32_t wd[4] = {q.x, q.y, q.z, q.w}, s = c & 1 ? sc.y : sc.x;
       uint32_t o[8], l[8];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t s2 = i & 2 ? dup_hi(s) : dup_lo(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t word = wi == 0 ? w.k[i].x : wi == 1 ? w.k[i].y : wi == 2 ? w.k[i].z : w.k[i].w;
-          const __half2 c = __hsub2(u2h(__byte_perm(word, 0x64646464u, x ? 0x4342 : 0x4140)), off);
+        for (int x = 0; x < 2; ++x) {
+          const __half2 v = __hsub2(u2h(__byte_perm(wd[i], 0x64646464u, x ? 0x4342 : 0x4140)), off);
           if (F32) {
             const float d = __low2float(u2h(s2));
-            const float2 f = __half22float2(c);
-            split2(d * f.x, d * f.y, o[4 * x + i], l[4 * x + i]);
+            const float2 f = __half22float2(v);
+            split2(d * f.x, d * f.y, o[2 * i + x], l[2 * i + x]);
           } else {
-            o[4 * x + i] = h2u(__hmul2(c, u2h(s2)));
+            o[2 * i + x] = h2u(__hmul2(v, u2h(s2)));
           }
         }
       }
-      const uint32_t at = col + 32 * ln.hf + 8 * wi;
+      const uint32_t at = col + 32 * ln.hf + 8 * c;
       tm_st8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
       if (F32) tm_st8(at + 64, make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]));
     }
   } else {
-    // the eight centroids' bytes in two register pairs (low bytes: cent.x, .y; high bytes: cent.z, .w), picked by
-    // byte permutes with the codes as selectors
+    uint4 k[2];
+    lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       uint4 o[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint4& q = w.k[i >> 2];
+        const uint4& q = k[i >> 2];
         const uint32_t word = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
-        const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
-        const uint32_t l0 = __byte_perm(cent.x, cent.y, sel), h0 = __byte_perm(cent.z, cent.w, sel);
-        const uint32_t l1 = __byte_perm(cent.x, cent.y, sel >> 16), h1 = __byte_perm(cent.z, cent.w, sel >> 16);
-        o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
-                          __byte_perm(l1, h1, 0x7362));
+        if (!SIGNS) {
+          // the eight centroids' bytes in two register pairs (low bytes: cent.x, .y; high bytes: cent.z, .w), picked by
+          // byte permutes with the codes as selectors
+          const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
+          const uint32_t l0 = __byte_perm(cent.x, cent.y, sel), h0 = __byte_perm(cent.z, cent.w, sel);
+          const uint32_t l1 = __byte_perm(cent.x, cent.y, sel >> 16), h1 = __byte_perm(cent.z, cent.w, sel >> 16);
+          o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                            __byte_perm(l1, h1, 0x7362));
+        } else {
+          // bit 6: projection 2j, bit 7: 2j + 1; set: +1.  Bytes 1 and 3 of the permute's result are all ones where the
+          // bit is set (it spreads the sign bit of a byte)
+          const uint32_t lo = word << 1;
+          uint32_t m[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t sel = (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12);
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m[j]) : "r"(lo), "r"(word), "r"(sel));
+            m[j] = 0xBC00BC00u ^ (m[j] & 0x80008000u);
+          }
+          o[x] = make_uint4(m[0], m[1], m[2], m[3]);
+        }
       }
       tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
     }
   }
 }
 
-// TQ3: the signs of the residual's projections, exactly +-1 (bit 6: projection 2j, bit 7: 2j + 1; set: +1)
-__device__ __forceinline__ void put_signs(uint32_t col, const Lane& ln, const Words<KVQ_TQ3_QJL>& w) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    uint32_t o[8];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint4& q = w.k[i >> 2];
-      const uint32_t hi = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
-      const uint32_t lo = hi << 1;  // bit 6 of each byte to its top
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // bytes 1 and 3: all ones where the bit is set (a permute that spreads the sign bit)
-        const uint32_t sel = (uint32_t)((8 + k) << 4) | (uint32_t)((12 + k) << 12);
-        uint32_t m;
-        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(lo), "r"(hi), "r"(sel));
-        o[4 * x + k] = 0xBC00BC00u ^ (m & 0x80008000u);
-      }
-    }
-    tm_st8(col + 32 * ln.hf + 4 * i, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-  }
-}
-
 // values of the thread's two positions, eight channels of each group; positions from `left` on (of the pair) are zero
 template <int KF, bool F32>
-__device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const Words<KF>& w, int left) {
+__device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t* rec, int left) {
+  using R = Rec<KF>;
   constexpr uint32_t PLANE = Cfg<KF, F32>::PLANE;
+  const uint8_t* hb = rec + R::V0 + (ln.vp >> 4) * R::VH;
+  const int pp = ln.vp & 15;
   const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;  // (records there may hold anything)
+  uint4 v[2];  // rows 2 vr and 2 vr + 1 stay neighbours in the rotated order of a pair's rows
+  lds32(hb + 128 * pp + 32 * ((ln.vr + pp) & 3), ln.vr & 1, v[0], v[1]);
+  const uint32_t* meta = reinterpret_cast<const uint32_t*>(hb + R::V_MAIN) + pp;
   uint8_t* base = vb + mm_off(8 * ln.vr, 2 * ln.vp);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool e = (i ^ ln.vr) & 1;  // which position of the pair
-    const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
-    uint8_t* dst = base + (e ? 16 : 0);
+  for (int G = 0; G < 4; ++G) {
+    const uint32_t w0 = G == 0 ? v[0].x : G == 1 ? v[0].y : G == 2 ? v[0].z : v[0].w;
+    const uint32_t w1 = G == 0 ? v[1].x : G == 1 ? v[1].y : G == 2 ? v[1].z : v[1].w;
+    const uint32_t vs = meta[16 * G] & keep, vz = meta[64 + 16 * G] & keep;
 #pragma unroll
-    for (int G = 0; G < 4; ++G) {
-      const uint32_t w0 = G == 0 ? w.v[0].x : G == 1 ? w.v[0].y : G == 2 ? w.v[0].z : w.v[0].w;
-      const uint32_t w1 = G == 0 ? w.v[1].x : G == 1 ? w.v[1].y : G == 2 ? w.v[1].z : w.v[1].w;
-      const uint32_t vs = w.vs[G] & keep, vz = w.vz[G] & keep;
+    for (int i = 0; i < 2; ++i) {
+      const bool e = (i ^ ln.vr) & 1;  // which position of the pair
+      const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
+      uint8_t* dst = base + (e ? 16 : 0) + 512 * G;
       uint4 o, l;
       dequant8<F32>(__byte_perm(w0, w1, pick), __byte_perm(vs, vs, dup), __byte_perm(vz, vz, dup), o, l);
-      *reinterpret_cast<uint4*>(dst + 512 * G) = o;
-      if (F32) *reinterpret_cast<uint4*>(dst + 512 * G + PLANE) = l;
+      *reinterpret_cast<uint4*>(dst) = o;
+      if (F32) *reinterpret_cast<uint4*>(dst + PLANE) = l;
     }
   }
 }
 
 // ------------------------------------------------------------------ 1. the tiles
-// dynamic shared memory: V planes | query image | P planes | prefix of the sequences' tiles
+// dynamic shared memory: V planes | query image | P planes | records | prefix of the sequences' tiles, lengths
 template <int KF, bool F32>
 struct Smem {
   using C = Cfg<KF, F32>;
   static constexpr uint32_t V = 0, Q = C::PL * C::PLANE;
   static __host__ __device__ constexpr uint32_t P(int N) { return Q + N * C::KD * 2 * C::PL; }
-  static __host__ __device__ constexpr uint32_t total(int N) { return P(N) + N * TILE * 2 * C::PL; }
+  static __host__ __device__ constexpr uint32_t R(int N) { return P(N) + N * TILE * 2 * C::PL; }
+  static __host__ __device__ constexpr uint32_t total(int N) { return R(N) + Rec<KF>::BYTES; }
 };
 
 template <int KF, int NC, bool F32>
@@ -355,15 +346,16 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   using SM = Smem<KF, F32>;
   constexpr int N = 2 * NC;  // rows, NC of them to a thread, CH at a time
   constexpr int CH = 8;
-  constexpr bool TQ = C::TQ, NIB = KF == KVQ_Q4G32;
+  constexpr bool TQ = C::TQ;
   // tensor memory: K (one or two planes of 64 columns) | S (TQ3: two) | O
   constexpr uint32_t C_S = 64 * C::PL, C_O = C_S + (TQ ? 2 * N : N), COLS = C_O + N;
   constexpr uint32_t TM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   constexpr uint32_t ID_S = idesc(TILE, N, false, false), ID_O = idesc(D, N, true, true);
   constexpr uint64_t LO_Q = (N * C::KD * 2) >> 4, LO_V = C::PLANE >> 4, LO_P = (N * TILE * 2) >> 4;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // k_bar: the keys of a tile are in place (one arrival a worker warp); p_bar: its values and weights are
-  __shared__ __align__(8) uint64_t k_bar, p_bar, qk_bar, pv_bar;
+  // kr_bar, vr_bar: a tile's records have landed; k_bar, v_bar: its keys, values are in place (one arrival a worker
+  // warp); p_bar: its weights are; qk_bar, pv_bar: its products are done
+  __shared__ __align__(8) uint64_t kr_bar, vr_bar, k_bar, v_bar, p_bar, qk_bar, pv_bar, end_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   __shared__ __align__(16) float mref[N], fac[N];
@@ -378,8 +370,12 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   int* lens = pre + a.batch + 1;
 
   if (tid == 0) {
+    bar_init(&kr_bar, 1);
+    bar_init(&vr_bar, 1);
     bar_init(&k_bar, WARPS);
+    bar_init(&v_bar, WARPS);
     bar_init(&p_bar, 1);
+    bar_init(&end_bar, 1);
     bar_init(&qk_bar, 1);
     bar_init(&pv_bar, 1);
     abort_sh = 0;
@@ -395,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
 
   // this CTA's range of the list of tiles
   const long long per_layer = (long long)pre[a.batch] * a.Hkv * p.rb, total = per_layer * a.n_layers_call;
-  const long long G = min((long long)p.G, total);  // no range is empty: the merge reads every range between a unit's ends
+  const long long G = min((long long)p.G, total);  // (no range is empty: the merge reads every range that has records of a unit)
   long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
   const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
 
@@ -408,7 +404,8 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     cent = make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.x, c.y, 0x7531),
                       __byte_perm(c.z, c.w, 0x7531));
   }
-  uint32_t k_phase = 0, p_phase = 0, qk_phase = 0, pv_phase = 0;
+  uint32_t kr_phase = 0, vr_phase = 0, k_phase = 0, v_phase = 0, p_phase = 0, qk_phase = 0, pv_phase = 0;
+  uint32_t kr_n = 0, vr_n = 0;  // copies that the ninth warp has begun
   bool pv_pending = false;
   const auto wait = [&](uint64_t* bar, uint32_t& phase) {
     bar_wait(bar, phase, &abort_sh, a.p.status);
@@ -443,17 +440,55 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     }
     const int b = lo, tiles = pre[b + 1] - pre[b];
     const long long r = in_layer - (long long)pre[b] * a.Hkv * p.rb;
-    const int hr = (int)quick_div(r, tiles), it0 = (int)(r - (long long)hr * tiles);
+    const int hr = (int)quick_div(r, tiles), place0 = (int)(r - (long long)hr * tiles);
     const int h = hr / p.rb, rbi = hr - h * p.rb, layer = a.layer0 + ll;
     const int u = ((ll * a.batch + b) * a.Hkv + h) * p.rb + rbi;
     const int L = lens[b], qend = quant_end(L, a.W, a.n), nq = (qend + TILE - 1) / TILE;
     // tiles of records come first, then those of raw positions; a part is of one kind
-    const bool raw = it0 >= nq;
-    const int it1 = (int)min((long long)(raw ? tiles : nq), it0 + (t_end - t));
-    t += it1 - it0;
+    const bool raw = place0 >= nq;
+    const int place1 = (int)min((long long)(raw ? tiles : nq), place0 + (t_end - t));
+    t += place1 - place0;
+    const int it0 = raw ? nq + (place0 - nq + RAW_PLACES - 1) / RAW_PLACES : place0;
+    const int it1 = raw ? nq + (place1 - nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    if (it0 == it1) continue;  // (the later places of a raw tile that an earlier range has)
 
+    const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
     if (warp == WARPS) {
-      // ================================================================ the products
+      // ================================================================ the products and the copies
+      const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
+      using R = Rec<KF>;
+      // the keys (or values) of tile `it`: lane i < 4 its half-page i (those past the end and on bad pages are left out:
+      // their positions are masked); phys: that half-page's page
+      const auto page_of = [&](int it) {
+        const int j = it * TILE + lane * HALF;
+        return lane < 4 && it < it1 && j < qend ? checked(__ldg(bt + j / PAGE), a.L.n_pages) : -1;
+      };
+      const auto copy = [&](int phys, bool keys) {
+        ++(keys ? kr_n : vr_n);
+        const uint32_t bytes = keys ? R::KH : R::VH;
+        const int n = __popc(__ballot_sync(FULL, phys >= 0));
+        uint64_t* bar = keys ? &kr_bar : &vr_bar;
+        if (lane == 0) bar_expect(bar, n * bytes);
+        __syncwarp();
+        if (phys >= 0) {
+          const uint8_t* src = unit_pages + (size_t)phys * page_stride + (lane & 1) * (size_t)(R::KH + R::VH);
+          uint8_t* dst = smem + SM::R(N) + (keys ? lane * R::KH : R::V0 + lane * R::VH);
+          if (keys) {
+            bulk_g2s(dst, src, R::K_MAIN, bar);
+            bulk_g2s(dst + R::K_MAIN, src + R::K_MAIN + R::V_MAIN, R::K_META, bar);
+          } else {
+            bulk_g2s(dst, src + R::K_MAIN, R::V_MAIN, bar);
+            bulk_g2s(dst + R::V_MAIN, src + R::K_MAIN + R::V_MAIN + R::K_META, R::V_META, bar);
+          }
+        }
+        __syncwarp();
+      };
+      int phys = -1;
+      if (!raw) {
+        phys = page_of(it0);
+        copy(phys, true);
+        copy(phys, false);
+      }
       if (TQ && !raw) {
         // S q~ of every row: the projection lies in the values' place
         wait(&k_bar, k_phase);
@@ -472,8 +507,10 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       for (int it = it0; it < it1; ++it) {
         // logits: a k-step of 16 channels is 8 columns of K and 32 N bytes of the queries; TQ3 records come twice, the
         // centroids and then, in their place, the signs
+        if (!raw) phys = page_of(it + 1);
         for (int part = 0; part < (TQ && !raw ? 2 : 1); ++part) {
           wait(&k_bar, k_phase);
+          if (*(volatile int*)&abort_sh) break;
           fence_after();
           uint64_t qa = sdesc(sbase + SM::Q + (part ? N * 256 : 0), N * 16, 128);
           uint32_t ka = tmem;
@@ -488,6 +525,10 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
           }
           mma_commit(&qk_bar);
         }
+        if (!raw && it + 1 < it1) copy(phys, true);  // the workers have read this tile's keys
+        wait(&v_bar, v_phase);
+        if (*(volatile int*)&abort_sh) break;
+        if (!raw && it + 1 < it1) copy(phys, false);
         // O += V^T P: a k-step of 16 positions is 4096 bytes of V and 32 N of P
         wait(&p_bar, p_phase);
         if (*(volatile int*)&abort_sh) break;
@@ -510,16 +551,10 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     // ================================================================ the workers
     const int nraw = raw_count(L, a.W, a.n), nring = nraw - a.n, rows = a.n * a.g;
     const int full_end = a.W > 0 ? L - a.W + 1 : L;  // positions below are read through records by every node
-    const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
-    const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
-    const auto pages_of = [&](int it) {
-      Pages g;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = it * TILE + i * PAGE;
-        g.p[i] = it < nq && j < qend ? __ldg(bt + j / PAGE) : -1;  // (checked where it is used, a tile later)
-      }
-      return g;
+    // pages of this thread's position and pair of tile `it` (read a tile ahead)
+    const auto page_of = [&](int it, bool second) {
+      const int j = it * TILE + (second ? PAGE : 0);
+      return it < it1 && !raw && j < qend ? __ldg(bt + j / PAGE) : -1;
     };
     // ---- its queries (to the values' place), the parents and the first pages are requested together
     constexpr int ESZ = F32 ? 4 : 2, Q_CHUNKS = D * ESZ / 16;
@@ -532,10 +567,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     }
     const bool masked = raw || it1 * TILE > full_end;  // some position is not for every node
     if (masked && tid < a.n) par[tid] = a.parents[(size_t)b * a.n + tid];
-    Words<KF> w;
-    Pages pg = pages_of(it0), pg1 = pages_of(it0 + 1);
-    load_k<KF>(a, unit_pages, page_stride, pg, ln, w);
-    load_v<KF>(a, unit_pages, page_stride, pg, ln, w);
+    int page = page_of(it0, ln.t & 64), vpage = page_of(it0, ln.vp & 32);
     if (tid < N) mref[tid] = NO_REF;
     cp_wait();
     part_sync(1, WORKERS);
@@ -554,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         y[e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
         if (a.sinkhorn && !raw) y[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
       }
-      put4<NIB, F32>(smem + SM::Q + km_off(r1, 4 * lane & ~7, N) + 8 * (lane & 1), N * C::KD * 2, y, lane);
+      put_q<KF, F32>(smem + SM::Q, r1, N, N * C::KD * 2, y, lane);
     }
     if (masked) {
       // ---- the nodes' ancestors, and what they are to this block's columns
@@ -643,13 +675,21 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
           return static_cast<const uint8_t*>(kv ? a.v : a.k) + ((((size_t)ll * a.batch + b) * a.Hkv + h) * a.n + x - nring) * D * ESZ;
         return nullptr;
       };
-      const auto raw_group = [&](const void* row, int kg, bool places, uint4& o, uint4& l) {
+      const auto raw_group = [&](const void* row, int kg, bool key, uint4& o, uint4& l) {
         float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
         if (row) {
-          f0 = load4_in(row, 8 * kg, !F32 && x >= nring);
-          f1 = load4_in(row, 8 * kg + 4, !F32 && x >= nring);
+          const bool bf = !F32 && x >= nring;
+          if (KF == KVQ_Q8G32 && key) {  // words 2 (kg & 1) and + 1 of chunk kg >> 1
+            const int c = 64 * ((kg >> 1) & 1) + 32 * (kg & 1) + 2 * (kg >> 2);
+            const float2 p0 = load2_in(row, c, bf), p1 = load2_in(row, c + 8, bf), p2 = load2_in(row, c + 16, bf), p3 = load2_in(row, c + 24, bf);
+            f0 = make_float4(p0.x, p0.y, p1.x, p1.y);
+            f1 = make_float4(p2.x, p2.y, p3.x, p3.y);
+          } else {
+            f0 = load4_in(row, 8 * kg, bf);
+            f1 = load4_in(row, 8 * kg + 4, bf);
+          }
         }
-        if (places) {  // 0 4 1 5 2 6 3 7
+        if (!key || KF == KVQ_Q4G32) {  // 0 4 1 5 2 6 3 7
           split2(f0.x, f1.x, o.x, l.x);
           split2(f0.y, f1.y, o.y, l.y);
           split2(f0.z, f1.z, o.z, l.z);
@@ -664,17 +704,23 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       // ---- keys (the previous tile's logits are done: its softmax has read them)
       uint32_t ng = 0;  // TQ3: norm and residual norm of this thread's position
       bool valid = true;
+      const uint8_t* rec_sh = smem + SM::R(N);
       if (!raw) {
-        put_k<KF, F32>(lane_addr, ln, w, cent);
-        ng = w.kx;
-        valid = pg.of(ln.t & 64, a.L.n_pages) >= 0;
+        valid = checked(page, a.L.n_pages) >= 0;
         if (!valid && it * TILE + (ln.t & 64) < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
+        page = page_of(it + 1, ln.t & 64);
+        wait(&kr_bar, kr_phase);
+        put_k<KF, F32, false>(lane_addr, ln, rec_sh, cent);
+        if (TQ) {
+          const unsigned short* m = reinterpret_cast<const unsigned short*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN);
+          ng = m[ln.t & 31] | (uint32_t)m[HALF + (ln.t & 31)] << 16;
+        }
       } else {
         const void* row = raw_row(0);
 #pragma unroll 4
         for (int i = 0; i < 8; ++i) {
           uint4 o, l;
-          raw_group(row, 8 * ln.hf + i, NIB, o, l);
+          raw_group(row, 8 * ln.hf + i, true, o, l);
           tm_st4(lane_addr + 32 * ln.hf + 4 * i, o);
           if (F32) tm_st4(lane_addr + 64 + 32 * ln.hf + 4 * i, l);
         }
@@ -683,31 +729,28 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       // ---- values, while the logits run (the previous tile's P V must be done with their place)
       wait_pv();
       if (!raw) {
-        put_v<KF, F32>(smem + SM::V, ln, w, qend - it * TILE - 2 * ln.vp);
+        wait(&vr_bar, vr_phase);
+        put_v<KF, F32>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
+        vpage = page_of(it + 1, ln.vp & 32);
       } else {
         const void* row = raw_row(1);
 #pragma unroll 4
         for (int i = 0; i < 8; ++i) {
           const int kg = 8 * ln.hf + i;
           uint4 o, l;
-          raw_group(row, kg, true, o, l);
+          raw_group(row, kg, false, o, l);
           *reinterpret_cast<uint4*>(smem + SM::V + mm_off(8 * kg, ln.t)) = o;
           if (F32) *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + mm_off(8 * kg, ln.t)) = l;
         }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&v_bar);
       if (TQ && !raw) {
         // the projections' signs take the centroids' place
         wait(&qk_bar, qk_phase);
         fence_after();
-        if constexpr (TQ) put_signs(lane_addr, ln, w);
+        if constexpr (TQ) put_k<KF, F32, true>(lane_addr, ln, rec_sh, cent);
         k_done();
-      }
-      // the next tile's words (its page numbers were read a tile earlier)
-      if (it + 1 < it1 && !raw) {
-        load_k<KF>(a, unit_pages, page_stride, pg1, ln, w);
-        load_v<KF>(a, unit_pages, page_stride, pg1, ln, w);
-        pg = pg1;
-        pg1 = pages_of(it + 2);
       }
       // ---- which of the thread's columns attend to its position: by records a node at depth d reads j <= L + d - W,
       // raw ones the rest, drafts its ancestors and itself
@@ -732,19 +775,20 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       fence_after();
       const float nn = TQ && !raw ? __low2float(u2h(ng)) : 1.f;
       const float nw = TQ && !raw ? nn * QJL_CONST * __high2float(u2h(ng)) : 0.f;
-      // CH columns' logits less `ref` from tensor memory
+      // CH columns' logits from tensor memory: requested, then waited for and finished less `ref`
+      float xs[CH], ys[TQ ? CH : 1];
+      const auto request = [&](int c) {
+        tm_ld(lane_addr + C_S + col0 + c, xs);
+        if constexpr (TQ) {
+          if (!raw) tm_ld(lane_addr + C_S + N + col0 + c, ys);
+        }
+      };
       const auto logits = [&](int c, float (&x)[CH], const float (&ref)[CH]) {
-        tm_ld(lane_addr + C_S + col0 + c, x);
-        if (TQ && !raw) {
-          float y[CH];
-          tm_ld(lane_addr + C_S + N + col0 + c, y);
-          tm_wait_ld();
+        tm_wait_ld();
 #pragma unroll
-          for (int i = 0; i < CH; ++i) x[i] = fmaf(y[i], nw, fmaf(x[i], nn, -ref[i]));
-        } else {
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < CH; ++i) x[i] -= ref[i];
+        for (int i = 0; i < CH; ++i) {
+          if constexpr (TQ) x[i] = raw ? xs[i] - ref[i] : fmaf(ys[i], nw, fmaf(xs[i], nn, -ref[i]));
+          else x[i] = xs[i] - ref[i];
         }
         if (!all) {
 #pragma unroll
@@ -761,6 +805,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
           for (int c = 0; c < NC; c += CH) {
             float x[CH];
             const float zero[CH] = {};
+            request(c);
             logits(c, x, zero);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -794,6 +839,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
           }
         }
         bool over = false;
+        request(0);
 #pragma unroll
         for (int c = 0; c < NC; c += CH) {
           float x[CH], ref[CH];
@@ -803,6 +849,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
             ref[i] = m.x, ref[i + 1] = m.y, ref[i + 2] = m.z, ref[i + 3] = m.w;
           }
           logits(c, x, ref);
+          if (c + CH < NC) request(c + CH);
           uint32_t ph[CH / 2], pl[CH / 2];
 #pragma unroll
           for (int i = 0; i < CH; ++i) x[i] = ex2(x[i]);
@@ -864,12 +911,17 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       rec[N + tid] = wmax[0][tid] + wmax[1][tid] + wmax[2][tid] + wmax[3][tid];
     }
   }
-  // products still running (a CTA that gave up) land before the columns are freed; the wait is bounded
+  // what a CTA that gave up still has under way, copies and products, lands before it leaves; the waits are bounded
   if (warp == WARPS && !ok) {
-    mma_commit(&pv_bar);
-    const unsigned long long t0 = gtimer();
-    while (!bar_try(&pv_bar, pv_phase) && gtimer() - t0 < WAIT_NS) {
-    }
+    const auto land = [&](uint64_t* bar, uint32_t parity) {
+      const unsigned long long t0 = gtimer();
+      while (!bar_try(bar, parity) && gtimer() - t0 < WAIT_NS) {
+      }
+    };
+    if (kr_n) land(&kr_bar, (kr_n - 1) & 1);
+    if (vr_n) land(&vr_bar, (vr_n - 1) & 1);
+    mma_commit(&end_bar);
+    land(&end_bar, 0);
   }
   fence_before();
   __syncthreads();
@@ -905,27 +957,34 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
   // the row's parts: first those of the records (o[0]), then those of the raw positions (o[1]), each kind in the order of
   // the ranges; range c holds tile x for c = floor(((x + 1) G - 1) / total)
   float M = NO_REF, l = 0.f, o[2][4] = {};
+  const auto owner = [&](long long x) { return (int)quick_div((x + 1) * G - 1, total); };
+  const auto add = [&](int kind, int c) {
+    const float* rec = p.records + (size_t)(2 * u + kind + c) * rec_floats;
+    const float m = rec[col], s = rec[p.N + col];
+    const float4 x = *reinterpret_cast<const float4*>(rec + 2 * p.N + (size_t)col * D + 4 * lane);
+    const float mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
+    M = mn;
+    l = l * f0 + s * f1;
+    if (kind) {
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const long long x0 = first + (kind ? nq : 0), x1 = first + (kind ? tiles : nq);
-    if (x0 == x1) continue;
-    const int c0 = (int)quick_div((x0 + 1) * G - 1, total), c1 = (int)quick_div(x1 * G - 1, total);
+      for (int e = 0; e < 4; ++e) o[0][e] *= f0;
+    }
+    o[kind][0] = o[kind][0] * f0 + x.x * f1;
+    o[kind][1] = o[kind][1] * f0 + x.y * f1;
+    o[kind][2] = o[kind][2] * f0 + x.z * f1;
+    o[kind][3] = o[kind][3] * f0 + x.w * f1;
+  };
+  if (nq > 0) {
+    const int c0 = owner(first), c1 = owner(first + nq - 1);
 #pragma unroll 4
-    for (int c = c0 + (WIDE ? warp : 0); c <= c1; c += WIDE ? MERGE_WARPS : 1) {
-      const float* rec = p.records + (size_t)(2 * u + kind + c) * rec_floats;
-      const float m = rec[col], s = rec[p.N + col];
-      const float4 x = *reinterpret_cast<const float4*>(rec + 2 * p.N + (size_t)col * D + 4 * lane);
-      const float mn = fmaxf(M, m), f0 = ex2(M - mn), f1 = ex2(m - mn);
-      M = mn;
-      l = l * f0 + s * f1;
-      if (kind) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[0][e] *= f0;
-      }
-      o[kind][0] = o[kind][0] * f0 + x.x * f1;
-      o[kind][1] = o[kind][1] * f0 + x.y * f1;
-      o[kind][2] = o[kind][2] * f0 + x.z * f1;
-      o[kind][3] = o[kind][3] * f0 + x.w * f1;
+    for (int c = c0 + (WIDE ? warp : 0); c <= c1; c += WIDE ? MERGE_WARPS : 1) add(0, c);
+  }
+  if (!WIDE || warp == MERGE_WARPS - 1) {
+    int last = -1;
+    for (int x = nq; x < tiles; x += RAW_PLACES) {
+      const int c = owner(first + x);
+      if (c != last) add(1, c);
+      last = c;
     }
   }
   if (WIDE) {
