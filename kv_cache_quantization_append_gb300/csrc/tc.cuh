@@ -31,12 +31,22 @@ __device__ __forceinline__ unsigned long long gtimer() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// try_wait that may sleep up to about 20 us for the phase
+__device__ __forceinline__ bool bar_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait on a phase; one that gives up flags the status word and the CTA's abort flag, which every
 // thread reads behind the CTA's next barrier
 __device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  if (bar_try(bar, parity)) return;
+  if (bar_sleep(bar, parity)) return;
   const unsigned long long t0 = gtimer();
-  while (!bar_try(bar, parity)) {
+  while (!bar_sleep(bar, parity)) {
     if (*abort_flag) return;
     if (gtimer() - t0 > WAIT_NS) {
       atomicOr(status, KVQ_DEV_TIMEOUT);
@@ -153,6 +163,13 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   const float2 hf = __half22float2(h);
   hi = h2u(h);
   lo = h2u(__floats2half2_rn(a - hf.x, b - hf.y));
+}
+
+// a byte permute whose selector is taken as it is (the intrinsic masks it first)
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
 }
 
 // Eight 4-bit codes of a word whose byte k holds codes 2k (low nibble) and 2k + 1, as exact fp16 in the order

@@ -23,9 +23,9 @@
 // it once cost 6 us of latency.
 //
 // Operands: bf16 caches take each of K~, V~, Q~ and P rounded once to fp16 (2^-11, an eighth of the bf16 output's own
-// rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys need
-// no rounding: the centroids and the signs are exact, their two products go to two accumulators, and the thread that
-// owns the position joins them as n (S1 + w S2).
+// rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys are
+// [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w = sqrt(pi/2)/128 gamma rounds
+// once (hi and lo for float caches), and the thread that owns the position multiplies by the norm n.
 #pragma once
 
 #include "tc.cuh"
@@ -101,6 +101,8 @@ struct Cfg {
   static constexpr int PL = F32 ? 2 : 1;            // fp16 planes per value
   static constexpr int KD = TQ ? 256 : 128;         // width of a query image: [q~] or [q~, S q~]
   static constexpr uint32_t PLANE = TILE * D * 2;   // 32 KB
+  // columns of keys in tensor memory: KD / 2 (hi), then lo (TQ3: of the weights and of raw keys only, which share them)
+  static constexpr uint32_t K_COLS = KD / 2 + (F32 ? 64 : 0);
 };
 
 // byte offset of (row, k) in a K-major operand of R rows
@@ -212,9 +214,9 @@ __device__ __forceinline__ void lds32(const uint8_t* at, bool swap, uint4& a, ui
   b = make_uint4(swap ? x.x : y.x, swap ? x.y : y.y, swap ? x.z : y.z, swap ? x.w : y.w);
 }
 
-// keys of the thread's position to its tensor-memory lane, 64 columns a plane (TQ3: the exact centroids, or with
-// SIGNS the signs of the residual's projections as exact +-1)
-template <int KF, bool F32, bool SIGNS>
+// keys of the thread's position to its tensor-memory lane: columns 0..63 (TQ3: centroids), then TQ3's signed weights,
+// then the lo parts
+template <int KF, bool F32>
 __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
   using R = Rec<KF>;
   const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
@@ -265,36 +267,39 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
   } else {
     uint4 k[2];
     lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+    const float wf = QJL_CONST * __half2float(reinterpret_cast<const __half*>(hb + R::K_MAIN)[HALF + tt]);
+    uint32_t wh, wl;
+    split2(wf, wf, wh, wl);
+    wh ^= 0x80008000u;  // -w
+    wl ^= 0x80008000u;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      uint4 o[2];
+      uint4 o[2], s[2], l[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint4& q = k[i >> 2];
         const uint32_t word = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
-        if (!SIGNS) {
-          // the eight centroids' bytes in two register pairs (low bytes: cent.x, .y; high bytes: cent.z, .w), picked by
-          // byte permutes with the codes as selectors
-          const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
-          const uint32_t l0 = __byte_perm(cent.x, cent.y, sel), h0 = __byte_perm(cent.z, cent.w, sel);
-          const uint32_t l1 = __byte_perm(cent.x, cent.y, sel >> 16), h1 = __byte_perm(cent.z, cent.w, sel >> 16);
-          o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
-                            __byte_perm(l1, h1, 0x7362));
-        } else {
-          // bit 6: projection 2j, bit 7: 2j + 1; set: +1.  Bytes 1 and 3 of the permute's result are all ones where the
-          // bit is set (it spreads the sign bit of a byte)
-          const uint32_t lo = word << 1;
-          uint32_t m[4];
+        // the eight centroids' bytes in two register pairs (low bytes: cent.x, .y; high bytes: cent.z, .w), picked by
+        // byte permutes with the codes as selectors
+        const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
+        const uint32_t l0 = prmt(cent.x, cent.y, sel), h0 = prmt(cent.z, cent.w, sel);
+        const uint32_t l1 = prmt(cent.x, cent.y, sel >> 16), h1 = prmt(cent.z, cent.w, sel >> 16);
+        o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                          __byte_perm(l1, h1, 0x7362));
+        // bit 6: sign of projection 2j, bit 7: of 2j + 1 (set: +w): a permute that spreads a byte's top bit
+        const uint32_t lo = word << 1;
+        uint32_t m[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t sel = (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12);
-            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m[j]) : "r"(lo), "r"(word), "r"(sel));
-            m[j] = 0xBC00BC00u ^ (m[j] & 0x80008000u);
-          }
-          o[x] = make_uint4(m[0], m[1], m[2], m[3]);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t pick = (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12);
+          m[j] = prmt(lo, word, pick) & 0x80008000u;
         }
+        s[x] = make_uint4(wh ^ m[0], wh ^ m[1], wh ^ m[2], wh ^ m[3]);
+        if (F32) l[x] = make_uint4(wl ^ m[0], wl ^ m[1], wl ^ m[2], wl ^ m[3]);
       }
       tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
+      tm_st8(col + 64 + 32 * ln.hf + 4 * i, s[0], s[1]);
+      if (F32) tm_st8(col + 128 + 32 * ln.hf + 4 * i, l[0], l[1]);
     }
   }
 }
@@ -322,7 +327,7 @@ __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t
       const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
       uint8_t* dst = base + (e ? 16 : 0) + 512 * G;
       uint4 o, l;
-      dequant8<F32>(__byte_perm(w0, w1, pick), __byte_perm(vs, vs, dup), __byte_perm(vz, vz, dup), o, l);
+      dequant8<F32>(prmt(w0, w1, pick), prmt(vs, vs, dup), prmt(vz, vz, dup), o, l);
       *reinterpret_cast<uint4*>(dst) = o;
       if (F32) *reinterpret_cast<uint4*>(dst + PLANE) = l;
     }
@@ -347,8 +352,8 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   constexpr int N = 2 * NC;  // rows, NC of them to a thread, CH at a time
   constexpr int CH = 8;
   constexpr bool TQ = C::TQ;
-  // tensor memory: K (one or two planes of 64 columns) | S (TQ3: two) | O
-  constexpr uint32_t C_S = 64 * C::PL, C_O = C_S + (TQ ? 2 * N : N), COLS = C_O + N;
+  // tensor memory: K | S | O
+  constexpr uint32_t C_S = C::K_COLS, C_O = C_S + N, COLS = C_O + N;
   constexpr uint32_t TM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   constexpr uint32_t ID_S = idesc(TILE, N, false, false), ID_O = idesc(D, N, true, true);
   constexpr uint64_t LO_Q = (N * C::KD * 2) >> 4, LO_V = C::PLANE >> 4, LO_P = (N * TILE * 2) >> 4;
@@ -505,22 +510,26 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         mma_commit(&qk_bar);
       }
       for (int it = it0; it < it1; ++it) {
-        // logits: a k-step of 16 channels is 8 columns of K and 32 N bytes of the queries; TQ3 records come twice, the
-        // centroids and then, in their place, the signs
+        // logits: a k-step of 16 channels is 8 columns of K and 32 N bytes of the queries
         if (!raw) phys = page_of(it + 1);
-        for (int part = 0; part < (TQ && !raw ? 2 : 1); ++part) {
-          wait(&k_bar, k_phase);
-          if (*(volatile int*)&abort_sh) break;
-          fence_after();
-          uint64_t qa = sdesc(sbase + SM::Q + (part ? N * 256 : 0), N * 16, 128);
+        wait(&k_bar, k_phase);
+        if (*(volatile int*)&abort_sh) break;
+        fence_after();
+        {
+          uint64_t qa = sdesc(sbase + SM::Q, N * 16, 128);
           uint32_t ka = tmem;
-          const uint32_t d = tmem + C_S + (part ? N : 0);
-#pragma unroll 1
+#pragma unroll 4
           for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
-            mma_ts(d, ka, qa, ID_S, ks > 0);
-            if (F32) {
-              mma_ts(d, ka, qa + LO_Q, ID_S, 1);
-              if (!TQ || raw) mma_ts(d, ka + 64, qa, ID_S, 1);
+            mma_ts(tmem + C_S, ka, qa, ID_S, ks > 0);
+            if (F32) mma_ts(tmem + C_S, ka, qa + LO_Q, ID_S, 1);
+            if (F32 && (!TQ || raw)) mma_ts(tmem + C_S, ka + C::KD / 2, qa, ID_S, 1);
+          }
+          if (TQ && !raw) {  // the signed weights against S q~
+#pragma unroll 4
+            for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
+              mma_ts(tmem + C_S, ka, qa, ID_S, 1);
+              if (F32) mma_ts(tmem + C_S, ka, qa + LO_Q, ID_S, 1);
+              if (F32) mma_ts(tmem + C_S, ka + 64, qa, ID_S, 1);
             }
           }
           mma_commit(&qk_bar);
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         if (*(volatile int*)&abort_sh) break;
         fence_after();
         uint64_t va = sdesc(sbase + SM::V, 2048, 128), pa = sdesc(sbase + SM::P(N), N * 16, 128);
-#pragma unroll 1
+#pragma unroll 4
         for (int ks = 0; ks < TILE / 16; ++ks, va += 256, pa += 2 * N) {
           mma_ss(tmem + C_O, va, pa, ID_O, it > it0 || ks > 0);
           if (F32) {
@@ -702,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         }
       };
       // ---- keys (the previous tile's logits are done: its softmax has read them)
-      uint32_t ng = 0;  // TQ3: norm and residual norm of this thread's position
+      float nn = 1.f;  // TQ3: norm of this thread's position
       bool valid = true;
       const uint8_t* rec_sh = smem + SM::R(N);
       if (!raw) {
@@ -710,11 +719,8 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         if (!valid && it * TILE + (ln.t & 64) < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
         page = page_of(it + 1, ln.t & 64);
         wait(&kr_bar, kr_phase);
-        put_k<KF, F32, false>(lane_addr, ln, rec_sh, cent);
-        if (TQ) {
-          const unsigned short* m = reinterpret_cast<const unsigned short*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN);
-          ng = m[ln.t & 31] | (uint32_t)m[HALF + (ln.t & 31)] << 16;
-        }
+        put_k<KF, F32>(lane_addr, ln, rec_sh, cent);
+        if (TQ) nn = __half2float(reinterpret_cast<const __half*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN)[ln.t & 31]);
       } else {
         const void* row = raw_row(0);
 #pragma unroll 4
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
           uint4 o, l;
           raw_group(row, 8 * ln.hf + i, true, o, l);
           tm_st4(lane_addr + 32 * ln.hf + 4 * i, o);
-          if (F32) tm_st4(lane_addr + 64 + 32 * ln.hf + 4 * i, l);
+          if (F32) tm_st4(lane_addr + C::KD / 2 + 32 * ln.hf + 4 * i, l);
         }
       }
       k_done();
@@ -745,13 +751,6 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&v_bar);
-      if (TQ && !raw) {
-        // the projections' signs take the centroids' place
-        wait(&qk_bar, qk_phase);
-        fence_after();
-        if constexpr (TQ) put_k<KF, F32, true>(lane_addr, ln, rec_sh, cent);
-        k_done();
-      }
       // ---- which of the thread's columns attend to its position: by records a node at depth d reads j <= L + d - W,
       // raw ones the rest, drafts its ancestors and itself
       uint32_t bits = 0xffffffffu;
@@ -773,22 +772,14 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       // ---- softmax down the thread's columns
       wait(&qk_bar, qk_phase);
       fence_after();
-      const float nn = TQ && !raw ? __low2float(u2h(ng)) : 1.f;
-      const float nw = TQ && !raw ? nn * QJL_CONST * __high2float(u2h(ng)) : 0.f;
       // CH columns' logits from tensor memory: requested, then waited for and finished less `ref`
-      float xs[CH], ys[TQ ? CH : 1];
-      const auto request = [&](int c) {
-        tm_ld(lane_addr + C_S + col0 + c, xs);
-        if constexpr (TQ) {
-          if (!raw) tm_ld(lane_addr + C_S + N + col0 + c, ys);
-        }
-      };
+      float xs[CH];
+      const auto request = [&](int c) { tm_ld(lane_addr + C_S + col0 + c, xs); };
       const auto logits = [&](int c, float (&x)[CH], const float (&ref)[CH]) {
         tm_wait_ld();
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          if constexpr (TQ) x[i] = raw ? xs[i] - ref[i] : fmaf(ys[i], nw, fmaf(xs[i], nn, -ref[i]));
-          else x[i] = xs[i] - ref[i];
+          x[i] = TQ ? fmaf(xs[i], nn, -ref[i]) : xs[i] - ref[i];
         }
         if (!all) {
 #pragma unroll
