@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libkvq.so")
 SOURCES = ["api.cu", "append.cu", "append_bulk.cu", "blocks.cu", "calibrate.cu", "decode.cu", "evict.cu", "multi.cu",
-           "noalloc.cu", "prefill.cu", "rope.cu", "tree_q4.cu", "tree_q8.cu", "tree_tq3.cu"]
+           "noalloc.cu", "prefill.cu", "rope.cu", "tree_q4.cu", "tree_q8.cu", "tree_tq3.cu",
+           "weights_q4.cu", "weights_q8.cu", "weights_tq3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off",
          "--expt-relaxed-constexpr"]

@@ -526,7 +526,7 @@ int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void
 size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries) {
   MultiArgs a;
   if (multi_args(cache, layer, batch, n_queries, &a) != KVQ_OK) return 0;
-  return std::max<size_t>(256, weights_scratch_bytes(a));
+  return std::max<size_t>(256, weights_scratch_bytes(a, decode_ctas(cache->device)));
 }
 
 int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* weights, float decay,
@@ -545,7 +545,9 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
   a.decay = decay;
   a.seq_lens = seq_lens;
   a.scratch = static_cast<uint8_t*>(scratch);
-  return cuda_err(launch_weights(a, static_cast<cudaStream_t>(stream)));
+  const int sms = decode_ctas(cache->device);
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  return cuda_err(launch_weights(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 static int evict_args(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget, EvictArgs* a) {

@@ -168,8 +168,8 @@ struct MultiArgs {
 };
 size_t tree_scratch_bytes(const MultiArgs& a, int sms);
 cudaError_t launch_tree(const MultiArgs& a, int sms, cudaStream_t s);
-size_t weights_scratch_bytes(const MultiArgs& a);
-cudaError_t launch_weights(const MultiArgs& a, cudaStream_t s);
+size_t weights_scratch_bytes(const MultiArgs& a, int sms);
+cudaError_t launch_weights(const MultiArgs& a, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__

@@ -28,22 +28,16 @@
 // once (hi and lo for float caches), and the thread that owns the position multiplies by the norm n.
 #pragma once
 
-#include "tc.cuh"
+#include "records.cuh"
 
 namespace kvq {
 namespace tree {
 
 using namespace tc;
+using namespace records;
 
-constexpr int TILE = 128;  // positions per tile = MMA M
-constexpr int WORKERS = 256;   // two threads to a position
-constexpr int WARPS = WORKERS / 32;
-constexpr int THREADS = WORKERS + 32;  // and the warp that issues the products
 constexpr int MAX_ROWS = 64;  // rows per CTA
 constexpr int MERGE_WARPS = 8;
-// Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
-// a tile ahead), and belongs to the range that holds its first place.
-constexpr int RAW_PLACES = 3;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
 
 // what the launches share: sizes from the host, pointers into the caller's scratch
@@ -63,38 +57,6 @@ __host__ __device__ inline int quant_end(int L, int W, int n) {
 __device__ __forceinline__ int seq_tiles(const MultiArgs& a, int L) {
   return (quant_end(L, a.W, a.n) + TILE - 1) / TILE + (raw_count(L, a.W, a.n) + TILE - 1) / TILE * RAW_PLACES;
 }
-// warp 0: the sequences' lengths (0 where out of range) and the exclusive prefix of their tiles, [batch + 1]
-__device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* lens, int* pre, bool flag) {
-  const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
-  const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
-  int s = 0;
-  for (int b = b0; b < b1; ++b) {
-    int L = a.seq_lens[b];
-    if (L < 0 || L > a.max_seq_len) {
-      if (flag) atomicOr(a.p.status, KVQ_DEV_SEQLEN_RANGE);
-      L = 0;
-    }
-    lens[b] = L;
-    s += seq_tiles(a, L);
-  }
-  int incl = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(FULL, incl, o);
-    if (lane >= o) incl += y;
-  }
-  int run = incl - s;
-  for (int b = b0; b < b1; ++b) {
-    pre[b] = run;
-    run += seq_tiles(a, lens[b]);
-  }
-  if (lane == 31) pre[a.batch] = incl;
-}
-// n / d of numbers that usually fit 32 bits
-__device__ __forceinline__ long long quick_div(long long n, long long d) {
-  return ((unsigned long long)n | (unsigned long long)d) < 0x80000000ull ? (long long)((unsigned)n / (unsigned)d) : n / d;
-}
-
 template <int KF, bool F32>
 struct Cfg {
   static constexpr bool TQ = KF == KVQ_TQ3_QJL;
@@ -104,43 +66,6 @@ struct Cfg {
   // columns of keys in tensor memory: KD / 2 (hi), then lo (TQ3: of the weights and of raw keys only, which share them)
   static constexpr uint32_t K_COLS = KD / 2 + (F32 ? 64 : 0);
 };
-
-// byte offset of (row, k) in a K-major operand of R rows
-__host__ __device__ constexpr uint32_t km_off(int row, int k, int R) {
-  return (uint32_t)((k >> 3) * (R >> 3) * 128 + (row >> 3) * 128 + (row & 7) * 16 + (k & 7) * 2);
-}
-// byte offset of (n, k) in an N-major (or M-major) operand of R n, and of (m, k) where they are 128
-__host__ __device__ constexpr uint32_t mn_off(int n, int k, int R) {
-  return (uint32_t)((k >> 3) * (R >> 3) * 128 + (n >> 3) * 128 + (k & 7) * 16 + (n & 7) * 2);
-}
-__host__ __device__ constexpr uint32_t mm_off(int m, int k) { return mn_off(m, k, D); }
-
-// Four channels (4 lane .. + 3) of a vector held by a warp, as the 8 bytes that belong at 8 (lane & 1) of their
-// 16-byte group: in order, or in the order in which nibbles() leaves eight codes
-template <bool NIBBLE_ORDER>
-__device__ __forceinline__ uint2 pack4(float y0, float y1, float y2, float y3, int lane) {
-  const uint32_t a = h2u(__floats2half2_rn(y0, y1)), b = h2u(__floats2half2_rn(y2, y3));
-  if (!NIBBLE_ORDER) return make_uint2(a, b);
-  const bool odd = lane & 1;
-  const uint32_t r = __shfl_xor_sync(FULL, odd ? a : b, 1);
-  // even: (c0 c4)(c1 c5), odd: (c2 c6)(c3 c7)
-  return odd ? make_uint2(__byte_perm(r, b, 0x5410), __byte_perm(r, b, 0x7632))
-             : make_uint2(__byte_perm(a, r, 0x5410), __byte_perm(a, r, 0x7632));
-}
-__device__ __forceinline__ float2 load2_in(const void* base, int off, bool bf16) {
-  if (!bf16) return *reinterpret_cast<const float2*>(static_cast<const float*>(base) + off);
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(base) + off);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-__device__ __forceinline__ float lo_part(float v) { return v - __half2float(__float2half_rn(v)); }
-// store the four channels to a plane and, with F32, their lo parts to the next
-template <bool NIBBLE_ORDER, bool F32>
-__device__ __forceinline__ void put4(uint8_t* dst, uint32_t plane, const float (&y)[4], int lane) {
-  *reinterpret_cast<uint2*>(dst) = pack4<NIBBLE_ORDER>(y[0], y[1], y[2], y[3], lane);
-  if (F32)
-    *reinterpret_cast<uint2*>(dst + plane) =
-        pack4<NIBBLE_ORDER>(lo_part(y[0]), lo_part(y[1]), lo_part(y[2]), lo_part(y[3]), lane);
-}
 
 // channels 4 lane .. + 3 of row r of a query image, in the order in which put_k leaves the keys' channels
 template <int KF, bool F32>
@@ -161,32 +86,6 @@ __device__ __forceinline__ void put_q(uint8_t* img, int r, int N, uint32_t plane
 }
 
 // ------------------------------------------------------------------ dequantising
-// A thread's part of a tile: keys of position t = tid & 127 (half hf of its record), values of the position pair vp and
-// rows 2 vr, 2 vr + 1.
-struct Lane {
-  int t, hf, vp, vr;
-};
-__device__ __forceinline__ Lane lane_of(int tid) {
-  // values: 8 consecutive lanes write 8 distinct 16-byte slots of their core matrices (the odd rows' lanes take the odd
-  // position of the pair first)
-  return {tid & 127, (tid >> 7) & 1, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3};
-}
-
-// The records of a tile in shared memory: four half-pages' keys (main, metadata), then their values.
-template <int KF>
-struct Rec {
-  static constexpr int K_MAIN = KF == KVQ_Q8G32 ? 128 * HALF : 64 * HALF, V_MAIN = 64 * HALF;
-  static constexpr int K_META = (KF == KVQ_Q8G32 ? 8 : KF == KVQ_TQ3_QJL ? 4 : 16) * HALF, V_META = 16 * HALF;
-  static constexpr int KH = K_MAIN + K_META, VH = V_MAIN + V_META;  // of one half-page
-  static constexpr int V0 = 4 * KH, BYTES = 4 * (KH + VH);
-};
-
-// physical page of position j of a sequence (-1: out of range)
-__device__ __forceinline__ int checked(int phys, int n_pages) { return phys < n_pages ? phys : -1; }
-
-__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
-
 // eight codes of a word times scale plus zero (and, with F32, their lo parts)
 template <bool F32>
 __device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2, uint4& o, uint4& l) {
@@ -205,13 +104,6 @@ __device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2
     split2(z + s * f2.x, z + s * f2.y, o.z, l.z);
     split2(z + s * f3.x, z + s * f3.y, o.w, l.w);
   }
-}
-
-// the 32 bytes at `at` as two words, the order in which they are read alternating over the lanes (fewer bank conflicts)
-__device__ __forceinline__ void lds32(const uint8_t* at, bool swap, uint4& a, uint4& b) {
-  const uint4 x = *reinterpret_cast<const uint4*>(at + (swap ? 16 : 0)), y = *reinterpret_cast<const uint4*>(at + (swap ? 0 : 16));
-  a = make_uint4(swap ? y.x : x.x, swap ? y.y : x.y, swap ? y.z : x.z, swap ? y.w : x.w);
-  b = make_uint4(swap ? x.x : y.x, swap ? x.y : y.y, swap ? x.z : y.z, swap ? x.w : y.w);
 }
 
 // keys of the thread's position to its tensor-memory lane: columns 0..63 (TQ3: centroids), then TQ3's signed weights,
@@ -386,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) tile_prefix(a, lens, pre, blockIdx.x == 0);
+  if (warp == 0) tile_prefix(a, lens, pre, blockIdx.x == 0, [&](int L) { return seq_tiles(a, L); });
   if (warp == 1) tm_alloc(&tmem_sh, TM_COLS);
   fence_before();
   asm volatile("griddepcontrol.launch_dependents;");
@@ -931,7 +823,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
   const MultiArgs& a = p.a;
   int* lens = pre + a.batch + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) tile_prefix(a, lens, pre, false);
+  if (warp == 0) tile_prefix(a, lens, pre, false, [&](int L) { return seq_tiles(a, L); });
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = a.n * a.g;
@@ -1034,24 +926,6 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ host
-template <typename... A>
-cudaError_t go(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, bool dependent, cudaStream_t s, A... args) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // sizes of a call, and its records in scratch (which may be null: sizes only); returns the scratch bytes
 template <int KF, bool F32>
 size_t make_plan(const MultiArgs& a, int sms, Plan* p) {

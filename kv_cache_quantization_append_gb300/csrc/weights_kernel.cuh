@@ -1,0 +1,740 @@
+// Attention weights of cached positions: the kernels of one key format (included by one translation unit per format).
+//
+// For the rows of a unit (query heads of its newest n tokens, row = token * g + head; at most 128 a launch, 64 for TQ3
+// keys) every position's logit is wanted twice: for the rows' normalisers, and for the positions' weights, the sum over
+// rows of 2^(logit - normaliser).  Two launches:
+//  1. weights_kernel<.., SUM = false>: per row the maximum and sum over this CTA's range of tiles (stream-K, as in tree
+//     attention: eight warps convert keys and finish logits, a ninth copies records and issues products, two CTAs an SM).
+//     With at most 8 rows it also stores the logits: 4 bytes a row and position against at least 68 of key record.
+//  2. With stored logits weights_add_kernel, an elementwise pass; else weights_kernel<.., SUM = true>, which takes the
+//     logits again.  Both join the ranges' maxima and sums in a fixed order first.
+//
+// The weights accumulate in fp32, so logits are taken to fp32's accuracy: the keys' codes go to the tensor cores as they
+// are, exact in fp16 (S^T = codes [128 positions x 128] Q~^T, the queries as fp16 hi and lo), one accumulator per group of
+// 32 channels (TQ3: centroids and signs), and the thread that owns the position applies its scales and zeros in fp32:
+//   logit = sum_G scale_G S_G + zero_G (sum of q~ over G);  TQ3: n (S_c + w S_sign).
+// Raw keys (the window) are fp16 hi and lo against the queries as they are, hi hi + hi lo + lo hi.
+// Each warp keeps its own reference per row, which moves only when a logit passes it by 2^60: no exchange between warps
+// until the range ends.
+#pragma once
+
+#include "records.cuh"
+
+namespace kvq {
+namespace weights {
+
+using namespace tc;
+using namespace records;
+
+constexpr float NO_REF = -1e30f;
+constexpr int STORE_ROWS = 8;
+constexpr int MAX_ROWS = 128, MAX_ROWS_TQ = 64;
+constexpr int ADD_THREADS = 256;
+
+struct Plan {
+  MultiArgs a;
+  int row0, rows;     // this launch's rows of every unit
+  int nb;             // blocks of N rows
+  int n_units, G;
+  long long s_pad;    // positions a row of stored logits has room for
+  float decay;
+  float* parts;       // [2 n_units + G][rows][2]: range c's maxima and sums of unit u's records (+ 0), raw keys (+ 1) at 2 u + c
+  float* logits;      // [n_units][rows][s_pad], or null
+};
+
+__host__ __device__ inline int quant_tiles(int L, int W) { return (L > W ? L - W + TILE - 1 : 0) / TILE; }
+__device__ __forceinline__ int seq_tiles(int L, int W) {
+  return quant_tiles(L, W) + ((L < W ? L : W) + TILE - 1) / TILE * RAW_PLACES;
+}
+
+template <int KF>
+struct Cfg {
+  static constexpr bool TQ = KF == KVQ_TQ3_QJL;
+  static constexpr int KD = TQ ? 256 : 128;   // width of a query
+  static constexpr int ACC = TQ ? 2 : 4;      // accumulators: centroids and signs, or groups of 32 channels
+};
+// place of channel c among the keys' K elements: groups of 32 channels stay together
+template <int KF>
+__host__ __device__ constexpr int place(int c) {
+  if (KF == KVQ_Q4G32) return (c & ~7) + nibble_place(c & 7);
+  if (KF == KVQ_TQ3_QJL) return c;
+  // Q8 record chunk 2 i + h, word w, byte: channel 16 (4 h + w) + 2 i + (byte & 1) + 8 (byte >> 1)
+  const int w = (c >> 4) & 3, h = c >> 6, i = (c & 7) >> 1, byte = (c & 1) + 2 * ((c >> 3) & 1);
+  return 8 * (8 * h + 4 * (w >> 1) + i) + 4 * (w & 1) + byte;
+}
+
+template <int KF>
+struct Smem {
+  using C = Cfg<KF>;
+  static __host__ __device__ constexpr uint32_t plane(int rows) { return rows * C::KD * 2; }  // of nb * N rows
+  static __host__ __device__ constexpr uint32_t rec(int rows) { return 2 * plane(rows); }
+  static __host__ __device__ constexpr uint32_t proj(int rows) { return rec(rows) + 4 * Rec<KF>::KH; }  // TQ3: a plane of S
+  static __host__ __device__ constexpr uint32_t wm(int rows) { return proj(rows) + (C::TQ ? 32768 : 0); }  // [8][rows / 2]
+  static __host__ __device__ constexpr uint32_t wl(int rows) { return wm(rows) + 16 * rows; }
+  static __host__ __device__ constexpr uint32_t qs(int rows) { return wl(rows) + 16 * rows; }              // [rows][4]
+  static __host__ __device__ constexpr uint32_t pre(int rows) { return qs(rows) + 16 * rows; }
+};
+
+// the codes of the thread's position, exact, to its tensor-memory lane (TQ3: centroids, then signs as +-1)
+template <int KF>
+__device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
+  using R = Rec<KF>;
+  const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
+  const int tt = ln.t & 31;
+  if (KF == KVQ_Q8G32) {
+    const __half2 off = u2h(0x64806480u);  // 1024 + 128
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {  // chunk 4 hf + c: i = 2 hf + (c >> 1), h = c & 1
+      const uint4 q = *reinterpret_cast<const uint4*>(hb + tt * 128 + 64 * ln.hf + 16 * (c ^ (tt & 1)));
+      const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = h2u(__hsub2(u2h(prmt(wd[2 * half + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), off));
+        tm_st4(col + 4 * (8 * (c & 1) + 4 * half + 2 * ln.hf + (c >> 1)), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+    return;
+  }
+  uint4 k[2];
+  lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+  if (KF == KVQ_Q4G32) {
+#pragma unroll
+    for (int G = 0; G < 4; ++G) {
+      uint4 o[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        __half2 c[4];
+        nibbles(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, c);
+        o[i] = make_uint4(h2u(c[0]), h2u(c[1]), h2u(c[2]), h2u(c[3]));
+      }
+      tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    uint4 o[2], s[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint4& q = k[i >> 2];
+      const uint32_t word = ((i + x) & 3) == 0 ? q.x : ((i + x) & 3) == 1 ? q.y : ((i + x) & 3) == 2 ? q.z : q.w;
+      const uint32_t sel = (word & 0x07070707u) | ((word << 1) & 0x70707070u);
+      const uint32_t l0 = prmt(cent.x, cent.y, sel), h0 = prmt(cent.z, cent.w, sel);
+      const uint32_t l1 = prmt(cent.x, cent.y, sel >> 16), h1 = prmt(cent.z, cent.w, sel >> 16);
+      o[x] = make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                        __byte_perm(l1, h1, 0x7362));
+      const uint32_t lo = word << 1;
+      uint32_t m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m[j] = 0xBC00BC00u ^ (prmt(lo, word, (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12)) & 0x80008000u);
+      s[x] = make_uint4(m[0], m[1], m[2], m[3]);
+    }
+    tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
+    tm_st8(col + 64 + 32 * ln.hf + 4 * i, s[0], s[1]);
+  }
+}
+
+// normaliser (base-2 logarithm of the sum) of one row of unit u by a warp: the parts of every range in a fixed order
+__device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long long first, int nq, int tiles, long long G,
+                                            long long total, int lane) {
+  const auto owner = [&](long long x) { return (int)quick_div((x + 1) * G - 1, total); };
+  const int c0 = owner(first), c1 = nq > 0 ? owner(first + nq - 1) : c0 - 1;
+  float m = NO_REF, l = 0.f;
+  const auto add = [&](int kind, int c) {
+    const float2 x = *reinterpret_cast<const float2*>(p.parts + ((size_t)(2 * u + kind + c) * p.rows + row) * 2);
+    const float mn = fmaxf(m, x.x);
+    l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
+    m = mn;
+  };
+  for (int c = c0 + lane; c <= c1; c += 32) add(0, c);
+  if (lane == 31) {
+    int last = -1;
+    for (int x = nq; x < tiles; x += RAW_PLACES) {
+      const int c = owner(first + x);
+      if (c != last) add(1, c);
+      last = c;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float m2 = __shfl_xor_sync(FULL, m, o), l2 = __shfl_xor_sync(FULL, l, o), mn = fmaxf(m, m2);
+    // (the lower lane's term first, on both sides)
+    const float a = l * ex2(m - mn), b = l2 * ex2(m2 - mn);
+    l = lane & o ? b + a : a + b;
+    m = mn;
+  }
+  return l > 0.f ? m + log2f(l) : INFINITY;
+}
+
+template <int KF, int N, bool SUM>
+__global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_constant__ Plan p) {
+  using C = Cfg<KF>;
+  using SM = Smem<KF>;
+  constexpr bool TQ = C::TQ, Q4 = KF == KVQ_Q4G32;
+  constexpr int ACC = C::ACC, CH = 4;
+  // tensor memory: K (128 columns: codes; raw keys' hi and lo; TQ3 centroids and signs) | S, ACC accumulators of N columns
+  constexpr uint32_t C_S = 128, COLS = C_S + ACC * N, TM_COLS = 256;
+  static_assert(COLS <= TM_COLS, "tensor memory");
+  constexpr uint32_t ID_S = idesc(TILE, N, false, false);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // kr_bar: a tile's keys have landed; k_bar: they are in place (one arrival a worker warp); s_bar: a block's logits have
+  // been read; qk_bar: a block's products are done
+  __shared__ __align__(8) uint64_t kr_bar, k_bar, s_bar, qk_bar, end_bar;
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  __shared__ float half_sum[TILE];
+  const MultiArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, NR = p.nb * N;
+  const uint32_t q_plane = SM::plane(NR);
+  float* qs = reinterpret_cast<float*>(smem + SM::qs(NR));
+  int* pre = reinterpret_cast<int*>(smem + SM::pre(NR));
+  int* lens = pre + a.batch + 1;
+
+  if (tid == 0) {
+    bar_init(&kr_bar, 1);
+    bar_init(&k_bar, WARPS);
+    bar_init(&s_bar, WARPS);
+    bar_init(&qk_bar, 1);
+    bar_init(&end_bar, 1);
+    abort_sh = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tile_prefix(a, lens, pre, blockIdx.x == 0, [&](int L) { return seq_tiles(L, a.W); });
+  if (warp == 1) tm_alloc(&tmem_sh, TM_COLS);
+  fence_before();
+  asm volatile("griddepcontrol.launch_dependents;");
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_sh, sbase = smem_u32(smem);
+  const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
+  const long long G = min((long long)p.G, total);
+  long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
+  const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const Lane ln = lane_of(tid);
+  const size_t page_stride = (size_t)a.Hkv * a.L.page_bytes;
+  const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
+  uint4 cent = make_uint4(0u, 0u, 0u, 0u);
+  if (TQ) {
+    const uint4 c = *reinterpret_cast<const uint4*>(a.p.cb->cent);
+    cent = make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.x, c.y, 0x7531),
+                      __byte_perm(c.z, c.w, 0x7531));
+  }
+  uint32_t kr_phase = 0, k_phase = 0, s_phase = 0, qk_phase = 0, kr_n = 0;
+  bool s_pending = false;
+  const auto wait = [&](uint64_t* bar, uint32_t& phase) {
+    bar_wait(bar, phase, &abort_sh, a.p.status);
+    phase ^= 1;
+  };
+  const auto k_done = [&] {
+    tm_wait_st();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&k_bar);
+  };
+  const int col0 = (warp >> 2) * (N / 2);
+  const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  float* wm = reinterpret_cast<float*>(smem + SM::wm(NR)) + warp * (NR / 2);  // this warp's references and sums
+  float* wl = reinterpret_cast<float*>(smem + SM::wl(NR)) + warp * (NR / 2);
+  float* lse = reinterpret_cast<float*>(smem + SM::wm(NR));                   // SUM: the rows' normalisers
+  bool ok = true;
+
+  while (t < t_end && ok) {
+    const int ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
+    const long long in_layer = t - ll * per_layer;
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)pre[mid] * a.Hkv <= in_layer) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo, tiles = pre[b + 1] - pre[b];
+    const long long r = in_layer - (long long)pre[b] * a.Hkv;
+    const int h = (int)quick_div(r, tiles), place0 = (int)(r - (long long)h * tiles), layer = a.layer0 + ll;
+    const int u = (ll * a.batch + b) * a.Hkv + h;
+    const int L = lens[b], qend = max(0, L - a.W), nq = quant_tiles(L, a.W);
+    const long long first = t - place0;
+    const bool raw = place0 >= nq;
+    const int place1 = (int)min((long long)(raw ? tiles : nq), place0 + (t_end - t));
+    t += place1 - place0;
+    const int it0 = raw ? nq + (place0 - nq + RAW_PLACES - 1) / RAW_PLACES : place0;
+    const int it1 = raw ? nq + (place1 - nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    if (it0 == it1) continue;
+    const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
+
+    if (warp == WARPS) {
+      // ================================================================ the products and the copies
+      const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
+      using R = Rec<KF>;
+      const auto page_of = [&](int it) {
+        const int j = it * TILE + lane * HALF;
+        return lane < 4 && it < it1 && j < qend ? checked(__ldg(bt + j / PAGE), a.L.n_pages) : -1;
+      };
+      const auto copy = [&](int phys) {
+        ++kr_n;
+        const int n = __popc(__ballot_sync(FULL, phys >= 0));
+        if (lane == 0) bar_expect(&kr_bar, n * R::KH);
+        __syncwarp();
+        if (phys >= 0) {
+          const uint8_t* src = unit_pages + (size_t)phys * page_stride + (lane & 1) * (size_t)(R::KH + R::VH);
+          uint8_t* dst = smem + SM::rec(NR) + lane * R::KH;
+          bulk_g2s(dst, src, R::K_MAIN, &kr_bar);
+          bulk_g2s(dst + R::K_MAIN, src + R::K_MAIN + R::V_MAIN, R::K_META, &kr_bar);
+        }
+        __syncwarp();
+      };
+      int phys = -1;
+      if (!raw) copy(page_of(it0));
+      if (TQ && !raw) {
+        // S q~ of all rows to columns 0 .. NR - 1: the projection comes as its hi plane, then its lo plane
+        for (int part = 0; part < 2; ++part) {
+          wait(&k_bar, k_phase);
+          fence_after();
+#pragma unroll 1
+          for (int rb = 0; rb < p.nb; ++rb) {
+            uint64_t sa = sdesc(sbase + SM::proj(NR), 2048, 128), qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
+#pragma unroll 1
+            for (int ks = 0; ks < D / 16; ++ks, sa += 256, qa += 2 * N) {
+              mma_ss(tmem + rb * N, sa, qa, ID_S, part > 0 || ks > 0);
+              if (part == 0) mma_ss(tmem + rb * N, sa, qa + (q_plane >> 4), ID_S, 1);
+            }
+          }
+          mma_commit(&qk_bar);
+        }
+      }
+      for (int it = it0; it < it1; ++it) {
+        if (!raw) phys = page_of(it + 1);
+        wait(&k_bar, k_phase);
+        if (*(volatile int*)&abort_sh) break;
+        if (!raw && it + 1 < it1) copy(phys);  // the workers have read this tile's keys
+        for (int rb = 0; rb < p.nb; ++rb) {
+          if (s_pending) wait(&s_bar, s_phase);
+          s_pending = true;
+          if (*(volatile int*)&abort_sh) break;
+          fence_after();
+          uint64_t qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
+          const uint64_t qb = q_plane >> 4;
+          uint32_t ka = tmem;
+          const uint32_t d = tmem + C_S;
+          if (raw) {
+#pragma unroll 2
+            for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
+              mma_ts(d, ka, qa, ID_S, ks > 0);
+              mma_ts(d, ka, qa + qb, ID_S, 1);
+              mma_ts(d, ka + 64, qa, ID_S, 1);
+            }
+          } else {
+            constexpr int STEPS = C::KD / 16 / ACC;  // k-steps per accumulator
+#pragma unroll 2
+            for (int ks = 0; ks < C::KD / 16; ++ks, ka += 8, qa += 2 * N) {
+              mma_ts(d + ks / STEPS * N, ka, qa, ID_S, ks % STEPS > 0);
+              mma_ts(d + ks / STEPS * N, ka, qa + qb, ID_S, 1);
+            }
+          }
+          mma_commit(&qk_bar);
+        }
+      }
+      ok = !*(volatile int*)&abort_sh;
+      continue;
+    }
+
+    // ================================================================ the workers
+    const auto page_of = [&](int it) {  // of this thread's position, read a tile ahead
+      const int j = it * TILE + (ln.t & 64);
+      return it < it1 && !raw && j < qend ? __ldg(bt + j / PAGE) : -1;
+    };
+    int page = page_of(it0);
+    // ---- queries in base-2 units as hi and lo images, for records rotated and balanced; sums over groups for the zeros
+#pragma unroll 1
+    for (int r0 = warp; r0 < NR; r0 += 4 * WARPS) {
+      float4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int lr = r0 + i * WARPS, row = p.row0 + lr;
+        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lr < p.rows)
+          q[i] = load4_in(a.q, ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + row / a.g) * D + 4 * lane,
+                          a.in_bf16);
+      }
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int lr = r0 + i * WARPS;
+        if (lr >= NR) break;
+        const float4 x = q[0];
+        q[0] = q[1], q[1] = q[2], q[2] = q[3];
+        float y[4] = {x.x, x.y, x.z, x.w};
+        if (!raw) {
+          y[0] *= sg.x, y[1] *= sg.y, y[2] *= sg.z, y[3] *= sg.w;
+          hadamard_warp(y[0], y[1], y[2], y[3], lane);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+          if (a.sinkhorn && !raw) y[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
+          uint8_t* dst = smem + (lr / N) * (N * C::KD * 2) + km_off(lr % N, place<KF>(4 * lane + e), N);
+          const __half hi16 = __float2half_rn(y[e]);
+          *reinterpret_cast<__half*>(dst) = hi16;
+          *reinterpret_cast<__half*>(dst + q_plane) = __float2half_rn(y[e] - __half2float(hi16));
+        }
+        if (Q4) {
+          float s = (y[0] + y[1]) + (y[2] + y[3]);
+          s += __shfl_xor_sync(FULL, s, 1);
+          s += __shfl_xor_sync(FULL, s, 2);
+          s += __shfl_xor_sync(FULL, s, 4);
+          if ((lane & 7) == 0) qs[4 * lr + (lane >> 3)] = raw ? 0.f : s;
+        }
+      }
+    }
+    if (SUM) {
+#pragma unroll 1
+      for (int lr = warp; lr < NR; lr += WARPS) {
+        const float v = lr < p.rows ? normaliser(p, u, lr, first, nq, tiles, G, total, lane) : INFINITY;
+        if (lane == 0) lse[lr] = v;
+      }
+    } else {
+      for (int c = lane; c < NR / 2; c += 32) {
+        wm[c] = NO_REF;
+        wl[c] = 0.f;
+      }
+    }
+    if (TQ && !raw) {
+      const int i = tid & 127;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        if (part) wait(&qk_bar, qk_phase);
+#pragma unroll 1
+        for (int kg = tid >> 7; kg < D / 8; kg += 2) {
+          float s[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = __ldg(a.p.qjl_t + (8 * kg + e) * D + i);
+          uint4 o, l;
+          split2(s[0], s[1], o.x, l.x);
+          split2(s[2], s[3], o.y, l.y);
+          split2(s[4], s[5], o.z, l.z);
+          split2(s[6], s[7], o.w, l.w);
+          *reinterpret_cast<uint4*>(smem + SM::proj(NR) + km_off(i, 8 * kg, D)) = part ? l : o;
+        }
+        fence_async_smem();
+        k_done();
+      }
+      wait(&qk_bar, qk_phase);
+      fence_after();
+#pragma unroll 1
+      for (int c = (warp >> 2) * (NR / 2); c < ((warp >> 2) + 1) * (NR / 2); c += 8) {
+        float x[8];
+        tm_ld(lane_addr + c, x);
+        tm_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint8_t* dst = smem + ((c + e) / N) * (N * C::KD * 2) + km_off((c + e) % N, D + i, N);
+          const __half hi16 = __float2half_rn(x[e]);
+          *reinterpret_cast<__half*>(dst) = hi16;
+          *reinterpret_cast<__half*>(dst + q_plane) = __float2half_rn(x[e] - __half2float(hi16));
+        }
+      }
+      fence_before();
+    }
+    fence_async_smem();
+    part_sync(1, WORKERS);
+
+    for (int it = it0; it < it1; ++it) {
+      const int x = (it - nq) * TILE + ln.t;                  // raw: place in the window
+      const int j = raw ? qend + x : it * TILE + ln.t;        // this thread's position
+      const bool mine = j < (raw ? L : qend);
+      bool valid = mine;                                      // (a page out of range takes no weight)
+      // ---- keys (the previous tile's products are done)
+      float s0[4] = {}, z0[4] = {};                           // scales and zeros; TQ3: norm, weight
+      if (!raw) {
+        if (checked(page, a.L.n_pages) < 0) {
+          if (valid && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
+          valid = false;
+        }
+        page = page_of(it + 1);
+        wait(&kr_bar, kr_phase);
+        const uint8_t* rec = smem + SM::rec(NR);
+        put_codes<KF>(lane_addr, ln, rec, cent);
+        const __half* m = reinterpret_cast<const __half*>(rec + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN);
+        const int tt = ln.t & 31;
+        if (TQ) {
+          s0[0] = __half2float(m[tt]);
+          s0[1] = s0[0] * QJL_CONST * __half2float(m[HALF + tt]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s0[i] = __half2float(m[(Q4 ? 8 : 4) * tt + i]);
+            if (Q4) z0[i] = __half2float(m[8 * tt + 4 + i]);
+          }
+        }
+      } else {
+        const float* row = a.p.ringk + ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (valid ? (unsigned)j % (unsigned)a.W : 0u)) * D;
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int kg = 8 * ln.hf + i;
+          float f[8];
+          if (KF == KVQ_Q8G32) {
+            const int c = 64 * (kg >> 3) + 32 * ((kg >> 2) & 1) + 2 * (kg & 3);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 v = *reinterpret_cast<const float2*>(row + c + 8 * y);
+              f[2 * y] = v.x, f[2 * y + 1] = v.y;
+            }
+          } else {
+            const float4 v0 = *reinterpret_cast<const float4*>(row + 8 * kg), v1 = *reinterpret_cast<const float4*>(row + 8 * kg + 4);
+            const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int y = 0; y < 8; ++y) f[y] = v[Q4 ? nibble_channel(y) : y];
+          }
+          uint4 o, l;
+          split2(f[0], f[1], o.x, l.x);
+          split2(f[2], f[3], o.y, l.y);
+          split2(f[4], f[5], o.z, l.z);
+          split2(f[6], f[7], o.w, l.w);
+          tm_st4(lane_addr + 4 * kg, o);
+          tm_st4(lane_addr + 64 + 4 * kg, l);
+        }
+      }
+      k_done();
+      // rows from this one on attend to the position (token of the row >= j - L + n)
+      const int cut = valid ? a.g * max(0, j - L + a.n) - p.row0 : 1 << 30;
+      float acc = 0.f;
+#pragma unroll 1
+      for (int rb = 0; rb < p.nb; ++rb) {
+        wait(&qk_bar, qk_phase);
+        fence_after();
+#pragma unroll 1
+        for (int c = col0; c < col0 + N / 2 && rb * N + c < p.rows; c += CH) {
+          const int row = rb * N + c;
+          // ---- four rows' logits
+          float s[CH], part[ACC][CH];
+#pragma unroll
+          for (int i = 0; i < ACC; ++i)
+            if (i == 0 || !raw) tm_ld(lane_addr + C_S + i * N + c, part[i]);
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            if (raw) {
+              s[i] = part[0][i];
+            } else if (TQ) {
+              s[i] = fmaf(part[1][i], s0[1], part[0][i] * s0[0]);
+            } else {
+              s[i] = part[0][i] * s0[0];
+#pragma unroll
+              for (int y = 1; y < ACC; ++y) s[i] = fmaf(part[y % ACC][i], s0[y], s[i]);
+              if (Q4) {
+                const float4 q = *reinterpret_cast<const float4*>(qs + 4 * (row + i));
+                s[i] = fmaf(q.x, z0[0], fmaf(q.y, z0[1], fmaf(q.z, z0[2], fmaf(q.w, z0[3], s[i]))));
+              }
+            }
+            if (row + i < cut) s[i] = -INFINITY;
+          }
+          if (SUM) {
+            const float4 n4 = *reinterpret_cast<const float4*>(lse + row);
+            const float nm[CH] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+            for (int i = 0; i < CH; ++i) acc += ex2(s[i] - nm[i]);
+            continue;
+          }
+          if (p.logits != nullptr && mine) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              if (row + i < p.rows) p.logits[((size_t)u * p.rows + row + i) * p.s_pad + j] = s[i];
+          }
+          const int at = rb * (N / 2) + c - col0;
+          float4 m4 = *reinterpret_cast<const float4*>(wm + at);
+          float m[CH] = {m4.x, m4.y, m4.z, m4.w};
+          bool over = false;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) over |= s[i] > m[i] + 60.f;
+          if (__any_sync(FULL, over)) {  // (the first tile, hardly ever another)
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int v = __float_as_int(s[i]);
+              const int top = __reduce_max_sync(FULL, v ^ ((v >> 31) & 0x7fffffff));
+              const float ft = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+              if (ft > m[i] + 60.f) {
+                if (lane == 0) wl[at + i] *= ex2(m[i] - ft);
+                m[i] = ft;
+              }
+            }
+            __syncwarp();
+            if (lane == 0) *reinterpret_cast<float4*>(wm + at) = make_float4(m[0], m[1], m[2], m[3]);
+            __syncwarp();
+          }
+          float e[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) e[i] = ex2(s[i] - m[i]);
+          // sums over the lanes: rows 2 (lane >> 4) + (lane >> 3 & 1) end in the lanes
+          const bool up = lane & 16, up2 = lane & 8;
+          float f0 = up ? e[2] : e[0], f1 = up ? e[3] : e[1];
+          f0 += __shfl_xor_sync(FULL, up ? e[0] : e[2], 16);
+          f1 += __shfl_xor_sync(FULL, up ? e[1] : e[3], 16);
+          float g0 = up2 ? f1 : f0;
+          g0 += __shfl_xor_sync(FULL, up2 ? f0 : f1, 8);
+          g0 += __shfl_xor_sync(FULL, g0, 4);
+          g0 += __shfl_xor_sync(FULL, g0, 2);
+          g0 += __shfl_xor_sync(FULL, g0, 1);
+          if ((lane & 7) == 0) wl[at + 2 * (lane >> 4) + ((lane >> 3) & 1)] += g0;
+          __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s_bar);
+      }
+      if (SUM) {
+        if (warp >= 4) half_sum[ln.t] = acc;
+        part_sync(1, WORKERS);
+        if (*(volatile int*)&abort_sh) break;  // (raised before the barrier: all workers leave together)
+        if (warp < 4 && mine) {
+          float* w = a.weights + (size_t)u * a.max_seq_len + j;
+          const float v = acc + half_sum[ln.t];
+          *w = p.decay != 0.f ? fmaf(p.decay, *w, v) : v;
+        }
+        part_sync(1, WORKERS);
+      }
+    }
+    part_sync(1, WORKERS);
+    if (*(volatile int*)&abort_sh) {  // (with the flag up every wait returns at once: all workers come here)
+      ok = false;
+      break;
+    }
+    if (!SUM) {
+      // ---- the range's maxima and sums: the four warps that hold a row's columns, joined in order
+      float* out = p.parts + (size_t)(2 * u + raw + blockIdx.x) * p.rows * 2;
+      for (int lr = tid; lr < p.rows; lr += WORKERS) {
+        const int c = lr % N, wg = c / (N / 2), at = lr / N * (N / 2) + c % (N / 2);
+        const float* m0 = reinterpret_cast<const float*>(smem + SM::wm(NR)) + 4 * wg * (NR / 2) + at;
+        const float* l0 = reinterpret_cast<const float*>(smem + SM::wl(NR)) + 4 * wg * (NR / 2) + at;
+        float m = NO_REF, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float mi = m0[i * (NR / 2)], mn = fmaxf(m, mi);
+          l = l * ex2(m - mn) + l0[i * (NR / 2)] * ex2(mi - mn);
+          m = mn;
+        }
+        out[2 * lr] = m;
+        out[2 * lr + 1] = l;
+      }
+    }
+    part_sync(1, WORKERS);  // the next part's queries and sums may come
+  }
+  if (warp == WARPS && !ok) {  // what is still under way lands before the CTA leaves; the waits are bounded
+    const auto land = [&](uint64_t* bar, uint32_t parity) {
+      const unsigned long long t0 = gtimer();
+      while (!bar_try(bar, parity) && gtimer() - t0 < WAIT_NS) {
+      }
+    };
+    if (kr_n) land(&kr_bar, (kr_n - 1) & 1);
+    mma_commit(&end_bar);
+    land(&end_bar, 0);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tm_free(tmem, TM_COLS);
+  }
+}
+
+// weights from stored logits: one CTA per 1024 positions of a unit
+static __global__ void __launch_bounds__(ADD_THREADS) weights_add_kernel(const __grid_constant__ Plan p) {
+  __shared__ float lse[STORE_ROWS];
+  extern __shared__ int pre[];
+  const MultiArgs& a = p.a;
+  int* lens = pre + a.batch + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int u = blockIdx.y + blockIdx.z * 32768;
+  if (warp == 0) tile_prefix(a, lens, pre, false, [&](int L) { return seq_tiles(L, a.W); });
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (u >= p.n_units) return;
+  const int h = u % a.Hkv, b = (u / a.Hkv) % a.batch, ll = u / (a.Hkv * a.batch), L = lens[b];
+  const int j0 = (blockIdx.x * ADD_THREADS + tid) * 4;
+  if (blockIdx.x * ADD_THREADS * 4 >= L) return;
+  float4 x[STORE_ROWS];
+  const float* src = p.logits + (size_t)u * p.rows * p.s_pad + j0;
+#pragma unroll
+  for (int r = 0; r < STORE_ROWS; ++r)
+    if (r < p.rows && j0 < L) x[r] = *reinterpret_cast<const float4*>(src + r * p.s_pad);
+  const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
+  const int tiles = pre[b + 1] - pre[b];
+  if (warp < p.rows) {
+    const float v = normaliser(p, u, warp, ll * per_layer + (long long)pre[b] * a.Hkv + (long long)h * tiles, quant_tiles(L, a.W), tiles,
+                               min((long long)p.G, total), total, lane);
+    if (lane == 0) lse[warp] = v;
+  }
+  __syncthreads();
+  if (j0 >= L) return;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < STORE_ROWS; ++r)
+    if (r < p.rows) {
+      s[0] += ex2(x[r].x - lse[r]);
+      s[1] += ex2(x[r].y - lse[r]);
+      s[2] += ex2(x[r].z - lse[r]);
+      s[3] += ex2(x[r].w - lse[r]);
+    }
+  float* w = a.weights + (size_t)u * a.max_seq_len + j0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j0 + i < L) w[i] = p.decay != 0.f ? fmaf(p.decay, w[i], s[i]) : s[i];
+}
+
+// rows of one launch, and the plan of the launches that begin at row0; returns the scratch bytes
+template <int KF>
+size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
+  const int all = a.n * a.g, most = KF == KVQ_TQ3_QJL ? MAX_ROWS_TQ : MAX_ROWS;
+  p->a = a;
+  p->row0 = row0;
+  p->rows = all - row0 < most ? all - row0 : most;
+  const int N = p->rows <= 16 ? 16 : 32;
+  p->nb = (p->rows + N - 1) / N;
+  p->n_units = a.n_layers_call * a.batch * a.Hkv;
+  p->G = 2 * sms;
+  p->s_pad = ((long long)a.max_seq_len + 3) / 4 * 4;
+  p->decay = row0 == 0 ? a.decay : 1.f;
+  const bool store = all <= STORE_ROWS;
+  const size_t parts = align256((size_t)(2 * p->n_units + p->G) * p->rows * 2 * sizeof(float));
+  p->parts = reinterpret_cast<float*>(a.scratch);
+  p->logits = store && a.scratch ? reinterpret_cast<float*>(a.scratch + parts) : nullptr;
+  return parts + (store ? (size_t)p->n_units * p->rows * p->s_pad * sizeof(float) : 0);
+}
+
+template <int KF, int N>
+cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
+  const size_t pre = (size_t)(2 * p.a.batch + 1) * 4, smem = Smem<KF>::pre(p.nb * N) + pre;
+  cudaError_t e = go(weights_kernel<KF, N, false>, (unsigned)p.G, THREADS, smem, false, s, p);
+  if (e != cudaSuccess) return e;
+  if (p.logits == nullptr) return go(weights_kernel<KF, N, true>, (unsigned)p.G, THREADS, smem, true, s, p);
+  cudaLaunchConfig_t cfg = {};
+  const unsigned y = p.n_units < 32768 ? p.n_units : 32768;
+  cfg.gridDim = dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768);
+  cfg.blockDim = dim3(ADD_THREADS);
+  cfg.dynamicSmemBytes = pre;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_add_kernel, p);
+}
+
+template <int KF>
+cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
+  for (int row0 = 0; row0 < a.n * a.g;) {
+    Plan p;
+    make_plan<KF>(a, sms, row0, &p);
+    const cudaError_t e = p.rows <= 16 ? launch_rows<KF, 16>(p, s) : launch_rows<KF, 32>(p, s);
+    if (e != cudaSuccess) return e;
+    row0 += p.rows;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace weights
+}  // namespace kvq

@@ -1,0 +1,12 @@
+// Attention weights over KVQ_Q8G32 keys (a translation unit per key format, compiled in parallel).
+#include "weights_kernel.cuh"
+
+namespace kvq {
+
+size_t weights_scratch_q8(const MultiArgs& a, int sms) {
+  weights::Plan p;
+  return weights::make_plan<KVQ_Q8G32>(a, sms, 0, &p);
+}
+cudaError_t launch_weights_q8(const MultiArgs& a, int sms, cudaStream_t s) { return weights::launch<KVQ_Q8G32>(a, sms, s); }
+
+}  // namespace kvq
