@@ -2,6 +2,8 @@
 // part of a tile, operand layouts in shared memory, launches.
 #pragma once
 
+#include <atomic>
+
 #include "tc.cuh"
 
 namespace kvq {
@@ -123,13 +125,24 @@ __device__ __forceinline__ void lds32(const uint8_t* at, bool swap, uint4& a, ui
 }
 
 // ------------------------------------------------------------------ launches
-template <typename... A>
-cudaError_t go(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, bool dependent, cudaStream_t s, A... args) {
+// Launches kernel K, as a programmatic dependent of the kernel before it in the stream or after it.  Its shared-memory
+// limit is set when a device first needs that much.
+template <auto K, typename... A>
+cudaError_t go(dim3 grid, unsigned threads, size_t smem, bool dependent, cudaStream_t s, A... args) {
+  constexpr int DEVICES = 64;
+  static std::atomic<size_t> limit[DEVICES];
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= DEVICES || limit[dev].load(std::memory_order_relaxed) < smem) {
+      e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      if (dev < DEVICES) limit[dev].store(smem, std::memory_order_relaxed);
+    }
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -138,9 +151,8 @@ cudaError_t go(void (*kernel)(A...), unsigned grid, unsigned threads, size_t sme
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, K, args...);
 }
-
 
 }  // namespace records
 }  // namespace kvq

@@ -946,14 +946,14 @@ cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
   const long long out_rows = (long long)(p.n_units / p.rb) * a.n * a.g;
   if (out_rows > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t pre = (size_t)(2 * a.batch + 1) * 4, smem = Smem<KF, F32>::total(p.N) + pre;
-  const cudaError_t e = p.N == 16   ? go(tree_kernel<KF, 8, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
-                        : p.N == 32 ? go(tree_kernel<KF, 16, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
-                        : p.N == 48 ? go(tree_kernel<KF, 24, F32>, (unsigned)p.G, THREADS, smem, false, s, p)
-                                    : go(tree_kernel<KF, 32, F32>, (unsigned)p.G, THREADS, smem, false, s, p);
+  const cudaError_t e = p.N == 16   ? go<tree_kernel<KF, 8, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
+                        : p.N == 32 ? go<tree_kernel<KF, 16, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
+                        : p.N == 48 ? go<tree_kernel<KF, 24, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
+                                    : go<tree_kernel<KF, 32, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p);
   if (e != cudaSuccess) return e;
   // many records a row (few units over all CTAs): a CTA per row, else a warp per row
-  if (p.G > 8 * p.n_units) return go(tree_merge_kernel<true>, (unsigned)out_rows, MERGE_WARPS * 32, pre, true, s, p);
-  return go(tree_merge_kernel<false>, (unsigned)((out_rows + MERGE_WARPS - 1) / MERGE_WARPS), MERGE_WARPS * 32, pre, true, s, p);
+  if (p.G > 8 * p.n_units) return go<tree_merge_kernel<true>>(dim3((unsigned)out_rows), MERGE_WARPS * 32, pre, true, s, p);
+  return go<tree_merge_kernel<false>>(dim3((unsigned)((out_rows + MERGE_WARPS - 1) / MERGE_WARPS)), MERGE_WARPS * 32, pre, true, s, p);
 }
 
 }  // namespace tree

@@ -4,7 +4,9 @@
 // keys) every position's logit is wanted twice: for the rows' normalisers, and for the positions' weights, the sum over
 // rows of 2^(logit - normaliser).  Two launches:
 //  1. weights_kernel<.., SUM = false>: per row the maximum and sum over this CTA's range of tiles (stream-K, as in tree
-//     attention: eight warps convert keys and finish logits, a ninth copies records and issues products, two CTAs an SM).
+//     attention: eight warps convert keys and finish logits, a ninth copies records and issues products, two CTAs an SM;
+//     the next tile's keys are converted while a tile's first products run, the next block's products run while a
+//     block's logits are finished).
 //     With at most 8 rows it also stores the logits: 4 bytes a row and position against at least 68 of key record.
 //  2. With stored logits weights_add_kernel, an elementwise pass; else weights_kernel<.., SUM = true>, which takes the
 //     logits again.  Both join the ranges' maxima and sums in a fixed order first.
@@ -27,6 +29,7 @@ using namespace tc;
 using namespace records;
 
 constexpr float NO_REF = -1e30f;
+constexpr int N = 16;           // rows of a block: the accumulators of two blocks fit beside the keys
 constexpr int STORE_ROWS = 8;
 constexpr int MAX_ROWS = 128, MAX_ROWS_TQ = 64;
 constexpr int ADD_THREADS = 256;
@@ -52,6 +55,8 @@ struct Cfg {
   static constexpr bool TQ = KF == KVQ_TQ3_QJL;
   static constexpr int KD = TQ ? 256 : 128;   // width of a query
   static constexpr int ACC = TQ ? 2 : 4;      // accumulators: centroids and signs, or groups of 32 channels
+  static constexpr int K_COLS = KD / 2;       // tensor-memory columns of a tile's keys
+  static constexpr int STAGES = KF == KVQ_Q8G32 ? 2 : 3;  // tiles of records in shared memory
 };
 // place of channel c among the keys' K elements: groups of 32 channels stay together
 template <int KF>
@@ -68,8 +73,9 @@ struct Smem {
   using C = Cfg<KF>;
   static __host__ __device__ constexpr uint32_t plane(int rows) { return rows * C::KD * 2; }  // of nb * N rows
   static __host__ __device__ constexpr uint32_t rec(int rows) { return 2 * plane(rows); }
-  static __host__ __device__ constexpr uint32_t proj(int rows) { return rec(rows) + 4 * Rec<KF>::KH; }  // TQ3: a plane of S
-  static __host__ __device__ constexpr uint32_t wm(int rows) { return proj(rows) + (C::TQ ? 32768 : 0); }  // [8][rows / 2]
+  static constexpr uint32_t REC = 4 * Rec<KF>::KH;
+  // (TQ3: a plane of the projection first takes the records' place)
+  static __host__ __device__ constexpr uint32_t wm(int rows) { return rec(rows) + (C::TQ ? 32768 : C::STAGES * REC); }  // [8][rows / 2]
   static __host__ __device__ constexpr uint32_t wl(int rows) { return wm(rows) + 16 * rows; }
   static __host__ __device__ constexpr uint32_t qs(int rows) { return wl(rows) + 16 * rows; }              // [rows][4]
   static __host__ __device__ constexpr uint32_t pre(int rows) { return qs(rows) + 16 * rows; }
@@ -170,20 +176,22 @@ __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long 
   return l > 0.f ? m + log2f(l) : INFINITY;
 }
 
-template <int KF, int N, bool SUM>
+template <int KF, bool SUM>
 __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF>;
   using SM = Smem<KF>;
   constexpr bool TQ = C::TQ, Q4 = KF == KVQ_Q4G32;
   constexpr int ACC = C::ACC, CH = 4;
-  // tensor memory: K (128 columns: codes; raw keys' hi and lo; TQ3 centroids and signs) | S, ACC accumulators of N columns
-  constexpr uint32_t C_S = 128, COLS = C_S + ACC * N, TM_COLS = 256;
-  static_assert(COLS <= TM_COLS, "tensor memory");
+  // tensor memory: K (128 columns: two tiles' codes; raw keys' hi and lo; TQ3 centroids and signs) | S, two buffers of ACC
+  // accumulators of N columns
+  constexpr uint32_t C_S = 128, TM_COLS = 256;
+  static_assert(C_S + 2 * ACC * N <= TM_COLS, "tensor memory");
+  static_assert(!TQ || C::STAGES * SM::REC <= 32768, "the records lie in the projection's place");
   constexpr uint32_t ID_S = idesc(TILE, N, false, false);
   extern __shared__ __align__(1024) uint8_t smem[];
   // kr_bar: a tile's keys have landed; k_bar: they are in place (one arrival a worker warp); s_bar: a block's logits have
   // been read; qk_bar: a block's products are done
-  __shared__ __align__(8) uint64_t kr_bar, k_bar, s_bar, qk_bar, end_bar;
+  __shared__ __align__(8) uint64_t kr_bar[C::STAGES], k_bar, s_bar[2], qk_bar[2], proj_bar, end_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   __shared__ float half_sum[TILE];
@@ -195,10 +203,13 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
   int* lens = pre + a.batch + 1;
 
   if (tid == 0) {
-    bar_init(&kr_bar, 1);
+    for (int i = 0; i < C::STAGES; ++i) bar_init(&kr_bar[i], 1);
     bar_init(&k_bar, WARPS);
-    bar_init(&s_bar, WARPS);
-    bar_init(&qk_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&s_bar[i], WARPS);
+      bar_init(&qk_bar[i], 1);
+    }
+    bar_init(&proj_bar, 1);
     bar_init(&end_bar, 1);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -225,12 +236,8 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     cent = make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.x, c.y, 0x7531),
                       __byte_perm(c.z, c.w, 0x7531));
   }
-  uint32_t kr_phase = 0, k_phase = 0, s_phase = 0, qk_phase = 0, kr_n = 0;
-  bool s_pending = false;
-  const auto wait = [&](uint64_t* bar, uint32_t& phase) {
-    bar_wait(bar, phase, &abort_sh, a.p.status);
-    phase ^= 1;
-  };
+  uint32_t k_n = 0, kr_n = 0, proj_n = 0, job = 0;  // tiles of keys, copies, projections and blocks so far: their phases
+  const auto wait_nth = [&](uint64_t* bar, uint32_t n) { bar_wait(bar, n & 1, &abort_sh, a.p.status); };
   const auto k_done = [&] {
     tm_wait_st();
     fence_before();
@@ -275,52 +282,54 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         const int j = it * TILE + lane * HALF;
         return lane < 4 && it < it1 && j < qend ? checked(__ldg(bt + j / PAGE), a.L.n_pages) : -1;
       };
-      const auto copy = [&](int phys) {
+      const auto copy = [&](int it) {
+        const int phys = page_of(it), stage = kr_n % C::STAGES;
         ++kr_n;
         const int n = __popc(__ballot_sync(FULL, phys >= 0));
-        if (lane == 0) bar_expect(&kr_bar, n * R::KH);
+        if (lane == 0) bar_expect(&kr_bar[stage], n * R::KH);
         __syncwarp();
         if (phys >= 0) {
           const uint8_t* src = unit_pages + (size_t)phys * page_stride + (lane & 1) * (size_t)(R::KH + R::VH);
-          uint8_t* dst = smem + SM::rec(NR) + lane * R::KH;
-          bulk_g2s(dst, src, R::K_MAIN, &kr_bar);
-          bulk_g2s(dst + R::K_MAIN, src + R::K_MAIN + R::V_MAIN, R::K_META, &kr_bar);
+          uint8_t* dst = smem + SM::rec(NR) + stage * SM::REC + lane * R::KH;
+          bulk_g2s(dst, src, R::K_MAIN, &kr_bar[stage]);
+          bulk_g2s(dst + R::K_MAIN, src + R::K_MAIN + R::V_MAIN, R::K_META, &kr_bar[stage]);
         }
         __syncwarp();
       };
-      int phys = -1;
-      if (!raw) copy(page_of(it0));
       if (TQ && !raw) {
         // S q~ of all rows to columns 0 .. NR - 1: the projection comes as its hi plane, then its lo plane
         for (int part = 0; part < 2; ++part) {
-          wait(&k_bar, k_phase);
+          wait_nth(&k_bar, k_n++);
           fence_after();
 #pragma unroll 1
           for (int rb = 0; rb < p.nb; ++rb) {
-            uint64_t sa = sdesc(sbase + SM::proj(NR), 2048, 128), qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
+            uint64_t sa = sdesc(sbase + SM::rec(NR), 2048, 128), qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
 #pragma unroll 1
             for (int ks = 0; ks < D / 16; ++ks, sa += 256, qa += 2 * N) {
               mma_ss(tmem + rb * N, sa, qa, ID_S, part > 0 || ks > 0);
               if (part == 0) mma_ss(tmem + rb * N, sa, qa + (q_plane >> 4), ID_S, 1);
             }
           }
-          mma_commit(&qk_bar);
+          mma_commit(&proj_bar);
         }
+        wait_nth(&proj_bar, proj_n + 1);  // (the records come to the projection's place)
+        proj_n += 2;
       }
+      if (!raw)
+        for (int it = it0; it < min(it1, it0 + C::STAGES); ++it) copy(it);
       for (int it = it0; it < it1; ++it) {
-        if (!raw) phys = page_of(it + 1);
-        wait(&k_bar, k_phase);
+        wait_nth(&k_bar, k_n++);
         if (*(volatile int*)&abort_sh) break;
-        if (!raw && it + 1 < it1) copy(phys);  // the workers have read this tile's keys
-        for (int rb = 0; rb < p.nb; ++rb) {
-          if (s_pending) wait(&s_bar, s_phase);
-          s_pending = true;
+        if (!raw && it + C::STAGES < it1) copy(it + C::STAGES);  // the workers have read this tile's keys
+        for (int rb = 0; rb < p.nb; ++rb, ++job) {
+          const int sb = job & 1;
+          if (job >= 2) wait_nth(&s_bar[sb], (job - 2) >> 1);
           if (*(volatile int*)&abort_sh) break;
           fence_after();
           uint64_t qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
           const uint64_t qb = q_plane >> 4;
-          uint32_t ka = tmem;
-          const uint32_t d = tmem + C_S;
+          uint32_t ka = tmem + (!TQ && !raw ? ((it - it0) & 1) * C::K_COLS : 0);
+          const uint32_t d = tmem + C_S + sb * (ACC * N);
           if (raw) {
 #pragma unroll 2
             for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
               mma_ts(d + ks / STEPS * N, ka, qa + qb, ID_S, 1);
             }
           }
-          mma_commit(&qk_bar);
+          mma_commit(&qk_bar[sb]);
         }
       }
       ok = !*(volatile int*)&abort_sh;
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       const int i = tid & 127;
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
-        if (part) wait(&qk_bar, qk_phase);
+        if (part) wait_nth(&proj_bar, proj_n);
 #pragma unroll 1
         for (int kg = tid >> 7; kg < D / 8; kg += 2) {
           float s[8];
@@ -417,12 +426,13 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
           split2(s[2], s[3], o.y, l.y);
           split2(s[4], s[5], o.z, l.z);
           split2(s[6], s[7], o.w, l.w);
-          *reinterpret_cast<uint4*>(smem + SM::proj(NR) + km_off(i, 8 * kg, D)) = part ? l : o;
+          *reinterpret_cast<uint4*>(smem + SM::rec(NR) + km_off(i, 8 * kg, D)) = part ? l : o;
         }
         fence_async_smem();
         k_done();
       }
-      wait(&qk_bar, qk_phase);
+      wait_nth(&proj_bar, proj_n + 1);
+      proj_n += 2;
       fence_after();
 #pragma unroll 1
       for (int c = (warp >> 2) * (NR / 2); c < ((warp >> 2) + 1) * (NR / 2); c += 8) {
@@ -442,36 +452,33 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     fence_async_smem();
     part_sync(1, WORKERS);
 
-    for (int it = it0; it < it1; ++it) {
-      const int x = (it - nq) * TILE + ln.t;                  // raw: place in the window
-      const int j = raw ? qend + x : it * TILE + ln.t;        // this thread's position
-      const bool mine = j < (raw ? L : qend);
-      bool valid = mine;                                      // (a page out of range takes no weight)
-      // ---- keys (the previous tile's products are done)
-      float s0[4] = {}, z0[4] = {};                           // scales and zeros; TQ3: norm, weight
+    // keys of tile `it` to tensor memory; scales and zeros (TQ3: norm, weight) of this thread's position as they are
+    uint4 meta = make_uint4(0u, 0u, 0u, 0u);
+    bool bad = false;
+    const auto put = [&](int it) {
+      const int j = (raw ? qend - nq * TILE : 0) + it * TILE + ln.t;
       if (!raw) {
-        if (checked(page, a.L.n_pages) < 0) {
-          if (valid && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
-          valid = false;
-        }
+        bad = checked(page, a.L.n_pages) < 0;
+        if (bad && j < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
         page = page_of(it + 1);
-        wait(&kr_bar, kr_phase);
-        const uint8_t* rec = smem + SM::rec(NR);
-        put_codes<KF>(lane_addr, ln, rec, cent);
-        const __half* m = reinterpret_cast<const __half*>(rec + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN);
+        const int stage = kr_n % C::STAGES;
+        wait_nth(&kr_bar[stage], kr_n / C::STAGES);
+        ++kr_n;
+        const uint8_t* rec = smem + SM::rec(NR) + stage * SM::REC;
+        put_codes<KF>(lane_addr + (TQ ? 0 : ((it - it0) & 1) * C::K_COLS), ln, rec, cent);
+        const uint8_t* m = rec + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN;
         const int tt = ln.t & 31;
         if (TQ) {
-          s0[0] = __half2float(m[tt]);
-          s0[1] = s0[0] * QJL_CONST * __half2float(m[HALF + tt]);
+          meta.x = reinterpret_cast<const unsigned short*>(m)[tt];
+          meta.y = reinterpret_cast<const unsigned short*>(m)[HALF + tt];
+        } else if (Q4) {
+          meta = *reinterpret_cast<const uint4*>(m + 16 * tt);
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s0[i] = __half2float(m[(Q4 ? 8 : 4) * tt + i]);
-            if (Q4) z0[i] = __half2float(m[8 * tt + 4 + i]);
-          }
+          const uint2 v = *reinterpret_cast<const uint2*>(m + 8 * tt);
+          meta.x = v.x, meta.y = v.y;
         }
       } else {
-        const float* row = a.p.ringk + ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (valid ? (unsigned)j % (unsigned)a.W : 0u)) * D;
+        const float* row = a.p.ringk + ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (j < L ? (unsigned)j % (unsigned)a.W : 0u)) * D;
 #pragma unroll 2
         for (int i = 0; i < 8; ++i) {
           const int kg = 8 * ln.hf + i;
@@ -499,12 +506,33 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         }
       }
       k_done();
+    };
+    put(it0);
+    for (int it = it0; it < it1; ++it) {
+      const int j = (raw ? qend - nq * TILE : 0) + it * TILE + ln.t;  // this thread's position
+      const bool mine = j < (raw ? L : qend), valid = mine && !bad;   // (a page out of range takes no weight)
+      float s0[4] = {}, z0[4] = {};
+      if (TQ) {
+        s0[0] = __half2float(__ushort_as_half((unsigned short)meta.x));
+        s0[1] = s0[0] * QJL_CONST * __half2float(__ushort_as_half((unsigned short)meta.y));
+      } else {
+        const float2 a0 = __half22float2(u2h(meta.x)), a1 = __half22float2(u2h(meta.y));
+        s0[0] = a0.x, s0[1] = a0.y, s0[2] = a1.x, s0[3] = a1.y;
+        if (Q4) {
+          const float2 b0 = __half22float2(u2h(meta.z)), b1 = __half22float2(u2h(meta.w));
+          z0[0] = b0.x, z0[1] = b0.y, z0[2] = b1.x, z0[3] = b1.y;
+        }
+      }
+      // the next tile's keys, while this one's products run (TQ3's and raw ones have no second place)
+      if (!TQ && !raw && it + 1 < it1) put(it + 1);
       // rows from this one on attend to the position (token of the row >= j - L + n)
       const int cut = valid ? a.g * max(0, j - L + a.n) - p.row0 : 1 << 30;
       float acc = 0.f;
 #pragma unroll 1
-      for (int rb = 0; rb < p.nb; ++rb) {
-        wait(&qk_bar, qk_phase);
+      for (int rb = 0; rb < p.nb; ++rb, ++job) {
+        const int sb = job & 1;
+        const uint32_t s_addr = lane_addr + C_S + sb * (ACC * N);
+        wait_nth(&qk_bar[sb], job >> 1);
         fence_after();
 #pragma unroll 1
         for (int c = col0; c < col0 + N / 2 && rb * N + c < p.rows; c += CH) {
@@ -513,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
           float s[CH], part[ACC][CH];
 #pragma unroll
           for (int i = 0; i < ACC; ++i)
-            if (i == 0 || !raw) tm_ld(lane_addr + C_S + i * N + c, part[i]);
+            if (i == 0 || !raw) tm_ld(s_addr + i * N + c, part[i]);
           tm_wait_ld();
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
@@ -583,8 +611,9 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&s_bar);
+        if (lane == 0) bar_arrive(&s_bar[sb]);
       }
+      if ((TQ || raw) && it + 1 < it1) put(it + 1);
       if (SUM) {
         if (warp >= 4) half_sum[ln.t] = acc;
         part_sync(1, WORKERS);
@@ -628,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       while (!bar_try(bar, parity) && gtimer() - t0 < WAIT_NS) {
       }
     };
-    if (kr_n) land(&kr_bar, (kr_n - 1) & 1);
+    for (uint32_t i = kr_n < C::STAGES ? 0 : kr_n - C::STAGES; i < kr_n; ++i) land(&kr_bar[i % C::STAGES], i / C::STAGES & 1);
     mma_commit(&end_bar);
     land(&end_bar, 0);
   }
@@ -691,7 +720,6 @@ size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
   p->a = a;
   p->row0 = row0;
   p->rows = all - row0 < most ? all - row0 : most;
-  const int N = p->rows <= 16 ? 16 : 32;
   p->nb = (p->rows + N - 1) / N;
   p->n_units = a.n_layers_call * a.batch * a.Hkv;
   p->G = 2 * sms;
@@ -704,24 +732,15 @@ size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
   return parts + (store ? (size_t)p->n_units * p->rows * p->s_pad * sizeof(float) : 0);
 }
 
-template <int KF, int N>
+template <int KF>
 cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
   const size_t pre = (size_t)(2 * p.a.batch + 1) * 4, smem = Smem<KF>::pre(p.nb * N) + pre;
-  cudaError_t e = go(weights_kernel<KF, N, false>, (unsigned)p.G, THREADS, smem, false, s, p);
+  cudaError_t e = go<weights_kernel<KF, false>>(dim3((unsigned)p.G), THREADS, smem, false, s, p);
   if (e != cudaSuccess) return e;
-  if (p.logits == nullptr) return go(weights_kernel<KF, N, true>, (unsigned)p.G, THREADS, smem, true, s, p);
-  cudaLaunchConfig_t cfg = {};
+  if (p.logits == nullptr) return go<weights_kernel<KF, true>>(dim3((unsigned)p.G), THREADS, smem, true, s, p);
   const unsigned y = p.n_units < 32768 ? p.n_units : 32768;
-  cfg.gridDim = dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768);
-  cfg.blockDim = dim3(ADD_THREADS);
-  cfg.dynamicSmemBytes = pre;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_add_kernel, p);
+  return go<weights_add_kernel>(dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768),
+                                ADD_THREADS, pre, true, s, p);
 }
 
 template <int KF>
@@ -729,7 +748,7 @@ cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
   for (int row0 = 0; row0 < a.n * a.g;) {
     Plan p;
     make_plan<KF>(a, sms, row0, &p);
-    const cudaError_t e = p.rows <= 16 ? launch_rows<KF, 16>(p, s) : launch_rows<KF, 32>(p, s);
+    const cudaError_t e = launch_rows<KF>(p, s);
     if (e != cudaSuccess) return e;
     row0 += p.rows;
   }

@@ -129,19 +129,21 @@ def _check(rc: int):
         raise KVQError(f"libkvq: {load().kv_strerror(rc).decode()} (code {rc})")
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream=None) -> int:
+    """The cudaStream_t of ``stream``, or of the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
+def _ptr(t: torch.Tensor | None) -> int:
     if t is None:
-        return ctypes.c_void_p(0)
+        return 0
     if not t.is_cuda:
         raise KVQError("device tensor expected")
     if not t.is_contiguous():
         raise KVQError("contiguous tensor expected")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _check_in_dtype(cache: kvq_cache, *tensors: torch.Tensor):
@@ -156,10 +158,10 @@ def _layers_in_call(cache: kvq_cache, layer: int) -> int:
     return cache.cfg.n_layers if layer == -1 else 1
 
 
-def _check_shape(name: str, t: torch.Tensor, want: tuple):
+def _check_shape(name: str, t: torch.Tensor, want: tuple):  # (a torch.Size is a tuple)
     """The library reads and writes whole rows of these shapes from the bare pointer; a tensor of
     another size would be read or written past its end, which the C ABI cannot see."""
-    if tuple(t.shape) != tuple(want):
+    if t.shape != want:
         raise KVQError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
