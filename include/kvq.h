@@ -405,15 +405,13 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
  *                a sequence of fewer than ``budget`` tokens (which is left as it is)
  *   new_lens     device int32 [batch] (out): min(seq_lens[b], budget); not the same buffer as seq_lens
  *   budget, recent   window <= recent <= budget <= max_seq_len
- *   scratch      device, >= kv_evict_scratch_bytes bytes (a copy of the kept records), any contents
  * All layers of a sequence have to be cut together (layer == -1, or each layer in turn) before its new length is
  * used.  A page must not be shared by several sequences, or by positions of one, when it is evicted from.  A
  * block-table entry outside [0, n_pages) is flagged KVQ_DEV_BAD_PAGE: records in it count as zeros, and slots in
  * it are not written.
  */
-size_t kv_evict_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget);
 int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
-             int32_t batch, int32_t budget, int32_t recent, void* scratch, size_t scratch_bytes, void* stream);
+             int32_t batch, int32_t budget, int32_t recent, void* stream);
 
 /*
  * Block codecs next to the cache: the TurboQuant MSE quantiser ([TQ] "key idea" row: random

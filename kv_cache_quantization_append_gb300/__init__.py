@@ -108,13 +108,7 @@ class QuantKVCache:
             kept = torch.empty(tuple(weights.shape[:-1]) + (budget,), dtype=torch.int32, device=weights.device)
         if new_lens is None:
             new_lens = torch.empty_like(seq_lens)
-        batch = seq_lens.shape[0]
-        # a copy of the kept records: one buffer, as large as the largest call so far
-        need = lib.kv_evict_scratch_bytes(self.handle, layer, batch, budget)
-        scratch = self._scratch.get("evict")
-        if scratch is None or scratch.numel() < need:
-            scratch = self._scratch["evict"] = torch.empty(max(1, need), dtype=torch.uint8, device=self.buffer.device)
-        lib.kv_evict(self.handle, layer, weights, seq_lens, kept, new_lens, budget, recent, scratch, stream)
+        lib.kv_evict(self.handle, layer, weights, seq_lens, kept, new_lens, budget, recent, stream)
         return kept, new_lens
 
     def status(self) -> int:

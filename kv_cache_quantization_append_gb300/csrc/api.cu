@@ -577,28 +577,19 @@ static int evict_args(const kvq_cache* cache, int32_t layer, int32_t batch, int3
   return KVQ_OK;
 }
 
-size_t kv_evict_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget) {
-  EvictArgs a;
-  if (evict_args(cache, layer, batch, budget, &a) != KVQ_OK) return 0;
-  return std::max<size_t>(256, evict_scratch_bytes(a.n_units, budget, a.L.half_bytes));
-}
-
 int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
-             int32_t batch, int32_t budget, int32_t recent, void* scratch, size_t scratch_bytes, void* stream) {
+             int32_t batch, int32_t budget, int32_t recent, void* stream) {
   EvictArgs a;
   int rc = evict_args(cache, layer, batch, budget, &a);
   if (rc != KVQ_OK) return rc;
-  if (!weights || !seq_lens || !kept || !new_lens || !scratch || new_lens == seq_lens) return KVQ_ERR_INVALID_ARG;
+  if (!weights || !seq_lens || !kept || !new_lens || new_lens == seq_lens) return KVQ_ERR_INVALID_ARG;
   if (recent < 0 || recent < cache->cfg.window || recent > budget) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(weights) || !aligned16(seq_lens) || !aligned16(kept) || !aligned16(new_lens) || !aligned16(scratch))
-    return KVQ_ERR_ALIGN;
-  if (scratch_bytes < kv_evict_scratch_bytes(cache, layer, batch, budget)) return KVQ_ERR_CAPACITY;
+  if (!aligned16(weights) || !aligned16(seq_lens) || !aligned16(kept) || !aligned16(new_lens)) return KVQ_ERR_ALIGN;
   if ((rc = check_device(cache)) != KVQ_OK) return rc;
   a.weights = weights;
   a.seq_lens = seq_lens;
   a.kept = kept;
   a.new_lens = new_lens;
-  a.images = static_cast<uint8_t*>(scratch);
   a.recent = recent;
   return cuda_err(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }

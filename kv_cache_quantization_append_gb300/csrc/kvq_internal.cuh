@@ -141,11 +141,9 @@ struct EvictArgs {
   const int32_t* seq_lens;
   int32_t* kept;            // [L?][batch][Hkv][budget]
   int32_t* new_lens;        // [batch]
-  uint8_t* images;          // scratch: [n_units][n_halves][half_bytes]
   int layer0, batch, max_batch, Hkv, W, k_format, max_pages_per_seq, max_seq_len;
   int budget, recent, n_units, n_halves;
 };
-size_t evict_scratch_bytes(int n_units, int budget, int half_bytes);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 // Attention of several queries per sequence over the cache as it stands: the nodes of drafted trees (their

@@ -40,8 +40,7 @@ EXPORTS = ("kv_cache_bytes", "kv_cache_init", "kv_calibrate_scratch_bytes", "kv_
            "kv_tbq_block_bytes", "kv_tbq_encode", "kv_tbq_decode", "kv_split_record_bytes",
            "kv_split_outliers", "kv_split_encode", "kv_split_decode", "kv_status", "kv_set_wait_limit_ns",
            "kv_strerror", "kv_rope_init", "kv_qk_norm_rope", "kv_tree_scratch_bytes", "kv_tree_attention",
-           "kv_tree_commit", "kv_weights_scratch_bytes", "kv_attention_weights", "kv_evict_scratch_bytes",
-           "kv_evict")
+           "kv_tree_commit", "kv_weights_scratch_bytes", "kv_attention_weights", "kv_evict")
 NOALLOC_SCRATCH_MAX = 32 * 1024 * 1024
 
 
@@ -113,8 +112,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kv_tree_commit": (ctypes.c_int, [cachep, I32, P, P, P, P, P, I32, I32, I32, P]),
         "kv_weights_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
         "kv_attention_weights": (ctypes.c_int, [cachep, I32, P, P, F32, P, I32, I32, P, SZ, P]),
-        "kv_evict_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
-        "kv_evict": (ctypes.c_int, [cachep, I32, P, P, P, P, I32, I32, I32, P, SZ, P]),
+        "kv_evict": (ctypes.c_int, [cachep, I32, P, P, P, P, I32, I32, I32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -404,14 +402,10 @@ def kv_attention_weights(cache: kvq_cache, layer: int, q: torch.Tensor, weights:
                                        _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
-def kv_evict_scratch_bytes(cache: kvq_cache, layer: int, batch: int, budget: int) -> int:
-    return int(load().kv_evict_scratch_bytes(ctypes.byref(cache), layer, batch, budget))
-
-
 def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torch.Tensor, kept: torch.Tensor,
-             new_lens: torch.Tensor, budget: int, recent: int, scratch: torch.Tensor, stream=None):
+             new_lens: torch.Tensor, budget: int, recent: int, stream=None):
     """weights: float32 [L?][B][Hkv][max_seq_len] (compacted); seq_lens: int32 [B]; kept: int32 [L?][B][Hkv][budget] and
-    new_lens: int32 [B] (written); scratch: device bytes, at least kv_evict_scratch_bytes."""
+    new_lens: int32 [B] (written)."""
     if seq_lens.dtype != torch.int32 or kept.dtype != torch.int32 or new_lens.dtype != torch.int32:
         raise KVQError("seq_lens, kept and new_lens must be int32")
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
@@ -420,7 +414,7 @@ def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torc
     _check_weights(cache, layer, B, weights)
     _check_shape("kept", kept, tuple(weights.shape[:-1]) + (budget,))
     _check(load().kv_evict(ctypes.byref(cache), layer, _ptr(weights), _ptr(seq_lens), _ptr(kept), _ptr(new_lens), B, budget,
-                           recent, _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
+                           recent, _stream(stream)))
 
 
 def _in_dtype_of(t: torch.Tensor) -> int:

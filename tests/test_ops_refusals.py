@@ -84,10 +84,9 @@ def test_uninitialised_cache(kvq):
         assert kvq.kv_tree_attention(cache, 0, d, d, d, d, d, d, 1, 4, d, 1 << 30, None) == code
         assert kvq.kv_tree_commit(cache, 0, d, d, d, d, d, 1, 4, 4, None) == code
         assert kvq.kv_attention_weights(cache, 0, d, d, 1.0, d, 1, 1, d, 1 << 30, None) == code
-        assert kvq.kv_evict(cache, 0, d, d, d, P(FAKE + 16), 1, 64, 64, d, 1 << 30, None) == code
+        assert kvq.kv_evict(cache, 0, d, d, d, P(FAKE + 16), 1, 64, 64, None) == code
         assert kvq.kv_tree_scratch_bytes(cache, 0, 1, 4) == 0
         assert kvq.kv_weights_scratch_bytes(cache, 0, 1, 4) == 0
-        assert kvq.kv_evict_scratch_bytes(cache, 0, 1, 64) == 0
 
 
 @pytest.mark.parametrize("i", [1, 2, 3, 4, 5, 6, 9])
@@ -146,19 +145,16 @@ def test_weights_ranges(kvq):
 def test_evict_ranges(kvq):
     c, d = _cache(), P(FAKE)
 
-    def call(layer=0, w=d, ln=d, kept=d, new=P(FAKE + 64), B=2, budget=256, recent=128, s=d, sb=1 << 40):
-        return kvq.kv_evict(ctypes.byref(c), layer, w, ln, kept, new, B, budget, recent, s, sb, None)
+    def call(layer=0, w=d, ln=d, kept=d, new=P(FAKE + 64), B=2, budget=256, recent=128):
+        return kvq.kv_evict(ctypes.byref(c), layer, w, ln, kept, new, B, budget, recent, None)
 
-    for name in ("w", "ln", "kept", "new", "s"):
+    for name in ("w", "ln", "kept", "new"):
         assert call(**{name: None}) == INVALID, name
         assert call(**{name: P(FAKE + 4)}) == ALIGN, name
     assert call(new=d) == INVALID                              # the lengths are still read while new ones are written
     assert call(recent=127) == INVALID and call(recent=-1) == INVALID and call(recent=257) == INVALID
     assert call(budget=0) == INVALID and call(budget=1025) == INVALID
     assert call(layer=5) == INVALID and call(B=5) == INVALID
-    assert call(sb=1024) == CAPACITY
-    # a copy of the kept records: 4 x 8 units of 8 half-pages of 5120 bytes
-    assert kvq.kv_evict_scratch_bytes(ctypes.byref(c), 0, 4, 256) == 4 * 8 * 8 * 5120
 
 
 def test_binding_shapes():
@@ -185,7 +181,7 @@ def test_binding_shapes():
                  (w, ln.long(), kept, ln.clone(), 256, 128), (w[:1], ln, kept, ln.clone(), 256, 128),
                  (w, ln, kept, ln[:1], 256, 128), (w, ln[None], kept, ln.clone(), 256, 128)):
         with pytest.raises(lib.KVQError):
-            lib.kv_evict(c, 0, *args, s)
+            lib.kv_evict(c, 0, *args)
     r = lib.kv_rope_init(128)
     x = z(2, 3, 12 * 128, dtype=bf)
     pos = z(2, 3, dtype=i32)
