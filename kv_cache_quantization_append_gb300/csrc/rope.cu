@@ -44,9 +44,9 @@ struct RopeArgs {
 
 enum { IN_LANE, ADJACENT, REREAD };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
+// place of a pair's sine and cosine in shared memory: eight lanes, each with eight consecutive pairs, read without conflicts
+__device__ __forceinline__ int cs_at(int pair) { return (pair & 7) * 8 + (pair >> 3); }
+
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -56,10 +56,16 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+// two running sums of squares
+__device__ __forceinline__ void fma2_acc(float& s0, float& s1, float x0, float x1) {
+  float a0 = x0, a1 = x1;
+  fma2(a0, a1, x0, x1, s0, s1);
+  s0 = a0;
+  s1 = a1;
 }
 __device__ __forceinline__ void store8v(__nv_bfloat16* p, const float (&v)[8]) {
   uint4 u;
@@ -82,87 +88,90 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 template <typename T, int MODE>
 __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constant__ RopeArgs a, int tpc) {
   __shared__ float2 cs[TPC_MAX][D / 2];
-  __shared__ int pos_sh[TPC_MAX];
+  __shared__ int2 tok_sh[TPC_MAX];  // sequence and token of each row; token < 0: a padded row
   const int tid = threadIdx.x;
   const int row0 = blockIdx.x * tpc, nrow = min(tpc, a.rows - row0);
   const int half = a.rot >> 1;
   for (int i = tid; i < nrow * (D / 2); i += THREADS) {
-    const int r = i / (D / 2), c = i % (D / 2);
-    const int p = a.pos[row0 + r];
-    if (c == 0) pos_sh[r] = p;
+    const int r = i / (D / 2), c = i % (D / 2), p = a.pos[row0 + r];
+    if (c == 0) {
+      const int b = (row0 + r) / a.T;
+      tok_sh[r] = make_int2(b, p < 0 ? -1 : row0 + r - b * a.T);
+    }
     if (c < half) {
       const long long turn = (long long)((uint64_t)(uint32_t)p * a.turns[c]);  // modulo one turn, signed
       float s, co;
       sincospif(__ll2float_rn(turn) * 1.0842021724855044e-19f, &s, &co);     // 2^-63: half turns
-      cs[r][c] = make_float2(co * a.attn, s * a.attn);
+      cs[r][cs_at(c)] = make_float2(co * a.attn, s * a.attn);
     }
   }
   __syncthreads();
-  const int l = tid & 7, grp = tid >> 3;
+  const int l = tid & 7;
   const int nb = a.rot >> 4;  // IN_LANE: blocks of 8 channels in each half
   const int b0 = MODE == IN_LANE ? (l < nb ? l : 2 * l) : 2 * l;
   const int b1 = MODE == IN_LANE && l < nb ? l + nb : b0 + 1;
-  for (int j = grp; j < nrow * a.jobs; j += GROUPS) {
-    const int r = j / a.jobs, hd = j - r * a.jobs;
-    const int row = row0 + r;
-    const T* src = static_cast<const T*>(a.x) + (int64_t)row * a.row_stride + (int64_t)hd * D;
-    const int kind = hd < a.Hq ? 0 : hd < a.Hq + a.Hkv ? 1 : 2;
-    float x0[8], x1[8];
-    load8(src + 8 * b0, x0);
-    load8(src + 8 * b1, x1);
-    const int b = row / a.T, t = row - b * a.T;
-    const int hh = kind == 0 ? hd : kind == 1 ? hd - a.Hq : hd - a.Hq - a.Hkv;
-    const int heads = kind == 0 ? a.Hq : a.Hkv;
-    T* dst = static_cast<T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + (((int64_t)b * heads + hh) * a.T + t) * D;
-    const T* w = static_cast<const T*>(kind == 0 ? a.wq : a.wk);
-    const bool norm = kind < 2 && w != nullptr;
-    float inv = 1.f;
-    // the eight lanes of a head take part together; heads of one warp may differ
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-    const unsigned grp_mask = 0xffu << (threadIdx.x & 24);
-    ss += __shfl_xor_sync(grp_mask, ss, 1);
-    ss += __shfl_xor_sync(grp_mask, ss, 2);
-    ss += __shfl_xor_sync(grp_mask, ss, 4);
-    if (norm) {
-      inv = rsqrtf(ss * (1.f / D) + a.eps);
-      float w0[8], w1[8];
-      load8(w + 8 * b0, w0);
-      load8(w + 8 * b1, w1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x0[i] *= inv * w0[i];
-        x1[i] *= inv * w1[i];
-      }
+  const unsigned grp_mask = 0xffu << (tid & 24);
+  const T* row = static_cast<const T*>(a.x) + (int64_t)row0 * a.row_stride;
+  int r = 0, hd = tid >> 3;  // this group's row and head vector
+  while (true) {
+    while (hd >= a.jobs) {
+      hd -= a.jobs;
+      row += a.row_stride;
+      ++r;
     }
+    if (r >= nrow) break;
+    const T* src = row + hd * D;
+    float x[16];
+    load8(src + 8 * b0, *reinterpret_cast<float(*)[8]>(x));
+    load8(src + 8 * b1, *reinterpret_cast<float(*)[8]>(x + 8));
+    const int kind = hd < a.Hq ? 0 : hd < a.Hq + a.Hkv ? 1 : 2;
+    const int2 tok = tok_sh[r];
+    const int heads = kind == 0 ? a.Hq : a.Hkv, hh = hd - (kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hkv);
+    T* dst = static_cast<T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + (((int64_t)tok.x * heads + hh) * a.T + max(tok.y, 0)) * D;
     if (kind < 2) {
+      const T* w = static_cast<const T*>(kind == 0 ? a.wq : a.wk);
+      const bool norm = w != nullptr;
+      float inv = 1.f;
+      if (norm) {
+        // (the eight lanes of a head take part together; heads of one warp may differ in kind)
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) fma2_acc(s0, s1, x[i], x[i + 1]);
+        float ss = s0 + s1;
+        ss += __shfl_xor_sync(grp_mask, ss, 1);
+        ss += __shfl_xor_sync(grp_mask, ss, 2);
+        ss += __shfl_xor_sync(grp_mask, ss, 4);
+        inv = rsqrtf(ss * (1.f / D) + a.eps);
+        float w0[8], w1[8];
+        load8(w + 8 * b0, w0);
+        load8(w + 8 * b1, w1);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          mul2(w0[i], w0[i + 1], inv, inv);
+          mul2(w1[i], w1[i + 1], inv, inv);
+          mul2(x[i], x[i + 1], w0[i], w0[i + 1]);
+          mul2(x[8 + i], x[9 + i], w1[i], w1[i + 1]);
+        }
+      }
       const float2* c = cs[r];
       if (MODE == IN_LANE) {
         if (l < nb) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 f = c[8 * l + i];
-            const float u = x0[i], v = x1[i];
-            x0[i] = u * f.x - v * f.y;
-            x1[i] = v * f.x + u * f.y;
+            const float2 f = c[i * 8 + l];
+            const float u = x[i], v = x[8 + i];
+            x[i] = u * f.x - v * f.y;
+            x[8 + i] = v * f.x + u * f.y;
           }
         }
       } else if (MODE == ADJACENT) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int p0 = 4 * b0 + (i >> 1), p1 = 4 * b1 + (i >> 1);
-          if (p0 < half) {
-            const float2 f = c[p0];
-            const float u = x0[i], v = x0[i + 1];
-            x0[i] = u * f.x - v * f.y;
-            x0[i + 1] = v * f.x + u * f.y;
-          }
-          if (p1 < half) {
-            const float2 f = c[p1];
-            const float u = x1[i], v = x1[i + 1];
-            x1[i] = u * f.x - v * f.y;
-            x1[i + 1] = v * f.x + u * f.y;
+        for (int i = 0; i < 8; ++i) {
+          if (8 * l + i < half) {
+            const float2 f = c[i * 8 + l];
+            const float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * f.x - v * f.y;
+            x[2 * i + 1] = v * f.x + u * f.y;
           }
         }
       } else {
@@ -174,17 +183,17 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
             const int mate = first ? ch + half : ch - half;
             float m = to_f(src[mate]);
             if (norm) m *= inv * to_f(w[mate]);
-            const float2 f = c[first ? ch : mate];
-            float& me = e < 8 ? x0[e & 7] : x1[e & 7];
-            me = first ? me * f.x - m * f.y : me * f.x + m * f.y;
+            const float2 f = c[cs_at(first ? ch : mate)];
+            x[e] = first ? x[e] * f.x - m * f.y : x[e] * f.x + m * f.y;
           }
         }
       }
     }
-    if (pos_sh[r] >= 0) {
-      store8v(dst + 8 * b0, x0);
-      store8v(dst + 8 * b1, x1);
+    if (tok.y >= 0) {
+      store8v(dst + 8 * b0, *reinterpret_cast<float(*)[8]>(x));
+      store8v(dst + 8 * b1, *reinterpret_cast<float(*)[8]>(x + 8));
     }
+    hd += GROUPS;
   }
 }
 
