@@ -2,14 +2,15 @@
 //
 // For the rows of a unit (query heads of its newest n tokens, row = token * g + head; at most 128 a launch, 64 for TQ3
 // keys) every position's logit is wanted twice: for the rows' normalisers, and for the positions' weights, the sum over
-// rows of 2^(logit - normaliser).  Two launches:
+// rows of 2^(logit - normaliser):
 //  1. weights_kernel<.., SUM = false>: per row the maximum and sum over this CTA's range of tiles (stream-K, as in tree
 //     attention: eight warps convert keys and finish logits, a ninth copies records and issues products, two CTAs an SM;
 //     the next tile's keys are converted while a tile's first products run, the next block's products run while a
 //     block's logits are finished).
 //     With at most 8 rows it also stores the logits: 4 bytes a row and position against at least 68 of key record.
-//  2. With stored logits weights_add_kernel, an elementwise pass; else weights_kernel<.., SUM = true>, which takes the
-//     logits again.  Both join the ranges' maxima and sums in a fixed order first.
+//  2. With stored logits weights_add_kernel, an elementwise pass that joins the ranges' maxima and sums in a fixed order
+//     first; else normaliser_kernel, which joins them once per row, and weights_kernel<.., SUM = true>, which takes the
+//     logits again.
 //
 // The weights accumulate in fp32, so logits are taken to fp32's accuracy: the keys' codes go to the tensor cores as they
 // are, exact in fp16 (S^T = codes [128 positions x 128] Q~^T, the queries as fp16 hi and lo), one accumulator per group of
@@ -43,6 +44,7 @@ struct Plan {
   float decay;
   float* parts;       // [2 n_units + G][rows][2]: range c's maxima and sums of unit u's records (+ 0), raw keys (+ 1) at 2 u + c
   float* logits;      // [n_units][rows][s_pad], or null
+  float* norms;       // [n_units][rows] normalisers, where logits are taken again
 };
 
 __host__ __device__ inline int quant_tiles(int L, int W) { return (L > W ? L - W + TILE - 1 : 0) / TILE; }
@@ -176,12 +178,14 @@ __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long 
   return l > 0.f ? m + log2f(l) : INFINITY;
 }
 
-template <int KF, bool SUM>
+// CH: a thread's rows of a block at a time: 8, or 4 where there are no more (they then keep their sums in registers)
+template <int KF, bool SUM, int CH>
 __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF>;
   using SM = Smem<KF>;
   constexpr bool TQ = C::TQ, Q4 = KF == KVQ_Q4G32;
-  constexpr int ACC = C::ACC, CH = 4;
+  constexpr int ACC = C::ACC;
+  constexpr bool FEW = CH == 4;
   // tensor memory: K (128 columns: two tiles' codes; raw keys' hi and lo; TQ3 centroids and signs) | S, two buffers of ACC
   // accumulators of N columns
   constexpr uint32_t C_S = 128, TM_COLS = 256;
@@ -265,7 +269,6 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     const int h = (int)quick_div(r, tiles), place0 = (int)(r - (long long)h * tiles), layer = a.layer0 + ll;
     const int u = (ll * a.batch + b) * a.Hkv + h;
     const int L = lens[b], qend = max(0, L - a.W), nq = quant_tiles(L, a.W);
-    const long long first = t - place0;
     const bool raw = place0 >= nq;
     const int place1 = (int)min((long long)(raw ? tiles : nq), place0 + (t_end - t));
     t += place1 - place0;
@@ -360,38 +363,44 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     int page = page_of(it0);
     // ---- queries in base-2 units as hi and lo images, for records rotated and balanced; sums over groups for the zeros
 #pragma unroll 1
-    for (int r0 = warp; r0 < NR; r0 += 4 * WARPS) {
-      float4 q[4];
+    for (int r0 = warp; r0 < NR; r0 += 2 * WARPS) {
+      float y[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int lr = r0 + i * WARPS, row = p.row0 + lr;
-        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
         if (lr < p.rows)
-          q[i] = load4_in(a.q, ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + row / a.g) * D + 4 * lane,
-                          a.in_bf16);
+          q = load4_in(a.q, ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + row / a.g) * D + 4 * lane,
+                       a.in_bf16);
+        y[i][0] = q.x, y[i][1] = q.y, y[i][2] = q.z, y[i][3] = q.w;
       }
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int lr = r0 + i * WARPS;
-        if (lr >= NR) break;
-        const float4 x = q[0];
-        q[0] = q[1], q[1] = q[2], q[2] = q[3];
-        float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int lr = r0 + i * WARPS;  // (NR is a multiple of 16: both rows are there)
         if (!raw) {
-          y[0] *= sg.x, y[1] *= sg.y, y[2] *= sg.z, y[3] *= sg.w;
-          hadamard_warp(y[0], y[1], y[2], y[3], lane);
+          y[i][0] *= sg.x, y[i][1] *= sg.y, y[i][2] *= sg.z, y[i][3] *= sg.w;
+          hadamard_warp(y[i][0], y[i][1], y[i][2], y[i][3], lane);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
-          if (a.sinkhorn && !raw) y[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
-          uint8_t* dst = smem + (lr / N) * (N * C::KD * 2) + km_off(lr % N, place<KF>(4 * lane + e), N);
-          const __half hi16 = __float2half_rn(y[e]);
-          *reinterpret_cast<__half*>(dst) = hi16;
-          *reinterpret_cast<__half*>(dst + q_plane) = __float2half_rn(y[e] - __half2float(hi16));
+          y[i][e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+          if (a.sinkhorn && !raw) y[i][e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
+        }
+        uint8_t* img = smem + (lr / N) * (N * C::KD * 2);
+        if (KF == KVQ_Q8G32) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {  // channels c and c + 1 are neighbours
+            uint32_t hi2, lo2;
+            split2(y[i][e], y[i][e + 1], hi2, lo2);
+            uint8_t* dst = img + km_off(lr % N, place<KF>(4 * lane + e), N);
+            *reinterpret_cast<uint32_t*>(dst) = hi2;
+            *reinterpret_cast<uint32_t*>(dst + q_plane) = lo2;
+          }
+        } else {
+          put4<Q4, true>(img + km_off(lr % N, 4 * lane & ~7, N) + 8 * (lane & 1), q_plane, y[i], lane);
         }
         if (Q4) {
-          float s = (y[0] + y[1]) + (y[2] + y[3]);
+          float s = (y[i][0] + y[i][1]) + (y[i][2] + y[i][3]);
           s += __shfl_xor_sync(FULL, s, 1);
           s += __shfl_xor_sync(FULL, s, 2);
           s += __shfl_xor_sync(FULL, s, 4);
@@ -400,11 +409,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       }
     }
     if (SUM) {
-#pragma unroll 1
-      for (int lr = warp; lr < NR; lr += WARPS) {
-        const float v = lr < p.rows ? normaliser(p, u, lr, first, nq, tiles, G, total, lane) : INFINITY;
-        if (lane == 0) lse[lr] = v;
-      }
+      for (int lr = tid; lr < NR; lr += WORKERS) lse[lr] = lr < p.rows ? p.norms[(size_t)u * p.rows + lr] : INFINITY;
     } else {
       for (int c = lane; c < NR / 2; c += 32) {
         wm[c] = NO_REF;
@@ -507,6 +512,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       }
       k_done();
     };
+    float rm[4] = {NO_REF, NO_REF, NO_REF, NO_REF}, rl[4] = {};  // FEW: the warp's references, the thread's sums
     put(it0);
     for (int it = it0; it < it1; ++it) {
       const int j = (raw ? qend - nq * TILE : 0) + it * TILE + ln.t;  // this thread's position
@@ -535,9 +541,9 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         wait_nth(&qk_bar[sb], job >> 1);
         fence_after();
 #pragma unroll 1
-        for (int c = col0; c < col0 + N / 2 && rb * N + c < p.rows; c += CH) {
+        for (int c = col0; c < col0 + (FEW ? (warp < 4 ? 4 : 0) : N / 2) && rb * N + c < p.rows; c += CH) {
           const int row = rb * N + c;
-          // ---- four rows' logits
+          // ---- CH rows' logits
           float s[CH], part[ACC][CH];
 #pragma unroll
           for (int i = 0; i < ACC; ++i)
@@ -561,10 +567,14 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
             if (row + i < cut) s[i] = -INFINITY;
           }
           if (SUM) {
-            const float4 n4 = *reinterpret_cast<const float4*>(lse + row);
-            const float nm[CH] = {n4.x, n4.y, n4.z, n4.w};
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < CH; ++i) acc += ex2(s[i] - nm[i]);
+            for (int i = 0; i < CH; i += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(lse + row + i);
+              sum[0] += ex2(s[i] - m.x) + ex2(s[i + 1] - m.y);
+              sum[1] += ex2(s[i + 2] - m.z) + ex2(s[i + 3] - m.w);
+            }
+            acc += sum[0] + sum[1];
             continue;
           }
           if (p.logits != nullptr && mine) {
@@ -573,8 +583,17 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
               if (row + i < p.rows) p.logits[((size_t)u * p.rows + row + i) * p.s_pad + j] = s[i];
           }
           const int at = rb * (N / 2) + c - col0;
-          float4 m4 = *reinterpret_cast<const float4*>(wm + at);
-          float m[CH] = {m4.x, m4.y, m4.z, m4.w};
+          float m[CH];
+          if constexpr (FEW) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) m[i] = rm[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < CH; i += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(wm + at + i);
+              m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
+            }
+          }
           bool over = false;
 #pragma unroll
           for (int i = 0; i < CH; ++i) over |= s[i] > m[i] + 60.f;
@@ -585,29 +604,50 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
               const int top = __reduce_max_sync(FULL, v ^ ((v >> 31) & 0x7fffffff));
               const float ft = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
               if (ft > m[i] + 60.f) {
-                if (lane == 0) wl[at + i] *= ex2(m[i] - ft);
+                if constexpr (FEW) rl[i] *= ex2(m[i] - ft);
+                else if (lane == 0) wl[at + i] *= ex2(m[i] - ft);
                 m[i] = ft;
               }
             }
-            __syncwarp();
-            if (lane == 0) *reinterpret_cast<float4*>(wm + at) = make_float4(m[0], m[1], m[2], m[3]);
-            __syncwarp();
+            if constexpr (FEW) {
+#pragma unroll
+              for (int i = 0; i < CH; ++i) rm[i] = m[i];
+            } else {
+              __syncwarp();
+              if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) wm[at + i] = m[i];
+              }
+              __syncwarp();
+            }
           }
           float e[CH];
 #pragma unroll
           for (int i = 0; i < CH; ++i) e[i] = ex2(s[i] - m[i]);
-          // sums over the lanes: rows 2 (lane >> 4) + (lane >> 3 & 1) end in the lanes
-          const bool up = lane & 16, up2 = lane & 8;
-          float f0 = up ? e[2] : e[0], f1 = up ? e[3] : e[1];
-          f0 += __shfl_xor_sync(FULL, up ? e[0] : e[2], 16);
-          f1 += __shfl_xor_sync(FULL, up ? e[1] : e[3], 16);
-          float g0 = up2 ? f1 : f0;
-          g0 += __shfl_xor_sync(FULL, up2 ? f0 : f1, 8);
-          g0 += __shfl_xor_sync(FULL, g0, 4);
-          g0 += __shfl_xor_sync(FULL, g0, 2);
-          g0 += __shfl_xor_sync(FULL, g0, 1);
-          if ((lane & 7) == 0) wl[at + 2 * (lane >> 4) + ((lane >> 3) & 1)] += g0;
-          __syncwarp();
+          if constexpr (FEW) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) rl[i] += e[i];
+          } else {
+            // sums over the lanes, halving the rows a lane holds: row lane >> 2 ends in the lanes
+            const bool u16 = lane & 16, u8 = lane & 8, u4 = lane & 4;
+            float f[4], g[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[i] = u16 ? e[4 + i] : e[i];
+              f[i] += __shfl_xor_sync(FULL, u16 ? e[i] : e[4 + i], 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              g[i] = u8 ? f[2 + i] : f[i];
+              g[i] += __shfl_xor_sync(FULL, u8 ? f[i] : f[2 + i], 8);
+            }
+            float v = u4 ? g[1] : g[0];
+            v += __shfl_xor_sync(FULL, u4 ? g[0] : g[1], 4);
+            v += __shfl_xor_sync(FULL, v, 2);
+            v += __shfl_xor_sync(FULL, v, 1);
+            if ((lane & 3) == 0) wl[at + (lane >> 2)] += v;
+            __syncwarp();
+          }
         }
         fence_before();
         __syncwarp();
@@ -624,6 +664,18 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
           *w = p.decay != 0.f ? fmaf(p.decay, *w, v) : v;
         }
         part_sync(1, WORKERS);
+      }
+    }
+    if (FEW && !SUM && warp < 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v = rl[i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+        if (lane == 0) {
+          wm[i] = rm[i];
+          wl[i] = v;
+        }
       }
     }
     part_sync(1, WORKERS);
@@ -667,6 +719,27 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     fence_after();
     tm_free(tmem, TM_COLS);
   }
+}
+
+// the rows' normalisers, a warp each
+static __global__ void __launch_bounds__(ADD_THREADS) normaliser_kernel(const __grid_constant__ Plan p) {
+  extern __shared__ int pre[];
+  const MultiArgs& a = p.a;
+  int* lens = pre + a.batch + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == 0) tile_prefix(a, lens, pre, false, [&](int L) { return seq_tiles(L, a.W); });
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long i = (long long)blockIdx.x * (ADD_THREADS / 32) + warp;
+  if (i >= (long long)p.n_units * p.rows) return;
+  const int u = (int)(i / p.rows), row = (int)(i % p.rows), h = u % a.Hkv, b = (u / a.Hkv) % a.batch, ll = u / (a.Hkv * a.batch);
+  const int L = lens[b], tiles = pre[b + 1] - pre[b];
+  if (L <= 0) return;
+  const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
+  const float v = normaliser(p, u, row, ll * per_layer + (long long)pre[b] * a.Hkv + (long long)h * tiles, quant_tiles(L, a.W), tiles,
+                             min((long long)p.G, total), total, lane);
+  if (lane == 0) p.norms[i] = v;
 }
 
 // weights from stored logits: one CTA per 1024 positions of a unit
@@ -729,15 +802,22 @@ size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
   const size_t parts = align256((size_t)(2 * p->n_units + p->G) * p->rows * 2 * sizeof(float));
   p->parts = reinterpret_cast<float*>(a.scratch);
   p->logits = store && a.scratch ? reinterpret_cast<float*>(a.scratch + parts) : nullptr;
-  return parts + (store ? (size_t)p->n_units * p->rows * p->s_pad * sizeof(float) : 0);
+  p->norms = !store && a.scratch ? reinterpret_cast<float*>(a.scratch + parts) : nullptr;
+  return parts + (size_t)p->n_units * p->rows * (store ? p->s_pad : 1) * sizeof(float);
 }
 
 template <int KF>
 cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
   const size_t pre = (size_t)(2 * p.a.batch + 1) * 4, smem = Smem<KF>::pre(p.nb * N) + pre;
-  cudaError_t e = go<weights_kernel<KF, false>>(dim3((unsigned)p.G), THREADS, smem, false, s, p);
+  const dim3 grid((unsigned)p.G);
+  cudaError_t e = p.rows <= 4 ? go<weights_kernel<KF, false, 4>>(grid, THREADS, smem, false, s, p)
+                              : go<weights_kernel<KF, false, 8>>(grid, THREADS, smem, false, s, p);
   if (e != cudaSuccess) return e;
-  if (p.logits == nullptr) return go<weights_kernel<KF, true>>(dim3((unsigned)p.G), THREADS, smem, true, s, p);
+  if (p.logits == nullptr) {
+    const long long rows = (long long)p.n_units * p.rows;
+    e = go<normaliser_kernel>(dim3((unsigned)((rows + ADD_THREADS / 32 - 1) / (ADD_THREADS / 32))), ADD_THREADS, pre, true, s, p);
+    return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8>>(grid, THREADS, smem, true, s, p);
+  }
   const unsigned y = p.n_units < 32768 ? p.n_units : 32768;
   return go<weights_add_kernel>(dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768),
                                 ADD_THREADS, pre, true, s, p);
