@@ -91,15 +91,17 @@ __device__ __forceinline__ void put4(uint8_t* dst, uint32_t plane, const float (
 }
 
 // ------------------------------------------------------------------ a tile's records
-// A thread's part of a tile: keys of position t = tid & 127 (half hf of its record), values of the position pair vp and
-// rows 2 vr, 2 vr + 1.
+// A thread's part of a tile, of P threads to a position (2 or 4): keys of position t = tid & 127 (part hf of its record),
+// values of the position pair vp, rows 2 vr and 2 vr + 1, all groups of 32 channels (P = 2) or groups 2 vg and 2 vg + 1.
 struct Lane {
-  int t, hf, vp, vr;
+  int t, hf, vp, vr, vg;
 };
+template <int P = 2>
 __device__ __forceinline__ Lane lane_of(int tid) {
   // values: 8 consecutive lanes write 8 distinct 16-byte slots of their core matrices (the odd rows' lanes take the odd
   // position of the pair first)
-  return {tid & 127, (tid >> 7) & 1, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3};
+  if (P == 4) return {tid & 127, (tid >> 7) & 3, (tid & 3) | ((tid >> 3) & 60), (tid >> 2) & 3, (tid >> 4) & 1};
+  return {tid & 127, (tid >> 7) & 1, (tid & 3) | ((tid >> 2) & 4) | ((tid >> 2) & 56), (tid >> 2) & 3, 0};
 }
 
 // The records of a tile in shared memory: four half-pages' keys (main, metadata), then their values.

@@ -36,7 +36,7 @@ namespace tree {
 using namespace tc;
 using namespace records;
 
-constexpr int MAX_ROWS = 64;  // rows per CTA
+constexpr int MAX_ROWS = 64, WIDE_ROWS = 128;  // rows per CTA of two, of four threads to a position
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
 
@@ -106,43 +106,55 @@ __device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2
   }
 }
 
-// keys of the thread's position to its tensor-memory lane: columns 0..63 (TQ3: centroids), then TQ3's signed weights,
-// then the lo parts
-template <int KF, bool F32>
+// keys of the thread's part of its position to the position's tensor-memory lane: columns 0..63 (TQ3: centroids), then
+// TQ3's signed weights, then the lo parts
+template <int KF, bool F32, int P>
 __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
   using R = Rec<KF>;
   const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
   const int tt = ln.t & 31;
-  if (KF == KVQ_Q4G32) {
-    uint4 k[2];
+  constexpr int CHUNKS = (KF == KVQ_Q8G32 ? 8 : 4) / P;  // 16-byte chunks of the record
+  uint4 k[CHUNKS];
+  if (KF == KVQ_Q8G32) {
+    // in the order of the record: 16-byte chunk m = 2 i + h, its word w the channels 16 (4 h + w) + 2 i + {0, 1, 8, 9};
+    // chunk m lies at m ^ (t & 1)
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) k[c] = *reinterpret_cast<const uint4*>(hb + tt * 128 + 16 * (CHUNKS * ln.hf + (c ^ (tt & 1))));
+  } else if constexpr (CHUNKS == 2) {
     lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+  } else {
+    k[0] = *reinterpret_cast<const uint4*>(hb + tt * 64 + 16 * ln.hf);
+  }
+  if (KF == KVQ_Q4G32) {
     const uint4 km = *reinterpret_cast<const uint4*>(hb + R::K_MAIN + tt * 16);
     const uint32_t sc[2] = {km.x, km.y}, zr[2] = {km.z, km.w};
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
       const uint32_t s2 = G & 1 ? dup_hi(sc[G >> 1]) : dup_lo(sc[G >> 1]), z2 = G & 1 ? dup_hi(zr[G >> 1]) : dup_lo(zr[G >> 1]);
-      uint4 o[2], l[2];
+      uint4 o[CHUNKS], l[CHUNKS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) dequant8<F32>(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, s2, z2, o[i], l[i]);
-      tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
-      if (F32) tm_st8(col + 64 + 16 * G + 8 * ln.hf, l[0], l[1]);
+      for (int i = 0; i < CHUNKS; ++i) dequant8<F32>(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, s2, z2, o[i], l[i]);
+      const uint32_t at = col + 16 * G + 4 * CHUNKS * ln.hf;
+      if constexpr (CHUNKS == 2) {
+        tm_st8(at, o[0], o[1]);
+        if (F32) tm_st8(at + 64, l[0], l[1]);
+      } else {
+        tm_st4(at, o[0]);
+      }
     }
   } else if (KF == KVQ_Q8G32) {
-    // in the order of the record: 16-byte chunk m = 2 i + h, its word w the channels 16 (4 h + w) + 2 i + {0, 1, 8, 9};
-    // chunk m lies at m ^ (t & 1)
     const __half2 off = u2h(0x64806480u);  // 1024 + 128
     const uint2 sc = *reinterpret_cast<const uint2*>(hb + R::K_MAIN + tt * 8);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 q = *reinterpret_cast<const uint4*>(hb + tt * 128 + 64 * ln.hf + 16 * (c ^ (tt & 1)));
-      const uint32_t wd[4] = {q.x, q.y, q.z, q.w}, s = c & 1 ? sc.y : sc.x;
+    for (int c = 0; c < CHUNKS; ++c) {
+      const uint32_t wd[4] = {k[c].x, k[c].y, k[c].z, k[c].w}, s = c & 1 ? sc.y : sc.x;
       uint32_t o[8], l[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t s2 = i & 2 ? dup_hi(s) : dup_lo(s);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const __half2 v = __hsub2(u2h(__byte_perm(wd[i], 0x64646464u, x ? 0x4342 : 0x4140)), off);
+          const __half2 v = __hsub2(u2h(prmt(wd[i], 0x64646464u, x ? 0x4342 : 0x4140)), off);
           if (F32) {
             const float d = __low2float(u2h(s2));
             const float2 f = __half22float2(v);
@@ -152,20 +164,18 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
           }
         }
       }
-      const uint32_t at = col + 32 * ln.hf + 8 * c;
+      const uint32_t at = col + 8 * (CHUNKS * ln.hf + c);
       tm_st8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
       if (F32) tm_st8(at + 64, make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]));
     }
   } else {
-    uint4 k[2];
-    lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
     const float wf = QJL_CONST * __half2float(reinterpret_cast<const __half*>(hb + R::K_MAIN)[HALF + tt]);
     uint32_t wh, wl;
     split2(wf, wf, wh, wl);
     wh ^= 0x80008000u;  // -w
     wl ^= 0x80008000u;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < 4 * CHUNKS; i += 2) {
       uint4 o[2], s[2], l[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -182,36 +192,45 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
         const uint32_t lo = word << 1;
         uint32_t m[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t pick = (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12);
-          m[j] = prmt(lo, word, pick) & 0x80008000u;
-        }
+        for (int j = 0; j < 4; ++j) m[j] = prmt(lo, word, (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12)) & 0x80008000u;
         s[x] = make_uint4(wh ^ m[0], wh ^ m[1], wh ^ m[2], wh ^ m[3]);
         if (F32) l[x] = make_uint4(wl ^ m[0], wl ^ m[1], wl ^ m[2], wl ^ m[3]);
       }
-      tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
-      tm_st8(col + 64 + 32 * ln.hf + 4 * i, s[0], s[1]);
-      if (F32) tm_st8(col + 128 + 32 * ln.hf + 4 * i, l[0], l[1]);
+      const uint32_t at = col + 16 * CHUNKS * ln.hf + 4 * i;
+      tm_st8(at, o[0], o[1]);
+      tm_st8(at + 64, s[0], s[1]);
+      if (F32) tm_st8(at + 128, l[0], l[1]);
     }
   }
 }
 
-// values of the thread's two positions, eight channels of each group; positions from `left` on (of the pair) are zero
-template <int KF, bool F32>
+// values of the thread's two positions, eight channels of each of its groups; positions from `left` on (of the pair) are
+// zero
+template <int KF, bool F32, int P>
 __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t* rec, int left) {
   using R = Rec<KF>;
   constexpr uint32_t PLANE = Cfg<KF, F32>::PLANE;
+  constexpr int GROUPS = 8 / P;
   const uint8_t* hb = rec + R::V0 + (ln.vp >> 4) * R::VH;
   const int pp = ln.vp & 15;
   const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;  // (records there may hold anything)
-  uint4 v[2];  // rows 2 vr and 2 vr + 1 stay neighbours in the rotated order of a pair's rows
-  lds32(hb + 128 * pp + 32 * ((ln.vr + pp) & 3), ln.vr & 1, v[0], v[1]);
-  const uint32_t* meta = reinterpret_cast<const uint32_t*>(hb + R::V_MAIN) + pp;
-  uint8_t* base = vb + mm_off(8 * ln.vr, 2 * ln.vp);
+  // rows 2 vr and 2 vr + 1 stay neighbours in the rotated order of a pair's rows
+  const uint8_t* at = hb + 128 * pp + 32 * ((ln.vr + pp) & 3);
+  uint32_t w0[GROUPS], w1[GROUPS];
+  if constexpr (GROUPS == 4) {
+    uint4 a, b;
+    lds32(at, ln.vr & 1, a, b);
+    w0[0] = a.x, w0[1] = a.y, w0[2] = a.z, w0[3] = a.w;
+    w1[0] = b.x, w1[1] = b.y, w1[2] = b.z, w1[3] = b.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(at + 8 * ln.vg), b = *reinterpret_cast<const uint2*>(at + 16 + 8 * ln.vg);
+    w0[0] = a.x, w0[1] = a.y;
+    w1[0] = b.x, w1[1] = b.y;
+  }
+  const uint32_t* meta = reinterpret_cast<const uint32_t*>(hb + R::V_MAIN) + 32 * ln.vg + pp;
+  uint8_t* base = vb + mm_off(64 * ln.vg + 8 * ln.vr, 2 * ln.vp);
 #pragma unroll
-  for (int G = 0; G < 4; ++G) {
-    const uint32_t w0 = G == 0 ? v[0].x : G == 1 ? v[0].y : G == 2 ? v[0].z : v[0].w;
-    const uint32_t w1 = G == 0 ? v[1].x : G == 1 ? v[1].y : G == 2 ? v[1].z : v[1].w;
+  for (int G = 0; G < GROUPS; ++G) {
     const uint32_t vs = meta[16 * G] & keep, vz = meta[64 + 16 * G] & keep;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -219,7 +238,7 @@ __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t
       const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
       uint8_t* dst = base + (e ? 16 : 0) + 512 * G;
       uint4 o, l;
-      dequant8<F32>(prmt(w0, w1, pick), prmt(vs, vs, dup), prmt(vz, vz, dup), o, l);
+      dequant8<F32>(prmt(w0[G], w1[G], pick), prmt(vs, vs, dup), prmt(vz, vz, dup), o, l);
       *reinterpret_cast<uint4*>(dst) = o;
       if (F32) *reinterpret_cast<uint4*>(dst + PLANE) = l;
     }
@@ -237,11 +256,14 @@ struct Smem {
   static __host__ __device__ constexpr uint32_t total(int N) { return R(N) + Rec<KF>::BYTES; }
 };
 
-template <int KF, int NC, bool F32>
-__global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid_constant__ Plan p) {
+// P threads to a position: 2 (two CTAs an SM), or 4 for more than MAX_ROWS rows, which then share the dequantised keys and
+// values (one CTA an SM)
+template <int KF, int NC, bool F32, int P>
+__global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF, F32>;
   using SM = Smem<KF, F32>;
-  constexpr int N = 2 * NC;  // rows, NC of them to a thread, CH at a time
+  constexpr int WORKERS = 128 * P, WARPS = WORKERS / 32;  // and the warp that issues the products
+  constexpr int N = P * NC;  // rows, NC of them to a thread, CH at a time
   constexpr int CH = 8;
   constexpr bool TQ = C::TQ;
   // tensor memory: K | S | O
@@ -259,7 +281,8 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   __shared__ float wmax[4][N];
   __shared__ unsigned long long nodes[KVQ_MAX_TREE];  // ancestors-or-self of each node (0: not there)
   // columns (rows of the unit) that are there and at depth at most i; that have node i among their ancestors-or-self
-  __shared__ unsigned long long shallow[KVQ_MAX_TREE], below[KVQ_MAX_TREE];
+  // (by the threads' groups of columns)
+  __shared__ uint32_t shallow[P][KVQ_MAX_TREE], below[P][KVQ_MAX_TREE];
   __shared__ int par[KVQ_MAX_TREE];
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -292,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
   long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
   const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
 
-  const Lane ln = lane_of(tid);
+  const Lane ln = lane_of<P>(tid);
   const size_t page_stride = (size_t)a.Hkv * a.L.page_bytes;
   const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
   uint4 cent = make_uint4(0u, 0u, 0u, 0u);
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
     __syncwarp();
     if (lane == 0) bar_arrive(&k_bar);
   };
-  const int col0 = (warp >> 2) * NC;                                      // this thread's columns (rows of the unit)
+  const int grp = (warp >> 2) % P, col0 = grp * NC;                                      // this thread's columns (rows of the unit)
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // its lane: position ln.t, channel ln.t
   bool ok = true;
 
@@ -506,21 +529,18 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         nodes[tid] = m;
       }
       part_sync(1, WORKERS);
-      unsigned long long anc[2];
-      int depth[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = lane + 32 * i, row = rbi * N + c;
-        anc[i] = c < N && row < rows ? nodes[row / a.g] : 0ull;
-        depth[i] = anc[i] ? __popcll(anc[i]) - 1 : KVQ_MAX_TREE;
-      }
+      for (int i = 0; i < P; ++i) {
+        const int row = rbi * N + i * NC + lane;
+        const unsigned long long anc = lane < NC && row < rows ? nodes[row / a.g] : 0ull;
+        const int depth = anc ? __popcll(anc) - 1 : KVQ_MAX_TREE;
 #pragma unroll 1
-      for (int x = warp; x < KVQ_MAX_TREE; x += WARPS) {
-        const uint32_t s0 = __ballot_sync(FULL, depth[0] <= x), s1 = __ballot_sync(FULL, depth[1] <= x);
-        const uint32_t b0 = __ballot_sync(FULL, (anc[0] >> x) & 1), b1 = __ballot_sync(FULL, (anc[1] >> x) & 1);
-        if (lane == 0) {
-          shallow[x] = s0 | (unsigned long long)s1 << 32;
-          below[x] = b0 | (unsigned long long)b1 << 32;
+        for (int x = warp; x < KVQ_MAX_TREE; x += WARPS) {
+          const uint32_t s = __ballot_sync(FULL, depth <= x), d = __ballot_sync(FULL, (anc >> x) & 1);
+          if (lane == 0) {
+            shallow[i][x] = s;
+            below[i][x] = d;
+          }
         }
       }
     }
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       // S q~ of every row by the tensor cores: the projection as an operand in the values' place
       const int i = tid & 127;
 #pragma unroll 1
-      for (int kg = tid >> 7; kg < D / 8; kg += 2) {
+      for (int kg = tid >> 7; kg < D / 8; kg += P) {
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = __ldg(a.p.qjl_t + (8 * kg + e) * D + i);
@@ -611,16 +631,17 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
         if (!valid && it * TILE + (ln.t & 64) < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
         page = page_of(it + 1, ln.t & 64);
         wait(&kr_bar, kr_phase);
-        put_k<KF, F32>(lane_addr, ln, rec_sh, cent);
+        put_k<KF, F32, P>(lane_addr, ln, rec_sh, cent);
         if (TQ) nn = __half2float(reinterpret_cast<const __half*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN)[ln.t & 31]);
       } else {
         const void* row = raw_row(0);
 #pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16 / P; ++i) {
+          const int kg = 16 / P * ln.hf + i;
           uint4 o, l;
-          raw_group(row, 8 * ln.hf + i, true, o, l);
-          tm_st4(lane_addr + 32 * ln.hf + 4 * i, o);
-          if (F32) tm_st4(lane_addr + C::KD / 2 + 32 * ln.hf + 4 * i, l);
+          raw_group(row, kg, true, o, l);
+          tm_st4(lane_addr + 4 * kg, o);
+          if (F32) tm_st4(lane_addr + C::KD / 2 + 4 * kg, l);
         }
       }
       k_done();
@@ -628,13 +649,13 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       wait_pv();
       if (!raw) {
         wait(&vr_bar, vr_phase);
-        put_v<KF, F32>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
+        put_v<KF, F32, P>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
         vpage = page_of(it + 1, ln.vp & 32);
       } else {
         const void* row = raw_row(1);
 #pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int kg = 8 * ln.hf + i;
+        for (int i = 0; i < 16 / P; ++i) {
+          const int kg = 16 / P * ln.hf + i;
           uint4 o, l;
           raw_group(row, kg, false, o, l);
           *reinterpret_cast<uint4*>(smem + SM::V + mm_off(8 * kg, ln.t)) = o;
@@ -648,16 +669,15 @@ __global__ void __launch_bounds__(THREADS, F32 ? 1 : 2) tree_kernel(const __grid
       uint32_t bits = 0xffffffffu;
       if (raw || (it + 1) * TILE > full_end || !valid) {
         const int j = raw ? L - nring + x : it * TILE + ln.t, d = j - L + a.W - 1;  // the deepest node that reads j raw
-        unsigned long long on = 0ull;
+        bits = 0u;
         if (!raw) {
-          if (valid && j < full_end) on = ~0ull;
-          else if (valid && j < L) on = shallow[KVQ_MAX_TREE - 1] & ~(a.W > 0 ? shallow[min(d, KVQ_MAX_TREE - 1)] : 0ull);
+          if (valid && j < full_end) bits = 0xffffffffu;
+          else if (valid && j < L) bits = shallow[grp][KVQ_MAX_TREE - 1] & ~(a.W > 0 ? shallow[grp][min(d, KVQ_MAX_TREE - 1)] : 0u);
         } else if (x < nring) {
-          on = d >= 0 ? shallow[min(d, KVQ_MAX_TREE - 1)] : 0ull;
+          bits = d >= 0 ? shallow[grp][min(d, KVQ_MAX_TREE - 1)] : 0u;
         } else if (x < nraw) {
-          on = below[x - nring];
+          bits = below[grp][x - nring];
         }
-        bits = (uint32_t)(on >> col0);
       }
       constexpr uint32_t ALL = NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1;
       const bool all = __all_sync(FULL, (bits & ALL) == ALL);
@@ -931,10 +951,14 @@ template <int KF, bool F32>
 size_t make_plan(const MultiArgs& a, int sms, Plan* p) {
   const int rows = a.n * a.g;
   p->a = a;
-  p->rb = (rows + MAX_ROWS - 1) / MAX_ROWS;
-  p->N = ((rows + p->rb - 1) / p->rb + 15) / 16 * 16;
+  // up to 64 rows: one block, two CTAs an SM (at most 101 KB of shared memory and 256 tensor-memory columns each); more:
+  // blocks of up to 128, one CTA an SM (128 rows over 8 x 32K TQ3: see the measurements below); float caches always in 64s
+  const bool wide = !F32 && rows > MAX_ROWS;
+  const int most = wide ? WIDE_ROWS : MAX_ROWS, step = wide ? 32 : 16;
+  p->rb = (rows + most - 1) / most;
+  p->N = ((rows + p->rb - 1) / p->rb + step - 1) / step * step;
   p->n_units = a.n_layers_call * a.batch * a.Hkv * p->rb;
-  p->G = sms * (F32 ? 1 : 2);  // two CTAs an SM (at most 80 KB of shared memory and 256 tensor-memory columns each)
+  p->G = sms * (F32 || wide ? 1 : 2);
   p->records = reinterpret_cast<float*>(a.scratch);
   return (size_t)(2 * p->n_units + p->G) * (2 * p->N + D * p->N) * 4;
 }
@@ -946,10 +970,16 @@ cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
   const long long out_rows = (long long)(p.n_units / p.rb) * a.n * a.g;
   if (out_rows > 0x7fffffffLL) return cudaErrorInvalidValue;
   const size_t pre = (size_t)(2 * a.batch + 1) * 4, smem = Smem<KF, F32>::total(p.N) + pre;
-  const cudaError_t e = p.N == 16   ? go<tree_kernel<KF, 8, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
-                        : p.N == 32 ? go<tree_kernel<KF, 16, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
-                        : p.N == 48 ? go<tree_kernel<KF, 24, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p)
-                                    : go<tree_kernel<KF, 32, F32>>(dim3((unsigned)p.G), THREADS, smem, false, s, p);
+  const dim3 grid((unsigned)p.G);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (p.N == 16) e = go<tree_kernel<KF, 8, F32, 2>>(grid, 288, smem, false, s, p);
+  if (p.N == 32) e = go<tree_kernel<KF, 16, F32, 2>>(grid, 288, smem, false, s, p);
+  if (p.N == 48) e = go<tree_kernel<KF, 24, F32, 2>>(grid, 288, smem, false, s, p);
+  if (p.N == 64 && (F32 || a.n * a.g <= MAX_ROWS)) e = go<tree_kernel<KF, 32, F32, 2>>(grid, 288, smem, false, s, p);
+  if constexpr (!F32) {
+    if (p.N == 96) e = go<tree_kernel<KF, 24, F32, 4>>(grid, 544, smem, false, s, p);
+    if (p.N == 128) e = go<tree_kernel<KF, 32, F32, 4>>(grid, 544, smem, false, s, p);
+  }
   if (e != cudaSuccess) return e;
   // many records a row (few units over all CTAs): a CTA per row, else a warp per row
   if (p.G > 8 * p.n_units) return go<tree_merge_kernel<true>>(dim3((unsigned)out_rows), MERGE_WARPS * 32, pre, true, s, p);

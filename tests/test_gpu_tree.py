@@ -80,6 +80,19 @@ def test_lengths_around_tiles_and_pages(L):
     _check(gpu, ora, k, v, q, np.array([L]), ref.random_tree(rng, 9)[None], "bf16")
 
 
+@pytest.mark.parametrize("k_format", ["q4g32", "q8g32", "tq3_qjl"])
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("g,N", [(1, 64), (3, 22), (3, 32), (2, 50), (4, 33), (3, 64)])
+def test_row_counts_around_the_blocks(k_format, in_dtype, g, N):
+    """64, 66, 96, 100, 132 and 192 rows a KV head: one block or two, full or not."""
+    rng = np.random.default_rng(100 * g + N)
+    gpu, ora, _ = harness.make_pair(1, 1, g, 2, 460, window=40, k_format=k_format, in_dtype=in_dtype)
+    lens = np.array([450, 333])
+    _fill(gpu, ora, lens, 450, rng, in_dtype)
+    k, v, q = _drafts(rng, gpu.cfg, 2, N, in_dtype)
+    _check(gpu, ora, k, v, q, lens, np.stack([ref.random_tree(rng, N) for _ in range(2)]), in_dtype)
+
+
 def test_chain_equals_single_token_steps():
     """A chain of drafts over a window that covers it: exactly what append + decode of each token computes."""
     rng = np.random.default_rng(5)
