@@ -245,6 +245,17 @@ __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t
   }
 }
 
+// the sums of 2 N columns with lane ^ BIT's: each keeps the N of its half
+template <int N, int BIT>
+__device__ __forceinline__ void halve(float* l, int lane) {
+  const bool up = lane & BIT;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float mine = up ? l[N + c] : l[c], other = up ? l[c] : l[N + c];
+    l[c] = mine + __shfl_xor_sync(FULL, other, BIT);
+  }
+}
+
 // ------------------------------------------------------------------ 1. the tiles
 // dynamic shared memory: V planes | query image | P planes | records | prefix of the sequences' tiles, lengths
 template <int KF, bool F32>
@@ -496,21 +507,37 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
     cp_wait();
     part_sync(1, WORKERS);
     // ---- queries in base-2 units, for records rotated and balanced
-#pragma unroll 1
-    for (int r1 = warp; r1 < N; r1 += WARPS) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (rbi * N + r1 < rows) x = load4_in(smem + SM::V, (size_t)r1 * D + 4 * lane, !F32);
-      float y[4] = {x.x, x.y, x.z, x.w};
-      if (!raw) {
-        y[0] *= sg.x, y[1] *= sg.y, y[2] *= sg.z, y[3] *= sg.w;
-        hadamard_warp(y[0], y[1], y[2], y[3], lane);
-      }
+    {
+      float f[4];  // of this lane's channels
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        y[e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
-        if (a.sinkhorn && !raw) y[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
+        f[e] = raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+        if (a.sinkhorn && !raw) f[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
       }
-      put_q<KF, F32>(smem + SM::Q, r1, N, N * C::KD * 2, y, lane);
+#pragma unroll 1
+      for (int r1 = warp; r1 < N; r1 += 2 * WARPS) {  // two rows at a time
+        float y[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = r1 + i * WARPS;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < N && rbi * N + row < rows) x = load4_in(smem + SM::V, (size_t)row * D + 4 * lane, !F32);
+          y[i][0] = x.x, y[i][1] = x.y, y[i][2] = x.z, y[i][3] = x.w;
+          if (!raw) {
+            y[i][0] *= sg.x, y[i][1] *= sg.y, y[i][2] *= sg.z, y[i][3] *= sg.w;
+          }
+        }
+        if (!raw) {
+          hadamard_warp(y[0][0], y[0][1], y[0][2], y[0][3], lane);
+          hadamard_warp(y[1][0], y[1][1], y[1][2], y[1][3], lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[i][e] *= f[e];
+          if (r1 + i * WARPS < N) put_q<KF, F32>(smem + SM::Q, r1 + i * WARPS, N, N * C::KD * 2, y[i], lane);
+        }
+      }
     }
     if (masked) {
       // ---- the nodes' ancestors, and what they are to this block's columns
@@ -791,12 +818,17 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
     wait_pv();
     fence_after();
     float* rec = p.records + (size_t)(2 * u + raw + blockIdx.x) * (2 * N + D * N);
+    // sums over the lanes; after three exchanges the lanes of one lane & 7 have NC / 8 columns, by its bits in reverse
+    halve<NC / 2, 1>(l, lane);
+    halve<NC / 4, 2>(l, lane);
+    halve<NC / 8, 4>(l, lane);
+    const int lc = ((lane & 1) * 4 + (lane & 2) + ((lane >> 2) & 1)) * (NC / 8);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NC / 8; ++c) {
       float s = l[c];
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-      if (lane == 0) wmax[warp & 3][col0 + c] = s;
+      s += __shfl_xor_sync(FULL, s, 8);
+      s += __shfl_xor_sync(FULL, s, 16);
+      if (lane < 8) wmax[warp & 3][col0 + lc + c] = s;
     }
     const int ch = (ln.t & ~7) + nibble_channel(ln.t & 7);  // tensor-memory lane = place of the channel
 #pragma unroll 1
