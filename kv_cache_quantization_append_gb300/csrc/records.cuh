@@ -11,10 +11,7 @@ namespace records {
 
 using namespace tc;
 
-constexpr int TILE = 128;              // positions per tile = MMA M
-constexpr int WORKERS = 256;           // two threads to a position
-constexpr int WARPS = WORKERS / 32;
-constexpr int THREADS = WORKERS + 32;  // and the warp that issues the products
+constexpr int TILE = 128;  // positions per tile = MMA M
 
 // Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
 // a tile ahead), and belongs to the range that holds its first place.
@@ -134,7 +131,7 @@ cudaError_t go(dim3 grid, unsigned threads, size_t smem, bool dependent, cudaStr
   constexpr int DEVICES = 64;
   static std::atomic<size_t> limit[DEVICES];
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {  // (static shared memory, up to 8 KB of it here, counts towards the 48 KB that need no leave)
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (dev >= DEVICES || limit[dev].load(std::memory_order_relaxed) < smem) {

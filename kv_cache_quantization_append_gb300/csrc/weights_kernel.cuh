@@ -30,15 +30,18 @@ using namespace tc;
 using namespace records;
 
 constexpr float NO_REF = -1e30f;
-constexpr int N = 16;           // rows of a block: the accumulators of two blocks fit beside the keys
 constexpr int STORE_ROWS = 8;
-constexpr int MAX_ROWS = 128, MAX_ROWS_TQ = 64;
+constexpr int MAX_ROWS = 128;   // of a launch
+// Rows of TQ3 keys whose queries (1 KB a row with their projections) leave room for two CTAs an SM.  More take one CTA an
+// SM with four threads to a position (96 rows over 32K: 160 us, in two launches of 64 and 32 rows 268); the other formats
+// have room for two at 128 rows, and one with four threads was no faster (96 rows over 32K Q8: 113 us against 111).
+constexpr int NARROW_ROWS = 64;
 constexpr int ADD_THREADS = 256;
 
 struct Plan {
   MultiArgs a;
   int row0, rows;     // this launch's rows of every unit
-  int nb;             // blocks of N rows
+  int P, nb;          // threads to a position, blocks of N = 8 P rows
   int n_units, G;
   long long s_pad;    // positions a row of stored logits has room for
   float decay;
@@ -77,14 +80,14 @@ struct Smem {
   static __host__ __device__ constexpr uint32_t rec(int rows) { return 2 * plane(rows); }
   static constexpr uint32_t REC = 4 * Rec<KF>::KH;
   // (TQ3: a plane of the projection first takes the records' place)
-  static __host__ __device__ constexpr uint32_t wm(int rows) { return rec(rows) + (C::TQ ? 32768 : C::STAGES * REC); }  // [8][rows / 2]
+  static __host__ __device__ constexpr uint32_t wm(int rows) { return rec(rows) + (C::TQ ? 32768 : C::STAGES * REC); }  // [4 P warps][rows / P]
   static __host__ __device__ constexpr uint32_t wl(int rows) { return wm(rows) + 16 * rows; }
   static __host__ __device__ constexpr uint32_t qs(int rows) { return wl(rows) + 16 * rows; }              // [rows][4]
   static __host__ __device__ constexpr uint32_t pre(int rows) { return qs(rows) + 16 * rows; }
 };
 
 // the codes of the thread's position, exact, to its tensor-memory lane (TQ3: centroids, then signs as +-1)
-template <int KF>
+template <int KF, int P>
 __device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
   using R = Rec<KF>;
   const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
@@ -92,8 +95,9 @@ __device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const ui
   if (KF == KVQ_Q8G32) {
     const __half2 off = u2h(0x64806480u);  // 1024 + 128
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {  // chunk 4 hf + c: i = 2 hf + (c >> 1), h = c & 1
-      const uint4 q = *reinterpret_cast<const uint4*>(hb + tt * 128 + 64 * ln.hf + 16 * (c ^ (tt & 1)));
+    for (int c = 0; c < 8 / P; ++c) {
+      const int m = 8 / P * ln.hf + c;  // chunk 2 i + h
+      const uint4 q = *reinterpret_cast<const uint4*>(hb + tt * 128 + 16 * (m ^ (tt & 1)));
       const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -101,29 +105,32 @@ __device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const ui
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           o[i] = h2u(__hsub2(u2h(prmt(wd[2 * half + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), off));
-        tm_st4(col + 4 * (8 * (c & 1) + 4 * half + 2 * ln.hf + (c >> 1)), make_uint4(o[0], o[1], o[2], o[3]));
+        tm_st4(col + 4 * (8 * (m & 1) + 4 * half + (m >> 1)), make_uint4(o[0], o[1], o[2], o[3]));
       }
     }
     return;
   }
-  uint4 k[2];
-  lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+  constexpr int CHUNKS = 4 / P;  // 16-byte chunks of the record
+  uint4 k[CHUNKS];
+  if constexpr (CHUNKS == 2) lds32(hb + tt * 64 + 32 * ln.hf, tt & 2, k[0], k[1]);
+  else k[0] = *reinterpret_cast<const uint4*>(hb + tt * 64 + 16 * ln.hf);
   if (KF == KVQ_Q4G32) {
 #pragma unroll
     for (int G = 0; G < 4; ++G) {
-      uint4 o[2];
+      uint4 o[CHUNKS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < CHUNKS; ++i) {
         __half2 c[4];
         nibbles(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, c);
         o[i] = make_uint4(h2u(c[0]), h2u(c[1]), h2u(c[2]), h2u(c[3]));
       }
-      tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
+      if constexpr (CHUNKS == 2) tm_st8(col + 16 * G + 8 * ln.hf, o[0], o[1]);
+      else tm_st4(col + 16 * G + 4 * ln.hf, o[0]);
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
+  for (int i = 0; i < 4 * CHUNKS; i += 2) {
     uint4 o[2], s[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -141,8 +148,8 @@ __device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const ui
         m[j] = 0xBC00BC00u ^ (prmt(lo, word, (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12)) & 0x80008000u);
       s[x] = make_uint4(m[0], m[1], m[2], m[3]);
     }
-    tm_st8(col + 32 * ln.hf + 4 * i, o[0], o[1]);
-    tm_st8(col + 64 + 32 * ln.hf + 4 * i, s[0], s[1]);
+    tm_st8(col + 16 * CHUNKS * ln.hf + 4 * i, o[0], o[1]);
+    tm_st8(col + 64 + 16 * CHUNKS * ln.hf + 4 * i, s[0], s[1]);
   }
 }
 
@@ -179,17 +186,19 @@ __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long 
 }
 
 // CH: a thread's rows of a block at a time: 8, or 4 where there are no more (they then keep their sums in registers)
-template <int KF, bool SUM, int CH>
-__global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_constant__ Plan p) {
+template <int KF, bool SUM, int CH, int P>
+__global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF>;
   using SM = Smem<KF>;
   constexpr bool TQ = C::TQ, Q4 = KF == KVQ_Q4G32;
+  constexpr int WORKERS = 128 * P, WARPS = WORKERS / 32;  // and the warp that issues the products
+  constexpr int N = 8 * P;                                // rows of a block: the accumulators of two blocks fit beside the keys
   constexpr int ACC = C::ACC;
   constexpr bool FEW = CH == 4;
   // tensor memory: K (128 columns: two tiles' codes; raw keys' hi and lo; TQ3 centroids and signs) | S, two buffers of ACC
   // accumulators of N columns
-  constexpr uint32_t C_S = 128, TM_COLS = 256;
-  static_assert(C_S + 2 * ACC * N <= TM_COLS, "tensor memory");
+  constexpr uint32_t C_S = 128, TM_COLS = C_S + 2 * ACC * N <= 256 ? 256 : 512;
+  static_assert(C_S + 2 * ACC * N <= TM_COLS && TM_COLS * (4 / P) <= 512, "tensor memory");
   static_assert(!TQ || C::STAGES * SM::REC <= 32768, "the records lie in the projection's place");
   constexpr uint32_t ID_S = idesc(TILE, N, false, false);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
   __shared__ __align__(8) uint64_t kr_bar[C::STAGES], k_bar, s_bar[2], qk_bar[2], proj_bar, end_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ float half_sum[TILE];
+  __shared__ float part_sum[P - 1][TILE];  // of the groups of columns after the first
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, NR = p.nb * N;
   const uint32_t q_plane = SM::plane(NR);
@@ -229,9 +238,8 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
   const long long G = min((long long)p.G, total);
   long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
   const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const Lane ln = lane_of(tid);
+  const Lane ln = lane_of<P>(tid);
   const size_t page_stride = (size_t)a.Hkv * a.L.page_bytes;
   const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
   uint4 cent = make_uint4(0u, 0u, 0u, 0u);
@@ -248,10 +256,10 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     __syncwarp();
     if (lane == 0) bar_arrive(&k_bar);
   };
-  const int col0 = (warp >> 2) * (N / 2);
+  const int col0 = (warp >> 2) * (N / P);
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-  float* wm = reinterpret_cast<float*>(smem + SM::wm(NR)) + warp * (NR / 2);  // this warp's references and sums
-  float* wl = reinterpret_cast<float*>(smem + SM::wl(NR)) + warp * (NR / 2);
+  float* wm = reinterpret_cast<float*>(smem + SM::wm(NR)) + warp * (NR / P);  // this warp's references and sums
+  float* wl = reinterpret_cast<float*>(smem + SM::wl(NR)) + warp * (NR / P);
   float* lse = reinterpret_cast<float*>(smem + SM::wm(NR));                   // SUM: the rows' normalisers
   bool ok = true;
 
@@ -362,30 +370,36 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     };
     int page = page_of(it0);
     // ---- queries in base-2 units as hi and lo images, for records rotated and balanced; sums over groups for the zeros
+    float f[4];  // of this lane's channels
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+      if (a.sinkhorn && !raw) f[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
+    }
+    const auto query = [&](int lr) {
+      const int row = p.row0 + lr;
+      return lr < p.rows ? load4_in(a.q, ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + row / a.g) * D + 4 * lane,
+                                    a.in_bf16)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 next[2] = {query(warp), query(warp + WARPS)};
 #pragma unroll 1
-    for (int r0 = warp; r0 < NR; r0 += 2 * WARPS) {
+    for (int r0 = warp; r0 < NR; r0 += 2 * WARPS) {  // two rows at a time, the next two under way
       float y[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int lr = r0 + i * WARPS, row = p.row0 + lr;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lr < p.rows)
-          q = load4_in(a.q, ((((size_t)ll * a.batch + b) * a.Hkv * a.g + (size_t)h * a.g + row % a.g) * a.n + row / a.g) * D + 4 * lane,
-                       a.in_bf16);
-        y[i][0] = q.x, y[i][1] = q.y, y[i][2] = q.z, y[i][3] = q.w;
+        y[i][0] = next[i].x, y[i][1] = next[i].y, y[i][2] = next[i].z, y[i][3] = next[i].w;
+        next[i] = query(r0 + (2 + i) * WARPS);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int lr = r0 + i * WARPS;  // (NR is a multiple of 16: both rows are there)
+        const int lr = r0 + i * WARPS;  // (NR is a multiple of 2 WARPS: both rows are there)
         if (!raw) {
           y[i][0] *= sg.x, y[i][1] *= sg.y, y[i][2] *= sg.z, y[i][3] *= sg.w;
           hadamard_warp(y[i][0], y[i][1], y[i][2], y[i][3], lane);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[i][e] *= raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
-          if (a.sinkhorn && !raw) y[i][e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
-        }
+        for (int e = 0; e < 4; ++e) y[i][e] *= f[e];
         uint8_t* img = smem + (lr / N) * (N * C::KD * 2);
         if (KF == KVQ_Q8G32) {
 #pragma unroll
@@ -409,9 +423,10 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       }
     }
     if (SUM) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the normalisers (what came before does not need them)
       for (int lr = tid; lr < NR; lr += WORKERS) lse[lr] = lr < p.rows ? p.norms[(size_t)u * p.rows + lr] : INFINITY;
     } else {
-      for (int c = lane; c < NR / 2; c += 32) {
+      for (int c = lane; c < NR / P; c += 32) {
         wm[c] = NO_REF;
         wl[c] = 0.f;
       }
@@ -422,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       for (int part = 0; part < 2; ++part) {
         if (part) wait_nth(&proj_bar, proj_n);
 #pragma unroll 1
-        for (int kg = tid >> 7; kg < D / 8; kg += 2) {
+        for (int kg = tid >> 7; kg < D / 8; kg += P) {
           float s[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = __ldg(a.p.qjl_t + (8 * kg + e) * D + i);
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       proj_n += 2;
       fence_after();
 #pragma unroll 1
-      for (int c = (warp >> 2) * (NR / 2); c < ((warp >> 2) + 1) * (NR / 2); c += 8) {
+      for (int c = (warp >> 2) * (NR / P); c < ((warp >> 2) + 1) * (NR / P); c += 8) {
         float x[8];
         tm_ld(lane_addr + c, x);
         tm_wait_ld();
@@ -470,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         wait_nth(&kr_bar[stage], kr_n / C::STAGES);
         ++kr_n;
         const uint8_t* rec = smem + SM::rec(NR) + stage * SM::REC;
-        put_codes<KF>(lane_addr + (TQ ? 0 : ((it - it0) & 1) * C::K_COLS), ln, rec, cent);
+        put_codes<KF, P>(lane_addr + (TQ ? 0 : ((it - it0) & 1) * C::K_COLS), ln, rec, cent);
         const uint8_t* m = rec + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN;
         const int tt = ln.t & 31;
         if (TQ) {
@@ -485,8 +500,8 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       } else {
         const float* row = a.p.ringk + ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (j < L ? (unsigned)j % (unsigned)a.W : 0u)) * D;
 #pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-          const int kg = 8 * ln.hf + i;
+        for (int i = 0; i < 16 / P; ++i) {
+          const int kg = 16 / P * ln.hf + i;
           float f[8];
           if (KF == KVQ_Q8G32) {
             const int c = 64 * (kg >> 3) + 32 * ((kg >> 2) & 1) + 2 * (kg & 3);
@@ -533,6 +548,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       if (!TQ && !raw && it + 1 < it1) put(it + 1);
       // rows from this one on attend to the position (token of the row >= j - L + n)
       const int cut = valid ? a.g * max(0, j - L + a.n) - p.row0 : 1 << 30;
+      const bool some_cut = __any_sync(FULL, cut > 0);
       float acc = 0.f;
 #pragma unroll 1
       for (int rb = 0; rb < p.nb; ++rb, ++job) {
@@ -541,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
         wait_nth(&qk_bar[sb], job >> 1);
         fence_after();
 #pragma unroll 1
-        for (int c = col0; c < col0 + (FEW ? (warp < 4 ? 4 : 0) : N / 2) && rb * N + c < p.rows; c += CH) {
+        for (int c = col0; c < col0 + (FEW ? (warp < 4 ? 4 : 0) : N / P) && rb * N + c < p.rows; c += CH) {
           const int row = rb * N + c;
           // ---- CH rows' logits
           float s[CH], part[ACC][CH];
@@ -564,7 +580,11 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
                 s[i] = fmaf(q.x, z0[0], fmaf(q.y, z0[1], fmaf(q.z, z0[2], fmaf(q.w, z0[3], s[i]))));
               }
             }
-            if (row + i < cut) s[i] = -INFINITY;
+          }
+          if (some_cut) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              if (row + i < cut) s[i] = -INFINITY;
           }
           if (SUM) {
             float sum[2] = {0.f, 0.f};
@@ -582,7 +602,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
             for (int i = 0; i < CH; ++i)
               if (row + i < p.rows) p.logits[((size_t)u * p.rows + row + i) * p.s_pad + j] = s[i];
           }
-          const int at = rb * (N / 2) + c - col0;
+          const int at = rb * (N / P) + c - col0;
           float m[CH];
           if constexpr (FEW) {
 #pragma unroll
@@ -594,20 +614,24 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
               m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
             }
           }
-          bool over = false;
+          float e[CH], top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < CH; ++i) over |= s[i] > m[i] + 60.f;
-          if (__any_sync(FULL, over)) {  // (the first tile, hardly ever another)
+          for (int i = 0; i < CH; ++i) {
+            e[i] = s[i] - m[i];
+            top = fmaxf(top, e[i]);
+          }
+          if (__any_sync(FULL, top > 60.f)) {  // (the first tile, hardly ever another)
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
               const int v = __float_as_int(s[i]);
-              const int top = __reduce_max_sync(FULL, v ^ ((v >> 31) & 0x7fffffff));
-              const float ft = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+              const int most = __reduce_max_sync(FULL, v ^ ((v >> 31) & 0x7fffffff));
+              const float ft = __int_as_float(most ^ ((most >> 31) & 0x7fffffff));
               if (ft > m[i] + 60.f) {
                 if constexpr (FEW) rl[i] *= ex2(m[i] - ft);
                 else if (lane == 0) wl[at + i] *= ex2(m[i] - ft);
                 m[i] = ft;
               }
+              e[i] = s[i] - m[i];
             }
             if constexpr (FEW) {
 #pragma unroll
@@ -621,9 +645,8 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
               __syncwarp();
             }
           }
-          float e[CH];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) e[i] = ex2(s[i] - m[i]);
+          for (int i = 0; i < CH; ++i) e[i] = ex2(e[i]);
           if constexpr (FEW) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) rl[i] += e[i];
@@ -655,12 +678,14 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       }
       if ((TQ || raw) && it + 1 < it1) put(it + 1);
       if (SUM) {
-        if (warp >= 4) half_sum[ln.t] = acc;
+        if (warp >= 4) part_sum[(warp >> 2) - 1][ln.t] = acc;
         part_sync(1, WORKERS);
         if (*(volatile int*)&abort_sh) break;  // (raised before the barrier: all workers leave together)
         if (warp < 4 && mine) {
           float* w = a.weights + (size_t)u * a.max_seq_len + j;
-          const float v = acc + half_sum[ln.t];
+          float v = acc;
+#pragma unroll
+          for (int i = 0; i < P - 1; ++i) v += part_sum[i][ln.t];
           *w = p.decay != 0.f ? fmaf(p.decay, *w, v) : v;
         }
         part_sync(1, WORKERS);
@@ -687,14 +712,14 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
       // ---- the range's maxima and sums: the four warps that hold a row's columns, joined in order
       float* out = p.parts + (size_t)(2 * u + raw + blockIdx.x) * p.rows * 2;
       for (int lr = tid; lr < p.rows; lr += WORKERS) {
-        const int c = lr % N, wg = c / (N / 2), at = lr / N * (N / 2) + c % (N / 2);
-        const float* m0 = reinterpret_cast<const float*>(smem + SM::wm(NR)) + 4 * wg * (NR / 2) + at;
-        const float* l0 = reinterpret_cast<const float*>(smem + SM::wl(NR)) + 4 * wg * (NR / 2) + at;
+        const int c = lr % N, wg = c / (N / P), at = lr / N * (N / P) + c % (N / P);
+        const float* m0 = reinterpret_cast<const float*>(smem + SM::wm(NR)) + 4 * wg * (NR / P) + at;
+        const float* l0 = reinterpret_cast<const float*>(smem + SM::wl(NR)) + 4 * wg * (NR / P) + at;
         float m = NO_REF, l = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float mi = m0[i * (NR / 2)], mn = fmaxf(m, mi);
-          l = l * ex2(m - mn) + l0[i * (NR / 2)] * ex2(mi - mn);
+          const float mi = m0[i * (NR / P)], mn = fmaxf(m, mi);
+          l = l * ex2(m - mn) + l0[i * (NR / P)] * ex2(mi - mn);
           m = mn;
         }
         out[2 * lr] = m;
@@ -713,6 +738,7 @@ __global__ void __launch_bounds__(THREADS, 2) weights_kernel(const __grid_consta
     mma_commit(&end_bar);
     land(&end_bar, 0);
   }
+  if (SUM) asm volatile("griddepcontrol.wait;" ::: "memory");  // (a CTA without tiles too: no kernel ends before the one it follows)
   fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -789,13 +815,14 @@ static __global__ void __launch_bounds__(ADD_THREADS) weights_add_kernel(const _
 // rows of one launch, and the plan of the launches that begin at row0; returns the scratch bytes
 template <int KF>
 size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
-  const int all = a.n * a.g, most = KF == KVQ_TQ3_QJL ? MAX_ROWS_TQ : MAX_ROWS;
+  const int all = a.n * a.g;
   p->a = a;
   p->row0 = row0;
-  p->rows = all - row0 < most ? all - row0 : most;
-  p->nb = (p->rows + N - 1) / N;
+  p->rows = all - row0 < MAX_ROWS ? all - row0 : MAX_ROWS;
+  p->P = KF == KVQ_TQ3_QJL && p->rows > NARROW_ROWS ? 4 : 2;
+  p->nb = (p->rows + 8 * p->P - 1) / (8 * p->P);
   p->n_units = a.n_layers_call * a.batch * a.Hkv;
-  p->G = 2 * sms;
+  p->G = sms * (4 / p->P);
   p->s_pad = ((long long)a.max_seq_len + 3) / 4 * 4;
   p->decay = row0 == 0 ? a.decay : 1.f;
   const bool store = all <= STORE_ROWS;
@@ -806,17 +833,30 @@ size_t make_plan(const MultiArgs& a, int sms, int row0, Plan* p) {
   return parts + (size_t)p->n_units * p->rows * (store ? p->s_pad : 1) * sizeof(float);
 }
 
+inline cudaError_t launch_norms(const Plan& p, size_t pre, cudaStream_t s) {
+  const long long rows = (long long)p.n_units * p.rows;
+  return go<normaliser_kernel>(dim3((unsigned)((rows + ADD_THREADS / 32 - 1) / (ADD_THREADS / 32))), ADD_THREADS, pre, true, s, p);
+}
+
 template <int KF>
 cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
-  const size_t pre = (size_t)(2 * p.a.batch + 1) * 4, smem = Smem<KF>::pre(p.nb * N) + pre;
+  const size_t pre = (size_t)(2 * p.a.batch + 1) * 4, smem = Smem<KF>::pre(p.nb * 8 * p.P) + pre;
   const dim3 grid((unsigned)p.G);
-  cudaError_t e = p.rows <= 4 ? go<weights_kernel<KF, false, 4>>(grid, THREADS, smem, false, s, p)
-                              : go<weights_kernel<KF, false, 8>>(grid, THREADS, smem, false, s, p);
+  const unsigned threads = 128 * p.P + 32;
+  cudaError_t e;
+  if constexpr (KF == KVQ_TQ3_QJL) {
+    if (p.P == 4) {
+      e = go<weights_kernel<KF, false, 8, 4>>(grid, threads, smem, false, s, p);
+      if (e == cudaSuccess) e = launch_norms(p, pre, s);
+      return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8, 4>>(grid, threads, smem, true, s, p);
+    }
+  }
+  e = p.rows <= 4 ? go<weights_kernel<KF, false, 4, 2>>(grid, threads, smem, false, s, p)
+                  : go<weights_kernel<KF, false, 8, 2>>(grid, threads, smem, false, s, p);
   if (e != cudaSuccess) return e;
   if (p.logits == nullptr) {
-    const long long rows = (long long)p.n_units * p.rows;
-    e = go<normaliser_kernel>(dim3((unsigned)((rows + ADD_THREADS / 32 - 1) / (ADD_THREADS / 32))), ADD_THREADS, pre, true, s, p);
-    return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8>>(grid, THREADS, smem, true, s, p);
+    e = launch_norms(p, pre, s);
+    return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8, 2>>(grid, threads, smem, true, s, p);
   }
   const unsigned y = p.n_units < 32768 ? p.n_units : 32768;
   return go<weights_add_kernel>(dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768),

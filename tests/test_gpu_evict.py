@@ -1,5 +1,9 @@
 """Attention weights of cached positions and eviction by them, against the 64-bit definitions."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -76,6 +80,40 @@ def test_weights_sinkhorn_paged_all_layers():
     for layer in range(2):
         want = ref.attention_weights(ora, layer, harness.to_np(q[layer]), lens, np.ones((3, 2, 300)), 0.25)
         assert np.abs(w[layer].double().cpu().numpy() - want).max() < 1e-4 * want.max()
+
+
+@pytest.mark.parametrize("k_format", ["q4g32", "q8g32", "tq3_qjl"])
+@pytest.mark.parametrize("g,T", [(3, 6), (3, 22), (2, 64), (3, 43), (4, 40)])
+def test_weights_row_counts_around_the_blocks(k_format, g, T):
+    """18, 66, 128, 129 and 160 rows a KV head: blocks of 16 or 32 rows full or not, one launch or two."""
+    rng = np.random.default_rng(50 * g + T)
+    gpu, ora, _ = harness.make_pair(1, 1, g, 2, 460, window=40, k_format=k_format)
+    lens = np.array([450, 333])
+    _fill(gpu, ora, lens, 450, rng, "bf16")
+    _, _, q = _drafts(rng, gpu.cfg, 2, T, "bf16")
+    _check_weights(gpu, ora, q, lens, 0.5, rng)
+
+
+def test_first_call_of_a_process_may_be_of_any_size():
+    """Shared-memory limits are set per kernel and device: a call's own must not depend on a larger one before it."""
+    code = """
+import torch
+import kv_cache_quantization_append_gb300 as kvq
+for n_q, n in ((24, 8), (8, 1), (16, 4), (32, 8), (32, 32)):
+    c = kvq.QuantKVCache(kvq.make_config(1, 8, n_q, 1, 400))
+    k = torch.randn(1, 8, 300, 128, device="cuda").bfloat16()
+    ln = torch.tensor([300], dtype=torch.int32, device="cuda")
+    c.append(0, k, k, torch.zeros_like(ln))
+    w = torch.zeros(1, 8, 400, device="cuda")
+    q = torch.randn(1, n_q, n, 128, device="cuda").bfloat16()
+    c.attention_weights(0, q, ln, w)
+    assert abs(w.sum().item() / (n_q * n) - 1) < 1e-3, (n_q, n, w.sum().item())
+    c.tree_decode(0, k[:, :, :n].contiguous(), k[:, :, :n].contiguous(), q, ln, torch.arange(-1, n - 1, dtype=torch.int32, device="cuda")[None])
+    torch.cuda.synchronize()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_weights_deterministic_and_captured():
