@@ -2,32 +2,35 @@
 // older ones, those with the largest accumulated attention weight; per (layer, sequence, kv-head), in place.
 //
 // Records move as they are (a token's codes and scales do not depend on its slot, only their place in the
-// half-page does), so nothing is quantised again; kept positions stay in order.  Two launches:
-//  1. select_kernel, one CTA per unit: radix select of the (budget - recent)-th largest weight over the older
-//     positions -- 11, 11 and 10 bits of the weights' order-preserving integer image, counted in shared memory,
-//     where the weights lie meanwhile (up to 48K of them; longer sequences are read again for each step) --
-//     then one ordered pass that lists the kept positions (weight above the threshold, or equal to it and among
-//     the lowest such indices) and compacts the weights.  Counting and ranking are integer sums: the result
-//     does not depend on timing.  Further CTAs turn the window ring meanwhile: its slot is position % window,
-//     and positions shift by the number of tokens cut.
-//  2. move_kernel, a cluster of CTAs per unit: windows of half-pages in ascending order, each gathered into
-//     shared memory by all CTAs of the cluster before any of it is written.  A slot's position is never below the
-//     slot, so a window's sources lie at or behind its own start, where no earlier window has written: one cluster
-//     barrier per window makes the move safe in place, and the next window is gathered while the last is written.
-//     Bound by memory: each kept record is read once and written once.
-#include "kvq_internal.cuh"
+// half-page does), so nothing is quantised again; kept positions stay in order.  One launch, a cluster of eight
+// CTAs per unit:
+//  1. radix select of the (budget - recent)-th largest weight over the older positions -- 11, 11 and 10 bits of
+//     the weights' order-preserving integer image, counted by each CTA over its share (which it keeps in shared
+//     memory where it fits, and reads again for each step where it does not) and added up over the cluster -- then
+//     one ordered pass that lists the kept positions (weight above the threshold, or equal to it and among the
+//     lowest such indices) and compacts the weights.  Counting and ranking are integer sums: the result does not
+//     depend on timing.
+//  2. the move: windows of half-pages in ascending order, each gathered into shared memory by all CTAs of the
+//     cluster before any of it is written.  A slot's position is never below the slot, so a window's sources lie at
+//     or behind its own start, where no earlier window has written: one cluster barrier per window makes the move
+//     safe in place, and the next window is gathered while the last is written.
+//  3. the window ring turns: its slot is position % window, and positions shift by the number of tokens cut.
+// Bound by memory: each kept record is read once and written once.
+#include "records.cuh"
 
 namespace kvq {
 
 namespace {
 
-constexpr int SEL_THREADS = 1024;
-constexpr int SEL_CACHE = 48 * 1024;   // weights that shared memory holds
+using namespace records;
+
 constexpr int BINS = 2048;
-constexpr int MOVE_THREADS = 256;
+constexpr int THREADS = 256;
 constexpr int CLUSTER = 8;
+constexpr int SHARE = 4 * THREADS;  // a CTA's weights of a window of the ordered pass
+constexpr int SEL_WINDOW = CLUSTER * SHARE;
 constexpr int HPW = 4;                 // half-pages of a CTA per window
-static_assert(MOVE_THREADS == 8 * HALF && HPW * HALF <= MOVE_THREADS, "a thread's share of a window");
+static_assert(THREADS == 8 * HALF && HPW * HALF <= THREADS, "a thread's share of a window");
 
 __device__ __forceinline__ int checked_len(const EvictArgs& a, int b, bool flag) {
   const int L = a.seq_lens[b];
@@ -44,8 +47,9 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// exclusive prefix of v over the block (32 warps), and its total
+// exclusive prefix of v over the block, and its total
 __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums, uint32_t& total) {
+  constexpr int WARPS = THREADS / 32;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   uint32_t incl = v;
 #pragma unroll
@@ -55,32 +59,49 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   }
   if (lane == 31) warp_sums[w] = incl;
   __syncthreads();
-  const uint32_t ws = warp_sums[lane];
-  uint32_t wi = ws;
+  uint32_t before = 0;
+  total = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(FULL, wi, o);
-    if (lane >= o) wi += y;
+  for (int i = 0; i < WARPS; ++i) {
+    const uint32_t s = warp_sums[i];
+    before += i < w ? s : 0;
+    total += s;
   }
-  total = __shfl_sync(FULL, wi, 31);
-  const uint32_t before = __shfl_sync(FULL, wi - ws, w);
   __syncthreads();
   return before + incl - v;
 }
 
-// The ring of one unit's keys or values: rows turn by the tokens cut, as many channels at a time as `room` floats hold.
-__device__ void turn_ring(const EvictArgs& a, int unit, int kv, float4* buf, int room) {
-  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.batch, layer = a.layer0 + unit / (a.Hkv * a.batch);
-  const int cut = checked_len(a, b, false) - a.budget, turn = cut > 0 ? cut % a.W : 0;
-  if (turn == 0) return;
-  float4* ring = reinterpret_cast<float4*>((kv ? a.p.ringv : a.p.ringk) +
-                                           (((size_t)layer * a.max_batch + b) * a.Hkv + h) * (size_t)a.W * D);
-  int cols = D / 4;  // float4 columns at a time: a power of two
-  while (cols * a.W * 4 > room) cols >>= 1;
-  for (int c0 = 0; c0 < D / 4; c0 += cols) {
-    for (int i = threadIdx.x; i < cols * a.W; i += SEL_THREADS) buf[i] = ring[(size_t)(i / cols) * (D / 4) + c0 + i % cols];
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of `p` (shared memory) in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int cluster_load(uint32_t at) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// CTA `rank`'s channels of the ring of one unit's keys or values: rows turn by `turn`, as many channels at a time as
+// `room` bytes hold (at least one float4 column: 16 KB at the widest window)
+__device__ void turn_ring(const EvictArgs& a, float* ring_f, int turn, int rank, float4* buf, int room) {
+  constexpr int MINE = D / 4 / CLUSTER;  // float4 columns
+  float4* ring = reinterpret_cast<float4*>(ring_f) + rank * MINE;
+  int cols = MINE;  // at a time: a power of two
+  while (cols * a.W * 16 > room) cols >>= 1;
+  for (int c0 = 0; c0 < MINE; c0 += cols) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < cols * a.W; i += THREADS) buf[i] = ring[(size_t)(i / cols) * (D / 4) + c0 + i % cols];
     __syncthreads();
-    for (int i = threadIdx.x; i < cols * a.W; i += SEL_THREADS) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < cols * a.W; i += THREADS) {
       int s = i / cols + turn;
       if (s >= a.W) s -= a.W;
       ring[(size_t)(i / cols) * (D / 4) + c0 + i % cols] = buf[s * cols + i % cols];
@@ -89,37 +110,29 @@ __device__ void turn_ring(const EvictArgs& a, int unit, int kv, float4* buf, int
   }
 }
 
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const __grid_constant__ EvictArgs a, int room) {
-  extern __shared__ __align__(16) float cache[];  // `room` floats
-  __shared__ int hist[BINS];
-  __shared__ uint32_t warp_sums[32];
-  __shared__ int pick_sh[2];
-  asm volatile("griddepcontrol.launch_dependents;");
+// Lists the kept positions of one unit and compacts its weights, by a cluster.  Of window n CTA `rank` has positions
+// n SEL_WINDOW + rank SHARE .. + SHARE - 1.  area: `room` bytes, the same place in every CTA.
+__device__ void select_kept(const EvictArgs& a, float* w, int32_t* kept, int L, int rank, uint8_t* area, int room) {
+  int* hist = reinterpret_cast<int*>(area);           // this CTA's counts
+  int* sums = hist + BINS;                            // the cluster's
+  float* cache = reinterpret_cast<float*>(sums + BINS);
+  __shared__ uint32_t warp_sums[THREADS / 32];
+  __shared__ int pick_sh[2], counts[2][CLUSTER];
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= a.n_units) {
-    turn_ring(a, (blockIdx.x - a.n_units) >> 1, (blockIdx.x - a.n_units) & 1, reinterpret_cast<float4*>(cache), room);
-    return;
-  }
-  const int unit = blockIdx.x;  // ((ll * batch) + b) * Hkv + h
-  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.batch;
-  const bool first = h == 0 && unit < a.batch * a.Hkv;
-  const int L = checked_len(a, b, first && tid == 0);
-  int32_t* kept = a.kept + (size_t)unit * a.budget;
-  if (first && tid == 0) a.new_lens[b] = min(L, a.budget);
-  if (L <= a.budget) {
-    for (int j = tid; j < a.budget; j += SEL_THREADS) kept[j] = j < L ? j : -1;
-    return;
-  }
-  float* w = a.weights + (size_t)unit * a.max_seq_len;
   const int old = L - a.recent, want = a.budget - a.recent;  // old > want >= 0
-  const bool cached = L <= room;
+  const int windows = (L + SEL_WINDOW - 1) / SEL_WINDOW;
+  const bool cached = windows * SHARE * 4 <= room - 2 * BINS * 4;
+  const auto position = [&](int i) { return i / SHARE * SEL_WINDOW + rank * SHARE + i % SHARE; };  // of this CTA's i-th weight
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  // four weights from position j on (zeros past the end)
+  const auto load4 = [&](int j) {
+    if (wide && j + 4 <= L) return *reinterpret_cast<const float4*>(w + j);
+    return make_float4(j < L ? w[j] : 0.f, j + 1 < L ? w[j + 1] : 0.f, j + 2 < L ? w[j + 2] : 0.f, j + 3 < L ? w[j + 3] : 0.f);
+  };
   if (cached) {
-    const int L4 = (reinterpret_cast<uintptr_t>(w) & 15) == 0 ? L / 4 : 0;
 #pragma unroll 4
-    for (int j = tid; j < L4; j += SEL_THREADS) reinterpret_cast<float4*>(cache)[j] = reinterpret_cast<const float4*>(w)[j];
-    for (int j = 4 * L4 + tid; j < L; j += SEL_THREADS) cache[j] = w[j];
+    for (int n = 0; n < windows; ++n) reinterpret_cast<float4*>(cache)[n * THREADS + tid] = load4(position(n * SHARE + 4 * tid));
   }
-  const float* src = cached ? cache : w;
   // threshold: the want-th largest image, and how many equal to it are kept
   uint32_t thr = 0u, mask = 0u;
   int need = want;
@@ -127,23 +140,49 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const __grid_consta
 #pragma unroll 1
     for (int step = 0; step < 3; ++step) {
       const int shift = step == 0 ? 21 : step == 1 ? 10 : 0, bins = step == 2 ? 1024 : 2048;
-      for (int i = tid; i < BINS; i += SEL_THREADS) hist[i] = 0;
+#pragma unroll
+      for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int j = tid; j < old; j += SEL_THREADS) {
-        const uint32_t u = order_of(src[j]);
-        if ((u & mask) == thr) atomicAdd(&hist[(u >> shift) & (bins - 1)], 1);
+#pragma unroll 2
+      for (int n = 0; n < windows; ++n) {
+        const int j = position(n * SHARE + 4 * tid);
+        const float4 x = cached ? reinterpret_cast<const float4*>(cache)[n * THREADS + tid] : load4(j);
+        const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = order_of(f[i]);
+          if (j + i < old && (u & mask) == thr) atomicAdd(&hist[(u >> shift) & (bins - 1)], 1);
+        }
       }
-      __syncthreads();
-      // digit d with count(> d) < need <= count(>= d), from the top: two bins a thread
-      const int hi = BINS - 1 - 2 * tid;
-      const int c0 = hist[hi], c1 = hist[hi - 1];
+      cluster_sync();
+      {  // an eighth of the bins each, and their sums to everyone
+        constexpr int MINE = BINS / CLUSTER;
+        static_assert(MINE == THREADS, "a bin a thread");
+        const int bin = rank * MINE + tid;
+        int s = 0;
+#pragma unroll
+        for (int r = 0; r < CLUSTER; ++r) s += cluster_load(in_cta(hist + bin, r));
+#pragma unroll
+        for (int r = 0; r < CLUSTER; ++r) cluster_store(in_cta(sums + bin, r), s);
+      }
+      cluster_sync();
+      // digit d with count(> d) < need <= count(>= d), from the top: eight bins a thread
+      constexpr int PER = BINS / THREADS;
+      const int top = BINS - 1 - PER * tid;
+      int c[PER], all = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) all += c[i] = sums[top - i];
       uint32_t total;
-      const int above = (int)block_exclusive((uint32_t)(c0 + c1), warp_sums, total);
-      if (above < need && need <= above + c0 + c1) {
-        const bool second = need > above + c0;
-        pick_sh[0] = second ? hi - 1 : hi;
-        pick_sh[1] = above + (second ? c0 : 0);
+      int above = (int)block_exclusive((uint32_t)all, warp_sums, total);
+      if (above < need && need <= above + all) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (above < need && need <= above + c[i]) {
+            pick_sh[0] = top - i;
+            pick_sh[1] = above;
+          }
+          above += c[i];
+        }
       }
       __syncthreads();
       thr |= (uint32_t)pick_sh[0] << shift;
@@ -151,47 +190,51 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const __grid_consta
       need -= pick_sh[1];
       __syncthreads();
     }
+  } else {
+    cluster_sync();  // (shared memory of a CTA that has not begun is nobody's to write)
   }
-  __syncthreads();
-  // ordered pass, eight consecutive positions a thread.  (Read again from global memory, a chunk's weights are all read
-  // before any is written, and no write passes the chunk's end.)
-  uint32_t n_above = 0, n_equal = 0;  // kept for their weight or age, and equal to the threshold, before the chunk
-  constexpr int PER = 8;
-  for (int j0 = 0; j0 < L; j0 += SEL_THREADS * PER) {
-    float wj[PER];
+  // Ordered pass, four consecutive positions a thread.  A window's weights are all read before any is written, and no
+  // write passes the window's end.
+  int n_above = 0, n_equal = 0;  // kept for their weight or age, and equal to the threshold, before the window
+#pragma unroll 1
+  for (int n = 0; n < windows; ++n) {
+    const int j = position(n * SHARE + 4 * tid);
+    const float4 x = cached ? reinterpret_cast<const float4*>(cache)[n * THREADS + tid] : load4(j);
+    const float f[4] = {x.x, x.y, x.z, x.w};
     uint32_t keep = 0, equal = 0;
-    const int jt = j0 + tid * PER;
-    if (cached && jt + PER <= L) {
-      const float4 x = *reinterpret_cast<const float4*>(cache + jt), y = *reinterpret_cast<const float4*>(cache + jt + 4);
-      wj[0] = x.x, wj[1] = x.y, wj[2] = x.z, wj[3] = x.w, wj[4] = y.x, wj[5] = y.y, wj[6] = y.z, wj[7] = y.w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) wj[i] = jt + i < L ? src[jt + i] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int j = jt + i;
-      const uint32_t u = order_of(wj[i]);
-      const bool cand = want > 0 && j < old;
-      keep |= (uint32_t)((j < L && j >= old) || (cand && u > thr)) << i;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = order_of(f[i]);
+      const bool cand = want > 0 && j + i < old;
+      keep |= (uint32_t)((j + i < L && j + i >= old) || (cand && u > thr)) << i;
       equal |= (uint32_t)(cand && u == thr) << i;
     }
     uint32_t total;
     const uint32_t before = block_exclusive((uint32_t)__popc(keep) | (uint32_t)__popc(equal) << 16, warp_sums, total);
-    uint32_t na = n_above + (before & 0xffffu), ne = n_equal + (before >> 16);
+    if (tid < CLUSTER) cluster_store(in_cta(&counts[n & 1][rank], tid), (int)total);
+    cluster_sync();
+    int na = n_above + (int)(before & 0xffffu), ne = n_equal + (int)(before >> 16);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int r = 0; r < CLUSTER; ++r) {
+      const uint32_t c = (uint32_t)counts[n & 1][r];
+      if (r < rank) {
+        na += (int)(c & 0xffffu);
+        ne += (int)(c >> 16);
+      }
+      n_above += (int)(c & 0xffffu);
+      n_equal += (int)(c >> 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const bool e = (equal >> i) & 1, k = (keep >> i) & 1;
-      if (k || (e && ne < (uint32_t)need)) {
-        const uint32_t at = na + min(ne, (uint32_t)need);
-        kept[at] = j0 + tid * PER + i;
-        w[at] = wj[i];
+      if (k || (e && ne < need)) {
+        const int at = na + min(ne, need);
+        kept[at] = j + i;
+        w[at] = f[i];
       }
       na += k;
       ne += e;
     }
-    n_above += total & 0xffffu;
-    n_equal += total >> 16;
   }
 }
 
@@ -199,19 +242,25 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const __grid_consta
 __device__ __forceinline__ int v_row(int p, int r) { return 128 * p + 16 * ((r + 2 * (p & 3)) & 7); }
 
 template <int KF>
-__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS) evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint8_t images[];  // [2][HPW][half_bytes]
   __shared__ int src_sh[2][HPW * HALF];              // source token (within its half-page) of each slot
   __shared__ const uint8_t* base_sh[2][HPW * HALF];  // the half-page that holds it (null: on a bad page)
-  const int tid = threadIdx.x, rank = blockIdx.x % CLUSTER, unit = blockIdx.x / CLUSTER;
+  const int tid = threadIdx.x, rank = blockIdx.x % CLUSTER, unit = blockIdx.x / CLUSTER;  // ((ll * batch) + b) * Hkv + h
   const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.batch, layer = a.layer0 + unit / (a.Hkv * a.batch);
-  const int L = checked_len(a, b, false);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (L <= a.budget) return;  // (the whole cluster)
+  const bool first = h == 0 && unit < a.batch * a.Hkv && rank == 0 && tid == 0;
+  const int L = checked_len(a, b, first);
+  int32_t* kept = a.kept + (size_t)unit * a.budget;
+  if (first) a.new_lens[b] = min(L, a.budget);
+  if (L <= a.budget) {  // (the whole cluster)
+    for (int j = rank * THREADS + tid; j < a.budget; j += CLUSTER * THREADS) kept[j] = j < L ? j : -1;
+    return;
+  }
+  select_kept(a, a.weights + (size_t)unit * a.max_seq_len, kept, L, rank, images, 2 * HPW * a.L.half_bytes);
+  cluster_sync();  // the list is complete
   const size_t page_stride = (size_t)a.Hkv * a.L.page_bytes;
   uint8_t* pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
   const int32_t* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
-  const int32_t* kept = a.kept + (size_t)unit * a.budget;
   const int hb = a.L.half_bytes, windows = (a.n_halves + CLUSTER * HPW - 1) / (CLUSTER * HPW);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
@@ -239,19 +288,19 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS) 
     const uint8_t* const* base = base_sh[w & 1];
     uint8_t* img0 = images + (size_t)(w & 1) * HPW * hb;
     constexpr int CH = KF == KVQ_Q8G32 ? 8 : 4;                  // 16-byte chunks of a key record
-    constexpr int NK = HPW * HALF * CH / MOVE_THREADS, NV = HPW * HALF * 4 / MOVE_THREADS, NM = HPW * HALF * 8 / MOVE_THREADS;
+    constexpr int NK = HPW * HALF * CH / THREADS, NV = HPW * HALF * 4 / THREADS, NM = HPW * HALF * 8 / THREADS;
     uint4 k[NK], x[NV], y[NV], km = zero;
     uint16_t vm[NM];
 #pragma unroll
     for (int q = 0; q < NK; ++q) {  // keys (Q8G32: chunk m at 16 (m ^ (token & 1)))
-      const int i = q * MOVE_THREADS + tid, t = i / CH, m = i % CH;
+      const int i = q * THREADS + tid, t = i / CH, m = i % CH;
       k[q] = zero;
       if (t < n * HALF && base[t])
         k[q] = *reinterpret_cast<const uint4*>(base[t] + (src[t] * CH + (KF == KVQ_Q8G32 ? m ^ (src[t] & 1) : m)) * 16);
     }
 #pragma unroll
     for (int q = 0; q < NV; ++q) {  // values: 16-byte row r of a pair holds both tokens' bytes interleaved
-      const int i = q * MOVE_THREADS + tid, pr = i >> 3, r = i & 7;
+      const int i = q * THREADS + tid, pr = i >> 3, r = i & 7;
       x[q] = y[q] = zero;
       if (pr < n * (HALF / 2)) {
         if (base[2 * pr]) x[q] = *reinterpret_cast<const uint4*>(base[2 * pr] + a.L.off_vmain + v_row(src[2 * pr] >> 1, r));
@@ -277,13 +326,13 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS) 
     }
 #pragma unroll
     for (int q = 0; q < NK; ++q) {
-      const int i = q * MOVE_THREADS + tid, t = i / CH, m = i % CH, td = t % HALF;
+      const int i = q * THREADS + tid, t = i / CH, m = i % CH, td = t % HALF;
       if (t < n * HALF)
         *reinterpret_cast<uint4*>(img0 + t / HALF * hb + (td * CH + (KF == KVQ_Q8G32 ? m ^ (td & 1) : m)) * 16) = k[q];
     }
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
-      const int i = q * MOVE_THREADS + tid, pr = i >> 3, r = i & 7;
+      const int i = q * THREADS + tid, pr = i >> 3, r = i & 7;
       if (pr < n * (HALF / 2)) {
         // bytes (slot, slot + 2) of the sources -> bytes (0, 2) and (1, 3)
         const uint32_t pick = (src[2 * pr] & 1 ? 0x0301u : 0x0200u) | (src[2 * pr + 1] & 1 ? 0x7050u : 0x6040u);
@@ -322,49 +371,31 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS) 
     const int half0 = half_of(w), n = min(HPW, a.n_halves - half0), chunks = hb / 16;
     const uint4* img = reinterpret_cast<const uint4*>(images + (size_t)(w & 1) * HPW * hb);
 #pragma unroll 2
-    for (int i = tid; i < n * chunks; i += MOVE_THREADS) {
+    for (int i = tid; i < n * chunks; i += THREADS) {
       const int half = i / chunks, g = half0 + half, phys = bt[g * HALF / PAGE];
       if (phys >= 0 && phys < a.L.n_pages)
         reinterpret_cast<uint4*>(pages + (size_t)phys * page_stride + (size_t)(g & 1) * hb)[i % chunks] = img[i];
     }
     __syncthreads();  // (the images are free for the window after next)
   }
+  if (a.W > 0 && (L - a.budget) % a.W != 0) {
+    const size_t at = (((size_t)layer * a.max_batch + b) * a.Hkv + h) * (size_t)a.W * D;
+    turn_ring(a, a.p.ringk + at, (L - a.budget) % a.W, rank, reinterpret_cast<float4*>(images), 2 * HPW * hb);
+    turn_ring(a, a.p.ringv + at, (L - a.budget) % a.W, rank, reinterpret_cast<float4*>(images), 2 * HPW * hb);
+  }
 }
 
 template <int KF>
-cudaError_t launch_move(const EvictArgs& a, cudaStream_t s) {
-  const size_t smem = 2 * HPW * (size_t)a.L.half_bytes;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(move_kernel<KF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.n_units * CLUSTER);
-  cfg.blockDim = dim3(MOVE_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, move_kernel<KF>, a);
+cudaError_t launch_format(const EvictArgs& a, cudaStream_t s) {
+  return go<evict_kernel<KF>>(dim3((unsigned)a.n_units * CLUSTER), THREADS, 2 * HPW * (size_t)a.L.half_bytes, false, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-  // the weights of the longest sequence, or of SEL_CACHE positions; at least eight channels of the largest ring
-  const int want = a.max_seq_len < SEL_CACHE ? a.max_seq_len : SEL_CACHE, least = 8 * MAX_WINDOW;
-  const int room = ((want > least ? want : least) + 3) / 4 * 4;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_CACHE * 4);
-  if (e != cudaSuccess) return e;
-  select_kernel<<<a.n_units + (a.W > 0 ? 2 * a.n_units : 0), SEL_THREADS, (size_t)room * 4, s>>>(a, room);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return a.k_format == KVQ_TQ3_QJL ? launch_move<KVQ_TQ3_QJL>(a, s)
-         : a.k_format == KVQ_Q8G32 ? launch_move<KVQ_Q8G32>(a, s)
-                                   : launch_move<KVQ_Q4G32>(a, s);
+  return a.k_format == KVQ_TQ3_QJL ? launch_format<KVQ_TQ3_QJL>(a, s)
+         : a.k_format == KVQ_Q8G32 ? launch_format<KVQ_Q8G32>(a, s)
+                                   : launch_format<KVQ_Q4G32>(a, s);
 }
 
 }  // namespace kvq
