@@ -16,7 +16,8 @@
 // are, exact in fp16 (S^T = codes [128 positions x 128] Q~^T, the queries as fp16 hi and lo), one accumulator per group of
 // 32 channels (TQ3: centroids and signs), and the thread that owns the position applies its scales and zeros in fp32:
 //   logit = sum_G scale_G S_G + zero_G (sum of q~ over G);  TQ3: n (S_c + w S_sign).
-// Raw keys (the window) are fp16 hi and lo against the queries as they are, hi hi + hi lo + lo hi.
+// Raw keys (the window) are fp16 hi and lo against the queries as they are: hi hi in all accumulators but one, hi lo + lo hi
+// in that.
 // Each warp keeps its own reference per row, which moves only when a logit passes it by 2^60: no exchange between warps
 // until the range ends.
 #pragma once
@@ -342,11 +343,15 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
           uint32_t ka = tmem + (!TQ && !raw ? ((it - it0) & 1) * C::K_COLS : 0);
           const uint32_t d = tmem + C_S + sb * (ACC * N);
           if (raw) {
-#pragma unroll 2
-            for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
-              mma_ts(d, ka, qa, ID_S, ks > 0);
-              mma_ts(d, ka, qa + qb, ID_S, 1);
-              mma_ts(d, ka + 64, qa, ID_S, 1);
+            // the tensor cores cut off each sum's low bits: hi hi over all accumulators but the last, which has the small rest
+            constexpr int LAST = (ACC - 1) * N;
+#pragma unroll 1
+            for (int ks = 0, i = -1; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
+              const int to = ks * (ACC - 1) / (D / 16);
+              mma_ts(d + to * N, ka, qa, ID_S, to == i);
+              mma_ts(d + LAST, ka, qa + qb, ID_S, ks > 0);
+              mma_ts(d + LAST, ka + 64, qa, ID_S, 1);
+              i = to;
             }
           } else {
             constexpr int STEPS = C::KD / 16 / ACC;  // k-steps per accumulator
@@ -562,13 +567,14 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
           // ---- CH rows' logits
           float s[CH], part[ACC][CH];
 #pragma unroll
-          for (int i = 0; i < ACC; ++i)
-            if (i == 0 || !raw) tm_ld(s_addr + i * N + c, part[i]);
+          for (int i = 0; i < ACC; ++i) tm_ld(s_addr + i * N + c, part[i]);
           tm_wait_ld();
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
             if (raw) {
               s[i] = part[0][i];
+#pragma unroll
+              for (int y = 1; y < ACC; ++y) s[i] += part[y][i];
             } else if (TQ) {
               s[i] = fmaf(part[1][i], s0[1], part[0][i] * s0[0]);
             } else {
