@@ -415,7 +415,23 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         __syncwarp();
       };
       int phys = -1;
-      if (!raw) {
+      if (raw) {
+        // raw rows go through registers a few at a time: the part's are brought to L2 while its queries are prepared
+        const int nraw = raw_count(L, a.W, a.n), nring = nraw - a.n, x1 = min(nraw, (it1 - nq) * TILE);
+        const size_t ring = (((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W, drafts = (((size_t)ll * a.batch + b) * a.Hkv + h) * a.n;
+        constexpr uint32_t ROW = D * (F32 ? 4 : 2);
+        for (int x = (it0 - nq) * TILE + lane; x < x1; x += 32) {
+          if (x < nring) {
+            const size_t at = (ring + (unsigned)(L - nring + x) % (unsigned)a.W) * D;
+            prefetch(a.p.ringk + at, D * 4);
+            prefetch(a.p.ringv + at, D * 4);
+          } else {
+            const size_t at = (drafts + x - nring) * ROW;
+            prefetch(static_cast<const uint8_t*>(a.k) + at, ROW);
+            prefetch(static_cast<const uint8_t*>(a.v) + at, ROW);
+          }
+        }
+      } else {
         phys = page_of(it0);
         copy(phys, true);
         copy(phys, false);

@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   static_assert(!TQ || C::STAGES * SM::REC <= 32768, "the records lie in the projection's place");
   constexpr uint32_t ID_S = idesc(TILE, N, false, false);
   extern __shared__ __align__(1024) uint8_t smem[];
-  // kr_bar: a tile's keys have landed; k_bar: they are in place (one arrival a worker warp); s_bar: a block's logits have
-  // been read; qk_bar: a block's products are done
-  __shared__ __align__(8) uint64_t kr_bar[C::STAGES], k_bar, s_bar[2], qk_bar[2], proj_bar, end_bar;
+  // kr_bar: a tile's keys have landed; k_bar: they are in place (one arrival a worker warp; two barriers by turns, as the
+  // workers place a second tile's before the ninth warp has to have seen the first's); s_bar: a block's logits have been
+  // read; qk_bar: a block's products are done
+  __shared__ __align__(8) uint64_t kr_bar[C::STAGES], k_bar[2], s_bar[2], qk_bar[2], proj_bar, end_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   __shared__ float part_sum[P - 1][TILE];  // of the groups of columns after the first
@@ -218,8 +219,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) bar_init(&kr_bar[i], 1);
-    bar_init(&k_bar, WARPS);
     for (int i = 0; i < 2; ++i) {
+      bar_init(&k_bar[i], WARPS);
       bar_init(&s_bar[i], WARPS);
       bar_init(&qk_bar[i], 1);
     }
@@ -255,7 +256,12 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
     tm_wait_st();
     fence_before();
     __syncwarp();
-    if (lane == 0) bar_arrive(&k_bar);
+    if (lane == 0) bar_arrive(&k_bar[k_n & 1]);
+    ++k_n;
+  };
+  const auto k_wait = [&] {
+    wait_nth(&k_bar[k_n & 1], k_n >> 1);
+    ++k_n;
   };
   const int col0 = (warp >> 2) * (N / P);
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       if (TQ && !raw) {
         // S q~ of all rows to columns 0 .. NR - 1: the projection comes as its hi plane, then its lo plane
         for (int part = 0; part < 2; ++part) {
-          wait_nth(&k_bar, k_n++);
+          k_wait();
           fence_after();
 #pragma unroll 1
           for (int rb = 0; rb < p.nb; ++rb) {
@@ -327,10 +333,16 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         wait_nth(&proj_bar, proj_n + 1);  // (the records come to the projection's place)
         proj_n += 2;
       }
-      if (!raw)
+      if (!raw) {
         for (int it = it0; it < min(it1, it0 + C::STAGES); ++it) copy(it);
+      } else {
+        // raw keys go through registers a few at a time: the part's are brought to L2 while its queries are prepared
+        const int j1 = min(L, qend + (it1 - nq) * TILE);
+        const size_t ring = (((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W;
+        for (int j = qend + (it0 - nq) * TILE + lane; j < j1; j += 32) prefetch(a.p.ringk + (ring + (unsigned)j % (unsigned)a.W) * D, D * 4);
+      }
       for (int it = it0; it < it1; ++it) {
-        wait_nth(&k_bar, k_n++);
+        k_wait();
         if (*(volatile int*)&abort_sh) break;
         if (!raw && it + C::STAGES < it1) copy(it + C::STAGES);  // the workers have read this tile's keys
         for (int rb = 0; rb < p.nb; ++rb, ++job) {
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         }
       } else {
         const float* row = a.p.ringk + ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (j < L ? (unsigned)j % (unsigned)a.W : 0u)) * D;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 16 / P; ++i) {
           const int kg = 16 / P * ln.hf + i;
           float f[8];

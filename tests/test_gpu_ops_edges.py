@@ -152,6 +152,29 @@ def test_two_streams_at_once():
                 assert torch.equal(ws[n][i][b, :, :lens[b]], weights[b, :, :lens[b]])
 
 
+@pytest.mark.parametrize("k_format", ["q4g32", "q8g32", "tq3_qjl"])
+@pytest.mark.parametrize("T", [1, 3])
+def test_weights_many_calls_none_gives_up(k_format, T):
+    """A wait between the warps of a CTA that missed its phase would run out of time, be flagged and leave weights out: over
+    many calls, with the caches of the GPU turned over in between, none does and all agree."""
+    rng = np.random.default_rng(91)
+    gpu, ora, _ = harness.make_pair(1, 8, 32, 4, 9000, k_format=k_format)
+    k = torch.as_tensor(rng.standard_normal((4, 8, 9000, 128)).astype(np.float32)).bfloat16().cuda()
+    gpu.append(0, k, k, _i32([0] * 4))
+    _, _, q = _drafts(rng, gpu.cfg, 4, T, "bf16")
+    q, ln = q.cuda(), _i32([9000, 8000, 5000, 8700])
+    first = gpu.attention_weights(0, q, ln, torch.zeros(4, 8, 9000, device="cuda"), 0.0)
+    other = torch.empty(160 << 20, dtype=torch.uint8, device="cuda")
+    bad = torch.zeros((), dtype=torch.bool, device="cuda")
+    w = torch.zeros_like(first)
+    for i in range(400):
+        if i % 2:
+            other.zero_()
+        gpu.attention_weights(0, q, ln, w, 0.0)
+        bad |= (w != first).any()
+    assert not bad.item() and gpu.status() == 0
+
+
 def test_captured_serving_step():
     """Tree, commit, weights and eviction in one graph, replayed on other lengths: what the calls give one by one."""
     rng = np.random.default_rng(81)
