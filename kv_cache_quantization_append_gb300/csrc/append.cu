@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(TQ_WARPS * 32) append_tq_keys_kernel(const App
 
 // Commit of accepted tree nodes: append_kernel with the vector's source read through the path and the token
 // range of each sequence its own; one vector per warp (paths are a few nodes, so what counts is how soon all
-// vectors are under way).  Same encoding, same bytes.
+// vectors are under way).  Same encoding, same bytes.  Measured: paths of up to 5 nodes of 4 sequences over 28
+// layers of 8 heads, Q8 keys, 7.7 us on the device and 8.5 a call, the host's: a chain of loads (path, count,
+// position, table, vector) and one encoding, far from any bandwidth.
 __global__ void __launch_bounds__(WARPS * 32) commit_kernel(const AppendArgs a, const CommitArgs c) {
   const int lane = threadIdx.x & 31;
   const unsigned total = (unsigned)a.n_layers_call * a.batch * a.Hkv * c.max_path * a.kv_n;

@@ -16,6 +16,9 @@
 // for halves, 2 l and 2 l + 1 for adjacent pairs): no exchange but the three steps of the norm's sum.
 // rot_dim not a multiple of 16 with halves reads the partner channels again (from L1).  The sines of a
 // token are computed once per CTA for all its heads.
+// Measured, bf16: 8192 tokens of 48 heads (201 MB) 39.9 us, 5.05 TB/s, 74 % of the copy rate (keeping the next
+// head's loads under way took registers, with them CTAs, and 57 us); 8 tokens 6 us on the device, one trip
+// through memory, and 10.5 a call, the host's.
 #include <cmath>
 
 #include "kvq_internal.cuh"

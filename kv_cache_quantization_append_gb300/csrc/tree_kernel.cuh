@@ -1,26 +1,33 @@
 // Tree attention: the kernels of one key format (included by one translation unit per format).
 //
 // A unit's rows (query heads of its nodes, node-major: row = node * g + head) are the N side of the products and
-// its positions the M side, so that the tensor cores do work for the rows there are (16 to 64 a CTA, more rows in
-// further CTAs) and a position's scales and norms belong to one thread:
+// its positions the M side, so that the tensor cores do work for the rows there are (16 to 64 a CTA with two threads to
+// a position, up to 128 with four, more rows in further CTAs) and a position's scales and norms belong to one thread:
 //   S^T [128 positions x N rows]  = K~ [128 x 128] Q~^T         (tcgen05.mma, K~ in tensor memory, Q~ in shared)
 //   O^T [128 channels x N rows] += V~^T [128 x 128] P^T         (both in shared memory)
 // where K~ and V~ are the dequantised records and Q~ the queries in the records' space (rotated, balanced), or the
-// window's and the drafts' raw vectors and the queries as they are.  The softmax runs in base 2 down a thread's own columns against a
-// reference per row that moves only when a logit passes it by 8 (weights stay below 2^8 in fp16): no exchange between
-// threads but one vote per tile.
+// window's and the drafts' raw vectors and the queries as they are.  The softmax runs in base 2 down a thread's own
+// columns against a reference per row that moves only when a logit passes it by 8 (weights stay below 2^8 in fp16): no
+// exchange between threads but one vote per tile.
 //
 // Two launches:
-//  1. tree_kernel: the tiles of all units in one list, cut into equal ranges, one per CTA (stream-K).  Eight warps of a
-//     CTA dequantise K~, then V~ while the tensor cores run the logits, then take the softmax, then go on to the next
-//     K~ while the tensor cores run P V; a ninth issues the products (issuing them costs a warp about as long as they
-//     take, which the others would all wait for) and the copies of the next tile's records, whose keys and values
-//     have one place each in shared memory (held in registers until used they spilled).  Two CTAs an SM fill each other's waits.  A range's part of a unit's
-//     records, and of its raw positions, ends as one partial record (reference, sum, O).
+//  1. tree_kernel: the tiles of all units in one list, cut into equal ranges, one per CTA (stream-K).  The worker warps
+//     (8, or 16 in one CTA an SM) dequantise K~, then V~ while the tensor cores run the logits, then take the softmax,
+//     then go on to the next K~ while the tensor cores run P V; one more warp issues the products (issuing them costs a
+//     warp about as long as they take, which the others would all wait for) and the copies of the next tile's records,
+//     whose keys and values have one place each in shared memory (held in registers until used they spilled).  Two CTAs
+//     an SM fill each other's waits.  A range's part of a unit's records, and of its raw positions, ends as one partial
+//     record (reference, sum, O).
 //  2. tree_merge_kernel (a programmatic dependent): joins a row's records in a fixed order, undoes the balancing and
 //     the rotation.
 // Rotating the queries and following the parents is done again by every CTA that needs them: a kernel in front that did
 // it once cost 6 us of latency.
+//
+// Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 47 us (137 TFLOP/s, 0.9 TB/s);
+// 128 rows over 8 sequences of up to 32K TQ3 249 us (387 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 96 us (222
+// TFLOP/s); 15 rows over 700 positions 18.6 us.  Bound by the workers in the long cases (converting a tile's codes to
+// operands and the exponentials keep the ALU pipe 53-57 % busy, and nobody waits for the tensor cores), by the latency of
+// one pass through both launches (lengths, table, records, product, softmax, product, join) in the short one.
 //
 // Operands: bf16 caches take each of K~, V~, Q~ and P rounded once to fp16 (2^-11, an eighth of the bf16 output's own
 // rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys are
@@ -1000,7 +1007,8 @@ size_t make_plan(const MultiArgs& a, int sms, Plan* p) {
   const int rows = a.n * a.g;
   p->a = a;
   // up to 64 rows: one block, two CTAs an SM (at most 101 KB of shared memory and 256 tensor-memory columns each); more:
-  // blocks of up to 128, one CTA an SM (128 rows over 8 x 32K TQ3: see the measurements below); float caches always in 64s
+  // blocks of up to 128, one CTA an SM, which dequantise a tile once where blocks of 64 do it twice (128 rows over 8 x
+  // 32K TQ3 250 us against 323, 192 rows over 4 x 9001 Q8 96 against 104); float caches' hi and lo parts fit 64
   const bool wide = !F32 && rows > MAX_ROWS;
   const int most = wide ? WIDE_ROWS : MAX_ROWS, step = wide ? 32 : 16;
   p->rb = (rows + most - 1) / most;

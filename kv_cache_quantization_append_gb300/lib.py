@@ -156,7 +156,7 @@ def _layers_in_call(cache: kvq_cache, layer: int) -> int:
     return cache.cfg.n_layers if layer == -1 else 1
 
 
-def _check_shape(name: str, t: torch.Tensor, want: tuple):  # (a torch.Size is a tuple)
+def _check_shape(name: str, t: torch.Tensor, want: tuple):
     """The library reads and writes whole rows of these shapes from the bare pointer; a tensor of
     another size would be read or written past its end, which the C ABI cannot see."""
     if t.shape != want:
