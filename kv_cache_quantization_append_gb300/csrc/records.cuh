@@ -13,10 +13,6 @@ using namespace tc;
 
 constexpr int TILE = 128;  // positions per tile = MMA M
 
-// Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
-// a tile ahead), and belongs to the range that holds its first place.
-constexpr int RAW_PLACES = 3;
-
 // warp 0: the sequences' lengths (0 where out of range) and the exclusive prefix of their tiles, [batch + 1]
 template <typename Tiles>
 __device__ __forceinline__ void tile_prefix(const MultiArgs& a, int* lens, int* pre, bool flag, Tiles tiles) {

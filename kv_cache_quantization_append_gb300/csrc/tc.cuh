@@ -126,6 +126,12 @@ __device__ __forceinline__ void tm_free(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 // this warp's 32 lanes x 4 or 8 consecutive columns
+__device__ __forceinline__ void tm_ld(uint32_t taddr, float (&f)[2]) {
+  uint32_t r[2];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+  f[0] = __uint_as_float(r[0]);
+  f[1] = __uint_as_float(r[1]);
+}
 __device__ __forceinline__ void tm_ld(uint32_t taddr, float (&f)[4]) {
   uint32_t r[4];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"

@@ -44,6 +44,9 @@ using namespace tc;
 using namespace records;
 
 constexpr int MAX_ROWS = 64, WIDE_ROWS = 128;  // rows per CTA of two, of four threads to a position
+// Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
+// a tile ahead), and belongs to the range that holds its first place.
+constexpr int RAW_PLACES = 3;
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
 

@@ -45,6 +45,9 @@ constexpr int MAX_ROWS = 128;   // of a launch
 // have room for two at 128 rows, and one with four threads was no faster (96 rows over 32K Q8: 113 us against 111).
 constexpr int NARROW_ROWS = 64;
 constexpr int ADD_THREADS = 256;
+// Places in the list of tiles: a raw tile counts as five of records (it comes with queries of its own), and belongs to the
+// range that holds its first place.  (32 queries at 32K Q8: three 112 us, four 110, five 109.)
+constexpr int RAW_PLACES = 5;
 
 struct Plan {
   MultiArgs a;
@@ -193,7 +196,7 @@ __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long 
   return l > 0.f ? m + log2f(l) : INFINITY;
 }
 
-// CH: a thread's rows of a block at a time: 8, or 4 where there are no more (they then keep their sums in registers)
+// CH: a thread's rows of a block at a time: 8, or 2 where there are no more than 4 (they then keep their sums in registers)
 template <int KF, bool SUM, int CH, int P>
 __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __grid_constant__ Plan p) {
   using C = Cfg<KF>;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   constexpr int WORKERS = 128 * P, WARPS = WORKERS / 32;  // and the warp that issues the products
   constexpr int N = 8 * P;                                // rows of a block: the accumulators of two blocks fit beside the keys
   constexpr int ACC = C::ACC;
-  constexpr bool FEW = CH == 4;
+  constexpr bool FEW = CH == 2;
   // tensor memory: K (128 columns: two tiles' codes; raw keys' hi and lo; TQ3 centroids and signs) | S, two buffers of ACC
   // accumulators of N columns
   constexpr uint32_t C_S = 128, TM_COLS = C_S + 2 * ACC * N <= 256 ? 256 : 512;
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
     wait_nth(&k_bar[k_n & 1], k_n >> 1);
     ++k_n;
   };
-  const int col0 = (warp >> 2) * (N / P);
+  const int col0 = (warp >> 2) * (FEW ? 2 : N / P);
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   float* wm = reinterpret_cast<float*>(smem + SM::wm(NR)) + warp * (NR / P);  // this warp's references and sums
   float* wl = reinterpret_cast<float*>(smem + SM::wl(NR)) + warp * (NR / P);
@@ -305,10 +308,10 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       using R = Rec<KF>;
       const auto page_of = [&](int it) {
         const int j = it * TILE + lane * HALF;
-        return lane < 4 && it < it1 && j < qend ? checked(__ldg(bt + j / PAGE), a.L.n_pages) : -1;
+        return lane < 4 && it < it1 && j < qend ? __ldg(bt + j / PAGE) : -1;
       };
-      const auto copy = [&](int it) {
-        const int phys = page_of(it), stage = kr_n % C::STAGES;
+      const auto copy = [&](int entry) {  // (checked here, not where it is read: nothing waits for it there)
+        const int phys = checked(entry, a.L.n_pages), stage = kr_n % C::STAGES;
         ++kr_n;
         const int n = __popc(__ballot_sync(FULL, phys >= 0));
         if (lane == 0) bar_expect(&kr_bar[stage], n * R::KH);
@@ -340,8 +343,15 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         wait_nth(&proj_bar, proj_n + 1);  // (the records come to the projection's place)
         proj_n += 2;
       }
+      int phys = -1;  // this lane's page of the tile to be copied next, read before it is needed
       if (!raw) {
-        for (int it = it0; it < min(it1, it0 + C::STAGES); ++it) copy(it);
+        int first[C::STAGES];
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i) first[i] = page_of(it0 + i);
+        phys = page_of(it0 + C::STAGES);
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i)
+          if (it0 + i < it1) copy(first[i]);
       } else {
         // raw keys go through registers a few at a time: the part's are brought to L2 while its queries are prepared
         const int j1 = min(L, qend + (it1 - nq) * TILE);
@@ -351,7 +361,10 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       for (int it = it0; it < it1; ++it) {
         k_wait();
         if (*(volatile int*)&abort_sh) break;
-        if (!raw && it + C::STAGES < it1) copy(it + C::STAGES);  // the workers have read this tile's keys
+        if (!raw && it + C::STAGES < it1) {  // the workers have read this tile's keys
+          copy(phys);
+          phys = page_of(it + C::STAGES + 1);
+        }
         for (int rb = 0; rb < p.nb; ++rb, ++job) {
           const int sb = job & 1;
           if (job >= 2) wait_nth(&s_bar[sb], (job - 2) >> 1);
@@ -551,7 +564,13 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       }
       k_done();
     };
-    float rm[4] = {NO_REF, NO_REF, NO_REF, NO_REF}, rl[4] = {};  // FEW: the warp's references, the thread's sums
+    float rm[2] = {NO_REF, NO_REF}, rl[2] = {};  // FEW: the warp's references, the thread's sums, its rows' sums for the zeros
+    float4 few_qs[2] = {};
+    if (FEW && Q4) {
+      few_qs[0] = *reinterpret_cast<const float4*>(qs + 4 * col0);
+      few_qs[1] = *reinterpret_cast<const float4*>(qs + 4 * col0 + 4);
+    }
+    float* const logits = p.logits ? p.logits + (size_t)u * p.rows * p.s_pad : nullptr;  // of this unit
     put(it0);
     for (int it = it0; it < it1; ++it) {
       const int j = (raw ? qend - nq * TILE : 0) + it * TILE + ln.t;  // this thread's position
@@ -581,7 +600,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         wait_nth(&qk_bar[sb], job >> 1);
         fence_after();
 #pragma unroll 1
-        for (int c = col0; c < col0 + (FEW ? (warp < 4 ? 4 : 0) : N / P) && rb * N + c < p.rows; c += CH) {
+        for (int c = col0; c < col0 + (FEW ? CH : N / P) && rb * N + c < p.rows; c += CH) {
           const int row = rb * N + c;
           // ---- CH rows' logits
           float s[CH], part[ACC][CH];
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
 #pragma unroll
               for (int y = 1; y < ACC; ++y) s[i] = fmaf(part[y % ACC][i], s0[y], s[i]);
               if (Q4) {
-                const float4 q = *reinterpret_cast<const float4*>(qs + 4 * (row + i));
+                const float4 q = FEW ? few_qs[i & 1] : *reinterpret_cast<const float4*>(qs + 4 * (row + i));
                 s[i] = fmaf(q.x, z0[0], fmaf(q.y, z0[1], fmaf(q.z, z0[2], fmaf(q.w, z0[3], s[i]))));
               }
             }
@@ -611,7 +630,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
             for (int i = 0; i < CH; ++i)
               if (row + i < cut) s[i] = -INFINITY;
           }
-          if (SUM) {
+          if constexpr (SUM) {
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < CH; i += 4) {
@@ -622,10 +641,11 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
             acc += sum[0] + sum[1];
             continue;
           }
-          if (p.logits != nullptr && mine) {
+          if (logits != nullptr && mine) {
+            float* at = logits + row * p.s_pad + j;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-              if (row + i < p.rows) p.logits[((size_t)u * p.rows + row + i) * p.s_pad + j] = s[i];
+            for (int i = 0; i < CH; ++i, at += p.s_pad)
+              if (row + i < p.rows) *at = s[i];
           }
           const int at = rb * (N / P) + c - col0;
           float m[CH];
@@ -716,9 +736,9 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         part_sync(1, WORKERS);
       }
     }
-    if (FEW && !SUM && warp < 4) {
+    if (FEW && !SUM) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         float v = rl[i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
@@ -737,7 +757,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       // ---- the range's maxima and sums: the four warps that hold a row's columns, joined in order
       float* out = p.parts + (size_t)(2 * u + raw + blockIdx.x) * p.rows * 2;
       for (int lr = tid; lr < p.rows; lr += WORKERS) {
-        const int c = lr % N, wg = c / (N / P), at = lr / N * (N / P) + c % (N / P);
+        const int c = lr % N, wg = FEW ? c / 2 : c / (N / P), at = FEW ? c % 2 : lr / N * (N / P) + c % (N / P);
         const float* m0 = reinterpret_cast<const float*>(smem + SM::wm(NR)) + 4 * wg * (NR / P) + at;
         const float* l0 = reinterpret_cast<const float*>(smem + SM::wl(NR)) + 4 * wg * (NR / P) + at;
         float m = NO_REF, l = 0.f;
@@ -876,7 +896,7 @@ cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
       return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8, 4>>(grid, threads, smem, true, s, p);
     }
   }
-  e = p.rows <= 4 ? go<weights_kernel<KF, false, 4, 2>>(grid, threads, smem, false, s, p)
+  e = p.rows <= 4 ? go<weights_kernel<KF, false, 2, 2>>(grid, threads, smem, false, s, p)
                   : go<weights_kernel<KF, false, 8, 2>>(grid, threads, smem, false, s, p);
   if (e != cudaSuccess) return e;
   if (p.logits == nullptr) {
