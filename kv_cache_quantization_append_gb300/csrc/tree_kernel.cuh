@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
   // warp); p_bar: its weights are; qk_bar, pv_bar: its products are done
   __shared__ __align__(8) uint64_t kr_bar, vr_bar, k_bar, v_bar, p_bar, qk_bar, pv_bar, end_bar;
   __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, leave_sh[2];  // leave_sh: what the workers act on, by turns of the tiles
   __shared__ __align__(16) float mref[N], fac[N];
   __shared__ float wmax[4][N];
   __shared__ unsigned long long nodes[KVQ_MAX_TREE];  // ancestors-or-self of each node (0: not there)
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
     bar_init(&end_bar, 1);
     bar_init(&qk_bar, 1);
     bar_init(&pv_bar, 1);
-    abort_sh = 0;
+    abort_sh = leave_sh[0] = leave_sh[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tile_prefix(a, lens, pre, blockIdx.x == 0, [&](int L) { return seq_tiles(a, L); });
@@ -829,10 +829,11 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         }
         fence_async_smem();
         fence_before();
+        if (tid == 0) leave_sh[it & 1] = *(volatile int*)&abort_sh;
         // (one raise puts every weight at or below 2^8; only an infinity or NaN is still over it then)
         if (!part_or(1, WORKERS, over) || raises >= 0) break;
       }
-      if (*(volatile int*)&abort_sh) {  // raised before the barrier above by whoever gave up: the workers leave together
+      if (leave_sh[it & 1]) {  // (read once, before the barrier above: all workers leave together or none does)
         ok = false;
         break;
       }

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   __shared__ __align__(8) uint64_t kr_bar[C::STAGES], k_bar[2], s_bar[2], qk_bar[2], proj_bar, end_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ float part_sum[P - 1][TILE];  // of the groups of columns after the first
+  __shared__ float part_sum[2][P - 1][TILE];  // of the groups of columns after the first, by turns of the tiles
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, NR = p.nb * N;
   const uint32_t q_plane = SM::plane(NR);
@@ -723,17 +723,16 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       }
       if ((TQ || raw) && it + 1 < it1) put(it + 1);
       if (SUM) {
-        if (warp >= 4) part_sum[(warp >> 2) - 1][ln.t] = acc;
-        part_sync(1, WORKERS);
-        if (*(volatile int*)&abort_sh) break;  // (raised before the barrier: all workers leave together)
+        float(*sums)[TILE] = part_sum[(it - it0) & 1];
+        if (warp >= 4) sums[(warp >> 2) - 1][ln.t] = acc;
+        if (part_or(1, WORKERS, *(volatile int*)&abort_sh != 0)) break;  // (all workers or none)
         if (warp < 4 && mine) {
           float* w = a.weights + (size_t)u * a.max_seq_len + j;
           float v = acc;
 #pragma unroll
-          for (int i = 0; i < P - 1; ++i) v += part_sum[i][ln.t];
+          for (int i = 0; i < P - 1; ++i) v += sums[i][ln.t];
           *w = p.decay != 0.f ? fmaf(p.decay, *w, v) : v;
         }
-        part_sync(1, WORKERS);
       }
     }
     if (FEW && !SUM) {
@@ -748,8 +747,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         }
       }
     }
-    part_sync(1, WORKERS);
-    if (*(volatile int*)&abort_sh) {  // (with the flag up every wait returns at once: all workers come here)
+    // (with the flag up every wait returns at once: all workers come here, and leave together or not at all)
+    if (part_or(1, WORKERS, *(volatile int*)&abort_sh != 0)) {
       ok = false;
       break;
     }
