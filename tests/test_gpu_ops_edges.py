@@ -120,6 +120,29 @@ def test_caches_past_four_gigabytes():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("L,budget,recent,offset", [(100001, 30001, 200, 0), (54000, 53000, 130, 3), (4100, 4099, 128, 0)])
+def test_evict_more_weights_than_shared_memory_holds(L, budget, recent, offset):
+    """Many equal weights over long sequences; a weights tensor whose units lie on odd addresses."""
+    rng = np.random.default_rng(L)
+    gpu = QuantKVCache(lib.make_config(1, 2, 2, 1, L + offset), "cuda")
+    k = torch.as_tensor(rng.standard_normal((1, 2, L, 128)).astype(np.float32)).bfloat16().cuda()
+    gpu.append(0, k, k, _i32([0]))
+    w = np.floor(rng.random((1, 2, L + offset)) ** 4 * 50).astype(np.float32)
+    wd = torch.as_tensor(w).cuda()
+    before = [harness.layout.read_unit(gpu.buffer, gpu.cfg, 0, 0, h, L) for h in range(2)]
+    kept, new = gpu.evict(0, wd, _i32([L]), budget, recent)
+    assert gpu.status() == 0 and new.item() == budget
+    for h in range(2):
+        src = ref.kept_positions(w[0, h], L, budget, recent)
+        assert np.array_equal(kept[0, h].cpu().numpy(), src)
+        want = w[0, h].copy()
+        want[:budget] = w[0, h, src]
+        assert np.array_equal(wd[0, h].cpu().numpy(), want)
+        after = harness.layout.read_unit(gpu.buffer, gpu.cfg, 0, 0, h, budget)
+        for name in after:
+            assert np.array_equal(after[name], before[h][name][src]), name
+
+
 def test_two_streams_at_once():
     """Calls with scratch of their own on two streams of one cache, many in flight: each gives what it gives alone."""
     rng = np.random.default_rng(71)
