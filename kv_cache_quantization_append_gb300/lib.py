@@ -328,13 +328,20 @@ def kv_qk_norm_rope(rope: kvq_rope, qkv: torch.Tensor, positions: torch.Tensor, 
     for w in (q_weight, k_weight):
         if w is not None:
             _check_shape("weight", w, (128,))
-    for x in (q, k, v, q_weight, k_weight):
-        if x is not None and x.dtype != qkv.dtype:
-            raise KVQError(f"dtype {x.dtype} does not match qkv's ({qkv.dtype})")
     if not qkv.is_cuda:
         raise KVQError("device tensor expected")
-    _check(load().kv_qk_norm_rope(ctypes.byref(rope), ctypes.c_void_p(qkv.data_ptr()), st, _ptr(positions), _ptr(q_weight),
-                                  _ptr(k_weight), eps, _ptr(q), _ptr(k), _ptr(v), B, T, hq, hkv, dt, _stream(stream)))
+    device, dtype = torch.cuda.current_device(), qkv.dtype  # (there is no cache whose device the library would check)
+    if qkv.get_device() != device or positions.get_device() != device:
+        raise KVQError("tensors must be on the current device")
+    for x in (q, k, v, q_weight, k_weight):
+        if x is not None:
+            if x.dtype != dtype:
+                raise KVQError(f"dtype {x.dtype} does not match qkv's ({dtype})")
+            if x.get_device() != device:
+                raise KVQError("tensors must be on the current device")
+    cuda_stream = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    _check(load().kv_qk_norm_rope(ctypes.byref(rope), qkv.data_ptr(), st, _ptr(positions), _ptr(q_weight), _ptr(k_weight),
+                                  eps, _ptr(q), _ptr(k), _ptr(v), B, T, hq, hkv, dt, cuda_stream))
 
 
 def kv_tree_scratch_bytes(cache: kvq_cache, layer: int, batch: int, n_nodes: int) -> int:

@@ -124,3 +124,16 @@ def test_captured_and_replayed():
     lib.kv_qk_norm_rope(rope, x, pos, *want)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_refuses_tensors_off_the_current_device(monkeypatch):
+    rope = lib.kv_rope_init(128)
+    x = torch.zeros(1, 1, 3 * 128, device="cuda")
+    q, k, v = (torch.zeros(1, 1, 1, 128, device="cuda") for _ in range(3))
+    pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    lib.kv_qk_norm_rope(rope, x, pos, q, k, v)
+    with pytest.raises(lib.KVQError):
+        lib.kv_qk_norm_rope(rope, x, pos.cpu(), q, k, v)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: x.get_device() + 1)
+    with pytest.raises(lib.KVQError):
+        lib.kv_qk_norm_rope(rope, x, pos, q, k, v)
