@@ -125,7 +125,8 @@ __device__ void select_kept(const EvictArgs& a, float* w, int32_t* kept, int L, 
   const int old = L - a.recent, want = a.budget - a.recent;  // old > want >= 0
   const int windows = (L + SEL_WINDOW - 1) / SEL_WINDOW;
   const bool cached = windows * SHARE * 4 <= room - 2 * BINS * 4;
-  const auto position = [&](int i) { return i / SHARE * SEL_WINDOW + rank * SHARE + i % SHARE; };  // of this CTA's i-th weight
+  // of this CTA's i-th weight
+  const auto position = [&](int i) { return i / SHARE * SEL_WINDOW + rank * SHARE + i % SHARE; };
   const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
   // four weights from position j on (zeros past the end)
   const auto load4 = [&](int j) {

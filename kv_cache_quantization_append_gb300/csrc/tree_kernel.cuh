@@ -25,9 +25,11 @@
 //
 // Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 47 us (137 TFLOP/s, 0.9 TB/s);
 // 128 rows over 8 sequences of up to 32K TQ3 249 us (387 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 96 us (222
-// TFLOP/s); 15 rows over 700 positions 18.6 us.  Bound by the workers in the long cases (converting a tile's codes to
-// operands and the exponentials keep the ALU pipe 53-57 % busy, and nobody waits for the tensor cores), by the latency of
-// one pass through both launches (lengths, table, records, product, softmax, product, join) in the short one.
+// TFLOP/s); 15 rows over 700 positions 18.6 us.  Bound by the workers in the long cases: 524 instructions a warp and tile
+// of 128 rows, a scheduler's four warps issuing in 53 % of the cycles (ALU pipe 48 %, tensor pipe 27 %), held by fixed
+// latencies and tensor-memory reads rather than by the products -- with a second place for the logits, taken a tile
+// ahead, nobody waited for them and the calls took 254, 48, 102 and 22 us.  The short case is one pass' latency through
+// both launches: lengths, table, records, product, softmax, product, join.
 //
 // Operands: bf16 caches take each of K~, V~, Q~ and P rounded once to fp16 (2^-11, an eighth of the bf16 output's own
 // rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys are
@@ -54,7 +56,8 @@ constexpr float NO_REF = -1e30f;  // reference of a row that has met no position
 struct Plan {
   MultiArgs a;
   int rb, N, n_units, G;  // row blocks of N rows per unit, units (with row blocks), CTAs
-  float* records;         // [2 n_units + G][2 N + 128 N]: range c's part of unit u's records (+ 0) or raw positions (+ 1) at 2 u + c
+  // [2 n_units + G][2 N + 128 N]: range c's part of unit u's records (+ 0) or raw positions (+ 1) at 2 u + c
+  float* records;       
 };
 
 __host__ __device__ inline int raw_count(int L, int W, int n) { return (W > 0 ? (L < W - 1 ? L : W - 1) : 0) + n; }
@@ -332,7 +335,8 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
 
   // this CTA's range of the list of tiles
   const long long per_layer = (long long)pre[a.batch] * a.Hkv * p.rb, total = per_layer * a.n_layers_call;
-  const long long G = min((long long)p.G, total);  // (no range is empty: the merge reads every range that has records of a unit)
+  // (no range is empty: the merge reads every range that has records of a unit)
+  const long long G = min((long long)p.G, total);
   long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
   const long long t_end = blockIdx.x < G ? quick_div(total * (blockIdx.x + 1), G) : 0;
 
@@ -365,7 +369,8 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
     __syncwarp();
     if (lane == 0) bar_arrive(&k_bar);
   };
-  const int grp = (warp >> 2) % P, col0 = grp * NC;                                      // this thread's columns (rows of the unit)
+  // this thread's columns (rows of the unit)
+  const int grp = (warp >> 2) % P, col0 = grp * NC;                                    
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // its lane: position ln.t, channel ln.t
   bool ok = true;
 

@@ -56,7 +56,8 @@ struct Plan {
   int n_units, G;
   long long s_pad;    // positions a row of stored logits has room for
   float decay;
-  float* parts;       // [2 n_units + G][rows][2]: range c's maxima and sums of unit u's records (+ 0), raw keys (+ 1) at 2 u + c
+  // [2 n_units + G][rows][2]: range c's maxima and sums of unit u's records (+ 0), raw keys (+ 1) at 2 u + c
+  float* parts;     
   float* logits;      // [n_units][rows][s_pad], or null
   float* norms;       // [n_units][rows] normalisers, where logits are taken again
 };
@@ -91,7 +92,8 @@ struct Smem {
   static __host__ __device__ constexpr uint32_t rec(int rows) { return 2 * plane(rows); }
   static constexpr uint32_t REC = 4 * Rec<KF>::KH;
   // (TQ3: a plane of the projection first takes the records' place)
-  static __host__ __device__ constexpr uint32_t wm(int rows) { return rec(rows) + (C::TQ ? 32768 : C::STAGES * REC); }  // [4 P warps][rows / P]
+  // [4 P warps][rows / P]
+  static __host__ __device__ constexpr uint32_t wm(int rows) { return rec(rows) + (C::TQ ? 32768 : C::STAGES * REC); }
   static __host__ __device__ constexpr uint32_t wl(int rows) { return wm(rows) + 16 * rows; }
   static __host__ __device__ constexpr uint32_t qs(int rows) { return wl(rows) + 16 * rows; }              // [rows][4]
   static __host__ __device__ constexpr uint32_t pre(int rows) { return qs(rows) + 16 * rows; }
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   using SM = Smem<KF>;
   constexpr bool TQ = C::TQ, Q4 = KF == KVQ_Q4G32;
   constexpr int WORKERS = 128 * P, WARPS = WORKERS / 32;  // and the warp that issues the products
-  constexpr int N = 8 * P;                                // rows of a block: the accumulators of two blocks fit beside the keys
+  // rows of a block: the accumulators of two blocks fit beside the keys
+  constexpr int N = 8 * P;                              
   constexpr int ACC = C::ACC;
   constexpr bool FEW = CH == 2;
   // tensor memory: K (128 columns: two tiles' codes; raw keys' hi and lo; TQ3 centroids and signs) | S, two buffers of ACC
@@ -375,7 +378,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
           uint32_t ka = tmem + (!TQ && !raw ? ((it - it0) & 1) * C::K_COLS : 0);
           const uint32_t d = tmem + C_S + sb * (ACC * N);
           if (raw) {
-            // the tensor cores cut off each sum's low bits: hi hi over all accumulators but the last, which has the small rest
+            // the tensor cores cut off each sum's low bits: hi hi over all accumulators but the last, which has the small
+            // rest
             constexpr int LAST = (ACC - 1) * N;
 #pragma unroll 1
             for (int ks = 0, i = -1; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
@@ -564,7 +568,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       }
       k_done();
     };
-    float rm[2] = {NO_REF, NO_REF}, rl[2] = {};  // FEW: the warp's references, the thread's sums, its rows' sums for the zeros
+    // FEW: the warp's references, the thread's sums, its rows' sums for the zeros
+    float rm[2] = {NO_REF, NO_REF}, rl[2] = {};
     float4 few_qs[2] = {};
     if (FEW && Q4) {
       few_qs[0] = *reinterpret_cast<const float4*>(qs + 4 * col0);
@@ -782,7 +787,8 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
     mma_commit(&end_bar);
     land(&end_bar, 0);
   }
-  if (SUM) asm volatile("griddepcontrol.wait;" ::: "memory");  // (a CTA without tiles too: no kernel ends before the one it follows)
+  // (a CTA without tiles too: no kernel ends before the one it follows)
+  if (SUM) asm volatile("griddepcontrol.wait;" ::: "memory");
   fence_before();
   __syncthreads();
   if (warp == 1) {
