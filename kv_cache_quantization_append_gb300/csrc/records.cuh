@@ -59,8 +59,7 @@ __host__ __device__ constexpr uint32_t mm_off(int m, int k) { return mn_off(m, k
 // Four channels (4 lane .. + 3) of a vector held by a warp, as the 8 bytes that belong at 8 (lane & 1) of their
 // 16-byte group: in order, or in the order in which nibbles() leaves eight codes
 template <bool NIBBLE_ORDER>
-__device__ __forceinline__ uint2 pack4(float y0, float y1, float y2, float y3, int lane) {
-  const uint32_t a = h2u(__floats2half2_rn(y0, y1)), b = h2u(__floats2half2_rn(y2, y3));
+__device__ __forceinline__ uint2 pack4(uint32_t a, uint32_t b, int lane) {  // pairs (0, 1) and (2, 3)
   if (!NIBBLE_ORDER) return make_uint2(a, b);
   const bool odd = lane & 1;
   const uint32_t r = __shfl_xor_sync(FULL, odd ? a : b, 1);
@@ -74,13 +73,14 @@ __device__ __forceinline__ float2 load2_in(const void* base, int off, bool bf16)
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 __device__ __forceinline__ float lo_part(float v) { return v - __half2float(__float2half_rn(v)); }
-// store the four channels to a plane and, with F32, their lo parts to the next
-template <bool NIBBLE_ORDER, bool F32>
+// store the four channels' hi parts to a plane and their lo parts to the next
+template <bool NIBBLE_ORDER>
 __device__ __forceinline__ void put4(uint8_t* dst, uint32_t plane, const float (&y)[4], int lane) {
-  *reinterpret_cast<uint2*>(dst) = pack4<NIBBLE_ORDER>(y[0], y[1], y[2], y[3], lane);
-  if (F32)
-    *reinterpret_cast<uint2*>(dst + plane) =
-        pack4<NIBBLE_ORDER>(lo_part(y[0]), lo_part(y[1]), lo_part(y[2]), lo_part(y[3]), lane);
+  uint32_t h[2], l[2];
+  split2(y[0], y[1], h[0], l[0]);
+  split2(y[2], y[3], h[1], l[1]);
+  *reinterpret_cast<uint2*>(dst) = pack4<NIBBLE_ORDER>(h[0], h[1], lane);
+  *reinterpret_cast<uint2*>(dst + plane) = pack4<NIBBLE_ORDER>(l[0], l[1], lane);
 }
 
 // ------------------------------------------------------------------ a tile's records

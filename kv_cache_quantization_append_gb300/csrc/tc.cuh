@@ -96,6 +96,7 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead, uint32_t
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+constexpr uint32_t BF16_OPERANDS = (1u << 7) | (1u << 10);  // or'ed to it: both operands bf16
 // D[tmem] (+)= A[smem] B[smem]^T; the whole warp calls, its elected lane issues
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(

@@ -1,13 +1,13 @@
 // Tree attention: the kernels of one key format (included by one translation unit per format).
 //
 // A unit's rows (query heads of its nodes, node-major: row = node * g + head) are the N side of the products and
-// its positions the M side, so that the tensor cores do work for the rows there are (16 to 64 a CTA with two threads to
-// a position, up to 128 with four, more rows in further CTAs) and a position's scales and norms belong to one thread:
+// its positions the M side, so that the tensor cores do work for the rows there are (16 a CTA with two threads to a
+// position, up to 96 with four, more rows in further CTAs) and a position's scales and norms belong to one thread:
 //   S^T [128 positions x N rows]  = K~ [128 x 128] Q~^T         (tcgen05.mma, K~ in tensor memory, Q~ in shared)
 //   O^T [128 channels x N rows] += V~^T [128 x 128] P^T         (both in shared memory)
 // where K~ and V~ are the dequantised records and Q~ the queries in the records' space (rotated, balanced), or the
 // window's and the drafts' raw vectors and the queries as they are.  The softmax runs in base 2 down a thread's own
-// columns against a reference per row that moves only when a logit passes it by 8 (weights stay below 2^8 in fp16): no
+// columns against a reference per row that moves only when a logit passes it by 8 (weights stay below 2^8): no
 // exchange between threads but one vote per tile.
 //
 // Two launches:
@@ -23,18 +23,17 @@
 // Rotating the queries and following the parents is done again by every CTA that needs them: a kernel in front that did
 // it once cost 6 us of latency.
 //
-// Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 47 us (137 TFLOP/s, 0.9 TB/s);
-// 128 rows over 8 sequences of up to 32K TQ3 249 us (387 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 96 us (222
-// TFLOP/s); 15 rows over 700 positions 18.6 us.  Bound by the workers in the long cases: 524 instructions a warp and tile
-// of 128 rows, a scheduler's four warps issuing in 53 % of the cycles (ALU pipe 48 %, tensor pipe 27 %), held by fixed
-// latencies and tensor-memory reads rather than by the products -- with a second place for the logits, taken a tile
-// ahead, nobody waited for them and the calls took 254, 48, 102 and 22 us.  The short case is one pass' latency through
-// both launches: lengths, table, records, product, softmax, product, join.
+// Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 68 us (95 TFLOP/s, 0.64 TB/s);
+// 128 rows over 8 sequences of up to 32K TQ3 641 us (150 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 141 us (151
+// TFLOP/s); 15 rows over 700 positions 21 us.
 //
-// Operands: bf16 caches take each of K~, V~, Q~ and P rounded once to fp16 (2^-11, an eighth of the bf16 output's own
-// rounding step); float caches split each into fp16 hi and lo and run hi hi + hi lo + lo hi (22 bits).  TQ3 keys are
-// [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w = sqrt(pi/2)/128 gamma rounds
-// once (hi and lo for float caches), and the thread that owns the position multiplies by the norm n.
+// Operands: each of K~, V~, Q~ and P is a pair of 16-bit values, hi and lo, and every product hi hi + hi lo + lo hi, so that
+// an output is the definition's up to its own rounding (1e-7 to 4e-6 of the largest beyond a bf16 output's half step).  fp16
+// pairs hold 22 bits of records; once-rounded fp16 operands took 18.5, 48, 250 and 96 us for the cases above, but their
+// errors, up to 1.3e-3 of the largest output where attention is peaked, came on top of the output's rounding.  Raw vectors
+// of a bf16 cache are bf16 pairs, which hold 16 bits of any magnitude (its queries one, exactly); a float cache's are fp16
+// pairs.  TQ3 keys are [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w =
+// sqrt(pi/2)/128 gamma is a pair, and the thread that owns the position multiplies by the norm n.
 #pragma once
 
 #include "records.cuh"
@@ -45,7 +44,10 @@ namespace tree {
 using namespace tc;
 using namespace records;
 
-constexpr int MAX_ROWS = 64, WIDE_ROWS = 128;  // rows per CTA of two, of four threads to a position
+// Rows of a block (a CTA's): up to 16 take two threads to a position and two CTAs an SM, more take four threads and one CTA;
+// what else a block has to hold in shared memory ends at 96 rows, for TQ3 keys, whose queries come with their projections,
+// at 64.
+constexpr int FEW_ROWS = 16, MAX_ROWS = 96, TQ_ROWS = 64;
 // Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
 // a tile ahead), and belongs to the range that holds its first place.
 constexpr int RAW_PLACES = 3;
@@ -70,58 +72,62 @@ __host__ __device__ inline int quant_end(int L, int W, int n) {
 __device__ __forceinline__ int seq_tiles(const MultiArgs& a, int L) {
   return (quant_end(L, a.W, a.n) + TILE - 1) / TILE + (raw_count(L, a.W, a.n) + TILE - 1) / TILE * RAW_PLACES;
 }
-template <int KF, bool F32>
+template <int KF>
 struct Cfg {
   static constexpr bool TQ = KF == KVQ_TQ3_QJL;
-  static constexpr int PL = F32 ? 2 : 1;            // fp16 planes per value
   static constexpr int KD = TQ ? 256 : 128;         // width of a query image: [q~] or [q~, S q~]
-  static constexpr uint32_t PLANE = TILE * D * 2;   // 32 KB
+  static constexpr uint32_t PLANE = TILE * D * 2;   // 32 KB: values are two of them, hi and lo
   // columns of keys in tensor memory: KD / 2 (hi), then lo (TQ3: of the weights and of raw keys only, which share them)
-  static constexpr uint32_t K_COLS = KD / 2 + (F32 ? 64 : 0);
+  static constexpr uint32_t K_COLS = KD / 2 + 64;
 };
 
+// hi and lo of a pair as fp16, or as bf16 (16 bits of any magnitude)
+__device__ __forceinline__ void split2(bool bf16, float a, float b, uint32_t& hi, uint32_t& lo) {
+  if (!bf16) return tc::split2(a, b, hi, lo);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const float2 hf = __bfloat1622float2(h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - hf.x, b - hf.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 // channels 4 lane .. + 3 of row r of a query image, in the order in which put_k leaves the keys' channels
-template <int KF, bool F32>
-__device__ __forceinline__ void put_q(uint8_t* img, int r, int N, uint32_t plane, const float (&y)[4], int lane) {
+template <int KF>
+__device__ __forceinline__ void put_q(uint8_t* img, int r, int N, uint32_t plane, const float (&y)[4], bool bf16, int lane) {
+  uint32_t h[2], l[2];
+  split2(bf16, y[0], y[1], h[0], l[0]);
+  split2(bf16, y[2], y[3], h[1], l[1]);
   if (KF != KVQ_Q8G32) {
-    put4<KF == KVQ_Q4G32, F32>(img + km_off(r, 4 * lane & ~7, N) + 8 * (lane & 1), plane, y, lane);
+    uint8_t* dst = img + km_off(r, 4 * lane & ~7, N) + 8 * (lane & 1);
+    *reinterpret_cast<uint2*>(dst) = pack4<KF == KVQ_Q4G32>(h[0], h[1], lane);
+    *reinterpret_cast<uint2*>(dst + plane) = pack4<KF == KVQ_Q4G32>(l[0], l[1], lane);
     return;
   }
   const int kk = lane >> 2, i0 = 2 * (lane & 1), at = 4 * (kk & 3) + (lane & 2);  // channels 16 kk + 4 (lane & 3) + e
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    uint32_t hi, lo;
-    split2(y[2 * p], y[2 * p + 1], hi, lo);
     uint8_t* dst = img + km_off(r, 16 * (2 * (i0 + p) + (kk >> 2)) + at, N);
-    *reinterpret_cast<uint32_t*>(dst) = hi;
-    if (F32) *reinterpret_cast<uint32_t*>(dst + plane) = lo;
+    *reinterpret_cast<uint32_t*>(dst) = h[p];
+    *reinterpret_cast<uint32_t*>(dst + plane) = l[p];
   }
 }
 
 // ------------------------------------------------------------------ dequantising
-// eight codes of a word times scale plus zero (and, with F32, their lo parts)
-template <bool F32>
+// eight codes of a word times scale plus zero, and their lo parts
 __device__ __forceinline__ void dequant8(uint32_t word, uint32_t s2, uint32_t z2, uint4& o, uint4& l) {
   __half2 c[4];
   nibbles(word, c);
-  if (!F32) {
-    o.x = h2u(__hfma2(c[0], u2h(s2), u2h(z2)));
-    o.y = h2u(__hfma2(c[1], u2h(s2), u2h(z2)));
-    o.z = h2u(__hfma2(c[2], u2h(s2), u2h(z2)));
-    o.w = h2u(__hfma2(c[3], u2h(s2), u2h(z2)));
-  } else {
-    const float s = __low2float(u2h(s2)), z = __low2float(u2h(z2));
-    const float2 f0 = __half22float2(c[0]), f1 = __half22float2(c[1]), f2 = __half22float2(c[2]), f3 = __half22float2(c[3]);
-    split2(z + s * f0.x, z + s * f0.y, o.x, l.x);
-    split2(z + s * f1.x, z + s * f1.y, o.y, l.y);
-    split2(z + s * f2.x, z + s * f2.y, o.z, l.z);
-    split2(z + s * f3.x, z + s * f3.y, o.w, l.w);
-  }
+  const float s = __low2float(u2h(s2)), z = __low2float(u2h(z2));
+  const float2 f0 = __half22float2(c[0]), f1 = __half22float2(c[1]), f2 = __half22float2(c[2]), f3 = __half22float2(c[3]);
+  tc::split2(z + s * f0.x, z + s * f0.y, o.x, l.x);
+  tc::split2(z + s * f1.x, z + s * f1.y, o.y, l.y);
+  tc::split2(z + s * f2.x, z + s * f2.y, o.z, l.z);
+  tc::split2(z + s * f3.x, z + s * f3.y, o.w, l.w);
 }
 
 // keys of the thread's part of its position to the position's tensor-memory lane: columns 0..63 (TQ3: centroids), then
 // TQ3's signed weights, then the lo parts
-template <int KF, bool F32, int P>
+template <int KF, int P>
 __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_t* rec, const uint4& cent) {
   using R = Rec<KF>;
   const uint8_t* hb = rec + (ln.t >> 5) * R::KH;
@@ -146,13 +152,14 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
       const uint32_t s2 = G & 1 ? dup_hi(sc[G >> 1]) : dup_lo(sc[G >> 1]), z2 = G & 1 ? dup_hi(zr[G >> 1]) : dup_lo(zr[G >> 1]);
       uint4 o[CHUNKS], l[CHUNKS];
 #pragma unroll
-      for (int i = 0; i < CHUNKS; ++i) dequant8<F32>(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, s2, z2, o[i], l[i]);
+      for (int i = 0; i < CHUNKS; ++i) dequant8(G == 0 ? k[i].x : G == 1 ? k[i].y : G == 2 ? k[i].z : k[i].w, s2, z2, o[i], l[i]);
       const uint32_t at = col + 16 * G + 4 * CHUNKS * ln.hf;
       if constexpr (CHUNKS == 2) {
         tm_st8(at, o[0], o[1]);
-        if (F32) tm_st8(at + 64, l[0], l[1]);
+        tm_st8(at + 64, l[0], l[1]);
       } else {
         tm_st4(at, o[0]);
+        tm_st4(at + 64, l[0]);
       }
     }
   } else if (KF == KVQ_Q8G32) {
@@ -168,23 +175,19 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const __half2 v = __hsub2(u2h(prmt(wd[i], 0x64646464u, x ? 0x4342 : 0x4140)), off);
-          if (F32) {
-            const float d = __low2float(u2h(s2));
-            const float2 f = __half22float2(v);
-            split2(d * f.x, d * f.y, o[2 * i + x], l[2 * i + x]);
-          } else {
-            o[2 * i + x] = h2u(__hmul2(v, u2h(s2)));
-          }
+          const float d = __low2float(u2h(s2));
+          const float2 f = __half22float2(v);
+          tc::split2(d * f.x, d * f.y, o[2 * i + x], l[2 * i + x]);
         }
       }
       const uint32_t at = col + 8 * (CHUNKS * ln.hf + c);
       tm_st8(at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-      if (F32) tm_st8(at + 64, make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]));
+      tm_st8(at + 64, make_uint4(l[0], l[1], l[2], l[3]), make_uint4(l[4], l[5], l[6], l[7]));
     }
   } else {
     const float wf = QJL_CONST * __half2float(reinterpret_cast<const __half*>(hb + R::K_MAIN)[HALF + tt]);
     uint32_t wh, wl;
-    split2(wf, wf, wh, wl);
+    tc::split2(wf, wf, wh, wl);
     wh ^= 0x80008000u;  // -w
     wl ^= 0x80008000u;
 #pragma unroll
@@ -207,22 +210,22 @@ __device__ __forceinline__ void put_k(uint32_t col, const Lane& ln, const uint8_
 #pragma unroll
         for (int j = 0; j < 4; ++j) m[j] = prmt(lo, word, (uint32_t)((8 + j) << 4) | (uint32_t)((12 + j) << 12)) & 0x80008000u;
         s[x] = make_uint4(wh ^ m[0], wh ^ m[1], wh ^ m[2], wh ^ m[3]);
-        if (F32) l[x] = make_uint4(wl ^ m[0], wl ^ m[1], wl ^ m[2], wl ^ m[3]);
+        l[x] = make_uint4(wl ^ m[0], wl ^ m[1], wl ^ m[2], wl ^ m[3]);
       }
       const uint32_t at = col + 16 * CHUNKS * ln.hf + 4 * i;
       tm_st8(at, o[0], o[1]);
       tm_st8(at + 64, s[0], s[1]);
-      if (F32) tm_st8(at + 128, l[0], l[1]);
+      tm_st8(at + 128, l[0], l[1]);
     }
   }
 }
 
 // values of the thread's two positions, eight channels of each of its groups; positions from `left` on (of the pair) are
 // zero
-template <int KF, bool F32, int P>
+template <int KF, int P>
 __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t* rec, int left) {
   using R = Rec<KF>;
-  constexpr uint32_t PLANE = Cfg<KF, F32>::PLANE;
+  constexpr uint32_t PLANE = Cfg<KF>::PLANE;
   constexpr int GROUPS = 8 / P;
   const uint8_t* hb = rec + R::V0 + (ln.vp >> 4) * R::VH;
   const int pp = ln.vp & 15;
@@ -251,9 +254,9 @@ __device__ __forceinline__ void put_v(uint8_t* vb, const Lane& ln, const uint8_t
       const uint32_t pick = e ? 0x7531u : 0x6420u, dup = e ? 0x3232u : 0x1010u;
       uint8_t* dst = base + (e ? 16 : 0) + 512 * G;
       uint4 o, l;
-      dequant8<F32>(prmt(w0[G], w1[G], pick), prmt(vs, vs, dup), prmt(vz, vz, dup), o, l);
+      dequant8(prmt(w0[G], w1[G], pick), prmt(vs, vs, dup), prmt(vz, vz, dup), o, l);
       *reinterpret_cast<uint4*>(dst) = o;
-      if (F32) *reinterpret_cast<uint4*>(dst + PLANE) = l;
+      *reinterpret_cast<uint4*>(dst + PLANE) = l;
     }
   }
 }
@@ -271,21 +274,21 @@ __device__ __forceinline__ void halve(float* l, int lane) {
 
 // ------------------------------------------------------------------ 1. the tiles
 // dynamic shared memory: V planes | query image | P planes | records | prefix of the sequences' tiles, lengths
-template <int KF, bool F32>
+template <int KF>
 struct Smem {
-  using C = Cfg<KF, F32>;
-  static constexpr uint32_t V = 0, Q = C::PL * C::PLANE;
-  static __host__ __device__ constexpr uint32_t P(int N) { return Q + N * C::KD * 2 * C::PL; }
-  static __host__ __device__ constexpr uint32_t R(int N) { return P(N) + N * TILE * 2 * C::PL; }
+  using C = Cfg<KF>;
+  static constexpr uint32_t V = 0, Q = 2 * C::PLANE;
+  static __host__ __device__ constexpr uint32_t P(int N) { return Q + N * C::KD * 4; }
+  static __host__ __device__ constexpr uint32_t R(int N) { return P(N) + N * TILE * 4; }
   static __host__ __device__ constexpr uint32_t total(int N) { return R(N) + Rec<KF>::BYTES; }
 };
 
-// P threads to a position: 2 (two CTAs an SM), or 4 for more than MAX_ROWS rows, which then share the dequantised keys and
-// values (one CTA an SM)
+// P threads to a position: 2 (two CTAs an SM), or 4 for more than FEW_ROWS rows, which then share the dequantised keys and
+// values (one CTA an SM); F32: the raw vectors and queries of a float cache
 template <int KF, int NC, bool F32, int P>
-__global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kernel(const __grid_constant__ Plan p) {
-  using C = Cfg<KF, F32>;
-  using SM = Smem<KF, F32>;
+__global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(const __grid_constant__ Plan p) {
+  using C = Cfg<KF>;
+  using SM = Smem<KF>;
   constexpr int WORKERS = 128 * P, WARPS = WORKERS / 32;  // and the warp that issues the products
   constexpr int N = P * NC;  // rows, NC of them to a thread, CH at a time
   constexpr int CH = 8;
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
   constexpr uint32_t C_S = C::K_COLS, C_O = C_S + N, COLS = C_O + N;
   constexpr uint32_t TM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   constexpr uint32_t ID_S = idesc(TILE, N, false, false), ID_O = idesc(D, N, true, true);
+  constexpr uint32_t RAW_TYPE = F32 ? 0 : BF16_OPERANDS;  // of raw parts
   constexpr uint64_t LO_Q = (N * C::KD * 2) >> 4, LO_V = C::PLANE >> 4, LO_P = (N * TILE * 2) >> 4;
   extern __shared__ __align__(1024) uint8_t smem[];
   // kr_bar, vr_bar: a tile's records have landed; k_bar, v_bar: its keys, values are in place (one arrival a worker
@@ -459,10 +463,8 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
 #pragma unroll 1
         for (int ks = 0; ks < D / 16; ++ks, sa += 256, qa += 2 * N) {
           mma_ss(tmem + C_S, sa, qa, ID_S, ks > 0);
-          if (F32) {
-            mma_ss(tmem + C_S, sa + LO_V, qa, ID_S, 1);
-            mma_ss(tmem + C_S, sa, qa + LO_Q, ID_S, 1);
-          }
+          mma_ss(tmem + C_S, sa + LO_V, qa, ID_S, 1);
+          mma_ss(tmem + C_S, sa, qa + LO_Q, ID_S, 1);
         }
         mma_commit(&qk_bar);
       }
@@ -475,18 +477,19 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         {
           uint64_t qa = sdesc(sbase + SM::Q, N * 16, 128);
           uint32_t ka = tmem;
+          const uint32_t id = raw ? ID_S | RAW_TYPE : ID_S;
 #pragma unroll 4
           for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
-            mma_ts(tmem + C_S, ka, qa, ID_S, ks > 0);
-            if (F32) mma_ts(tmem + C_S, ka, qa + LO_Q, ID_S, 1);
-            if (F32 && (!TQ || raw)) mma_ts(tmem + C_S, ka + C::KD / 2, qa, ID_S, 1);
+            mma_ts(tmem + C_S, ka, qa, id, ks > 0);
+            if (F32 || !raw) mma_ts(tmem + C_S, ka, qa + LO_Q, id, 1);  // (bf16 queries have no lo part)
+            if (!TQ || raw) mma_ts(tmem + C_S, ka + C::KD / 2, qa, id, 1);
           }
           if (TQ && !raw) {  // the signed weights against S q~
 #pragma unroll 4
             for (int ks = 0; ks < D / 16; ++ks, ka += 8, qa += 2 * N) {
               mma_ts(tmem + C_S, ka, qa, ID_S, 1);
-              if (F32) mma_ts(tmem + C_S, ka, qa + LO_Q, ID_S, 1);
-              if (F32) mma_ts(tmem + C_S, ka + 64, qa, ID_S, 1);
+              mma_ts(tmem + C_S, ka, qa + LO_Q, ID_S, 1);
+              mma_ts(tmem + C_S, ka + 64, qa, ID_S, 1);
             }
           }
           mma_commit(&qk_bar);
@@ -500,13 +503,12 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         if (*(volatile int*)&abort_sh) break;
         fence_after();
         uint64_t va = sdesc(sbase + SM::V, 2048, 128), pa = sdesc(sbase + SM::P(N), N * 16, 128);
+        const uint32_t id = raw ? ID_O | RAW_TYPE : ID_O;
 #pragma unroll 4
         for (int ks = 0; ks < TILE / 16; ++ks, va += 256, pa += 2 * N) {
-          mma_ss(tmem + C_O, va, pa, ID_O, it > it0 || ks > 0);
-          if (F32) {
-            mma_ss(tmem + C_O, va + LO_V, pa, ID_O, 1);
-            mma_ss(tmem + C_O, va, pa + LO_P, ID_O, 1);
-          }
+          mma_ss(tmem + C_O, va, pa, id, it > it0 || ks > 0);
+          mma_ss(tmem + C_O, va + LO_V, pa, id, 1);
+          mma_ss(tmem + C_O, va, pa + LO_P, id, 1);
         }
         mma_commit(&pv_bar);
       }
@@ -537,12 +539,14 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
     if (tid < N) mref[tid] = NO_REF;
     cp_wait();
     part_sync(1, WORKERS);
-    // ---- queries in base-2 units, for records rotated and balanced
+    // ---- queries in base-2 units, for records rotated and balanced (a bf16 cache's for raw positions as they are: the
+    // logits are scaled instead)
+    constexpr float raw_q = F32 ? LOGIT_SCALE : 1.f, raw_logit = F32 ? 1.f : LOGIT_SCALE;
     {
       float f[4];  // of this lane's channels
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[e] = raw ? LOGIT_SCALE : C_WHT * LOGIT_SCALE;
+        f[e] = raw ? raw_q : C_WHT * LOGIT_SCALE;
         if (a.sinkhorn && !raw) f[e] *= __half2float(a.p.sigk[((size_t)layer * a.Hkv + h) * D + 4 * lane + e]);
       }
 #pragma unroll 1
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[i][e] *= f[e];
-          if (r1 + i * WARPS < N) put_q<KF, F32>(smem + SM::Q, r1 + i * WARPS, N, N * C::KD * 2, y[i], lane);
+          if (r1 + i * WARPS < N) put_q<KF>(smem + SM::Q, r1 + i * WARPS, N, N * C::KD * 2, y[i], !F32 && raw, lane);
         }
       }
     }
@@ -612,12 +616,12 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = __ldg(a.p.qjl_t + (8 * kg + e) * D + i);
         uint4 o, l;
-        split2(s[0], s[1], o.x, l.x);
-        split2(s[2], s[3], o.y, l.y);
-        split2(s[4], s[5], o.z, l.z);
-        split2(s[6], s[7], o.w, l.w);
+        tc::split2(s[0], s[1], o.x, l.x);
+        tc::split2(s[2], s[3], o.y, l.y);
+        tc::split2(s[4], s[5], o.z, l.z);
+        tc::split2(s[6], s[7], o.w, l.w);
         *reinterpret_cast<uint4*>(smem + SM::V + km_off(i, 8 * kg, D)) = o;
-        if (F32) *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + km_off(i, 8 * kg, D)) = l;
+        *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + km_off(i, 8 * kg, D)) = l;
       }
       fence_async_smem();
       k_done();
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         for (int e = 0; e < CH; ++e) {
           uint8_t* dst = smem + SM::Q + km_off(col0 + c + e, D + i, N);
           *reinterpret_cast<__half*>(dst) = __float2half_rn(x[e]);
-          if (F32) *reinterpret_cast<__half*>(dst + N * C::KD * 2) = __float2half_rn(lo_part(x[e]));
+          *reinterpret_cast<__half*>(dst + N * C::KD * 2) = __float2half_rn(lo_part(x[e]));
         }
       }
     }
@@ -669,19 +673,19 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
           }
         }
         if (!key || KF == KVQ_Q4G32) {  // 0 4 1 5 2 6 3 7
-          split2(f0.x, f1.x, o.x, l.x);
-          split2(f0.y, f1.y, o.y, l.y);
-          split2(f0.z, f1.z, o.z, l.z);
-          split2(f0.w, f1.w, o.w, l.w);
+          split2(!F32, f0.x, f1.x, o.x, l.x);
+          split2(!F32, f0.y, f1.y, o.y, l.y);
+          split2(!F32, f0.z, f1.z, o.z, l.z);
+          split2(!F32, f0.w, f1.w, o.w, l.w);
         } else {
-          split2(f0.x, f0.y, o.x, l.x);
-          split2(f0.z, f0.w, o.y, l.y);
-          split2(f1.x, f1.y, o.z, l.z);
-          split2(f1.z, f1.w, o.w, l.w);
+          split2(!F32, f0.x, f0.y, o.x, l.x);
+          split2(!F32, f0.z, f0.w, o.y, l.y);
+          split2(!F32, f1.x, f1.y, o.z, l.z);
+          split2(!F32, f1.z, f1.w, o.w, l.w);
         }
       };
       // ---- keys (the previous tile's logits are done: its softmax has read them)
-      float nn = 1.f;  // TQ3: norm of this thread's position
+      float nn = raw ? raw_logit : 1.f;  // TQ3: norm of this thread's position
       bool valid = true;
       const uint8_t* rec_sh = smem + SM::R(N);
       if (!raw) {
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         if (!valid && it * TILE + (ln.t & 64) < qend && (tid & 63) == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
         page = page_of(it + 1, ln.t & 64);
         wait(&kr_bar, kr_phase);
-        put_k<KF, F32, P>(lane_addr, ln, rec_sh, cent);
+        put_k<KF, P>(lane_addr, ln, rec_sh, cent);
         if (TQ) nn = __half2float(reinterpret_cast<const __half*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN)[ln.t & 31]);
       } else {
         const void* row = raw_row(0);
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
           uint4 o, l;
           raw_group(row, kg, true, o, l);
           tm_st4(lane_addr + 4 * kg, o);
-          if (F32) tm_st4(lane_addr + C::KD / 2 + 4 * kg, l);
+          tm_st4(lane_addr + C::KD / 2 + 4 * kg, l);
         }
       }
       k_done();
@@ -707,7 +711,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
       wait_pv();
       if (!raw) {
         wait(&vr_bar, vr_phase);
-        put_v<KF, F32, P>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
+        put_v<KF, P>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
         vpage = page_of(it + 1, ln.vp & 32);
       } else {
         const void* row = raw_row(1);
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
           uint4 o, l;
           raw_group(row, kg, false, o, l);
           *reinterpret_cast<uint4*>(smem + SM::V + mm_off(8 * kg, ln.t)) = o;
-          if (F32) *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + mm_off(8 * kg, ln.t)) = l;
+          *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + mm_off(8 * kg, ln.t)) = l;
         }
       }
       __syncwarp();
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
         tm_wait_ld();
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          x[i] = TQ ? fmaf(xs[i], nn, -ref[i]) : xs[i] - ref[i];
+          x[i] = fmaf(xs[i], nn, -ref[i]);
         }
         if (!all) {
 #pragma unroll
@@ -812,19 +816,19 @@ __global__ void __launch_bounds__(128 * P + 32, F32 || P == 4 ? 1 : 2) tree_kern
           logits(c, x, ref);
           if (c + CH < NC) request(c + CH);
           uint32_t ph[CH / 2], pl[CH / 2];
+          float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < CH; ++i) x[i] = ex2(x[i]);
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            if (F32) split2(x[2 * i], x[2 * i + 1], ph[i], pl[i]);
-            else ph[i] = h2u(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+          for (int i = 0; i < CH; ++i) {
+            x[i] = ex2(x[i]);
+            top = fmaxf(top, x[i]);
           }
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) split2(!F32 && raw, x[2 * i], x[2 * i + 1], ph[i], pl[i]);
           uint8_t* dst = smem + SM::P(N) + mn_off(col0 + c, ln.t, N);
           *reinterpret_cast<uint4*>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          if (F32) *reinterpret_cast<uint4*>(dst + N * TILE * 2) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-          const __half2 top = __hmax2(__hmax2(u2h(ph[0]), u2h(ph[1])), __hmax2(u2h(ph[2]), u2h(ph[3])));
+          *reinterpret_cast<uint4*>(dst + N * TILE * 2) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
           // a weight over 2^8 (infinity among them) waits for a higher reference
-          if (__any_sync(FULL, __hgt(__hmax(__low2half(top), __high2half(top)), __ushort_as_half(0x5C00)))) {
+          if (__any_sync(FULL, top > 256.f)) {
             over = true;
           } else if (!((summed >> (c / CH)) & 1)) {
             summed |= 1u << (c / CH);
@@ -1011,19 +1015,16 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
 
 // ------------------------------------------------------------------ host
 // sizes of a call, and its records in scratch (which may be null: sizes only); returns the scratch bytes
-template <int KF, bool F32>
+template <int KF>
 size_t make_plan(const MultiArgs& a, int sms, Plan* p) {
   const int rows = a.n * a.g;
   p->a = a;
-  // up to 64 rows: one block, two CTAs an SM (at most 101 KB of shared memory and 256 tensor-memory columns each); more:
-  // blocks of up to 128, one CTA an SM, which dequantise a tile once where blocks of 64 do it twice (128 rows over 8 x
-  // 32K TQ3 250 us against 323, 192 rows over 4 x 9001 Q8 96 against 104); float caches' hi and lo parts fit 64
-  const bool wide = !F32 && rows > MAX_ROWS;
-  const int most = wide ? WIDE_ROWS : MAX_ROWS, step = wide ? 32 : 16;
+  const bool few = rows <= FEW_ROWS;
+  const int most = few ? FEW_ROWS : KF == KVQ_TQ3_QJL ? TQ_ROWS : MAX_ROWS, step = few ? 16 : 32;
   p->rb = (rows + most - 1) / most;
   p->N = ((rows + p->rb - 1) / p->rb + step - 1) / step * step;
   p->n_units = a.n_layers_call * a.batch * a.Hkv * p->rb;
-  p->G = sms * (F32 || wide ? 1 : 2);
+  p->G = sms * (few ? 2 : 1);
   p->records = reinterpret_cast<float*>(a.scratch);
   return (size_t)(2 * p->n_units + p->G) * (2 * p->N + D * p->N) * 4;
 }
@@ -1031,19 +1032,17 @@ size_t make_plan(const MultiArgs& a, int sms, Plan* p) {
 template <int KF, bool F32>
 cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
   Plan p;
-  make_plan<KF, F32>(a, sms, &p);
+  make_plan<KF>(a, sms, &p);
   const long long out_rows = (long long)(p.n_units / p.rb) * a.n * a.g;
   if (out_rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t pre = (size_t)(2 * a.batch + 1) * 4, smem = Smem<KF, F32>::total(p.N) + pre;
+  const size_t pre = (size_t)(2 * a.batch + 1) * 4, smem = Smem<KF>::total(p.N) + pre;
   const dim3 grid((unsigned)p.G);
   cudaError_t e = cudaErrorInvalidValue;
   if (p.N == 16) e = go<tree_kernel<KF, 8, F32, 2>>(grid, 288, smem, false, s, p);
-  if (p.N == 32) e = go<tree_kernel<KF, 16, F32, 2>>(grid, 288, smem, false, s, p);
-  if (p.N == 48) e = go<tree_kernel<KF, 24, F32, 2>>(grid, 288, smem, false, s, p);
-  if (p.N == 64 && (F32 || a.n * a.g <= MAX_ROWS)) e = go<tree_kernel<KF, 32, F32, 2>>(grid, 288, smem, false, s, p);
-  if constexpr (!F32) {
+  if (p.N == 32) e = go<tree_kernel<KF, 8, F32, 4>>(grid, 544, smem, false, s, p);
+  if (p.N == 64) e = go<tree_kernel<KF, 16, F32, 4>>(grid, 544, smem, false, s, p);
+  if constexpr (KF != KVQ_TQ3_QJL) {
     if (p.N == 96) e = go<tree_kernel<KF, 24, F32, 4>>(grid, 544, smem, false, s, p);
-    if (p.N == 128) e = go<tree_kernel<KF, 32, F32, 4>>(grid, 544, smem, false, s, p);
   }
   if (e != cudaSuccess) return e;
   // many records a row (few units over all CTAs): a CTA per row, else a warp per row

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
             *reinterpret_cast<uint32_t*>(dst + q_plane) = lo2;
           }
         } else {
-          put4<Q4, true>(img + km_off(lr % N, 4 * lane & ~7, N) + 8 * (lane & 1), q_plane, y[i], lane);
+          put4<Q4>(img + km_off(lr % N, 4 * lane & ~7, N) + 8 * (lane & 1), q_plane, y[i], lane);
         }
         if (Q4) {
           float s = (y[i][0] + y[i][1]) + (y[i][2] + y[i][3]);
