@@ -32,7 +32,7 @@
 // pairs hold 22 bits of records; once-rounded fp16 operands took 18.5, 48, 250 and 96 us for the cases above, but their
 // errors, up to 1.3e-3 of the largest output where attention is peaked, came on top of the output's rounding.  Raw vectors
 // of a bf16 cache are bf16 pairs, which hold 16 bits of any magnitude (its queries one, exactly); a float cache's are fp16
-// pairs.  TQ3 keys are [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w =
+// pairs, the values scaled.  TQ3 keys are [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w =
 // sqrt(pi/2)/128 gamma is a pair, and the thread that owns the position multiplies by the norm n.
 #pragma once
 
@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   // (by the threads' groups of columns)
   __shared__ uint32_t shallow[P][KVQ_MAX_TREE], below[P][KVQ_MAX_TREE];
   __shared__ int par[KVQ_MAX_TREE];
+  __shared__ int vtop;  // float caches: largest raw value of the part, as an integer
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem + SM::total(N));
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
     if (masked && tid < a.n) par[tid] = a.parents[(size_t)b * a.n + tid];
     int page = page_of(it0, ln.t & 64), vpage = page_of(it0, ln.vp & 32);
     if (tid < N) mref[tid] = NO_REF;
+    if (F32 && tid == 0) vtop = 0;
     cp_wait();
     part_sync(1, WORKERS);
     // ---- queries in base-2 units, for records rotated and balanced (a bf16 cache's for raw positions as they are: the
@@ -640,6 +642,40 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         }
       }
     }
+    // raw vector of place x in the list of ring positions and drafts (null: none; nodes that are not there may hold anything)
+    const auto raw_row = [&](int x, int kv) -> const void* {
+      if (x < nring)
+        return (kv ? a.p.ringv : a.p.ringk) +
+               ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (unsigned)(L - nring + x) % (unsigned)a.W) * D;
+      if (x < nraw && nodes[x - nring])
+        return static_cast<const uint8_t*>(kv ? a.v : a.k) + ((((size_t)ll * a.batch + b) * a.Hkv + h) * a.n + x - nring) * D * ESZ;
+      return nullptr;
+    };
+    // A float cache's raw values go into fp16 pairs scaled by a power of two that brings the part's largest to 2^14..2^15:
+    // its output keeps 22 bits whatever their size (below 2^-14 fp16 would lose them).  bf16 pairs need no scale.
+    float v_scale = 1.f, v_unscale = 1.f;
+    if (F32 && raw) {
+      float top = 0.f;
+#pragma unroll 1
+      for (int x = (it0 - nq) * TILE + ln.t; x < min(nraw, (it1 - nq) * TILE); x += TILE) {
+        const float4* row = static_cast<const float4*>(raw_row(x, 1));
+        if (row == nullptr) continue;
+#pragma unroll
+        for (int i = 0; i < 32 / P; ++i) {
+          const float4 f = row[32 / P * ln.hf + i];
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+        }
+      }
+      const int most = __reduce_max_sync(FULL, __float_as_int(top));  // (not negative: ordered as integers)
+      if (lane == 0) atomicMax(&vtop, most);
+      part_sync(1, WORKERS);
+      // exponents of 2^-98 and less are taken as 2^-98
+      const int e = max(vtop >> 23, 127 - 98);
+      if (e < 255) {
+        v_scale = __int_as_float((127 + 14 - (e - 127)) << 23);
+        v_unscale = __int_as_float((127 - 14 + (e - 127)) << 23);
+      }
+    }
     fence_async_smem();
     part_sync(1, WORKERS);  // the columns' masks and references
     float l[NC];
@@ -647,18 +683,9 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
 
     for (int it = it0; it < it1; ++it) {
-      // raw tiles: this thread's position in the list of ring positions and drafts, its vector (null: none; nodes that are
-      // not there may hold anything) and the vector's eight channels of a group in nibble order
-      const int x = (it - nq) * TILE + ln.t;
-      const auto raw_row = [&](int kv) -> const void* {
-        if (x < nring)
-          return (kv ? a.p.ringv : a.p.ringk) +
-                 ((((size_t)layer * a.max_batch + b) * a.Hkv + h) * a.W + (unsigned)(L - nring + x) % (unsigned)a.W) * D;
-        if (x < nraw && nodes[x - nring])
-          return static_cast<const uint8_t*>(kv ? a.v : a.k) + ((((size_t)ll * a.batch + b) * a.Hkv + h) * a.n + x - nring) * D * ESZ;
-        return nullptr;
-      };
-      const auto raw_group = [&](const void* row, int kg, bool key, uint4& o, uint4& l) {
+      const int x = (it - nq) * TILE + ln.t;  // raw tiles: this thread's position in the list of ring positions and drafts
+      // the eight channels of a group in nibble order, values times `scale`
+      const auto raw_group = [&](const void* row, int kg, bool key, float scale, uint4& o, uint4& l) {
         float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
         if (row) {
           const bool bf = !F32 && x >= nring;
@@ -671,6 +698,10 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
             f0 = load4_in(row, 8 * kg, bf);
             f1 = load4_in(row, 8 * kg + 4, bf);
           }
+        }
+        if (F32 && !key) {
+          f0.x *= scale, f0.y *= scale, f0.z *= scale, f0.w *= scale;
+          f1.x *= scale, f1.y *= scale, f1.z *= scale, f1.w *= scale;
         }
         if (!key || KF == KVQ_Q4G32) {  // 0 4 1 5 2 6 3 7
           split2(!F32, f0.x, f1.x, o.x, l.x);
@@ -696,12 +727,12 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         put_k<KF, P>(lane_addr, ln, rec_sh, cent);
         if (TQ) nn = __half2float(reinterpret_cast<const __half*>(rec_sh + (ln.t >> 5) * Rec<KF>::KH + Rec<KF>::K_MAIN)[ln.t & 31]);
       } else {
-        const void* row = raw_row(0);
+        const void* row = raw_row(x, 0);
 #pragma unroll 4
         for (int i = 0; i < 16 / P; ++i) {
           const int kg = 16 / P * ln.hf + i;
           uint4 o, l;
-          raw_group(row, kg, true, o, l);
+          raw_group(row, kg, true, 1.f, o, l);
           tm_st4(lane_addr + 4 * kg, o);
           tm_st4(lane_addr + C::KD / 2 + 4 * kg, l);
         }
@@ -714,12 +745,12 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         put_v<KF, P>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
         vpage = page_of(it + 1, ln.vp & 32);
       } else {
-        const void* row = raw_row(1);
+        const void* row = raw_row(x, 1);
 #pragma unroll 4
         for (int i = 0; i < 16 / P; ++i) {
           const int kg = 16 / P * ln.hf + i;
           uint4 o, l;
-          raw_group(row, kg, false, o, l);
+          raw_group(row, kg, false, v_scale, o, l);
           *reinterpret_cast<uint4*>(smem + SM::V + mm_off(8 * kg, ln.t)) = o;
           *reinterpret_cast<uint4*>(smem + SM::V + C::PLANE + mm_off(8 * kg, ln.t)) = l;
         }
@@ -873,7 +904,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       tm_ld(lane_addr + C_O + col0 + c, o);
       tm_wait_ld();
 #pragma unroll
-      for (int i = 0; i < CH; ++i) rec[2 * N + (col0 + c + i) * D + ch] = o[i];
+      for (int i = 0; i < CH; ++i) rec[2 * N + (col0 + c + i) * D + ch] = F32 ? o[i] * v_unscale : o[i];
     }
     fence_before();
     part_sync(1, WORKERS);

@@ -47,7 +47,8 @@ def test_outputs_are_the_definition_rounded_once(k_format, in_dtype, n_q, N, L, 
     assert err.max() <= TOL["f32"] * np.abs(want).max(), err.max() / np.abs(want).max()
 
 
-@pytest.mark.parametrize("in_dtype,scale", [("bf16", 2.0 ** -24), ("bf16", 2.0 ** 12)])
+@pytest.mark.parametrize("in_dtype,scale", [("bf16", 2.0 ** -24), ("bf16", 2.0 ** 12), ("f32", 2.0 ** -110),
+                                            ("f32", 2.0 ** -24), ("f32", 2.0 ** -10), ("f32", 2.0 ** 12)])
 def test_raw_values_of_any_size(in_dtype, scale):
     """Values in the ring and the drafts far below and above one: the output scales with them."""
     rng = np.random.default_rng(3)
