@@ -7,7 +7,7 @@
 //   O^T [128 channels x N rows] += V~^T [128 x 128] P^T         (both in shared memory)
 // where K~ and V~ are the dequantised records and Q~ the queries in the records' space (rotated, balanced), or the
 // window's and the drafts' raw vectors and the queries as they are.  The softmax runs in base 2 down a thread's own
-// columns against a reference per row that moves only when a logit passes it by 8 (weights stay below 2^8): no
+// columns against a reference per row that moves only when a logit passes it by 15 (weights stay below 2^15): no
 // exchange between threads but one vote per tile.
 //
 // Two launches:
@@ -53,6 +53,10 @@ constexpr int FEW_ROWS = 16, MAX_ROWS = 96, TQ_ROWS = 64;
 constexpr int RAW_PLACES = 3;
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
+// A reference is put so that the row's largest weight so far is 2^START, and put again when one passes 2^MOST.  Pairs of fp16
+// end at 2^-24: with the first tile's largest at 1 the positions behind an early sink 17 above them lost a third of their
+// weight in sums of 6400 positions (2.4e-3 of the output); at 2^7 what is lost is below 2^-32 of the sink's weight each.
+constexpr float START = 7.f, MOST = 15.f;
 
 // what the launches share: sizes from the host, pointers into the caller's scratch
 struct Plan {
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
           part_sync(1, WORKERS);
           if (tid < N) {
             const float top = fmaxf(fmaxf(wmax[0][tid], wmax[1][tid]), fmaxf(wmax[2][tid], wmax[3][tid]));
-            const float m0 = mref[tid], m1 = top > m0 + 8.f ? top : m0;
+            const float m0 = mref[tid], m1 = top > m0 + MOST ? top - START : m0;
             fac[tid] = ex2(m0 - m1);
             mref[tid] = m1;
           }
@@ -858,8 +862,8 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
           uint8_t* dst = smem + SM::P(N) + mn_off(col0 + c, ln.t, N);
           *reinterpret_cast<uint4*>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
           *reinterpret_cast<uint4*>(dst + N * TILE * 2) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-          // a weight over 2^8 (infinity among them) waits for a higher reference
-          if (__any_sync(FULL, top > 256.f)) {
+          // a weight over 2^MOST (infinity among them) waits for a higher reference
+          if (__any_sync(FULL, top > 32768.f)) {
             over = true;
           } else if (!((summed >> (c / CH)) & 1)) {
             summed |= 1u << (c / CH);
@@ -870,7 +874,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         fence_async_smem();
         fence_before();
         if (tid == 0) leave_sh[it & 1] = *(volatile int*)&abort_sh;
-        // (one raise puts every weight at or below 2^8; only an infinity or NaN is still over it then)
+        // (one raise puts every weight at or below 2^MOST; only an infinity or NaN is still over it then)
         if (!part_or(1, WORKERS, over) || raises >= 0) break;
       }
       if (leave_sh[it & 1]) {  // (read once, before the barrier above: all workers leave together or none does)

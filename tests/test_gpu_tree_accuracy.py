@@ -65,3 +65,36 @@ def test_raw_values_of_any_size(in_dtype, scale):
     want = ref.tree_attention(ora, 0, harness.to_np(k), harness.to_np(v), harness.to_np(q), np.array([100]), parents)
     err = np.abs(got - want) - _half_step(in_dtype, want)
     assert err.max() <= TOL["f32"] * np.abs(want).max(), err.max() / np.abs(want).max()
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gap", [12.0, 16.7, 17.3, 20.0])
+def test_positions_behind_a_sink_keep_their_weight(in_dtype, gap):
+    """The first position's logit is ``gap`` above all others, its value small: the output is the sum of thousands of weights
+    of e^-gap.  160 sequences share the pages, so that a CTA meets the sink and many tiles behind it.  A weight's absolute
+    error is at most 2^-32 of the sink's (below half of e^-gap 2^-2 for each gap here), 6400 of them 1.5e-6 of it; outputs are
+    at least 0.02, so 1e-4 of the largest, within the float bound; bf16 adds its half step."""
+    rng = np.random.default_rng(2)
+    B, L = 160, 6400
+    pages = np.tile(np.arange(L // 64, dtype=np.int32), (B, 1))
+    gpu, _, _ = harness.make_pair(1, 2, 2, B, L, window=0, k_format="q8g32", in_dtype=in_dtype, n_pages=L // 64, block_table=pages)
+    ora = harness.make_pair(1, 2, 2, 1, L, window=0, k_format="q8g32", in_dtype=in_dtype)[1]
+    dt = torch.bfloat16 if in_dtype == "bf16" else torch.float32
+    u = rng.standard_normal(128)
+    u /= np.linalg.norm(u)
+    k, v = rng.standard_normal((1, 2, L, 128)) * 0.05, 1 + 0.3 * rng.standard_normal((1, 2, L, 128))
+    k[:, :, 0] += u * gap
+    v[:, :, 0] = -0.05
+    k, v = (torch.as_tensor(x.astype(np.float32)).to(dt) for x in (k, v))
+    wide = lambda t: t.expand(B, *t.shape[1:]).contiguous()  # noqa: E731
+    pos = np.full(B, -1)
+    pos[0] = 0
+    gpu.append(0, wide(k).cuda(), wide(v).cuda(), _i32(pos))
+    ora.append(0, harness.to_np(k), harness.to_np(v), np.zeros(1, int))
+    q = torch.as_tensor(np.tile(u * 128 ** 0.5, (1, 2, 1, 1)).astype(np.float32)).to(dt)
+    dk = torch.as_tensor((rng.standard_normal((1, 2, 1, 128)) * 0.05).astype(np.float32)).to(dt)
+    dv = torch.ones(1, 2, 1, 128, dtype=dt)
+    got = _tree(gpu, wide(dk), wide(dv), wide(q), [L] * B, [[-1]] * B)
+    want = ref.tree_attention(ora, 0, *(harness.to_np(t) for t in (dk, dv, q)), np.array([L]), np.array([[-1]]))
+    err = np.abs(got - want) - _half_step(in_dtype, want)
+    assert err.max() <= TOL["f32"] * np.abs(want).max(), err.max() / np.abs(want).max()
