@@ -338,7 +338,8 @@ int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, c
  * tokens are always raw.
  *   k, v         device, cfg.in_dtype [L?][batch][n_kv_heads][n_nodes][128]: the drafts' raw keys and values, within
  *                the range that kv_quant_append takes (nodes that are not there may hold anything)
- *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_nodes][128]
+ *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_nodes][128] (that of nodes that are not there may hold
+ *                anything; a query that is not finite spoils its own row of out only)
  *   out          device, cfg.in_dtype, like q: the definition to about 1e-5 of its largest value, rounded once
  *   seq_lens     device int32 [batch]: cached tokens, drafts not counted; 0 is an empty context.  Out of range:
  *                flagged KVQ_DEV_SEQLEN_RANGE, treated as 0

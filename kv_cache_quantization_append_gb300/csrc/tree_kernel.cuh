@@ -862,10 +862,11 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
           uint8_t* dst = smem + SM::P(N) + mn_off(col0 + c, ln.t, N);
           *reinterpret_cast<uint4*>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
           *reinterpret_cast<uint4*>(dst + N * TILE * 2) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-          // a weight over 2^MOST (infinity among them) waits for a higher reference
-          if (__any_sync(FULL, top > 32768.f)) {
-            over = true;
-          } else if (!((summed >> (c / CH)) & 1)) {
+          // A weight over 2^MOST (infinity among them) waits for a higher reference, and the columns taken with it wait too.
+          // What is over it once the references have moved belongs to rows that are not finite: their columns' own affair.
+          const bool high = __any_sync(FULL, top > 32768.f);
+          over = over || high;
+          if ((!high || raises >= 0) && !((summed >> (c / CH)) & 1)) {
             summed |= 1u << (c / CH);
 #pragma unroll
             for (int i = 0; i < CH; ++i) l[c + i] += x[i];

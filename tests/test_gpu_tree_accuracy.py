@@ -98,3 +98,53 @@ def test_positions_behind_a_sink_keep_their_weight(in_dtype, gap):
     want = ref.tree_attention(ora, 0, *(harness.to_np(t) for t in (dk, dv, q)), np.array([L]), np.array([[-1]]))
     err = np.abs(got - want) - _half_step(in_dtype, want)
     assert err.max() <= TOL["f32"] * np.abs(want).max(), err.max() / np.abs(want).max()
+
+
+@pytest.mark.parametrize("k_format", ["q4g32", "q8g32", "tq3_qjl"])
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_queries_of_absent_nodes_touch_no_other_row(k_format, in_dtype):
+    """What the queries of nodes that are not there hold -- finite values whose rotated channels pass fp16's range here and
+    there, infinities, NaN -- leaves the rows beside them as they are, over tiles that every node reads in full."""
+    rng = np.random.default_rng(9)
+    B, L = 120, 900
+    pages = np.tile(np.arange(15, dtype=np.int32), (B, 1))
+    gpu, ora, _ = harness.make_pair(1, 2, 4, B, 960, window=64, k_format=k_format, in_dtype=in_dtype, n_pages=15, block_table=pages)
+    dt = torch.bfloat16 if in_dtype == "bf16" else torch.float32
+    k, v = (torch.as_tensor(rng.standard_normal((B, 2, L, 128)).astype(np.float32)).to(dt) for _ in range(2))
+    pos = np.full(B, -1)
+    pos[0] = 0
+    gpu.append(0, k.cuda(), v.cuda(), _i32(pos))           # (the other sequences read the first one's pages, rings of their own)
+    pos[:] = L - 64
+    gpu.append(0, k[:1, :, L - 64:].expand(B, 2, 64, 128).contiguous().cuda(), v[:1, :, L - 64:].expand(B, 2, 64, 128).contiguous().cuda(), _i32(pos))
+    k, v, q = _drafts(rng, gpu.cfg, B, 7, in_dtype)
+    parents = [[-1, 0, -2, 1, -2, 0, 4]] * B               # 2 and 4 are not there, nor is 4's child
+    gone = [2, 4, 6]
+    q[:, :, gone] = 0
+    base = _tree(gpu, k, v, q, [L] * B, parents)
+    assert np.isfinite(base).all() and (base[:, :, gone] == 0).all()
+    for b in range(B):                                     # from 2^14 to 2^20, then infinities and NaN
+        q[b, :, gone] = torch.as_tensor(rng.standard_normal((4, 3, 128)).astype(np.float32) * 2.0 ** (14 + 6 * b / (B - 4))).to(dt)
+    q[-3, :, gone], q[-2, :, gone], q[-1, :, gone] = float("inf"), float("-inf"), float("nan")
+    got = _tree(gpu, k, v, q, [L] * B, parents)
+    assert [b for b in range(B) if not np.array_equal(got[b], base[b])] == []
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("inf"), 3e38])
+def test_a_query_out_of_range_spoils_its_own_row_only(in_dtype, value):
+    """Nodes whose query holds infinities, or values so large that products with keys above one overflow, in two channels: by
+    the keys' signs their logits are infinities of both signs and NaN.  Every other row is what it is without them."""
+    rng = np.random.default_rng(19)
+    gpu, ora, _ = harness.make_pair(1, 2, 4, 2, 500, in_dtype=in_dtype)
+    lens = [400, 90]
+    _fill(gpu, ora, lens, 400, rng, in_dtype)
+    k, v, q = _drafts(rng, gpu.cfg, 2, 9, in_dtype)
+    k[:, :, 0, 3] = 0
+    parents = np.stack([ref.random_tree(rng, 9, chain=True)] * 2)
+    base = _tree(gpu, k, v, q, lens, parents)
+    q[:, :, 2, 3:5], q[:, 1:3, 5, 3:5] = value, -value
+    got = _tree(gpu, k, v, q, lens, parents)
+    bad = np.zeros((2, 4, 9), bool)
+    bad[:, :, 2] = bad[:, 1:3, 5] = True
+    assert not np.isfinite(got[bad]).all(-1).any()
+    assert np.array_equal(got[~bad], base[~bad])
