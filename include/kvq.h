@@ -337,7 +337,8 @@ int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, c
  * path would: cached positions j <= P - window through their records, the newer ones raw from the ring; drafted
  * tokens are always raw.
  *   k, v         device, cfg.in_dtype [L?][batch][n_kv_heads][n_nodes][128]: the drafts' raw keys and values, within
- *                the range that kv_quant_append takes (nodes that are not there may hold anything)
+ *                the range that kv_quant_append takes (nodes that are not there may hold anything; an infinity or NaN
+ *                among them, or in the ring, makes NaN of the nodes that attend to it and of no other)
  *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_nodes][128] (that of nodes that are not there may hold
  *                anything; a query that is not finite spoils its own row of out only)
  *   out          device, cfg.in_dtype, like q: the definition to about 1e-5 of its largest value, rounded once

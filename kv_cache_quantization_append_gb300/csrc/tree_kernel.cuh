@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   // (by the threads' groups of columns)
   __shared__ uint32_t shallow[P][KVQ_MAX_TREE], below[P][KVQ_MAX_TREE];
   __shared__ int par[KVQ_MAX_TREE];
+  __shared__ bool sick_sh[P][TILE];  // a raw position's values (by the threads that share it) were not all finite
   __shared__ int vtop;  // float caches: largest raw value of the part, as an integer
   const MultiArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -667,7 +668,9 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
 #pragma unroll
         for (int i = 0; i < 32 / P; ++i) {
           const float4 f = row[32 / P * ln.hf + i];
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+          const float v[4] = {fabsf(f.x), fabsf(f.y), fabsf(f.z), fabsf(f.w)};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) top = v[y] < INFINITY ? fmaxf(top, v[y]) : top;
         }
       }
       const int most = __reduce_max_sync(FULL, __float_as_int(top));  // (not negative: ordered as integers)
@@ -675,10 +678,8 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       part_sync(1, WORKERS);
       // exponents of 2^-98 and less are taken as 2^-98
       const int e = max(vtop >> 23, 127 - 98);
-      if (e < 255) {
-        v_scale = __int_as_float((127 + 14 - (e - 127)) << 23);
-        v_unscale = __int_as_float((127 - 14 + (e - 127)) << 23);
-      }
+      v_scale = __int_as_float((127 + 14 - (e - 127)) << 23);
+      v_unscale = __int_as_float((127 - 14 + (e - 127)) << 23);
     }
     fence_async_smem();
     part_sync(1, WORKERS);  // the columns' masks and references
@@ -689,6 +690,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
     for (int it = it0; it < it1; ++it) {
       const int x = (it - nq) * TILE + ln.t;  // raw tiles: this thread's position in the list of ring positions and drafts
       // the eight channels of a group in nibble order, values times `scale`
+      float sick = 0.f;  // not zero once one of them was an infinity or NaN, which then counts as zero here
       const auto raw_group = [&](const void* row, int kg, bool key, float scale, uint4& o, uint4& l) {
         float4 f0 = make_float4(0.f, 0.f, 0.f, 0.f), f1 = f0;
         if (row) {
@@ -701,6 +703,15 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
           } else {
             f0 = load4_in(row, 8 * kg, bf);
             f1 = load4_in(row, 8 * kg + 4, bf);
+          }
+        }
+        if (!key) {
+          float* const f[8] = {&f0.x, &f0.y, &f0.z, &f0.w, &f1.x, &f1.y, &f1.z, &f1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sick = fmaf(*f[i], 0.f, sick);
+          if (sick != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *f[i] = fabsf(*f[i]) < INFINITY ? *f[i] : 0.f;
           }
         }
         if (F32 && !key) {
@@ -761,6 +772,15 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&v_bar);
+      // Zero times such a value would be NaN for the rows that do not attend to it; those that do get a weight of NaN instead.
+      bool spoilt = false;
+      if (raw) {
+        sick_sh[ln.hf][ln.t] = sick != 0.f;
+        if (part_or(1, WORKERS, sick != 0.f)) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) spoilt = spoilt || sick_sh[i][ln.t];
+        }
+      }
       // ---- which of the thread's columns attend to its position: by records a node at depth d reads j <= L + d - W,
       // raw ones the rest, drafts its ancestors and itself
       uint32_t bits = 0xffffffffu;
@@ -777,7 +797,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         }
       }
       constexpr uint32_t ALL = NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1;
-      const bool all = __all_sync(FULL, (bits & ALL) == ALL);
+      const bool all = __all_sync(FULL, (bits & ALL) == ALL && !spoilt);
       // ---- softmax down the thread's columns
       wait(&qk_bar, qk_phase);
       fence_after();
@@ -793,7 +813,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         if (!all) {
 #pragma unroll
           for (int i = 0; i < CH; ++i)
-            if (!((bits >> (c + i)) & 1)) x[i] = -INFINITY;
+            x[i] = !((bits >> (c + i)) & 1) ? -INFINITY : spoilt ? NAN : x[i];
         }
       };
       uint32_t summed = 0;  // by groups of CH columns, warp-uniform: the weights are in the sums

@@ -148,3 +148,35 @@ def test_a_query_out_of_range_spoils_its_own_row_only(in_dtype, value):
     bad[:, :, 2] = bad[:, 1:3, 5] = True
     assert not np.isfinite(got[bad]).all(-1).any()
     assert np.array_equal(got[~bad], base[~bad])
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_values_that_are_not_finite_reach_who_attends_to_them(in_dtype, value):
+    """An infinity or NaN in a draft's value or key: outputs of the node and its descendants are not finite, those of the
+    other branches are what they are without it.  The same in a ring slot that only shallow nodes read raw."""
+    rng = np.random.default_rng(29)
+    gpu, ora, _ = harness.make_pair(1, 2, 6, 2, 500, window=8, in_dtype=in_dtype)
+    lens = np.array([400, 90])
+    _fill(gpu, ora, lens, 400, rng, in_dtype)
+    k, v, q = _drafts(rng, gpu.cfg, 2, 9, in_dtype)
+    parents = np.array([[-1, 0, 0, 1, 1, 2, 3, -1, 7]] * 2)
+    base = _tree(gpu, k, v, q, lens, parents)
+    hit = np.array([i for i in range(9) if 1 in ref.chain_of(parents[0], i)])
+    rest = np.setdiff1d(np.arange(9), hit)
+    v2, k2 = v.clone(), k.clone()
+    v2[:, :, 1, 77] = value
+    k2[:, :, 1, 5] = value
+    for kk, vv in ((k, v2), (k2, v)):
+        got = _tree(gpu, kk, vv, q, lens, parents)
+        assert np.array_equal(got[:, :, rest], base[:, :, rest])
+        assert not np.isfinite(got[:, :, hit]).all(-1).any()
+    # the oldest raw position, L - 7: read raw by nodes at depth 0, through its record by deeper ones
+    at = harness.layout.regions(gpu.cfg, gpu.buffer.numel())["off_ringv"]
+    ring = gpu.buffer[at:at + 2 * 2 * 8 * 128 * 4].view(torch.float32).view(2, 2, 8, 128)
+    for b, L in enumerate(lens):
+        ring[b, :, (int(L) - 7) % 8, 100] = value
+    got = _tree(gpu, k, v, q, lens, parents)
+    shallow = [0, 7]
+    deep = np.setdiff1d(np.arange(9), shallow)
+    assert np.array_equal(got[:, :, deep], base[:, :, deep]) and not np.isfinite(got[:, :, shallow]).all(-1).any()
