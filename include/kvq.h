@@ -58,7 +58,7 @@ enum {
   KVQ_DEV_BAD_PAGE = 1u,       /* block-table entry outside [0, n_pages): the token was skipped */
   KVQ_DEV_POS_RANGE = 2u,      /* pos + n_tokens > max_seq_len: the sequence was skipped */
   KVQ_DEV_SEQLEN_RANGE = 4u,   /* seq_lens[b] < 0 or > max_seq_len: treated as empty */
-  KVQ_DEV_TIMEOUT = 8u,        /* a copy-pipeline wait gave up after ~1 s: output is incomplete */
+  KVQ_DEV_TIMEOUT = 8u,        /* a wait within a kernel gave up (kv_set_wait_limit_ns): output is incomplete */
   KVQ_DEV_BAD_NODE = 16u,      /* a tree node's parent is not an earlier node, or a path entry is no node: skipped */
 };
 
@@ -462,15 +462,18 @@ int kv_split_decode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int
 /* Read and clear the device status word (synchronises ``stream``); *flags gets KVQ_DEV_* bits. */
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream);
 
-/* The stall limit, in nanoseconds, of the decode copy pipeline's producer wait (a producer warp
- * waiting for its consumers to release a stage) for every later kv_decode_attention / _noalloc
- * call of this process: a serving loop can tighten the ~1 s default to detect a stalled decode
- * sooner.  ns must lie in [1, 1e10], else KVQ_ERR_INVALID_ARG and the limit is unchanged.  A
- * producer whose wait runs out stops issuing copies and sets KVQ_DEV_TIMEOUT in the status word
- * (the call's output is then incomplete); its consumers give up on the stages that never come after
- * their own ~1 s limit, and the streaming kernel still waits for every copy it started before its
- * blocks exit.  The prefill and append kernels keep their own ~1 s limits.  Not thread-safe against
- * concurrent decode launches from other host threads. */
+/* The stall limit, in nanoseconds, of every later kv_decode_attention / _noalloc, kv_tree_attention and
+ * kv_attention_weights call of this process: a serving loop can tighten the ~1 s default to detect a stalled call
+ * sooner.  ns must lie in [1, 1e10], else KVQ_ERR_INVALID_ARG and the limit is unchanged.
+ *   decode    the copy pipeline's producer wait (a producer warp waiting for its consumers to release a stage): a
+ *             producer whose wait runs out stops issuing copies and sets KVQ_DEV_TIMEOUT in the status word (the
+ *             call's output is then incomplete); its consumers give up on the stages that never come after their
+ *             own ~1 s limit, and the streaming kernel still waits for every copy it started before its blocks exit
+ *   tree      every wait between the warps of a block.  A block whose wait runs out sets KVQ_DEV_TIMEOUT, waits (up
+ *             to ~1 s) for its copies and products under way and leaves; the rows that it had a part of are NaN
+ *   weights   the same; the units (layer, sequence, kv-head) that it had a part of take no weight from the call:
+ *             their entries are the old ones, times decay or not
+ * The prefill and append kernels keep their own ~1 s limits.  A captured call keeps the limit of its capture. */
 int kv_set_wait_limit_ns(uint64_t ns);
 
 /* Static string for a KVQ_* status code. */

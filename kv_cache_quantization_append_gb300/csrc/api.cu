@@ -171,7 +171,7 @@ static int check_device(const kvq_cache* c) {
   return dev == c->device ? KVQ_OK : KVQ_ERR_INVALID_ARG;
 }
 
-// give-up limit of the decode pipeline's waits (kv_set_wait_limit_ns)
+// give-up limit of the decode pipeline's, the tree's and the weights' waits (kv_set_wait_limit_ns)
 std::atomic<unsigned long long> g_decode_wait_ns{1000000000ull};
 unsigned long long decode_wait_ns() { return g_decode_wait_ns.load(); }
 
@@ -490,6 +490,7 @@ static int multi_args(const kvq_cache* cache, int32_t layer, int32_t batch, int3
   a->in_bf16 = cache->cfg.in_dtype == KVQ_IN_BF16;
   a->max_pages_per_seq = cache->max_pages_per_seq;
   a->max_seq_len = cache->cfg.max_seq_len;
+  a->wait_ns = decode_wait_ns();
   return KVQ_OK;
 }
 

@@ -163,6 +163,7 @@ struct MultiArgs {
   uint8_t* scratch;
   int layer0, n_layers_call, batch, max_batch, Hkv, g, W, n, k_format, sinkhorn, in_bf16;
   int max_pages_per_seq, max_seq_len;
+  unsigned long long wait_ns;  // give-up limit of the waits within a CTA
 };
 size_t tree_scratch_bytes(const MultiArgs& a, int sms);
 cudaError_t launch_tree(const MultiArgs& a, int sms, cudaStream_t s);

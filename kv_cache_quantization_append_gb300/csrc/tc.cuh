@@ -8,7 +8,7 @@
 namespace kvq {
 namespace tc {
 
-constexpr unsigned long long WAIT_NS = 1000000000ull;  // give up a wait after ~1 s
+constexpr unsigned long long LAND_NS = 1000000000ull;  // what is under way when a CTA gives up has ~1 s to land
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
@@ -31,29 +31,50 @@ __device__ __forceinline__ unsigned long long gtimer() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// try_wait that may sleep up to about 20 us for the phase
+// try_wait that may sleep up to about NAP_NS for the phase
+constexpr unsigned NAP_NS = 20000;
 __device__ __forceinline__ bool bar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(NAP_NS)
       : "memory");
   return ok != 0;
 }
-// Bounded wait on a phase; one that gives up flags the status word and the CTA's abort flag, which every
-// thread reads behind the CTA's next barrier
-__device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  if (bar_sleep(bar, parity)) return;
-  const unsigned long long t0 = gtimer();
-  while (!bar_sleep(bar, parity)) {
-    if (*abort_flag) return;
-    if (gtimer() - t0 > WAIT_NS) {
-      atomicOr(status, KVQ_DEV_TIMEOUT);
-      *abort_flag = 1;
-      return;
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A warp's wait on a phase, of at most about `limit` ns (one shorter than a nap asks again and again).  One that gives up
+// flags the status word and the CTA's abort flag, at which every other wait of the CTA gives up too.
+__device__ __forceinline__ void bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                         unsigned long long limit) {
+  const bool nap = limit >= NAP_NS;
+  if (!nap || !bar_sleep(bar, parity)) {
+    const unsigned long long t0 = gtimer();
+    while (nap ? !bar_sleep(bar, parity) : !bar_test(bar, parity)) {
+      if (*abort_flag) break;
+      if (gtimer() - t0 > limit) {
+        atomicOr(status, KVQ_DEV_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
     }
   }
+  __syncwarp();
+}
+// A warp's wait for what it has under way when its CTA gives up
+__device__ __forceinline__ void bar_land(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = gtimer();
+  while (!bar_try(bar, parity) && gtimer() - t0 < LAND_NS) {
+  }
+  __syncwarp();
 }
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");

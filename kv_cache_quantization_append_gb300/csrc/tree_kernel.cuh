@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   uint32_t kr_n = 0, vr_n = 0;  // copies that the ninth warp has begun
   bool pv_pending = false;
   const auto wait = [&](uint64_t* bar, uint32_t& phase) {
-    bar_wait(bar, phase, &abort_sh, a.p.status);
+    bar_wait(bar, phase, &abort_sh, a.p.status, a.wait_ns);
     phase ^= 1;
   };
   const auto wait_pv = [&] {
@@ -384,28 +384,48 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // its lane: position ln.t, channel ln.t
   bool ok = true;
 
-  while (t < t_end && ok) {
-    // ---- the next unit: its sequence, head and row block, and this CTA's tiles of it
-    const int ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
-    const long long in_layer = t - ll * per_layer;
+  // the part that begins at place t: its unit (sequence, head and row block) and this CTA's tiles of it; t goes on behind it
+  struct Part {
+    int ll, b, h, rbi, u, it0, it1, nq, qend;
+    bool raw;
+  };
+  const auto part_at = [&](long long& t) {
+    Part w;
+    w.ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
+    const long long in_layer = t - w.ll * per_layer;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if ((long long)pre[mid] * a.Hkv * p.rb <= in_layer) lo = mid;
       else hi = mid - 1;
     }
-    const int b = lo, tiles = pre[b + 1] - pre[b];
-    const long long r = in_layer - (long long)pre[b] * a.Hkv * p.rb;
+    w.b = lo;
+    const int tiles = pre[lo + 1] - pre[lo];
+    const long long r = in_layer - (long long)pre[lo] * a.Hkv * p.rb;
     const int hr = (int)quick_div(r, tiles), place0 = (int)(r - (long long)hr * tiles);
-    const int h = hr / p.rb, rbi = hr - h * p.rb, layer = a.layer0 + ll;
-    const int u = ((ll * a.batch + b) * a.Hkv + h) * p.rb + rbi;
-    const int L = lens[b], qend = quant_end(L, a.W, a.n), nq = (qend + TILE - 1) / TILE;
+    w.h = hr / p.rb;
+    w.rbi = hr - w.h * p.rb;
+    w.u = ((w.ll * a.batch + lo) * a.Hkv + w.h) * p.rb + w.rbi;
+    w.qend = quant_end(lens[lo], a.W, a.n);
+    w.nq = (w.qend + TILE - 1) / TILE;
     // tiles of records come first, then those of raw positions; a part is of one kind
-    const bool raw = place0 >= nq;
-    const int place1 = (int)min((long long)(raw ? tiles : nq), place0 + (t_end - t));
+    w.raw = place0 >= w.nq;
+    const int place1 = (int)min((long long)(w.raw ? tiles : w.nq), place0 + (t_end - t));
     t += place1 - place0;
-    const int it0 = raw ? nq + (place0 - nq + RAW_PLACES - 1) / RAW_PLACES : place0;
-    const int it1 = raw ? nq + (place1 - nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    w.it0 = w.raw ? w.nq + (place0 - w.nq + RAW_PLACES - 1) / RAW_PLACES : place0;
+    w.it1 = w.raw ? w.nq + (place1 - w.nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    return w;
+  };
+  const auto record_of = [&](const Part& w) { return p.records + (size_t)(2 * w.u + w.raw + blockIdx.x) * (2 * N + D * N); };
+  const auto gave_up = [&] { return *(volatile int*)&abort_sh != 0; };
+  long long t_part = t;
+
+  while (t < t_end && ok) {
+    t_part = t;
+    const Part w = part_at(t);
+    const int ll = w.ll, b = w.b, h = w.h, rbi = w.rbi, layer = a.layer0 + ll, it0 = w.it0, it1 = w.it1, nq = w.nq, qend = w.qend;
+    const int L = lens[b];
+    const bool raw = w.raw;
     if (it0 == it1) continue;  // (the later places of a raw tile that an earlier range has)
 
     const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         // logits: a k-step of 16 channels is 8 columns of K and 32 N bytes of the queries
         if (!raw) phys = page_of(it + 1);
         wait(&k_bar, k_phase);
-        if (*(volatile int*)&abort_sh) break;
+        if (__any_sync(FULL, gave_up())) break;  // (the whole warp)
         fence_after();
         {
           uint64_t qa = sdesc(sbase + SM::Q, N * 16, 128);
@@ -502,11 +522,11 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         }
         if (!raw && it + 1 < it1) copy(phys, true);  // the workers have read this tile's keys
         wait(&v_bar, v_phase);
-        if (*(volatile int*)&abort_sh) break;
+        if (__any_sync(FULL, gave_up())) break;  // (the whole warp)
         if (!raw && it + 1 < it1) copy(phys, false);
         // O += V^T P: a k-step of 16 positions is 4096 bytes of V and 32 N of P
         wait(&p_bar, p_phase);
-        if (*(volatile int*)&abort_sh) break;
+        if (__any_sync(FULL, gave_up())) break;  // (the whole warp)
         fence_after();
         uint64_t va = sdesc(sbase + SM::V, 2048, 128), pa = sdesc(sbase + SM::P(N), N * 16, 128);
         const uint32_t id = raw ? ID_O | RAW_TYPE : ID_O;
@@ -518,7 +538,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         }
         mma_commit(&pv_bar);
       }
-      ok = !*(volatile int*)&abort_sh;
+      ok = !__any_sync(FULL, gave_up());
       continue;
     }
 
@@ -894,7 +914,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         }
         fence_async_smem();
         fence_before();
-        if (tid == 0) leave_sh[it & 1] = *(volatile int*)&abort_sh;
+        if (tid == 0) leave_sh[it & 1] = gave_up();
         // (one raise puts every weight at or below 2^MOST; only an infinity or NaN is still over it then)
         if (!part_or(1, WORKERS, over) || raises >= 0) break;
       }
@@ -909,7 +929,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
     // ---- the range's part of the unit: reference, sum and O of every row
     wait_pv();
     fence_after();
-    float* rec = p.records + (size_t)(2 * u + raw + blockIdx.x) * (2 * N + D * N);
+    float* rec = record_of(w);
     // sums over the lanes; after three exchanges the lanes of one lane & 7 have NC / 8 columns, by its bits in reverse
     halve<NC / 2, 1>(l, lane);
     halve<NC / 4, 2>(l, lane);
@@ -932,23 +952,33 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       for (int i = 0; i < CH; ++i) rec[2 * N + (col0 + c + i) * D + ch] = F32 ? o[i] * v_unscale : o[i];
     }
     fence_before();
-    part_sync(1, WORKERS);
+    if (part_or(1, WORKERS, gave_up())) {
+      ok = false;
+      break;
+    }
     if (tid < N) {
       rec[tid] = mref[tid];
       rec[N + tid] = wmax[0][tid] + wmax[1][tid] + wmax[2][tid] + wmax[3][tid];
     }
   }
-  // what a CTA that gave up still has under way, copies and products, lands before it leaves; the waits are bounded
-  if (warp == WARPS && !ok) {
-    const auto land = [&](uint64_t* bar, uint32_t parity) {
-      const unsigned long long t0 = gtimer();
-      while (!bar_try(bar, parity) && gtimer() - t0 < WAIT_NS) {
+  // A CTA that gave up leaves sums that are NaN in the records of its part and of those it did not come to (the merge reads
+  // them), and what it still has under way, copies and products, lands before it leaves; the waits are bounded.
+  if (warp < WARPS && !ok) {
+    for (t = t_part; t < t_end;) {
+      const Part w = part_at(t);
+      float* rec = record_of(w);
+      if (w.it0 < w.it1 && tid < N) {
+        rec[tid] = NO_REF;
+        rec[N + tid] = NAN;
       }
-    };
-    if (kr_n) land(&kr_bar, (kr_n - 1) & 1);
-    if (vr_n) land(&vr_bar, (vr_n - 1) & 1);
+    }
+  }
+  __syncthreads();  // (nobody waits any more)
+  if (warp == WARPS && gave_up()) {
+    if (kr_n) bar_land(&kr_bar, (kr_n - 1) & 1);
+    if (vr_n) bar_land(&vr_bar, (vr_n - 1) & 1);
     mma_commit(&end_bar);
-    land(&end_bar, 0);
+    bar_land(&end_bar, 0);
   }
   fence_before();
   __syncthreads();
@@ -1047,7 +1077,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const __gr
     there = there && q >= -1 && q < j;
     j = there ? q : -1;
   }
-  const float inv = there && l > 0.f ? 1.f / l : 0.f;
+  const float inv = there && l != 0.f ? 1.f / l : 0.f;  // (a sum of NaN, where a range gave up too, makes NaN of the row)
   const __half* sig = a.p.sigv + ((size_t)(a.layer0 + ll) * a.Hkv + h) * D + 4 * lane;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

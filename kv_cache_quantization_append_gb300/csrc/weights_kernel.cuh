@@ -166,14 +166,17 @@ __device__ __forceinline__ void put_codes(uint32_t col, const Lane& ln, const ui
   }
 }
 
-// normaliser (base-2 logarithm of the sum) of one row of unit u by a warp: the parts of every range in a fixed order
+// normaliser (base-2 logarithm of the sum) of one row of unit u by a warp: the parts of every range in a fixed order; NaN
+// where one of them gave up
 __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long long first, int nq, int tiles, long long G,
                                             long long total, int lane) {
   const auto owner = [&](long long x) { return (int)quick_div((x + 1) * G - 1, total); };
   const int c0 = owner(first), c1 = nq > 0 ? owner(first + nq - 1) : c0 - 1;
   float m = NO_REF, l = 0.f;
+  bool lost = false;
   const auto add = [&](int kind, int c) {
     const float2 x = *reinterpret_cast<const float2*>(p.parts + ((size_t)(2 * u + kind + c) * p.rows + row) * 2);
+    lost = lost || x.x != x.x;
     const float mn = fmaxf(m, x.x);
     l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
     m = mn;
@@ -195,6 +198,7 @@ __device__ __forceinline__ float normaliser(const Plan& p, int u, int row, long 
     l = lane & o ? b + a : a + b;
     m = mn;
   }
+  if (__any_sync(FULL, lost)) return NAN;
   return l > 0.f ? m + log2f(l) : INFINITY;
 }
 
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
                       __byte_perm(c.z, c.w, 0x7531));
   }
   uint32_t k_n = 0, kr_n = 0, proj_n = 0, job = 0;  // tiles of keys, copies, projections and blocks so far: their phases
-  const auto wait_nth = [&](uint64_t* bar, uint32_t n) { bar_wait(bar, n & 1, &abort_sh, a.p.status); };
+  const auto wait_nth = [&](uint64_t* bar, uint32_t n) { bar_wait(bar, n & 1, &abort_sh, a.p.status, a.wait_ns); };
   const auto k_done = [&] {
     tm_wait_st();
     fence_before();
@@ -283,25 +287,45 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   float* lse = reinterpret_cast<float*>(smem + SM::wm(NR));                   // SUM: the rows' normalisers
   bool ok = true;
 
-  while (t < t_end && ok) {
-    const int ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
-    const long long in_layer = t - ll * per_layer;
+  // the part that begins at place t: its unit (sequence and head) and this CTA's tiles of it; t goes on behind it
+  struct Part {
+    int ll, b, h, u, it0, it1, nq;
+    bool raw;
+  };
+  const auto part_at = [&](long long& t) {
+    Part w;
+    w.ll = a.n_layers_call > 1 ? (int)quick_div(t, per_layer) : 0;
+    const long long in_layer = t - w.ll * per_layer;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if ((long long)pre[mid] * a.Hkv <= in_layer) lo = mid;
       else hi = mid - 1;
     }
-    const int b = lo, tiles = pre[b + 1] - pre[b];
-    const long long r = in_layer - (long long)pre[b] * a.Hkv;
-    const int h = (int)quick_div(r, tiles), place0 = (int)(r - (long long)h * tiles), layer = a.layer0 + ll;
-    const int u = (ll * a.batch + b) * a.Hkv + h;
-    const int L = lens[b], qend = max(0, L - a.W), nq = quant_tiles(L, a.W);
-    const bool raw = place0 >= nq;
-    const int place1 = (int)min((long long)(raw ? tiles : nq), place0 + (t_end - t));
+    w.b = lo;
+    const int tiles = pre[lo + 1] - pre[lo];
+    const long long r = in_layer - (long long)pre[lo] * a.Hkv;
+    w.h = (int)quick_div(r, tiles);
+    const int place0 = (int)(r - (long long)w.h * tiles);
+    w.u = (w.ll * a.batch + lo) * a.Hkv + w.h;
+    w.nq = quant_tiles(lens[lo], a.W);
+    w.raw = place0 >= w.nq;
+    const int place1 = (int)min((long long)(w.raw ? tiles : w.nq), place0 + (t_end - t));
     t += place1 - place0;
-    const int it0 = raw ? nq + (place0 - nq + RAW_PLACES - 1) / RAW_PLACES : place0;
-    const int it1 = raw ? nq + (place1 - nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    w.it0 = w.raw ? w.nq + (place0 - w.nq + RAW_PLACES - 1) / RAW_PLACES : place0;
+    w.it1 = w.raw ? w.nq + (place1 - w.nq + RAW_PLACES - 1) / RAW_PLACES : place1;
+    return w;
+  };
+  const auto part_sums = [&](const Part& w) { return p.parts + (size_t)(2 * w.u + w.raw + blockIdx.x) * p.rows * 2; };
+  const auto gave_up = [&] { return *(volatile int*)&abort_sh != 0; };
+  long long t_part = t;
+
+  while (t < t_end && ok) {
+    t_part = t;
+    const Part w = part_at(t);
+    const int ll = w.ll, b = w.b, h = w.h, layer = a.layer0 + ll, u = w.u, nq = w.nq, it0 = w.it0, it1 = w.it1;
+    const int L = lens[b], qend = max(0, L - a.W);
+    const bool raw = w.raw;
     if (it0 == it1) continue;
     const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
 
@@ -363,7 +387,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       }
       for (int it = it0; it < it1; ++it) {
         k_wait();
-        if (*(volatile int*)&abort_sh) break;
+        if (__any_sync(FULL, gave_up())) break;  // (the whole warp)
         if (!raw && it + C::STAGES < it1) {  // the workers have read this tile's keys
           copy(phys);
           phys = page_of(it + C::STAGES + 1);
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
         for (int rb = 0; rb < p.nb; ++rb, ++job) {
           const int sb = job & 1;
           if (job >= 2) wait_nth(&s_bar[sb], (job - 2) >> 1);
-          if (*(volatile int*)&abort_sh) break;
+          if (__any_sync(FULL, gave_up())) break;
           fence_after();
           uint64_t qa = sdesc(sbase + rb * N * C::KD * 2, N * 16, 128);
           const uint64_t qb = q_plane >> 4;
@@ -400,7 +424,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
           mma_commit(&qk_bar[sb]);
         }
       }
-      ok = !*(volatile int*)&abort_sh;
+      ok = !__any_sync(FULL, gave_up());
       continue;
     }
 
@@ -730,7 +754,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       if (SUM) {
         float(*sums)[TILE] = part_sum[(it - it0) & 1];
         if (warp >= 4) sums[(warp >> 2) - 1][ln.t] = acc;
-        if (part_or(1, WORKERS, *(volatile int*)&abort_sh != 0)) break;  // (all workers or none)
+        if (part_or(1, WORKERS, gave_up())) break;  // (all workers or none)
         if (warp < 4 && mine) {
           float* w = a.weights + (size_t)u * a.max_seq_len + j;
           float v = acc;
@@ -753,13 +777,13 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
       }
     }
     // (with the flag up every wait returns at once: all workers come here, and leave together or not at all)
-    if (part_or(1, WORKERS, *(volatile int*)&abort_sh != 0)) {
+    if (part_or(1, WORKERS, gave_up())) {
       ok = false;
       break;
     }
     if (!SUM) {
       // ---- the range's maxima and sums: the four warps that hold a row's columns, joined in order
-      float* out = p.parts + (size_t)(2 * u + raw + blockIdx.x) * p.rows * 2;
+      float* out = part_sums(w);
       for (int lr = tid; lr < p.rows; lr += WORKERS) {
         const int c = lr % N, wg = FEW ? c / 2 : c / (N / P), at = FEW ? c % 2 : lr / N * (N / P) + c % (N / P);
         const float* m0 = reinterpret_cast<const float*>(smem + SM::wm(NR)) + 4 * wg * (NR / P) + at;
@@ -777,15 +801,21 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
     }
     part_sync(1, WORKERS);  // the next part's queries and sums may come
   }
-  if (warp == WARPS && !ok) {  // what is still under way lands before the CTA leaves; the waits are bounded
-    const auto land = [&](uint64_t* bar, uint32_t parity) {
-      const unsigned long long t0 = gtimer();
-      while (!bar_try(bar, parity) && gtimer() - t0 < WAIT_NS) {
-      }
-    };
-    for (uint32_t i = kr_n < C::STAGES ? 0 : kr_n - C::STAGES; i < kr_n; ++i) land(&kr_bar[i % C::STAGES], i / C::STAGES & 1);
+  // A CTA that gave up leaves maxima that are NaN for its part and those it did not come to: their units take no weight from
+  // the call.  What it still has under way lands before it leaves; the waits are bounded.
+  if (!SUM && warp < WARPS && !ok) {
+    for (t = t_part; t < t_end;) {
+      const Part w = part_at(t);
+      float* out = part_sums(w);
+      if (w.it0 < w.it1)
+        for (int lr = tid; lr < p.rows; lr += WORKERS) out[2 * lr] = NAN;
+    }
+  }
+  __syncthreads();  // (nobody waits any more)
+  if (warp == WARPS && gave_up()) {
+    for (uint32_t i = kr_n < C::STAGES ? 0 : kr_n - C::STAGES; i < kr_n; ++i) bar_land(&kr_bar[i % C::STAGES], i / C::STAGES & 1);
     mma_commit(&end_bar);
-    land(&end_bar, 0);
+    bar_land(&end_bar, 0);
   }
   // (a CTA without tiles too: no kernel ends before the one it follows)
   if (SUM) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -815,7 +845,7 @@ static __global__ void __launch_bounds__(ADD_THREADS) normaliser_kernel(const __
   const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
   const float v = normaliser(p, u, row, ll * per_layer + (long long)pre[b] * a.Hkv + (long long)h * tiles, quant_tiles(L, a.W), tiles,
                              min((long long)p.G, total), total, lane);
-  if (lane == 0) p.norms[i] = v;
+  if (lane == 0) p.norms[i] = v == v ? v : INFINITY;  // (no weight from a row that was given up)
 }
 
 // weights from stored logits: one CTA per 1024 positions of a unit
@@ -850,7 +880,7 @@ static __global__ void __launch_bounds__(ADD_THREADS) weights_add_kernel(const _
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int r = 0; r < STORE_ROWS; ++r)
-    if (r < p.rows) {
+    if (r < p.rows && lse[r] == lse[r]) {  // (a row that was given up has logits that were never written)
       s[0] += ex2(x[r].x - lse[r]);
       s[1] += ex2(x[r].y - lse[r]);
       s[2] += ex2(x[r].z - lse[r]);
