@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kvq.h"
 
 namespace kvq {
@@ -172,6 +174,24 @@ cudaError_t launch_weights(const MultiArgs& a, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__
+// Lets kernel K have as much dynamic shared memory as a block may hold, once per device: the same value whoever sets it, so
+// host threads whose calls need different amounts cannot take it from one another.  (No host call after the first, and none
+// in a stream capture that follows a call outside one.)
+template <auto K>
+cudaError_t allow_shared_memory() {
+  constexpr int DEVICES = 64;
+  static std::atomic<bool> allowed[DEVICES];
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < DEVICES && allowed[dev].load(std::memory_order_relaxed))) return e;
+  cudaFuncAttributes f;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&f, K)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)f.sharedSizeBytes);
+  if (e == cudaSuccess && dev < DEVICES) allowed[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 __device__ __forceinline__ float4 load4_in(const void* base, size_t elem_off, int bf16) {
   if (bf16) {
     const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + elem_off);

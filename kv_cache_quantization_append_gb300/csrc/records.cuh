@@ -2,8 +2,6 @@
 // part of a tile, operand layouts in shared memory, launches.
 #pragma once
 
-#include <atomic>
-
 #include "tc.cuh"
 
 namespace kvq {
@@ -120,21 +118,12 @@ __device__ __forceinline__ void lds32(const uint8_t* at, bool swap, uint4& a, ui
 }
 
 // ------------------------------------------------------------------ launches
-// Launches kernel K, as a programmatic dependent of the kernel before it in the stream or after it.  Its shared-memory
-// limit is set when a device first needs that much.
+// Launches kernel K, as a programmatic dependent of the kernel before it in the stream or after it
 template <auto K, typename... A>
 cudaError_t go(dim3 grid, unsigned threads, size_t smem, bool dependent, cudaStream_t s, A... args) {
-  constexpr int DEVICES = 64;
-  static std::atomic<size_t> limit[DEVICES];
-  cudaError_t e = cudaSuccess;
   if (smem > 32 * 1024) {  // (static shared memory, up to 8 KB of it here, counts towards the 48 KB that need no leave)
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if (dev >= DEVICES || limit[dev].load(std::memory_order_relaxed) < smem) {
-      e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-      if (dev < DEVICES) limit[dev].store(smem, std::memory_order_relaxed);
-    }
+    const cudaError_t e = allow_shared_memory<K>();
+    if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
