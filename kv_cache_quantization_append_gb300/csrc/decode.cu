@@ -26,7 +26,6 @@
 //    query head's records in a fixed order (deterministic), undoes the rotation of the quantised
 //    part and combines it with the window part.  No inter-CTA flags, fences or atomics inside the
 //    streaming kernel.
-#include <atomic>
 #include <cfloat>
 
 #include "kvq_internal.cuh"
@@ -1614,28 +1613,11 @@ size_t decode_record_slots(int n_units, int n_ctas, int k_format) {
   return (size_t)n_units + (size_t)n_ctas * decode_consumer_warps(k_format);
 }
 
-// largest dynamic shared-memory size granted so far to decode_kernel<KF>, per device: the attribute
-// is set again only when a call needs more (no host call per launch, none during stream capture
-// once a call of the same or a larger batch has run)
-constexpr int MAX_DEVICES = 64;
-template <int KF>
-std::atomic<int> g_smem_granted[MAX_DEVICES];
-
 template <int KF>
 static cudaError_t launch_kf(const DecodeArgs& a, cudaStream_t s) {
   const size_t smem = Geo<KF>::SM_SEQ + 6 * (size_t)(a.batch + 1) * sizeof(int);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_shared_memory<decode_kernel<KF>>();
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= MAX_DEVICES || g_smem_granted<KF>[dev].load() < (int)smem) {
-    e = cudaFuncSetAttribute(decode_kernel<KF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < MAX_DEVICES) {
-      int cur = g_smem_granted<KF>[dev].load();
-      while (cur < (int)smem && !g_smem_granted<KF>[dev].compare_exchange_weak(cur, (int)smem)) {
-      }
-    }
-  }
   // programmatic dependent launch: the CTAs may be launched while the previous kernel of the
   // stream (typically the append of the step's new tokens) is finishing; each waits for it
   // (griddepcontrol.wait) before reading anything

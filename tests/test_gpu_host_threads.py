@@ -57,7 +57,7 @@ assert not errors, (len(errors), errors[:3])
 """
 
 
-@pytest.mark.parametrize("which", ["tree"])
+@pytest.mark.parametrize("which", ["tree", "decode"])
 def test_two_threads_grow_the_shared_memory(which):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     for _ in range(3):
