@@ -18,7 +18,12 @@ from .lib import (KVQ_IN_BF16, KVQ_IN_F32, KVQ_Q4G32, KVQ_Q8G32, KVQ_TQ3_QJL, kv
 
 
 class QuantKVCache:
-    """Device buffers of one cache, allocated with torch; all work runs in libkvq's kernels."""
+    """Device buffers of one cache, allocated with torch; all work runs in libkvq's kernels.
+
+    Calls may run on several streams at once: what an operation needs besides its arguments is kept per operation and
+    stream, one buffer that grows to the largest call so far.  A captured call takes memory of its graph's own, so that
+    graphs may be replayed at the same time as each other and as calls.
+    """
 
     def __init__(self, cfg: lib.kvq_config, device="cuda", block_table: torch.Tensor | None = None,
                  qjl_proj=None):
@@ -29,31 +34,49 @@ class QuantKVCache:
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.block_table = block_table
         self.handle = kv_cache_init(cfg, self.buffer, block_table, qjl_proj)
-        self._scratch = {}
+        self._work = {}    # (operation, stream) -> its buffer
+        self._needs = {}   # (operation, sizes) -> bytes
 
-    def scratch(self, layer: int, batch: int) -> torch.Tensor:
-        """Decode scratch (uninitialised), kept per (layer-mode, batch) and reused across calls."""
-        key = (layer == -1, batch)
-        need = kv_decode_scratch_bytes(self.handle, layer, batch)
-        t = self._scratch.get(key)
+    def _workspace(self, op: str, size, sizes: tuple, stream=None) -> torch.Tensor:
+        """Uninitialised bytes for one call of ``op`` on ``stream``, at least size(handle, *sizes) (the layer first)."""
+        key = (op, sizes[0] == -1) + sizes[1:]
+        need = self._needs.get(key)
+        if need is None:
+            need = max(1, size(self.handle, *sizes))  # (no size: the call itself will be refused)
+            self._needs[key] = need
+        if stream is None:
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
+            raw = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        else:
+            with torch.cuda.stream(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    return torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
+            raw = stream.cuda_stream
+        t = self._work.get((op, raw))
         if t is None or t.numel() < need:
-            t = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
-            self._scratch[key] = t
+            # allocated on the stream it is used on, so that the buffer it replaces is not handed out before its calls end
+            with torch.cuda.stream(stream):
+                t = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
+            self._work[op, raw] = t
         return t
+
+    def scratch(self, layer: int, batch: int, stream=None) -> torch.Tensor:
+        """Decode scratch (uninitialised) for calls on ``stream`` (the current one), kept and reused by them."""
+        return self._workspace("decode", kv_decode_scratch_bytes, (layer, batch), stream)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, stream=None):
         kv_quant_append(self.handle, layer, k, v, pos, stream)
 
     def calibrate(self, layer: int, k_calib: torch.Tensor, v_calib: torch.Tensor, stream=None):
-        need = kv_calibrate_scratch_bytes(self.handle, layer, k_calib.shape[-2])
-        work = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
+        work = self._workspace("calibrate", kv_calibrate_scratch_bytes, (layer, k_calib.shape[-2]), stream)
         kv_calibrate(self.handle, layer, k_calib, v_calib, work, stream)
 
     def decode(self, layer: int, q: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
         if out is None:
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        kv_decode_attention(self.handle, layer, q, out, seq_lens, self.scratch(layer, q.shape[-3]), stream)
+        kv_decode_attention(self.handle, layer, q, out, seq_lens, self.scratch(layer, q.shape[-3], stream), stream)
         return out
 
     def prefill(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, pos: torch.Tensor,
@@ -61,30 +84,16 @@ class QuantKVCache:
         """Append the chunk (k, v at pos) and return its queries' attention [L?][B][Hq][T][128]."""
         if out is None:
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        need = lib.kv_prefill_scratch_bytes(self.handle, layer, q.shape[-4])
-        key = ("prefill", layer == -1, q.shape[-4])
-        t = self._scratch.get(key)
-        if t is None or t.numel() < need:
-            t = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
-            self._scratch[key] = t
+        t = self._workspace("prefill", lib.kv_prefill_scratch_bytes, (layer, q.shape[-4]), stream)
         lib.kv_prefill_attention(self.handle, layer, k, v, q, out, pos, t, stream)
         return out
-
-    def _kept_scratch(self, key: tuple, size, *args) -> torch.Tensor:
-        """Scratch of size(handle, *args) bytes (at least one), kept per key and reused across calls."""
-        t = self._scratch.get(key)
-        if t is None:
-            t = torch.empty(max(1, size(self.handle, *args)), dtype=torch.uint8, device=self.buffer.device)
-            self._scratch[key] = t
-        return t
 
     def tree_decode(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor,
                     parents: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of a tree of drafted tokens (k, v, q; parents [B][N]) over the cache: [L?][B][Hq][N][128]."""
         if out is None:
             out = torch.empty_like(q)
-        key = ("tree", layer == -1, q.shape[-4], q.shape[-2])
-        scratch = self._kept_scratch(key, lib.kv_tree_scratch_bytes, layer, q.shape[-4], q.shape[-2])
+        scratch = self._workspace("tree", lib.kv_tree_scratch_bytes, (layer, q.shape[-4], q.shape[-2]), stream)
         lib.kv_tree_attention(self.handle, layer, k, v, q, out, seq_lens, parents, scratch, stream)
         return out
 
@@ -96,8 +105,7 @@ class QuantKVCache:
     def attention_weights(self, layer: int, q: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
                           decay: float = 1.0, stream=None) -> torch.Tensor:
         """Add the attention weight that cached positions receive from the newest tokens' queries to ``weights``."""
-        key = ("weights", layer == -1, q.shape[-4], q.shape[-2])
-        scratch = self._kept_scratch(key, lib.kv_weights_scratch_bytes, layer, q.shape[-4], q.shape[-2])
+        scratch = self._workspace("weights", lib.kv_weights_scratch_bytes, (layer, q.shape[-4], q.shape[-2]), stream)
         lib.kv_attention_weights(self.handle, layer, q, weights, decay, seq_lens, scratch, stream)
         return weights
 
