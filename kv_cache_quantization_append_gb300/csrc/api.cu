@@ -142,8 +142,6 @@ static void build_codebook(CodebookDev* cb) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-static int cuda_err(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
-
 static int check_cache(const kvq_cache* c, Layout* L) {
   if (!c) return KVQ_ERR_INVALID_ARG;
   if (c->magic != MAGIC) return KVQ_ERR_NOT_INIT;
@@ -167,7 +165,7 @@ static int layers_of_call(const kvq_cache* c, int32_t layer, int* l0, int* nl) {
 // another device current would hand that device foreign addresses, so such calls are refused.
 static int check_device(const kvq_cache* c) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (call_status(cudaGetDevice(&dev)) != KVQ_OK) return KVQ_ERR_CUDA;
   return dev == c->device ? KVQ_OK : KVQ_ERR_INVALID_ARG;
 }
 
@@ -177,8 +175,7 @@ unsigned long long decode_wait_ns() { return g_decode_wait_ns.load(); }
 
 int decode_ctas(int device) {
   int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
-  return sms;
+  return call_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) == KVQ_OK ? sms : 0;
 }
 
 }  // namespace kvq
@@ -204,7 +201,7 @@ int kv_cache_init(kvq_cache* cache, const kvq_config* cfg, void* dev_mem, size_t
   if (cfg->k_format == KVQ_TQ3_QJL && !qjl_proj_host) return KVQ_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (call_status(cudaGetDevice(&dev)) != KVQ_OK) return KVQ_ERR_CUDA;
 
   // header image on the host, copied in one piece
   const size_t hdr = L.off_ringk;
@@ -224,7 +221,7 @@ int kv_cache_init(kvq_cache* cache, const kvq_config* cfg, void* dev_mem, size_t
   for (long long i = 0; i < (long long)cfg->max_batch * L.max_pages_per_seq; ++i) bt[i] = (int32_t)i;
   cudaError_t e = cudaMemcpyAsync(dev_mem, h.data(), hdr, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  if (call_status(e) != KVQ_OK) return KVQ_ERR_CUDA;
 
   std::memset(cache, 0, sizeof(*cache));
   cache->cfg = *cfg;
@@ -269,7 +266,7 @@ int kv_calibrate(kvq_cache* cache, int32_t layer, const void* k_calib, const voi
   a.Hkv = cache->cfg.n_kv_heads;
   a.ntok = n_tokens;
   a.in_bf16 = cache->cfg.in_dtype == KVQ_IN_BF16;
-  return cuda_err(launch_calibrate(a, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_calibrate(a, static_cast<cudaStream_t>(stream)));
 }
 
 int kv_quant_append(kvq_cache* cache, int32_t layer, const void* k, const void* v,
@@ -301,7 +298,7 @@ int kv_quant_append(kvq_cache* cache, int32_t layer, const void* k, const void* 
   a.sinkhorn = cache->cfg.sinkhorn;
   a.in_bf16 = cache->cfg.in_dtype == KVQ_IN_BF16;
   a.max_batch = cache->cfg.max_batch;
-  return cuda_err(launch_append(a, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kv_decode_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch) {
@@ -356,7 +353,7 @@ int kv_decode_attention(kvq_cache* cache, int32_t layer, const void* q, float* o
   a.n_units = n_units;
   a.n_ctas = ctas;
   a.wait_ns = decode_wait_ns();
-  return cuda_err(launch_decode(a, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kv_prefill_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch) {
@@ -424,7 +421,7 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
   a.in_bf16 = ap.in_bf16;
   a.max_pages_per_seq = cache->max_pages_per_seq;
   a.max_seq_len = cache->cfg.max_seq_len;
-  return cuda_err(launch_prefill(a, ap, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_prefill(a, ap, static_cast<cudaStream_t>(stream)));
 }
 
 int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v, const int32_t* path,
@@ -462,7 +459,7 @@ int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v
   c.n_accept = n_accept;
   c.n_nodes = n_nodes;
   c.max_path = max_path;
-  return cuda_err(launch_commit(a, c, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_commit(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 // what kv_tree_attention and kv_attention_weights share: the cache, the queries' shape and the layers of the call
@@ -521,7 +518,7 @@ int kv_tree_attention(kvq_cache* cache, int32_t layer, const void* k, const void
   a.scratch = static_cast<uint8_t*>(scratch);
   const int sms = decode_ctas(cache->device);
   if (sms <= 0) return KVQ_ERR_CUDA;
-  return cuda_err(launch_tree(a, sms, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_tree(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries) {
@@ -548,7 +545,7 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
   a.scratch = static_cast<uint8_t*>(scratch);
   const int sms = decode_ctas(cache->device);
   if (sms <= 0) return KVQ_ERR_CUDA;
-  return cuda_err(launch_weights(a, sms, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_weights(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 static int evict_args(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t budget, EvictArgs* a) {
@@ -592,7 +589,7 @@ int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq
   a.kept = kept;
   a.new_lens = new_lens;
   a.recent = recent;
-  return cuda_err(launch_evict(a, static_cast<cudaStream_t>(stream)));
+  return call_status(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream) {
@@ -606,7 +603,7 @@ int kv_status(kvq_cache* cache, uint32_t* flags, void* stream) {
   cudaError_t e = cudaMemcpyAsync(&v, st, sizeof(v), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(st, 0, sizeof(unsigned), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  if (call_status(e) != KVQ_OK) return KVQ_ERR_CUDA;
   *flags = v;
   return KVQ_OK;
 }

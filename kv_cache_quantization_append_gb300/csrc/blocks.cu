@@ -463,8 +463,6 @@ int grid_for(long long items) {
   return (int)(blocks < cap ? blocks : cap);
 }
 
-int launch_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
-
 }  // namespace
 
 }  // namespace kvq
@@ -497,7 +495,7 @@ int kv_tbq_encode(int32_t bits, uint64_t seed, const void* x, int32_t in_dtype, 
   a.in_bf16 = in_dtype == KVQ_IN_BF16;
   a.rec_bytes = (int)kv_tbq_block_bytes(bits);
   tbq_encode_kernel<<<grid_for(n_blocks), WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status(cudaGetLastError());
+  return call_status(cudaGetLastError());
 }
 
 int kv_tbq_decode(int32_t bits, uint64_t seed, const void* blocks, int64_t n_blocks, float* x, void* stream) {
@@ -516,7 +514,7 @@ int kv_tbq_decode(int32_t bits, uint64_t seed, const void* blocks, int64_t n_blo
   a.n_items = n_blocks;
   a.rec_bytes = (int)kv_tbq_block_bytes(bits);
   tbq_decode_kernel<<<grid_for(n_blocks), WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status(cudaGetLastError());
+  return call_status(cudaGetLastError());
 }
 
 int kv_split_outliers(const void* calib, int32_t in_dtype, int32_t n_sets, int32_t n_tokens, int16_t* outliers,
@@ -526,7 +524,7 @@ int kv_split_outliers(const void* calib, int32_t in_dtype, int32_t n_sets, int32
   if (!aligned16(calib) || !aligned16(outliers)) return KVQ_ERR_ALIGN;
   split_outliers_kernel<<<n_sets, D, 0, static_cast<cudaStream_t>(stream)>>>(calib, in_dtype == KVQ_IN_BF16, n_tokens,
                                                                               outliers);
-  return launch_status(cudaGetLastError());
+  return call_status(cudaGetLastError());
 }
 
 static int split_args(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int32_t n_sets, int64_t n_vectors,
@@ -561,7 +559,7 @@ int kv_split_encode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int
   a.rec = static_cast<uint8_t*>(records);
   a.in_bf16 = in_dtype == KVQ_IN_BF16;
   split_encode_kernel<<<grid_for(n_vectors), WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status(cudaGetLastError());
+  return call_status(cudaGetLastError());
 }
 
 int kv_split_decode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int32_t n_sets, const void* records,
@@ -575,7 +573,7 @@ int kv_split_decode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int
   a.rec_in = static_cast<const uint8_t*>(records);
   a.out = x;
   split_decode_kernel<<<grid_for(n_vectors), WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status(cudaGetLastError());
+  return call_status(cudaGetLastError());
 }
 
 }  // extern "C"

@@ -30,6 +30,14 @@ constexpr float LOGIT_SCALE = 0.127517431974411f;
 // sqrt(pi / 2) / 128: QJL inner-product estimator constant for m = 128 projections
 constexpr float QJL_CONST = 0.009791516698896885f;
 
+// What an entry point returns for the outcome of its CUDA calls.  A failure is reported here and forgotten by the runtime,
+// whose last error a later call's launch would otherwise take for its own.
+inline int call_status(cudaError_t e) {
+  if (e == cudaSuccess) return KVQ_OK;
+  cudaGetLastError();
+  return KVQ_ERR_CUDA;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {

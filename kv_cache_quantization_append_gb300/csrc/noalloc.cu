@@ -28,7 +28,7 @@ int scratch_address(int device, void** out) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_scratch_addr[device]) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return KVQ_ERR_CUDA;
+    if (call_status(cudaGetSymbolAddress(&p, g_noalloc_scratch)) != KVQ_OK || !p) return KVQ_ERR_CUDA;
     g_scratch_addr[device] = p;
   }
   *out = g_scratch_addr[device];
@@ -43,7 +43,7 @@ int decode_attention_noalloc(kvq_cache* cache, int32_t layer, const void* q, flo
   if (layer < -1 || layer >= cache->cfg.n_layers) return KVQ_ERR_INVALID_ARG;
   if (batch < 1 || batch > cache->cfg.max_batch) return KVQ_ERR_INVALID_ARG;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (call_status(cudaGetDevice(&dev)) != KVQ_OK) return KVQ_ERR_CUDA;
   if (dev != cache->device) return KVQ_ERR_INVALID_ARG;
   const size_t need = kv_decode_scratch_bytes(cache, layer, batch);
   if (need == 0) return KVQ_ERR_CUDA;

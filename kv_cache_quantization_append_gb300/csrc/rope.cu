@@ -311,7 +311,7 @@ int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, c
   const int mode = rope->layout == KVQ_ROPE_INTERLEAVED ? ADJACENT : a.rot % 16 == 0 ? IN_LANE : REREAD;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = in_dtype == KVQ_IN_BF16 ? launch<__nv_bfloat16>(a, mode, s) : launch<float>(a, mode, s);
-  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return call_status(e);
 }
 
 }  // extern "C"
