@@ -134,11 +134,14 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _ptr(t: torch.Tensor | None) -> int:
+def _ptr(t: torch.Tensor | None, device: int | None = None) -> int:
+    """The address of a tensor on the device (on the cache's, where that is given: the library could not tell)."""
     if t is None:
         return 0
     if not t.is_cuda:
         raise KVQError("device tensor expected")
+    if device is not None and t.get_device() != device:
+        raise KVQError(f"tensor on device {t.get_device()}, the cache is on device {device} (code 1)")
     if not t.is_contiguous():
         raise KVQError("contiguous tensor expected")
     return t.data_ptr()
@@ -225,8 +228,9 @@ def kv_calibrate(cache: kvq_cache, layer: int, k_calib: torch.Tensor, v_calib: t
     lead = (_layers_in_call(cache, layer),) if layer == -1 else ()
     _check_shape("k_calib", k_calib, lead + (cache.cfg.n_kv_heads, n_tokens, 128))
     _check_shape("v_calib", v_calib, tuple(k_calib.shape))
-    _check(load().kv_calibrate(ctypes.byref(cache), layer, _ptr(k_calib), _ptr(v_calib), n_tokens,
-                               _ptr(scratch), scratch.numel() * scratch.element_size(),
+    dev = cache.device
+    _check(load().kv_calibrate(ctypes.byref(cache), layer, _ptr(k_calib, dev), _ptr(v_calib, dev), n_tokens,
+                               _ptr(scratch, dev), scratch.numel() * scratch.element_size(),
                                _stream(stream)))
 
 
@@ -237,7 +241,8 @@ def kv_quant_append(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Tens
         raise KVQError("pos must be int32")
     _check_in_dtype(cache, k, v)
     B, T = _check_append_shapes(cache, layer, k, v, pos)
-    _check(load().kv_quant_append(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(pos), B, T,
+    dev = cache.device
+    _check(load().kv_quant_append(ctypes.byref(cache), layer, _ptr(k, dev), _ptr(v, dev), _ptr(pos, dev), B, T,
                                   _stream(stream)))
 
 
@@ -253,8 +258,9 @@ def kv_decode_attention(cache: kvq_cache, layer: int, q: torch.Tensor, out: torc
         raise KVQError("seq_lens must be int32 and out float32")
     _check_in_dtype(cache, q)
     B = _check_decode_shapes(cache, layer, q, out, seq_lens)
-    _check(load().kv_decode_attention(ctypes.byref(cache), layer, _ptr(q), _ptr(out), _ptr(seq_lens),
-                                      B, _ptr(scratch), scratch.numel() * scratch.element_size(),
+    dev = cache.device
+    _check(load().kv_decode_attention(ctypes.byref(cache), layer, _ptr(q, dev), _ptr(out, dev), _ptr(seq_lens, dev),
+                                      B, _ptr(scratch, dev), scratch.numel() * scratch.element_size(),
                                       _stream(stream)))
 
 
@@ -266,8 +272,9 @@ def kv_decode_attention_noalloc(cache: kvq_cache, layer: int, q: torch.Tensor, o
         raise KVQError("seq_lens must be int32 and out float32")
     _check_in_dtype(cache, q)
     B = _check_decode_shapes(cache, layer, q, out, seq_lens)
-    _check(load().kv_decode_attention_noalloc(ctypes.byref(cache), layer, _ptr(q), _ptr(out),
-                                              _ptr(seq_lens), B, _stream(stream)))
+    dev = cache.device
+    _check(load().kv_decode_attention_noalloc(ctypes.byref(cache), layer, _ptr(q, dev), _ptr(out, dev),
+                                              _ptr(seq_lens, dev), B, _stream(stream)))
 
 
 def kv_prefill_scratch_bytes(cache: kvq_cache, layer: int, batch: int) -> int:
@@ -285,9 +292,10 @@ def kv_prefill_attention(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch
     lead = (_layers_in_call(cache, layer),) if layer == -1 else ()
     _check_shape("q", q, lead + (B, cache.cfg.n_q_heads, T, 128))
     _check_shape("out", out, tuple(q.shape))
-    _check(load().kv_prefill_attention(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(q), _ptr(out),
-                                       _ptr(pos), B, T, _ptr(scratch), scratch.numel() * scratch.element_size(),
-                                       _stream(stream)))
+    dev = cache.device
+    _check(load().kv_prefill_attention(ctypes.byref(cache), layer, _ptr(k, dev), _ptr(v, dev), _ptr(q, dev),
+                                       _ptr(out, dev), _ptr(pos, dev), B, T, _ptr(scratch, dev),
+                                       scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
 def kv_rope_init(rot_dim: int, layout: int = ROPE_HALF, theta: float = 10000.0, scaling: int = ROPE_PLAIN,
@@ -361,9 +369,10 @@ def kv_tree_attention(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Te
     _check_shape("q", q, lead + (B, cache.cfg.n_q_heads, N, 128))
     _check_shape("out", out, tuple(q.shape))
     _check_shape("parents", parents, (B, N))
-    _check(load().kv_tree_attention(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(q), _ptr(out), _ptr(seq_lens),
-                                    _ptr(parents), B, N, _ptr(scratch), scratch.numel() * scratch.element_size(),
-                                    _stream(stream)))
+    dev = cache.device
+    _check(load().kv_tree_attention(ctypes.byref(cache), layer, _ptr(k, dev), _ptr(v, dev), _ptr(q, dev),
+                                    _ptr(out, dev), _ptr(seq_lens, dev), _ptr(parents, dev), B, N, _ptr(scratch, dev),
+                                    scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
 def kv_tree_commit(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Tensor, path: torch.Tensor,
@@ -376,8 +385,9 @@ def kv_tree_commit(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch.Tenso
     if path.dim() != 2 or path.shape[0] != B:
         raise KVQError(f"path must be [{B}][max_path], got {tuple(path.shape)}")
     _check_shape("n_accept", n_accept, (B,))
-    _check(load().kv_tree_commit(ctypes.byref(cache), layer, _ptr(k), _ptr(v), _ptr(path), _ptr(n_accept), _ptr(pos), B, N,
-                                 path.shape[1], _stream(stream)))
+    dev = cache.device
+    _check(load().kv_tree_commit(ctypes.byref(cache), layer, _ptr(k, dev), _ptr(v, dev), _ptr(path, dev),
+                                 _ptr(n_accept, dev), _ptr(pos, dev), B, N, path.shape[1], _stream(stream)))
 
 
 def kv_weights_scratch_bytes(cache: kvq_cache, layer: int, batch: int, n_queries: int) -> int:
@@ -405,8 +415,10 @@ def kv_attention_weights(cache: kvq_cache, layer: int, q: torch.Tensor, weights:
     _check_shape("q", q, lead + (B, cache.cfg.n_q_heads, T, 128))
     _check_shape("seq_lens", seq_lens, (B,))
     _check_weights(cache, layer, B, weights)
-    _check(load().kv_attention_weights(ctypes.byref(cache), layer, _ptr(q), _ptr(weights), decay, _ptr(seq_lens), B, T,
-                                       _ptr(scratch), scratch.numel() * scratch.element_size(), _stream(stream)))
+    dev = cache.device
+    _check(load().kv_attention_weights(ctypes.byref(cache), layer, _ptr(q, dev), _ptr(weights, dev), decay,
+                                       _ptr(seq_lens, dev), B, T, _ptr(scratch, dev),
+                                       scratch.numel() * scratch.element_size(), _stream(stream)))
 
 
 def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torch.Tensor, kept: torch.Tensor,
@@ -420,8 +432,9 @@ def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torc
     _check_shape("new_lens", new_lens, (B,))
     _check_weights(cache, layer, B, weights)
     _check_shape("kept", kept, tuple(weights.shape[:-1]) + (budget,))
-    _check(load().kv_evict(ctypes.byref(cache), layer, _ptr(weights), _ptr(seq_lens), _ptr(kept), _ptr(new_lens), B, budget,
-                           recent, _stream(stream)))
+    dev = cache.device
+    _check(load().kv_evict(ctypes.byref(cache), layer, _ptr(weights, dev), _ptr(seq_lens, dev), _ptr(kept, dev),
+                           _ptr(new_lens, dev), B, budget, recent, _stream(stream)))
 
 
 def _in_dtype_of(t: torch.Tensor) -> int:

@@ -109,3 +109,25 @@ def test_one_buffer_for_all_sizes(made):
 
     assert gpu._work[next(k for k in gpu._work if k[0] == "tree")].numel() == max(
         lib.kv_tree_scratch_bytes(gpu.handle, 0, b, n) for b in (1, 2, 3) for n in (1, 24, 7))
+
+
+def test_the_library_refuses_a_call_while_another_device_is_current(made):
+    """The C entry points of trees, commits, weights and eviction look at the current device themselves."""
+    import ctypes
+
+    from kv_cache_quantization_append_gb300 import lib
+
+    gpu = made[0]
+    other = lib.kvq_cache.from_buffer_copy(gpu.handle)
+    other.device = gpu.handle.device + 1
+    buf = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    p, r, c = buf.data_ptr(), ctypes.byref(other), lib.load()
+    before = gpu.buffer.clone()
+    assert c.kv_tree_commit(r, 0, p, p, p, p, p, 1, 4, 4, None) == 1
+    assert c.kv_evict(r, 0, p, p, p, p + 64, 1, 200, 128, None) == 1
+    assert c.kv_quant_append(r, 0, p, p, p, 1, 1, None) == 1
+    for call in (lambda n: c.kv_tree_attention(r, 0, p, p, p, p, p, p, 1, 4, p, n, None),
+                 lambda n: c.kv_attention_weights(r, 0, p, p, 1.0, p, 1, 1, p, n, None)):
+        assert call(1 << 60) == 1
+    torch.cuda.synchronize()
+    assert torch.equal(before, gpu.buffer) and not buf.any()

@@ -194,3 +194,47 @@ def test_binding_shapes():
                  (x, pos, qo, ko, ko)):             # the last: host tensors
         with pytest.raises(lib.KVQError):
             lib.kv_qk_norm_rope(r, *args)
+
+
+class _Elsewhere:
+    """A tensor that says it is on another GPU than the cache (device 0)."""
+
+    def __init__(self, t):
+        self._t = t
+        self.is_cuda = True
+
+    def get_device(self):
+        return 1
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def test_tensors_of_another_device_are_refused():
+    """Each tensor argument in turn is on another device than the cache's, the ones before it on the cache's own."""
+
+    class Here(_Elsewhere):
+        def get_device(self):
+            return 0
+
+    c = _cache()
+    bf, i32, z = torch.bfloat16, torch.int32, torch.zeros
+    kv, q, ln, par = z(2, 8, 4, 128, dtype=bf), z(2, 24, 4, 128, dtype=bf), z(2, dtype=i32), z(2, 4, dtype=i32)
+    q1, o1, s, w = z(2, 24, 128, dtype=bf), z(2, 24, 128), z(16, dtype=torch.uint8), z(2, 8, 1024)
+    calls = {
+        lib.kv_tree_attention: (kv, kv, q, q, ln, par, s),
+        lib.kv_tree_commit: (kv, kv, par, ln, ln),
+        lib.kv_attention_weights: (q, w, 1.0, ln, s),
+        lib.kv_evict: (w, ln, z(2, 8, 256, dtype=i32), ln, 256, 128),
+        lib.kv_quant_append: (kv, kv, ln),
+        lib.kv_decode_attention: (q1, o1, ln, s),
+        lib.kv_decode_attention_noalloc: (q1, o1, ln),
+        lib.kv_prefill_attention: (kv, kv, q, q.float(), ln, s),
+        lib.kv_calibrate: (kv[0], kv[0], s),
+    }
+    for call, args in calls.items():
+        tensors = [i for i, a in enumerate(args) if isinstance(a, torch.Tensor)]
+        for n in tensors:
+            given = [a if i not in tensors else _Elsewhere(a) if i == n else Here(a) for i, a in enumerate(args)]
+            with pytest.raises(lib.KVQError, match="tensor on device 1"):
+                call(c, 0, *given)
