@@ -386,7 +386,11 @@ int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v
  *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; positions >= seq_lens[b] are left as they were
  *   decay        0..1; 0 writes without reading what was there
  *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
- *   scratch      device, >= kv_weights_scratch_bytes bytes, any contents, not shared by overlapping calls
+ *   scratch      device, >= kv_weights_scratch_bytes bytes, any contents, not shared by overlapping calls.  Up to 8 query
+ *                rows (n_queries times query heads per kv-head) have their logits stored: 4 bytes a row, kv-head and
+ *                position of capacity, of as many layers at a time as 256 MB hold (of one at least: a layer's batch *
+ *                n_kv_heads * rows * max_seq_len * 4).  More rows take a few MB.  The time follows seq_lens, not
+ *                max_seq_len.
  */
 size_t kv_weights_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_queries);
 int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* weights, float decay,

@@ -848,48 +848,82 @@ static __global__ void __launch_bounds__(ADD_THREADS) normaliser_kernel(const __
   if (lane == 0) p.norms[i] = v == v ? v : INFINITY;  // (no weight from a row that was given up)
 }
 
-// weights from stored logits: one CTA per 1024 positions of a unit
+// Weights from stored logits: pieces of 1024 positions of the units, in one list (of the positions there are, whatever the
+// capacity), dealt out to the CTAs in turn.
+constexpr int PIECE = 4 * ADD_THREADS;
 static __global__ void __launch_bounds__(ADD_THREADS) weights_add_kernel(const __grid_constant__ Plan p) {
   __shared__ float lse[STORE_ROWS];
   extern __shared__ int pre[];
   const MultiArgs& a = p.a;
   int* lens = pre + a.batch + 1;
+  int* pieces = lens + a.batch;                // prefix of the sequences' pieces
+  int* again = pieces + a.batch + 1;           // the lengths once more (by another warp)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int u = blockIdx.y + blockIdx.z * 32768;
   if (warp == 0) tile_prefix(a, lens, pre, false, [&](int L) { return seq_tiles(L, a.W); });
+  if (warp == 1) tile_prefix(a, again, pieces, false, [&](int L) { return (L + PIECE - 1) / PIECE; });
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (u >= p.n_units) return;
-  const int h = u % a.Hkv, b = (u / a.Hkv) % a.batch, ll = u / (a.Hkv * a.batch), L = lens[b];
-  const int j0 = (blockIdx.x * ADD_THREADS + tid) * 4;
-  if (blockIdx.x * ADD_THREADS * 4 >= L) return;
-  float4 x[STORE_ROWS];
-  const float* src = p.logits + (size_t)u * p.rows * p.s_pad + j0;
-#pragma unroll
-  for (int r = 0; r < STORE_ROWS; ++r)
-    if (r < p.rows && j0 < L) x[r] = *reinterpret_cast<const float4*>(src + r * p.s_pad);
   const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
-  const int tiles = pre[b + 1] - pre[b];
-  if (warp < p.rows) {
-    const float v = normaliser(p, u, warp, ll * per_layer + (long long)pre[b] * a.Hkv + (long long)h * tiles, quant_tiles(L, a.W), tiles,
-                               min((long long)p.G, total), total, lane);
-    if (lane == 0) lse[warp] = v;
-  }
-  __syncthreads();
-  if (j0 >= L) return;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int r = 0; r < STORE_ROWS; ++r)
-    if (r < p.rows && lse[r] == lse[r]) {  // (a row that was given up has logits that were never written)
-      s[0] += ex2(x[r].x - lse[r]);
-      s[1] += ex2(x[r].y - lse[r]);
-      s[2] += ex2(x[r].z - lse[r]);
-      s[3] += ex2(x[r].w - lse[r]);
+  const long long layer_pieces = (long long)pieces[a.batch] * a.Hkv;
+  for (long long i = blockIdx.x; i < layer_pieces * a.n_layers_call; i += gridDim.x) {
+    const int ll = a.n_layers_call > 1 ? (int)quick_div(i, layer_pieces) : 0;
+    const long long in_layer = i - ll * layer_pieces;
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)pieces[mid] * a.Hkv <= in_layer) lo = mid;
+      else hi = mid - 1;
     }
-  float* w = a.weights + (size_t)u * a.max_seq_len + j0;
+    const int b = lo, L = lens[b], n = pieces[b + 1] - pieces[b], tiles = pre[b + 1] - pre[b];
+    const long long r = in_layer - (long long)pieces[b] * a.Hkv;
+    const int h = (int)quick_div(r, n), j0 = (int)(r - (long long)h * n) * PIECE + tid * 4;
+    const int u = (ll * a.batch + b) * a.Hkv + h;
+    float4 x[STORE_ROWS];
+    const float* src = p.logits + (size_t)u * p.rows * p.s_pad + j0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (j0 + i < L) w[i] = p.decay != 0.f ? fmaf(p.decay, w[i], s[i]) : s[i];
+    for (int r = 0; r < STORE_ROWS; ++r)
+      if (r < p.rows && j0 < L) x[r] = *reinterpret_cast<const float4*>(src + r * p.s_pad);
+    if (warp < p.rows) {
+      const float v = normaliser(p, u, warp, ll * per_layer + (long long)pre[b] * a.Hkv + (long long)h * tiles, quant_tiles(L, a.W),
+                                 tiles, min((long long)p.G, total), total, lane);
+      if (lane == 0) lse[warp] = v;
+    }
+    __syncthreads();
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < STORE_ROWS; ++r)
+      if (r < p.rows && lse[r] == lse[r]) {  // (a row that was given up has logits that were never written)
+        s[0] += ex2(x[r].x - lse[r]);
+        s[1] += ex2(x[r].y - lse[r]);
+        s[2] += ex2(x[r].z - lse[r]);
+        s[3] += ex2(x[r].w - lse[r]);
+      }
+    float* w = a.weights + (size_t)u * a.max_seq_len + j0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j0 + i < L) w[i] = p.decay != 0.f ? fmaf(p.decay, w[i], s[i]) : s[i];
+    __syncthreads();  // (the normalisers have been read)
+  }
+}
+
+// layers of one set of launches: stored logits take up to LOGITS_ROOM (or one layer's), the layers after them their place
+constexpr size_t LOGITS_ROOM = (size_t)256 << 20;
+inline int layers_at_once(const MultiArgs& a) {
+  const int rows = a.n * a.g;
+  if (rows > STORE_ROWS) return a.n_layers_call;
+  const size_t layer = (size_t)a.batch * a.Hkv * rows * (((size_t)a.max_seq_len + 3) / 4 * 4) * sizeof(float);
+  const size_t n = layer >= LOGITS_ROOM ? 1 : LOGITS_ROOM / layer;
+  return n < (size_t)a.n_layers_call ? (int)n : a.n_layers_call;
+}
+// layers l0 .. of a call, as a call of their own
+inline MultiArgs layers_of(const MultiArgs& a, int l0, int n) {
+  MultiArgs s = a;
+  const size_t units = (size_t)l0 * a.batch * a.Hkv;
+  s.layer0 += l0;
+  s.n_layers_call = n;
+  s.q = static_cast<const uint8_t*>(a.q) + units * a.g * a.n * D * (a.in_bf16 ? 2 : 4);
+  s.weights = a.weights + units * a.max_seq_len;
+  return s;
 }
 
 // rows of one launch, and the plan of the launches that begin at row0; returns the scratch bytes
@@ -938,19 +972,29 @@ cudaError_t launch_rows(const Plan& p, cudaStream_t s) {
     e = launch_norms(p, pre, s);
     return e != cudaSuccess ? e : go<weights_kernel<KF, true, 8, 2>>(grid, threads, smem, true, s, p);
   }
-  const unsigned y = p.n_units < 32768 ? p.n_units : 32768;
-  return go<weights_add_kernel>(dim3((unsigned)((p.a.max_seq_len + 4 * ADD_THREADS - 1) / (4 * ADD_THREADS)), y, (p.n_units + 32767) / 32768),
-                                ADD_THREADS, pre, true, s, p);
+  // eight CTAs an SM at most: no more than are there at once
+  const long long most = (long long)p.n_units * ((p.a.max_seq_len + PIECE - 1) / PIECE), there = (long long)p.G * 4;
+  return go<weights_add_kernel>(dim3((unsigned)(most < there ? most : there)), ADD_THREADS, (size_t)(4 * p.a.batch + 2) * 4, true, s, p);
+}
+
+template <int KF>
+size_t scratch_bytes(const MultiArgs& a, int sms) {
+  Plan p;
+  return make_plan<KF>(layers_of(a, 0, layers_at_once(a)), sms, 0, &p);
 }
 
 template <int KF>
 cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
-  for (int row0 = 0; row0 < a.n * a.g;) {
-    Plan p;
-    make_plan<KF>(a, sms, row0, &p);
-    const cudaError_t e = launch_rows<KF>(p, s);
-    if (e != cudaSuccess) return e;
-    row0 += p.rows;
+  const int most = layers_at_once(a);
+  for (int l0 = 0; l0 < a.n_layers_call; l0 += most) {
+    const MultiArgs part = layers_of(a, l0, a.n_layers_call - l0 < most ? a.n_layers_call - l0 : most);
+    for (int row0 = 0; row0 < a.n * a.g;) {
+      Plan p;
+      make_plan<KF>(part, sms, row0, &p);
+      const cudaError_t e = launch_rows<KF>(p, s);
+      if (e != cudaSuccess) return e;
+      row0 += p.rows;
+    }
   }
   return cudaSuccess;
 }

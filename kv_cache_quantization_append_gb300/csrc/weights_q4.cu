@@ -3,10 +3,7 @@
 
 namespace kvq {
 
-size_t weights_scratch_q4(const MultiArgs& a, int sms) {
-  weights::Plan p;
-  return weights::make_plan<KVQ_Q4G32>(a, sms, 0, &p);
-}
+size_t weights_scratch_q4(const MultiArgs& a, int sms) { return weights::scratch_bytes<KVQ_Q4G32>(a, sms); }
 cudaError_t launch_weights_q4(const MultiArgs& a, int sms, cudaStream_t s) { return weights::launch<KVQ_Q4G32>(a, sms, s); }
 
 }  // namespace kvq

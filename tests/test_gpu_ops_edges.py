@@ -243,3 +243,27 @@ def test_captured_serving_step():
             assert torch.equal(state["a"][key], state["b"][key]), key
         assert torch.equal(a.buffer, b.buffer)
     assert a.status() == 0 and b.status() == 0
+
+
+def test_weights_of_more_layers_than_the_scratch_holds():
+    """Stored logits of 160 MiB a layer, of which the 256 MiB hold one: a call of every layer gives, to the bit, what the layers' own
+    calls give (layers taken together are cut into other ranges, whose sums join in another order)."""
+    T = 2
+    rng = np.random.default_rng(101)
+    L, B, H, g, S = 3, 5, 8, 4, 131072
+    gpu = QuantKVCache(lib.make_config(L, H, H * g, B, S), "cuda")
+    lens = [5000, 0, 1025, 130, 2048]
+    k = torch.as_tensor(rng.standard_normal((L, B, H, 5000, 128)).astype(np.float32)).bfloat16().cuda()
+    gpu.append(-1, k, k, _i32([0] * B))
+    q = torch.as_tensor(rng.standard_normal((L, B, H * g, T, 128)).astype(np.float32)).bfloat16().cuda()
+    old = torch.rand(L, B, H, S, device="cuda")
+    w = gpu.attention_weights(-1, q, _i32(lens), old.clone(), 0.5)
+    for layer in range(L):
+        one = gpu.attention_weights(layer, q[layer].contiguous(), _i32(lens), old[layer].clone(), 0.5)
+        assert torch.equal(w[layer], one)
+        for b, n in enumerate(lens):
+            assert torch.equal(one[b, :, n:], old[layer, b, :, n:])
+            if n:
+                got = (one[b, :, :n].double() - 0.5 * old[layer, b, :, :n].double()).sum(-1)
+                assert (got - g * T).abs().max() < 1e-3
+    assert gpu.status() == 0

@@ -142,6 +142,20 @@ def test_weights_ranges(kvq):
     assert call(sb=16) == CAPACITY
 
 
+def test_weights_scratch_does_not_grow_with_the_layers(kvq):
+    c = _cache()
+    sizes = []
+    for layers in (1, 28):
+        c.cfg = lib.make_config(layers, 8, 32, 8, 131072)
+        c.max_pages_per_seq, c.n_pages = 2048, 8 * 2048
+        sizes.append([kvq.kv_weights_scratch_bytes(ctypes.byref(c), -1, 8, n) for n in (1, 2, 3)])
+    one, all_ = sizes
+    assert one[0] >= 8 * 8 * 4 * 131072 * 4 and one[1] >= 8 * 8 * 8 * 131072 * 4      # a layer's logits
+    for i in range(2):
+        assert all_[i] <= (256 << 20) + (32 << 20)
+    assert all_[2] < 64 << 20                               # 12 rows: logits are not stored
+
+
 def test_evict_ranges(kvq):
     c, d = _cache(), P(FAKE)
 
