@@ -376,14 +376,16 @@ int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v
                    void* stream);
 
 /*
- * Attention weight that each cached position receives, accumulated for eviction: the n_queries newest tokens'
- * queries (query t of sequence b at position P = seq_lens[b] - n_queries + t, attending to positions 0..P; P < 0:
+ * Attention weight that each cached position receives, accumulated for eviction: the n_queries newest cached tokens'
+ * queries, after their append or commit (query t of sequence b at position P = seq_lens[b] - n_queries + t, attending to positions 0..P; P < 0:
  * the query is ignored) against the cache as it stands -- positions below seq_lens[b] - window through their
  * records, the rest raw -- and for every position j < seq_lens[b]
  *   weights[j] = decay weights[j] + sum over the queries and the query heads of the kv-head of softmax(...)_j.
  * With n_queries == 1 the softmax is that of kv_decode_attention at the same lengths.
  *   q            device, cfg.in_dtype [L?][batch][n_q_heads][n_queries][128], n_queries 1..KVQ_MAX_TREE
- *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; positions >= seq_lens[b] are left as they were
+ *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; positions >= seq_lens[b] are left as they were.  With
+ *                a decay above 0 whatever stands at a position counts as its weight so far: zeros before the first
+ *                call, and wherever tokens are appended after an eviction (see kv_evict)
  *   decay        0..1; 0 writes without reading what was there
  *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
  *   scratch      device, >= kv_weights_scratch_bytes bytes, any contents, not shared by overlapping calls.  Up to 8 query
@@ -404,7 +406,8 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
  * its record as it is, and the ring is turned to match, so that every entry point above goes on at length budget
  * (new keys keep their true rotary positions: those are the caller's, see kv_qk_norm_rope).
  *   weights      device float [L?][batch][n_kv_heads][max_seq_len]; compacted like the records, entries at and
- *                after ``budget`` left as they were
+ *                after ``budget`` left as they were: weights of positions that have moved or are gone, to be set to zero
+ *                before tokens appended there take weight
  *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
  *   kept         device int32 [L?][batch][n_kv_heads][budget] (out): the position each slot held; -1 past the end of
  *                a sequence of fewer than ``budget`` tokens (which is left as it is)

@@ -104,14 +104,21 @@ class QuantKVCache:
 
     def attention_weights(self, layer: int, q: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
                           decay: float = 1.0, stream=None) -> torch.Tensor:
-        """Add the attention weight that cached positions receive from the newest tokens' queries to ``weights``."""
+        """Add the attention weight that cached positions receive from the newest cached tokens' queries to ``weights``.
+
+        q: [L?][B][Hq][T][128] of the T newest tokens of seq_lens, in order of position; ``weights`` holds zeros where a
+        position has taken no weight yet.
+        """
         scratch = self._workspace("weights", lib.kv_weights_scratch_bytes, (layer, q.shape[-4], q.shape[-2]), stream)
         lib.kv_attention_weights(self.handle, layer, q, weights, decay, seq_lens, scratch, stream)
         return weights
 
     def evict(self, layer: int, weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, recent: int,
               kept: torch.Tensor | None = None, new_lens: torch.Tensor | None = None, stream=None):
-        """Cut every sequence to ``budget`` positions by weight; returns (kept, new_lens)."""
+        """Cut every sequence to ``budget`` positions by weight; returns (kept, new_lens).
+
+        ``weights`` is compacted; set weights[..., budget:] to zero before tokens appended there take weight.
+        """
         if kept is None:
             kept = torch.empty(tuple(weights.shape[:-1]) + (budget,), dtype=torch.int32, device=weights.device)
         if new_lens is None:
