@@ -411,7 +411,7 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
  *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
  *   kept         device int32 [L?][batch][n_kv_heads][budget] (out): the position each slot held; -1 past the end of
  *                a sequence of fewer than ``budget`` tokens (which is left as it is)
- *   new_lens     device int32 [batch] (out): min(seq_lens[b], budget); not the same buffer as seq_lens
+ *   new_lens     device int32 [batch] (out): min(seq_lens[b], budget); must not overlap seq_lens
  *   budget, recent   window <= recent <= budget <= max_seq_len
  * All layers of a sequence have to be cut together (layer == -1, or each layer in turn) before its new length is
  * used.  A page must not be shared by several sequences, or by positions of one, when it is evicted from.  A

@@ -580,9 +580,13 @@ int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq
   EvictArgs a;
   int rc = evict_args(cache, layer, batch, budget, &a);
   if (rc != KVQ_OK) return rc;
-  if (!weights || !seq_lens || !kept || !new_lens || new_lens == seq_lens) return KVQ_ERR_INVALID_ARG;
+  if (!weights || !seq_lens || !kept || !new_lens) return KVQ_ERR_INVALID_ARG;
   if (recent < 0 || recent < cache->cfg.window || recent > budget) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(weights) || !aligned16(seq_lens) || !aligned16(kept) || !aligned16(new_lens)) return KVQ_ERR_ALIGN;
+  // lengths are read by every block while new ones are written
+  const uintptr_t old_at = reinterpret_cast<uintptr_t>(seq_lens), new_at = reinterpret_cast<uintptr_t>(new_lens);
+  const uintptr_t apart = old_at < new_at ? new_at - old_at : old_at - new_at;
+  if (apart < (uintptr_t)batch * sizeof(int32_t)) return KVQ_ERR_INVALID_ARG;
   if ((rc = check_device(cache)) != KVQ_OK) return rc;
   a.weights = weights;
   a.seq_lens = seq_lens;

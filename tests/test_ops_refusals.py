@@ -252,3 +252,13 @@ def test_tensors_of_another_device_are_refused():
             given = [a if i not in tensors else _Elsewhere(a) if i == n else Here(a) for i, a in enumerate(args)]
             with pytest.raises(lib.KVQError, match="tensor on device 1"):
                 call(c, 0, *given)
+
+
+def test_evict_lengths_that_overlap(kvq):
+    c, d = _cache(), P(FAKE)
+    call = lambda ln, new, B: kvq.kv_evict(ctypes.byref(c), 0, d, P(ln), d, P(new), B, 256, 128, None)  # noqa: E731
+    c.cfg = lib.make_config(2, 8, 24, 40, 1024)
+    c.n_pages = 640
+    for B, apart in ((40, 144), (40, 16), (5, 16)):
+        assert call(FAKE, FAKE + apart, B) == INVALID and call(FAKE + apart, FAKE, B) == INVALID
+    assert call(FAKE, FAKE + 160, 40) != INVALID and call(FAKE + 16, FAKE, 4) != INVALID   # (no device here)
