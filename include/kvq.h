@@ -302,7 +302,7 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
  *                ln(original_len / (2 pi r)) / (2 ln theta)
  *   factor, original_len, low, high   as the scaling uses them (ignored otherwise)
  *   attn_factor  multiplies every sine and cosine (1: plain rotation)
- * Angles are exact at any position (a 64-bit fraction of a turn per position).
+ * Angles wrap exactly at any position (a 64-bit fraction of a turn per position, itself good to 2^-54 of a turn).
  *
  * kv_qk_norm_rope (no cache is involved; pointers belong to the current device):
  *   qkv          device, in_dtype: row r = b n_tokens + t at qkv + r row_stride elements holds the n_q_heads

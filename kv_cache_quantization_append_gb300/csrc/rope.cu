@@ -7,9 +7,9 @@
 // everything in fp32, rounded once to the output type.
 //
 // Angles: f_i / (2 pi) is kept as a 64-bit binary fraction of a turn, so pos * f_i modulo one turn is the
-// wrapping 64-bit product -- exact to pos * 2^-65 turns at any position, where an fp32 product at position
-// 100,000 is off by 0.01 rad, and without fp64 instructions.  The fraction goes to fp32 (2^-24 relative,
-// under 2e-7 rad) and through sincospi.
+// wrapping 64-bit product, exact at any position and without fp64 instructions.  The fraction comes from a
+// double: the angle is good to pos * 2^-54 turns (at position 2^20 6e-11 of a turn), where an fp32 product at
+// position 100,000 is off by 0.01 rad.  It goes to fp32 (2^-24 relative, under 2e-7 rad) and through sincospi.
 //
 // Bound by memory: every value is read once and written once.  Eight lanes hold a head, each two 16-byte
 // blocks of 8 channels chosen so that both members of a pair sit in one lane (blocks l and l + rot_dim / 16

@@ -54,6 +54,23 @@ def test_rope_handle(kvq):
     assert r.magic == 0
 
 
+def test_rope_turns_against_60_digits(kvq):
+    """Turns per position of every pair: pow, the division and the quotient in double round by a few 2^-53 of at most 0.16
+    turns, and the 64-bit fraction is cut at 2^-64: within 2^-54 in all."""
+    from decimal import Decimal, getcontext
+
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    for rot, theta, kind, factor in ((128, 1e4, 0, 1.0), (128, 5e5, 0, 1.0), (96, 1e6, 1, 8.0), (64, 1e4, 2, 8.0), (90, 1e7, 0, 1.0)):
+        base = Decimal(theta)
+        if kind == 2:
+            base *= Decimal(factor) ** (Decimal(rot) / (rot - 2))
+        r = lib.kv_rope_init(rot, theta=theta, scaling=kind, factor=factor)
+        for i in range(rot // 2):
+            f = base ** (Decimal(-2 * i) / rot) / two_pi / (Decimal(factor) if kind == 1 else 1)
+            assert abs(Decimal(r.turns[i]) / 2 ** 64 - f % 1) < Decimal(2) ** -54, (rot, theta, kind, i)
+
+
 def test_norm_rope(kvq):
     r = lib.kv_rope_init(128)
     d = P(FAKE)
