@@ -333,9 +333,10 @@ int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, c
  * Attention of a tree of drafted tokens over the cache: one pass over the cached positions for all nodes, what
  * speculative decoding verifies a draft with.  Nothing is appended.  Node i of sequence b, at depth d below the
  * cached context (children of the context have d = 0), sits at position P = seq_lens[b] + d and attends to the
- * cached positions and to itself and its ancestors among the drafts, as its own single-token step along that
- * path would: cached positions j <= P - window through their records, the newer ones raw from the ring; drafted
- * tokens are always raw.
+ * cached positions and to itself and its ancestors among the drafts: cached positions j <= P - window through their
+ * records, the newer ones raw from the ring, drafted tokens always raw.  Where the window covers the draft (window >
+ * d) that is what the node's own single-token step along its path reads; under a smaller window, or none, such a step
+ * would read the path's oldest tokens (with window 0 all of them, itself too) through their records instead.
  *   k, v         device, cfg.in_dtype [L?][batch][n_kv_heads][n_nodes][128]: the drafts' raw keys and values, within
  *                the range that kv_quant_append takes (nodes that are not there may hold anything; an infinity or NaN
  *                among them, or in the ring, makes NaN of the nodes that attend to it and of no other)

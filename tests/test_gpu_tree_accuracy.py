@@ -180,3 +180,19 @@ def test_values_that_are_not_finite_reach_who_attends_to_them(in_dtype, value):
     shallow = [0, 7]
     deep = np.setdiff1d(np.arange(9), shallow)
     assert np.array_equal(got[:, :, deep], base[:, :, deep]) and not np.isfinite(got[:, :, shallow]).all(-1).any()
+
+
+@pytest.mark.parametrize("window", [0, 8, 128])
+def test_where_a_chain_is_what_single_tokens_see(window):
+    """Nodes that the window covers (depth < window) equal their own single-token steps; deeper ones read their path raw where
+    those read records, which shows."""
+    rng = np.random.default_rng(5)
+    gpu, ora, _ = harness.make_pair(1, 1, 2, 1, 400, window=window, in_dtype="f32")
+    _fill(gpu, ora, [90], 90, rng, "f32")
+    k, v, q = _drafts(rng, gpu.cfg, 1, 14, "f32")
+    got = _tree(gpu, k, v, q, [90], ref.random_tree(rng, 14, chain=True)[None])
+    for i in range(14):
+        ora.append(0, harness.to_np(k[:, :, i:i + 1]), harness.to_np(v[:, :, i:i + 1]), np.array([90 + i]))
+        step = ora.decode(0, harness.to_np(q[:, :, i]), np.array([91 + i]))
+        err = np.abs(got[:, :, i] - step).max() / np.abs(step).max()
+        assert err <= TOL["f32"] if i < window else err > 10 * TOL["f32"], (i, err)
