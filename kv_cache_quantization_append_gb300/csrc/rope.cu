@@ -17,8 +17,8 @@
 // rot_dim not a multiple of 16 with halves reads the partner channels again (from L1).  The sines of a
 // token are computed once per CTA for all its heads.
 // Measured, bf16: 8192 tokens of 48 heads (201 MB) 39.9 us, 5.05 TB/s, 74 % of the copy rate (keeping the next
-// head's loads under way took registers, with them CTAs, and 57 us); 8 tokens 6 us on the device, one trip
-// through memory, and 10.5 a call, the host's.
+// head's loads under way took registers, with them CTAs, and 57 us); 8 tokens 3.1 us on the device (one of many
+// in a graph), one trip through memory, and 10.4 a call, the host's.
 #include <cmath>
 
 #include "kvq_internal.cuh"
@@ -202,8 +202,10 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
 
 template <typename T>
 cudaError_t launch(const RopeArgs& a, int mode, cudaStream_t s) {
-  // few rows: a CTA each (latency); many: four, which share the launch and its sines' set-up
-  const int tpc = a.rows >= 4 * 608 ? TPC_MAX : 1;
+  // A token a CTA while there are hardly more of them than run at once (8 an SM); more tokens go four to a CTA, which share
+  // the sines' set-up.  On the device, 48 heads: 8 tokens 3.1 us, four to a CTA 5.8; 1216 6.8 and 7.2; 1300 7.0 and 8.3; 1800
+  // 9.2 and 8.4; 2431 11.6 and 9.8.
+  const int tpc = a.rows > 10 * 152 ? TPC_MAX : 1;
   const unsigned grid = (unsigned)((a.rows + tpc - 1) / tpc);
   if (mode == IN_LANE) norm_rope_kernel<T, IN_LANE><<<grid, THREADS, 0, s>>>(a, tpc);
   else if (mode == ADJACENT) norm_rope_kernel<T, ADJACENT><<<grid, THREADS, 0, s>>>(a, tpc);

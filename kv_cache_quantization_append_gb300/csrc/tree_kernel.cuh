@@ -24,8 +24,12 @@
 // it once cost 6 us of latency.
 //
 // Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 68 us (95 TFLOP/s, 0.64 TB/s);
-// 128 rows over 8 sequences of up to 32K TQ3 641 us (150 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 141 us (151
-// TFLOP/s); 15 rows over 700 positions 21 us.
+// 128 rows over 8 sequences of up to 32K TQ3 644 us (149 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 137 us (156
+// TFLOP/s); 15 rows over 700 positions 22 us.  Bound in the long cases by the chain of one tile, one under way in a CTA: keys
+// in place, logits, softmax, weights in place, P V, and the hand-overs between them.  In trials that left work out of a
+// private copy the TQ3 case took 613 us without value conversion, 528 without the products of lo parts, 516 without either
+// and without key conversion, 465 without the weights' stores as well: 151 tiles of 64 rows a CTA at 3 us each.  The short
+// case is one pass' latency through both launches: lengths, table, records, product, softmax, product, join.
 //
 // Operands: each of K~, V~, Q~ and P is a pair of 16-bit values, hi and lo, and every product hi hi + hi lo + lo hi, so that
 // an output is the definition's up to its own rounding (1e-7 to 4e-6 of the largest beyond a bf16 output's half step).  fp16
@@ -44,12 +48,15 @@ namespace tree {
 using namespace tc;
 using namespace records;
 
-// Rows of a block (a CTA's): up to 16 take two threads to a position and two CTAs an SM, more take four threads and one CTA;
-// what else a block has to hold in shared memory ends at 96 rows, for TQ3 keys, whose queries come with their projections,
-// at 64.
+// Rows of a block (a CTA's): up to 16 take two threads to a position and two CTAs an SM (15 rows over 32K Q4 47 us, as a
+// block of one CTA an SM 64; over 4000 positions 27 and 23), more take four threads and one CTA.  What a block holds in shared
+// memory ends at 96 rows (192 rows over 4 x 9001 Q8 137 us, in blocks of 64 166), for TQ3 keys, whose queries come with their
+// projections, at 64 (128 rows over 8 x 32K 643 us, in blocks of 32 1222; two threads to a position 710).
 constexpr int FEW_ROWS = 16, MAX_ROWS = 96, TQ_ROWS = 64;
 // Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
-// a tile ahead), and belongs to the range that holds its first place.
+// a tile ahead), and belongs to the range that holds its first place.  Measured with 1, 2, 3, 4 and 5 places: 5 nodes at
+// 32K Q4 59, 52, 47, 59, 53 us; 16 nodes 82, 74, 68, 66, 68; 16 nodes over 2 x 2000 TQ3 45, 33, 45, 45, 48; six other sizes the
+// same within 5 %.
 constexpr int RAW_PLACES = 3;
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
@@ -1131,7 +1138,8 @@ cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
     if (p.N == 96) e = go<tree_kernel<KF, 24, F32, 4>>(grid, 544, smem, false, s, p);
   }
   if (e != cudaSuccess) return e;
-  // many records a row (few units over all CTAs): a CTA per row, else a warp per row
+  // Many records a row (few units over all CTAs): a CTA per row, else a warp per row.  16 nodes at 32K (8 units over 152 CTAs)
+  // 68 us, by warps 74; 64 nodes over 4 x 9001 (64 units) by warps 137, by CTAs 158.
   if (p.G > 8 * p.n_units) return go<tree_merge_kernel<true>>(dim3((unsigned)out_rows), MERGE_WARPS * 32, pre, true, s, p);
   return go<tree_merge_kernel<false>>(dim3((unsigned)((out_rows + MERGE_WARPS - 1) / MERGE_WARPS)), MERGE_WARPS * 32, pre, true, s, p);
 }

@@ -21,12 +21,11 @@
 // Each warp keeps its own reference per row, which moves only when a logit passes it by 2^60: no exchange between warps
 // until the range ends.
 //
-// Measured (a call): 4 rows of each of 8 KV heads over 8 sequences of up to 16K Q4 56 us (1.3 TB/s: 45 us of logits, 11
-// of the elementwise pass under a profiler), bound by the workers' chain per tile -- code conversion, barrier, product,
-// barrier, 4 rows of logits; 96 rows over 32K Q8 109 us, two passes of about 50, of which 8 us each are the queries'
-// preparation and code seen for the first time.  In that case dropping half of the products, three quarters of the
-// accumulators' reads and the sums over lanes together saves 12 %: what bounds it is not one pipe but the sequence of
-// short steps between barriers.
+// Measured (a call): 4 rows of each of 8 KV heads over 8 sequences of up to 16K Q4 54 us (1.3 TB/s, 9 of them the adding
+// pass), bound by the workers' chain per tile -- code conversion, barrier, product, barrier, 4 rows of logits; 96 rows over
+// 32K Q8 111 us, two passes of about 50, of which 8 us each are the queries' preparation and code seen for the first time.  In
+// that case dropping half of the products, three quarters of the accumulators' reads and the sums over lanes together saves
+// 12 %: what bounds it is not one pipe but the sequence of short steps between barriers.
 #pragma once
 
 #include "records.cuh"
@@ -45,9 +44,10 @@ constexpr int MAX_ROWS = 128;   // of a launch
 // have room for two at 128 rows, and one with four threads was no faster (96 rows over 32K Q8: 113 us against 111).
 constexpr int NARROW_ROWS = 64;
 constexpr int ADD_THREADS = 256;
-// Places in the list of tiles: a raw tile counts as five of records (it comes with queries of its own), and belongs to the
-// range that holds its first place.  (32 queries at 32K Q8: three 112 us, four 110, five 109.)
-constexpr int RAW_PLACES = 5;
+// Places in the list of tiles: a raw tile counts as four of records (it comes with queries of its own), and belongs to the
+// range that holds its first place.  Measured with 3, 4, 5 and 6 places: 16 queries over 4 x 1000 Q4 39, 41, 57, 59 us; a
+// step over 8 x 16K 56, 54, 56, 56; 32 queries at 32K Q8 114, 111, 110, 108; six other sizes the same within 3 %.
+constexpr int RAW_PLACES = 4;
 
 struct Plan {
   MultiArgs a;
