@@ -69,7 +69,9 @@ class QuantKVCache:
         kv_quant_append(self.handle, layer, k, v, pos, stream)
 
     def calibrate(self, layer: int, k_calib: torch.Tensor, v_calib: torch.Tensor, stream=None):
-        work = self._workspace("calibrate", kv_calibrate_scratch_bytes, (layer, k_calib.shape[-2]), stream)
+        need = kv_calibrate_scratch_bytes(self.handle, layer, k_calib.shape[-2])
+        with torch.cuda.stream(stream):  # (given back to the stream that used it)
+            work = torch.empty(need, dtype=torch.uint8, device=self.buffer.device)
         kv_calibrate(self.handle, layer, k_calib, v_calib, work, stream)
 
     def decode(self, layer: int, q: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor | None = None,

@@ -131,3 +131,14 @@ def test_the_library_refuses_a_call_while_another_device_is_current(made):
         assert call(1 << 60) == 1
     torch.cuda.synchronize()
     assert torch.equal(before, gpu.buffer) and not buf.any()
+
+
+def test_calibration_keeps_no_workspace():
+    """Calibration happens once: its copies (here 16 MB) go back to the allocator."""
+    gpu, _, _ = harness.make_pair(1, 2, 2, 1, 64, window=0, sinkhorn=True)
+    x = torch.randn(2, 4096, 128, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    gpu.calibrate(0, x, x, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
