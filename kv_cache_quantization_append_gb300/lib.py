@@ -321,7 +321,6 @@ def kv_qk_norm_rope(rope: kvq_rope, qkv: torch.Tensor, positions: torch.Tensor, 
     sb, st, s1 = qkv.stride()
     if row > 1 and s1 != 1 or T > 1 and B > 1 and sb != T * st:
         raise KVQError("qkv's rows must be contiguous and of one stride")
-    st = st if T > 1 else sb if B > 1 else row
     if q.dim() != 4 and not (T == 1 and q.dim() == 3) or k.dim() != q.dim():
         raise KVQError(f"q and k must be [B][heads][T][128], got {tuple(q.shape)} and {tuple(k.shape)}")
     hq, hkv = q.shape[1], k.shape[1]
@@ -331,7 +330,9 @@ def kv_qk_norm_rope(rope: kvq_rope, qkv: torch.Tensor, positions: torch.Tensor, 
     _check_shape("positions", positions, (B, T))
     if v is not None:
         _check_shape("v", v, tuple(k.shape))
-    if row < (hq + (1 if v is None else 2) * hkv) * 128:
+    need = (hq + (1 if v is None else 2) * hkv) * 128
+    st = st if T > 1 else sb if B > 1 else need  # (a single row has no stride)
+    if row < need:
         raise KVQError(f"qkv rows hold {row} values, fewer than their heads")
     for w in (q_weight, k_weight):
         if w is not None:

@@ -32,3 +32,15 @@ def test_a_failed_query_does_not_fail_the_next_call():
         call()
     torch.cuda.synchronize()
     assert gpu.status() == 0
+
+
+def test_a_single_row_of_any_width():
+    """One row of projections with a few values behind its heads: there is no second row that its width could misalign."""
+    rope = lib.kv_rope_init(128)
+    wide = torch.randn(1, 1, 3 * 128 + 3, device="cuda")
+    outs = []
+    for x in (wide, wide[:, :, :3 * 128].contiguous()):
+        q, k, v = (torch.empty(1, 1, 1, 128, device="cuda") for _ in range(3))
+        lib.kv_qk_norm_rope(rope, x, torch.full((1, 1), 5, dtype=torch.int32, device="cuda"), q, k, v)
+        outs.append(torch.cat([q, k, v]))
+    assert torch.equal(*outs)
