@@ -38,11 +38,13 @@
 //  * The output row is normalised, unfolded (sigma_v) and unrotated at the end.
 #include <cfloat>
 
-#include "kvq_internal.cuh"
+#include "tc.cuh"
 
 namespace kvq {
 
 namespace {
+
+using namespace tc;
 
 constexpr int ROWS = 128;    // (query, head) rows per CTA = MMA M = TMEM lanes
 constexpr int NT = 64;       // key positions per tile (one page) = logits N
@@ -85,29 +87,7 @@ struct Cfg {
   static_assert((uint32_t)ROWS * (D + 4) * 4 <= SMEM, "output staging fits the ring");
 };
 
-// ------------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long gtimer() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
+// ------------------------------------------------------------------ PTX helpers (besides tc.cuh's)
 // Bounded wait on a phase.  false: this CTA gave up (another role gave up first, or ~1 s passed:
 // the status word gets KVQ_DEV_TIMEOUT and the CTA's abort flag is raised).
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
@@ -124,35 +104,6 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
     }
   }
 }
-// make this thread's generic shared-memory writes visible to the tensor core (async proxy)
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// shared-memory matrix descriptor: K-major, no swizzle; lbo = byte stride between core matrices
-// along K, sbo = byte stride between 8-row groups
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T, issued by the warp's elected lane (lane 0 of a converged warp);
-// every lane of the warp executes the call
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p, e;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-// arrive on bar once every tcgen05 operation the elected lane issued so far has completed (the
-// same lane that issued the products: elect.sync picks the lowest lane of a converged warp)
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-
 #define KVQ_R8(o, i) o(r[i + 0]), o(r[i + 1]), o(r[i + 2]), o(r[i + 3]), o(r[i + 4]), o(r[i + 5]), o(r[i + 6]), o(r[i + 7])
 #define KVQ_OUT(x) "=r"(x)
 #define KVQ_IN(x) "r"(x)
@@ -178,22 +129,6 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
           taddr),
       KVQ_R8(KVQ_IN, 0), KVQ_R8(KVQ_IN, 8)
       : "memory");
-}
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-// fp16 hi/lo split of a pair: hi = fp16(v), lo = fp16(v - hi); element a in the low half
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 hf = __half22float2(h);
-  hi = h2u(h);
-  lo = h2u(__floats2half2_rn(a - hf.x, b - hf.y));
 }
 // 8 consecutive K-elements of one row as hi and lo 16-byte chunks
 __device__ __forceinline__ void store8(uint8_t* hi_plane, uint8_t* lo_plane, uint32_t off, const float (&v)[8]) {
@@ -293,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                  "r"(TMEM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    tc_fence_before();
+    fence_before();
   }
 
   // ---- query tile: q~ = c H (s . q) [. sigma_k] in base-2 logit units (TQ3: also S q~), staged as
@@ -346,7 +281,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     }
   }
   __syncthreads();
-  tc_fence_after();
+  fence_after();
   const uint32_t tmem = tmem_base_sh;
   if (warp < N_SOFT) {
     // row = TMEM lane 32 warp + lane: column c of a plane holds K-elements 2c (low half), 2c + 1
@@ -369,9 +304,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       }
     tm_wait_st();
   }
-  tc_fence_before();
+  fence_before();
   __syncthreads();
-  tc_fence_after();
+  fence_after();
 
   auto tile_j0 = [&](int it) { return it < nqt ? it * NT : rbeg + (it - nqt) * NT; };
 
@@ -392,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         ok = __all_sync(FULL, bar_wait(&kfull[s], (it / NS) & 1, &abort_sh, a.p.status) &&
                                   (it < 2 || bar_wait(&pvdone[bb], ((it - 2) >> 1) & 1, &abort_sh, a.p.status)));
         if (!ok) break;
-        tc_fence_after();
+        fence_after();
         uint64_t kh = sdesc(sbase + s * C::STAGE, 1024, 128);
         uint32_t qa = tmem + C::C_QHI;
         const uint32_t dS = tmem + C::C_S + NT * bb;
@@ -431,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         ok = __all_sync(FULL, bar_wait(&pfull[bb], (it >> 1) & 1, &abort_sh, a.p.status) &&
                                   bar_wait(&vfull[s], (it / NS) & 1, &abort_sh, a.p.status));
         if (!ok) break;
-        tc_fence_after();
+        fence_after();
         uint64_t vh = sdesc(sbase + s * C::STAGE + C::V_OFF, 2048, 128);
         uint32_t pa = tmem + C::C_S + NT * bb;
 #pragma unroll 1
@@ -727,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         ok = false;
         break;
       }
-      tc_fence_after();
+      fence_after();
       uint32_t sr[2][32];
       tm_ld32(lane_addr + C::C_S + NT * bb, sr[0]);
       tm_ld32(lane_addr + C::C_S + NT * bb + 32, sr[1]);
@@ -759,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           ok = false;
           break;
         }
-        tc_fence_after();
+        fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
@@ -791,13 +726,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       }
       lsum += ls0 + ls1;
       tm_wait_st();
-      tc_fence_before();
+      fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&pfull[bb]);
     }
     // ---- epilogue: O / l, unfold sigma_v, undo the rotation
     if (ok && __all_sync(FULL, bar_wait(&ofull, 0, &abort_sh, a.p.status))) {
-      tc_fence_after();
+      fence_after();
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
       float* sO = reinterpret_cast<float*>(smem);  // [ROWS][D + 4]: the ring is idle once every product landed
 #pragma unroll 1
@@ -832,10 +767,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   }
 
   // ---- tear-down: every tensor-memory access of the CTA is done before the columns are freed
-  tc_fence_before();
+  fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
-    tc_fence_after();
+    fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   }
 }
