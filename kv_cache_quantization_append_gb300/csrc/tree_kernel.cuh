@@ -64,6 +64,9 @@ constexpr float NO_REF = -1e30f;  // reference of a row that has met no position
 // end at 2^-24: with the first tile's largest at 1 the positions behind an early sink 17 above them lost a third of their
 // weight in sums of 6400 positions (2.4e-3 of the output); at 2^7 what is lost is below 2^-32 of the sink's weight each.
 constexpr float START = 7.f, MOST = 15.f;
+// Tiles whose P V share an accumulator.  The tensor cores cut off each sum's low bits, 24 sums a tile: 512 tiles in one lost
+// 3e-4 of the output, 16 lose 2.3e-5 at most and are then added to the part's record with rounding to nearest (128 rows over 8 x 32K TQ3 645 us -> 654).
+constexpr int DRAIN = 16;
 
 // what the launches share: sizes from the host, pointers into the caller's scratch
 struct Plan {
@@ -317,6 +320,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh, leave_sh[2];  // leave_sh: what the workers act on, by turns of the tiles
   __shared__ __align__(16) float mref[N], fac[N];
+  __shared__ float mrec[N];  // the references of the part's record so far
   __shared__ float wmax[4][N];
   __shared__ unsigned long long nodes[KVQ_MAX_TREE];  // ancestors-or-self of each node (0: not there)
   // columns (rows of the unit) that are there and at depth at most i; that have node i among their ancestors-or-self
@@ -539,7 +543,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
         const uint32_t id = raw ? ID_O | RAW_TYPE : ID_O;
 #pragma unroll 4
         for (int ks = 0; ks < TILE / 16; ++ks, va += 256, pa += 2 * N) {
-          mma_ss(tmem + C_O, va, pa, id, it > it0 || ks > 0);
+          mma_ss(tmem + C_O, va, pa, id, (it - it0) % DRAIN > 0 || ks > 0);
           mma_ss(tmem + C_O, va + LO_V, pa, id, 1);
           mma_ss(tmem + C_O, va, pa + LO_P, id, 1);
         }
@@ -708,6 +712,29 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       v_scale = __int_as_float((127 + 14 - (e - 127)) << 23);
       v_unscale = __int_as_float((127 - 14 + (e - 127)) << 23);
     }
+    // adds the accumulated O (of products that are done) to the part's record, whose first it may be
+    float* const rec = record_of(w);
+    const int ch = (ln.t & ~7) + nibble_channel(ln.t & 7);  // tensor-memory lane = place of the channel
+    const auto drain = [&](bool first) {
+      if (!first) {
+        if (tid < N) fac[tid] = ex2(mrec[tid] - mref[tid]);
+        part_sync(1, WORKERS);
+      }
+      if (tid < N) mrec[tid] = mref[tid];
+      fence_after();
+#pragma unroll 1
+      for (int c = 0; c < NC; c += CH) {
+        float o[CH];
+        tm_ld(lane_addr + C_O + col0 + c, o);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          float* at = rec + 2 * N + (col0 + c + i) * D + ch;
+          const float v = F32 ? o[i] * v_unscale : o[i];
+          *at = first ? v : fmaf(*at, fac[col0 + c + i], v);
+        }
+      }
+    };
     fence_async_smem();
     part_sync(1, WORKERS);  // the columns' masks and references
     float l[NC];
@@ -782,6 +809,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       k_done();
       // ---- values, while the logits run (the previous tile's P V must be done with their place)
       wait_pv();
+      if (it > it0 && (it - it0) % DRAIN == 0) drain(it - it0 == DRAIN);
       if (!raw) {
         wait(&vr_bar, vr_phase);
         put_v<KF, P>(smem + SM::V, ln, rec_sh, checked(vpage, a.L.n_pages) >= 0 ? qend - it * TILE - 2 * ln.vp : 0);
@@ -869,7 +897,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
             mref[tid] = m1;
           }
           part_sync(1, WORKERS);
-          if (it > it0) {
+          if (it > it0) {  // (O where it has just been drained is overwritten)
 #pragma unroll
             for (int c = 0; c < NC; ++c) l[c] *= fac[col0 + c];
 #pragma unroll 1
@@ -935,8 +963,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
     if (!ok) break;
     // ---- the range's part of the unit: reference, sum and O of every row
     wait_pv();
-    fence_after();
-    float* rec = record_of(w);
+    drain(it1 - it0 <= DRAIN);
     // sums over the lanes; after three exchanges the lanes of one lane & 7 have NC / 8 columns, by its bits in reverse
     halve<NC / 2, 1>(l, lane);
     halve<NC / 4, 2>(l, lane);
@@ -948,15 +975,6 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
       s += __shfl_xor_sync(FULL, s, 8);
       s += __shfl_xor_sync(FULL, s, 16);
       if (lane < 8) wmax[warp & 3][col0 + lc + c] = s;
-    }
-    const int ch = (ln.t & ~7) + nibble_channel(ln.t & 7);  // tensor-memory lane = place of the channel
-#pragma unroll 1
-    for (int c = 0; c < NC; c += CH) {
-      float o[CH];
-      tm_ld(lane_addr + C_O + col0 + c, o);
-      tm_wait_ld();
-#pragma unroll
-      for (int i = 0; i < CH; ++i) rec[2 * N + (col0 + c + i) * D + ch] = F32 ? o[i] * v_unscale : o[i];
     }
     fence_before();
     if (part_or(1, WORKERS, gave_up())) {

@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+from kv_cache_quantization_append_gb300 import lib
+
 from . import harness
 from . import ops_reference as ref
 from .test_gpu_tree import TOL, _drafts, _fill
@@ -196,3 +198,28 @@ def test_where_a_chain_is_what_single_tokens_see(window):
         step = ora.decode(0, harness.to_np(q[:, :, i]), np.array([91 + i]))
         err = np.abs(got[:, :, i] - step).max() / np.abs(step).max()
         assert err <= TOL["f32"] if i < window else err > 10 * TOL["f32"], (i, err)
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_long_contexts_sum_as_short_ones(in_dtype):
+    """512 tiles in one CTA (320 units that share their pages), values of one sign: the tensor cores cut off every sum's low
+    bits, so that 512 tiles of 24 sums in one accumulator would lose 512 * 24 * 2^-24 = 7e-4 of the last sum, half of it on the
+    way up to it.  Sums of 16 tiles lose 2.3e-5 at most, and are joined with rounding to nearest."""
+    rng = np.random.default_rng(31)
+    B, L = 160, 65536
+    pages = np.tile(np.arange(L // 64, dtype=np.int32), (B, 1))
+    gpu, _, _ = harness.make_pair(1, 2, 2, B, L, window=0, in_dtype=in_dtype, n_pages=L // 64, block_table=pages)
+    ora = harness.make_pair(1, 2, 2, 1, L, window=0, in_dtype=in_dtype)[1]
+    dt = torch.bfloat16 if in_dtype == "bf16" else torch.float32
+    for at in range(0, L, 8192):
+        k = torch.as_tensor(rng.standard_normal((1, 2, 8192, 128)).astype(np.float32)).to(dt)
+        v = torch.as_tensor((1 + 0.3 * rng.standard_normal((1, 2, 8192, 128))).astype(np.float32)).to(dt)
+        one = lib.kvq_cache.from_buffer_copy(gpu.handle)       # (the first sequence's pages are everyone's)
+        lib.kv_quant_append(one, 0, k.cuda(), v.cuda(), _i32([at]))
+        ora.append(0, harness.to_np(k), harness.to_np(v), np.array([at]))
+    k, v, q = _drafts(rng, gpu.cfg, 1, 1, in_dtype)
+    wide = lambda t: t.expand(B, *t.shape[1:]).contiguous()  # noqa: E731
+    got = _tree(gpu, wide(k), wide(v), wide(q), [L] * B, [[-1]] * B)
+    want = ref.tree_attention(ora, 0, *(harness.to_np(t) for t in (k, v, q)), np.array([L]), np.array([[-1]]))
+    err = np.abs(got - want) - _half_step(in_dtype, want)
+    assert err.max() <= 0.25 * TOL["f32"] * np.abs(want).max(), err.max() / np.abs(want).max()
