@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   __shared__ bool sick_sh[P][TILE];  // a raw position's values (by the threads that share it) were not all finite
   __shared__ int vtop;  // float caches: largest raw value of the part, as an integer
   const MultiArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem + SM::total(N));
   int* lens = pre + a.batch + 1;
 
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_sh, sbase = smem_u32(smem);
+  const uint32_t tmem = __shfl_sync(FULL, tmem_sh, 0), sbase = smem_u32(smem);
 
   // this CTA's range of the list of tiles
   const long long per_layer = (long long)pre[a.batch] * a.Hkv * p.rb, total = per_layer * a.n_layers_call;
@@ -441,6 +441,10 @@ __global__ void __launch_bounds__(128 * P + 32, P == 4 ? 1 : 2) tree_kernel(cons
 
     const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
     if (warp == WARPS) {
+      // (taken from one lane, as the warp's number and the tensor memory's address: its lanes branch together by construction,
+      // and the products' operands are computed once for the warp)
+      const int it0 = __shfl_sync(FULL, w.it0, 0), it1 = __shfl_sync(FULL, w.it1, 0);
+      const bool raw = __shfl_sync(FULL, (int)w.raw, 0) != 0;
       // ================================================================ the products and the copies
       const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
       using R = Rec<KF>;

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   __shared__ int abort_sh;
   __shared__ float part_sum[2][P - 1][TILE];  // of the groups of columns after the first, by turns of the tiles
   const MultiArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, NR = p.nb * N;
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31, NR = p.nb * N;
   const uint32_t q_plane = SM::plane(NR);
   float* qs = reinterpret_cast<float*>(smem + SM::qs(NR));
   int* pre = reinterpret_cast<int*>(smem + SM::pre(NR));
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_sh, sbase = smem_u32(smem);
+  const uint32_t tmem = __shfl_sync(FULL, tmem_sh, 0), sbase = smem_u32(smem);
   const long long per_layer = (long long)pre[a.batch] * a.Hkv, total = per_layer * a.n_layers_call;
   const long long G = min((long long)p.G, total);
   long long t = blockIdx.x < G ? quick_div(total * blockIdx.x, G) : 0;
@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(128 * P + 32, 4 / P) weights_kernel(const __gr
     const int* bt = a.block_table + (size_t)b * a.max_pages_per_seq;
 
     if (warp == WARPS) {
+      // (taken from one lane, as the warp's number and the tensor memory's address: its lanes branch together by construction,
+      // and the products' operands are computed once for the warp)
+      const int it0 = __shfl_sync(FULL, w.it0, 0), it1 = __shfl_sync(FULL, w.it1, 0);
+      const bool raw = __shfl_sync(FULL, (int)w.raw, 0) != 0;
       // ================================================================ the products and the copies
       const uint8_t* unit_pages = a.p.pages + ((size_t)layer * a.L.n_pages * a.Hkv + h) * (size_t)a.L.page_bytes;
       using R = Rec<KF>;
