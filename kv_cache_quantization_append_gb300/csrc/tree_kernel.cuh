@@ -23,21 +23,21 @@
 // Rotating the queries and following the parents is done again by every CTA that needs them: a kernel in front that did
 // it once cost 6 us of latency.
 //
-// Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 68 us (95 TFLOP/s, 0.64 TB/s);
-// 128 rows over 8 sequences of up to 32K TQ3 644 us (149 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 137 us (156
-// TFLOP/s); 15 rows over 700 positions 22 us.  Bound in the long cases by the chain of one tile, one under way in a CTA: keys
-// in place, logits, softmax, weights in place, P V, and the hand-overs between them.  In trials that left work out of a
-// private copy the TQ3 case took 613 us without value conversion, 528 without the products of lo parts, 516 without either
-// and without key conversion, 465 without the weights' stores as well: 151 tiles of 64 rows a CTA at 3 us each.  The short
-// case is one pass' latency through both launches: lengths, table, records, product, softmax, product, join.
+// Measured (a call, both launches): 48 rows of each of 8 KV heads over 32K positions Q4 60 us (108 TFLOP/s, 0.72 TB/s);
+// 128 rows over 8 sequences of up to 32K TQ3 516 us (187 TFLOP/s); 192 rows over 4 sequences of up to 9001 Q8 119 us (180
+// TFLOP/s); 15 rows over 700 positions 22.5 us.  Bound in the long cases by the chain of one tile, one under way in a CTA.  By
+// clocks read in a private copy, TQ3 and 64 rows, a tile takes 6200 cycles: keys' records 500, key conversion 1250, the end of
+// the last P V 400, value conversion 1750 (the logits are issued meanwhile, 54 cycles a product), logits 350, softmax 1500, and
+// hand-overs.  The short case is one pass' latency through both launches: lengths, table, records, product, softmax, product,
+// join.
 //
 // Operands: each of K~, V~, Q~ and P is a pair of 16-bit values, hi and lo, and every product hi hi + hi lo + lo hi, so that
 // an output is the definition's up to its own rounding (1e-7 to 4e-6 of the largest beyond a bf16 output's half step).  fp16
-// pairs hold 22 bits of records; once-rounded fp16 operands took 18.5, 48, 250 and 96 us for the cases above, but their
+// pairs hold 22 bits of records; once-rounded fp16 operands took 48, 250, 96 and 18.5 us for the cases above, but their
 // errors, up to 1.3e-3 of the largest output where attention is peaked, came on top of the output's rounding.  Raw vectors
 // of a bf16 cache are bf16 pairs, which hold 16 bits of any magnitude (its queries one, exactly); a float cache's are fp16
-// pairs, the values scaled.  TQ3 keys are [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's weight w =
-// sqrt(pi/2)/128 gamma is a pair, and the thread that owns the position multiplies by the norm n.
+// pairs, the values scaled.  TQ3 keys are [c, +-w], 256 wide against [q~, S q~]: the centroids c are exact, the residual's
+// weight w = sqrt(pi/2)/128 gamma is a pair, and the thread that owns the position multiplies by the norm n.
 #pragma once
 
 #include "records.cuh"
@@ -48,15 +48,15 @@ namespace tree {
 using namespace tc;
 using namespace records;
 
-// Rows of a block (a CTA's): up to 16 take two threads to a position and two CTAs an SM (15 rows over 32K Q4 47 us, as a
-// block of one CTA an SM 64; over 4000 positions 27 and 23), more take four threads and one CTA.  What a block holds in shared
-// memory ends at 96 rows (192 rows over 4 x 9001 Q8 137 us, in blocks of 64 166), for TQ3 keys, whose queries come with their
-// projections, at 64 (128 rows over 8 x 32K 643 us, in blocks of 32 1222; two threads to a position 710).
+// Rows of a block (a CTA's): up to 16 take two threads to a position and two CTAs an SM (15 rows over 32K Q4 46 us, as a
+// block of one CTA an SM 56; over 4000 positions 27 and 23), more take four threads and one CTA.  What a block holds in
+// shared memory ends at 96 rows (192 rows over 4 x 9001 Q8 118 us, in blocks of 64 140), for TQ3 keys, whose queries come
+// with their projections, at 64 (128 rows over 8 x 32K 515 us, in blocks of 32 948).
 constexpr int FEW_ROWS = 16, MAX_ROWS = 96, TQ_ROWS = 64;
 // Places in the list of tiles: a raw tile counts as three of records (its rows come as fp32 or bf16 and are not requested
-// a tile ahead), and belongs to the range that holds its first place.  Measured with 1, 2, 3, 4 and 5 places: 5 nodes at
-// 32K Q4 59, 52, 47, 59, 53 us; 16 nodes 82, 74, 68, 66, 68; 16 nodes over 2 x 2000 TQ3 45, 33, 45, 45, 48; six other sizes the
-// same within 5 %.
+// a tile ahead), and belongs to the range that holds its first place.  Measured with 1 to 5 places: 5 nodes at 32K Q4 58, 52,
+// 46, 59, 52 us; 16 nodes 72, 66, 60, 56, 56; 16 nodes over 2 x 2000 TQ3 43, 31, 43, 43, 45; six other sizes the same within
+// 6 %.
 constexpr int RAW_PLACES = 3;
 constexpr int MERGE_WARPS = 8;
 constexpr float NO_REF = -1e30f;  // reference of a row that has met no position yet
@@ -65,7 +65,8 @@ constexpr float NO_REF = -1e30f;  // reference of a row that has met no position
 // weight in sums of 6400 positions (2.4e-3 of the output); at 2^7 what is lost is below 2^-32 of the sink's weight each.
 constexpr float START = 7.f, MOST = 15.f;
 // Tiles whose P V share an accumulator.  The tensor cores cut off each sum's low bits, 24 sums a tile: 512 tiles in one lost
-// 3e-4 of the output, 16 lose 2.3e-5 at most and are then added to the part's record with rounding to nearest (128 rows over 8 x 32K TQ3 645 us -> 654).
+// 3e-4 of the output, 16 lose 2.3e-5 at most and are then added to the part's record with rounding to nearest (1 % of the
+// time).
 constexpr int DRAIN = 16;
 
 // what the launches share: sizes from the host, pointers into the caller's scratch
@@ -1161,7 +1162,7 @@ cudaError_t launch(const MultiArgs& a, int sms, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   // Many records a row (few units over all CTAs): a CTA per row, else a warp per row.  16 nodes at 32K (8 units over 152 CTAs)
-  // 68 us, by warps 74; 64 nodes over 4 x 9001 (64 units) by warps 137, by CTAs 158.
+  // 60 us, by warps 67; 64 nodes over 4 x 9001 (64 units) by warps 118, by CTAs 140.
   if (p.G > 8 * p.n_units) return go<tree_merge_kernel<true>>(dim3((unsigned)out_rows), MERGE_WARPS * 32, pre, true, s, p);
   return go<tree_merge_kernel<false>>(dim3((unsigned)((out_rows + MERGE_WARPS - 1) / MERGE_WARPS)), MERGE_WARPS * 32, pre, true, s, p);
 }

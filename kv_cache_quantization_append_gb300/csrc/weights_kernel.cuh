@@ -21,11 +21,12 @@
 // Each warp keeps its own reference per row, which moves only when a logit passes it by 2^60: no exchange between warps
 // until the range ends.
 //
-// Measured (a call): 4 rows of each of 8 KV heads over 8 sequences of up to 16K Q4 54 us (1.3 TB/s, 9 of them the adding
+// Measured (a call): 4 rows of each of 8 KV heads over 8 sequences of up to 16K Q4 49 us (1.5 TB/s, 9 of them the adding
 // pass), bound by the workers' chain per tile -- code conversion, barrier, product, barrier, 4 rows of logits; 96 rows over
-// 32K Q8 111 us, two passes of about 50, of which 8 us each are the queries' preparation and code seen for the first time.  In
-// that case dropping half of the products, three quarters of the accumulators' reads and the sums over lanes together saves
-// 12 %: what bounds it is not one pipe but the sequence of short steps between barriers.
+// 32K Q8 93 us, two passes of about 42, of which 8 us each are the queries' preparation and code seen for the first time.
+// Before the issuing warp's values were taken from one lane (111 us) leaving out half of the products, three quarters of the
+// accumulators' reads and the sums over lanes together saved 12 %: what bounds it is not one pipe but the sequence of short
+// steps between barriers.
 #pragma once
 
 #include "records.cuh"
@@ -40,13 +41,13 @@ constexpr float NO_REF = -1e30f;
 constexpr int STORE_ROWS = 8;
 constexpr int MAX_ROWS = 128;   // of a launch
 // Rows of TQ3 keys whose queries (1 KB a row with their projections) leave room for two CTAs an SM.  More take one CTA an
-// SM with four threads to a position (96 rows over 32K: 160 us, in two launches of 64 and 32 rows 268); the other formats
-// have room for two at 128 rows, and one with four threads was no faster (96 rows over 32K Q8: 113 us against 111).
+// SM with four threads to a position (96 rows over 32K: 125 us, with two threads 203); the other formats have room for two
+// at 128 rows, and one with four threads was no faster (96 rows over 32K Q8: 113 us against 111).
 constexpr int NARROW_ROWS = 64;
 constexpr int ADD_THREADS = 256;
 // Places in the list of tiles: a raw tile counts as four of records (it comes with queries of its own), and belongs to the
-// range that holds its first place.  Measured with 3, 4, 5 and 6 places: 16 queries over 4 x 1000 Q4 39, 41, 57, 59 us; a
-// step over 8 x 16K 56, 54, 56, 56; 32 queries at 32K Q8 114, 111, 110, 108; six other sizes the same within 3 %.
+// range that holds its first place.  Measured with 2 to 6 places: 16 queries over 4 x 1000 Q4 35, 36, 38, 49, 54 us; a step over
+// 8 x 16K 51, 50, 49, 49, 50; 32 queries at 32K Q8 101, 95, 92, 91, 90; five other sizes the same within 8 %.
 constexpr int RAW_PLACES = 4;
 
 struct Plan {
