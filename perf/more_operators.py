@@ -232,7 +232,9 @@ def _buffers(c, layers, B, mpp, n_pages, hq, dtype, bt):
         s["ring_v"] = cache.buffer[off - rb:off - rb + nf].view(torch.float32).view(ring)
         s["ring_k"] = cache.buffer[off - 2 * rb:off - 2 * rb + nf].view(torch.float32).view(ring)
         if c["op"] not in ("decode", "prefill"):
-            cache.pool_init()
+            table = bt.clone()
+            cache.pool_init()                                              # (clears the table)
+            bt.copy_(table)
             s["refs"] = cache.page_refs
         s["pages"].zero_()
     else:
