@@ -30,7 +30,7 @@
  *     length out of range, a pipeline wait that gave up) set bits in the cache's device status
  *     word, read with kv_status.
  *   - head_dim is 128; n_q_heads is a multiple of n_kv_heads with a GQA group of 1..4 query heads
- *     per kv-head; page_tokens is 64; window is 0 or a multiple of 4 up to 1024.
+ *     per kv-head; page_tokens is 64; window is 0 or a multiple of 4 up to 1024 (from 32 for KVQ_Q8B32).
  */
 #ifndef KVQ_H
 #define KVQ_H
@@ -60,6 +60,8 @@ enum {
   KVQ_DEV_SEQLEN_RANGE = 4u,   /* seq_lens[b] < 0 or > max_seq_len: treated as empty */
   KVQ_DEV_TIMEOUT = 8u,        /* a wait within a kernel gave up (kv_set_wait_limit_ns): output is incomplete */
   KVQ_DEV_BAD_NODE = 16u,      /* a tree node's parent is not an earlier node, or a path entry is no node: skipped */
+  KVQ_DEV_NO_PAGES = 32u,      /* the pool has fewer free pages than a sequence needs: it got none (kv_pool_reserve) */
+  KVQ_DEV_BAD_PARENT = 64u,    /* a parent is no sequence of the call: the sequence was left as it is (kv_pool_fork) */
 };
 
 /* ---------------------------------------------------------------- formats */
@@ -68,6 +70,8 @@ enum {
   KVQ_TQ3_QJL = 3,   /* keys only: 3-bit Lloyd-Max codes of the unit vector, fp16 norm, 128 QJL
                         residual sign bits and fp16 residual norm */
   KVQ_Q8G32 = 4,     /* keys only: 8-bit symmetric codes, groups of 32 channels, fp16 scale */
+  KVQ_Q8B32 = 5,     /* keys and values together: 8-bit symmetric codes, one float scale for each block of 32 tokens of a
+                        kv-head (and for keys and values each) */
 };
 enum { KVQ_IN_F32 = 0, KVQ_IN_BF16 = 1 };
 
@@ -81,8 +85,8 @@ typedef struct kvq_config {
   int32_t window;        /* most recent tokens also kept in FP32; 0 = flat 4-bit ([QC]: 128) */
   int32_t page_tokens;   /* 64 */
   int32_t n_pages;       /* physical pages per layer; 0 = max_batch * ceil(max_seq_len / 64) */
-  int32_t k_format;      /* KVQ_Q4G32, KVQ_TQ3_QJL or KVQ_Q8G32 */
-  int32_t v_format;      /* KVQ_Q4G32 */
+  int32_t k_format;      /* KVQ_Q4G32, KVQ_TQ3_QJL, KVQ_Q8G32 or KVQ_Q8B32 */
+  int32_t v_format;      /* KVQ_Q4G32; KVQ_Q8B32 with KVQ_Q8B32 keys (then window is at least 32) */
   int32_t sinkhorn;      /* 1 = per-channel balancing scales (not with KVQ_TQ3_QJL keys) */
   int32_t group;         /* 32 */
   int32_t in_dtype;      /* KVQ_IN_F32 or KVQ_IN_BF16: dtype of k, v, q and calibration inputs */
@@ -133,6 +137,13 @@ typedef struct kvq_cache {
  *   TQ3_QJL K record (64 B per token): byte j holds the 3-bit codes of channels 2j (bits 0-2) and
  *     2j + 1 (bits 3-5) and the QJL sign bits (1 = (S r)_i >= 0) of projections i = 2j (bit 6) and
  *     2j + 1 (bit 7).
+ *   Q8B32: a half is one block, 8208 B: key codes at 0, value codes at 4096, then at 8192 the float scales of the
+ *     keys and of the values and 8 bytes that nothing reads.  Codes are stored as u = c + 128 (c in -127..127).
+ *     Key code of token t, channel c:   512 (4 (t / 16) + c / 32) + 16 (4 (t mod 8) + (c mod 8) / 2) + 8 (c / 16 mod 2)
+ *                                       + 4 (c / 8 mod 2) + 2 (t / 8 mod 2) + c mod 2
+ *     value code of token t, channel c: 4096 + 512 (c / 16) + 16 (4 (c mod 8) + (t mod 8) / 2) + 8 (t / 16)
+ *                                       + 4 (t / 8 mod 2) + 2 (c / 8 mod 2) + t mod 2
+ *     A block is written when its 32nd token is appended; until then its tokens are in the window ring only.
  */
 
 /*
@@ -199,6 +210,12 @@ int kv_calibrate(kvq_cache* cache, int32_t layer, const void* k_calib, const voi
  *   k, v       device, cfg.in_dtype, [L?][batch][n_kv_heads][n_tokens][128], contiguous
  *   pos        device int32 [batch]; pos[b] < 0 leaves sequence b untouched (lets a caller
  *              append ragged chunks to a subset of the batch)
+ * KVQ_Q8B32: the scale of a block of 32 tokens is the largest magnitude of its rotated (and balanced) values / 127, in
+ * float, for keys and for values; code = clamp(rint(y / scale), -127, 127), 0 where the scale is 0.  A block is coded
+ * once, by the call that appends its last token, from that call's vectors and, for earlier tokens, the window ring's
+ * raw ones: so a call at pos[b] relies on the ring holding the tokens from 32 (pos[b] / 32) on, as the calls before
+ * left it.  Every position that has left the window (at least 32) lies in a finished block.  These values need only be
+ * finite; where max |y| / 127 underflows, codes saturate.
  * Value range: scales, zeros, norms and sigma are stored as fp16, so each vector must be finite
  * with Euclidean norm below 65504 (after division by sigma when balanced; the rotation keeps the
  * norm).  TQ3 keys must also be zero or have some rotated element above 2^-75 in magnitude: when
@@ -353,7 +370,8 @@ int kv_qk_norm_rope(const kvq_rope* rope, const void* qkv, int64_t row_stride, c
  *   scratch      device, >= kv_tree_scratch_bytes(cache, layer, batch, n_nodes) bytes, any contents; calls that
  *                share it must not overlap on the GPU
  * Results do not depend on timing.  May be captured in a CUDA graph once a call of the same cache has run
- * outside capture.
+ * outside capture.  Trees, their commits, attention weights and eviction are not offered for KVQ_Q8B32 caches
+ * (KVQ_ERR_UNSUPPORTED): a block's positions share a scale and are written together.
  */
 #define KVQ_MAX_TREE 64
 size_t kv_tree_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch, int32_t n_nodes);
@@ -421,6 +439,59 @@ int kv_attention_weights(kvq_cache* cache, int32_t layer, const void* q, float* 
  */
 int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
              int32_t batch, int32_t budget, int32_t recent, void* stream);
+
+/*
+ * Pages of a cache taken and given back on the device: sequences share pages, a shared page is copied before it is
+ * written, a sequence is forked with what its ring holds, and the pages in use are moved together.  Nothing of it
+ * passes through the host, and every call may be captured in a CUDA graph.  A pool belongs to a cache that was given
+ * a block table at kv_cache_init (KVQ_ERR_UNSUPPORTED otherwise); these calls, and no one else, write that table from
+ * kv_pool_init on.  Entry -1: no page.  Every cache format has them.
+ *   pool         device, >= kv_pool_bytes(cache) bytes, caller-owned.  It begins with int32 refs[n_pages], how many
+ *                entries of the block table name each page; refs and the table are the whole state between calls (a copy
+ *                of the buffer saves it), what follows refs is workspace.  n_pages is the handle's.
+ * Calls on one pool, and calls that append to, read or evict from its cache, must not overlap on the GPU.  A page
+ * is free when refs is 0; the lowest free page is taken first, so results do not depend on timing.
+ *
+ * kv_pool_init: no page in use, every entry of the table (all max_batch sequences) -1.
+ *
+ * kv_pool_reserve: pages for positions pos[b] .. pos[b] + count - 1 of the first ``batch`` sequences, so that they can
+ * be written: an entry without a page gets a free one, in order of sequence and position, and a page that other
+ * entries name too is copied, every layer of it, and the copy taken in its place.  (Where all the entries that name a
+ * page are of the call, the last of them keeps the page itself.)  A call with pos 0 and the sequence's length makes
+ * a whole sequence's pages its own, as kv_evict wants them.
+ *   pos          device int32 [batch]; < 0: not part of the call
+ *   counts       device int32 [batch] tokens of each sequence, or NULL: n_tokens each; 0 or less: no pages are needed
+ *   granted      device int32 [batch] (out; may be pos itself): pos[b], or -1 where the sequence got no pages: what to
+ *                pass on as pos to kv_quant_append or kv_prefill_attention.  A sequence gets all its pages or none: none
+ *                where it or a sequence before it no longer fits (flagged KVQ_DEV_NO_PAGES), or where pos[b] + count >
+ *                max_seq_len (flagged KVQ_DEV_POS_RANGE)
+ *
+ * kv_pool_fork: sequence b becomes what sequence parents[b] was before the call, for all b < batch at once (beams may
+ * change places): its table names the parent's pages that hold the parent's first seq_lens[parents[b]] tokens, its
+ * window ring holds the parent's, in every layer, and its former pages are given back.
+ *   parents      device int32 [batch], 0..batch-1; b itself or -1: the sequence stays as it is (with every page it has).
+ *                Anything else: flagged KVQ_DEV_BAD_PARENT, stays as it is
+ *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
+ *   new_lens     device int32 [batch] (out): seq_lens[parents[b]]; must not overlap parents or seq_lens
+ * Tokens appended next go to pages of the sequence's own once kv_pool_reserve has been called for them.
+ *
+ * kv_pool_release: give back the pages of each sequence that hold none of its first keep_lens[b] tokens (0: all of
+ * them; < 0: none).
+ *   keep_lens    device int32 [batch]
+ *
+ * kv_pool_compact: move pages so that the U pages in use are pages 0 .. U - 1: the i-th page (in order) of those in use
+ * from U on goes to the i-th free page below U, every layer of it, and the table follows.
+ *   n_used       device int32 (out): U
+ */
+size_t kv_pool_bytes(const kvq_cache* cache);
+int kv_pool_init(kvq_cache* cache, void* pool, size_t pool_bytes, void* stream);
+int kv_pool_reserve(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* pos, const int32_t* counts,
+                    int32_t* granted, int32_t batch, int32_t n_tokens, void* stream);
+int kv_pool_fork(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* parents, const int32_t* seq_lens,
+                 int32_t* new_lens, int32_t batch, void* stream);
+int kv_pool_release(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* keep_lens, int32_t batch,
+                    void* stream);
+int kv_pool_compact(kvq_cache* cache, void* pool, size_t pool_bytes, int32_t* n_used, void* stream);
 
 /*
  * Block codecs next to the cache: the TurboQuant MSE quantiser ([TQ] "key idea" row: random

@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import lib
-from .lib import (KVQ_IN_BF16, KVQ_IN_F32, KVQ_Q4G32, KVQ_Q8G32, KVQ_TQ3_QJL, kv_cache_bytes,  # noqa: F401
+from .lib import (KVQ_IN_BF16, KVQ_IN_F32, KVQ_Q4G32, KVQ_Q8B32, KVQ_Q8G32, KVQ_TQ3_QJL, kv_cache_bytes,  # noqa: F401
                   kv_cache_init,
                   kv_calibrate, kv_calibrate_scratch_bytes, kv_decode_attention,
                   kv_decode_scratch_bytes, kv_qk_norm_rope, kv_quant_append, kv_rope_init, kv_status, kv_strerror,
@@ -33,6 +33,7 @@ class QuantKVCache:
             raise lib.KVQError("unsupported cache configuration")
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.block_table = block_table
+        self.pool = None   # the pages' pool, once pool_init has been called
         self.handle = kv_cache_init(cfg, self.buffer, block_table, qjl_proj)
         self._work = {}    # (operation, stream) -> its buffer
         self._needs = {}   # (operation, sizes) -> bytes
@@ -127,6 +128,53 @@ class QuantKVCache:
             new_lens = torch.empty_like(seq_lens)
         lib.kv_evict(self.handle, layer, weights, seq_lens, kept, new_lens, budget, recent, stream)
         return kept, new_lens
+
+    def pool_init(self, stream=None):
+        """Give the block table (the caller's, see __init__) to a pool of the cache's pages, none of them in use."""
+        if self.pool is None:
+            with torch.cuda.stream(stream):
+                self.pool = torch.empty(lib.kv_pool_bytes(self.handle), dtype=torch.uint8, device=self.buffer.device)
+        lib.kv_pool_init(self.handle, self.pool, stream)
+
+    def _the_pool(self) -> torch.Tensor:
+        if self.pool is None:
+            raise lib.KVQError("pool_init has not been called")
+        return self.pool
+
+    @property
+    def page_refs(self) -> torch.Tensor:
+        """int32 [n_pages]: how many entries of the block table name each page (a view of the pool)."""
+        return self._the_pool()[:4 * self.handle.n_pages].view(torch.int32)
+
+    def reserve(self, pos: torch.Tensor, n_tokens, granted: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Pages of their own for positions pos .. pos + n_tokens - 1 of each sequence (n_tokens: a number, or int32 [B]);
+        returns pos, -1 where there were not enough: the pos to append at."""
+        pool = self._the_pool()
+        if granted is None:
+            granted = torch.empty_like(pos)
+        lib.kv_pool_reserve(self.handle, pool, pos, n_tokens, granted, stream)
+        return granted
+
+    def fork(self, parents: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+        """Sequence b becomes what sequence parents[b] is (b or -1: stays); returns the new lengths."""
+        pool = self._the_pool()
+        if new_lens is None:
+            new_lens = torch.empty_like(seq_lens)
+        lib.kv_pool_fork(self.handle, pool, parents, seq_lens, new_lens, stream)
+        return new_lens
+
+    def release(self, keep_lens: torch.Tensor, stream=None):
+        """Give back the pages past each sequence's first keep_lens[b] tokens (-1: none)."""
+        lib.kv_pool_release(self.handle, self._the_pool(), keep_lens, stream)
+
+    def compact(self, n_used: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Move the pages in use together, to the lowest ids; returns how many there are, int32 [1] on the device."""
+        pool = self._the_pool()
+        if n_used is None:
+            n_used = torch.empty(1, dtype=torch.int32, device=self.buffer.device)
+        lib.kv_pool_compact(self.handle, pool, n_used, stream)
+        return n_used
 
     def status(self) -> int:
         return kv_status(self.handle)

@@ -21,8 +21,13 @@ static bool config_ok(const kvq_config& c) {
   if (g < 1 || g > MAX_GQA) return false;
   if (c.max_batch < 1 || c.max_batch > MAX_BATCH || c.max_seq_len < 1) return false;
   if (c.window < 0 || c.window > MAX_WINDOW || c.window % WCHUNK != 0) return false;
-  if (c.k_format != KVQ_Q4G32 && c.k_format != KVQ_TQ3_QJL && c.k_format != KVQ_Q8G32) return false;
-  if (c.v_format != KVQ_Q4G32) return false;
+  if (c.k_format == KVQ_Q8B32) {
+    // a position that has left the window lies in a finished block only if the window covers a block
+    if (c.v_format != KVQ_Q8B32 || c.window < HALF) return false;
+  } else {
+    if (c.k_format != KVQ_Q4G32 && c.k_format != KVQ_TQ3_QJL && c.k_format != KVQ_Q8G32) return false;
+    if (c.v_format != KVQ_Q4G32) return false;
+  }
   if (c.sinkhorn != 0 && c.sinkhorn != 1) return false;
   if (c.sinkhorn && c.k_format == KVQ_TQ3_QJL) return false;
   if (c.in_dtype != KVQ_IN_F32 && c.in_dtype != KVQ_IN_BF16) return false;
@@ -44,6 +49,13 @@ bool compute_layout(const kvq_config& c, Layout* L) {
   l.off_kmeta = l.off_vmain + 64 * HALF;
   l.off_vmeta = l.off_kmeta + l.kmeta_bytes * HALF;
   l.half_bytes = l.off_vmeta + 16 * HALF;
+  if (c.k_format == KVQ_Q8B32) {  // codes, codes, two float scales
+    l.kmeta_bytes = 0;
+    l.off_vmain = D * HALF;
+    l.off_kmeta = 2 * D * HALF;
+    l.off_vmeta = l.off_kmeta + 4;
+    l.half_bytes = l.off_kmeta + 16;
+  }
   l.page_bytes = 2 * l.half_bytes;
   size_t o = 0;
   l.off_status = o; o = align256(o + 16);
@@ -361,7 +373,13 @@ size_t kv_prefill_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t b
   if (check_cache(cache, &L) != KVQ_OK || batch < 1 || batch > cache->cfg.max_batch) return 0;
   int l0, nl;
   if (layers_of_call(cache, layer, &l0, &nl) != KVQ_OK) return 0;
-  return std::max<size_t>(256, prefill_scratch_bytes(nl, batch, cache->cfg.n_kv_heads, cache->cfg.window));
+  size_t bytes = prefill_scratch_bytes(nl, batch, cache->cfg.n_kv_heads, cache->cfg.window);
+  if (cache->cfg.k_format == KVQ_Q8B32) {
+    const int sms = decode_ctas(cache->device);
+    if (sms <= 0) return 0;
+    bytes += prefill_block_scratch_bytes(sms);
+  }
+  return std::max<size_t>(256, bytes);
 }
 
 int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
@@ -376,7 +394,9 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
     return KVQ_ERR_ALIGN;
   int l0, nl;
   if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
-  if (scratch_bytes < kv_prefill_scratch_bytes(cache, layer, batch)) return KVQ_ERR_CAPACITY;
+  const size_t need = kv_prefill_scratch_bytes(cache, layer, batch);
+  if (need == 0) return KVQ_ERR_CUDA;
+  if (scratch_bytes < need) return KVQ_ERR_CAPACITY;
   if ((rc = check_device(cache)) != KVQ_OK) return rc;
   AppendArgs ap;
   ap.p = dev_ptrs(*cache, L);
@@ -408,6 +428,8 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
   const size_t snap = prefill_scratch_bytes(nl, batch, cache->cfg.n_kv_heads, cache->cfg.window) / 2;
   a.snap_k = static_cast<float*>(scratch);
   a.snap_v = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + snap);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + 2 * snap);
+  a.sms = cache->cfg.k_format == KVQ_Q8B32 ? decode_ctas(cache->device) : 0;
   a.layer0 = l0;
   a.n_layers_call = nl;
   a.batch = batch;
@@ -433,6 +455,7 @@ int kv_tree_commit(kvq_cache* cache, int32_t layer, const void* k, const void* v
   if (!k || !v || !path || !n_accept || !pos) return KVQ_ERR_INVALID_ARG;
   if (batch < 1 || batch > cache->cfg.max_batch || n_nodes < 1 || n_nodes > KVQ_MAX_TREE) return KVQ_ERR_INVALID_ARG;
   if (max_path < 1 || max_path > n_nodes) return KVQ_ERR_INVALID_ARG;
+  if (cache->cfg.k_format == KVQ_Q8B32) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v) || !aligned16(path) || !aligned16(n_accept) || !aligned16(pos)) return KVQ_ERR_ALIGN;
   int l0, nl;
   if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
@@ -468,6 +491,7 @@ static int multi_args(const kvq_cache* cache, int32_t layer, int32_t batch, int3
   int rc = check_cache(cache, &L);
   if (rc != KVQ_OK) return rc;
   if (batch < 1 || batch > cache->cfg.max_batch || n < 1 || n > KVQ_MAX_TREE) return KVQ_ERR_INVALID_ARG;
+  if (cache->cfg.k_format == KVQ_Q8B32) return KVQ_ERR_UNSUPPORTED;
   int l0, nl;
   if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
   *a = MultiArgs{};
@@ -553,6 +577,7 @@ static int evict_args(const kvq_cache* cache, int32_t layer, int32_t batch, int3
   int rc = check_cache(cache, &L);
   if (rc != KVQ_OK) return rc;
   if (batch < 1 || batch > cache->cfg.max_batch || budget < 1 || budget > cache->cfg.max_seq_len) return KVQ_ERR_INVALID_ARG;
+  if (cache->cfg.k_format == KVQ_Q8B32) return KVQ_ERR_UNSUPPORTED;
   int l0, nl;
   if ((rc = layers_of_call(cache, layer, &l0, &nl)) != KVQ_OK) return rc;
   const long long units = (long long)nl * batch * cache->cfg.n_kv_heads;
@@ -594,6 +619,107 @@ int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq
   a.new_lens = new_lens;
   a.recent = recent;
   return call_status(launch_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+// what the pool's calls share: the cache, whose table is the caller's, and the pool's buffer
+static int pool_args(kvq_cache* cache, void* pool, size_t bytes, PoolArgs* a) {
+  Layout L;
+  int rc = check_cache(cache, &L);
+  if (rc != KVQ_OK) return rc;
+  if (!pool) return KVQ_ERR_INVALID_ARG;
+  if (cache->block_table == reinterpret_cast<const int32_t*>(static_cast<uint8_t*>(cache->dev) + L.off_bt)) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned16(pool)) return KVQ_ERR_ALIGN;
+  if (bytes < kv_pool_bytes(cache)) return KVQ_ERR_CAPACITY;
+  *a = PoolArgs{};
+  a->p = dev_ptrs(*cache, L);
+  a->L = L;
+  a->table = const_cast<int32_t*>(cache->block_table);
+  pool_layout(pool, L.n_pages, a);
+  a->n_layers = cache->cfg.n_layers;
+  a->max_batch = cache->cfg.max_batch;
+  a->Hkv = cache->cfg.n_kv_heads;
+  a->W = cache->cfg.window;
+  a->max_seq_len = cache->cfg.max_seq_len;
+  return KVQ_OK;
+}
+
+static bool apart(const void* x, const void* y, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return (a < b ? b - a : a - b) >= bytes;
+}
+
+size_t kv_pool_bytes(const kvq_cache* cache) {
+  Layout L;
+  if (check_cache(cache, &L) != KVQ_OK) return 0;
+  return pool_layout(nullptr, L.n_pages, nullptr);
+}
+
+int kv_pool_init(kvq_cache* cache, void* pool, size_t pool_bytes, void* stream) {
+  PoolArgs a;
+  int rc = pool_args(cache, pool, pool_bytes, &a);
+  if (rc != KVQ_OK) return rc;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  return call_status(launch_pool_init(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pool_reserve(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* pos, const int32_t* counts,
+                    int32_t* granted, int32_t batch, int32_t n_tokens, void* stream) {
+  PoolArgs a;
+  int rc = pool_args(cache, pool, pool_bytes, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!pos || !granted || batch < 1 || batch > cache->cfg.max_batch) return KVQ_ERR_INVALID_ARG;
+  if (!counts && n_tokens < 1) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(pos) || !aligned16(granted) || (counts && !aligned16(counts))) return KVQ_ERR_ALIGN;
+  if (granted != pos && !apart(granted, pos, (size_t)batch * 4)) return KVQ_ERR_INVALID_ARG;
+  if (counts && !apart(granted, counts, (size_t)batch * 4)) return KVQ_ERR_INVALID_ARG;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.pos = pos;
+  a.counts = counts;
+  a.out = granted;
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  return call_status(launch_pool_reserve(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pool_fork(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* parents, const int32_t* seq_lens,
+                 int32_t* new_lens, int32_t batch, void* stream) {
+  PoolArgs a;
+  int rc = pool_args(cache, pool, pool_bytes, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!parents || !seq_lens || !new_lens || batch < 1 || batch > cache->cfg.max_batch) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(parents) || !aligned16(seq_lens) || !aligned16(new_lens)) return KVQ_ERR_ALIGN;
+  // parents and lengths are read by every block while new lengths are written
+  if (!apart(new_lens, seq_lens, (size_t)batch * 4) || !apart(new_lens, parents, (size_t)batch * 4)) return KVQ_ERR_INVALID_ARG;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.pos = parents;
+  a.counts = seq_lens;
+  a.out = new_lens;
+  a.batch = batch;
+  return call_status(launch_pool_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pool_release(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t* keep_lens, int32_t batch,
+                    void* stream) {
+  PoolArgs a;
+  int rc = pool_args(cache, pool, pool_bytes, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!keep_lens || batch < 1 || batch > cache->cfg.max_batch) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(keep_lens)) return KVQ_ERR_ALIGN;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.pos = keep_lens;
+  a.batch = batch;
+  return call_status(launch_pool_release(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pool_compact(kvq_cache* cache, void* pool, size_t pool_bytes, int32_t* n_used, void* stream) {
+  PoolArgs a;
+  int rc = pool_args(cache, pool, pool_bytes, &a);
+  if (rc != KVQ_OK) return rc;
+  if (!n_used) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(n_used)) return KVQ_ERR_ALIGN;
+  if ((rc = check_device(cache)) != KVQ_OK) return rc;
+  a.out = n_used;
+  return call_status(launch_pool_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream) {

@@ -53,6 +53,7 @@ template <int KF>
 struct Geo {
   static constexpr bool TQ = KF == KVQ_TQ3_QJL;
   static constexpr bool Q8 = KF == KVQ_Q8G32;
+  static constexpr bool QB = KF == KVQ_Q8B32;
 #ifndef KVQ_TQ_CONSUMER_WARPS
 #define KVQ_TQ_CONSUMER_WARPS 11
 #endif
@@ -62,16 +63,19 @@ struct Geo {
 #ifndef KVQ_Q8_CONSUMER_WARPS
 #define KVQ_Q8_CONSUMER_WARPS 11
 #endif
-  static constexpr int NCW = TQ ? KVQ_TQ_CONSUMER_WARPS : Q8 ? KVQ_Q8_CONSUMER_WARPS : KVQ_Q4_CONSUMER_WARPS;
+#ifndef KVQ_QB_CONSUMER_WARPS
+#define KVQ_QB_CONSUMER_WARPS 11
+#endif
+  static constexpr int NCW = TQ ? KVQ_TQ_CONSUMER_WARPS : Q8 ? KVQ_Q8_CONSUMER_WARPS : QB ? KVQ_QB_CONSUMER_WARPS : KVQ_Q4_CONSUMER_WARPS;
   static constexpr int NTHREADS = (NCW + 1) * 32;      // + 1 producer warp
 #ifndef KVQ_Q4_SLOTS
 #define KVQ_Q4_SLOTS 2
 #endif
-  static constexpr int NSLOT = (TQ || Q8) ? 2 : KVQ_Q4_SLOTS;   // stages owned by each consumer warp
+  static constexpr int NSLOT = (TQ || Q8 || QB) ? 2 : KVQ_Q4_SLOTS;   // stages owned by each consumer warp
   static constexpr int NSTAGE = NSLOT * NCW;
-  // a stage holds one half-page (Q4/Q4 5120 B, TQ3/Q4 4736 B, Q8/Q4 6912 B) or one window chunk
-  // (4096 B)
-  static constexpr int STAGE = TQ ? 4736 : Q8 ? 6912 : 5120;
+  // a stage holds one half-page (Q4/Q4 5120 B, TQ3/Q4 4736 B, Q8/Q4 6912 B, Q8B32 8208 B) or one
+  // window chunk (4096 B)
+  static constexpr int STAGE = TQ ? 4736 : Q8 ? 6912 : QB ? 8208 : 5120;
   // TQ3 record-byte table: entry v (256 of them) at 256 v: lane j's copy of the centroid pair at
   // +4 j, of the sign pair at +128 + 4 j
   static constexpr int LUT_BYTES = TQ ? 256 * 256 : 0;
@@ -303,6 +307,7 @@ struct QuantState {
   uint32_t qb[8][2];   // B fragments of q~ (K logits), hi/lo interleaved columns
   uint32_t sb[8][2];   // B fragments of S q~ (TQ sign dot)
   uint32_t zb;         // B fragment of the per-group sums of q~ (Q4 zero-point term), hi/lo columns
+  float qs;            // Q8B32: what head (lane & 3)'s logits are multiplied by (its q~ is scaled by a power of two)
   float acc[8][4];     // P.V accumulators, m-tile j (16 channels), C fragment
   float zacc[4];       // sum_t p_t z_{t,G}: rows = groups, cols = heads
   float m, l;          // running max / partial sum for head (lane & 3)
@@ -512,6 +517,24 @@ struct Kernel {
     const bool lo = r & 1;
     const bool hv = head < g;
     const float* qh = qs + head * D;
+    float up = 1.f;
+    if constexpr (KF == KVQ_Q8B32) {
+      // q~ as fp16 hi and lo parts keeps its 22 bits whatever its size: scaled by a power of two to a largest
+      // magnitude in [1, 2) (or as near as exponents go), the inverse multiplies the logits
+      float m = 0.f;
+      const float* qi = qs + i * D + 16 * r;  // head i's channels, sixteen a lane
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(qi + j);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+      }
+      m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
+      m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+      float inv;
+      st.qs = pow2_of(m, inv);
+      up = __shfl_sync(FULL, inv, head);
+    }
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       int d0, d1, d2, d3;
@@ -521,7 +544,7 @@ struct Kernel {
         d1 = d0 + 1;
         d2 = d0 + 2;
         d3 = d0 + 3;
-      } else if (KF == KVQ_Q8G32) {
+      } else if (KF == KVQ_Q8G32 || KF == KVQ_Q8B32) {
         // Q8: k-step kk holds channels 16kk + {2i, 2i+1 | 2i+8, 2i+9}
         d0 = 16 * kk + 2 * i;
         d1 = d0 + 1;
@@ -536,7 +559,7 @@ struct Kernel {
         d2 = d0 + 1;
         d3 = d0 + 3;
       }
-      const float us = (KF == KVQ_Q4G32) ? CODE_UNSCALE : 1.f;
+      const float us = (KF == KVQ_Q4G32) ? CODE_UNSCALE : (KF == KVQ_Q8B32) ? up : 1.f;
       const uint32_t v0 = hv ? split_pick(qh[d0] * us, lo) : 0u, v1 = hv ? split_pick(qh[d1] * us, lo) : 0u;
       const uint32_t v2 = hv ? split_pick(qh[d2] * us, lo) : 0u, v3 = hv ? split_pick(qh[d3] * us, lo) : 0u;
       st.qb[kk][0] = v0 | (v1 << 16);
@@ -676,9 +699,10 @@ struct Kernel {
   // ---------------------------------------------------------------- quantised half-page
   // regions of a 32-token half-page (bytes): K main at 0, V main at 64*HALF, K meta at 128*HALF,
   // V meta after K meta
-  static constexpr int OFF_VMAIN = (KF == KVQ_Q8G32 ? 128 : 64) * HALF;
-  static constexpr int OFF_KMETA = OFF_VMAIN + 64 * HALF;
-  static constexpr int OFF_VMETA = OFF_KMETA + (KF == KVQ_TQ3_QJL ? 4 : KF == KVQ_Q8G32 ? 8 : 16) * HALF;
+  static constexpr bool QB = KF == KVQ_Q8B32;  // (codes of both 128 B a token, then the block's two scales)
+  static constexpr int OFF_VMAIN = (KF == KVQ_Q8G32 || QB ? 128 : 64) * HALF;
+  static constexpr int OFF_KMETA = OFF_VMAIN + (QB ? 128 : 64) * HALF;
+  static constexpr int OFF_VMETA = OFF_KMETA + (QB ? 4 : KF == KVQ_TQ3_QJL ? 4 * HALF : KF == KVQ_Q8G32 ? 8 * HALF : 16 * HALF);
 
   // logits of tokens ta = 16mt + r and tb = ta + 8 for head i (this thread's column pair)
   __device__ __forceinline__ void tile_logits(const uint8_t* stage, int mt, const QuantState& st, float& la,
@@ -687,7 +711,20 @@ struct Kernel {
     const int ta = 16 * mt + r, tb = ta + 8;
     const uint8_t* kmain = stage;
     const uint8_t* kmeta = stage + OFF_KMETA;
-    if (KF == KVQ_Q8G32) {
+    if constexpr (KF == KVQ_Q8B32) {
+      // this lane's A operands of k-steps 2p, 2p + 1 are the 16 bytes at 16 lane of chunk 4 mt + p: a byte u = c + 128
+      // under the exponent of 1024 is 1152 + c, exactly
+      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint4 u = *reinterpret_cast<const uint4*>(kmain + (4 * mt + p) * 512 + 16 * lane);
+        mma16816(acc[0], codes_lo(u.x), codes_hi(u.x), codes_lo(u.y), codes_hi(u.y), st.qb[2 * p][0], st.qb[2 * p][1]);
+        mma16816(acc[1], codes_lo(u.z), codes_hi(u.z), codes_lo(u.w), codes_hi(u.w), st.qb[2 * p + 1][0], st.qb[2 * p + 1][1]);
+      }
+      const float d = *reinterpret_cast<const float*>(kmeta) * st.qs;
+      la = d * ((acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]));
+      lb = d * ((acc[0][2] + acc[1][2]) + (acc[0][3] + acc[1][3]));
+    } else if (KF == KVQ_Q8G32) {
       // Q8 keys: a token's 16-byte chunks 2i (k-steps 0-3) and 2i + 1 (4-7), swizzled by the token's
       // parity (ta and tb have the parity of r); word kk & 3 of a chunk holds the stored bytes
       // u = c + 128 of this lane's A operands, and a byte permute with 0x64 high bytes makes each
@@ -877,6 +914,27 @@ struct Kernel {
                                            QuantState& st) {
     const int r = lane >> 2, i = lane & 3;
     const uint8_t* vmain = stage + OFF_VMAIN;
+    if constexpr (QB) {
+      // channels 16j + r, 16j + r + 8 of both k-steps are the 16 bytes at 16 lane of chunk j; the scale is the block's
+      uint32_t bA[2], bB[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const __half* at = pcol + (lo ? MAX_GQA * HALF : 0) + 16 * ks + 2 * i;
+        bA[ks] = *reinterpret_cast<const uint32_t*>(at);
+        bB[ks] = *reinterpret_cast<const uint32_t*>(at + 8);
+      }
+      const float d = *reinterpret_cast<const float*>(stage + OFF_VMETA);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4*>(vmain + j * 512 + 16 * lane);
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(c, codes_lo(u.x), codes_hi(u.x), codes_lo(u.y), codes_hi(u.y), bA[0], bB[0]);
+        mma16816(c, codes_lo(u.z), codes_hi(u.z), codes_lo(u.w), codes_hi(u.w), bA[1], bB[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.acc[j][e] = fmaf(d, c[e], st.acc[j][e]);
+      }
+      return;
+    }
     const __half* vscale = reinterpret_cast<const __half*>(stage + OFF_VMETA);
     const __half* vzero = vscale + 4 * HALF;
 
@@ -941,12 +999,16 @@ struct Kernel {
     }
   }
 
+  // Q8B32: the reference stays 2^BOOST below the largest logit, so that the fp16 parts of weights keep their bits down
+  // to 2^-34 of the largest (weights up to 2^(BOOST + LAZY_RAISE) = 16384)
+  static constexpr float BOOST = QB ? 10.f : 0.f;
+
   __device__ void quant_step(uint8_t* stage, int ntok, QuantState& st) {
     const int r = lane >> 2, i = lane & 3;
     __half* pw = reinterpret_cast<__half*>(smem + SM_P) + warp * 2 * MAX_GQA * HALF;
     const float lmask = (i < g) ? 0.f : -INFINITY;  // column pair of a missing head: never attended
     const bool tail = ntok < HALF;
-    if (tail) sanitize_tail(stage, ntok);
+    if (!QB && tail) sanitize_tail(stage, ntok);  // (a Q8B32 block is finite as a whole: it was written at once)
 
     // ---- logits of the 32 tokens (two 16-token m-tiles)
     float lg[4];  // head i, tokens r, r + 8, r + 16, r + 24
@@ -959,12 +1021,12 @@ struct Kernel {
     // max is needed.  Any reference gives the same acc / l; 2^(-inf - m) = 0 handles masked tokens,
     // and a head with nothing valid yet keeps m = -inf (reference 0).
     const float lmax = fmaxf(fmaxf(lg[0], lg[1]), fmaxf(lg[2], lg[3]));
-    if (__any_sync(FULL, lmax > st.m + LAZY_RAISE)) {
+    if (__any_sync(FULL, lmax > st.m + (LAZY_RAISE + BOOST))) {
       float mx = lmax;
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-      const float mnew = fmaxf(st.m, mx);
+      const float mnew = fmaxf(st.m, mx - BOOST);
       const float alpha = (mnew == -INFINITY) ? 1.f : ex2(st.m - mnew);
       st.m = mnew;
       st.l *= alpha;
@@ -1014,7 +1076,7 @@ struct Kernel {
     // undo the 2^-9 of the converted codes and fold in the zero-point term:
     // acc[h][c] = 512 * acc[h][c] + zterm[G(c)][h]
 #pragma unroll
-    for (int G = 0; G < 4; ++G) {
+    for (int G = 0; G < (QB ? 0 : 4); ++G) {
       const float z0 = __shfl_sync(FULL, st.zacc[0], 4 * G + i);
       const float z1 = __shfl_sync(FULL, st.zacc[1], 4 * G + i);
 #pragma unroll
@@ -1048,9 +1110,10 @@ struct Kernel {
           for (int G = 0; G < 4; ++G)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int c0 = 32 * G + 4 * r + 2 * e;
+              // Q8B32: m-tile j = 2G + e holds channels 16j + r and 16j + 8 + r
+              const int c0 = QB ? 16 * (2 * G + e) + r : 32 * G + 4 * r + 2 * e;
               dst[c0] = st.acc[2 * G + e][cidx];
-              dst[c0 + 1] = st.acc[2 * G + e][2 + cidx];
+              dst[c0 + (QB ? 8 : 1)] = st.acc[2 * G + e][2 + cidx];
             }
         }
       }
@@ -1601,6 +1664,7 @@ __global__ void __launch_bounds__(Geo<KF>::NTHREADS, 1) decode_kernel(const __gr
 int decode_consumer_warps(int k_format) {
   return k_format == KVQ_TQ3_QJL ? Geo<KVQ_TQ3_QJL>::NCW
          : k_format == KVQ_Q8G32 ? Geo<KVQ_Q8G32>::NCW
+         : k_format == KVQ_Q8B32 ? Geo<KVQ_Q8B32>::NCW
                                  : Geo<KVQ_Q4G32>::NCW;
 }
 
@@ -1653,6 +1717,7 @@ static cudaError_t launch_kf(const DecodeArgs& a, cudaStream_t s) {
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
   return a.k_format == KVQ_TQ3_QJL ? launch_kf<KVQ_TQ3_QJL>(a, s)
          : a.k_format == KVQ_Q8G32 ? launch_kf<KVQ_Q8G32>(a, s)
+         : a.k_format == KVQ_Q8B32 ? launch_kf<KVQ_Q8B32>(a, s)
                                    : launch_kf<KVQ_Q4G32>(a, s);
 }
 

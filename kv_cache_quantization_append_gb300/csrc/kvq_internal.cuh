@@ -96,6 +96,9 @@ cudaError_t launch_commit(const AppendArgs& a, const CommitArgs& c, cudaStream_t
 // programmatic dependent (the two overlap; the values grid ends after the keys grid)
 cudaError_t launch_append_bulk(const AppendArgs& a, cudaStream_t s, bool after_keys = false);
 
+// KVQ_Q8B32 keys and values
+cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t s);
+
 struct CalibArgs {
   DevPtrs p;
   const void* kc;
@@ -139,9 +142,13 @@ struct PrefillArgs {
   float* snap_v;
   int layer0, n_layers_call, batch, max_batch, Hkv, g, W, T, k_format, sinkhorn, in_bf16;
   int max_pages_per_seq, max_seq_len;
+  float* parts;      // KVQ_Q8B32: partial results of row tiles that several CTAs share
+  int sms;
 };
 size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W);
 cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStream_t s);
+size_t prefill_block_scratch_bytes(int sms);
+cudaError_t launch_prefill_blocks(const PrefillArgs& a, int sms, cudaStream_t s);
 
 struct EvictArgs {
   DevPtrs p;
@@ -180,6 +187,29 @@ cudaError_t launch_tree(const MultiArgs& a, int sms, cudaStream_t s);
 size_t weights_scratch_bytes(const MultiArgs& a, int sms);
 cudaError_t launch_weights(const MultiArgs& a, int sms, cudaStream_t s);
 
+// The pages of a cache and who names them (kv_pool_*)
+struct PoolArgs {
+  DevPtrs p;
+  Layout L;
+  int32_t* table;       // [max_batch][max_pages_per_seq]
+  int32_t* refs;        // [n_pages] entries of the table that name a page
+  int32_t* writers;     // [n_pages] entries of a call that would write a shared page; 0 between calls
+  int32_t* last;        // [n_pages] the last of them; -1 between calls
+  int32_t* pick;        // [n_pages] free pages in order; compact: where a page goes
+  int2* copies;         // [n_pages] (from, to)
+  int32_t* n_copies;
+  const int32_t* pos;     // reserve: first positions; fork: parents; release: tokens kept
+  const int32_t* counts;  // reserve: tokens, or null; fork: lengths
+  int32_t* out;           // reserve: positions granted; fork: new lengths; compact: pages in use
+  int n_layers, max_batch, Hkv, W, max_seq_len, batch, n_tokens;
+};
+size_t pool_layout(void* pool, int n_pages, PoolArgs* a);  // the buffer's parts, where there is one; its bytes
+cudaError_t launch_pool_init(const PoolArgs& a, cudaStream_t s);
+cudaError_t launch_pool_reserve(const PoolArgs& a, cudaStream_t s);
+cudaError_t launch_pool_fork(const PoolArgs& a, cudaStream_t s);
+cudaError_t launch_pool_release(const PoolArgs& a, cudaStream_t s);
+cudaError_t launch_pool_compact(const PoolArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__
 // Lets kernel K have as much dynamic shared memory as a block may hold, once per device: the same value whoever sets it, so
@@ -211,6 +241,22 @@ __device__ __forceinline__ float4 load4_in(const void* base, size_t elem_off, in
     return r;
   }
   return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem_off);
+}
+
+// Two stored 8-bit codes u = c + 128 (the lower or upper two bytes of a word) as the fp16 pair of c, exactly: a byte under
+// the exponent of 1024 is 1024 + u
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t sel) {
+  const uint32_t u = __byte_perm(w, 0x64646464u, sel), k = 0x64806480u;
+  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&c);
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return code_pair(w, 0x4140u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return code_pair(w, 0x4342u); }
+// 2^floor(log2 m) of a magnitude, within the exponents whose inverse is a number too (1 to 253), and that inverse
+__device__ __forceinline__ float pow2_of(float m, float& inv) {
+  const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
+  inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  return __uint_as_float((uint32_t)e << 23);
 }
 
 // Packed pairs of IEEE fp32 operations (sm_100+ `add/sub/mul/fma.rn.f32x2`): each half is rounded

@@ -806,6 +806,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStre
   }
   cudaError_t e = launch_append(app, s);
   if (e != cudaSuccess) return e;
+  if (a.k_format == KVQ_Q8B32) return launch_prefill_blocks(a, a.sms, s);  // (prefill_block.cu)
   return a.k_format == KVQ_TQ3_QJL ? launch_kf<KVQ_TQ3_QJL>(a, s)
          : a.k_format == KVQ_Q8G32 ? launch_kf<KVQ_Q8G32>(a, s)
                                    : launch_kf<KVQ_Q4G32>(a, s);

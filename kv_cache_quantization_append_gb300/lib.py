@@ -19,8 +19,9 @@ LIB_PATH = os.path.join(HERE, "_lib", "libkvq.so")
 KVQ_Q4G32 = 1
 KVQ_TQ3_QJL = 3
 KVQ_Q8G32 = 4
+KVQ_Q8B32 = 5
 # the key formats by the names the workloads and the oracle use
-K_FORMATS = {"q4g32": KVQ_Q4G32, "tq3_qjl": KVQ_TQ3_QJL, "q8g32": KVQ_Q8G32}
+K_FORMATS = {"q4g32": KVQ_Q4G32, "tq3_qjl": KVQ_TQ3_QJL, "q8g32": KVQ_Q8G32, "q8b32": KVQ_Q8B32}
 KVQ_IN_F32 = 0
 KVQ_IN_BF16 = 1
 
@@ -29,6 +30,8 @@ DEV_POS_RANGE = 2
 DEV_SEQLEN_RANGE = 4
 DEV_TIMEOUT = 8
 DEV_BAD_NODE = 16
+DEV_NO_PAGES = 32
+DEV_BAD_PARENT = 64
 
 MAX_TREE = 64
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
@@ -40,7 +43,8 @@ EXPORTS = ("kv_cache_bytes", "kv_cache_init", "kv_calibrate_scratch_bytes", "kv_
            "kv_tbq_block_bytes", "kv_tbq_encode", "kv_tbq_decode", "kv_split_record_bytes",
            "kv_split_outliers", "kv_split_encode", "kv_split_decode", "kv_status", "kv_set_wait_limit_ns",
            "kv_strerror", "kv_rope_init", "kv_qk_norm_rope", "kv_tree_scratch_bytes", "kv_tree_attention",
-           "kv_tree_commit", "kv_weights_scratch_bytes", "kv_attention_weights", "kv_evict")
+           "kv_tree_commit", "kv_weights_scratch_bytes", "kv_attention_weights", "kv_evict",
+           "kv_pool_bytes", "kv_pool_init", "kv_pool_reserve", "kv_pool_fork", "kv_pool_release", "kv_pool_compact")
 NOALLOC_SCRATCH_MAX = 32 * 1024 * 1024
 
 
@@ -113,6 +117,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kv_weights_scratch_bytes": (SZ, [cachep, I32, I32, I32]),
         "kv_attention_weights": (ctypes.c_int, [cachep, I32, P, P, F32, P, I32, I32, P, SZ, P]),
         "kv_evict": (ctypes.c_int, [cachep, I32, P, P, P, P, I32, I32, I32, P]),
+        "kv_pool_bytes": (SZ, [cachep]),
+        "kv_pool_init": (ctypes.c_int, [cachep, P, SZ, P]),
+        "kv_pool_reserve": (ctypes.c_int, [cachep, P, SZ, P, P, P, I32, I32, P]),
+        "kv_pool_fork": (ctypes.c_int, [cachep, P, SZ, P, P, P, I32, P]),
+        "kv_pool_release": (ctypes.c_int, [cachep, P, SZ, P, I32, P]),
+        "kv_pool_compact": (ctypes.c_int, [cachep, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -194,8 +204,11 @@ def _check_append_shapes(cache: kvq_cache, layer: int, k: torch.Tensor, v: torch
 
 
 def make_config(n_layers, n_kv_heads, n_q_heads, max_batch, max_seq_len, window=128, n_pages=0,
-                k_format=KVQ_Q4G32, v_format=KVQ_Q4G32, sinkhorn=False, in_dtype=KVQ_IN_BF16,
+                k_format=KVQ_Q4G32, v_format=None, sinkhorn=False, in_dtype=KVQ_IN_BF16,
                 seed=0) -> kvq_config:
+    """A cache's configuration; v_format None is what goes with the keys' format (Q8B32 values with Q8B32 keys, else Q4G32)."""
+    if v_format is None:
+        v_format = KVQ_Q8B32 if k_format == KVQ_Q8B32 else KVQ_Q4G32
     return kvq_config(n_layers, n_kv_heads, n_q_heads, 128, max_batch, max_seq_len, window, 64,
                       n_pages, k_format, v_format, int(bool(sinkhorn)), 32, in_dtype, seed)
 
@@ -436,6 +449,58 @@ def kv_evict(cache: kvq_cache, layer: int, weights: torch.Tensor, seq_lens: torc
     dev = cache.device
     _check(load().kv_evict(ctypes.byref(cache), layer, _ptr(weights, dev), _ptr(seq_lens, dev), _ptr(kept, dev),
                            _ptr(new_lens, dev), B, budget, recent, _stream(stream)))
+
+
+def kv_pool_bytes(cache: kvq_cache) -> int:
+    return int(load().kv_pool_bytes(ctypes.byref(cache)))
+
+
+def _pool(cache: kvq_cache, pool: torch.Tensor, *ints: torch.Tensor):
+    """The pool's address and size, after checks of the call's int32 [batch] tensors."""
+    for t in ints:
+        if t.dtype != torch.int32:
+            raise KVQError("the pool's arguments are int32 tensors")
+        _check_shape("argument", t, (ints[0].numel(),))
+    return _ptr(pool, cache.device), pool.numel() * pool.element_size()
+
+
+def kv_pool_init(cache: kvq_cache, pool: torch.Tensor, stream=None):
+    """pool: device bytes, at least kv_pool_bytes; the cache's block table (all of it) becomes -1."""
+    at, size = _pool(cache, pool)
+    _check(load().kv_pool_init(ctypes.byref(cache), at, size, _stream(stream)))
+
+
+def kv_pool_reserve(cache: kvq_cache, pool: torch.Tensor, pos: torch.Tensor, n_tokens, granted: torch.Tensor, stream=None):
+    """pos, granted (written; may be pos): int32 [B]; n_tokens: one number, or int32 [B] on the device."""
+    counts = n_tokens if isinstance(n_tokens, torch.Tensor) else None
+    at, size = _pool(cache, pool, pos, granted, *(() if counts is None else (counts,)))
+    dev = cache.device
+    _check(load().kv_pool_reserve(ctypes.byref(cache), at, size, _ptr(pos, dev), _ptr(counts, dev), _ptr(granted, dev),
+                                  pos.numel(), 0 if counts is not None else n_tokens, _stream(stream)))
+
+
+def kv_pool_fork(cache: kvq_cache, pool: torch.Tensor, parents: torch.Tensor, seq_lens: torch.Tensor,
+                 new_lens: torch.Tensor, stream=None):
+    """parents, seq_lens, new_lens (written): int32 [B]."""
+    at, size = _pool(cache, pool, parents, seq_lens, new_lens)
+    dev = cache.device
+    _check(load().kv_pool_fork(ctypes.byref(cache), at, size, _ptr(parents, dev), _ptr(seq_lens, dev),
+                               _ptr(new_lens, dev), parents.numel(), _stream(stream)))
+
+
+def kv_pool_release(cache: kvq_cache, pool: torch.Tensor, keep_lens: torch.Tensor, stream=None):
+    """keep_lens: int32 [B]."""
+    at, size = _pool(cache, pool, keep_lens)
+    _check(load().kv_pool_release(ctypes.byref(cache), at, size, _ptr(keep_lens, cache.device), keep_lens.numel(),
+                                  _stream(stream)))
+
+
+def kv_pool_compact(cache: kvq_cache, pool: torch.Tensor, n_used: torch.Tensor, stream=None):
+    """n_used: int32 [1] (written)."""
+    at, size = _pool(cache, pool, n_used)
+    if n_used.numel() != 1:
+        raise KVQError("n_used must be int32 [1]")
+    _check(load().kv_pool_compact(ctypes.byref(cache), at, size, _ptr(n_used, cache.device), _stream(stream)))
 
 
 def _in_dtype_of(t: torch.Tensor) -> int:
