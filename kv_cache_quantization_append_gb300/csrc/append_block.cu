@@ -63,48 +63,6 @@ __device__ __forceinline__ void store32(float* dst, const float (&x)[32]) {
     reinterpret_cast<float4*>(dst)[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
 }
 
-// y = c H (s . x) [/ sigma] of the token whose channels 32 G .. + 31 this lane holds (lanes 4 v + G)
-__device__ __forceinline__ void rotate32(float (&x)[32], int G, const float* signs, const __half* sigma) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float4 s = *reinterpret_cast<const float4*>(signs + 32 * G + 4 * c);
-    mul2(x[4 * c], x[4 * c + 1], s.x, s.y);
-    mul2(x[4 * c + 2], x[4 * c + 3], s.z, s.w);
-  }
-#pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const float u = x[j], v = x[j + 1];
-    x[j] = __fadd_rn(u, v);
-    x[j + 1] = __fsub_rn(u, v);
-  }
-#pragma unroll
-  for (int hs = 2; hs < 32; hs <<= 1) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      if (j & hs) continue;
-      bfly2(x[j], x[j + 1], x[j + hs], x[j + hs + 1]);
-    }
-  }
-#pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    const float sg = (G & m) ? -1.0f : 1.0f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2)
-      fma2(x[j], x[j + 1], sg, sg, __shfl_xor_sync(FULL, x[j], m), __shfl_xor_sync(FULL, x[j + 1], m));
-  }
-#pragma unroll
-  for (int j = 0; j < 32; j += 2) mul2(x[j], x[j + 1], C_WHT, C_WHT);
-  if (sigma != nullptr) {
-    const __half2* sg = reinterpret_cast<const __half2*>(sigma + 32 * G);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 s = __half22float2(sg[j]);
-      x[2 * j] = __fdiv_rn(x[2 * j], s.x);
-      x[2 * j + 1] = __fdiv_rn(x[2 * j + 1], s.y);
-    }
-  }
-}
-
 // codes + 128 of the lane's 32 values, four channels a word.  y / d is formed as y RN(1 / d), which is within 3.1e-5 of the
 // IEEE quotient for magnitudes up to 127.5; where that lies within 2^-14 of a half-integer, or is larger (a scale that
 // underflowed), the lane takes the IEEE quotients instead: every code is clamp(rint(RN(y / d)), -127, 127).

@@ -17,10 +17,10 @@
 //    queries and weights follow: 16 stored bytes become two 16-byte operand rows by byte permutes, nothing is transposed.
 //  * Raw tiles are taken as they are, not rotated: queries are also kept unrotated (in shared memory), and the output
 //    accumulator, a row per thread in registers, is rotated back once, before the first raw tile.
-//  * Warps: two groups of four soften alternate tiles (a row a thread: lanes of tensor memory), each with a reference, a sum
-//    and an output accumulator of its own, joined at the end; four warps turn bytes into operands; one issues the logits'
-//    products, one those of the values.  Every tile's P V starts from zero and is added to the registers: the tensor
-//    cores' truncating sums stay within a tile.
+//  * Warps: two groups of four soften alternate tiles (a row a thread: lanes of tensor memory), each with a reference and a
+//    sum of its own; four add every tile's P V, which starts from zero, to the output accumulator in registers (the tensor
+//    cores' truncating sums stay within a tile, and a reference that moves rescales registers only); four turn bytes into
+//    operands; one issues the logits' products, one those of the values.  Registers are shared out among them.
 //  * Queries, raw keys and raw values are scaled by powers of two, each vector by its own, and weights against the largest
 //    scale of values so far: fp16 parts keep their bits at any magnitude.
 //  * Every wait is bounded; one that runs out flags the status word and the CTA leaves as a whole.
@@ -37,35 +37,44 @@ using namespace tc;
 
 constexpr int ROWS = 128;            // rows of a row tile = MMA M = lanes of tensor memory
 constexpr int NT = 64;               // recorded positions of a tile = a page
-constexpr int NS = 4;                // operand stages
+constexpr int NS = 3;                // operand stages
+constexpr int RS = 2;                // pages under way
 constexpr int N_SOFT = 8;            // softmax warps, two groups
-constexpr int DQ0 = 8, N_DQ = 4;     // operand warps
-constexpr int S_WARP = 12, PV_WARP = 13, NEXT_WARP = 14;
-constexpr int THREADS = 512;
-constexpr int SOFT_REGS = 184, OTHER_REGS = 72;  // 256 x (184 + 72) = 512 x 128, what the block is launched with
+constexpr int N_SUM = 4;             // warps that hold the output
+constexpr int DQ0 = 12, N_DQ = 4;    // operand warps
+constexpr int S_WARP = 16, PV_WARP = 17, PAGE_WARP = 18, NEXT_WARP = 19;
+constexpr int THREADS = 640, ROW_WARPS = 16;  // ROW_WARPS: those that prepare queries and write rows out
+constexpr int LAUNCH_REGS = 96;
+// registers: 256 x 96 + 128 x (168 + 80 + 40) = 640 x 96, what the block is launched with
+constexpr int SOFT_REGS = 96, SUM_REGS = 168, DQ_REGS = 80, ISSUE_REGS = 40;
 constexpr uint32_t TMEM_COLS = 512, C_QHI = 0, C_QLO = 64, C_S = 128, C_O = 256;  // Q hi | lo | two S or P | two O
-constexpr uint32_t V_OFF = 16384, STAGE = 32768;        // a stage: keys, values; planes of 64 x 128 (or two of 32 x 128) fp16
-constexpr uint32_t LO_PLANE = 8192;                     // raw tiles of float caches: from hi to lo
+// K-groups of an operand (8 channels of 64 keys, 8 positions of 128 value channels) are 32 bytes further apart than they
+// are long, so that lanes which write one row of four neighbouring groups each do not meet in a bank
+constexpr uint32_t K_LEAD = NT * 16 + 32, V_LEAD = D * 16 + 32;
+constexpr uint32_t V_OFF = 16 * K_LEAD, STAGE = V_OFF + 8 * V_LEAD;  // a stage: keys, values
+constexpr uint32_t LO_K = 8192, LO_V = 4 * V_LEAD;      // raw tiles of float caches (32 positions): from hi to lo
 constexpr uint32_t Q_STRIDE = 2 * D * 2 + 16;           // query staging row: hi, lo, pad
 constexpr uint32_t QR_LEAD = ROWS * 16 + 16;            // unrotated queries: from one 8 channels to the next
 constexpr uint32_t QR_PLANE = 16 * QR_LEAD;
-constexpr uint32_t QR_OFF = NS * STAGE, SMEM = QR_OFF + 2 * QR_PLANE;
+constexpr uint32_t QR_OFF = NS * STAGE, PAGE_OFF = QR_OFF + 2 * QR_PLANE, PAGE_SLOT = 2 * 8208;
+constexpr uint32_t SMEM = PAGE_OFF + RS * PAGE_SLOT;
+static_assert(V_OFF >= 16384, "raw keys fit too");
 constexpr uint32_t O_STRIDE = (D + 4) * 4;
-static_assert(ROWS * Q_STRIDE <= NS * STAGE && 2 * ROWS * O_STRIDE <= SMEM, "what borrows the stages");
-constexpr int MAX_RAW = ((MAX_WINDOW + ROWS) / 64 + 1) * 64;  // raw positions of a row tile, in whole tiles
-constexpr float BOOST = 9.f;         // log2 of the largest weight over its reference when that is set
-constexpr float RAISE_AT = 4.f;      // ... and how much further it may grow before the reference follows
+static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "what borrows the stages");
+constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
+constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
 constexpr long long K0 = 192;        // a row tile's fixed cost, in positions
 constexpr long long MIN_SHARE = 512; // positions that a CTA takes at least
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 constexpr int REC = ROWS * D + 2 * ROWS;  // floats of a partial result: O, m, l
 
-// place of channel c (position c of a tile) along K, in the order in which 16-byte chunks hold codes; what is at a place
-__host__ __device__ constexpr int place_of(int c) {
-  return (c & ~31) | (((c >> 1) & 3) << 3) | (((c >> 4) & 1) << 2) | (((c >> 3) & 1) << 1) | (c & 1);
-}
+// Along K, channels (keys) and positions of a tile (values) stand in the order in which 16-byte chunks hold their codes: which
+// of them is at a place, and the place of each
 __host__ __device__ constexpr int at_place(int k) {
   return (k & ~31) | (((k >> 2) & 1) << 4) | (((k >> 1) & 1) << 3) | (((k >> 3) & 3) << 1) | (k & 1);
+}
+__host__ __device__ constexpr int place_of(int c) {
+  return (c & ~31) | (((c >> 1) & 3) << 3) | (((c >> 4) & 1) << 2) | (((c >> 3) & 1) << 1) | (c & 1);
 }
 // (row, k) of a K-major operand whose groups of 8 k are `lead` bytes apart
 __device__ __forceinline__ uint32_t km(int row, int k, uint32_t lead) {
@@ -84,6 +93,8 @@ struct Work {
   int B, T, qpt, nx, HL, n;
   const int* p0;           // per sequence; -1: not part of the call
   const long long* pre;    // cost before each sequence, [B + 1]
+  __device__ Work(const PrefillArgs& a, const int* p, const long long* c, int ctas)
+      : B(a.batch), T(a.T), qpt(ROWS / a.g), nx((a.T + ROWS / a.g - 1) / (ROWS / a.g)), HL(a.Hkv * a.n_layers_call), n(ctas), p0(p), pre(c) {}
   __device__ __forceinline__ long long cost(int b, int x) const { return p0[b] + (long long)(x + 1) * qpt + K0; }
   __device__ __forceinline__ long long upto(int b, int x) const {
     return (x * (p0[b] + K0) + (long long)qpt * x * (x + 1) / 2) * HL;
@@ -115,14 +126,8 @@ struct Work {
   }
 };
 // warp 0: positions and prefix of the sequences' costs into shared memory
-__device__ void plan(const PrefillArgs& a, Work& w, int* p0, long long* pre, int ctas) {
-  w.B = a.batch;
-  w.T = a.T;
-  w.qpt = ROWS / a.g;
-  w.nx = (a.T + w.qpt - 1) / w.qpt;
-  w.HL = a.Hkv * a.n_layers_call;
-  w.p0 = p0;
-  w.pre = pre;
+__device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas) {
+  Work w(a, p0, pre, 0);
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
@@ -147,6 +152,7 @@ __device__ void plan(const PrefillArgs& a, Work& w, int* p0, long long* pre, int
   }
   __syncthreads();
   w.n = (int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE));
+  return w;
 }
 
 // A row tile: its queries' positions, the recorded positions [0, qend) that any of them reads, the raw ones from rlo
@@ -199,18 +205,11 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32])
       KVQ_R8(KVQ_IN, 0), KVQ_R8(KVQ_IN, 8), KVQ_R8(KVQ_IN, 16), KVQ_R8(KVQ_IN, 24)
       : "memory");
 }
-// four columns at each of taddr, + 8, + 16, + 24
-__device__ __forceinline__ void tm_ld4x4(uint32_t taddr, float (&f)[16]) {
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    uint32_t r[4];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr + 8 * n));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[4 * n + e] = __uint_as_float(r[e]);
-  }
-  tm_wait_ld();
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      KVQ_R8(KVQ_IN, 0), KVQ_R8(KVQ_IN, 8)
+      : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -220,10 +219,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // A warp's bounded wait.  false: this CTA gives up (a wait elsewhere ran out, or this one: flagged).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gone, unsigned* status) {
   bool ok = bar_try(bar, parity);
-  if (!ok) {
+  if (__builtin_expect(!ok, 0)) {
     const unsigned long long t0 = gtimer();
-    while (!(ok = bar_sleep(bar, parity))) {
-      if (*gone) break;
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = bar_try(bar, parity);
+      if (ok || *gone) break;
       if (gtimer() - t0 > WAIT_NS) {
         atomicOr(status, KVQ_DEV_TIMEOUT);
         *gone = 1;
@@ -233,10 +234,35 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
   return __all_sync(FULL, ok);
 }
-__device__ __forceinline__ float warp_max(float m) {
+// the largest magnitude of 128 values in four neighbouring lanes
+__device__ __forceinline__ float quad_max(const float (&x)[32]) {
+  float m = 0.f;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-  return m;
+  for (int i = 0; i < 32; i += 2) m = max3(m, fabsf(x[i]), fabsf(x[i + 1]));
+  m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+  return fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+}
+// eight bf16 values
+__device__ __forceinline__ void unpack8(uint4 w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(u[e] << 16);
+    x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+  }
+}
+// the upper halves of eight floats that are bf16 values
+__device__ __forceinline__ uint4 pack8(float4 a, float4 b) {
+  return make_uint4(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632u), __byte_perm(__float_as_uint(a.z), __float_as_uint(a.w), 0x7632u),
+                    __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632u), __byte_perm(__float_as_uint(b.z), __float_as_uint(b.w), 0x7632u));
+}
+
+// This warp group's registers per thread from here on (taking more and giving some back are two instructions)
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  static_assert(N % 8 == 0 && 8 * 32 * SOFT_REGS + 4 * 32 * (SUM_REGS + DQ_REGS + ISSUE_REGS) <= THREADS * LAUNCH_REGS, "more than there are");
+  if constexpr (N > LAUNCH_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <bool BF16>
@@ -247,13 +273,16 @@ struct Kernel {
 
   // shared by the CTA, besides the stages
   struct Shared {
-    uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], sfull[2], pfull[2], pvdone[2], done[2];
+    uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], sfull[2], pfull[2], pvdone[2], ofree[2], done[2], rfull[RS], rempty[RS], begun[4], most;
     uint32_t tmem;
     int gone;
     float qscale[ROWS], qraw[ROWS];        // powers of two that the queries were divided by
-    float m[2][ROWS], l[2][ROWS];          // both groups' references and sums, at the end
-    float2 scale[8][2];                    // (keys', values') of a tile's two blocks
-    float rawk[MAX_RAW], rawv[MAX_RAW];    // the raw vectors' powers of two
+    float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' references and sums, the output's reference, at the end
+    float mt[4][ROWS], vt[4], vt0[4];              // a tile's references: of its weights, of its values' scales
+    int ctas;                              // that have work
+    int halves[RS];                        // of a page under way that are read (0: there is no such page)
+    float2 scale[8][2];                    // (keys', values') of a tile's two blocks; of a raw tile: its powers of two
+    float warp_most[2][N_DQ];              // largest magnitude of a raw tile's keys, values, in each operand warp
     alignas(16) float signs[D];            // (read four at a time)
     int p0[MAX_BATCH];
     long long pre[MAX_BATCH + 1];
@@ -265,21 +294,25 @@ struct Kernel {
   const PrefillArgs& a;
   Shared& sh;
   uint8_t* smem;
-  Work& work;
-  float* recs;
   int warp, lane;
   uint32_t tmem;
-  int gt = 0;  // tiles so far
+  int gt = 0, gr = 0, gb = 0, gm = 0;  // tiles so far, those among them with pages, stretches of two tiles or more, raw operands
 
-  __device__ Kernel(const PrefillArgs& args, Shared& s, uint8_t* sm, Work& w, float* r) : a(args), sh(s), smem(sm), work(w), recs(r) {
-    warp = threadIdx.x >> 5;
-    lane = threadIdx.x & 31;
+  // Made within each role: nothing is then live where the roles part and their registers are shared out (a value that is
+  // takes a register that the smallest share has, or memory)
+  __device__ Kernel(const PrefillArgs& args, Shared& s, uint8_t* sm) : a(args), sh(s), smem(sm) {
+    uint32_t tid;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+    warp = tid >> 5;
+    lane = tid & 31;
+    tmem = *const_cast<volatile uint32_t*>(&s.tmem);
   }
   __device__ __forceinline__ bool held(uint64_t* bar, uint32_t parity) { return wait(bar, parity, &sh.gone, a.p.status); }
   __device__ __forceinline__ void sync_all() { part_sync(1, THREADS); }
 
-  // the first stretch with tiles from y on (lo: where the CTA began)
-  __device__ void locate(long long y, long long lo, long long hi, Stretch& st) const {
+  // the first stretch with tiles from y on
+  __device__ void locate(const Work& work, long long y, Stretch& st) const {
+    const long long lo = work.cut(blockIdx.x), hi = work.cut(blockIdx.x + 1);
     st.tb = -1;
     while (y < hi) {
       const Unit u = work.find(y);
@@ -301,53 +334,66 @@ struct Kernel {
   }
 
   // ---------------------------------------------------------------- queries
-  // rows warp, warp + 16, ...: unrotated (scaled) hi and lo to their operand, rotated ones to the staging rows
+  // Rows 8 warp .. + 7, four lanes a row with 32 channels each: unrotated hi and lo to their operand, rotated ones to the
+  // staging rows, each over its own power of two
   __device__ void queries(const Stretch& u) {
     const Tiles& tl = u.tl;
-    const int g = a.g, h = u.h;
-    const size_t head0 = (size_t)u.unit * g;
-    const float4 sg = *reinterpret_cast<const float4*>(a.p.signs + 4 * lane);
-    float4 sk = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (a.sinkhorn) {
-      const __half* sig = a.p.sigk + ((size_t)u.layer * a.Hkv + h) * D + 4 * lane;
-      sk = make_float4(__half2float(sig[0]), __half2float(sig[1]), __half2float(sig[2]), __half2float(sig[3]));
-    }
-    const int nrows = tl.nq * g;
-#pragma unroll 1
-    for (int row = warp; row < ROWS; row += THREADS / 32) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < nrows) x = load4_in(a.q, ((head0 + row % g) * a.T + tl.t0 + row / g) * D + 4 * lane, a.in_bf16);
-      {
-        const float z[4] = {x.x * LOGIT_SCALE, x.y * LOGIT_SCALE, x.z * LOGIT_SCALE, x.w * LOGIT_SCALE};
-        float inv;
-        const float s2 = pow2_of(warp_max(fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])))), inv);
-        if (lane == 0) sh.qraw[row] = s2;
-        uint2 hv, lv;
-        split2(z[0] * inv, z[1] * inv, hv.x, lv.x);
-        split2(z[2] * inv, z[3] * inv, hv.y, lv.y);
-        uint8_t* at = smem + QR_OFF + km(row, 4 * lane, QR_LEAD);
-        *reinterpret_cast<uint2*>(at) = hv;
-        *reinterpret_cast<uint2*>(at + QR_PLANE) = lv;
+    const int g = a.g, v = lane >> 2, G = lane & 3, row = 8 * warp + v;
+    float x[32];
+    if (row < tl.nq * g) {
+      const size_t off = (((size_t)u.unit * g + row % g) * a.T + tl.t0 + row / g) * D + 32 * G;
+      if (BF16) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off);
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = __ldg(src + c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) unpack8(w[c], x + 8 * c);
+      } else {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + off);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<float4*>(x + 4 * c) = __ldg(src + c);
       }
-      float y0 = x.x * sg.x, y1 = x.y * sg.y, y2 = x.z * sg.z, y3 = x.w * sg.w;
-      hadamard_warp(y0, y1, y2, y3, lane);
-      const float sc = C_WHT * LOGIT_SCALE;
-      y0 *= sc * sk.x;
-      y1 *= sc * sk.y;
-      y2 *= sc * sk.z;
-      y3 *= sc * sk.w;
-      float inv;
-      const float s2 = pow2_of(warp_max(fmaxf(fmaxf(fabsf(y0), fabsf(y1)), fmaxf(fabsf(y2), fabsf(y3)))), inv);
-      if (lane == 0) sh.qscale[row] = s2;
-      uint32_t h0, l0, h1, l1;
-      split2(y0 * inv, y1 * inv, h0, l0);
-      split2(y2 * inv, y3 * inv, h1, l1);
-      uint8_t* st = smem + (size_t)row * Q_STRIDE;
-      const int pa = 2 * place_of(4 * lane), pb = 2 * place_of(4 * lane + 2);
-      *reinterpret_cast<uint32_t*>(st + pa) = h0;
-      *reinterpret_cast<uint32_t*>(st + pb) = h1;
-      *reinterpret_cast<uint32_t*>(st + 2 * D + pa) = l0;
-      *reinterpret_cast<uint32_t*>(st + 2 * D + pb) = l1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) mul2(x[i], x[i + 1], LOGIT_SCALE, LOGIT_SCALE);
+    float inv;
+    float s2 = pow2_of(quad_max(x), inv);
+    if (G == 0) sh.qraw[row] = s2;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(x[8 * c + 2 * e] * inv, x[8 * c + 2 * e + 1] * inv, hi[e], lo[e]);
+      uint8_t* at = smem + QR_OFF + km(row, 32 * G + 8 * c, QR_LEAD);
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(at + QR_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    rotate32(x, G, a.p.signs, nullptr);
+    if (a.sinkhorn) {
+      const __half2* sig = reinterpret_cast<const __half2*>(a.p.sigk + ((size_t)u.layer * a.Hkv + u.h) * D + 32 * G);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 f = __half22float2(sig[i / 2]);
+        mul2(x[i], x[i + 1], f.x, f.y);
+      }
+    }
+    s2 = pow2_of(quad_max(x), inv);
+    if (G == 0) sh.qscale[row] = s2;
+    uint8_t* st = smem + (size_t)row * Q_STRIDE + 64 * G;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = at_place(8 * i + 2 * e);
+        split2(x[c] * inv, x[c + 1] * inv, hi[e], lo[e]);
+      }
+      *reinterpret_cast<uint4*>(st + 16 * i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(st + 2 * D + 16 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     fence_async_smem();
   }
@@ -376,6 +422,7 @@ struct Kernel {
   __device__ void issue_logits(const Stretch& u) {
     const Tiles& tl = u.tl;
     const uint32_t base = smem_u32(smem);
+#pragma unroll 1
     for (int it = u.ta; it < u.tb; ++it, ++gt) {
       const int s = gt % NS, bb = gt & 1;
       // the stage's keys; the buffer is free once the values' products of two tiles before have read its weights
@@ -384,12 +431,12 @@ struct Kernel {
       fence_after();
       const uint32_t dS = tmem + C_S + NT * bb;
       if (it < tl.nqt) {
-        uint64_t k = sdesc(base + s * STAGE, 1024, 128);
-        uint32_t q = tmem + C_QHI;
-#pragma unroll 1
-        for (int ks = 0; ks < D / 16; ++ks, k += 128, q += 8) {
-          mma_ts(dS, q, k, ID_S, ks > 0);
-          mma_ts(dS, q + (C_QLO - C_QHI), k, ID_S, 1);
+        const uint64_t k = sdesc(base + s * STAGE, K_LEAD, 128);
+        const uint32_t q = tmem + C_QHI;
+#pragma unroll 2
+        for (int ks = 0; ks < D / 16; ++ks) {
+          mma_ts(dS, q + 8 * ks, k + 2 * K_LEAD / 16 * ks, ID_S, ks > 0);
+          mma_ts(dS, q + 8 * ks + (C_QLO - C_QHI), k + 2 * K_LEAD / 16 * ks, ID_S, 1);
         }
       } else {
         uint64_t k = sdesc(base + s * STAGE, RNT * 16, 128), q = sdesc(base + QR_OFF, QR_LEAD, 128);
@@ -397,7 +444,7 @@ struct Kernel {
         for (int ks = 0; ks < D / 16; ++ks, k += RNT * 2, q += 2 * QR_LEAD / 16) {
           mma_ss(dS, q, k, ID_SR, ks > 0);
           mma_ss(dS, q + QR_PLANE / 16, k, ID_SR, 1);
-          if (!BF16) mma_ss(dS, q, k + LO_PLANE / 16, ID_SR, 1);
+          if (!BF16) mma_ss(dS, q, k + LO_K / 16, ID_SR, 1);
         }
       }
       mma_commit(&sh.sfull[bb]);
@@ -407,24 +454,27 @@ struct Kernel {
   __device__ void issue_values(const Stretch& u) {
     const Tiles& tl = u.tl;
     const uint32_t base = smem_u32(smem);
+#pragma unroll 1
     for (int it = u.ta; it < u.tb; ++it, ++gt) {
       const int s = gt % NS, bb = gt & 1;
       if (!held(&sh.pfull[bb], (gt >> 1) & 1) || !held(&sh.vfull[s], (gt / NS) & 1)) return;
+      if (gt >= 2 && !held(&sh.ofree[bb], ((gt - 2) >> 1) & 1)) return;
       fence_after();
-      uint64_t v = sdesc(base + s * STAGE + V_OFF, 2048, 128);
       uint32_t p = tmem + C_S + NT * bb;
       const uint32_t dO = tmem + C_O + D * bb;
       if (it < tl.nqt) {
-#pragma unroll 1
-        for (int ks = 0; ks < NT / 16; ++ks, v += 256, p += 16) {
-          mma_ts(dO, p + 8, v, ID_O, ks > 0);
-          mma_ts(dO, p, v, ID_O, 1);
+        const uint64_t v = sdesc(base + s * STAGE + V_OFF, V_LEAD, 128);
+#pragma unroll 2
+        for (int ks = 0; ks < NT / 16; ++ks) {
+          mma_ts(dO, p + 16 * ks + 8, v + 2 * V_LEAD / 16 * ks, ID_O, ks > 0);
+          mma_ts(dO, p + 16 * ks, v + 2 * V_LEAD / 16 * ks, ID_O, 1);
         }
       } else {
+        uint64_t v = sdesc(base + s * STAGE + V_OFF, V_LEAD, 128);
 #pragma unroll 1
-        for (int ks = 0; ks < RNT / 16; ++ks, v += 256, p += 16) {
+        for (int ks = 0; ks < RNT / 16; ++ks, v += 2 * V_LEAD / 16, p += 16) {
           mma_ts(dO, p + 8, v, ID_OR, ks > 0);
-          if (!BF16) mma_ts(dO, p, v + LO_PLANE / 16, ID_OR, 1);
+          if (!BF16) mma_ts(dO, p, v + LO_V / 16, ID_OR, 1);
           mma_ts(dO, p, v, ID_OR, 1);
         }
       }
@@ -433,368 +483,458 @@ struct Kernel {
     }
   }
 
-  // ---------------------------------------------------------------- operands
-  // Lane (r, i) = (lane & 7, lane >> 3): the eight lanes of a store phase write eight rows of one core matrix.
-  __device__ void operands(const Stretch& u) {
-    const Tiles& tl = u.tl;
-    const int ta = u.ta, tb = u.tb;
-    const int dw = warp - DQ0, r = lane & 7, i = lane >> 3, h = u.h;
+  // ---------------------------------------------------------------- pages and operands
+  // One lane brings the pages of the stretch's recorded tiles, two ahead; the others read the block table ahead of it.
+  __device__ void fetch(const Stretch& u) {
     const int32_t* bt = a.block_table + (size_t)u.b * a.max_pages_per_seq;
-    const uint8_t* pages = a.p.pages + ((size_t)u.layer * a.L.n_pages * a.Hkv + h) * a.L.page_bytes;
-    const size_t page_step = (size_t)a.Hkv * a.L.page_bytes;
-    const int last_q = min(tb, tl.nqt);
-    uint4 kw[4], vw[4];
-    float2 sc = make_float2(0.f, 0.f);
-    auto page_of = [&](int it) { return it < last_q ? __ldg(bt + it) : 0; };
-    auto load = [&](int it, int phys, bool keys, uint4 (&w)[4]) {
-      // chunk dw + 4 (q & 1) of block q >> 1
-#pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-      if (keys) sc = make_float2(0.f, 0.f);
-      if (it >= last_q || phys < 0 || phys >= a.L.n_pages) return;
-      const uint8_t* at = pages + phys * page_step + (keys ? 0 : 4096) + dw * 512 + (r * 4 + i) * 16;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (it * NT + HALF * (q >> 1) < tl.qend)
-          w[q] = __ldg(reinterpret_cast<const uint4*>(at + (size_t)(q >> 1) * a.L.half_bytes + (q & 1) * 2048));
-      if (keys && dw == 0 && lane < 2 && it * NT + HALF * lane < tl.qend)
-        sc = __ldg(reinterpret_cast<const float2*>(pages + phys * page_step + (size_t)lane * a.L.half_bytes + a.L.off_kmeta));
-    };
-    int phys = page_of(ta), next = page_of(ta + 1);
-    load(ta, phys, true, kw);
-    load(ta, phys, false, vw);
-    for (int it = ta; it < tb; ++it, ++gt) {
-      const int s = gt % NS;
-      const uint32_t before = ((gt / NS) & 1) ^ 1;  // phase of the stage's previous use
-      uint8_t* kp = smem + s * STAGE;
-      uint8_t* vp = kp + V_OFF;
-      if (gt >= NS && !held(&sh.kempty[s], before)) return;
-      if (it < tl.nqt) {
-        if ((phys < 0 || phys >= a.L.n_pages) && dw == 0 && lane == 0) atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
-        phys = next;
-        next = page_of(it + 2);
-        if (dw == 0 && lane < 2) sh.scale[gt & 7][lane] = sc;
-        // chunk 4 mt + p (p = dw, mt = q & 1): tokens 16 mt + r and + 8, channels of K-group 4 p + i
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t o = km(32 * (q >> 1) + 16 * (q & 1) + r, 8 * (4 * dw + i), 1024);
-          *reinterpret_cast<uint4*>(kp + o) = make_uint4(codes_lo(kw[q].x), codes_lo(kw[q].y), codes_lo(kw[q].z), codes_lo(kw[q].w));
-          *reinterpret_cast<uint4*>(kp + o + 128) = make_uint4(codes_hi(kw[q].x), codes_hi(kw[q].y), codes_hi(kw[q].z), codes_hi(kw[q].w));
+    const int last = min(u.tb, u.tl.nqt);
+#pragma unroll 1
+    for (int it0 = u.ta; it0 < last; it0 += 32) {
+      const int mine = it0 + lane < last ? __ldg(bt + it0 + lane) : 0;
+#pragma unroll 1
+      for (int it = it0; it < min(last, it0 + 32); ++it, ++gr) {
+        const int phys = __shfl_sync(FULL, mine, it - it0), s = gr % RS;
+        if (gr >= RS && !held(&sh.rempty[s], ((gr / RS) & 1) ^ 1)) return;
+        if (lane == 0) {
+          if (phys < 0 || phys >= a.L.n_pages) {
+            atomicOr(a.p.status, KVQ_DEV_BAD_PAGE);
+            sh.halves[s] = 0;
+            bar_arrive(&sh.rfull[s]);
+          } else {
+            const int n = it * NT + HALF < u.tl.qend ? 2 : 1;
+            sh.halves[s] = n;
+            bar_expect(&sh.rfull[s], n * a.L.half_bytes);
+            bulk_g2s(smem + PAGE_OFF + s * PAGE_SLOT, a.p.pages + (((size_t)u.layer * a.L.n_pages + phys) * a.Hkv + u.h) * a.L.page_bytes,
+                     n * a.L.half_bytes, &sh.rfull[s]);
+          }
         }
-        fence_async_smem();
         __syncwarp();
-        if (lane == 0) bar_arrive(&sh.kfull[s]);
-        load(it + 1, phys, true, kw);
-        if (gt >= NS && !held(&sh.vempty[s], before)) return;
-        // chunk j = dw + 4 (q & 1): channels 16 j + r and + 8, positions of K-group 4 (q >> 1) + i
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t o = km(16 * (dw + 4 * (q & 1)) + r, 8 * (4 * (q >> 1) + i), 2048);
-          *reinterpret_cast<uint4*>(vp + o) = make_uint4(codes_lo(vw[q].x), codes_lo(vw[q].y), codes_lo(vw[q].z), codes_lo(vw[q].w));
-          *reinterpret_cast<uint4*>(vp + o + 128) = make_uint4(codes_hi(vw[q].x), codes_hi(vw[q].y), codes_hi(vw[q].z), codes_hi(vw[q].w));
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sh.vfull[s]);
-        load(it + 1, phys, false, vw);
-      } else {
-        const int j0 = tl.rlo + (it - tl.nqt) * RNT;
-        raw(u, j0, j0 - tl.rlo, false, kp);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sh.kfull[s]);
-        if (gt >= NS && !held(&sh.vempty[s], before)) return;
-        raw(u, j0, j0 - tl.rlo, true, vp);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sh.vfull[s]);
       }
     }
   }
-  // raw keys (K-major) or values (N-major: rows are positions too) of positions j0 .. j0 + RNT - 1 as operand planes, each
-  // vector over its power of two.  A bf16 vector's elements that its fp16 plane does not hold exactly are 2^-14 of the
-  // largest or smaller and off by 2^-25 of it at most.
-  __device__ void raw(const Stretch& u, int j0, int slot0, bool values, uint8_t* plane) {
+  // Lane (r, i) = (lane >> 2, lane & 3) takes the 16 bytes of (r, i) of a chunk, in order.  (A half that is not there, or not
+  // read, may hold anything: its codes are finite and its weights zero.)
+  __device__ void operands(const Stretch& u) {
+    const int dw = warp - DQ0, r = lane >> 2, i = lane & 3;
+    const int last_q = min(u.tb, u.tl.nqt);
+    int it = u.ta;
+#pragma unroll 1
+    for (; it < last_q; ++it, ++gt, ++gr) {
+      const int s = gt % NS, rs = gr % RS;
+      const uint32_t before = ((gt / NS) & 1) ^ 1;  // phase of the stage's previous use
+      uint8_t* kp = smem + s * STAGE + km(r, 8 * (4 * dw + i), K_LEAD);
+      uint8_t* vp = smem + s * STAGE + V_OFF + km(16 * dw + r, 8 * i, V_LEAD);
+      const uint8_t* pg = smem + PAGE_OFF + rs * PAGE_SLOT + dw * 512 + lane * 16;
+      if (!held(&sh.rfull[rs], (gr / RS) & 1)) return;
+      if (gt >= NS && !held(&sh.kempty[s], before)) return;
+      if (dw == 0 && lane < 2)
+        sh.scale[gt & 7][lane] = lane < sh.halves[rs] ? *reinterpret_cast<const float2*>(smem + PAGE_OFF + rs * PAGE_SLOT + lane * (PAGE_SLOT / 2) + 8192)
+                                                      : make_float2(0.f, 0.f);
+      // chunk 4 mt + p (p = dw, mt = q & 1) of block q >> 1: tokens 16 mt + r and + 8, channels of K-group 4 p + i
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 w = *reinterpret_cast<const uint4*>(pg + (q >> 1) * (PAGE_SLOT / 2) + (q & 1) * 2048);
+        uint8_t* o = kp + (32 * (q >> 1) + 16 * (q & 1)) * 16;
+        *reinterpret_cast<uint4*>(o) = make_uint4(codes_lo(w.x), codes_lo(w.y), codes_lo(w.z), codes_lo(w.w));
+        *reinterpret_cast<uint4*>(o + 128) = make_uint4(codes_hi(w.x), codes_hi(w.y), codes_hi(w.z), codes_hi(w.w));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.kfull[s]);
+      if (gt >= NS && !held(&sh.vempty[s], before)) return;
+      // chunk j = dw + 4 (q & 1): channels 16 j + r and + 8, positions of K-group 4 (q >> 1) + i
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 w = *reinterpret_cast<const uint4*>(pg + (q >> 1) * (PAGE_SLOT / 2) + 4096 + (q & 1) * 2048);
+        uint8_t* o = vp + 64 * (q & 1) * 16 + 4 * (q >> 1) * V_LEAD;
+        *reinterpret_cast<uint4*>(o) = make_uint4(codes_lo(w.x), codes_lo(w.y), codes_lo(w.z), codes_lo(w.w));
+        *reinterpret_cast<uint4*>(o + 128) = make_uint4(codes_hi(w.x), codes_hi(w.y), codes_hi(w.z), codes_hi(w.w));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(&sh.vfull[s]);
+        bar_arrive(&sh.rempty[rs]);
+      }
+    }
+#pragma unroll 1
+    for (; it < u.tb; ++it, ++gt) {
+      const int s = gt % NS, j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+      const uint32_t before = ((gt / NS) & 1) ^ 1;
+      uint8_t* kp = smem + s * STAGE;
+      if (gt >= NS && !held(&sh.kempty[s], before)) return;
+      if (!raw<false>(u, j0, kp)) return;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.kfull[s]);
+      if (gt >= NS && !held(&sh.vempty[s], before)) return;
+      if (!raw<true>(u, j0, kp + V_OFF)) return;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.vfull[s]);
+    }
+  }
+  // Raw keys (K-major) or values (N-major: rows are positions too, in the order of the places) of positions j0 .. j0 + RNT - 1
+  // as operand planes, over a power of two of the tile.  An element of a bf16 vector that its one fp16 plane does not hold
+  // exactly is below 2^-14 of the tile's largest and off by 2^-25 of that at most.
+  template <bool VALUES>
+  __device__ bool raw(const Stretch& u, int j0, uint8_t* plane) {
     const int dw = warp - DQ0, r = lane & 7, i = lane >> 3;
     const int p0 = u.p0;
     const size_t unit = u.unit;
-    const void* chunk = values ? a.v : a.k;
-    const float* old = values ? a.snap_v : a.snap_k;
-#pragma unroll 1
-    for (int t = 8 * dw + r; t < RNT; t += 8 * N_DQ) {
-      const int j = j0 + t;
-      const bool here = j <= u.tl.Pmax;
-      const size_t off = j < p0 ? (unit * a.W + j % a.W) * D : (unit * a.T + (j - p0)) * D;
-      const void* src = j < p0 ? (const void*)old : chunk;
-      const int bf16 = j < p0 ? 0 : a.in_bf16;
-      auto load8 = [&](int q, float (&x)[8]) {  // channels 8 (4 q + i) ..
+    const void* chunk = VALUES ? a.v : a.k;
+    const float* old = VALUES ? a.snap_v : a.snap_k;
+    constexpr int ROUNDS = RNT / (8 * N_DQ);
+    uint4 w[ROUNDS][BF16 ? 4 : 8];  // bf16 values, or floats; every load of the tile under way at once
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 f = here ? load4_in(src, off + 8 * (4 * q + i) + e, bf16) : make_float4(0.f, 0.f, 0.f, 0.f);
-          x[e] = f.x;
-          x[e + 1] = f.y;
-          x[e + 2] = f.z;
-          x[e + 3] = f.w;
+    for (int n = 0; n < ROUNDS; ++n) {
+      const int j = j0 + 8 * dw + r + 8 * N_DQ * n;
+#pragma unroll
+      for (int q = 0; q < (BF16 ? 4 : 8); ++q) w[n][q] = make_uint4(0u, 0u, 0u, 0u);
+      if (j > u.tl.Pmax) continue;
+      if (j < p0) {
+        const float4* f = reinterpret_cast<const float4*>(old + (unit * a.W + j % a.W) * D) + 2 * i;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 x = __ldg(f + 8 * q), y = __ldg(f + 8 * q + 1);
+          if (BF16) w[n][q] = pack8(x, y);
+          else {
+            w[n][2 * q] = *reinterpret_cast<const uint4*>(&x);
+            w[n][2 * q + 1] = *reinterpret_cast<const uint4*>(&y);
+          }
         }
-      };
-      float m = 0.f;
+      } else {
+        const uint4* f = static_cast<const uint4*>(chunk) + (unit * a.T + (j - p0)) * (BF16 ? 16 : 32) + (BF16 ? 1 : 2) * i;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (BF16) w[n][q] = __ldg(f + 4 * q);
+          else {
+            w[n][2 * q] = __ldg(f + 8 * q);
+            w[n][2 * q + 1] = __ldg(f + 8 * q + 1);
+          }
+        }
+      }
+    }
+    auto eight = [&](int n, int q, float (&x)[8]) {  // channels 8 (4 q + i) ..
+      if (BF16) unpack8(w[n][q], x);
+      else {
+        *reinterpret_cast<uint4*>(x) = w[n][(2 * q) % (BF16 ? 4 : 8)];
+        *reinterpret_cast<uint4*>(x + 4) = w[n][(2 * q + 1) % (BF16 ? 4 : 8)];
+      }
+    };
+    float m = 0.f;
+#pragma unroll
+    for (int n = 0; n < ROUNDS; ++n)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
-        load8(q, x);
+        eight(n, q, x);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) m = max3(m, fabsf(x[e]), fabsf(x[e + 1]));
       }
-      m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
-      m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
-      float inv;
-      const float s2 = pow2_of(m, inv);
-      if (i == 0) (values ? sh.rawv : sh.rawk)[slot0 + t] = here ? s2 : 0.f;
-#pragma unroll 2
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    if (lane == 0) {
+      sh.warp_most[VALUES][dw] = m;
+      bar_arrive(&sh.most);
+    }
+    if (!held(&sh.most, gm++ & 1)) return false;
+#pragma unroll
+    for (int o = 0; o < N_DQ; ++o) m = fmaxf(m, sh.warp_most[VALUES][o]);
+    float inv;
+    const float s2 = pow2_of(m, inv);
+    if (dw == 0 && lane < 2) reinterpret_cast<float*>(&sh.scale[gt & 7][lane])[VALUES] = s2;
+#pragma unroll
+    for (int n = 0; n < ROUNDS; ++n) {
+      const int t = 8 * dw + r + 8 * N_DQ * n, k = place_of(t);
+#pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
-        load8(q, x);
+        eight(n, q, x);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(x[2 * e] * inv, x[2 * e + 1] * inv, hi[e], lo[e]);
         const int kg = 4 * q + i;
-        const uint32_t o = values ? (uint32_t)((t >> 3) * 2048 + kg * 128 + (t & 7) * 16) : km(t, 8 * kg, RNT * 16);
+        const uint32_t o = VALUES ? (uint32_t)((k >> 3) * V_LEAD + kg * 128 + (k & 7) * 16) : km(t, 8 * kg, RNT * 16);
         *reinterpret_cast<uint4*>(plane + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (!BF16) *reinterpret_cast<uint4*>(plane + LO_PLANE + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (!BF16) *reinterpret_cast<uint4*>(plane + (VALUES ? LO_V : LO_K) + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
+    return true;
   }
 
   // ---------------------------------------------------------------- softmax
   struct Row {
-    float acc[D];  // sum of weights times values over vref, of this group's tiles
-    float m, l;    // the weights' reference and their sum
-    float vref, rvref;
+    float m, l;  // the weights' reference and their sum, of this group's tiles
+    float vref;  // power of two that the values' scales are held against
+    // its inverse (0 before there is one)
+    __device__ __forceinline__ float rvref() const { return vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f; }
   };
-  // acc += this group's last P V
-  __device__ __forceinline__ void drain(Row& w, uint32_t addr) {
-#pragma unroll
-    for (int c0 = 0; c0 < D; c0 += 32) {
-      float o[32];
-      tm_ld32(addr + c0, o);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) add2(w.acc[c0 + i], w.acc[c0 + i + 1], o[i], o[i + 1]);
-    }
-  }
-  __device__ __forceinline__ void rescale(Row& w, float f) {
-#pragma unroll
-    for (int i = 0; i < D; i += 2) mul2(w.acc[i], w.acc[i + 1], f, f);
-  }
   // a larger logit or a larger scale of values than the references allow for
   __device__ __forceinline__ void follow(Row& w, float mx, float vmax) {
-    float f = 1.f;
     if (mx > w.m + (BOOST + RAISE_AT)) {
       const float mnew = mx - BOOST;
-      f = w.m == -INFINITY ? 0.f : ex2(w.m - mnew);
-      w.l *= f;
+      w.l = w.m == -INFINITY ? w.l : w.l * ex2(w.m - mnew);
       w.m = mnew;
     }
-    if (vmax > 4.f * w.vref) {
-      float inv;
-      const float vnew = pow2_of(vmax, inv);
-      f *= w.vref * inv;
-      w.vref = vnew;
-      w.rvref = inv;
-    }
-    if (__any_sync(FULL, f != 1.f)) rescale(w, f);
+    float inv;
+    if (vmax > 4.f * w.vref) w.vref = pow2_of(vmax, inv);
   }
+  // The largest logit of a tile; MASKED: some row does not attend to all of it, but to columns first .. last
+  template <bool MASKED>
+  __device__ __forceinline__ float top_of(uint32_t sa, const float (&dk)[2], int first, int last) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c0 = 0; c0 < NT; c0 += 32) {
+      float t = -INFINITY, v[32];
+      tm_ld32(sa + c0, v);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        if (MASKED) {
+          if (c0 + i < first || c0 + i > last) v[i] = -INFINITY;
+          if (c0 + i + 1 < first || c0 + i + 1 > last) v[i + 1] = -INFINITY;
+        }
+        t = max3(t, v[i], v[i + 1]);
+      }
+      // (a block of which nothing is attended to may have a scale of zero)
+      if (!MASKED || t > -INFINITY) mx = fmaxf(mx, t * dk[c0 >> 5]);
+    }
+    return mx;
+  }
+  // Its weights, each with its value's scale f (over vref) in the exponent: w' = 2^(l - m + log2 f); the sum of weights
+  // over a block is that of the w' over f.  (An f of zero, or so small that its w' are below fp16's smallest number,
+  // counts as 2^-42.)  A weight's hi part is its upper 11 bits, cut, lo the rest rounded to 11.
+  template <bool MASKED>
+  __device__ __forceinline__ void weigh(Row& w, uint32_t sa, const float (&dk)[2], const float (&dv)[2], int first, int last) {
+    const float m0 = w.m == -INFINITY ? 0.f : w.m;
+#pragma unroll 1
+    for (int c0 = 0; c0 < NT; c0 += 32) {
+      const float f = fmaxf((c0 ? dv[1] : dv[0]) * w.rvref(), 0x1p-42f), k = c0 ? dk[1] : dk[0], b = __log2f(f) - m0;
+      float s0 = 0.f, s1 = 0.f, v[32];
+      tm_ld32(sa + c0, v);
+      // K-step by K-step of P V, in the order of the places
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = at_place(16 * ks + 2 * e);
+          float x = v[c], y = v[c + 1];
+          fma2(x, y, k, k, b, b);
+          x = ex2(MASKED && (c0 + c < first || c0 + c > last) ? -INFINITY : x);
+          y = ex2(MASKED && (c0 + c + 1 < first || c0 + c + 1 > last) ? -INFINITY : y);
+          add2(s0, s1, x, y);
+          const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
+          sub2(x, y, hx, hy);
+          pw[e] = h2u(__floats2half2_rn(hx, hy));
+          pw[8 + e] = h2u(__floats2half2_rn(x, y));
+        }
+        tm_st16(sa + c0 + 16 * ks, pw);
+      }
+      w.l += __fdividef(s0 + s1, f);
+    }
+  }
+  // a tile's references, for whoever adds its P V
+  __device__ __forceinline__ void leave(const Row& w, int row) {
+    sh.mt[gt & 3][row] = w.m;
+    if (row == 0) sh.vt[gt & 3] = w.vref;
+  }
+  // its weights are in tensor memory
+  __device__ __forceinline__ void hand_over(int grp) {
+    tm_wait_st();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&sh.pfull[grp]);
+  }
+  // Little lives from tile to tile in registers (a tile takes most of them): the rest is read again from shared memory.
+  __device__ void softmax(const Stretch& u) {
+    const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t sa = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C_S + NT * grp;
+    // rows past the last query go along with it (and are not written)
+    const int P = min(u.p0 + u.tl.t0 + row / a.g, u.tl.Pmax);
+    Row w = {-INFINITY, 0.f, 0.f};
+    const int first = u.ta + ((gt & 1) != grp), left = u.tb - u.ta;
+    gt += first - u.ta;
+    int it = first;
+#pragma unroll 1
+    while (it < u.tb) {
+      // recorded tiles that every row attends to as a whole
+      bool rec = false;
+      float dk[2], dv[2];
+      const int hi = P - a.W;  // the last recorded position that is attended to, as long as it is there
+#pragma unroll 1
+      for (; it < u.tb; it += 2, gt += 2) {
+        if (!held(&sh.sfull[grp], (gt >> 1) & 1)) return;
+        fence_after();
+        rec = it < u.tl.nqt;
+        const float2 s0 = sh.scale[gt & 7][0], s1 = sh.scale[gt & 7][1];
+        const float qs = sh.qscale[row];
+        dk[0] = s0.x * qs;
+        dk[1] = s1.x * qs;
+        dv[0] = s0.y;
+        dv[1] = s1.y;
+        // (the first tiles share references, and a page that is not there has scales of zero: below)
+        if (!__all_sync(FULL, rec && it > u.ta + 1 && it * NT + NT - 1 <= hi && fmaxf(s0.y, s1.y) > 0.f)) break;
+        follow(w, top_of<false>(sa, dk, 0, 0), fmaxf(s0.y, s1.y));
+        leave(w, row);
+        weigh<false>(w, sa, dk, dv, 0, 0);
+        hand_over(grp);
+      }
+      if (it >= u.tb) break;
+      // any other tile: columns first .. last are attended to
+      int first, last;
+      if (rec) {
+        first = 0;
+        last = page_bad(u, it) ? -1 : hi - it * NT;
+      } else {
+        if (!held(&sh.vfull[gt % NS], (gt / NS) & 1)) return;  // (both its powers of two are there)
+        const float2 s0 = sh.scale[gt & 7][0];
+        dk[0] = dk[1] = s0.x * sh.qraw[row];
+        dv[0] = dv[1] = s0.y;
+        const int j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+        first = hi + 1 - j0;
+        last = min(P - j0, RNT - 1);
+      }
+      const float mx = top_of<true>(sa, dk, first, last);
+      // The second group begins with the first one's references: as long as neither moves, their parts add up as they are.
+      if (it == u.ta + 1) {
+        if (!held(&sh.begun[warp & 3], gb & 1)) return;
+        w.m = sh.mt[(gt - 1) & 3][row];
+        w.vref = sh.vt0[warp & 3];
+      }
+      follow(w, mx, fmaxf(dv[0], dv[1]));
+      leave(w, row);
+      if (it == u.ta && left > 1) {
+        if (lane == 0) sh.vt0[warp & 3] = w.vref;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.begun[warp & 3]);
+      }
+      weigh<true>(w, sa, dk, dv, first, last);
+      hand_over(grp);
+      it += 2;
+      gt += 2;
+    }
+    gb += left > 1;
+    gt += left - (first - u.ta) - ((left - (first - u.ta) + 1) & ~1);  // tiles of the stretch, whoever softened them
+    sh.m[grp][row] = w.m;
+    sh.l[grp][row] = w.l;
+  }
+  __device__ __forceinline__ bool page_bad(const Stretch& u, int it) const {
+    const int phys = __ldg(a.block_table + (size_t)u.b * a.max_pages_per_seq + it);
+    return phys < 0 || phys >= a.L.n_pages;
+  }
+
+  // ---------------------------------------------------------------- the output
   // the accumulator from the values' quantised space to the heads': s . (c H (sigma . y))
-  __device__ __forceinline__ void to_heads(Row& w, const Stretch& u) {
+  __device__ __forceinline__ void to_heads(float (&acc)[D], const Stretch& u) {
     if (a.sinkhorn) {
       const __half2* sig = reinterpret_cast<const __half2*>(a.p.sigv + ((size_t)u.layer * a.Hkv + u.h) * D);
 #pragma unroll
       for (int i = 0; i < D; i += 2) {
         const float2 s = __half22float2(__ldg(sig + i / 2));
-        mul2(w.acc[i], w.acc[i + 1], s.x, s.y);
+        mul2(acc[i], acc[i + 1], s.x, s.y);
       }
     }
 #pragma unroll
     for (int i = 0; i < D; i += 2) {
-      const float p = w.acc[i], q = w.acc[i + 1];
-      w.acc[i] = p + q;
-      w.acc[i + 1] = p - q;
+      const float p = acc[i], q = acc[i + 1];
+      acc[i] = p + q;
+      acc[i + 1] = p - q;
     }
 #pragma unroll
     for (int hs = 2; hs < D; hs <<= 1) {
 #pragma unroll
       for (int i = 0; i < D; i += 2) {
         if (i & hs) continue;
-        bfly2(w.acc[i], w.acc[i + 1], w.acc[i + hs], w.acc[i + hs + 1]);
+        bfly2(acc[i], acc[i + 1], acc[i + hs], acc[i + hs + 1]);
       }
     }
 #pragma unroll
     for (int i = 0; i < D; i += 4) {
       const float4 s = *reinterpret_cast<const float4*>(sh.signs + i);
-      mul2(w.acc[i], w.acc[i + 1], C_WHT * s.x, C_WHT * s.y);
-      mul2(w.acc[i + 2], w.acc[i + 3], C_WHT * s.z, C_WHT * s.w);
+      mul2(acc[i], acc[i + 1], C_WHT * s.x, C_WHT * s.y);
+      mul2(acc[i + 2], acc[i + 3], C_WHT * s.z, C_WHT * s.w);
     }
   }
-  // a tile of recorded positions; MASKED: some row does not attend to all of them
-  template <bool MASKED>
-  __device__ __forceinline__ void soften(Row& w, uint32_t sa, const float (&dk)[2], const float (&dv)[2], int j0, int hi) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int c0 = 0; c0 < NT; c0 += 32) {
-      float v[32];
-      tm_ld32(sa + c0, v);
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        m = MASKED ? max3(m, j0 + c0 + i <= hi ? v[i] : -INFINITY, j0 + c0 + i + 1 <= hi ? v[i + 1] : -INFINITY) : max3(m, v[i], v[i + 1]);
-      if (!MASKED || j0 + c0 <= hi) mx = fmaxf(mx, m * dk[c0 >> 5]);
-    }
-    follow(w, mx, fmaxf(dv[0], dv[1]));
-    const float m0 = w.m == -INFINITY ? 0.f : w.m;
-    // K-step by K-step of P V: the first of a block needs columns 8 n .. + 3, the second 8 n + 4 .. + 7, so the first one's
-    // weights wait until the second one's logits are read
-#pragma unroll
-    for (int c0 = 0; c0 < NT; c0 += 32) {
-      const float k = dk[c0 >> 5], f = dv[c0 >> 5] * w.rvref;
-      float s0 = 0.f, s1 = 0.f;
-      uint32_t pw[32];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float v[16];  // v[4 n + e]: column 8 n + 4 half + e
-        tm_ld4x4(sa + c0 + 4 * half, v);
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const int c = j0 + c0 + 8 * (i >> 2) + 4 * half + (i & 3);
-          fma2(v[i], v[i + 1], k, k, -m0, -m0);
-          v[i] = ex2(!MASKED || c <= hi ? v[i] : -INFINITY);
-          v[i + 1] = ex2(!MASKED || c + 1 <= hi ? v[i + 1] : -INFINITY);
-          add2(s0, s1, v[i], v[i + 1]);
-          mul2(v[i], v[i + 1], f, f);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int col = at_place(16 * half + 2 * e), i = 4 * (col >> 3) + (col & 3);
-          split2(v[i], v[i + 1], pw[16 * half + e], pw[16 * half + 8 + e]);
-        }
-      }
-      w.l += s0 + s1;
-      tm_st32(sa + c0, pw);
-    }
+  __device__ __forceinline__ void free_output() {
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(&sh.ofree[gt & 1]);
   }
-  // a tile of raw positions, lo < j <= hi attended
-  __device__ __forceinline__ void soften_raw(Row& w, uint32_t sa, float qs, int slot0, int j0, int lo, int hi) {
-    float mx = -INFINITY, vmax = 0.f;
+  // acc 2^M V is the sum of weights times values so far, of both groups' tiles
+  __device__ void sums(const Stretch& u) {
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C_O;
+    float acc[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) acc[i] = 0.f;
+    float M = -INFINITY, V = 0.f;
+    int it = u.ta;
+    // recorded tiles, then raw ones
 #pragma unroll 1
-    for (int c0 = 0; c0 < RNT; c0 += 32) {
-      float v[32];
-      tm_ld32(sa + c0, v);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int j = j0 + c0 + i;
-        if (j > lo && j <= hi) mx = fmaxf(mx, v[i] * (sh.rawk[slot0 + c0 + i] * qs));
-        vmax = fmaxf(vmax, sh.rawv[slot0 + c0 + i]);
-      }
-    }
-    follow(w, mx, vmax);
-    const float m0 = w.m == -INFINITY ? 0.f : w.m;
+    for (int part = 0; part < 2; ++part) {
+      const int end = part ? u.tb : min(u.tb, u.tl.nqt);
 #pragma unroll 1
-    for (int c0 = 0; c0 < RNT; c0 += 32) {
-      float v[32];
-      tm_ld32(sa + c0, v);
+      while (it < end) {
+        float m, v;
+        // tiles under the references of those before
+#pragma unroll 1
+        for (; it < end; ++it, ++gt) {
+          if (!held(&sh.pvdone[gt & 1], (gt >> 1) & 1)) return;
+          fence_after();
+          m = sh.mt[gt & 3][row];
+          v = sh.vt[gt & 3];
+          if (__any_sync(FULL, m != M || v != V)) break;
+          const uint32_t oa = at + D * (gt & 1);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int j = j0 + c0 + i;
-        const float p = j > lo && j <= hi ? ex2(v[i] * (sh.rawk[slot0 + c0 + i] * qs) - m0) : 0.f;
-        w.l += p;
-        v[i] = p * (sh.rawv[slot0 + c0 + i] * w.rvref);
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tm_ld32(oa + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) add2(acc[c0 + i], acc[c0 + i + 1], o[i], o[i + 1]);
+          }
+          free_output();
+        }
+        if (it >= end) break;
+        const float Mn = fmaxf(M, m), Vn = fmaxf(V, v), rv = Vn > 0.f ? 1.f / Vn : 0.f;
+        // (where nothing was attended to the part is zero)
+        const float fa = (M == -INFINITY ? 1.f : ex2(M - Mn)) * (V * rv), fo = (m == -INFINITY ? 1.f : ex2(m - Mn)) * (v * rv);
+        M = Mn;
+        V = Vn;
+        const uint32_t oa = at + D * (gt & 1);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          tm_ld32(oa + c0, o);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            mul2(o[i], o[i + 1], fo, fo);
+            fma2(acc[c0 + i], acc[c0 + i + 1], fa, fa, o[i], o[i + 1]);
+          }
+        }
+        free_output();
+        ++it;
+        ++gt;
       }
-      uint32_t pw[32];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split2(v[16 * k + 2 * e], v[16 * k + 2 * e + 1], pw[16 * k + e], pw[16 * k + 8 + e]);
-      tm_st32(sa + c0, pw);
+      if (part == 0 && it > u.ta) to_heads(acc, u);
     }
-  }
-  __device__ void softmax(const Stretch& u, Row& w) {
-    const Tiles& tl = u.tl;
-    const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
-    const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16), sa = at + C_S + NT * grp, oa = at + C_O + D * grp;
-    // rows past the last query go along with it (and are not written)
-    const int P = min(u.p0 + tl.t0 + row / a.g, tl.Pmax), W = a.W;
-    const float qs = sh.qscale[row], qr = sh.qraw[row];
+    // (no operand is in use any more: every product of the stretch has been waited for)
+    float* o = reinterpret_cast<float*>(smem + (size_t)row * O_STRIDE);
 #pragma unroll
-    for (int i = 0; i < D; ++i) w.acc[i] = 0.f;
-    w.m = -INFINITY;
-    w.l = w.vref = w.rvref = 0.f;
-    bool pending = false, heads = false;
-    for (int it = u.ta; it < u.tb; ++it, ++gt) {
-      if ((gt & 1) != grp) continue;
-      if (pending) {
-        if (!held(&sh.pvdone[grp], ((gt - 2) >> 1) & 1)) return;
-        fence_after();
-        drain(w, oa);
-      }
-      if (it >= tl.nqt && !heads) {
-        if (pending) to_heads(w, u);
-        heads = true;
-      }
-      if (!held(&sh.sfull[grp], (gt >> 1) & 1)) return;
-      fence_after();
-      if (it < tl.nqt) {
-        const float2 s0 = sh.scale[gt & 7][0], s1 = sh.scale[gt & 7][1];
-        const float dk[2] = {s0.x * qs, s1.x * qs}, dv[2] = {s0.y, s1.y};
-        const int j0 = it * NT, hi = P - W;
-        // (a page that is not there has scales of zero: nothing of it is attended to)
-        const int top = s0.x == 0.f && s1.x == 0.f && s0.y == 0.f && s1.y == 0.f && page_bad(u, it) ? -1 : hi;
-        if (__all_sync(FULL, j0 + NT - 1 <= top)) soften<false>(w, sa, dk, dv, j0, top);
-        else soften<true>(w, sa, dk, dv, j0, top);
-      } else {
-        const int slot0 = (it - tl.nqt) * RNT;
-        if (!held(&sh.vfull[gt % NS], (gt / NS) & 1)) return;  // (the values' powers of two are there)
-        soften_raw(w, sa, qr, slot0, tl.rlo + slot0, P - W, P);
-      }
-      tm_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.pfull[grp]);
-      pending = true;
-    }
-    if (pending) {
-      // the group's last tile: the last of the segment or the one before
-      const int last = (gt & 1) != grp ? gt - 1 : gt - 2;
-      if (!held(&sh.pvdone[grp], (last >> 1) & 1)) return;
-      fence_after();
-      drain(w, oa);
-      if (!heads) to_heads(w, u);
-    }
+    for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(acc[i] * V, acc[i + 1] * V, acc[i + 2] * V, acc[i + 3] * V);
+    sh.M[row] = M;
   }
-  __device__ __forceinline__ bool page_bad(const Stretch& u, int it) const {
-    const int phys = __ldg(a.block_table + (size_t)u.b * a.max_pages_per_seq + it);
-    return phys < 0 || phys >= a.L.n_pages;
-  }
-  __device__ void leave_row(const Row& w) {
-    const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
-    float* o = reinterpret_cast<float*>(smem + ((size_t)grp * ROWS + row) * O_STRIDE);
-#pragma unroll
-    for (int i = 0; i < D; i += 4)
-      *reinterpret_cast<float4*>(o + i) = make_float4(w.acc[i] * w.vref, w.acc[i + 1] * w.vref, w.acc[i + 2] * w.vref, w.acc[i + 3] * w.vref);
-    sh.m[grp][row] = w.m;
-    sh.l[grp][row] = w.l;
-  }
-  // both groups' parts together, to the output or to a partial result
+  // rows to the output, or to a partial result
   __device__ void rows_out(const Stretch& u) {
     const Tiles& tl = u.tl;
-    float* rec = u.rec < 0 ? nullptr : recs + (size_t)u.rec * REC;
+    float* rec = u.rec < 0 ? nullptr : a.parts + (size_t)u.rec * REC;
     const int g = a.g, nrows = tl.nq * g;
     const size_t head0 = (size_t)u.unit * g;
-#pragma unroll 2
-    for (int row = warp; row < nrows; row += THREADS / 32) {
-      const float m0 = sh.m[0][row], m1 = sh.m[1][row], M = fmaxf(m0, m1);
-      const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-      const float l = sh.l[0][row] * f0 + sh.l[1][row] * f1;
-      const float4 x = *reinterpret_cast<const float4*>(smem + (size_t)row * O_STRIDE + 16 * lane);
-      const float4 y = *reinterpret_cast<const float4*>(smem + (size_t)(ROWS + row) * O_STRIDE + 16 * lane);
-      float4 o = make_float4(x.x * f0 + y.x * f1, x.y * f0 + y.y * f1, x.z * f0 + y.z * f1, x.w * f0 + y.w * f1);
+#pragma unroll 1
+    for (int row = warp; row < nrows; row += ROW_WARPS) {
+      const float M = sh.M[row], m0 = sh.m[0][row], m1 = sh.m[1][row];
+      const float l = sh.l[0][row] * (m0 == -INFINITY ? 1.f : ex2(m0 - M)) + sh.l[1][row] * (m1 == -INFINITY ? 1.f : ex2(m1 - M));
+      float4 o = *reinterpret_cast<const float4*>(smem + (size_t)row * O_STRIDE + 16 * lane);
       if (rec) {
         *reinterpret_cast<float4*>(rec + row * D + 4 * lane) = o;
         if (lane == 0) {
@@ -809,46 +949,59 @@ struct Kernel {
     }
   }
 
-  // ---------------------------------------------------------------- a warp's life: ROLE 0 softmax, 1 operands, 2 logits, 3 values, 4 where to go on
+  // ---------------------------------------------------------------- a warp's life
+  enum { SOFTMAX, SUMS, OPERANDS, LOGITS, VALUES, PAGES, AHEAD };
   template <int ROLE>
   __device__ void run() {
+    stretches<ROLE>();
+    // everything that a warp has issued lands before the columns are freed
+    if (ROLE == LOGITS || ROLE == VALUES) {
+      uint64_t* bar = &sh.done[ROLE - LOGITS];
+      mma_commit(bar);
+      bar_land(bar, 0);
+    }
+    if (ROLE == PAGES && sh.gone)
+      for (int n = max(0, gr - RS); n < gr; ++n) bar_land(&sh.rfull[n % RS], (n / RS) & 1);
+    fence_before();
+    sync_all();
+    if (ROLE == LOGITS) {
+      fence_after();
+      tm_free(tmem, TMEM_COLS);
+    }
+  }
+  template <int ROLE>
+  __device__ void stretches() {
+#pragma unroll 1
     for (int k = 0;; ++k) {
       const Stretch& u = sh.at[k & 1];
       if (u.tb < 0) return;
-      queries(u);
+      if (ROLE <= OPERANDS) queries(u);
       sync_all();
-      if (ROLE == 0) queries_to_tmem();
+      if (ROLE == SOFTMAX) queries_to_tmem();
       fence_before();
       sync_all();
       fence_after();
-      if constexpr (ROLE == 0) {
-        Row w;
-        softmax(u, w);
-        sync_all();
-        if (sh.gone) return;
-        leave_row(w);
-      } else {
-        if (ROLE == 1) operands(u);
-        else if (ROLE == 2) issue_logits(u);
-        else if (ROLE == 3) issue_values(u);
-        else if (warp == NEXT_WARP && lane == 0)
-          locate(u.next, work.cut(blockIdx.x), work.cut(blockIdx.x + 1), sh.at[(k + 1) & 1]);
-        sync_all();
-        if (sh.gone) return;
-      }
+      if (ROLE == SOFTMAX) softmax(u);
+      if (ROLE == SUMS) sums(u);
+      if (ROLE == OPERANDS) operands(u);
+      if (ROLE == LOGITS) issue_logits(u);
+      if (ROLE == VALUES) issue_values(u);
+      if (ROLE == PAGES) fetch(u);
+      if (ROLE == AHEAD && lane == 0)
+        locate(Work(a, sh.p0, sh.pre, sh.ctas), u.next, sh.at[(k + 1) & 1]);
       sync_all();
-      rows_out(u);
+      if (sh.gone) return;
+      if (ROLE <= OPERANDS) rows_out(u);
       sync_all();
     }
   }
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_constant__ PrefillArgs a, float* recs) {
+__global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_constant__ PrefillArgs a) {
   using K = Kernel<BF16>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ typename K::Shared sh;
-  Work work;
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid < D) sh.signs[tid] = a.p.signs[tid];
   if (tid == 32) {
@@ -858,16 +1011,23 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
       bar_init(&sh.vfull[s], N_DQ);
       bar_init(&sh.vempty[s], 1);
     }
+    for (int i = 0; i < 4; ++i) bar_init(&sh.begun[i], 1);
+    bar_init(&sh.most, N_DQ);
+    for (int i = 0; i < RS; ++i) {
+      bar_init(&sh.rfull[i], 1);
+      bar_init(&sh.rempty[i], N_DQ);
+    }
     for (int i = 0; i < 2; ++i) {
       bar_init(&sh.sfull[i], 1);
       bar_init(&sh.pfull[i], N_SOFT / 2);
       bar_init(&sh.pvdone[i], 1);
+      bar_init(&sh.ofree[i], N_SUM);
       bar_init(&sh.done[i], 1);
     }
     sh.gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  plan(a, work, sh.p0, sh.pre, gridDim.x);
+  const Work work = plan(a, sh.p0, sh.pre, gridDim.x);
   // sequences that are not part of the call, or past capacity: zeros
   for (int b = 0; b < a.batch; ++b) {
     if (sh.p0[b] >= 0) continue;
@@ -884,34 +1044,26 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
   }
   __syncthreads();
   fence_after();
-  K k(a, sh, smem, work, recs);
-  k.tmem = sh.tmem;
   if (tid == NEXT_WARP * 32) {
-    const long long lo = work.cut(blockIdx.x);
-    k.locate(lo, lo, work.cut(blockIdx.x + 1), sh.at[0]);
+    sh.ctas = work.n;
+    K(a, sh, smem).locate(work, work.cut(blockIdx.x), sh.at[0]);
   }
   __syncthreads();
   if (warp < N_SOFT) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFT_REGS));
-    k.template run<0>();
+    take_registers<SOFT_REGS>();
+    K(a, sh, smem).template run<K::SOFTMAX>();
+  } else if (warp < DQ0) {
+    take_registers<SUM_REGS>();
+    K(a, sh, smem).template run<K::SUMS>();
+  } else if (warp < S_WARP) {
+    take_registers<DQ_REGS>();
+    K(a, sh, smem).template run<K::OPERANDS>();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp < DQ0 + N_DQ) k.template run<1>();
-    else if (warp == S_WARP) k.template run<2>();
-    else if (warp == PV_WARP) k.template run<3>();
-    else k.template run<4>();
-    // everything that a warp has issued lands before the columns are freed
-    if (warp == S_WARP || warp == PV_WARP) {
-      uint64_t* bar = &sh.done[warp - S_WARP];
-      mma_commit(bar);
-      bar_land(bar, 0);
-    }
-  }
-  fence_before();
-  part_sync(1, THREADS);
-  if (warp == S_WARP) {
-    fence_after();
-    tm_free(k.tmem, TMEM_COLS);
+    take_registers<ISSUE_REGS>();
+    if (warp == S_WARP) K(a, sh, smem).template run<K::LOGITS>();
+    else if (warp == PV_WARP) K(a, sh, smem).template run<K::VALUES>();
+    else if (warp == PAGE_WARP) K(a, sh, smem).template run<K::PAGES>();
+    else K(a, sh, smem).template run<K::AHEAD>();
   }
 }
 
@@ -919,12 +1071,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
 // row tile, for a share of the rows; parts in the order of their CTAs.
 constexpr int JOIN_SHARES = 8, JOIN_WARPS = ROWS / JOIN_SHARES;
 template <bool BF16>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __grid_constant__ PrefillArgs a, const float* recs, int ctas) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int ctas) {
+  const float* recs = a.parts;
   __shared__ int p0s[MAX_BATCH];
   __shared__ long long pre[MAX_BATCH + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  Work w;
-  plan(a, w, p0s, pre, ctas);
+  const Work w = plan(a, p0s, pre, ctas);
   const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
   if (c >= w.n || w.total() == 0) return;
   const long long y = w.cut(c);
@@ -973,7 +1125,7 @@ template <bool BF16>
 cudaError_t launch(const PrefillArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = allow_shared_memory<prefill_block_kernel<BF16>>();
   if (e != cudaSuccess) return e;
-  prefill_block_kernel<BF16><<<sms, THREADS, SMEM, s>>>(a, a.parts);
+  prefill_block_kernel<BF16><<<sms, THREADS, SMEM, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms, JOIN_SHARES);
@@ -984,7 +1136,7 @@ cudaError_t launch(const PrefillArgs& a, int sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_join_kernel<BF16>, a, (const float*)a.parts, sms);
+  return cudaLaunchKernelEx(&cfg, prefill_join_kernel<BF16>, a, sms);
 }
 
 }  // namespace
