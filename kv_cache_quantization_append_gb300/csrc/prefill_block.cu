@@ -88,19 +88,26 @@ struct Unit {
 };
 
 // Costs in positions: row tile x of a sequence at p0 counts p0 + (x + 1) qpt + K0, about the positions it visits.  The line
-// goes through sequences, row tiles, (layer, kv-head) pairs; cut c is at total * c / n.
+// goes through sequences, row tiles, (layer, kv-head) pairs, and is cut into n parts of equal cost.
 struct Work {
   int B, T, qpt, nx, HL, n;
+  long long share, rest;   // of the n parts, the first `rest` are one longer
   const int* p0;           // per sequence; -1: not part of the call
   const long long* pre;    // cost before each sequence, [B + 1]
+  Work() = default;
   __device__ Work(const PrefillArgs& a, const int* p, const long long* c, int ctas)
       : B(a.batch), T(a.T), qpt(ROWS / a.g), nx((a.T + ROWS / a.g - 1) / (ROWS / a.g)), HL(a.Hkv * a.n_layers_call), n(ctas), p0(p), pre(c) {}
+  __device__ void divide(int ctas) {
+    n = ctas;
+    share = total() / n;
+    rest = total() - share * n;
+  }
   __device__ __forceinline__ long long cost(int b, int x) const { return p0[b] + (long long)(x + 1) * qpt + K0; }
   __device__ __forceinline__ long long upto(int b, int x) const {
     return (x * (p0[b] + K0) + (long long)qpt * x * (x + 1) / 2) * HL;
   }
   __device__ __forceinline__ long long total() const { return pre[B]; }
-  __device__ __forceinline__ long long cut(int c) const { return total() / n * c + total() % n * c / n; }
+  __device__ __forceinline__ long long cut(int c) const { return share * c + min((long long)c, rest); }
   __device__ Unit find(long long y) const {
     Unit u;
     int lo = 0, hi = B - 1;
@@ -151,7 +158,7 @@ __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas) {
     if (lane == 31) pre[a.batch] = incl;
   }
   __syncthreads();
-  w.n = (int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE));
+  w.divide((int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE)));
   return w;
 }
 
@@ -987,8 +994,11 @@ struct Kernel {
       if (ROLE == LOGITS) issue_logits(u);
       if (ROLE == VALUES) issue_values(u);
       if (ROLE == PAGES) fetch(u);
-      if (ROLE == AHEAD && lane == 0)
-        locate(Work(a, sh.p0, sh.pre, sh.ctas), u.next, sh.at[(k + 1) & 1]);
+      if (ROLE == AHEAD && lane == 0) {
+        Work w(a, sh.p0, sh.pre, 1);
+        w.divide(sh.ctas);
+        locate(w, u.next, sh.at[(k + 1) & 1]);
+      }
       sync_all();
       if (sh.gone) return;
       if (ROLE <= OPERANDS) rows_out(u);
@@ -1067,62 +1077,69 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
   }
 }
 
-// Joins the partial results of the row tiles that a cut divides.  Block (c, part): cut c + 1, if it is the first within its
-// row tile, for a share of the rows; parts in the order of their CTAs.
-constexpr int JOIN_SHARES = 8, JOIN_WARPS = ROWS / JOIN_SHARES;
+// Joins the partial results of the row tiles that a cut divides.  Block (c, share): cut c + 1, if it is the first within its
+// row tile, for a share of the rows; parts in the order of their CTAs.  One thread finds the parts (a CTA's stretch of the
+// row tile is its first unless it began before), a warp joins a row.
+constexpr int JOIN_SHARES = 8, JOIN_WARPS = ROWS / JOIN_SHARES, MAX_CTAS = 256;
 template <bool BF16>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int ctas) {
-  const float* recs = a.parts;
   __shared__ int p0s[MAX_BATCH];
   __shared__ long long pre[MAX_BATCH + 1];
+  __shared__ int part[MAX_CTAS + 1], n_parts;
+  __shared__ Unit unit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Work w = plan(a, p0s, pre, ctas);
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), g = a.g;
   if (c >= w.n || w.total() == 0) return;
-  const long long y = w.cut(c);
-  const Unit u = w.find(y);
-  const Tiles tl(w, u, a.W, Kernel<BF16>::RNT);
-  const int at = tl.before(y - u.start);
-  if (at == 0 || at == tl.n) return;
-  const long long y1 = w.cut(c - 1);
-  if (y1 > u.start && tl.before(y1 - u.start) > 0) return;  // an earlier cut within the row tile
-  const int row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), g = a.g;
-  if (row >= tl.nq * g) return;
-  // parts: of CTA c - 1 (its first stretch only if that begins in this row tile), then of those that begin in it
-  const long long end = u.start + u.cost;
-  auto part_of = [&](int k) { return recs + (size_t)(2 * k + (w.cut(k) >= u.start ? 0 : 1)) * REC; };
-  auto empty = [&](int k) {
-    const long long lo = w.cut(k), hi = w.cut(k + 1);
-    return (lo > u.start ? tl.before(lo - u.start) : 0) >= (hi >= end ? tl.n : tl.before(hi - u.start));
-  };
-  int last = c;
-  while (last + 1 < w.n && w.cut(last + 1) < end) ++last;
+  if (threadIdx.x == 0) {
+    n_parts = 0;
+    const Unit u = w.find(w.cut(c));
+    const Tiles tl(w, u, a.W, Kernel<BF16>::RNT);
+    const int at = tl.before(w.cut(c) - u.start);
+    const long long y1 = w.cut(c - 1), end = u.start + u.cost;
+    if (at > 0 && at < tl.n && !(y1 > u.start && tl.before(y1 - u.start) > 0)) {  // (no earlier cut within the row tile)
+      int from = 0, n = 0;
+      for (int k = c - 1; k < w.n && w.cut(k) < end; ++k) {
+        const int to = w.cut(k + 1) >= end ? tl.n : tl.before(w.cut(k + 1) - u.start);
+        if (to > from) part[n++] = 2 * k + (w.cut(k) >= u.start ? 0 : 1);
+        from = to;
+      }
+      n_parts = n;
+      unit = u;
+    }
+  }
+  __syncthreads();
+  const int n = n_parts;
+  if (n == 0) return;
+  const int t0 = unit.x * w.qpt;
+  if (row >= min(w.qpt, w.T - t0) * g) return;
   float M = -INFINITY;
-  for (int k = c - 1; k <= last; ++k)
-    if (!empty(k)) M = fmaxf(M, __ldcg(part_of(k) + ROWS * D + row));
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(a.parts + (size_t)part[k] * REC + ROWS * D + row));
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = c - 1; k <= last; ++k) {
-    if (empty(k)) continue;
-    const float* rec = part_of(k);
-    const float m = __ldcg(rec + ROWS * D + row);
-    const float f = m == -INFINITY ? 0.f : ex2(m - M);
+  for (int k = 0; k < n; ++k) {
+    const float* rec = a.parts + (size_t)part[k] * REC;
+    const float m = __ldcg(rec + ROWS * D + row), lk = __ldcg(rec + ROWS * D + ROWS + row);
     const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + row * D) + lane);
-    l += __ldcg(rec + ROWS * D + ROWS + row) * f;
+    const float f = m == -INFINITY ? 0.f : ex2(m - M);
+    l += lk * f;
     o.x += x.x * f;
     o.y += x.y * f;
     o.z += x.z * f;
     o.w += x.w * f;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t unit = ((size_t)(u.hl / a.Hkv) * a.batch + u.b) * a.Hkv + u.hl % a.Hkv;
-  *reinterpret_cast<float4*>(a.out + ((unit * g + row % g) * a.T + tl.t0 + row / g) * D + 4 * lane) =
+  const size_t head0 = (((size_t)(unit.hl / a.Hkv) * a.batch + unit.b) * a.Hkv + unit.hl % a.Hkv) * g;
+  *reinterpret_cast<float4*>(a.out + ((head0 + row % g) * a.T + t0 + row / g) * D + 4 * lane) =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
 template <bool BF16>
 cudaError_t launch(const PrefillArgs& a, int sms, cudaStream_t s) {
+  if (sms > MAX_CTAS) sms = MAX_CTAS;
   cudaError_t e = allow_shared_memory<prefill_block_kernel<BF16>>();
   if (e != cudaSuccess) return e;
   prefill_block_kernel<BF16><<<sms, THREADS, SMEM, s>>>(a);
