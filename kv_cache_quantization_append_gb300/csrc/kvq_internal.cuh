@@ -202,6 +202,7 @@ struct PoolArgs {
   const int32_t* counts;  // reserve: tokens, or null; fork: lengths
   int32_t* out;           // reserve: positions granted; fork: new lengths; compact: pages in use
   int n_layers, max_batch, Hkv, W, max_seq_len, batch, n_tokens;
+  int fork_smem;  // bytes of a fork block's stages
 };
 size_t pool_layout(void* pool, int n_pages, PoolArgs* a);  // the buffer's parts, where there is one; its bytes
 cudaError_t launch_pool_init(const PoolArgs& a, cudaStream_t s);

@@ -2,20 +2,24 @@
 //
 // State: refs[n_pages], how many entries of the block table name each page, and the table.  A free page is one with refs
 // 0; the lowest is taken first.  Planning (which entry gets which page) is one CTA's work: prefix sums over the call's
-// entries, then over refs.  What weighs is moved by a second, wide launch, a programmatic dependent of the plan, from the
-// plan's list of (from, to) pages: a page of one layer is contiguous, n_kv_heads * page_bytes.
-#include "kvq_internal.cuh"
+// entries, then over refs.  It is a chain of barriers and of trips to L2, so a call of few sequences takes a quarter of
+// the threads.  What weighs is moved by a second, wide launch, a programmatic dependent of the plan, from the plan's list
+// of (from, to) pages: a page of one layer is contiguous, n_kv_heads * page_bytes.
+#include "tc.cuh"
 
 namespace kvq {
 
 namespace {
 
-constexpr int PLAN = 1024;          // threads of a planning CTA
-constexpr int COPY_THREADS = 256;
+constexpr int PLAN = 1024, PLAN_FEW = 256;  // threads of a planning CTA
+constexpr int COPY_THREADS = 512;
 constexpr int COPY_VECS = 4;        // 16-byte vectors under way per thread
+constexpr int THREADS = 256;
 constexpr int COLS = 32;            // table columns of a fork's table CTA
+constexpr int FORK_SMEM = 96 * 1024, FORK_STAGES = 3, FORK_STAGE = FORK_SMEM / FORK_STAGES, MAX_SLICE = 16 * 1024, FORK_LISTS = 5;
 
-// Inclusive prefix sum over the CTA's PLAN threads; total gets the sum.  sums: 33 ints.
+// Inclusive prefix sum over the CTA's N threads; total gets the sum.  sums: 32 ints.
+template <int N>
 __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int incl = v;
@@ -27,30 +31,33 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
   __syncthreads();  // (the sums of the scan before have been read)
   if (lane == 31) sums[w] = incl;
   __syncthreads();
-  if (w == 0) {
-    int s = sums[lane];
+  // every warp adds up the warps' sums for itself
+  int s = lane < N / 32 ? sums[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(FULL, s, o);
-      if (lane >= o) s += y;
-    }
-    sums[lane] = s;
+  for (int o = 1; o < N / 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();
-  total = sums[31];
-  return incl + (w > 0 ? sums[w - 1] : 0);
+  total = __shfl_sync(FULL, s, N / 32 - 1);
+  const int before = __shfl_sync(FULL, s, w > 0 ? w - 1 : 0);
+  return incl + (w > 0 ? before : 0);
 }
 
 // The free pages in ascending order into pick[0 ..], until there are `want` of them; how many there are (up to the end
 // of the stretch that holds the last wanted one).
+template <int N>
 __device__ int list_free(const PoolArgs& a, int want, int* sums) {
   int found = 0;
-  for (int p0 = 0; p0 < a.L.n_pages && found < want; p0 += PLAN) {
-    const int p = p0 + threadIdx.x;
-    const bool is = p < a.L.n_pages && __ldcg(a.refs + p) == 0;
+  for (int p0 = 0; p0 < a.L.n_pages && found < want; p0 += 4 * N) {
+    const int p = p0 + 4 * threadIdx.x;
+    int4 r = make_int4(1, 1, 1, 1);  // (refs has room for whole vectors: what follows it is 256 bytes aligned)
+    if (p < a.L.n_pages) r = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
+    const bool is[4] = {r.x == 0, r.y == 0 && p + 1 < a.L.n_pages, r.z == 0 && p + 2 < a.L.n_pages, r.w == 0 && p + 3 < a.L.n_pages};
     int total;
-    const int at = found + block_scan(is, sums, total) - 1;
-    if (is) a.pick[at] = p;
+    int at = found + block_scan<N>(is[0] + is[1] + is[2] + is[3], sums, total) - (is[0] + is[1] + is[2] + is[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (is[k]) a.pick[at++] = p + k;
     found += total;
   }
   return found;
@@ -60,9 +67,10 @@ struct Item {
   int b, lp, page;  // page -1: none
 };
 
-__global__ void __launch_bounds__(PLAN) reserve_kernel(const __grid_constant__ PoolArgs a) {
-  __shared__ int sums[33];
-  __shared__ int start[PLAN + 1], first[PLAN], needs[PLAN];
+template <int N>
+__global__ void __launch_bounds__(N) reserve_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ int sums[32];
+  __shared__ int start[N], first[N], needs[N];
   __shared__ int n_copies;
   const int t = threadIdx.x, n_pages = a.L.n_pages, mpp = a.L.max_pages_per_seq;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -81,9 +89,7 @@ __global__ void __launch_bounds__(PLAN) reserve_kernel(const __grid_constant__ P
   needs[t] = 0;
   if (t == 0) n_copies = 0;
   int items;
-  const int incl = block_scan(pages, sums, items);
-  start[t] = incl - pages;
-  if (t == PLAN - 1) start[PLAN] = incl;
+  start[t] = block_scan<N>(pages, sums, items) - pages;
   __syncthreads();
   auto item = [&](int i) {
     int lo = 0, hi = a.batch - 1;
@@ -99,99 +105,111 @@ __global__ void __launch_bounds__(PLAN) reserve_kernel(const __grid_constant__ P
     it.page = e >= 0 && e < n_pages ? e : -1;
     return it;
   };
-  // pages that several entries name: how many of the call's would write each, and the last of them
-  for (int i = t; i < items; i += PLAN) {
+  // entries without a page; pages that several entries name: how many of the call's would write each, and the last of them
+  bool shares = false;
+  for (int i = t; i < items; i += N) {
     const Item it = item(i);
-    if (it.page >= 0 && __ldcg(a.refs + it.page) > 1) {
+    if (it.page < 0) {
+      atomicAdd(&needs[it.b], 1);
+    } else if (__ldcg(a.refs + it.page) > 1) {
+      shares = true;
       atomicAdd(a.writers + it.page, 1);
       atomicMax(a.last + it.page, i);
     }
   }
-  __syncthreads();
+  shares = __syncthreads_or(shares);
   // 0: has its page, 1: needs one, 2: needs a copy
   auto need = [&](const Item& it, int i) {
     if (it.page < 0) return 1;
+    if (!shares) return 0;
     const int r = __ldcg(a.refs + it.page);
     if (r <= 1) return 0;
     return __ldcg(a.writers + it.page) == r && __ldcg(a.last + it.page) == i ? 0 : 2;
   };
-  for (int i = t; i < items; i += PLAN) {
-    const Item it = item(i);
-    if (need(it, i)) atomicAdd(&needs[it.b], 1);
+  if (shares) {
+    for (int i = t; i < items; i += N) {
+      const Item it = item(i);
+      if (need(it, i) == 2) atomicAdd(&needs[it.b], 1);
+    }
+    __syncthreads();
   }
-  __syncthreads();
   int wanted;
-  const int upto = block_scan(needs[t], sums, wanted);
-  const int found = list_free(a, wanted, sums);
+  const int upto = block_scan<N>(needs[t], sums, wanted);
+  const int found = list_free<N>(a, wanted, sums);
   const bool fits = upto <= found;
   __syncthreads();
   needs[t] = fits;
   if (t < a.batch) {
     if (!fits && p >= 0) atomicOr(a.p.status, KVQ_DEV_NO_PAGES);
-    a.out[t] = fits ? (p >= 0 ? p : -1) : -1;
+    a.out[t] = fits ? p : -1;
   }
   __syncthreads();
-  int taken = 0;
-  for (int i0 = 0; i0 < items; i0 += PLAN) {
-    const int i = i0 + t;
-    Item it = {0, 0, -1};
-    int kind = 0;
-    if (i < items) {
-      it = item(i);
-      kind = need(it, i);
+  if (wanted > 0) {
+    int taken = 0;
+    for (int i0 = 0; i0 < items; i0 += N) {
+      const int i = i0 + t;
+      Item it = {0, 0, -1};
+      int kind = 0;
+      if (i < items) {
+        it = item(i);
+        kind = need(it, i);
+      }
+      int total;
+      const int at = taken + block_scan<N>(kind != 0, sums, total) - 1;
+      taken += total;
+      if (kind != 0 && needs[it.b]) {
+        const int page = __ldcg(a.pick + at);
+        a.table[(size_t)it.b * mpp + it.lp] = page;
+        a.refs[page] = 1;
+        if (kind == 2) a.copies[atomicAdd(&n_copies, 1)] = make_int2(it.page, page);
+      }
     }
-    int total;
-    const int at = taken + block_scan(kind != 0, sums, total) - 1;
-    taken += total;
-    if (kind != 0 && needs[it.b]) {
-      const int page = __ldcg(a.pick + at);
-      a.table[(size_t)it.b * mpp + it.lp] = page;
-      a.refs[page] = 1;
-      if (kind == 2) a.copies[atomicAdd(&n_copies, 1)] = make_int2(it.page, page);
+    __syncthreads();
+  }
+  if (shares) {
+    // the counts of shared pages, and their marks as they were
+    for (int c = t; c < n_copies; c += N) {
+      const int from = __ldcg(a.copies + c).x;
+      atomicSub(a.refs + from, 1);
+      a.writers[from] = 0;
+      a.last[from] = -1;
     }
-  }
-  __syncthreads();
-  // the counts of shared pages, and their marks as they were
-  for (int c = t; c < n_copies; c += PLAN) {
-    const int from = __ldcg(a.copies + c).x;
-    atomicSub(a.refs + from, 1);
-    a.writers[from] = 0;
-    a.last[from] = -1;
-  }
-  for (int i = t; i < items; i += PLAN) {
-    const Item it = item(i);
-    if (it.page >= 0 && __ldcg(a.writers + it.page) != 0) {
-      a.writers[it.page] = 0;
-      a.last[it.page] = -1;
+    for (int i = t; i < items; i += N) {
+      const Item it = item(i);
+      if (it.page >= 0 && __ldcg(a.writers + it.page) != 0) {
+        a.writers[it.page] = 0;
+        a.last[it.page] = -1;
+      }
     }
   }
   if (t == 0) *a.n_copies = n_copies;
 }
 
 // Pages in use: U of them.  Those from U on and the free ones below U, each in order, are the moves' two ends.
-__global__ void __launch_bounds__(PLAN) compact_kernel(const __grid_constant__ PoolArgs a) {
-  __shared__ int sums[33];
+template <int N>
+__global__ void __launch_bounds__(N) compact_kernel(const __grid_constant__ PoolArgs a) {
+  __shared__ int sums[32];
   const int t = threadIdx.x, n_pages = a.L.n_pages;
   asm volatile("griddepcontrol.launch_dependents;");
   int mine = 0;
-  for (int p = t; p < n_pages; p += PLAN) mine += __ldcg(a.refs + p) > 0;
+  for (int p = t; p < n_pages; p += N) mine += __ldcg(a.refs + p) > 0;
   int used;
-  block_scan(mine, sums, used);
+  block_scan<N>(mine, sums, used);
   int free_ends = 0, moves = 0;
-  for (int p0 = 0; p0 < n_pages; p0 += PLAN) {
+  for (int p0 = 0; p0 < n_pages; p0 += N) {
     const int p = p0 + t;
     const bool in_use = p < n_pages && __ldcg(a.refs + p) > 0;
     const bool hole = p < used && !in_use, mover = in_use && p >= used;
     int total;
-    // (a stretch of PLAN pages may hold both ends: counted in the two halves of one sum)
-    const int at = block_scan((int)hole | ((int)mover << 16), sums, total);
+    // (a stretch of pages may hold both ends: counted in the two halves of one sum)
+    const int at = block_scan<N>((int)hole | ((int)mover << 16), sums, total);
     if (hole) a.copies[free_ends + (at & 0xffff) - 1].y = p;
     if (mover) a.copies[moves + (at >> 16) - 1].x = p;
     free_ends += total & 0xffff;
     moves += total >> 16;
   }
   __syncthreads();
-  for (int c = t; c < moves; c += PLAN) {
+  for (int c = t; c < moves; c += N) {
     const int2 m = __ldcg(a.copies + c);
     a.pick[m.x] = m.y;
     a.refs[m.y] = __ldcg(a.refs + m.x);
@@ -253,75 +271,138 @@ __device__ __forceinline__ int length_of(const PoolArgs& a, int b, bool flag) {
   return 0;
 }
 
-// Blocks below table_ctas: COLS columns of the table each, all sequences of the call (entries of a page are in one
-// column: its counts are one block's).  The others: `slice` bytes of the rings of one (layer, head, keys or values),
-// every parent's read before any child's is written.
-__global__ void __launch_bounds__(COPY_THREADS) fork_kernel(const __grid_constant__ PoolArgs a, int table_ctas, int slice) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int t = threadIdx.x, B = a.batch;
-  if ((int)blockIdx.x < table_ctas) {
-    int* old = reinterpret_cast<int*>(smem);  // [B][COLS]
-    const int mpp = a.L.max_pages_per_seq, c = blockIdx.x * COLS + (t & (COLS - 1));
-    const bool here = c < mpp;
-    for (int b = t / COLS; b < B; b += COPY_THREADS / COLS) old[b * COLS + (t & (COLS - 1))] = here ? a.table[(size_t)b * mpp + c] : -1;
-    if (blockIdx.x == 0)
-      for (int b = t; b < B; b += COPY_THREADS) a.out[b] = length_of(a, parent_of(a, b, true), true);
-    __syncthreads();
-    for (int b = t / COLS; b < B; b += COPY_THREADS / COLS) {
-      const int q = parent_of(a, b, false);
-      if (q == b || !here) continue;
-      const int was = old[b * COLS + (t & (COLS - 1))];
-      const int now = c < (length_of(a, q, false) + PAGE - 1) / PAGE ? old[q * COLS + (t & (COLS - 1))] : -1;
-      if (was == now) continue;
-      if (was >= 0 && was < a.L.n_pages) atomicSub(a.refs + was, 1);
-      if (now >= 0 && now < a.L.n_pages) atomicAdd(a.refs + now, 1);
-      a.table[(size_t)b * mpp + c] = now;
-    }
-    return;
-  }
-  const size_t ring = (size_t)a.W * D * sizeof(float);  // of one (layer, sequence, head)
-  const int parts = (int)((ring + slice - 1) / slice);
-  unsigned r = blockIdx.x - table_ctas;
-  const int part = (int)(r % parts);
-  r /= parts;
-  const int h = (int)(r % a.Hkv);
-  r /= a.Hkv;
-  const int kv = (int)(r & 1), layer = (int)(r >> 1);
-  const size_t off = (size_t)part * slice;
-  uint8_t* base = reinterpret_cast<uint8_t*>(kv ? a.p.ringv : a.p.ringk) + ((size_t)layer * a.max_batch * a.Hkv + h) * ring + off;
-  const size_t step = (size_t)a.Hkv * ring;  // from one sequence to the next
-  int* parent = reinterpret_cast<int*>(smem);
-  int* bytes = parent + B;  // of the parent's slice that hold tokens
-  int* wanted = bytes + B;
-  uint8_t* held = smem + ((size_t)3 * B * 4 + 15) / 16 * 16;
-  for (int b = t; b < B; b += COPY_THREADS) {
+// What a fork does to the block table: COLS columns of it, all sequences of the call (entries that name a page are in one
+// column: its counts are one block's)
+__device__ void fork_table(const PoolArgs& a, int* old) {
+  const int t = threadIdx.x, B = a.batch, mpp = a.L.max_pages_per_seq, col = t & (COLS - 1), c = blockIdx.x * COLS + col;
+  const bool here = c < mpp;
+  for (int b = t / COLS; b < B; b += THREADS / COLS) old[b * COLS + col] = here ? a.table[(size_t)b * mpp + c] : -1;
+  if (blockIdx.x == 0)
+    for (int b = t; b < B; b += THREADS) a.out[b] = length_of(a, parent_of(a, b, true), true);
+  __syncthreads();
+  for (int b = t / COLS; b < B; b += THREADS / COLS) {
     const int q = parent_of(a, b, false);
-    parent[b] = q;
-    const long long n = (long long)min(length_of(a, q, false), a.W) * D * 4 - (long long)off;
-    bytes[b] = (int)max(0LL, min((long long)min((size_t)slice, ring - off), n));
-    wanted[b] = 0;
-  }
-  __syncthreads();
-  for (int b = t; b < B; b += COPY_THREADS)
-    if (parent[b] != b) wanted[parent[b]] = bytes[b];
-  __syncthreads();
-  const int vecs = slice / 16;
-  for (int i = t; i < B * vecs; i += COPY_THREADS) {
-    const int b = i / vecs, v = i % vecs;
-    if (16 * v < wanted[b]) *reinterpret_cast<uint4*>(held + (size_t)i * 16) = __ldcs(reinterpret_cast<const uint4*>(base + b * step) + v);
-  }
-  __syncthreads();
-  for (int i = t; i < B * vecs; i += COPY_THREADS) {
-    const int b = i / vecs, v = i % vecs;
-    if (parent[b] != b && 16 * v < bytes[b])
-      reinterpret_cast<uint4*>(base + b * step)[v] = *reinterpret_cast<const uint4*>(held + ((size_t)parent[b] * vecs + v) * 16);
+    if (q == b || !here) continue;
+    const int was = old[b * COLS + col];
+    const int now = c < (length_of(a, q, false) + PAGE - 1) / PAGE ? old[q * COLS + col] : -1;
+    if (was == now) continue;
+    if (was >= 0 && was < a.L.n_pages) atomicSub(a.refs + was, 1);
+    if (now >= 0 && now < a.L.n_pages) atomicAdd(a.refs + now, 1);
+    a.table[(size_t)b * mpp + c] = now;
   }
 }
 
-__global__ void __launch_bounds__(COPY_THREADS) release_kernel(const __grid_constant__ PoolArgs a) {
+// The rings.  A task is a slice of one (layer, head, keys or values): every parent's slice comes into shared memory by a
+// bulk copy (each parent's once, however many children it has), and once all of them are there each child's goes out by
+// another; so beams change places without a second copy of anything.  A CTA goes through its tasks FORK_STAGES deep; one
+// warp issues.  Bounded by memory: reads of the parents, writes of the children.
+__device__ void fork_rings(const PoolArgs& a, uint8_t* smem, int cta, int ctas) {
+  __shared__ __align__(8) uint64_t full[FORK_STAGES];
+  __shared__ int gone, n_parents, n_children, longest;
+  const int t = threadIdx.x, B = a.batch;
+  int* slot = reinterpret_cast<int*>(smem);  // of a sequence that is a parent: its place in a stage; -1: it is none
+  int* from = slot + B;                      // parents, in the order of their places
+  int* held = from + B;                      // bytes of a parent's ring that hold tokens
+  int* to = held + B;                        // children
+  int* of = to + B;                          // a child's parent's place
+  uint8_t* stages = smem + ((size_t)FORK_LISTS * B * 4 + 127) / 128 * 128;
+  if (t == 0) {
+    for (int i = 0; i < FORK_STAGES; ++i) tc::bar_init(&full[i], 1);
+    gone = n_parents = n_children = longest = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int b = t; b < B; b += THREADS) slot[b] = -1;
+  __syncthreads();
+  for (int b = t; b < B; b += THREADS) {
+    const int q = parent_of(a, b, false), n = min(length_of(a, q, false), a.W);
+    if (q != b && n > 0) {
+      slot[q] = 0;
+      const int i = atomicAdd(&n_children, 1);  // (their order does not matter)
+      to[i] = b;
+      of[i] = q;
+      atomicMax(&longest, n);
+    }
+  }
+  __syncthreads();
+  for (int b = t; b < B; b += THREADS)
+    if (slot[b] == 0) {
+      const int s = atomicAdd(&n_parents, 1);
+      from[s] = b;
+      held[s] = min(length_of(a, b, false), a.W) * D * 4;
+      slot[b] = s;
+    }
+  __syncthreads();
+  for (int i = t; i < n_children; i += THREADS) of[i] = slot[of[i]];
+  __syncthreads();
+  if (t >= 32 || n_children == 0) return;
+  const int lane = t, np = n_parents, nc = n_children;
+  const int used = longest * D * 4;                                     // bytes of the longest ring that hold tokens
+  const int slice = min(min(max(FORK_STAGE / np / 128 * 128, 128), MAX_SLICE), used);
+  const int stage_bytes = max(FORK_STAGE, np * slice), n_stages = max(1, min(FORK_STAGES, a.fork_smem / stage_bytes));
+  const size_t ring = (size_t)a.W * D * 4, step = (size_t)a.Hkv * ring;  // of one (layer, sequence, head); between sequences
+  const int parts = (used + slice - 1) / slice;
+  const long long tasks = (long long)2 * a.n_layers * a.Hkv * parts;
+  auto bytes_of = [&](int s, int off) { return max(0, min(slice, held[s] - off)); };  // of the slice of parent s's ring
+  auto place = [&](long long task, int& off) {
+    const int part = (int)(task % parts);
+    const long long r = task / parts;
+    const int h = (int)(r % a.Hkv);
+    const long long kl = r / a.Hkv;
+    off = part * slice;
+    return reinterpret_cast<uint8_t*>((kl & 1) ? a.p.ringv : a.p.ringk) + ((size_t)(kl >> 1) * a.max_batch * a.Hkv + h) * ring + off;
+  };
+  auto load = [&](long long task, int st) {
+    int off, sum = 0;
+    const uint8_t* base = place(task, off);
+    for (int i = lane; i < np; i += 32) sum += bytes_of(i, off);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (lane == 0) tc::bar_expect(&full[st], sum);
+    __syncwarp();
+    for (int i = lane; i < np; i += 32) {
+      const int n = bytes_of(i, off);
+      if (n > 0) tc::bulk_g2s(stages + (size_t)st * stage_bytes + (size_t)i * slice, base + from[i] * step, n, &full[st]);
+    }
+  };
+  // stage i % n_stages holds the CTA's i-th task
+  long long next = cta;
+  int loaded = 0;
+  for (; loaded < n_stages && next < tasks; ++loaded, next += ctas) load(next, loaded);
+  int done = 0;
+  for (long long task = cta; task < tasks; task += ctas, ++done) {
+    const int st = done % n_stages;
+    tc::bar_wait(&full[st], (done / n_stages) & 1, &gone, a.p.status, tc::LAND_NS);
+    if (__any_sync(FULL, *const_cast<volatile int*>(&gone))) break;
+    int off;
+    uint8_t* base = place(task, off);
+    for (int i = lane; i < nc; i += 32) {
+      const int n = bytes_of(of[i], off);
+      if (n > 0) tc::bulk_s2g(base + to[i] * step, stages + (size_t)st * stage_bytes + (size_t)of[i] * slice, n);
+    }
+    tc::bulk_commit();
+    if (next < tasks) {
+      tc::bulk_read_wait();  // the stage's stores have read it
+      __syncwarp();
+      load(next, st);
+      next += ctas;
+      ++loaded;
+    }
+  }
+  // what is under way lands before the CTA leaves
+  for (; done < loaded; ++done) tc::bar_land(&full[done % n_stages], (done / n_stages) & 1);
+  tc::bulk_wait();
+}
+
+__global__ void __launch_bounds__(THREADS) fork_kernel(const __grid_constant__ PoolArgs a, int table_ctas) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  if ((int)blockIdx.x < table_ctas) fork_table(a, reinterpret_cast<int*>(smem));
+  else fork_rings(a, smem, blockIdx.x - table_ctas, gridDim.x - table_ctas);
+}
+
+__global__ void __launch_bounds__(THREADS) release_kernel(const __grid_constant__ PoolArgs a) {
   const int mpp = a.L.max_pages_per_seq;
   const long long n = (long long)a.batch * mpp;
-  for (long long i = (long long)blockIdx.x * COPY_THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * COPY_THREADS) {
+  for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * THREADS) {
     const int b = (int)(i / mpp), lp = (int)(i % mpp);
     const int keep = a.pos[b];
     if (keep < 0 || (long long)lp * PAGE < keep) continue;
@@ -332,10 +413,10 @@ __global__ void __launch_bounds__(COPY_THREADS) release_kernel(const __grid_cons
   }
 }
 
-__global__ void __launch_bounds__(COPY_THREADS) init_kernel(const __grid_constant__ PoolArgs a) {
+__global__ void __launch_bounds__(THREADS) init_kernel(const __grid_constant__ PoolArgs a) {
   const long long entries = (long long)a.max_batch * a.L.max_pages_per_seq;
   const long long n = max(entries, (long long)a.L.n_pages);
-  for (long long i = (long long)blockIdx.x * COPY_THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * COPY_THREADS) {
+  for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < n; i += (long long)gridDim.x * THREADS) {
     if (i < entries) a.table[i] = -1;
     if (i < a.L.n_pages) {
       a.refs[i] = 0;
@@ -347,7 +428,7 @@ __global__ void __launch_bounds__(COPY_THREADS) init_kernel(const __grid_constan
 }
 
 unsigned blocks_for(long long threads) {
-  const long long b = (threads + COPY_THREADS - 1) / COPY_THREADS;
+  const long long b = (threads + THREADS - 1) / THREADS;
   return (unsigned)(b < 1 ? 1 : b > 2048 ? 2048 : b);
 }
 
@@ -358,7 +439,7 @@ cudaError_t launch_copies(const PoolArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(8 * sms));
+  cfg.gridDim = dim3((unsigned)(3 * sms));
   cfg.blockDim = dim3(COPY_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -387,42 +468,47 @@ size_t pool_layout(void* pool, int n_pages, PoolArgs* a) {
 
 cudaError_t launch_pool_init(const PoolArgs& a, cudaStream_t s) {
   const long long entries = (long long)a.max_batch * a.L.max_pages_per_seq;
-  init_kernel<<<blocks_for(entries > a.L.n_pages ? entries : a.L.n_pages), COPY_THREADS, 0, s>>>(a);
+  init_kernel<<<blocks_for(entries > a.L.n_pages ? entries : a.L.n_pages), THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pool_reserve(const PoolArgs& a, cudaStream_t s) {
   static_assert(MAX_BATCH <= PLAN, "a thread for each sequence");
-  reserve_kernel<<<1, PLAN, 0, s>>>(a);
+  if (a.batch <= PLAN_FEW) reserve_kernel<PLAN_FEW><<<1, PLAN_FEW, 0, s>>>(a);
+  else reserve_kernel<PLAN><<<1, PLAN, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_copies<false>(a, s);
 }
 
 cudaError_t launch_pool_compact(const PoolArgs& a, cudaStream_t s) {
-  compact_kernel<<<1, PLAN, 0, s>>>(a);
+  if (a.L.n_pages <= 4 * PLAN_FEW) compact_kernel<PLAN_FEW><<<1, PLAN_FEW, 0, s>>>(a);
+  else compact_kernel<PLAN><<<1, PLAN, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_copies<true>(a, s);
 }
 
-cudaError_t launch_pool_fork(const PoolArgs& a, cudaStream_t s) {
-  const int table_ctas = (a.L.max_pages_per_seq + COLS - 1) / COLS;
-  const size_t ring = (size_t)a.W * D * sizeof(float);
-  // slices of every sequence's ring side by side: about 32 KB of them a block, so that several blocks share an SM, but
-  // whole 128-byte lines
-  int slice = 32 * 1024 / a.batch / 128 * 128;
-  slice = slice < 128 ? 128 : slice > 4096 ? 4096 : slice;
-  const long long ring_ctas = (long long)2 * a.n_layers * a.Hkv * (long long)((ring + slice - 1) / slice);
-  if (table_ctas + ring_ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t table_smem = (size_t)a.batch * COLS * 4, ring_smem = ((size_t)3 * a.batch * 4 + 15) / 16 * 16 + (size_t)a.batch * slice;
-  const size_t smem = table_smem > ring_smem ? table_smem : ring_smem;
-  const cudaError_t e = allow_shared_memory<fork_kernel>();
+cudaError_t launch_pool_fork(const PoolArgs& a0, cudaStream_t s) {
+  PoolArgs a = a0;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = allow_shared_memory<fork_kernel>();
   if (e != cudaSuccess) return e;
-  fork_kernel<<<(unsigned)(table_ctas + ring_ctas), COPY_THREADS, smem, s>>>(a, table_ctas, slice);
+  const int table_ctas = (a.L.max_pages_per_seq + COLS - 1) / COLS;
+  // stages for slices of at least 128 bytes of as many parents as there may be; two blocks share an SM.  As many ring blocks
+  // as there are slices of MAX_SLICE at least (more parents make shorter ones), two an SM at most.
+  a.fork_smem = a.batch * 128 > FORK_SMEM ? a.batch * 128 : FORK_SMEM;
+  const long long ring = (long long)a.W * D * 4;
+  const long long slices = (long long)2 * a.n_layers * a.Hkv * ((ring + 2047) / 2048);
+  const int ring_ctas = (int)(slices < 2LL * sms ? slices : 2LL * sms);
+  const size_t table_smem = (size_t)a.batch * COLS * 4, ring_smem = ((size_t)FORK_LISTS * a.batch * 4 + 127) / 128 * 128 + a.fork_smem;
+  const size_t smem = table_smem > ring_smem ? table_smem : ring_smem;
+  fork_kernel<<<(unsigned)(table_ctas + ring_ctas), THREADS, smem, s>>>(a, table_ctas);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pool_release(const PoolArgs& a, cudaStream_t s) {
-  release_kernel<<<blocks_for((long long)a.batch * a.L.max_pages_per_seq), COPY_THREADS, 0, s>>>(a);
+  release_kernel<<<blocks_for((long long)a.batch * a.L.max_pages_per_seq), THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
