@@ -64,7 +64,7 @@ struct Geo {
 #define KVQ_Q8_CONSUMER_WARPS 11
 #endif
 #ifndef KVQ_QB_CONSUMER_WARPS
-#define KVQ_QB_CONSUMER_WARPS 11
+#define KVQ_QB_CONSUMER_WARPS 10
 #endif
   static constexpr int NCW = TQ ? KVQ_TQ_CONSUMER_WARPS : Q8 ? KVQ_Q8_CONSUMER_WARPS : QB ? KVQ_QB_CONSUMER_WARPS : KVQ_Q4_CONSUMER_WARPS;
   static constexpr int NTHREADS = (NCW + 1) * 32;      // + 1 producer warp

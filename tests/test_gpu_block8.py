@@ -352,3 +352,88 @@ def test_noalloc_and_named_streams():
     got = gpu.decode(0, q, ln, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_the_largest_batch():
+    """1024 sequences: decode, a chunk of two tokens each, some left alone."""
+    rng = np.random.default_rng(27)
+    gpu, ref = br.make(1, 1, 2, 1024, 96, window=32)
+    lens = rng.integers(0, 90, 1024)
+    k, v = (_vectors(rng, (1024, 1, 90), "bf16") for _ in range(2))
+    for n in sorted(set(lens.tolist()) - {0}):
+        pos = np.where(lens == n, 0, -1)
+        gpu.append(0, k[:, :, :n].contiguous().cuda(), v[:, :, :n].contiguous().cuda(), _i32(pos))
+        ref.append(0, harness.to_np(k[:, :, :n]), harness.to_np(v[:, :, :n]), pos.tolist())
+    _check_decode(gpu, ref, rng, lens, "bf16")
+    k, v, q = (_vectors(rng, (1024, h, 2), "bf16") for h in (1, 1, 2))
+    pos = np.where(np.arange(1024) % 5 == 3, -1, lens)
+    _check_prefill(gpu, ref, rng, k, v, q, pos.tolist())
+    br.check_state(gpu, ref, [(0, b, 0) for b in range(0, 1024, 31)])
+
+
+@pytest.mark.parametrize("lens,T", [([3000, 0, 17, 900, 2047, 64, 333, -1], 250), ([5000, 10, 20, 30], 33), ([700] * 30, 20)])
+def test_prefill_divided_over_all_blocks(lens, T):
+    """Sequences of very different lengths over several layers: row tiles that many blocks work on, and many in one block."""
+    rng = np.random.default_rng(28)
+    gpu, ref = br.make(3, 2, 6, len(lens), max(lens) + T, window=96)
+    for b, n in enumerate(lens):
+        if n > 0:
+            at = [-1] * len(lens)
+            at[b] = 0
+            _append(gpu, ref, -1, rng, n, at, "bf16")
+    k, v = (_vectors(rng, (3, len(lens), 2, T), "bf16") for _ in range(2))
+    q = _vectors(rng, (3, len(lens), 6, T), "bf16")
+    out = gpu.prefill(-1, k.cuda(), v.cuda(), q.cuda(), _i32(lens)).double().cpu().numpy()
+    assert gpu.status() == 0
+    ref.append(-1, harness.to_np(k), harness.to_np(v), lens)
+    qn = harness.to_np(q)
+    for b, n in enumerate(lens):
+        if n < 0:
+            assert (out[:, b] == 0).all()
+            continue
+        for lay in range(3):
+            for t in {0, T - 1, int(rng.integers(0, T))}:
+                want = np.stack([ref.attend(lay, b, j, qn[lay, b, j, t], n + t + 1) for j in range(6)])
+                harness.assert_attention_close(out[lay, b, :, t], want, TOL)
+
+
+def test_pages_past_4_gib():
+    """The last pages of a pool of 5 GB, keys and values of two layers."""
+    rng = np.random.default_rng(29)
+    n_pages = 20500
+    table = n_pages - 1 - np.arange(2 * 8).reshape(2, 8)
+    gpu, ref = br.make(2, 8, 8, 2, 512, window=64, n_pages=n_pages, table=table)
+    _append(gpu, ref, -1, rng, 400, [0, 0], "bf16")  # (decode reads the newest tokens from the ring: lengths are what was appended)
+    br.check_state(gpu, ref, [(lay, b, h) for lay in range(2) for b in range(2) for h in (0, 7)], table)
+    _check_decode(gpu, ref, rng, [400, 400], "bf16", 1)
+    k, v, q = (_vectors(rng, (2, 8, 45), "bf16") for _ in range(3))
+    _check_prefill(gpu, ref, rng, k, v, q, [400, 400], layer=1)
+    br.check_state(gpu, ref, [(1, b, h) for b in range(2) for h in (0, 7)], table)
+
+
+def test_a_captured_chunk_at_other_positions():
+    """A chunk captured once and replayed while positions and inputs change gives what calls give."""
+    rng = np.random.default_rng(30)
+    a, _ = br.make(2, 2, 8, 3, 1500, window=64)
+    b, _ = br.make(2, 2, 8, 3, 1500, window=64)
+    T = 90
+    k, v, q = (torch.zeros(2, 3, h, T, 128, dtype=torch.bfloat16, device="cuda") for h in (2, 2, 8))
+    pos, out = _i32([0, 0, 0]), torch.zeros(2, 3, 8, T, 128, device="cuda")
+    for x in (a, b):                                    # (also the calls outside capture before the first inside)
+        x.prefill(-1, k, v, q, pos, out=out)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        b.prefill(-1, k, v, q, pos, out=out)
+    at = np.array([0, 5, 0])
+    for step in range(12):
+        p = at.copy()
+        if step % 3 == 1:
+            p[1] = -1
+        for x, h in ((k, 2), (v, 2), (q, 8)):
+            x.copy_(_vectors(rng, (2, 3, h, T), "bf16"))
+        pos.copy_(_i32(p))
+        graph.replay()
+        want = a.prefill(-1, k, v, q, _i32(p))
+        assert torch.equal(out, want)
+        at[p >= 0] += T
+    assert a.status() == 0 and b.status() == 0

@@ -366,3 +366,43 @@ def test_prefill_onto_a_fork_and_eviction_of_a_shared_one():
     assert np.array_equal(x.bt.cpu().numpy(), x.ref.table)
     kept = x.bt[0].long()
     assert torch.equal(x.pages[:, kept], before[:, kept]) and (x.bt[1] >= 0).sum() == 4
+
+
+def test_pages_and_rings_past_4_gib():
+    """Pages copied, moved and rings forked at the far ends of arrays of 5 GB."""
+    n_pages, n_seqs = 33000, 600
+    cfg = lib.make_config(2, 8, 8, n_seqs, 640, window=1024, n_pages=n_pages)
+    bt = torch.zeros(n_seqs, 10, dtype=torch.int32, device="cuda")
+    gpu = QuantKVCache(cfg, "cuda", bt)
+    gpu.pool_init()
+    page, ring = 8 * 10240, 2 * n_seqs * 8 * 1024 * 512
+    size = -(-2 * n_pages * page // 256) * 256
+    off = lib.kv_cache_bytes(cfg) - size
+    pages = gpu.buffer[off:off + 2 * n_pages * page].view(2, n_pages, page)
+    assert ring % 256 == 0 and ring > 1 << 32 and n_pages * page * 2 > 1 << 32
+    rings = [gpu.buffer[o:o + ring].view(torch.float32).view(2, n_seqs, 8, 1024, 128) for o in (off - 2 * ring, off - ring)]
+    for r in rings:
+        r[:, 3] = torch.randn_like(r[:, 3])
+        r[:, 599] = 0
+    pages[:, 32990] = torch.randint(0, 256, (2, page), dtype=torch.uint8, device="cuda")
+    # sequence 3 has the far page, all the others below 32995 are counted as in use
+    bt[3, 0] = 32990
+    gpu.page_refs[:32995] = 1
+    parents = torch.full((n_seqs,), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros_like(parents)
+    parents[599], lens[3] = 3, 50
+    new = gpu.fork(parents, lens)
+    assert new[599] == 50 and bt[599, 0] == 32990 and gpu.page_refs[32990] == 2
+    for r in rings:
+        assert torch.equal(r[:, 599, :, :50], r[:, 3, :, :50]) and (r[:, 599, :, 50:] == 0).all()
+    pos = torch.full_like(parents, -1)
+    pos[599] = 50
+    assert torch.equal(gpu.reserve(pos, 4), pos)
+    assert bt[599, 0] == 32995 and gpu.page_refs[32990] == 1 and gpu.page_refs[32995] == 1
+    assert torch.equal(pages[:, 32995], pages[:, 32990])
+    # all but two pages given up, two far ones move to the front
+    gpu.page_refs[:32990] = 0
+    gpu.page_refs[32991:32995] = 0
+    assert gpu.compact().item() == 2 and bt[3, 0] == 0 and bt[599, 0] == 1 and gpu.page_refs.sum() == 2
+    assert torch.equal(pages[:, 0], pages[:, 32990]) and torch.equal(pages[:, 1], pages[:, 32990])
+    assert gpu.status() == 0
