@@ -500,7 +500,7 @@ constexpr int BULK_MIN_T = 16;
 
 cudaError_t launch_append(const AppendArgs& a0, cudaStream_t s) {
   AppendArgs a = a0;
-  if (a.k_format == KVQ_Q8B32) return launch_append_blocks(a, s);
+  if (a.k_format == KVQ_Q8B32) return launch_append_blocks(a, false, s);
   // the bulk kernel's grid has y = (layer, kv-head, K|V) and z = sequence (at most 65535 each)
   if (a.T < BULK_MIN_T || (long long)a.n_layers_call * a.Hkv * 2 > 65535 || a.batch > 65535) {
     if (a.k_format == KVQ_TQ3_QJL) {

@@ -185,13 +185,8 @@ __global__ void __launch_bounds__(WARPS * 32) append_block_kernel(const __grid_c
   const int layer = a.layer0 + ll;
 
   const int p0 = a.pos[b];
-  if (p0 < 0) return;  // sequence not part of this append
-  if ((long long)p0 + T > a.max_seq_len) {
-    if (threadIdx.x == 0 && bi == 0 && kv == 0 && h == 0) atomicOr(a.p.status, KVQ_DEV_POS_RANGE);
-    return;
-  }
+  const bool in = p0 >= 0 && (long long)p0 + T <= a.max_seq_len;
   const int end = p0 + T, first = p0 / HALF * HALF, base = first + bi * HALF;
-  if (base >= end) return;
   const bool whole = base + HALF <= end;
   const int tok = kv ? value_token(w, v) : key_token(w, v), pos = base + tok;
   const bool bf16 = a.in_bf16;
@@ -199,10 +194,15 @@ __global__ void __launch_bounds__(WARPS * 32) append_block_kernel(const __grid_c
   const size_t unit = ((size_t)ll * a.batch + b) * H + h;
   float* ring = (kv ? a.p.ringv : a.p.ringk) + (((size_t)layer * a.max_batch + b) * H + h) * W * D;
 
-  const bool mine = pos >= p0 && pos < end;
+  const bool mine = in && pos >= p0 && pos < end;
   float x[32];
   if (mine) load32(src, (unit * T + (pos - p0)) * D + 32 * G, bf16, x);
-  else if (whole) load32(ring, (size_t)(pos % W) * D + 32 * G, false, x);
+  // Before a prefill this is a dependent launch of the copy of the ring: what it writes waits for that.  (All threads do, so
+  // that this grid never ends before the other.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p0 >= 0 && !in && threadIdx.x == 0 && bi == 0 && kv == 0 && h == 0) atomicOr(a.p.status, KVQ_DEV_POS_RANGE);
+  if (!in || base >= end) return;  // (or the sequence is not part of the call)
+  if (!mine && whole) load32(ring, (size_t)(pos % W) * D + 32 * G, false, x);
   // The newest W tokens of the call go to the ring raw.  Those whose slots hold tokens that the first block still has to
   // read are left to the CTA of that block, after it has read them.
   const int held = p0 - first;
@@ -246,11 +246,19 @@ __global__ void __launch_bounds__(WARPS * 32) append_block_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t s) {
+cudaError_t launch_append_blocks(const AppendArgs& a, bool dependent, cudaStream_t s) {
   const long long ctas = (long long)((a.T - 1) / HALF + 2) * 2 * a.Hkv * a.batch * a.n_layers_call;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  append_block_kernel<<<(unsigned)ctas, WARPS * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, append_block_kernel, a);
 }
 
 }  // namespace kvq

@@ -97,7 +97,7 @@ cudaError_t launch_commit(const AppendArgs& a, const CommitArgs& c, cudaStream_t
 cudaError_t launch_append_bulk(const AppendArgs& a, cudaStream_t s, bool after_keys = false);
 
 // KVQ_Q8B32 keys and values
-cudaError_t launch_append_blocks(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_append_blocks(const AppendArgs& a, bool dependent, cudaStream_t s);  // dependent: programmatic, of the launch before
 
 struct CalibArgs {
   DevPtrs p;
@@ -142,7 +142,8 @@ struct PrefillArgs {
   float* snap_v;
   int layer0, n_layers_call, batch, max_batch, Hkv, g, W, T, k_format, sinkhorn, in_bf16;
   int max_pages_per_seq, max_seq_len;
-  float* parts;      // KVQ_Q8B32: partial results of row tiles that several CTAs share
+  float* parts;      // KVQ_Q8B32: partial results of row tiles that several CTAs share, two a CTA
+  int2* keys;        // behind them: (unit, row tile) of each; -1: there is none
   int sms;
 };
 size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W);

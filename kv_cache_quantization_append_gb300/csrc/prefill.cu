@@ -148,6 +148,7 @@ __device__ __forceinline__ uint32_t cm_off(int row, int k, int R) {
 
 // Copy the window ring of every (layer, sequence < batch, kv-head) of the call to scratch.
 __global__ void snapshot_kernel(const __grid_constant__ PrefillArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");  // (of 8-bit blocks: the append, which waits before it writes)
   const size_t per_layer = (size_t)a.batch * a.Hkv * a.W * D / 4;  // float4s of one layer's sequences
   const size_t n = per_layer * a.n_layers_call;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
@@ -804,9 +805,12 @@ cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStre
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  if (a.k_format == KVQ_Q8B32) {  // (append_block.cu, prefill_block.cu)
+    const cudaError_t e = launch_append_blocks(app, a.W > 0, s);
+    return e != cudaSuccess ? e : launch_prefill_blocks(a, a.sms, s);
+  }
   cudaError_t e = launch_append(app, s);
   if (e != cudaSuccess) return e;
-  if (a.k_format == KVQ_Q8B32) return launch_prefill_blocks(a, a.sms, s);  // (prefill_block.cu)
   return a.k_format == KVQ_TQ3_QJL ? launch_kf<KVQ_TQ3_QJL>(a, s)
          : a.k_format == KVQ_Q8G32 ? launch_kf<KVQ_Q8G32>(a, s)
                                    : launch_kf<KVQ_Q4G32>(a, s);

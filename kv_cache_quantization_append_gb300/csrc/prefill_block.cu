@@ -335,7 +335,10 @@ struct Kernel {
       st.p0 = work.p0[u.b];
       st.tl = tl;
       y = st.next = u.start + u.cost;
-      if (st.ta < st.tb) return;
+      if (st.ta < st.tb) {
+        if (st.rec >= 0) a.keys[st.rec] = make_int2(st.unit, u.x);
+        return;
+      }
       st.tb = -1;
     }
   }
@@ -985,6 +988,7 @@ struct Kernel {
       if (ROLE <= OPERANDS) queries(u);
       sync_all();
       if (ROLE == SOFTMAX) queries_to_tmem();
+      if (k == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the call's tokens are appended, older ones copied
       fence_before();
       sync_all();
       fence_after();
@@ -1038,6 +1042,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const Work work = plan(a, sh.p0, sh.pre, gridDim.x);
+  if (tid == NEXT_WARP * 32) a.keys[2 * blockIdx.x] = a.keys[2 * blockIdx.x + 1] = make_int2(-1, -1);
   // sequences that are not part of the call, or past capacity: zeros
   for (int b = 0; b < a.batch; ++b) {
     if (sh.p0[b] >= 0) continue;
@@ -1047,7 +1052,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
       for (size_t i = (size_t)blockIdx.x * THREADS + tid; i < per; i += (size_t)gridDim.x * THREADS) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (blockIdx.x >= work.n || work.total() == 0) return;
+  if (blockIdx.x >= work.n || work.total() == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (this grid ends after those before it)
+    return;
+  }
   if (warp == S_WARP) {
     tm_alloc(&sh.tmem, TMEM_COLS);
     fence_before();
@@ -1077,88 +1085,84 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
   }
 }
 
-// Joins the partial results of the row tiles that a cut divides.  Block (c, share): cut c + 1, if it is the first within its
-// row tile, for a share of the rows; parts in the order of their CTAs.  One thread finds the parts (a CTA's stretch of the
-// row tile is its first unless it began before), a warp joins a row.
+// Joins the partial results of the row tiles that a cut divides, a share of the rows a block.  Records stand in the order
+// of the cost line (two a CTA: of the row tile that it begins in, of the one that it ends in), those of one row tile have
+// its key.  Blocks (c, .) join the row tile whose first record is CTA c's: its last one, or no other is the first of its
+// kind.  A warp joins a row.
 constexpr int JOIN_SHARES = 8, JOIN_WARPS = ROWS / JOIN_SHARES, MAX_CTAS = 256;
-template <bool BF16>
+static_assert(2 * MAX_CTAS <= JOIN_WARPS * 32, "a thread for each record");
 __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int ctas) {
-  __shared__ int p0s[MAX_BATCH];
-  __shared__ long long pre[MAX_BATCH + 1];
-  __shared__ int part[MAX_CTAS + 1], n_parts;
-  __shared__ Unit unit;
+  __shared__ int part[2 * MAX_CTAS], before[JOIN_WARPS + 1];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, g = a.g, qpt = ROWS / g;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Work w = plan(a, p0s, pre, ctas);
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), g = a.g;
-  if (c >= w.n || w.total() == 0) return;
-  if (threadIdx.x == 0) {
-    n_parts = 0;
-    const Unit u = w.find(w.cut(c));
-    const Tiles tl(w, u, a.W, Kernel<BF16>::RNT);
-    const int at = tl.before(w.cut(c) - u.start);
-    const long long y1 = w.cut(c - 1), end = u.start + u.cost;
-    if (at > 0 && at < tl.n && !(y1 > u.start && tl.before(y1 - u.start) > 0)) {  // (no earlier cut within the row tile)
-      int from = 0, n = 0;
-      for (int k = c - 1; k < w.n && w.cut(k) < end; ++k) {
-        const int to = w.cut(k + 1) >= end ? tl.n : tl.before(w.cut(k + 1) - u.start);
-        if (to > from) part[n++] = 2 * k + (w.cut(k) >= u.start ? 0 : 1);
-        from = to;
-      }
-      n_parts = n;
-      unit = u;
-    }
-  }
+  const int2 k0 = __ldcg(a.keys + 2 * blockIdx.x), k1 = __ldcg(a.keys + 2 * blockIdx.x + 1), key = k1.x >= 0 ? k1 : k0;
+  const int2 k = t < 2 * ctas ? __ldcg(a.keys + t) : make_int2(-1, -1);
+  if (key.x < 0) return;
+  const bool mine = k.x == key.x && k.y == key.y;
+  const unsigned same = __ballot_sync(FULL, mine);
+  if (lane == 0) before[warp + 1] = __popc(same);
   __syncthreads();
-  const int n = n_parts;
-  if (n == 0) return;
-  const int t0 = unit.x * w.qpt;
-  if (row >= min(w.qpt, w.T - t0) * g) return;
+  int at = 0, n = 0;
+#pragma unroll
+  for (int i = 0; i < JOIN_WARPS; ++i) {
+    if (i < warp) at += before[i + 1];
+    n += before[i + 1];
+  }
+  if (mine) part[at + __popc(same & ((1u << lane) - 1))] = t;
+  __syncthreads();
+  if (part[0] < 2 * (int)blockIdx.x) return;
+  const int t0 = key.y * qpt, row = blockIdx.y * JOIN_WARPS + warp;
+  if (row >= min(qpt, a.T - t0) * g) return;
   float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(a.parts + (size_t)part[k] * REC + ROWS * D + row));
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.parts + (size_t)part[i] * REC + ROWS * D + row));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* rec = a.parts + (size_t)part[k] * REC;
-    const float m = __ldcg(rec + ROWS * D + row), lk = __ldcg(rec + ROWS * D + ROWS + row);
+  for (int i = 0; i < n; ++i) {
+    const float* rec = a.parts + (size_t)part[i] * REC;
+    const float m = __ldcg(rec + ROWS * D + row), li = __ldcg(rec + ROWS * D + ROWS + row);
     const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + row * D) + lane);
     const float f = m == -INFINITY ? 0.f : ex2(m - M);
-    l += lk * f;
+    l += li * f;
     o.x += x.x * f;
     o.y += x.y * f;
     o.z += x.z * f;
     o.w += x.w * f;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t head0 = (((size_t)(unit.hl / a.Hkv) * a.batch + unit.b) * a.Hkv + unit.hl % a.Hkv) * g;
-  *reinterpret_cast<float4*>(a.out + ((head0 + row % g) * a.T + t0 + row / g) * D + 4 * lane) =
+  *reinterpret_cast<float4*>(a.out + (((size_t)key.x * g + row % g) * a.T + t0 + row / g) * D + 4 * lane) =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
 template <bool BF16>
-cudaError_t launch(const PrefillArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch(PrefillArgs a, int sms, cudaStream_t s) {
   if (sms > MAX_CTAS) sms = MAX_CTAS;
+  a.keys = reinterpret_cast<int2*>(a.parts + (size_t)2 * sms * REC);
   cudaError_t e = allow_shared_memory<prefill_block_kernel<BF16>>();
   if (e != cudaSuccess) return e;
-  prefill_block_kernel<BF16><<<sms, THREADS, SMEM, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms, JOIN_SHARES);
-  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_join_kernel<BF16>, a, sms);
+  // (a dependent of the append: it has its queries by the time that the append ends)
+  if ((e = cudaLaunchKernelEx(&cfg, prefill_block_kernel<BF16>, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)sms, JOIN_SHARES);
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prefill_join_kernel, a, sms);
 }
 
 }  // namespace
 
-size_t prefill_block_scratch_bytes(int sms) { return (size_t)2 * sms * REC * sizeof(float); }
+size_t prefill_block_scratch_bytes(int sms) { return (size_t)2 * sms * (REC * sizeof(float) + sizeof(int2)); }
 
 cudaError_t launch_prefill_blocks(const PrefillArgs& a, int sms, cudaStream_t s) {
   return a.in_bf16 ? launch<true>(a, sms, s) : launch<false>(a, sms, s);
