@@ -43,7 +43,7 @@ constexpr int N_SOFT = 8;            // softmax warps, two groups
 constexpr int N_SUM = 4;             // warps that hold the output
 constexpr int DQ0 = 12, N_DQ = 4;    // operand warps
 constexpr int S_WARP = 16, PV_WARP = 17, PAGE_WARP = 18, NEXT_WARP = 19;
-constexpr int THREADS = 640, ROW_WARPS = 16;  // ROW_WARPS: those that prepare queries and write rows out
+constexpr int THREADS = 640;
 constexpr int LAUNCH_REGS = 96;
 // registers: 256 x 96 + 128 x (168 + 80 + 40) = 640 x 96, what the block is launched with
 constexpr int SOFT_REGS = 96, SUM_REGS = 168, DQ_REGS = 80, ISSUE_REGS = 40;
@@ -63,8 +63,8 @@ constexpr uint32_t O_STRIDE = (D + 4) * 4;
 static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "what borrows the stages");
 constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
 constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
-constexpr long long K0 = 192;        // a row tile's fixed cost, in positions
-constexpr long long MIN_SHARE = 512; // positions that a CTA takes at least
+constexpr long long K0 = 1024;        // a row tile's fixed cost, in positions
+constexpr long long MIN_SHARE = 128; // positions that a CTA takes at least
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 constexpr int REC = ROWS * D + 2 * ROWS;  // floats of a partial result: O, m, l
 
@@ -166,10 +166,10 @@ __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas) {
 struct Tiles {
   int t0, nq, Pmin, Pmax, qend, nqt, rlo, n;
   Tiles() = default;
-  __device__ Tiles(const Work& w, const Unit& u, int W, int raw_nt) {
-    t0 = u.x * w.qpt;
-    nq = min(w.qpt, w.T - t0);
-    Pmin = w.p0[u.b] + t0;
+  __device__ Tiles(const int* p0, int T, int qpt, const Unit& u, int W, int raw_nt) {
+    t0 = u.x * qpt;
+    nq = min(qpt, T - t0);
+    Pmin = p0[u.b] + t0;
     Pmax = Pmin + nq - 1;
     qend = max(0, Pmax - W + 1);
     nqt = (qend + NT - 1) / NT;
@@ -184,7 +184,7 @@ struct Tiles {
 
 // A CTA's stretch of one row tile: tiles ta .. tb - 1 of it, whole or to be joined with others
 struct Stretch {
-  int b, hl, unit, layer, h;  // unit: (layer of the call, sequence, kv-head)
+  int b, x, hl, unit, layer, h;  // unit: (layer of the call, sequence, kv-head)
   int p0, ta, tb, rec;        // rec: -1: the row tile as a whole
   Tiles tl;
   long long next;             // where on the cost line the CTA goes on
@@ -274,6 +274,7 @@ __device__ __forceinline__ void take_registers() {
 
 template <bool BF16>
 struct Kernel {
+  static constexpr int ROW_BYTES = D * (BF16 ? 2 : 4);  // of a raw vector of the call
   static constexpr int RNT = BF16 ? 64 : 32;  // raw positions of a tile: one plane of a bf16 cache's, hi and lo of a float one's
   static constexpr uint32_t ID_S = idesc(ROWS, NT, false, false), ID_SR = idesc(ROWS, RNT, false, false);
   static constexpr uint32_t ID_O = idesc(ROWS, D, false, false), ID_OR = idesc(ROWS, D, false, true);
@@ -286,7 +287,7 @@ struct Kernel {
     float qscale[ROWS], qraw[ROWS];        // powers of two that the queries were divided by
     float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' references and sums, the output's reference, at the end
     float mt[4][ROWS], vt[4], vt0[4];              // a tile's references: of its weights, of its values' scales
-    int ctas;                              // that have work
+    long long hi;                          // where the CTA's stretch of the cost line ends
     int halves[RS];                        // of a page under way that are read (0: there is no such page)
     float2 scale[8][2];                    // (keys', values') of a tile's two blocks; of a raw tile: its powers of two
     float warp_most[2][N_DQ];              // largest magnitude of a raw tile's keys, values, in each operand warp
@@ -317,93 +318,133 @@ struct Kernel {
   __device__ __forceinline__ bool held(uint64_t* bar, uint32_t parity) { return wait(bar, parity, &sh.gone, a.p.status); }
   __device__ __forceinline__ void sync_all() { part_sync(1, THREADS); }
 
-  // the first stretch with tiles from y on
-  __device__ void locate(const Work& work, long long y, Stretch& st) const {
-    const long long lo = work.cut(blockIdx.x), hi = work.cut(blockIdx.x + 1);
+  // the CTA's first stretch with tiles
+  __device__ void locate(const Work& work, Stretch& st) {
+    const long long y = work.cut(blockIdx.x), hi = work.cut(blockIdx.x + 1);
+    sh.hi = hi;
+    const Unit u = work.find(y);
+    const Tiles tl(sh.p0, a.T, work.qpt, u, a.W, RNT);
+    if (!take(u, tl, tl.before(y - u.start), hi, 0, st)) follow_up(st, st);
+  }
+  // a value whose derivatives are computed where they are used, and not kept through the tiles of a stretch
+  __device__ __forceinline__ static int once(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+  }
+  // the one after it: the next row tiles of the line
+  __device__ void follow_up(const Stretch& u, Stretch& st) const {
+    const int qpt = ROWS / a.g, nx = (a.T + qpt - 1) / qpt, HL = a.Hkv * a.n_layers_call;
+    const long long hi = sh.hi;
+    long long y = u.next;
+    int b = u.b, x = u.x, hl = u.hl;
     st.tb = -1;
     while (y < hi) {
-      const Unit u = work.find(y);
-      const Tiles tl(work, u, a.W, RNT);
-      st.ta = tl.before(y - u.start);
-      st.tb = hi >= u.start + u.cost ? tl.n : tl.before(hi - u.start);
-      st.rec = st.ta == 0 && st.tb == tl.n ? -1 : 2 * (int)blockIdx.x + (y == lo ? 0 : 1);
-      st.b = u.b;
-      st.hl = u.hl;
-      st.h = u.hl % a.Hkv;
-      st.layer = a.layer0 + u.hl / a.Hkv;
-      st.unit = ((u.hl / a.Hkv) * a.batch + u.b) * a.Hkv + st.h;
-      st.p0 = work.p0[u.b];
-      st.tl = tl;
-      y = st.next = u.start + u.cost;
-      if (st.ta < st.tb) {
-        if (st.rec >= 0) a.keys[st.rec] = make_int2(st.unit, u.x);
-        return;
+      if (++hl == HL) {
+        hl = 0;
+        if (++x == nx) {
+          x = 0;
+          do ++b;
+          while (sh.p0[b] < 0);  // (there is one: the line goes on)
+        }
       }
-      st.tb = -1;
+      Unit n;
+      n.b = b;
+      n.x = x;
+      n.hl = hl;
+      n.start = y;
+      n.cost = sh.p0[b] + (long long)(x + 1) * qpt + K0;
+      if (take(n, Tiles(sh.p0, a.T, qpt, n, a.W, RNT), 0, hi, 1, st)) return;
+      y = st.next;
     }
+  }
+  // A row tile's tiles from ta on, as far as this CTA goes; false: there are none
+  __device__ __forceinline__ bool take(const Unit& u, const Tiles& tl, int ta, long long hi, int slot, Stretch& st) const {
+    st.ta = ta;
+    st.tb = hi >= u.start + u.cost ? tl.n : tl.before(hi - u.start);
+    st.rec = st.ta == 0 && st.tb == tl.n ? -1 : 2 * (int)blockIdx.x + slot;
+    st.b = u.b;
+    st.x = u.x;
+    st.hl = u.hl;
+    const int l = u.hl / a.Hkv;
+    st.h = u.hl - l * a.Hkv;
+    st.layer = a.layer0 + l;
+    st.unit = (l * a.batch + u.b) * a.Hkv + st.h;
+    st.p0 = sh.p0[u.b];
+    st.tl = tl;
+    st.next = u.start + u.cost;
+    if (st.ta < st.tb) {
+      if (st.rec >= 0) a.keys[st.rec] = make_int2(st.unit, u.x);
+      return true;
+    }
+    st.tb = -1;
+    return false;
   }
 
   // ---------------------------------------------------------------- queries
-  // Rows 8 warp .. + 7, four lanes a row with 32 channels each: unrotated hi and lo to their operand, rotated ones to the
+  // Four lanes a row with 32 channels each, eight rows a warp and round: unrotated hi and lo to their operand, rotated ones to the
   // staging rows, each over its own power of two
   __device__ void queries(const Stretch& u) {
     const Tiles& tl = u.tl;
-    const int g = a.g, v = lane >> 2, G = lane & 3, row = 8 * warp + v;
-    float x[32];
-    if (row < tl.nq * g) {
-      const size_t off = (((size_t)u.unit * g + row % g) * a.T + tl.t0 + row / g) * D + 32 * G;
-      if (BF16) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off);
-        uint4 w[4];
+    const int g = a.g, lane = once(this->lane), v = lane >> 2, G = lane & 3;
+#pragma unroll 1
+    for (int round = 0; round < ROWS / (8 * N_SOFT); ++round) {
+      const int row = 8 * (warp + N_SOFT * round) + v;
+      float x[32];
+      if (row < tl.nq * g) {
+        const size_t off = (((size_t)u.unit * g + row % g) * a.T + tl.t0 + row / g) * D + 32 * G;
+        if (BF16) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off);
+          uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = __ldg(src + c);
+          for (int c = 0; c < 4; ++c) w[c] = __ldg(src + c);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) unpack8(w[c], x + 8 * c);
+          for (int c = 0; c < 4; ++c) unpack8(w[c], x + 8 * c);
+        } else {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + off);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<float4*>(x + 4 * c) = __ldg(src + c);
+        }
       } else {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + off);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<float4*>(x + 4 * c) = __ldg(src + c);
+        for (int i = 0; i < 32; ++i) x[i] = 0.f;
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = 0.f;
-    }
+      for (int i = 0; i < 32; i += 2) mul2(x[i], x[i + 1], LOGIT_SCALE, LOGIT_SCALE);
+      float inv;
+      float s2 = pow2_of(quad_max(x), inv);
+      if (G == 0) sh.qraw[row] = s2;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) mul2(x[i], x[i + 1], LOGIT_SCALE, LOGIT_SCALE);
-    float inv;
-    float s2 = pow2_of(quad_max(x), inv);
-    if (G == 0) sh.qraw[row] = s2;
+      for (int c = 0; c < 4; ++c) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) split2(x[8 * c + 2 * e] * inv, x[8 * c + 2 * e + 1] * inv, hi[e], lo[e]);
-      uint8_t* at = smem + QR_OFF + km(row, 32 * G + 8 * c, QR_LEAD);
-      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(at + QR_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    rotate32(x, G, a.p.signs, nullptr);
-    if (a.sinkhorn) {
-      const __half2* sig = reinterpret_cast<const __half2*>(a.p.sigk + ((size_t)u.layer * a.Hkv + u.h) * D + 32 * G);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 f = __half22float2(sig[i / 2]);
-        mul2(x[i], x[i + 1], f.x, f.y);
+        for (int e = 0; e < 4; ++e) split2(x[8 * c + 2 * e] * inv, x[8 * c + 2 * e + 1] * inv, hi[e], lo[e]);
+        uint8_t* at = smem + QR_OFF + km(row, 32 * G + 8 * c, QR_LEAD);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + QR_PLANE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-    }
-    s2 = pow2_of(quad_max(x), inv);
-    if (G == 0) sh.qscale[row] = s2;
-    uint8_t* st = smem + (size_t)row * Q_STRIDE + 64 * G;
+      rotate32(x, G, a.p.signs, nullptr);
+      if (a.sinkhorn) {
+        const __half2* sig = reinterpret_cast<const __half2*>(a.p.sigk + ((size_t)u.layer * a.Hkv + u.h) * D + 32 * G);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = at_place(8 * i + 2 * e);
-        split2(x[c] * inv, x[c + 1] * inv, hi[e], lo[e]);
+        for (int i = 0; i < 32; i += 2) {
+          const float2 f = __half22float2(sig[i / 2]);
+          mul2(x[i], x[i + 1], f.x, f.y);
+        }
       }
-      *reinterpret_cast<uint4*>(st + 16 * i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(st + 2 * D + 16 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      s2 = pow2_of(quad_max(x), inv);
+      if (G == 0) sh.qscale[row] = s2;
+      uint8_t* st = smem + (size_t)row * Q_STRIDE + 64 * G;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = at_place(8 * i + 2 * e);
+          split2(x[c] * inv, x[c + 1] * inv, hi[e], lo[e]);
+        }
+        *reinterpret_cast<uint4*>(st + 16 * i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(st + 2 * D + 16 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
     fence_async_smem();
   }
@@ -521,6 +562,26 @@ struct Kernel {
         __syncwarp();
       }
     }
+    // Raw tiles of the call's own tokens come the same way, keys then values, a slot each.  (Loads of their own, which only a
+    // tile's other half overlapped, took 3000 cycles each of a raw tile's 10000.)
+    static_assert(RNT * ROW_BYTES <= PAGE_SLOT, "a raw operand fits a slot");
+#pragma unroll 1
+    for (int it = max(u.ta, u.tl.nqt); it < u.tb; ++it) {
+      const int j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+      if (j0 < u.p0) continue;
+      const uint32_t bytes = min(RNT, u.tl.Pmax - j0 + 1) * ROW_BYTES;
+      const size_t off = ((size_t)u.unit * a.T + (j0 - u.p0)) * ROW_BYTES;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++gr) {
+        const int s = gr % RS;
+        if (gr >= RS && !held(&sh.rempty[s], ((gr / RS) & 1) ^ 1)) return;
+        if (lane == 0) {
+          bar_expect(&sh.rfull[s], bytes);
+          bulk_g2s(smem + PAGE_OFF + s * PAGE_SLOT, static_cast<const uint8_t*>(kv ? a.v : a.k) + off, bytes, &sh.rfull[s]);
+        }
+        __syncwarp();
+      }
+    }
   }
   // Lane (r, i) = (lane >> 2, lane & 3) takes the 16 bytes of (r, i) of a chunk, in order.  (A half that is not there, or not
   // read, may hold anything: its codes are finite and its weights zero.)
@@ -571,42 +632,43 @@ struct Kernel {
     for (; it < u.tb; ++it, ++gt) {
       const int s = gt % NS, j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
       const uint32_t before = ((gt / NS) & 1) ^ 1;
-      uint8_t* kp = smem + s * STAGE;
-      if (gt >= NS && !held(&sh.kempty[s], before)) return;
-      if (!raw<false>(u, j0, kp)) return;
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.kfull[s]);
-      if (gt >= NS && !held(&sh.vempty[s], before)) return;
-      if (!raw<true>(u, j0, kp + V_OFF)) return;
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.vfull[s]);
+#pragma unroll 1
+      for (int values = 0; values < 2; ++values) {
+        if (gt >= NS && !held(values ? &sh.vempty[s] : &sh.kempty[s], before)) return;
+        if (!raw(u, j0, smem + s * STAGE + (values ? V_OFF : 0), values)) return;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(values ? &sh.vfull[s] : &sh.kfull[s]);
+      }
     }
   }
   // Raw keys (K-major) or values (N-major: rows are positions too, in the order of the places) of positions j0 .. j0 + RNT - 1
   // as operand planes, over a power of two of the tile.  An element of a bf16 vector that its one fp16 plane does not hold
   // exactly is below 2^-14 of the tile's largest and off by 2^-25 of that at most.
-  template <bool VALUES>
-  __device__ bool raw(const Stretch& u, int j0, uint8_t* plane) {
-    const int dw = warp - DQ0, r = lane & 7, i = lane >> 3;
+  __device__ __forceinline__ bool raw(const Stretch& u, int j0, uint8_t* plane, int values) {
+    // the lane's q-th eight channels are group 4 ((q + r / 4) mod 4) + (i + r) mod 4: eight lanes' reads of a slot hit all banks
+    const int lane = once(this->lane), dw = once(warp) - DQ0, r = lane & 7, b = ((lane >> 3) + r) & 3, q0 = r >> 2;
     const int p0 = u.p0;
     const size_t unit = u.unit;
-    const void* chunk = VALUES ? a.v : a.k;
-    const float* old = VALUES ? a.snap_v : a.snap_k;
+    const bool staged = j0 >= p0;
+    const int slot = gr % RS;
+    if (staged && !held(&sh.rfull[slot], (gr / RS) & 1)) return false;
+    const float* old = values ? a.snap_v : a.snap_k;
+    const uint8_t* mine = staged ? smem + PAGE_OFF + slot * PAGE_SLOT
+                                 : static_cast<const uint8_t*>(values ? a.v : a.k) + ((size_t)unit * a.T * ROW_BYTES + (long long)(j0 - p0) * ROW_BYTES);
     constexpr int ROUNDS = RNT / (8 * N_DQ);
     uint4 w[ROUNDS][BF16 ? 4 : 8];  // bf16 values, or floats; every load of the tile under way at once
 #pragma unroll
     for (int n = 0; n < ROUNDS; ++n) {
-      const int j = j0 + 8 * dw + r + 8 * N_DQ * n;
+      const int t = 8 * dw + r + 8 * N_DQ * n, j = j0 + t;
 #pragma unroll
       for (int q = 0; q < (BF16 ? 4 : 8); ++q) w[n][q] = make_uint4(0u, 0u, 0u, 0u);
       if (j > u.tl.Pmax) continue;
       if (j < p0) {
-        const float4* f = reinterpret_cast<const float4*>(old + (unit * a.W + j % a.W) * D) + 2 * i;
+        const float4* f = reinterpret_cast<const float4*>(old + (unit * a.W + j % a.W) * D) + 2 * b;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 x = __ldg(f + 8 * q), y = __ldg(f + 8 * q + 1);
+          const float4 x = __ldg(f + 8 * ((q + q0) & 3)), y = __ldg(f + 8 * ((q + q0) & 3) + 1);
           if (BF16) w[n][q] = pack8(x, y);
           else {
             w[n][2 * q] = *reinterpret_cast<const uint4*>(&x);
@@ -614,18 +676,18 @@ struct Kernel {
           }
         }
       } else {
-        const uint4* f = static_cast<const uint4*>(chunk) + (unit * a.T + (j - p0)) * (BF16 ? 16 : 32) + (BF16 ? 1 : 2) * i;
+        const uint4* f = reinterpret_cast<const uint4*>(mine + t * ROW_BYTES) + (BF16 ? 1 : 2) * b;  // (of either memory)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (BF16) w[n][q] = __ldg(f + 4 * q);
+          if (BF16) w[n][q] = f[4 * ((q + q0) & 3)];
           else {
-            w[n][2 * q] = __ldg(f + 8 * q);
-            w[n][2 * q + 1] = __ldg(f + 8 * q + 1);
+            w[n][2 * q] = f[8 * ((q + q0) & 3)];
+            w[n][2 * q + 1] = f[8 * ((q + q0) & 3) + 1];
           }
         }
       }
     }
-    auto eight = [&](int n, int q, float (&x)[8]) {  // channels 8 (4 q + i) ..
+    auto eight = [&](int n, int q, float (&x)[8]) {  // the q-th channels
       if (BF16) unpack8(w[n][q], x);
       else {
         *reinterpret_cast<uint4*>(x) = w[n][(2 * q) % (BF16 ? 4 : 8)];
@@ -645,18 +707,21 @@ struct Kernel {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
     if (lane == 0) {
-      sh.warp_most[VALUES][dw] = m;
+      sh.warp_most[values][dw] = m;
       bar_arrive(&sh.most);
+      if (staged) bar_arrive(&sh.rempty[slot]);
     }
+    gr += staged;
     if (!held(&sh.most, gm++ & 1)) return false;
 #pragma unroll
-    for (int o = 0; o < N_DQ; ++o) m = fmaxf(m, sh.warp_most[VALUES][o]);
+    for (int o = 0; o < N_DQ; ++o) m = fmaxf(m, sh.warp_most[values][o]);
     float inv;
     const float s2 = pow2_of(m, inv);
-    if (dw == 0 && lane < 2) reinterpret_cast<float*>(&sh.scale[gt & 7][lane])[VALUES] = s2;
+    if (dw == 0 && lane < 2) reinterpret_cast<float*>(&sh.scale[gt & 7][lane])[values] = s2;
 #pragma unroll
     for (int n = 0; n < ROUNDS; ++n) {
       const int t = 8 * dw + r + 8 * N_DQ * n, k = place_of(t);
+      uint8_t* to = plane + (values ? (k >> 3) * V_LEAD + (k & 7) * 16 : (uint32_t)((t >> 3) * 128 + (t & 7) * 16));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
@@ -664,10 +729,10 @@ struct Kernel {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(x[2 * e] * inv, x[2 * e + 1] * inv, hi[e], lo[e]);
-        const int kg = 4 * q + i;
-        const uint32_t o = VALUES ? (uint32_t)((k >> 3) * V_LEAD + kg * 128 + (k & 7) * 16) : km(t, 8 * kg, RNT * 16);
-        *reinterpret_cast<uint4*>(plane + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (!BF16) *reinterpret_cast<uint4*>(plane + (VALUES ? LO_V : LO_K) + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int kg = 4 * ((q + q0) & 3) + b;
+        uint8_t* o = to + kg * (values ? 128 : RNT * 16);
+        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (!BF16) *reinterpret_cast<uint4*>(o + (values ? LO_V : LO_K)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     return true;
@@ -934,27 +999,34 @@ struct Kernel {
     for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(acc[i] * V, acc[i + 1] * V, acc[i + 2] * V, acc[i + 3] * V);
     sh.M[row] = M;
   }
-  // rows to the output, or to a partial result
+  // rows to the output, or to a partial result: lane i & 15 knows of the warp's i-th row, then all write each row
   __device__ void rows_out(const Stretch& u) {
-    const Tiles& tl = u.tl;
-    float* rec = u.rec < 0 ? nullptr : a.parts + (size_t)u.rec * REC;
-    const int g = a.g, nrows = tl.nq * g;
-    const size_t head0 = (size_t)u.unit * g;
-#pragma unroll 1
-    for (int row = warp; row < nrows; row += ROW_WARPS) {
+    static_assert(ROWS == 16 * N_SOFT, "");
+    const int g = a.g, nrows = u.tl.nq * g, lane = once(this->lane), warp = once(this->warp), row = warp + N_SOFT * (lane & 15);
+    float* dst = a.parts + (size_t)max(u.rec, 0) * REC;
+    float f = 0.f;
+    if (row < nrows) {
       const float M = sh.M[row], m0 = sh.m[0][row], m1 = sh.m[1][row];
       const float l = sh.l[0][row] * (m0 == -INFINITY ? 1.f : ex2(m0 - M)) + sh.l[1][row] * (m1 == -INFINITY ? 1.f : ex2(m1 - M));
-      float4 o = *reinterpret_cast<const float4*>(smem + (size_t)row * O_STRIDE + 16 * lane);
-      if (rec) {
-        *reinterpret_cast<float4*>(rec + row * D + 4 * lane) = o;
-        if (lane == 0) {
-          rec[ROWS * D + row] = M;
-          rec[ROWS * D + ROWS + row] = l;
+      if (u.rec >= 0) {
+        if (lane < 16) {
+          dst[ROWS * D + row] = M;
+          dst[ROWS * D + ROWS + row] = l;
         }
+        f = 1.f;
+        dst += row * D;
       } else {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        *reinterpret_cast<float4*>(a.out + ((head0 + row % g) * a.T + tl.t0 + row / g) * D + 4 * lane) = o;
+        f = l > 0.f ? 1.f / l : 0.f;
+        dst = a.out + (((size_t)u.unit * g + row % g) * a.T + u.tl.t0 + row / g) * D;
+      }
+    }
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const float fi = __shfl_sync(FULL, f, i);
+      float* to = reinterpret_cast<float*>(__shfl_sync(FULL, reinterpret_cast<unsigned long long>(dst), i));
+      if (warp + N_SOFT * i < nrows) {
+        const float4 o = *reinterpret_cast<const float4*>(smem + (size_t)(warp + N_SOFT * i) * O_STRIDE + 16 * lane);
+        *reinterpret_cast<float4*>(to + 4 * lane) = make_float4(o.x * fi, o.y * fi, o.z * fi, o.w * fi);
       }
     }
   }
@@ -985,7 +1057,7 @@ struct Kernel {
     for (int k = 0;; ++k) {
       const Stretch& u = sh.at[k & 1];
       if (u.tb < 0) return;
-      if (ROLE <= OPERANDS) queries(u);
+      if (ROLE == SOFTMAX) queries(u);
       sync_all();
       if (ROLE == SOFTMAX) queries_to_tmem();
       if (k == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the call's tokens are appended, older ones copied
@@ -998,14 +1070,10 @@ struct Kernel {
       if (ROLE == LOGITS) issue_logits(u);
       if (ROLE == VALUES) issue_values(u);
       if (ROLE == PAGES) fetch(u);
-      if (ROLE == AHEAD && lane == 0) {
-        Work w(a, sh.p0, sh.pre, 1);
-        w.divide(sh.ctas);
-        locate(w, u.next, sh.at[(k + 1) & 1]);
-      }
+      if (ROLE == AHEAD && lane == 0) follow_up(u, sh.at[(k + 1) & 1]);
       sync_all();
       if (sh.gone) return;
-      if (ROLE <= OPERANDS) rows_out(u);
+      if (ROLE == SOFTMAX) rows_out(u);
       sync_all();
     }
   }
@@ -1063,8 +1131,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
   __syncthreads();
   fence_after();
   if (tid == NEXT_WARP * 32) {
-    sh.ctas = work.n;
-    K(a, sh, smem).locate(work, work.cut(blockIdx.x), sh.at[0]);
+    K(a, sh, smem).locate(work, sh.at[0]);
   }
   __syncthreads();
   if (warp < N_SOFT) {
