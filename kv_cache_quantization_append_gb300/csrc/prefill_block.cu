@@ -28,8 +28,8 @@
 //  * Every wait is bounded; one that runs out flags the status word and the CTA leaves as a whole.
 //
 // One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 421 us (two passes of the products over recorded
-// positions at the measured bf16 rate: 204 us, 48 %), a prompt of 2048 tokens of 32 heads 206 us, three float turns of 37
-// tokens of 8 heads at 1000 positions 37 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
+// positions at the measured bf16 rate: 204 us, 48 %), a prompt of 2048 tokens of 32 heads 208 us, three float turns of 37
+// tokens of 8 heads at 1000 positions 33 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
 // 1100: bound by the weights (1500 cycles a tile and group of warps, two groups) and the rate at which instructions come.
 #include <cfloat>
 #include <cstddef>
@@ -70,10 +70,11 @@ constexpr uint32_t O_STRIDE = (D + 4) * 4;
 static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "what borrows the stages");
 constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
 constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
-// A row tile's fixed cost (queries, raw tiles, output) in positions, and the positions that a CTA takes at least.  A prompt of
-// 2048 tokens and 32 heads: 518 us at a cost of 32, 345 at 128, 240 at 448, 212 at 1024, 209 at 1280; at 15001 positions and three
-// short turns it hardly matters.  Three turns of 37 tokens at 1000: 55 us with shares of 512, 49 of 256, 38 of 128.
-constexpr long long K0 = 1024, MIN_SHARE = 128;
+// A row tile's fixed cost in positions, KF of it before its first tile (queries, the start of the products), the rest for raw
+// tiles and the output; and the positions that a CTA takes at least.  A prompt of 2048 tokens and 32 heads: 518 us at a cost of
+// 32, 345 at 128, 240 at 448, 208 at 1024, 213 at 1536; at 15001 positions it hardly matters.  Three turns of 37 tokens at 1000
+// positions: 55 us with shares of 512, 49 of 256, 38 of 128, 33 with raw tiles' cost at their end.
+constexpr long long K0 = 1024, KF = 512, MIN_SHARE = 128;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 constexpr int REC = ROWS * D + 2 * ROWS;  // floats of a partial result: O, m, l
 
@@ -185,9 +186,13 @@ struct Tiles {
     rlo = max(0, Pmin - W + 1);
     n = nqt + (Pmax - rlo) / raw_nt + 1;
   }
-  // tiles before offset `off` of the row tile's stretch of the cost line
-  __device__ __forceinline__ int before(long long off) const {
-    return off <= K0 ? 0 : (int)min((long long)n, (off - K0 + NT - 1) / NT);
+  // tiles before offset `off` of the row tile's stretch of the cost line, `cost` long: what is fixed, recorded tiles of
+  // their positions, raw ones of equal shares of the rest
+  __device__ __forceinline__ int before(long long off, long long cost) const {
+    const int o = (int)(off - KF), rest = o - nqt * NT;
+    if (o <= 0) return 0;
+    if (rest <= 0) return min(n, (o + NT - 1) / NT);
+    return min(n, nqt + rest * (n - nqt) / max(1, (int)(cost - KF) - nqt * NT));
   }
 };
 
@@ -333,7 +338,7 @@ struct Kernel {
     sh.hi = hi;
     const Unit u = work.find(y);
     const Tiles tl(sh.p0, a.T, work.qpt, u, a.W, RNT);
-    if (!take(u, tl, tl.before(y - u.start), hi, 0, st)) follow_up(st, st);
+    if (!take(u, tl, tl.before(y - u.start, u.cost), hi, 0, st)) follow_up(st, st);
   }
   // a value whose derivatives are computed where they are used, and not kept through the tiles of a stretch
   __device__ __forceinline__ static int once(int x) {
@@ -369,7 +374,7 @@ struct Kernel {
   // A row tile's tiles from ta on, as far as this CTA goes; false: there are none
   __device__ __forceinline__ bool take(const Unit& u, const Tiles& tl, int ta, long long hi, int slot, Stretch& st) const {
     st.ta = ta;
-    st.tb = hi >= u.start + u.cost ? tl.n : tl.before(hi - u.start);
+    st.tb = hi >= u.start + u.cost ? tl.n : tl.before(hi - u.start, u.cost);
     st.rec = st.ta == 0 && st.tb == tl.n ? -1 : 2 * (int)blockIdx.x + slot;
     st.b = u.b;
     st.x = u.x;
