@@ -293,9 +293,11 @@ int kv_decode_attention_noalloc(kvq_cache* cache, int32_t layer, const void* q, 
  *   pos        device int32 [batch]
  *   scratch    device, >= kv_prefill_scratch_bytes(cache, layer, batch) bytes, any contents: holds a
  *              copy of the window ring taken before the chunk's append (its raw values are read by
- *              the chunk's first queries after the append has overwritten their ring slots)
+ *              the chunk's first queries after the append has overwritten their ring slots), and for
+ *              KVQ_Q8B32 partial results behind it (about 20 MB)
  * Three launches on ``stream``: the ring copy, the append, the attention (tensor-core logits and
- * P.V over tiles of 32 positions, 64 (query, head) rows per block).
+ * P.V over tiles of 32 positions, 64 (query, head) rows per block).  KVQ_Q8B32: four; tiles of 64 positions, 128 rows,
+ * divided evenly over the device, and a launch that joins the rows that were divided.
  */
 size_t kv_prefill_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch);
 int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,

@@ -12,6 +12,9 @@
 // butterfly's stages 1 .. 16 stay in a lane, 32 and 64 are one shuffle a value); each warp's eight tokens are those that
 // share 16-byte chunks of the stored order, so codes reach their places by few shuffles and whole 16-byte stores.  Every
 // floating-point step is one IEEE operation in the order that the codec defines.
+//
+// Bound by latency: input or ring, rotation, the block's largest, codes.  2048 tokens of 8 heads (21 MB in and out, 3 us at the
+// copy rate) take 12.6 us, 3 x 37 tokens of 2 heads 6.5; before a prefill its start overlaps the ring's copy.
 #include "kvq_internal.cuh"
 
 namespace kvq {
