@@ -455,52 +455,55 @@ def kv_pool_bytes(cache: kvq_cache) -> int:
     return int(load().kv_pool_bytes(ctypes.byref(cache)))
 
 
-def _pool(cache: kvq_cache, pool: torch.Tensor, *ints: torch.Tensor):
-    """The pool's address and size, after checks of the call's int32 [batch] tensors."""
+def _pool(cache: kvq_cache, pool: torch.Tensor, *ints: torch.Tensor) -> list:
+    """The cache, the pool's address and size and the addresses of the call's int32 [batch] tensors, after checks of all."""
+    dev = cache.device
+    args = [ctypes.byref(cache), _ptr(pool, dev), pool.numel() * pool.element_size()]
+    shape = (ints[0].numel(),) if ints else ()
     for t in ints:
-        if t.dtype != torch.int32:
-            raise KVQError("the pool's arguments are int32 tensors")
-        _check_shape("argument", t, (ints[0].numel(),))
-    return _ptr(pool, cache.device), pool.numel() * pool.element_size()
+        # (one test where all is well: these calls are a few microseconds long)
+        if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            if t.dtype is not torch.int32:
+                raise KVQError("the pool's arguments are int32 tensors")
+            _check_shape("argument", t, shape)
+            _ptr(t, dev)
+        args.append(t.data_ptr())
+    return args
 
 
 def kv_pool_init(cache: kvq_cache, pool: torch.Tensor, stream=None):
     """pool: device bytes, at least kv_pool_bytes; the cache's block table (all of it) becomes -1."""
-    at, size = _pool(cache, pool)
-    _check(load().kv_pool_init(ctypes.byref(cache), at, size, _stream(stream)))
+    _check(load().kv_pool_init(*_pool(cache, pool), _stream(stream)))
 
 
 def kv_pool_reserve(cache: kvq_cache, pool: torch.Tensor, pos: torch.Tensor, n_tokens, granted: torch.Tensor, stream=None):
     """pos, granted (written; may be pos): int32 [B]; n_tokens: one number, or int32 [B] on the device."""
-    counts = n_tokens if isinstance(n_tokens, torch.Tensor) else None
-    at, size = _pool(cache, pool, pos, granted, *(() if counts is None else (counts,)))
-    dev = cache.device
-    _check(load().kv_pool_reserve(ctypes.byref(cache), at, size, _ptr(pos, dev), _ptr(counts, dev), _ptr(granted, dev),
-                                  pos.numel(), 0 if counts is not None else n_tokens, _stream(stream)))
+    if isinstance(n_tokens, torch.Tensor):
+        c, at, size, p, out, counts = _pool(cache, pool, pos, granted, n_tokens)
+        n_tokens = 0
+    else:
+        c, at, size, p, out = _pool(cache, pool, pos, granted)
+        counts = 0
+    _check(load().kv_pool_reserve(c, at, size, p, counts, out, pos.numel(), n_tokens, _stream(stream)))
 
 
 def kv_pool_fork(cache: kvq_cache, pool: torch.Tensor, parents: torch.Tensor, seq_lens: torch.Tensor,
                  new_lens: torch.Tensor, stream=None):
     """parents, seq_lens, new_lens (written): int32 [B]."""
-    at, size = _pool(cache, pool, parents, seq_lens, new_lens)
-    dev = cache.device
-    _check(load().kv_pool_fork(ctypes.byref(cache), at, size, _ptr(parents, dev), _ptr(seq_lens, dev),
-                               _ptr(new_lens, dev), parents.numel(), _stream(stream)))
+    _check(load().kv_pool_fork(*_pool(cache, pool, parents, seq_lens, new_lens), parents.numel(), _stream(stream)))
 
 
 def kv_pool_release(cache: kvq_cache, pool: torch.Tensor, keep_lens: torch.Tensor, stream=None):
     """keep_lens: int32 [B]."""
-    at, size = _pool(cache, pool, keep_lens)
-    _check(load().kv_pool_release(ctypes.byref(cache), at, size, _ptr(keep_lens, cache.device), keep_lens.numel(),
-                                  _stream(stream)))
+    _check(load().kv_pool_release(*_pool(cache, pool, keep_lens), keep_lens.numel(), _stream(stream)))
 
 
 def kv_pool_compact(cache: kvq_cache, pool: torch.Tensor, n_used: torch.Tensor, stream=None):
     """n_used: int32 [1] (written)."""
-    at, size = _pool(cache, pool, n_used)
+    args = _pool(cache, pool, n_used)
     if n_used.numel() != 1:
         raise KVQError("n_used must be int32 [1]")
-    _check(load().kv_pool_compact(ctypes.byref(cache), at, size, _ptr(n_used, cache.device), _stream(stream)))
+    _check(load().kv_pool_compact(*args, _stream(stream)))
 
 
 def _in_dtype_of(t: torch.Tensor) -> int:
