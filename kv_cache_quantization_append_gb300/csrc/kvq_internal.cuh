@@ -144,12 +144,14 @@ struct PrefillArgs {
   int max_pages_per_seq, max_seq_len;
   float* parts;      // KVQ_Q8B32: partial results of row tiles that several CTAs share, two a CTA
   int2* keys;        // behind them: (unit, row tile) of each; -1: there is none
+  int* taken;        // behind these: row tiles that CTAs have taken whole, past the first of each; cleared with the ring's copy
   int sms;
 };
 size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W);
 cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStream_t s);
 size_t prefill_block_scratch_bytes(int sms);
-cudaError_t launch_prefill_blocks(const PrefillArgs& a, int sms, cudaStream_t s);
+void prefill_block_places(PrefillArgs* a);  // sms, keys, taken, from parts
+cudaError_t launch_prefill_blocks(const PrefillArgs& a, cudaStream_t s);
 
 struct EvictArgs {
   DevPtrs p;

@@ -149,6 +149,7 @@ __device__ __forceinline__ uint32_t cm_off(int row, int k, int R) {
 // Copy the window ring of every (layer, sequence < batch, kv-head) of the call to scratch.
 __global__ void snapshot_kernel(const __grid_constant__ PrefillArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");  // (of 8-bit blocks: the append, which waits before it writes)
+  if (a.taken && blockIdx.x == 0 && threadIdx.x == 0) *a.taken = 0;
   const size_t per_layer = (size_t)a.batch * a.Hkv * a.W * D / 4;  // float4s of one layer's sequences
   const size_t n = per_layer * a.n_layers_call;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
@@ -796,7 +797,10 @@ size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W) {
   return 2 * align256((size_t)n_layers_call * batch * Hkv * W * D * sizeof(float));
 }
 
-cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStream_t s) {
+cudaError_t launch_prefill(const PrefillArgs& args, const AppendArgs& app, cudaStream_t s) {
+  PrefillArgs a = args;
+  a.taken = nullptr;
+  if (a.k_format == KVQ_Q8B32) prefill_block_places(&a);
   if (a.W > 0) {
     const size_t n4 = (size_t)a.n_layers_call * a.batch * a.Hkv * a.W * D / 4;
     const size_t want = (n4 + 255) / 256;
@@ -807,7 +811,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStre
   }
   if (a.k_format == KVQ_Q8B32) {  // (append_block.cu, prefill_block.cu)
     const cudaError_t e = launch_append_blocks(app, a.W > 0, s);
-    return e != cudaSuccess ? e : launch_prefill_blocks(a, a.sms, s);
+    return e != cudaSuccess ? e : launch_prefill_blocks(a, s);
   }
   cudaError_t e = launch_append(app, s);
   if (e != cudaSuccess) return e;

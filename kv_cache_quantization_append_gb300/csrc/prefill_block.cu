@@ -142,17 +142,20 @@ struct Work {
     return u;
   }
 };
-// warp 0: positions and prefix of the sequences' costs into shared memory
-__device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas) {
+// warp 0: positions and prefix of the sequences' costs into shared memory; whole: row tiles are many and none is long against
+// a CTA's share, so that CTAs take them whole, one after the other
+__device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas, int* whole) {
   Work w(a, p0, pre, 0);
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
     long long s = 0;
+    int far = -1;
     for (int b = b0; b < b1; ++b) {
       const int p = a.pos[b];
       p0[b] = p >= 0 && (long long)p + a.T <= a.max_seq_len ? p : -1;
       if (p0[b] >= 0) s += w.upto(b, w.nx);
+      far = max(far, p0[b]);
     }
     long long incl = s;
 #pragma unroll
@@ -166,6 +169,9 @@ __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas) {
       if (p0[b] >= 0) run += w.upto(b, w.nx);
     }
     if (lane == 31) pre[a.batch] = incl;
+    far = __reduce_max_sync(FULL, far);
+    const long long total = __shfl_sync(FULL, incl, 31);
+    if (lane == 0) *whole = 5 * (far + a.T + K0) * ctas <= 3 * total;
   }
   __syncthreads();
   w.divide((int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE)));
@@ -302,6 +308,7 @@ struct Kernel {
     float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' references and sums, the output's reference, at the end
     float mt[4][ROWS], vt[4], vt0[4];              // a tile's references: of its weights, of its values' scales
     long long hi;                          // where the CTA's stretch of the cost line ends
+    int whole;                             // row tiles are taken whole
     int halves[RS];                        // of a page under way that are read (0: there is no such page)
     float2 scale[8][2];                    // (keys', values') of a tile's two blocks; of a raw tile: its powers of two
     float warp_most[2][N_DQ];              // largest magnitude of a raw tile's keys, values, in each operand warp
@@ -334,6 +341,10 @@ struct Kernel {
 
   // the CTA's first stretch with tiles
   __device__ void locate(const Work& work, Stretch& st) {
+    if (sh.whole) {
+      grab(blockIdx.x, st);
+      return;
+    }
     const long long y = work.cut(blockIdx.x), hi = work.cut(blockIdx.x + 1);
     sh.hi = hi;
     const Unit u = work.find(y);
@@ -344,6 +355,28 @@ struct Kernel {
   __device__ __forceinline__ static int once(int x) {
     asm volatile("" : "+r"(x));
     return x;
+  }
+  // Row tile i of the list, the long ones (of the chunk's end) first, or the next that no CTA has taken.  Which CTA computes a
+  // row tile does not change its result.
+  __device__ void grab(int i, Stretch& st) const {
+    const int qpt = ROWS / a.g, nx = (a.T + qpt - 1) / qpt, HL = a.Hkv * a.n_layers_call, per = a.batch * HL;
+    st.tb = -1;
+    while (true) {
+      if (i < 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // (the ring's copy clears the count)
+        i = gridDim.x + atomicAdd(a.taken, 1);
+      }
+      if (i >= nx * per) return;
+      Unit n;
+      n.x = nx - 1 - i / per;
+      i %= per;
+      n.b = i / HL;
+      n.hl = i - n.b * HL;
+      n.start = 0;
+      n.cost = 1;
+      if (sh.p0[n.b] >= 0 && take(n, Tiles(sh.p0, a.T, qpt, n, a.W, RNT), 0, 1, 0, st)) return;
+      i = -1;
+    }
   }
   // the one after it: the next row tiles of the line
   __device__ void follow_up(const Stretch& u, Stretch& st) const {
@@ -1021,7 +1054,9 @@ struct Kernel {
     float f = 0.f;
     if (row < nrows) {
       const float M = sh.M[row], m0 = sh.m[0][row], m1 = sh.m[1][row];
-      const float l = sh.l[0][row] * (m0 == -INFINITY ? 1.f : ex2(m0 - M)) + sh.l[1][row] * (m1 == -INFINITY ? 1.f : ex2(m1 - M));
+      // (alike whichever group had the first tile)
+      const float l = __fadd_rn(__fmul_rn(sh.l[0][row], m0 == -INFINITY ? 1.f : ex2(m0 - M)),
+                                __fmul_rn(sh.l[1][row], m1 == -INFINITY ? 1.f : ex2(m1 - M)));
       if (u.rec >= 0) {
         if (lane < 16) {
           dst[ROWS * D + row] = M;
@@ -1084,7 +1119,10 @@ struct Kernel {
       if (ROLE == LOGITS) issue_logits(u);
       if (ROLE == VALUES) issue_values(u);
       if (ROLE == PAGES) fetch(u);
-      if (ROLE == AHEAD && lane == 0) follow_up(u, sh.at[(k + 1) & 1]);
+      if (ROLE == AHEAD && lane == 0) {
+        if (sh.whole) grab(-1, sh.at[(k + 1) & 1]);
+        else follow_up(u, sh.at[(k + 1) & 1]);
+      }
       sync_all();
       if (sh.gone) return;
       if (ROLE == SOFTMAX) rows_out(u);
@@ -1123,7 +1161,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
     sh.gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const Work work = plan(a, sh.p0, sh.pre, gridDim.x);
+  const Work work = plan(a, sh.p0, sh.pre, gridDim.x, &sh.whole);
   if (tid == NEXT_WARP * 32) a.keys[2 * blockIdx.x] = a.keys[2 * blockIdx.x + 1] = make_int2(-1, -1);
   // sequences that are not part of the call, or past capacity: zeros
   for (int b = 0; b < a.batch; ++b) {
@@ -1218,9 +1256,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __g
 }
 
 template <bool BF16>
-cudaError_t launch(PrefillArgs a, int sms, cudaStream_t s) {
-  if (sms > MAX_CTAS) sms = MAX_CTAS;
-  a.keys = reinterpret_cast<int2*>(a.parts + (size_t)2 * sms * REC);
+cudaError_t launch(const PrefillArgs& a, cudaStream_t s) {
+  const int sms = a.sms;
   cudaError_t e = allow_shared_memory<prefill_block_kernel<BF16>>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1243,10 +1280,14 @@ cudaError_t launch(PrefillArgs a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-size_t prefill_block_scratch_bytes(int sms) { return (size_t)2 * sms * (REC * sizeof(float) + sizeof(int2)); }
+size_t prefill_block_scratch_bytes(int sms) { return (size_t)2 * sms * (REC * sizeof(float) + sizeof(int2)) + 16; }
 
-cudaError_t launch_prefill_blocks(const PrefillArgs& a, int sms, cudaStream_t s) {
-  return a.in_bf16 ? launch<true>(a, sms, s) : launch<false>(a, sms, s);
+void prefill_block_places(PrefillArgs* a) {
+  a->sms = a->sms < MAX_CTAS ? a->sms : MAX_CTAS;
+  a->keys = reinterpret_cast<int2*>(a->parts + (size_t)2 * a->sms * REC);
+  a->taken = reinterpret_cast<int*>(a->keys + (size_t)2 * a->sms);
 }
+
+cudaError_t launch_prefill_blocks(const PrefillArgs& a, cudaStream_t s) { return a.in_bf16 ? launch<true>(a, s) : launch<false>(a, s); }
 
 }  // namespace kvq

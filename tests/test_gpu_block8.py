@@ -437,3 +437,31 @@ def test_a_captured_chunk_at_other_positions():
         assert torch.equal(out, want)
         at[p >= 0] += T
     assert a.status() == 0 and b.status() == 0
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_prefill_of_many_row_tiles(in_dtype):
+    """More row tiles than blocks divide: each is one block's, whichever is free; two calls give the same bytes."""
+    rng = np.random.default_rng(31)
+    gpu, ref = br.make(3, 4, 16, 4, 1200, window=64, in_dtype=in_dtype)
+    pos, T = [0, -1, 300, 77], 700
+    for b in (2, 3):
+        at = [-1] * 4
+        at[b] = 0
+        _append(gpu, ref, -1, rng, pos[b], at, in_dtype)
+    k, v = (_vectors(rng, (3, 4, 4, T), in_dtype) for _ in range(2))
+    q = _vectors(rng, (3, 4, 16, T), in_dtype)
+    state = gpu.buffer.clone()
+    first = gpu.prefill(-1, k.cuda(), v.cuda(), q.cuda(), _i32(pos))
+    gpu.buffer.copy_(state)
+    out = gpu.prefill(-1, k.cuda(), v.cuda(), q.cuda(), _i32(pos))
+    assert torch.equal(first, out) and gpu.status() == 0 and (out[:, 1] == 0).all()
+    out = out.double().cpu().numpy()
+    ref.append(-1, harness.to_np(k), harness.to_np(v), pos)
+    qn = harness.to_np(q)
+    for b in (0, 2, 3):
+        for lay in range(3):
+            ts = sorted({0, T - 1, *(int(t) for t in rng.integers(0, T, 3))})
+            want = np.stack([[ref.attend(lay, b, j, qn[lay, b, j, t], pos[b] + t + 1) for t in ts] for j in range(16)])
+            harness.assert_attention_close(out[lay, b][:, ts], want, TOL)
+    br.check_state(gpu, ref, [(lay, b, h) for lay in (0, 2) for b in (0, 2, 3) for h in (0, 3)])
