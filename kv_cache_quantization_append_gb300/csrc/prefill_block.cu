@@ -142,20 +142,31 @@ struct Work {
     return u;
   }
 };
-// warp 0: positions and prefix of the sequences' costs into shared memory; whole: row tiles are many and none is long against
-// a CTA's share, so that CTAs take them whole, one after the other
+// Whether CTAs take row tiles whole, the long ones first, instead of equal stretches of the line, whose cuts cost most CTAs a
+// row tile's fixed cost more: when the sum of the longest of each round is below 1.15 of a share with that cost.  (`each` row
+// tiles for every x.)  Whole against cut: a prompt of 2048 tokens of 32 heads 152 against 209 us, 4096 tokens 400 / 498, 1024
+// tokens 78 / 98, 1500 of 24 heads 99 / 120; 2048 of 16 heads at position 6000 (256 long row tiles) 315 / 282, not taken.
+__device__ bool take_whole(const Work& w, int ctas, int far, long long each, long long total) {
+  const long long units = each * w.nx;
+  if (units >= 16LL * ctas) return true;
+  long long rounds = 0;
+  for (long long i = 0; i < units; i += ctas) rounds += far + (w.nx - i / each) * w.qpt + K0;
+  return 20 * rounds <= 23 * (total / ctas + K0);
+}
+// warp 0: positions and prefix of the sequences' costs into shared memory
 __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas, int* whole) {
   Work w(a, p0, pre, 0);
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
     long long s = 0;
-    int far = -1;
+    int far = -1, active = 0;
     for (int b = b0; b < b1; ++b) {
       const int p = a.pos[b];
       p0[b] = p >= 0 && (long long)p + a.T <= a.max_seq_len ? p : -1;
       if (p0[b] >= 0) s += w.upto(b, w.nx);
       far = max(far, p0[b]);
+      active += p0[b] >= 0;
     }
     long long incl = s;
 #pragma unroll
@@ -171,7 +182,8 @@ __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas, in
     if (lane == 31) pre[a.batch] = incl;
     far = __reduce_max_sync(FULL, far);
     const long long total = __shfl_sync(FULL, incl, 31);
-    if (lane == 0) *whole = 5 * (far + a.T + K0) * ctas <= 3 * total;
+    active = __reduce_add_sync(FULL, active);
+    if (lane == 0) *whole = active > 0 && take_whole(w, ctas, far, (long long)active * w.HL, total);
   }
   __syncthreads();
   w.divide((int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE)));
