@@ -190,9 +190,12 @@ __device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas, in
   return w;
 }
 
-// A row tile: its queries' positions, the recorded positions [0, qend) that any of them reads, the raw ones from rlo
+// A row tile: its queries' positions, the recorded positions [0, qend) that any of them reads, the raw ones from rlo.  Raw tiles
+// have hi and lo planes of FULL_NT positions, but those of a bf16 cache's own call one plane of RNT: first n_full of the former,
+// for tokens of earlier calls, whose copies are floats.
+constexpr int FULL_NT = 32;
 struct Tiles {
-  int t0, nq, Pmin, Pmax, qend, nqt, rlo, n;
+  int t0, nq, Pmin, Pmax, qend, nqt, rlo, n_full, n;
   Tiles() = default;
   __device__ Tiles(const int* p0, int T, int qpt, const Unit& u, int W, int raw_nt) {
     t0 = u.x * qpt;
@@ -202,8 +205,11 @@ struct Tiles {
     qend = max(0, Pmax - W + 1);
     nqt = (qend + NT - 1) / NT;
     rlo = max(0, Pmin - W + 1);
-    n = nqt + (Pmax - rlo) / raw_nt + 1;
+    n_full = raw_nt == FULL_NT ? 0 : max(0, p0[u.b] - rlo + FULL_NT - 1) / FULL_NT;
+    n = nqt + n_full + max(0, Pmax - rlo - n_full * FULL_NT + raw_nt) / raw_nt;
   }
+  // the first position of raw tile r
+  __device__ __forceinline__ int raw_at(int r, int raw_nt) const { return rlo + min(r, n_full) * FULL_NT + max(0, r - n_full) * raw_nt; }
   // tiles before offset `off` of the row tile's stretch of the cost line, `cost` long: what is fixed, recorded tiles of
   // their positions, raw ones of equal shares of the rest
   __device__ __forceinline__ int before(long long off, long long cost) const {
@@ -290,11 +296,6 @@ __device__ __forceinline__ void unpack8(uint4 w, float* x) {
     x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
   }
 }
-// the upper halves of eight floats that are bf16 values
-__device__ __forceinline__ uint4 pack8(float4 a, float4 b) {
-  return make_uint4(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632u), __byte_perm(__float_as_uint(a.z), __float_as_uint(a.w), 0x7632u),
-                    __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632u), __byte_perm(__float_as_uint(b.z), __float_as_uint(b.w), 0x7632u));
-}
 
 // This warp group's registers per thread from here on (taking more and giving some back are two instructions)
 template <int N>
@@ -307,8 +308,9 @@ __device__ __forceinline__ void take_registers() {
 template <bool BF16>
 struct Kernel {
   static constexpr int ROW_BYTES = D * (BF16 ? 2 : 4);  // of a raw vector of the call
-  static constexpr int RNT = BF16 ? 64 : 32;  // raw positions of a tile: one plane of a bf16 cache's, hi and lo of a float one's
-  static constexpr uint32_t ID_S = idesc(ROWS, NT, false, false), ID_SR = idesc(ROWS, RNT, false, false);
+  static constexpr int RNT = BF16 ? 64 : FULL_NT;  // raw positions of a tile: one plane of a bf16 cache's, hi and lo of a float one's
+  static constexpr uint32_t ID_S = idesc(ROWS, NT, false, false), ID_SR = idesc(ROWS, FULL_NT, false, false);
+  static_assert(!BF16 || RNT == NT, "as wide as a recorded tile");
   static constexpr uint32_t ID_O = idesc(ROWS, D, false, false), ID_OR = idesc(ROWS, D, false, true);
 
   // shared by the CTA, besides the stages
@@ -549,12 +551,14 @@ struct Kernel {
           mma_ts(dS, q + 8 * ks + (C_QLO - C_QHI), k + 2 * K_LEAD / 16 * ks, ID_S, 1);
         }
       } else {
-        uint64_t k = sdesc(base + s * STAGE, RNT * 16, 128), q = sdesc(base + QR_OFF, QR_LEAD, 128);
+        const bool full = !BF16 || it < tl.nqt + tl.n_full;
+        const uint32_t nt = full ? FULL_NT : RNT, id = full ? ID_SR : ID_S;
+        uint64_t k = sdesc(base + s * STAGE, nt * 16, 128), q = sdesc(base + QR_OFF, QR_LEAD, 128);
 #pragma unroll 1
-        for (int ks = 0; ks < D / 16; ++ks, k += RNT * 2, q += 2 * QR_LEAD / 16) {
-          mma_ss(dS, q, k, ID_SR, ks > 0);
-          mma_ss(dS, q + QR_PLANE / 16, k, ID_SR, 1);
-          if (!BF16) mma_ss(dS, q, k + LO_K / 16, ID_SR, 1);
+        for (int ks = 0; ks < D / 16; ++ks, k += nt * 2, q += 2 * QR_LEAD / 16) {
+          mma_ss(dS, q, k, id, ks > 0);
+          mma_ss(dS, q + QR_PLANE / 16, k, id, 1);
+          if (full) mma_ss(dS, q, k + LO_K / 16, id, 1);
         }
       }
       mma_commit(&sh.sfull[bb]);
@@ -580,11 +584,12 @@ struct Kernel {
           mma_ts(dO, p + 16 * ks, v + 2 * V_LEAD / 16 * ks, ID_O, 1);
         }
       } else {
+        const bool full = !BF16 || it < tl.nqt + tl.n_full;
         uint64_t v = sdesc(base + s * STAGE + V_OFF, V_LEAD, 128);
 #pragma unroll 1
-        for (int ks = 0; ks < RNT / 16; ++ks, v += 2 * V_LEAD / 16, p += 16) {
+        for (int ks = 0; ks < (full ? FULL_NT : RNT) / 16; ++ks, v += 2 * V_LEAD / 16, p += 16) {
           mma_ts(dO, p + 8, v, ID_OR, ks > 0);
-          if (!BF16) mma_ts(dO, p, v + LO_V / 16, ID_OR, 1);
+          if (full) mma_ts(dO, p, v + LO_V / 16, ID_OR, 1);
           mma_ts(dO, p, v, ID_OR, 1);
         }
       }
@@ -626,7 +631,7 @@ struct Kernel {
     static_assert(RNT * ROW_BYTES <= PAGE_SLOT, "a raw operand fits a slot");
 #pragma unroll 1
     for (int it = max(u.ta, u.tl.nqt); it < u.tb; ++it) {
-      const int j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+      const int j0 = u.tl.raw_at(it - u.tl.nqt, RNT);
       if (j0 < u.p0) continue;
       const uint32_t bytes = min(RNT, u.tl.Pmax - j0 + 1) * ROW_BYTES;
       const size_t off = ((size_t)u.unit * a.T + (j0 - u.p0)) * ROW_BYTES;
@@ -689,68 +694,74 @@ struct Kernel {
     }
 #pragma unroll 1
     for (; it < u.tb; ++it, ++gt) {
-      const int s = gt % NS, j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+      const int s = gt % NS, j0 = u.tl.raw_at(it - u.tl.nqt, RNT);
+      const bool full = !BF16 || it < u.tl.nqt + u.tl.n_full;
       const uint32_t before = ((gt / NS) & 1) ^ 1;
 #pragma unroll 1
       for (int values = 0; values < 2; ++values) {
         if (gt >= NS && !held(values ? &sh.vempty[s] : &sh.kempty[s], before)) return;
-        if (!raw(u, j0, smem + s * STAGE + (values ? V_OFF : 0), values)) return;
+        uint8_t* plane = smem + s * STAGE + (values ? V_OFF : 0);
+        if (!(full ? raw<true>(u, j0, plane, values) : raw<false>(u, j0, plane, values))) return;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(values ? &sh.vfull[s] : &sh.kfull[s]);
       }
     }
   }
-  // Raw keys (K-major) or values (N-major: rows are positions too, in the order of the places) of positions j0 .. j0 + RNT - 1
-  // as operand planes, over a power of two of the tile.  An element of a bf16 vector that its one fp16 plane does not hold
-  // exactly is below 2^-14 of the tile's largest and off by 2^-25 of that at most.
+  // Raw keys (K-major) or values (N-major: rows are positions too, in the order of the places) of positions j0 .. as operand
+  // planes, over a power of two of the tile: FULL: hi and lo of FULL_NT positions, else one of RNT of the call's own bf16 ones.
+  // An element of a bf16 vector that its one fp16 plane does not hold exactly is below 2^-14 of the tile's largest and off by
+  // 2^-25 of that at most.
+  template <bool FULL>
   __device__ __forceinline__ bool raw(const Stretch& u, int j0, uint8_t* plane, int values) {
     // the lane's q-th eight channels are group 4 ((q + r / 4) mod 4) + (i + r) mod 4: eight lanes' reads of a slot hit all banks
     const int lane = once(this->lane), dw = once(warp) - DQ0, r = lane & 7, b = ((lane >> 3) + r) & 3, q0 = r >> 2;
     const int p0 = u.p0;
     const size_t unit = u.unit;
-    const bool staged = j0 >= p0;
+    constexpr bool PACKED = !FULL;  // kept as bf16
+    const bool staged = PACKED || j0 >= p0;
     const int slot = gr % RS;
     if (staged && !held(&sh.rfull[slot], (gr / RS) & 1)) return false;
     const float* old = values ? a.snap_v : a.snap_k;
     const uint8_t* mine = staged ? smem + PAGE_OFF + slot * PAGE_SLOT
                                  : static_cast<const uint8_t*>(values ? a.v : a.k) + ((size_t)unit * a.T * ROW_BYTES + (long long)(j0 - p0) * ROW_BYTES);
-    constexpr int ROUNDS = RNT / (8 * N_DQ);
-    uint4 w[ROUNDS][BF16 ? 4 : 8];  // bf16 values, or floats; every load of the tile under way at once
+    constexpr int TILE = FULL ? FULL_NT : RNT, ROUNDS = TILE / (8 * N_DQ), WORDS = PACKED ? 4 : 8;
+    uint4 w[ROUNDS][WORDS];  // bf16 values, or floats; every load of the tile under way at once
 #pragma unroll
     for (int n = 0; n < ROUNDS; ++n) {
       const int t = 8 * dw + r + 8 * N_DQ * n, j = j0 + t;
 #pragma unroll
-      for (int q = 0; q < (BF16 ? 4 : 8); ++q) w[n][q] = make_uint4(0u, 0u, 0u, 0u);
+      for (int q = 0; q < WORDS; ++q) w[n][q] = make_uint4(0u, 0u, 0u, 0u);
       if (j > u.tl.Pmax) continue;
-      if (j < p0) {
+      if (FULL && j < p0) {
         const float4* f = reinterpret_cast<const float4*>(old + (unit * a.W + j % a.W) * D) + 2 * b;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 x = __ldg(f + 8 * ((q + q0) & 3)), y = __ldg(f + 8 * ((q + q0) & 3) + 1);
-          if (BF16) w[n][q] = pack8(x, y);
-          else {
-            w[n][2 * q] = *reinterpret_cast<const uint4*>(&x);
-            w[n][2 * q + 1] = *reinterpret_cast<const uint4*>(&y);
-          }
+          w[n][(2 * q) % WORDS] = *reinterpret_cast<const uint4*>(&x);
+          w[n][(2 * q + 1) % WORDS] = *reinterpret_cast<const uint4*>(&y);
         }
       } else {
         const uint4* f = reinterpret_cast<const uint4*>(mine + t * ROW_BYTES) + (BF16 ? 1 : 2) * b;  // (of either memory)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (BF16) w[n][q] = f[4 * ((q + q0) & 3)];
-          else {
-            w[n][2 * q] = f[8 * ((q + q0) & 3)];
-            w[n][2 * q + 1] = f[8 * ((q + q0) & 3) + 1];
+          if (PACKED) w[n][q] = f[4 * ((q + q0) & 3)];
+          else if (BF16) {
+            const uint4 x = f[4 * ((q + q0) & 3)];
+            w[n][(2 * q) % WORDS] = make_uint4(x.x << 16, x.x & 0xffff0000u, x.y << 16, x.y & 0xffff0000u);
+            w[n][(2 * q + 1) % WORDS] = make_uint4(x.z << 16, x.z & 0xffff0000u, x.w << 16, x.w & 0xffff0000u);
+          } else {
+            w[n][(2 * q) % WORDS] = f[8 * ((q + q0) & 3)];
+            w[n][(2 * q + 1) % WORDS] = f[8 * ((q + q0) & 3) + 1];
           }
         }
       }
     }
     auto eight = [&](int n, int q, float (&x)[8]) {  // the q-th channels
-      if (BF16) unpack8(w[n][q], x);
+      if (PACKED) unpack8(w[n][q], x);
       else {
-        *reinterpret_cast<uint4*>(x) = w[n][(2 * q) % (BF16 ? 4 : 8)];
-        *reinterpret_cast<uint4*>(x + 4) = w[n][(2 * q + 1) % (BF16 ? 4 : 8)];
+        *reinterpret_cast<uint4*>(x) = w[n][(2 * q) % WORDS];
+        *reinterpret_cast<uint4*>(x + 4) = w[n][(2 * q + 1) % WORDS];
       }
     };
     float m = 0.f;
@@ -789,9 +800,9 @@ struct Kernel {
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(x[2 * e] * inv, x[2 * e + 1] * inv, hi[e], lo[e]);
         const int kg = 4 * ((q + q0) & 3) + b;
-        uint8_t* o = to + kg * (values ? 128 : RNT * 16);
+        uint8_t* o = to + kg * (values ? 128 : TILE * 16);
         *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (!BF16) *reinterpret_cast<uint4*>(o + (values ? LO_V : LO_K)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (FULL) *reinterpret_cast<uint4*>(o + (values ? LO_V : LO_K)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     return true;
@@ -925,9 +936,9 @@ struct Kernel {
         const float2 s0 = sh.scale[gt & 7][0];
         dk[0] = dk[1] = s0.x * sh.qraw[row];
         dv[0] = dv[1] = s0.y;
-        const int j0 = u.tl.rlo + (it - u.tl.nqt) * RNT;
+        const int r = it - u.tl.nqt, j0 = u.tl.raw_at(r, RNT);
         first = hi + 1 - j0;
-        last = min(P - j0, RNT - 1);
+        last = min(P - j0, (BF16 && r >= u.tl.n_full ? RNT : FULL_NT) - 1);
       }
       const float mx = top_of<true>(sa, dk, first, last);
       // The second group begins with the first one's references: as long as neither moves, their parts add up as they are.

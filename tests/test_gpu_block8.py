@@ -465,3 +465,25 @@ def test_prefill_of_many_row_tiles(in_dtype):
             want = np.stack([[ref.attend(lay, b, j, qn[lay, b, j, t], pos[b] + t + 1) for t in ts] for j in range(16)])
             harness.assert_attention_close(out[lay, b][:, ts], want, TOL)
     br.check_state(gpu, ref, [(lay, b, h) for lay in (0, 2) for b in (0, 2, 3) for h in (0, 3)])
+
+
+@pytest.mark.parametrize("T", [1, 20, 150])
+def test_the_ring_is_read_in_full(T):
+    """Tokens of earlier calls are what the ring holds, floats, in a bf16 cache too (as decode reads them)."""
+    rng = np.random.default_rng(32)
+    gpu, ref = br.make(1, 2, 4, 2, 400, window=64)
+    pos = [127, 127]
+    _append(gpu, ref, 0, rng, 127, [0, 0], "bf16")
+    n = 2 * 2 * 64 * 128 * 4
+    v0 = lib.kv_cache_bytes(gpu.cfg) - -(-2 * 7 * 2 * 16416 // 256) * 256 - n
+    p = np.arange(96, 127)                       # of a block that is not yet coded
+    for side, o in enumerate((v0 - n, v0)):
+        ring = gpu.buffer[o:o + n].view(torch.float32).view(2, 2, 64, 128)
+        x = rng.standard_normal((2, 2, len(p), 128)).astype(np.float32)
+        ring[:, :, torch.as_tensor(p % 64).cuda()] = torch.as_tensor(x).cuda()
+        ref.raw[side][0, :, :, p] = np.moveaxis(x, 2, 0)
+    _check_decode(gpu, ref, rng, pos, "bf16")
+    k, v, q = (_vectors(rng, (2, h, T), "bf16") for h in (2, 2, 4))
+    # (bounded by float's error: bf16's would be 4e-3)
+    _check_prefill(gpu, ref, rng, k, v, q, pos)
+    br.check_state(gpu, ref, _units(gpu.cfg))
