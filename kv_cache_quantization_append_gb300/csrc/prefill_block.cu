@@ -11,8 +11,9 @@
 //  * Work: a row tile is 128 (query, head) rows of one (layer, sequence, kv-head); its positions go in tiles of 64 recorded
 //    ones (a page), then of raw ones.  The call's tiles form one list that is cut into equal ranges, one per CTA (one CTA
 //    an SM), whatever the chunk's and the contexts' lengths: a row tile that a cut divides leaves partial results, which a
-//    second launch joins in order.  Without the cut 1024 tokens of 24 heads are 192 row tiles on 152 SMs, and three short
-//    turns keep 6 of them busy.
+//    second launch joins in order.  Without the cut 1024 tokens of 24 heads are 200 row tiles on 152 SMs, and three short
+//    turns keep 12 of them busy.  Where row tiles are many and not long (take_whole) nothing is cut: CTAs take them one
+//    after the other.
 //  * A tile's stored order is the operands' order up to a permutation of channels (keys) or positions (values), which
 //    queries and weights follow: 16 stored bytes become two 16-byte operand rows by byte permutes, nothing is transposed.
 //  * Raw tiles are taken as they are, not rotated: queries are also kept unrotated (in shared memory), and the output
@@ -27,9 +28,9 @@
 //    for one phase are computed in it (once()), what a row tile does once is done by one group of warps.
 //  * Every wait is bounded; one that runs out flags the status word and the CTA leaves as a whole.
 //
-// One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 421 us (two passes of the products over recorded
-// positions at the measured bf16 rate: 204 us, 48 %), a prompt of 2048 tokens of 32 heads 208 us, three float turns of 37
-// tokens of 8 heads at 1000 positions 33 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
+// One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 435 us (two passes of the products over recorded
+// positions at the measured bf16 rate: 204 us, 47 %), a prompt of 2048 tokens of 32 heads 154 us, three float turns of 37
+// tokens of 8 heads at 1000 positions 35 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
 // 1100: bound by the weights (1500 cycles a tile and group of warps, two groups) and the rate at which instructions come.
 #include <cfloat>
 #include <cstddef>
@@ -71,7 +72,7 @@ static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "w
 constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
 constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
 // A row tile's fixed cost in positions, KF of it before its first tile (queries, the start of the products), the rest for raw
-// tiles and the output; and the positions that a CTA takes at least.  A prompt of 2048 tokens and 32 heads: 518 us at a cost of
+// tiles and the output; and the positions that a CTA takes at least.  A prompt of 2048 tokens and 32 heads, cut: 518 us at a cost of
 // 32, 345 at 128, 240 at 448, 208 at 1024, 213 at 1536; at 15001 positions it hardly matters.  Three turns of 37 tokens at 1000
 // positions: 55 us with shares of 512, 49 of 256, 38 of 128, 33 with raw tiles' cost at their end.
 constexpr long long K0 = 1024, KF = 512, MIN_SHARE = 128;
