@@ -487,3 +487,25 @@ def test_the_ring_is_read_in_full(T):
     # (bounded by float's error: bf16's would be 4e-3)
     _check_prefill(gpu, ref, rng, k, v, q, pos)
     br.check_state(gpu, ref, _units(gpu.cfg))
+
+
+def test_many_row_tiles_captured():
+    """The count of row tiles taken begins anew with each replay, at other positions too."""
+    rng = np.random.default_rng(33)
+    a, _ = br.make(4, 4, 16, 2, 1200, window=64)
+    b, _ = br.make(4, 4, 16, 2, 1200, window=64)
+    T = 500
+    k, v, q = (torch.zeros(4, 2, h, T, 128, dtype=torch.bfloat16, device="cuda") for h in (4, 4, 16))
+    pos, out = _i32([0, 0]), torch.zeros(4, 2, 16, T, 128, device="cuda")
+    for x in (a, b):
+        x.prefill(-1, k, v, q, pos, out=out)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        b.prefill(-1, k, v, q, pos, out=out)
+    for p in ([0, 0], [500, -1], [650, 500], [0, 0]):
+        for x, h in ((k, 4), (v, 4), (q, 16)):
+            x.copy_(_vectors(rng, (4, 2, h, T), "bf16"))
+        pos.copy_(_i32(p))
+        graph.replay()
+        assert torch.equal(out, a.prefill(-1, k, v, q, _i32(p)))
+    assert a.status() == 0 and b.status() == 0
