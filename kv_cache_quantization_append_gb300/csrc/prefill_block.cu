@@ -13,7 +13,7 @@
 //    an SM), whatever the chunk's and the contexts' lengths: a row tile that a cut divides leaves partial results, which a
 //    second launch joins in order.  Without the cut 1024 tokens of 24 heads are 200 row tiles on 152 SMs, and three short
 //    turns keep 12 of them busy.  Where row tiles are many and not long (take_whole) nothing is cut: CTAs take them one
-//    after the other.
+//    after the other.  (The arithmetic of the list stands in prefill_list.cuh.)
 //  * A tile's stored order is the operands' order up to a permutation of channels (keys) or positions (values), which
 //    queries and weights follow: 16 stored bytes become two 16-byte operand rows by byte permutes, nothing is transposed.
 //  * Raw tiles are taken as they are, not rotated: queries are also kept unrotated (in shared memory), and the output
@@ -35,6 +35,7 @@
 #include <cfloat>
 #include <cstddef>
 
+#include "prefill_list.cuh"
 #include "tc.cuh"
 
 namespace kvq {
@@ -42,9 +43,8 @@ namespace kvq {
 namespace {
 
 using namespace tc;
+using namespace prefill_list;
 
-constexpr int ROWS = 128;            // rows of a row tile = MMA M = lanes of tensor memory
-constexpr int NT = 64;               // recorded positions of a tile = a page
 constexpr int NS = 3;                // operand stages
 constexpr int RS = 2;                // pages under way
 constexpr int N_SOFT = 8;            // softmax warps, two groups
@@ -71,11 +71,6 @@ constexpr uint32_t O_STRIDE = (D + 4) * 4;
 static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "what borrows the stages");
 constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
 constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
-// A row tile's fixed cost in positions, KF of it before its first tile (queries, the start of the products), the rest for raw
-// tiles and the output; and the positions that a CTA takes at least.  A prompt of 2048 tokens and 32 heads, cut: 518 us at a cost of
-// 32, 345 at 128, 240 at 448, 208 at 1024, 213 at 1536; at 15001 positions it hardly matters.  Three turns of 37 tokens at 1000
-// positions: 55 us with shares of 512, 49 of 256, 38 of 128, 33 with raw tiles' cost at their end.
-constexpr long long K0 = 1024, KF = 512, MIN_SHARE = 128;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 constexpr int REC = ROWS * D + 2 * ROWS;  // floats of a partial result: O, m, l
 
@@ -93,140 +88,59 @@ __device__ __forceinline__ uint32_t km(int row, int k, uint32_t lead) {
 }
 
 // ------------------------------------------------------------------ the list of tiles
-struct Unit {
-  int b, x, hl;           // sequence, row tile, (layer, kv-head)
-  long long start, cost;  // on the cost line
-};
-
-// Costs in positions: row tile x of a sequence at p0 counts p0 + (x + 1) qpt + K0, about the positions it visits.  The line
-// goes through sequences, row tiles, (layer, kv-head) pairs, and is cut into n parts of equal cost.
-struct Work {
-  int B, T, qpt, nx, HL, n;
-  long long share, rest;   // of the n parts, the first `rest` are one longer
-  const int* p0;           // per sequence; -1: not part of the call
-  const long long* pre;    // cost before each sequence, [B + 1]
-  Work() = default;
-  __device__ Work(const PrefillArgs& a, const int* p, const long long* c, int ctas)
-      : B(a.batch), T(a.T), qpt(ROWS / a.g), nx((a.T + ROWS / a.g - 1) / (ROWS / a.g)), HL(a.Hkv * a.n_layers_call), n(ctas), p0(p), pre(c) {}
-  __device__ void divide(int ctas) {
-    n = ctas;
-    share = total() / n;
-    rest = total() - share * n;
-  }
-  __device__ __forceinline__ long long cost(int b, int x) const { return p0[b] + (long long)(x + 1) * qpt + K0; }
-  __device__ __forceinline__ long long upto(int b, int x) const {
-    return (x * (p0[b] + K0) + (long long)qpt * x * (x + 1) / 2) * HL;
-  }
-  __device__ __forceinline__ long long total() const { return pre[B]; }
-  __device__ __forceinline__ long long cut(int c) const { return share * c + min((long long)c, rest); }
-  __device__ Unit find(long long y) const {
-    Unit u;
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {  // the last sequence that starts at or before y (those without work start where the next does)
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= y) lo = mid;
-      else hi = mid - 1;
-    }
-    u.b = lo;
-    const long long r = y - pre[lo];
-    int xl = 0, xh = nx - 1;
-    while (xl < xh) {
-      const int mid = (xl + xh + 1) >> 1;
-      if (upto(lo, mid) <= r) xl = mid;
-      else xh = mid - 1;
-    }
-    u.x = xl;
-    u.cost = cost(lo, xl);
-    const long long r2 = r - upto(lo, xl);
-    u.hl = (int)(r2 / u.cost);
-    u.start = y - r2 % u.cost;
-    return u;
-  }
-};
-// Whether CTAs take row tiles whole, the long ones first, instead of equal stretches of the line, whose cuts cost most CTAs a
-// row tile's fixed cost more: when the sum of the longest of each round is below 1.15 of a share with that cost.  (`each` row
-// tiles for every x.)  Whole against cut: a prompt of 2048 tokens of 32 heads 152 against 209 us, 4096 tokens 400 / 498, 1024
-// tokens 78 / 98, 1500 of 24 heads 99 / 120; 2048 of 16 heads at position 6000 (256 long row tiles) 315 / 282, not taken.
-__device__ bool take_whole(const Work& w, int ctas, int far, long long each, long long total) {
-  const long long units = each * w.nx;
-  if (units >= 16LL * ctas) return true;
-  long long rounds = 0;
-  for (long long i = 0; i < units; i += ctas) rounds += far + (w.nx - i / each) * w.qpt + K0;
-  return 20 * rounds <= 23 * (total / ctas + K0);
-}
-// warp 0: positions and prefix of the sequences' costs into shared memory
-__device__ Work plan(const PrefillArgs& a, int* p0, long long* pre, int ctas, int* whole) {
-  Work w(a, p0, pre, 0);
+// warp 0: positions, active sequences and prefix of the sequences' costs into shared memory; how the CTAs share the list
+template <typename Shared>
+__device__ void plan(const PrefillArgs& a, Shared& sh, int ctas, int raw_nt) {
   if (threadIdx.x < 32) {
+    const List w(a.batch, a.T, a.g, a.Hkv * a.n_layers_call, a.W, raw_nt, sh.p0, sh.pre, sh.act, 0);
     const int lane = threadIdx.x, per = (a.batch + 31) / 32;
     const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
     long long s = 0;
     int far = -1, active = 0;
     for (int b = b0; b < b1; ++b) {
       const int p = a.pos[b];
-      p0[b] = p >= 0 && (long long)p + a.T <= a.max_seq_len ? p : -1;
-      if (p0[b] >= 0) s += w.upto(b, w.nx);
-      far = max(far, p0[b]);
-      active += p0[b] >= 0;
+      sh.p0[b] = p >= 0 && (long long)p + a.T <= a.max_seq_len ? p : -1;
+      if (sh.p0[b] >= 0) s += w.upto(b, w.nx);
+      far = max(far, sh.p0[b]);
+      active += sh.p0[b] >= 0;
     }
     long long incl = s;
+    int upto = active;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += y;
+      const int z = __shfl_up_sync(FULL, upto, o);
+      if (lane >= o) {
+        incl += y;
+        upto += z;
+      }
     }
     long long run = incl - s;
+    int at = upto - active;
     for (int b = b0; b < b1; ++b) {
-      pre[b] = run;
-      if (p0[b] >= 0) run += w.upto(b, w.nx);
+      sh.pre[b] = run;
+      if (sh.p0[b] < 0) continue;
+      run += w.upto(b, w.nx);
+      sh.act[at++] = (unsigned short)b;
     }
-    if (lane == 31) pre[a.batch] = incl;
+    if (lane == 31) sh.pre[a.batch] = incl;
     far = __reduce_max_sync(FULL, far);
-    const long long total = __shfl_sync(FULL, incl, 31);
     active = __reduce_add_sync(FULL, active);
-    if (lane == 0) *whole = active > 0 && take_whole(w, ctas, far, (long long)active * w.HL, total);
+    __syncwarp();
+    if (lane == 0) {
+      List l = w;
+      l.n_act = sh.n_act = active;
+      sh.whole = l.take_whole(ctas, far);
+      sh.parts = l.parts(ctas, sh.whole);
+    }
   }
   __syncthreads();
-  w.divide((int)max(1LL, min((long long)ctas, w.total() / MIN_SHARE)));
-  return w;
 }
 
-// A row tile: its queries' positions, the recorded positions [0, qend) that any of them reads, the raw ones from rlo.  Raw tiles
-// have hi and lo planes of FULL_NT positions, but those of a bf16 cache's own call one plane of RNT: first n_full of the former,
-// for tokens of earlier calls, whose copies are floats.
-constexpr int FULL_NT = 32;
-struct Tiles {
-  int t0, nq, Pmin, Pmax, qend, nqt, rlo, n_full, n;
-  Tiles() = default;
-  __device__ Tiles(const int* p0, int T, int qpt, const Unit& u, int W, int raw_nt) {
-    t0 = u.x * qpt;
-    nq = min(qpt, T - t0);
-    Pmin = p0[u.b] + t0;
-    Pmax = Pmin + nq - 1;
-    qend = max(0, Pmax - W + 1);
-    nqt = (qend + NT - 1) / NT;
-    rlo = max(0, Pmin - W + 1);
-    n_full = raw_nt == FULL_NT ? 0 : max(0, p0[u.b] - rlo + FULL_NT - 1) / FULL_NT;
-    n = nqt + n_full + max(0, Pmax - rlo - n_full * FULL_NT + raw_nt) / raw_nt;
-  }
-  // the first position of raw tile r
-  __device__ __forceinline__ int raw_at(int r, int raw_nt) const { return rlo + min(r, n_full) * FULL_NT + max(0, r - n_full) * raw_nt; }
-  // tiles before offset `off` of the row tile's stretch of the cost line, `cost` long: what is fixed, recorded tiles of
-  // their positions, raw ones of equal shares of the rest
-  __device__ __forceinline__ int before(long long off, long long cost) const {
-    const int o = (int)(off - KF), rest = o - nqt * NT;
-    if (o <= 0) return 0;
-    if (rest <= 0) return min(n, (o + NT - 1) / NT);
-    return min(n, nqt + rest * (n - nqt) / max(1, (int)(cost - KF) - nqt * NT));
-  }
-};
-
 // A CTA's stretch of one row tile: tiles ta .. tb - 1 of it, whole or to be joined with others
-struct Stretch {
-  int b, x, hl, unit, layer, h;  // unit: (layer of the call, sequence, kv-head)
-  int p0, ta, tb, rec;        // rec: -1: the row tile as a whole
-  Tiles tl;
-  long long next;             // where on the cost line the CTA goes on
+struct Stretch : Part {
+  int unit, layer, h;  // unit: (layer of the call, sequence, kv-head)
+  int p0, rec;         // rec: -1: the row tile as a whole
 };
 
 // ------------------------------------------------------------------ PTX helpers (besides tc.cuh's)
@@ -323,12 +237,13 @@ struct Kernel {
     float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' references and sums, the output's reference, at the end
     float mt[4][ROWS], vt[4], vt0[4];              // a tile's references: of its weights, of its values' scales
     long long hi;                          // where the CTA's stretch of the cost line ends
-    int whole;                             // row tiles are taken whole
+    int whole, parts, n_act;               // row tiles are taken whole; CTAs that have work; sequences of the call
     int halves[RS];                        // of a page under way that are read (0: there is no such page)
     float2 scale[8][2];                    // (keys', values') of a tile's two blocks; of a raw tile: its powers of two
     float warp_most[2][N_DQ];              // largest magnitude of a raw tile's keys, values, in each operand warp
     alignas(16) float signs[D];            // (read four at a time)
     int p0[MAX_BATCH];
+    unsigned short act[MAX_BATCH];
     long long pre[MAX_BATCH + 1];
     Stretch at[2];                         // this stretch and the next
   };
@@ -354,92 +269,50 @@ struct Kernel {
   __device__ __forceinline__ bool held(uint64_t* bar, uint32_t parity) { return wait(bar, parity, &sh.gone, a.p.status); }
   __device__ __forceinline__ void sync_all() { part_sync(1, THREADS); }
 
+  __device__ __forceinline__ List list() const {
+    return List(a.batch, a.T, a.g, a.Hkv * a.n_layers_call, a.W, RNT, sh.p0, sh.pre, sh.act, sh.n_act);
+  }
   // the CTA's first stretch with tiles
-  __device__ void locate(const Work& work, Stretch& st) {
+  __device__ void locate(Stretch& st) {
     if (sh.whole) {
       grab(blockIdx.x, st);
       return;
     }
-    const long long y = work.cut(blockIdx.x), hi = work.cut(blockIdx.x + 1);
+    const List l = list();
+    long long lo, hi;
+    l.cut(blockIdx.x, sh.parts, lo, hi);
     sh.hi = hi;
-    const Unit u = work.find(y);
-    const Tiles tl(sh.p0, a.T, work.qpt, u, a.W, RNT);
-    if (!take(u, tl, tl.before(y - u.start, u.cost), hi, 0, st)) follow_up(st, st);
+    fill(l.first(lo, hi, st) ? 0 : 1, st);
   }
   // a value whose derivatives are computed where they are used, and not kept through the tiles of a stretch
   __device__ __forceinline__ static int once(int x) {
     asm volatile("" : "+r"(x));
     return x;
   }
-  // Row tile i of the list, the long ones (of the chunk's end) first, or the next that no CTA has taken.  Which CTA computes a
-  // row tile does not change its result.
+  // Row tile i of the list, or (-1) the next that no CTA has taken.  Which CTA computes a row tile does not change its result.
   __device__ void grab(int i, Stretch& st) const {
-    const int qpt = ROWS / a.g, nx = (a.T + qpt - 1) / qpt, HL = a.Hkv * a.n_layers_call, per = a.batch * HL;
-    st.tb = -1;
-    while (true) {
-      if (i < 0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // (the ring's copy clears the count)
-        i = gridDim.x + atomicAdd(a.taken, 1);
-      }
-      if (i >= nx * per) return;
-      Unit n;
-      n.x = nx - 1 - i / per;
-      i %= per;
-      n.b = i / HL;
-      n.hl = i - n.b * HL;
-      n.start = 0;
-      n.cost = 1;
-      if (sh.p0[n.b] >= 0 && take(n, Tiles(sh.p0, a.T, qpt, n, a.W, RNT), 0, 1, 0, st)) return;
-      i = -1;
+    if (i < 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // (the ring's copy clears the count)
+      i = gridDim.x + atomicAdd(a.taken, 1);
     }
+    list().whole(i, st);
+    fill(0, st);
   }
   // the one after it: the next row tiles of the line
   __device__ void follow_up(const Stretch& u, Stretch& st) const {
-    const int qpt = ROWS / a.g, nx = (a.T + qpt - 1) / qpt, HL = a.Hkv * a.n_layers_call;
-    const long long hi = sh.hi;
-    long long y = u.next;
-    int b = u.b, x = u.x, hl = u.hl;
-    st.tb = -1;
-    while (y < hi) {
-      if (++hl == HL) {
-        hl = 0;
-        if (++x == nx) {
-          x = 0;
-          do ++b;
-          while (sh.p0[b] < 0);  // (there is one: the line goes on)
-        }
-      }
-      Unit n;
-      n.b = b;
-      n.x = x;
-      n.hl = hl;
-      n.start = y;
-      n.cost = sh.p0[b] + (long long)(x + 1) * qpt + K0;
-      if (take(n, Tiles(sh.p0, a.T, qpt, n, a.W, RNT), 0, hi, 1, st)) return;
-      y = st.next;
-    }
+    list().follow(u, sh.hi, st);
+    fill(1, st);
   }
-  // A row tile's tiles from ta on, as far as this CTA goes; false: there are none
-  __device__ __forceinline__ bool take(const Unit& u, const Tiles& tl, int ta, long long hi, int slot, Stretch& st) const {
-    st.ta = ta;
-    st.tb = hi >= u.start + u.cost ? tl.n : tl.before(hi - u.start, u.cost);
-    st.rec = st.ta == 0 && st.tb == tl.n ? -1 : 2 * (int)blockIdx.x + slot;
-    st.b = u.b;
-    st.x = u.x;
-    st.hl = u.hl;
-    const int l = u.hl / a.Hkv;
-    st.h = u.hl - l * a.Hkv;
+  // what else the CTA goes by
+  __device__ __forceinline__ void fill(int slot, Stretch& st) const {
+    if (st.tb < 0) return;
+    st.rec = st.ta == 0 && st.tb == st.tl.n ? -1 : 2 * (int)blockIdx.x + slot;
+    const int l = st.hl / a.Hkv;
+    st.h = st.hl - l * a.Hkv;
     st.layer = a.layer0 + l;
-    st.unit = (l * a.batch + u.b) * a.Hkv + st.h;
-    st.p0 = sh.p0[u.b];
-    st.tl = tl;
-    st.next = u.start + u.cost;
-    if (st.ta < st.tb) {
-      if (st.rec >= 0) a.keys[st.rec] = make_int2(st.unit, u.x);
-      return true;
-    }
-    st.tb = -1;
-    return false;
+    st.unit = (l * a.batch + st.b) * a.Hkv + st.h;
+    st.p0 = sh.p0[st.b];
+    if (st.rec >= 0) a.keys[st.rec] = make_int2(st.unit, st.x);
   }
 
   // ---------------------------------------------------------------- queries
@@ -1185,7 +1058,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
     sh.gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const Work work = plan(a, sh.p0, sh.pre, gridDim.x, &sh.whole);
+  plan(a, sh, gridDim.x, K::RNT);
   if (tid == NEXT_WARP * 32) a.keys[2 * blockIdx.x] = a.keys[2 * blockIdx.x + 1] = make_int2(-1, -1);
   // sequences that are not part of the call, or past capacity: zeros
   for (int b = 0; b < a.batch; ++b) {
@@ -1196,7 +1069,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
       for (size_t i = (size_t)blockIdx.x * THREADS + tid; i < per; i += (size_t)gridDim.x * THREADS) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (blockIdx.x >= work.n || work.total() == 0) {
+  if ((int)blockIdx.x >= sh.parts) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // (this grid ends after those before it)
     return;
   }
@@ -1207,7 +1080,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
   __syncthreads();
   fence_after();
   if (tid == NEXT_WARP * 32) {
-    K(a, sh, smem).locate(work, sh.at[0]);
+    K(a, sh, smem).locate(sh.at[0]);
   }
   __syncthreads();
   if (warp < N_SOFT) {
