@@ -3,7 +3,8 @@
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(l_j - m),  l_j = log2(e) / sqrt(128) q.k_j
 //   recorded j:  q.k_j = d_k (q~ . c_j), v_j = d_v H c'_j ...: the codes c are the operands, the two scales of a block of 32
-//   positions never meet them: logits are multiplied by d_k, weights by d_v before they go to P V
+//   positions never meet them: logits are multiplied by d_k, weights by d_v before they go to P V, in their exponents:
+//   w'_j = 2^(l_j + log2 d_v - R), R a row's running reference of these; sum_j w_j has a reference m of its own
 //
 // The products run on the 5th-generation tensor cores (tcgen05.mma, kind::f16, fp32 accumulators in tensor memory).  Codes
 // are exact in one fp16 plane, so a product takes two passes (hi and lo of the queries, or of the weights: 22 bits) where
@@ -22,8 +23,10 @@
 //    sum of its own; four add every tile's P V, which starts from zero, to the output accumulator in registers (the tensor
 //    cores' truncating sums stay within a tile, and a reference that moves rescales registers only); four turn bytes into
 //    operands; one issues the logits' products, one those of the values.  Registers are shared out among them.
-//  * Queries, raw keys and raw values are scaled by powers of two, each vector by its own, and weights against the largest
-//    scale of values so far: fp16 parts keep their bits at any magnitude.
+//  * Queries, raw keys and raw values are scaled by powers of two, each vector by its own, and what is kept to fp16's range is
+//    a weight together with its value's scale, against the row's own largest: fp16 parts keep their bits at any magnitude, and
+//    what a row does not attend to, or hardly, takes none of them.  (One scale for a raw tile, and the largest scale of values
+//    for all rows, lost an early row whose chunk had values 2^40 times larger further on.)
 //  * A kernel's small first-level cache (shared memory takes the rest) makes spilled registers and code that is run once dear: values
 //    for one phase are computed in it (once()), what a row tile does once is done by one group of warps.
 //  * Every wait is bounded; one that runs out flags the status word and the CTA leaves as a whole.
@@ -33,7 +36,6 @@
 // tokens of 8 heads at 1000 positions 35 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
 // 1100: bound by the weights (1500 cycles a tile and group of warps, two groups) and the rate at which instructions come.
 #include <cfloat>
-#include <cstddef>
 
 #include "prefill_list.cuh"
 #include "tc.cuh"
@@ -69,10 +71,11 @@ constexpr uint32_t SMEM = PAGE_OFF + RS * PAGE_SLOT;
 static_assert(V_OFF >= 16384, "raw keys fit too");
 constexpr uint32_t O_STRIDE = (D + 4) * 4;
 static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "what borrows the stages");
-constexpr float BOOST = 4.f;         // log2 of the largest weight over its reference when that is set
-constexpr float RAISE_AT = 9.f;      // ... and how much further it may grow before the reference follows (and 2 for the values' scales: 2^15)
+// References are whole numbers: a factor between two of them is exact.  One is set BOOST to BOOST + 1 below the largest exponent
+// so far and follows when that is RAISE_AT further up: weights stay below 2^15.
+constexpr float BOOST = 4.f, RAISE_AT = 10.f;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
-constexpr int REC = ROWS * D + 2 * ROWS;  // floats of a partial result: O, m, l
+constexpr int REC = ROWS * D + 3 * ROWS;  // floats of a partial result: O, its reference, l, its reference
 
 // Along K, channels (keys) and positions of a tile (values) stand in the order in which 16-byte chunks hold their codes: which
 // of them is at a place, and the place of each
@@ -202,6 +205,17 @@ __device__ __forceinline__ float quad_max(const float (&x)[32]) {
   m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
   return fmaxf(m, __shfl_xor_sync(FULL, m, 2));
 }
+// log2 of a scale, its fraction to 2^-22 whatever its size; -inf of zero
+__device__ __forceinline__ float log2_of(float x) {
+  if (!(x > 0.f) || x == INFINITY) return x > 0.f ? x : x == 0.f ? -INFINITY : x;
+  int e = 0;
+  if (x < FLT_MIN) {
+    x *= 0x1p24f;
+    e = -24;
+  }
+  const uint32_t u = __float_as_uint(x);
+  return (float)(e + (int)(u >> 23) - 127) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
 // eight bf16 values
 __device__ __forceinline__ void unpack8(uint4 w, float* x) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -220,6 +234,13 @@ __device__ __forceinline__ void take_registers() {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 2^n / l, the factor from sums to outputs (n: between the references of the two sums)
+__device__ __forceinline__ float share_of(float n, float l) {
+  if (!(l > 0.f) || !(n > -INFINITY)) return 0.f;
+  const float h = floorf(0.5f * n);  // (the sum of weights may be as far from 1 as the factor)
+  return ex2(h) / l * ex2(n - h);
+}
+
 template <bool BF16>
 struct Kernel {
   static constexpr int ROW_BYTES = D * (BF16 ? 2 : 4);  // of a raw vector of the call
@@ -230,17 +251,17 @@ struct Kernel {
 
   // shared by the CTA, besides the stages
   struct Shared {
-    uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], sfull[2], pfull[2], pvdone[2], ofree[2], done[2], rfull[RS], rempty[RS], begun[4], most;
+    uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], sfull[2], pfull[2], pvdone[2], ofree[2], done[2], rfull[RS], rempty[RS], begun[4];
     uint32_t tmem;
     int gone;
     float qscale[ROWS], qraw[ROWS];        // powers of two that the queries were divided by
-    float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' references and sums, the output's reference, at the end
-    float mt[4][ROWS], vt[4], vt0[4];              // a tile's references: of its weights, of its values' scales
+    float m[2][ROWS], l[2][ROWS], M[ROWS]; // both groups' sums and their references, the output's reference, at the end
+    float mt[4][ROWS];                     // a tile's references of its weights
     long long hi;                          // where the CTA's stretch of the cost line ends
     int whole, parts, n_act;               // row tiles are taken whole; CTAs that have work; sequences of the call
     int halves[RS];                        // of a page under way that are read (0: there is no such page)
-    float2 scale[8][2];                    // (keys', values') of a tile's two blocks; of a raw tile: its powers of two
-    float warp_most[2][N_DQ];              // largest magnitude of a raw tile's keys, values, in each operand warp
+    alignas(16) float4 blk[8][2];          // of a recorded tile's two blocks: the keys' scale, log2 of the values', both again
+    alignas(16) float2 col[8][NT];         // of a raw tile's positions: the keys' power of two, log2 of the values'
     alignas(16) float signs[D];            // (read four at a time)
     int p0[MAX_BATCH];
     unsigned short act[MAX_BATCH];
@@ -248,14 +269,14 @@ struct Kernel {
     Stretch at[2];                         // this stretch and the next
   };
 
-  static_assert(offsetof(Shared, signs) % 16 == 0 && alignof(Shared) % 16 == 0, "read as float4");
+  static_assert(alignof(Shared) % 16 == 0, "parts of it are read as float4");
 
   const PrefillArgs& a;
   Shared& sh;
   uint8_t* smem;
   int warp, lane;
   uint32_t tmem;
-  int gt = 0, gr = 0, gb = 0, gm = 0;  // tiles so far, those among them with pages, stretches of two tiles or more, raw operands
+  int gt = 0, gr = 0, gb = 0;  // tiles so far, slots of pages and raw operands, stretches of two tiles or more
 
   // Made within each role: nothing is then live where the roles part and their registers are shared out (a value that is
   // takes a register that the smallest share has, or memory)
@@ -536,9 +557,12 @@ struct Kernel {
       const uint8_t* pg = smem + PAGE_OFF + rs * PAGE_SLOT + dw * 512 + lane * 16;
       if (!held(&sh.rfull[rs], (gr / RS) & 1)) return;
       if (gt >= NS && !held(&sh.kempty[s], before)) return;
-      if (dw == 0 && lane < 2)
-        sh.scale[gt & 7][lane] = lane < sh.halves[rs] ? *reinterpret_cast<const float2*>(smem + PAGE_OFF + rs * PAGE_SLOT + lane * (PAGE_SLOT / 2) + 8192)
-                                                      : make_float2(0.f, 0.f);
+      if (dw == 0 && lane < 2) {
+        const float2 d = lane < sh.halves[rs] ? *reinterpret_cast<const float2*>(smem + PAGE_OFF + rs * PAGE_SLOT + lane * (PAGE_SLOT / 2) + 8192)
+                                              : make_float2(0.f, 0.f);
+        const float e = log2_of(d.y);
+        sh.blk[gt & 7][lane] = make_float4(d.x, e, d.x, e);
+      }
       // chunk 4 mt + p (p = dw, mt = q & 1) of block q >> 1: tokens 16 mt + r and + 8, channels of K-group 4 p + i
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -583,9 +607,9 @@ struct Kernel {
     }
   }
   // Raw keys (K-major) or values (N-major: rows are positions too, in the order of the places) of positions j0 .. as operand
-  // planes, over a power of two of the tile: FULL: hi and lo of FULL_NT positions, else one of RNT of the call's own bf16 ones.
-  // An element of a bf16 vector that its one fp16 plane does not hold exactly is below 2^-14 of the tile's largest and off by
-  // 2^-25 of that at most.
+  // planes, each vector over a power of two of its own: FULL: hi and lo of FULL_NT positions, else one of RNT of the call's own
+  // bf16 ones.  An element of a bf16 vector that its one fp16 plane does not hold exactly is below 2^-14 of the vector's largest
+  // and off by 2^-25 of that at most.
   template <bool FULL>
   __device__ __forceinline__ bool raw(const Stretch& u, int j0, uint8_t* plane, int values) {
     // the lane's q-th eight channels are group 4 ((q + r / 4) mod 4) + (i + r) mod 4: eight lanes' reads of a slot hit all banks
@@ -638,9 +662,10 @@ struct Kernel {
         *reinterpret_cast<uint4*>(x + 4) = w[n][(2 * q + 1) % WORDS];
       }
     };
-    float m = 0.f;
+    float most[ROUNDS];  // of each vector (the lanes of r have one)
 #pragma unroll
-    for (int n = 0; n < ROUNDS; ++n)
+    for (int n = 0; n < ROUNDS; ++n) {
+      float m = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
@@ -648,24 +673,18 @@ struct Kernel {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) m = max3(m, fabsf(x[e]), fabsf(x[e + 1]));
       }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-    if (lane == 0) {
-      sh.warp_most[values][dw] = m;
-      bar_arrive(&sh.most);
-      if (staged) bar_arrive(&sh.rempty[slot]);
+      m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+      most[n] = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
     }
+    if (lane == 0 && staged) bar_arrive(&sh.rempty[slot]);
     gr += staged;
-    if (!held(&sh.most, gm++ & 1)) return false;
-#pragma unroll
-    for (int o = 0; o < N_DQ; ++o) m = fmaxf(m, sh.warp_most[values][o]);
-    float inv;
-    const float s2 = pow2_of(m, inv);
-    if (dw == 0 && lane < 2) reinterpret_cast<float*>(&sh.scale[gt & 7][lane])[values] = s2;
 #pragma unroll
     for (int n = 0; n < ROUNDS; ++n) {
       const int t = 8 * dw + r + 8 * N_DQ * n, k = place_of(t);
       uint8_t* to = plane + (values ? (k >> 3) * V_LEAD + (k & 7) * 16 : (uint32_t)((t >> 3) * 128 + (t & 7) * 16));
+      float inv;
+      const float s2 = pow2_of(most[n], inv);
+      if (lane < 8) reinterpret_cast<float*>(&sh.col[gt & 7][t])[values] = values ? (float)((int)(__float_as_uint(s2) >> 23) - 127) : s2;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
@@ -684,51 +703,65 @@ struct Kernel {
 
   // ---------------------------------------------------------------- softmax
   struct Row {
-    float m, l;  // the weights' reference and their sum, of this group's tiles
-    float vref;  // power of two that the values' scales are held against
-    // its inverse (0 before there is one)
-    __device__ __forceinline__ float rvref() const { return vref > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.f; }
+    float m, l;  // the reference of the weights' sum, that sum, of this group's tiles
+    float R;     // the reference of the weights with their values' scales
   };
-  // a larger logit or a larger scale of values than the references allow for
-  __device__ __forceinline__ void follow(Row& w, float mx, float vmax) {
+  // a larger logit, or logit with its value's scale, than the references allow for
+  __device__ __forceinline__ void follow(Row& w, float mx, float rx) {
     if (mx > w.m + (BOOST + RAISE_AT)) {
-      const float mnew = mx - BOOST;
+      const float mnew = floorf(mx) - BOOST;
       w.l = w.m == -INFINITY ? w.l : w.l * ex2(w.m - mnew);
       w.m = mnew;
     }
-    float inv;
-    if (vmax > 4.f * w.vref) w.vref = pow2_of(vmax, inv);
+    if (rx > w.R + (BOOST + RAISE_AT)) w.R = floorf(rx) - BOOST;
   }
-  // The largest logit of a tile; MASKED: some row does not attend to all of it, but to columns first .. last
-  template <bool MASKED>
-  __device__ __forceinline__ float top_of(uint32_t sa, const float (&dk)[2], int first, int last) {
-    float mx = -INFINITY;
+  // The largest logit of a tile that every row attends to as a whole, and that of logits with their values' scales
+  __device__ __forceinline__ void top_of(uint32_t sa, const float (&dk)[2], const float (&lv)[2], float& mx, float& rx) {
+    mx = rx = -INFINITY;
 #pragma unroll
     for (int c0 = 0; c0 < NT; c0 += 32) {
       float t = -INFINITY, v[32];
       tm_ld32(sa + c0, v);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        if (MASKED) {
-          if (c0 + i < first || c0 + i > last) v[i] = -INFINITY;
-          if (c0 + i + 1 < first || c0 + i + 1 > last) v[i + 1] = -INFINITY;
-        }
-        t = max3(t, v[i], v[i + 1]);
-      }
-      // (a block of which nothing is attended to may have a scale of zero)
-      if (!MASKED || t > -INFINITY) mx = fmaxf(mx, t * dk[c0 >> 5]);
+      for (int i = 0; i < 32; i += 2) t = max3(t, v[i], v[i + 1]);
+      t *= dk[c0 >> 5];
+      mx = fmaxf(mx, t);
+      rx = fmaxf(rx, t + lv[c0 >> 5]);
     }
-    return mx;
   }
-  // Its weights, each with its value's scale f (over vref) in the exponent: w' = 2^(l - m + log2 f); the sum of weights
-  // over a block is that of the w' over f.  (An f of zero, or so small that its w' are below fp16's smallest number,
-  // counts as 2^-42.)  A weight's hi part is its upper 11 bits, cut, lo the rest rounded to 11.
-  template <bool MASKED>
-  __device__ __forceinline__ void weigh(Row& w, uint32_t sa, const float (&dk)[2], const float (&dv)[2], int first, int last) {
-    const float m0 = w.m == -INFINITY ? 0.f : w.m;
+  // ... of columns first .. last of any other tile of nt, whose scales of columns c, c + 1 are at[(c >> 5) half + (c / 2 mod 16) step]
+  __device__ __forceinline__ void top_of(uint32_t sa, const float4* at, int half, int step, int nt, float qs, int first, int last, float& mx, float& rx) {
+    mx = rx = -INFINITY;
+#pragma unroll 1
+    for (int c0 = 0; c0 < nt; c0 += 32, at += half) {
+      float v[32];
+      tm_ld32(sa + c0, v);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float4 s = at[step * (i / 2)];
+        float x = v[i] * (s.x * qs), y = v[i + 1] * (s.z * qs);
+        if (c0 + i < first || c0 + i > last) x = -INFINITY;
+        if (c0 + i + 1 < first || c0 + i + 1 > last) y = -INFINITY;
+        mx = max3(mx, x, y);
+        rx = max3(rx, x + s.y, y + s.w);
+      }
+    }
+  }
+  // fp16 hi and lo of weights: hi is a weight's upper 11 bits, cut, lo the rest rounded to 11
+  __device__ __forceinline__ static void halves_of(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
+    sub2(x, y, hx, hy);
+    hi = h2u(__floats2half2_rn(hx, hy));
+    lo = h2u(__floats2half2_rn(x, y));
+  }
+  // The weights of a tile that a row attends to as a whole, each with its value's scale in the exponent: w' = 2^(l + lv - R); the
+  // sum of a block's weights over 2^m is that of the w' times 2^(R - m - lv).  (A scale so small that its w' would be below 2^-80
+  // counts as that: fp16 has no such numbers, but the sum does.)
+  __device__ __forceinline__ void weigh(Row& w, uint32_t sa, const float (&dk)[2], const float (&lv)[2]) {
+    const float R = w.R == -INFINITY ? w.m : w.R, Rm = R - w.m;
 #pragma unroll 1
     for (int c0 = 0; c0 < NT; c0 += 32) {
-      const float f = fmaxf((c0 ? dv[1] : dv[0]) * w.rvref(), 0x1p-42f), k = c0 ? dk[1] : dk[0], b = __log2f(f) - m0;
+      const float f = fmaxf(c0 ? lv[1] : lv[0], Rm - 100.f), k = c0 ? dk[1] : dk[0], b = f - R;
       float s0 = 0.f, s1 = 0.f, v[32];
       tm_ld32(sa + c0, v);
       // K-step by K-step of P V, in the order of the places
@@ -740,24 +773,44 @@ struct Kernel {
           const int c = at_place(16 * ks + 2 * e);
           float x = v[c], y = v[c + 1];
           fma2(x, y, k, k, b, b);
-          x = ex2(MASKED && (c0 + c < first || c0 + c > last) ? -INFINITY : x);
-          y = ex2(MASKED && (c0 + c + 1 < first || c0 + c + 1 > last) ? -INFINITY : y);
+          x = ex2(x);
+          y = ex2(y);
           add2(s0, s1, x, y);
-          const float hx = __uint_as_float(__float_as_uint(x) & 0xffffe000u), hy = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
-          sub2(x, y, hx, hy);
-          pw[e] = h2u(__floats2half2_rn(hx, hy));
-          pw[8 + e] = h2u(__floats2half2_rn(x, y));
+          halves_of(x, y, pw[e], pw[8 + e]);
         }
         tm_st16(sa + c0 + 16 * ks, pw);
       }
-      w.l += __fdividef(s0 + s1, f);
+      w.l += (s0 + s1) * ex2(Rm - f);
     }
   }
-  // a tile's references, for whoever adds its P V
-  __device__ __forceinline__ void leave(const Row& w, int row) {
-    sh.mt[gt & 3][row] = w.m;
-    if (row == 0) sh.vt[gt & 3] = w.vref;
+  // ... of any other tile (scales as for top_of): weights and their sum each by its own exponent
+  __device__ __forceinline__ void weigh(Row& w, uint32_t sa, const float4* at, int half, int step, int nt, float qs, int first, int last) {
+    const float m0 = w.m == -INFINITY ? 0.f : w.m, R = w.R == -INFINITY ? m0 : w.R;
+#pragma unroll 1
+    for (int c0 = 0; c0 < nt; c0 += 32, at += half) {
+      float s0 = 0.f, s1 = 0.f, v[32];
+      tm_ld32(sa + c0, v);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = at_place(16 * ks + 2 * e);
+          const float4 s = at[step * (c / 2)];
+          const bool ox = c0 + c < first || c0 + c > last, oy = c0 + c + 1 < first || c0 + c + 1 > last;
+          float x = v[c] * (s.x * qs), y = v[c + 1] * (s.z * qs);
+          add2(s0, s1, ex2(ox ? -INFINITY : x - m0), ex2(oy ? -INFINITY : y - m0));
+          x = ex2(ox ? -INFINITY : x + (s.y - R));
+          y = ex2(oy ? -INFINITY : y + (s.w - R));
+          halves_of(x, y, pw[e], pw[8 + e]);
+        }
+        tm_st16(sa + c0 + 16 * ks, pw);
+      }
+      w.l += s0 + s1;
+    }
   }
+  // a tile's reference, for whoever adds its P V
+  __device__ __forceinline__ void leave(const Row& w, int row) { sh.mt[gt & 3][row] = w.R; }
   // its weights are in tensor memory
   __device__ __forceinline__ void hand_over(int grp) {
     tm_wait_st();
@@ -771,7 +824,7 @@ struct Kernel {
     const uint32_t sa = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C_S + NT * grp;
     // rows past the last query go along with it (and are not written)
     const int P = min(u.p0 + u.tl.t0 + row / a.g, u.tl.Pmax);
-    Row w = {-INFINITY, 0.f, 0.f};
+    Row w = {-INFINITY, 0.f, -INFINITY};
     const int first = u.ta + ((gt & 1) != grp), left = u.tb - u.ta;
     gt += first - u.ta;
     int it = first;
@@ -779,56 +832,56 @@ struct Kernel {
     while (it < u.tb) {
       // recorded tiles that every row attends to as a whole
       bool rec = false;
-      float dk[2], dv[2];
+      float mx, rx;
       const int hi = P - a.W;  // the last recorded position that is attended to, as long as it is there
 #pragma unroll 1
       for (; it < u.tb; it += 2, gt += 2) {
         if (!held(&sh.sfull[grp], (gt >> 1) & 1)) return;
         fence_after();
         rec = it < u.tl.nqt;
-        const float2 s0 = sh.scale[gt & 7][0], s1 = sh.scale[gt & 7][1];
-        const float qs = sh.qscale[row];
-        dk[0] = s0.x * qs;
-        dk[1] = s1.x * qs;
-        dv[0] = s0.y;
-        dv[1] = s1.y;
+        const float4 s0 = sh.blk[gt & 7][0], s1 = sh.blk[gt & 7][1];
         // (the first tiles share references, and a page that is not there has scales of zero: below)
-        if (!__all_sync(FULL, rec && it > u.ta + 1 && it * NT + NT - 1 <= hi && fmaxf(s0.y, s1.y) > 0.f)) break;
-        follow(w, top_of<false>(sa, dk, 0, 0), fmaxf(s0.y, s1.y));
+        if (!__all_sync(FULL, rec && it > u.ta + 1 && it * NT + NT - 1 <= hi && fmaxf(s0.y, s1.y) > -INFINITY)) break;
+        const float qs = sh.qscale[row], dk[2] = {s0.x * qs, s1.x * qs}, lv[2] = {s0.y, s1.y};
+        top_of(sa, dk, lv, mx, rx);
+        follow(w, mx, rx);
         leave(w, row);
-        weigh<false>(w, sa, dk, dv, 0, 0);
+        weigh(w, sa, dk, lv);
         hand_over(grp);
       }
       if (it >= u.tb) break;
       // any other tile: columns first .. last are attended to
-      int first, last;
+      int first, last, half = 1, step = 0, nt = NT;
+      const float4* at = sh.blk[gt & 7];
+      float qs;
       if (rec) {
         first = 0;
         last = page_bad(u, it) ? -1 : hi - it * NT;
+        qs = sh.qscale[row];
       } else {
-        if (!held(&sh.vfull[gt % NS], (gt / NS) & 1)) return;  // (both its powers of two are there)
-        const float2 s0 = sh.scale[gt & 7][0];
-        dk[0] = dk[1] = s0.x * sh.qraw[row];
-        dv[0] = dv[1] = s0.y;
+        if (!held(&sh.vfull[gt % NS], (gt / NS) & 1)) return;  // (all its powers of two are there)
+        at = reinterpret_cast<const float4*>(sh.col[gt & 7]);
+        half = NT / 4;
+        step = 1;
+        qs = sh.qraw[row];
         const int r = it - u.tl.nqt, j0 = u.tl.raw_at(r, RNT);
         first = hi + 1 - j0;
-        last = min(P - j0, (BF16 && r >= u.tl.n_full ? RNT : FULL_NT) - 1);
+        nt = BF16 && r >= u.tl.n_full ? RNT : FULL_NT;
+        last = min(P - j0, nt - 1);
       }
-      const float mx = top_of<true>(sa, dk, first, last);
-      // The second group begins with the first one's references: as long as neither moves, their parts add up as they are.
+      top_of(sa, at, half, step, nt, qs, first, last, mx, rx);
+      // The second group begins with the first one's reference: as long as neither moves, their parts add up as they are.
       if (it == u.ta + 1) {
         if (!held(&sh.begun[warp & 3], gb & 1)) return;
-        w.m = sh.mt[(gt - 1) & 3][row];
-        w.vref = sh.vt0[warp & 3];
+        w.R = sh.mt[(gt - 1) & 3][row];
       }
-      follow(w, mx, fmaxf(dv[0], dv[1]));
+      follow(w, mx, rx);
       leave(w, row);
       if (it == u.ta && left > 1) {
-        if (lane == 0) sh.vt0[warp & 3] = w.vref;
         __syncwarp();
         if (lane == 0) bar_arrive(&sh.begun[warp & 3]);
       }
-      weigh<true>(w, sa, dk, dv, first, last);
+      weigh(w, sa, at, half, step, nt, qs, first, last);
       hand_over(grp);
       it += 2;
       gt += 2;
@@ -880,14 +933,14 @@ struct Kernel {
     __syncwarp();
     if (lane == 0) bar_arrive(&sh.ofree[gt & 1]);
   }
-  // acc 2^M V is the sum of weights times values so far, of both groups' tiles
+  // acc 2^M is the sum of weights times values so far, of both groups' tiles
   __device__ void sums(const Stretch& u) {
     const int row = 32 * (warp & 3) + lane;
     const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C_O;
     float acc[D];
 #pragma unroll
     for (int i = 0; i < D; ++i) acc[i] = 0.f;
-    float M = -INFINITY, V = 0.f;
+    float M = -INFINITY;
     int it = u.ta;
     // recorded tiles, then raw ones
 #pragma unroll 1
@@ -895,15 +948,14 @@ struct Kernel {
       const int end = part ? u.tb : min(u.tb, u.tl.nqt);
 #pragma unroll 1
       while (it < end) {
-        float m, v;
+        float m;
         // tiles under the references of those before
 #pragma unroll 1
         for (; it < end; ++it, ++gt) {
           if (!held(&sh.pvdone[gt & 1], (gt >> 1) & 1)) return;
           fence_after();
           m = sh.mt[gt & 3][row];
-          v = sh.vt[gt & 3];
-          if (__any_sync(FULL, m != M || v != V)) break;
+          if (__any_sync(FULL, m != M)) break;
           const uint32_t oa = at + D * (gt & 1);
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -915,11 +967,10 @@ struct Kernel {
           free_output();
         }
         if (it >= end) break;
-        const float Mn = fmaxf(M, m), Vn = fmaxf(V, v), rv = Vn > 0.f ? 1.f / Vn : 0.f;
+        const float Mn = fmaxf(M, m);
         // (where nothing was attended to the part is zero)
-        const float fa = (M == -INFINITY ? 1.f : ex2(M - Mn)) * (V * rv), fo = (m == -INFINITY ? 1.f : ex2(m - Mn)) * (v * rv);
+        const float fa = M == -INFINITY ? 1.f : ex2(M - Mn), fo = m == -INFINITY ? 1.f : ex2(m - Mn);
         M = Mn;
-        V = Vn;
         const uint32_t oa = at + D * (gt & 1);
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -940,7 +991,7 @@ struct Kernel {
     // (no operand is in use any more: every product of the stretch has been waited for)
     float* o = reinterpret_cast<float*>(smem + (size_t)row * O_STRIDE);
 #pragma unroll
-    for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(acc[i] * V, acc[i + 1] * V, acc[i + 2] * V, acc[i + 3] * V);
+    for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     sh.M[row] = M;
   }
   // rows to the output, or to a partial result: lane i & 15 knows of the warp's i-th row, then all write each row
@@ -952,17 +1003,18 @@ struct Kernel {
     if (row < nrows) {
       const float M = sh.M[row], m0 = sh.m[0][row], m1 = sh.m[1][row];
       // (alike whichever group had the first tile)
-      const float l = __fadd_rn(__fmul_rn(sh.l[0][row], m0 == -INFINITY ? 1.f : ex2(m0 - M)),
-                                __fmul_rn(sh.l[1][row], m1 == -INFINITY ? 1.f : ex2(m1 - M)));
+      const float m = fmaxf(m0, m1), l = __fadd_rn(__fmul_rn(sh.l[0][row], m0 == -INFINITY ? 1.f : ex2(m0 - m)),
+                                                   __fmul_rn(sh.l[1][row], m1 == -INFINITY ? 1.f : ex2(m1 - m)));
       if (u.rec >= 0) {
         if (lane < 16) {
           dst[ROWS * D + row] = M;
           dst[ROWS * D + ROWS + row] = l;
+          dst[ROWS * D + 2 * ROWS + row] = m;
         }
         f = 1.f;
         dst += row * D;
       } else {
-        f = l > 0.f ? 1.f / l : 0.f;
+        f = share_of(M - m, l);
         dst = a.out + (((size_t)u.unit * g + row % g) * a.T + u.tl.t0 + row / g) * D;
       }
     }
@@ -1043,7 +1095,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_block_kernel(const __grid_
       bar_init(&sh.vempty[s], 1);
     }
     for (int i = 0; i < 4; ++i) bar_init(&sh.begun[i], 1);
-    bar_init(&sh.most, N_DQ);
     for (int i = 0; i < RS; ++i) {
       bar_init(&sh.rfull[i], 1);
       bar_init(&sh.rempty[i], N_DQ);
@@ -1129,27 +1180,35 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) prefill_join_kernel(const __g
   if (part[0] < 2 * (int)blockIdx.x) return;
   const int t0 = key.y * qpt, row = blockIdx.y * JOIN_WARPS + warp;
   if (row >= min(qpt, a.T - t0) * g) return;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.parts + (size_t)part[i] * REC + ROWS * D + row));
+  float M = -INFINITY, m = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float* rec = a.parts + (size_t)part[i] * REC + ROWS * D + row;
+    M = fmaxf(M, __ldcg(rec));
+    m = fmaxf(m, __ldcg(rec + 2 * ROWS));
+  }
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+  for (int o = 16; o >= 1; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+  }
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const float* rec = a.parts + (size_t)part[i] * REC;
-    const float m = __ldcg(rec + ROWS * D + row), li = __ldcg(rec + ROWS * D + ROWS + row);
+    const float* refs = rec + ROWS * D + row;
+    const float Mi = __ldcg(refs), li = __ldcg(refs + ROWS), mi = __ldcg(refs + 2 * ROWS);
     const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + row * D) + lane);
-    const float f = m == -INFINITY ? 0.f : ex2(m - M);
-    l += li * f;
+    const float f = Mi == -INFINITY ? 0.f : ex2(Mi - M);
+    l += li * (mi == -INFINITY ? 0.f : ex2(mi - m));
     o.x += x.x * f;
     o.y += x.y * f;
     o.z += x.z * f;
     o.w += x.w * f;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float f = share_of(M - m, l);
   *reinterpret_cast<float4*>(a.out + (((size_t)key.x * g + row % g) * a.T + t0 + row / g) * D + 4 * lane) =
-      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 }
 
 template <bool BF16>

@@ -1,0 +1,170 @@
+"""Prefill over KVQ_Q8B32 caches, row by row: what a query does not attend to, or hardly, costs its output no bits.
+
+The error of a row (one query of one head) is measured against S = sum_j p_j rms(v_j), p its weights: RMS over the 128
+channels, which a rotation keeps.  Bound, before any run, with A = max_j |q| |k_j| log2(e) / sqrt(128) over the attended j:
+
+  a logit is off by A (2 * 2^-22 (operands of 22 bits) + 24 * 2^-23 (up to 24 truncated sums, each below A)) and by 2^-18
+  (exponents of up to 64, rounded twice in float): dl; a weight by ln 2 dl, an average of values by twice that;
+  the products with the values: their weights and values have 22 bits, 24 truncated sums: 2 * 2^-22 + 24 * 2^-23, and as
+  much again for float sums over tiles and the rotation back;
+  weights below the largest's 2^-29 are rounded to multiples of 2^-28 of the largest, n of them: n 2^-28.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from . import block_reference as br
+from . import harness
+from .test_gpu_block8 import _i32
+
+pytestmark = pytest.mark.gpu
+
+LOG2E = 1.4426950408889634
+SUMS = 2 * 2.0 ** -22 + 24 * 2.0 ** -23
+
+
+def _rows(ref, b, j, q, p, t):
+    """(output, S, A, n) in 64 bits of one query (head j, token t of a chunk at p)."""
+    h = j // (ref.cfg.n_q_heads // ref.cfg.n_kv_heads)
+    L = p + t + 1
+    m = max(0, L - ref.cfg.window)
+    k, v = (np.concatenate([ref.records(s, 0, b, h, m), ref.raw[s][0, b, h, m:L].astype(np.float64)]) for s in range(2))
+    q = q.astype(np.float64)
+    lg = k @ q / np.sqrt(128.0)
+    w = np.exp(lg - lg.max())
+    w /= w.sum()
+    A = np.linalg.norm(q) * np.linalg.norm(k, axis=1).max() * LOG2E / np.sqrt(128.0)
+    return w @ v, w @ np.sqrt((v * v).mean(1)), A, L
+
+
+def _check(out, ref, b, q, p, ts, typical=None):
+    """Every head's row of the tokens ts."""
+    errs = []
+    for j in range(q.shape[1]):
+        for t in ts:
+            want, S, A, n = _rows(ref, b, j, q[b, j, t], p, t)
+            err = np.sqrt(((out[b, j, t] - want) ** 2).mean())
+            tol = 2 * np.log(2) * (A * SUMS + 2.0 ** -18) + 2 * SUMS + n * 2.0 ** -28
+            assert err <= tol * S + 1e-37, (j, t, err / S, tol)
+            errs.append(err / S)
+    if typical is not None:
+        assert np.median(errs) <= typical, np.median(errs)
+    return errs
+
+
+def _to(x, in_dtype):
+    return torch.as_tensor(np.asarray(x, np.float32)).to(torch.bfloat16 if in_dtype == "bf16" else torch.float32).contiguous()
+
+
+def _prefill(gpu, ref, k, v, q, p):
+    out = gpu.prefill(0, k.cuda(), v.cuda(), q.cuda(), _i32([p])).double().cpu().numpy()
+    assert gpu.status() == 0
+    ref.append(0, harness.to_np(k), harness.to_np(v), [p])
+    return out
+
+
+def _normal(rng, h, T):
+    return rng.standard_normal((1, h, T, 128))
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("p,T,window", [(0, 300, 128), (1000, 90, 64), (517, 1, 100), (3000, 40, 128)])
+def test_both_planes_of_every_product(in_dtype, p, T, window):
+    """Peaked attention (logits of 9 and more): weights feel the last bits of queries and keys.  Logits of about 9 are off by
+    24 * 2^-23 * 9 = 2.6e-5 at most, a third of it on average, and half of that cancels between weight and sum: 2e-5 is
+    kept by the median row, where queries, weights or float values without their lower parts (2^-12 each) give 1e-4."""
+    rng = np.random.default_rng(p + T)
+    gpu, ref = br.make(1, 2, 8, 1, p + T, window=window, in_dtype=in_dtype)
+    if p:
+        k, v = (_to(_normal(rng, 2, p), in_dtype) for _ in range(2))
+        gpu.append(0, k.cuda(), v.cuda(), _i32([0]))
+        ref.append(0, harness.to_np(k), harness.to_np(v), [0])
+    k, v, q = _to(_normal(rng, 2, T), in_dtype), _to(_normal(rng, 2, T), in_dtype), _to(3 * _normal(rng, 8, T), in_dtype)
+    out = _prefill(gpu, ref, k, v, q, p)
+    _check(out, ref, 0, harness.to_np(q), p, sorted({0, T // 3, T // 2, T - 1}), typical=2e-5)
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["values", "keys", "both"])
+@pytest.mark.parametrize("size", [2.0 ** 16, 2.0 ** 40, 2.0 ** -30])
+@pytest.mark.parametrize("p", [0, 77])
+def test_later_tokens_take_no_bits(in_dtype, what, size, p):
+    """A later token of the chunk, masked for the queries before it, is far larger or smaller than they."""
+    rng = np.random.default_rng(41)
+    T = 60
+    gpu, ref = br.make(1, 1, 4, 1, 300, window=64, in_dtype=in_dtype)
+    if p:
+        k, v = (_to(_normal(rng, 1, p), in_dtype) for _ in range(2))
+        gpu.append(0, k.cuda(), v.cuda(), _i32([0]))
+        ref.append(0, harness.to_np(k), harness.to_np(v), [0])
+    k, v, q = (_normal(rng, h, T) for h in (1, 1, 4))
+    for t in (20, 41):
+        if what != "keys":
+            v[:, :, t] *= size
+        if what != "values" and size < 2.0 ** 30:
+            k[:, :, t] *= size
+    k, v, q = (_to(x, in_dtype) for x in (k, v, q))
+    out = _prefill(gpu, ref, k, v, q, p)
+    ts = [t for t in range(T) if what == "values" or t < 20]     # (logits of 2^16 behind it: the bound says nothing)
+    _check(out, ref, 0, harness.to_np(q), p, ts)
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e8])
+@pytest.mark.parametrize("where", ["window", "chunk", "block", "first"])
+def test_large_values_of_next_to_no_weight(in_dtype, size, where):
+    """Tokens with values `size` times larger, whose logits are so low that even so they count for 1e-3 of the output; a sink
+    and thousands of equal weights 12 powers of two below it, whose values are the small ones."""
+    rng = np.random.default_rng(42)
+    p, T, W = 5000, 30, 64
+    gpu, ref = br.make(1, 1, 4, 1, p + T, window=W, in_dtype=in_dtype)
+    d = rng.standard_normal(128)
+    d /= np.linalg.norm(d)
+    unit = np.sqrt(128.0) / LOG2E                       # a key of x unit d has a logit of x (base 2) under the query d
+    k, v = 0.02 * rng.standard_normal((p + T, 128)), 1 + 0.1 * rng.standard_normal((p + T, 128))
+    k[10] += 12 * unit * d
+    v[10] *= -1
+    at = {"window": range(p - 40, p - 20), "chunk": range(p + 3, p + 9), "block": range(2048, 2080), "first": range(64, 96)}[where]
+    low = np.log2(size * 1e3)
+    for i in at:
+        k[i] = 0.02 * rng.standard_normal(128) - low * unit * d
+        v[i] = size * rng.standard_normal(128)
+    q = np.broadcast_to(d, (1, 4, T, 128)) * (1 + 0.01 * rng.standard_normal((1, 4, T, 1)))
+    k, v, q = (_to(x, in_dtype) for x in (k[None, None], v[None, None], q))
+    old, new = (x[:, :, :p].contiguous() for x in (k, v)), [x[:, :, p:].contiguous() for x in (k, v)]
+    old = list(old)
+    gpu.append(0, old[0].cuda(), old[1].cuda(), _i32([0]))
+    ref.append(0, harness.to_np(old[0]), harness.to_np(old[1]), [0])
+    out = _prefill(gpu, ref, new[0], new[1], q, p)
+    _check(out, ref, 0, harness.to_np(q), p, [0, 5, 15, T - 1])
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_values_that_grow_and_shrink(in_dtype):
+    """Every token's values (and some blocks') have a size of their own, over 2^60: each row is what its weights make of it."""
+    rng = np.random.default_rng(43)
+    p, T, W = 700, 140, 96
+    gpu, ref = br.make(1, 1, 4, 1, p + T, window=W, in_dtype=in_dtype)
+    k = rng.standard_normal((p + T, 128))
+    size = 2.0 ** rng.integers(-30, 31, p + T)
+    size[:p // 32 * 32] = np.repeat(2.0 ** rng.integers(-30, 31, p // 32), 32)
+    size[64:128] = 0
+    v = rng.standard_normal((p + T, 128)) * size[:, None]
+    k, v, q = (_to(x, in_dtype) for x in (k[None, None], v[None, None], _normal(rng, 4, T)))
+    gpu.append(0, k[:, :, :p].contiguous().cuda(), v[:, :, :p].contiguous().cuda(), _i32([0]))
+    ref.append(0, harness.to_np(k[:, :, :p]), harness.to_np(v[:, :, :p]), [0])
+    out = _prefill(gpu, ref, k[:, :, p:].contiguous(), v[:, :, p:].contiguous(), q, p)
+    _check(out, ref, 0, harness.to_np(q), p, [0, 1, 30, 31, 64, 100, T - 1])
+
+
+def test_values_of_zero_and_then_not():
+    """Rows whose first positions all have values of zero, and one that attends to nothing else."""
+    rng = np.random.default_rng(44)
+    gpu, ref = br.make(1, 1, 4, 1, 600, window=32, in_dtype="f32")
+    k, v = rng.standard_normal((1, 1, 500, 128)), rng.standard_normal((1, 1, 500, 128))
+    v[:, :, :320] = 0
+    k, v, q = (_to(x, "f32") for x in (k, v, _normal(rng, 4, 500)))
+    out = _prefill(gpu, ref, k, v, q, 0)
+    assert (out[:, :, :320] == 0).all()
+    _check(out, ref, 0, harness.to_np(q), 0, [320, 321, 352, 383, 384, 499])
