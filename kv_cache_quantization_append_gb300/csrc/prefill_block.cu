@@ -179,6 +179,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// (NaN if one is)
+__device__ __forceinline__ float max3nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // A warp's bounded wait.  false: this CTA gives up (a wait elsewhere ran out, or this one: flagged).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gone, unsigned* status) {
   bool ok = bar_try(bar, parity);
@@ -663,6 +669,7 @@ struct Kernel {
       }
     };
     float most[ROUNDS];  // of each vector (the lanes of r have one)
+    unsigned sick = 0;   // those that are not finite
 #pragma unroll
     for (int n = 0; n < ROUNDS; ++n) {
       float m = 0.f;
@@ -671,10 +678,11 @@ struct Kernel {
         float x[8];
         eight(n, q, x);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) m = max3(m, fabsf(x[e]), fabsf(x[e + 1]));
+        for (int e = 0; e < 8; e += 2) m = max3nan(m, fabsf(x[e]), fabsf(x[e + 1]));
       }
-      m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
-      most[n] = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+      m = max3nan(m, m, __shfl_xor_sync(FULL, m, 8));
+      most[n] = max3nan(m, m, __shfl_xor_sync(FULL, m, 16));
+      if (!(most[n] < INFINITY)) sick |= 1u << n;
     }
     if (lane == 0 && staged) bar_arrive(&sh.rempty[slot]);
     gr += staged;
@@ -684,7 +692,9 @@ struct Kernel {
       uint8_t* to = plane + (values ? (k >> 3) * V_LEAD + (k & 7) * 16 : (uint32_t)((t >> 3) * 128 + (t & 7) * 16));
       float inv;
       const float s2 = pow2_of(most[n], inv);
-      if (lane < 8) reinterpret_cast<float*>(&sh.col[gt & 7][t])[values] = values ? (float)((int)(__float_as_uint(s2) >> 23) - 127) : s2;
+      if (lane < 8)
+        reinterpret_cast<float*>(&sh.col[gt & 7][t])[values] =
+            sick >> n & 1 ? NAN : values ? (float)((int)(__float_as_uint(s2) >> 23) - 127) : s2;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
@@ -696,6 +706,18 @@ struct Kernel {
         uint8_t* o = to + kg * (values ? 128 : TILE * 16);
         *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if (FULL) *reinterpret_cast<uint4*>(o + (values ? LO_V : LO_K)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    // A vector that is not finite counts as zero in the products, where rows that do not attend to it meet it too; those that do
+    // get NaN by its power of two.
+    if (__any_sync(FULL, sick != 0)) {
+#pragma unroll 1
+      for (int i = 0; i < 4 * ROUNDS; ++i) {
+        if (!(sick >> (i >> 2) & 1)) continue;
+        const int t = 8 * dw + r + 8 * N_DQ * (i >> 2), k = place_of(t), kg = 4 * (i & 3) + b;
+        uint8_t* o = plane + (values ? (k >> 3) * V_LEAD + (k & 7) * 16 + kg * 128 : (uint32_t)((t >> 3) * 128 + (t & 7) * 16) + kg * (TILE * 16));
+        *reinterpret_cast<uint4*>(o) = make_uint4(0u, 0u, 0u, 0u);
+        if (FULL) *reinterpret_cast<uint4*>(o + (values ? LO_V : LO_K)) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     return true;

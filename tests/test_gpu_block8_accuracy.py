@@ -168,3 +168,58 @@ def test_values_of_zero_and_then_not():
     out = _prefill(gpu, ref, k, v, q, 0)
     assert (out[:, :, :320] == 0).all()
     _check(out, ref, 0, harness.to_np(q), 0, [320, 321, 352, 383, 384, 499])
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["nan value", "inf value", "nan key", "-inf key"])
+@pytest.mark.parametrize("p", [0, 77])
+def test_what_is_not_finite_spoils_who_attends_to_it(in_dtype, what, p):
+    """A token of the chunk that is not finite makes NaN of its own query and the later ones, and nothing of the earlier ones."""
+    rng = np.random.default_rng(45)
+    T, at = 60, 21
+    k, v, q = (_to(_normal(rng, h, T), in_dtype).cuda() for h in (2, 2, 8))
+    old = [_to(_normal(rng, 2, max(p, 1)), in_dtype).cuda() for _ in range(2)]
+    outs = []
+    for sick in (False, True):
+        gpu, _ = br.make(1, 2, 8, 1, 300, window=64, in_dtype=in_dtype)
+        if p:
+            gpu.append(0, old[0], old[1], _i32([0]))
+        kk, vv = k.clone(), v.clone()
+        if sick:
+            (vv if "value" in what else kk)[0, 1, at, 5] = float(what.split()[0])
+        outs.append(gpu.prefill(0, kk, vv, q, _i32([p])))
+    good, out = outs
+    assert torch.isfinite(good).all()
+    assert torch.equal(out[:, :4], good[:, :4]) and torch.equal(out[:, 4:, :at], good[:, 4:, :at])
+    assert torch.isnan(out[:, 4:, at:]).all()
+
+
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_an_earlier_token_that_is_not_finite(in_dtype):
+    """... and one of an earlier call, of the queries whose window has left it: its block is what the append made of it."""
+    rng = np.random.default_rng(46)
+    W, p, T, at = 32, 90, 30, 65
+    k, v, q = (_to(_normal(rng, h, T), in_dtype).cuda() for h in (1, 1, 4))
+    old = [_to(_normal(rng, 1, p), in_dtype).cuda() for _ in range(2)]
+    outs = []
+    for sick in (False, True):
+        gpu, _ = br.make(1, 1, 4, 1, 300, window=W, in_dtype=in_dtype)
+        gpu.append(0, old[0], old[1], _i32([0]))
+        if sick:
+            _slots(gpu)[1][0, 0, 0, at % W, 9] = float("nan")     # (only the ring's copy)
+        outs.append(gpu.prefill(0, k, v, q, _i32([p])))
+    good, out = outs
+    last = at + W - 1 - p                                          # the last query that attends to it raw
+    assert torch.isnan(out[:, :, :last + 1]).all() and torch.isfinite(out[:, :, last + 1:]).all()
+    assert torch.isfinite(good).all()
+
+
+def _slots(gpu):
+    """The rings of keys and values, [layers][batch][heads][window][128] each."""
+    cfg = gpu.cfg
+    a = lambda x: -(-x // 256) * 256  # noqa: E731
+    n = cfg.n_layers * cfg.max_batch * cfg.n_kv_heads * cfg.window * 512
+    n_pages = cfg.n_pages or cfg.max_batch * -(-cfg.max_seq_len // 64)
+    v0 = br.lib.kv_cache_bytes(cfg) - a(cfg.n_layers * n_pages * cfg.n_kv_heads * 16416) - a(n)
+    shape = (cfg.n_layers, cfg.max_batch, cfg.n_kv_heads, cfg.window, 128)
+    return [gpu.buffer[o:o + n].view(torch.float32).view(shape) for o in (v0 - a(n), v0)]
