@@ -297,7 +297,8 @@ int kv_decode_attention_noalloc(kvq_cache* cache, int32_t layer, const void* q, 
  *              KVQ_Q8B32 partial results behind it (about 20 MB)
  * Three launches on ``stream``: the ring copy, the append, the attention (tensor-core logits and
  * P.V over tiles of 32 positions, 64 (query, head) rows per block).  KVQ_Q8B32: four; tiles of 64 positions, 128 rows,
- * divided evenly over the device, and a launch that joins the rows that were divided.
+ * divided evenly over the device, and a launch that joins the rows that were divided; a token that is not finite makes
+ * NaN of the outputs of the queries that attend to it raw, and of no others.
  */
 size_t kv_prefill_scratch_bytes(const kvq_cache* cache, int32_t layer, int32_t batch);
 int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
@@ -544,8 +545,8 @@ int kv_split_decode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream);
 
 /* The stall limit, in nanoseconds, of every later kv_decode_attention / _noalloc, kv_tree_attention and
- * kv_attention_weights call of this process: a serving loop can tighten the ~1 s default to detect a stalled call
- * sooner.  ns must lie in [1, 1e10], else KVQ_ERR_INVALID_ARG and the limit is unchanged.
+ * kv_attention_weights call of this process, and of kv_prefill_attention over KVQ_Q8B32 caches: a serving loop can
+ * tighten the ~1 s default to detect a stalled call sooner.  ns must lie in [1, 1e10], else KVQ_ERR_INVALID_ARG and the limit is unchanged.
  *   decode    the copy pipeline's producer wait (a producer warp waiting for its consumers to release a stage): a
  *             producer whose wait runs out stops issuing copies and sets KVQ_DEV_TIMEOUT in the status word (the
  *             call's output is then incomplete); its consumers give up on the stages that never come after their
@@ -554,7 +555,9 @@ int kv_status(kvq_cache* cache, uint32_t* flags, void* stream);
  *             to ~1 s) for its copies and products under way and leaves; the rows that it had a part of are NaN
  *   weights   the same; the units (layer, sequence, kv-head) that it had a part of take no weight from the call:
  *             their entries are the old ones, times decay or not
- * The prefill and append kernels keep their own ~1 s limits.  A captured call keeps the limit of its capture. */
+ *   prefill   (KVQ_Q8B32) as for trees: the rows that the block had a part of, or would have come to, are NaN.  The
+ *             chunk is appended all the same
+ * The prefill of the other formats and the append kernels keep their own ~1 s limits.  A captured call keeps the limit of its capture. */
 int kv_set_wait_limit_ns(uint64_t ns);
 
 /* Static string for a KVQ_* status code. */

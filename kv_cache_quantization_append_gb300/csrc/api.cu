@@ -181,7 +181,7 @@ static int check_device(const kvq_cache* c) {
   return dev == c->device ? KVQ_OK : KVQ_ERR_INVALID_ARG;
 }
 
-// give-up limit of the decode pipeline's, the tree's and the weights' waits (kv_set_wait_limit_ns)
+// give-up limit of the waits of the decode's pipeline, the trees, the weights and the prefill over 8-bit blocks (kv_set_wait_limit_ns)
 std::atomic<unsigned long long> g_decode_wait_ns{1000000000ull};
 unsigned long long decode_wait_ns() { return g_decode_wait_ns.load(); }
 
@@ -430,6 +430,7 @@ int kv_prefill_attention(kvq_cache* cache, int32_t layer, const void* k, const v
   a.snap_v = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + snap);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + 2 * snap);
   a.sms = cache->cfg.k_format == KVQ_Q8B32 ? decode_ctas(cache->device) : 0;
+  a.wait_ns = decode_wait_ns();
   a.layer0 = l0;
   a.n_layers_call = nl;
   a.batch = batch;

@@ -146,6 +146,7 @@ struct PrefillArgs {
   int2* keys;        // behind them: (unit, row tile) of each; -1: there is none
   int* taken;        // behind these: row tiles that CTAs have taken whole, past the first of each; cleared with the ring's copy
   int sms;
+  unsigned long long wait_ns;  // KVQ_Q8B32: give-up limit of the waits within a CTA
 };
 size_t prefill_scratch_bytes(int n_layers_call, int batch, int Hkv, int W);
 cudaError_t launch_prefill(const PrefillArgs& a, const AppendArgs& app, cudaStream_t s);

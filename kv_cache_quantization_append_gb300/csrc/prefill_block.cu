@@ -29,7 +29,8 @@
 //    for all rows, lost an early row whose chunk had values 2^40 times larger further on.)
 //  * A kernel's small first-level cache (shared memory takes the rest) makes spilled registers and code that is run once dear: values
 //    for one phase are computed in it (once()), what a row tile does once is done by one group of warps.
-//  * Every wait is bounded; one that runs out flags the status word and the CTA leaves as a whole.
+//  * Every wait is bounded (kv_set_wait_limit_ns); one that runs out flags the status word, and the CTA makes NaN of the row
+//    tiles, or parts of them, that it is at and that it would have come to.
 //
 // One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 435 us (two passes of the products over recorded
 // positions at the measured bf16 rate: 204 us, 47 %), a prompt of 2048 tokens of 32 heads 154 us, three float turns of 37
@@ -74,7 +75,6 @@ static_assert(ROWS * Q_STRIDE <= NS * STAGE && ROWS * O_STRIDE <= NS * STAGE, "w
 // References are whole numbers: a factor between two of them is exact.  One is set BOOST to BOOST + 1 below the largest exponent
 // so far and follows when that is RAISE_AT further up: weights stay below 2^15.
 constexpr float BOOST = 4.f, RAISE_AT = 10.f;
-constexpr unsigned long long WAIT_NS = 1000000000ull;
 constexpr int REC = ROWS * D + 3 * ROWS;  // floats of a partial result: O, its reference, l, its reference
 
 // Along K, channels (keys) and positions of a tile (values) stand in the order in which 16-byte chunks hold their codes: which
@@ -185,16 +185,19 @@ __device__ __forceinline__ float max3nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// A warp's bounded wait.  false: this CTA gives up (a wait elsewhere ran out, or this one: flagged).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gone, unsigned* status) {
-  bool ok = bar_try(bar, parity);
+// A warp's bounded wait, of about `limit` ns at most.  false: this CTA gives up (a wait elsewhere ran out, or this one: flagged).
+// NAP false: looks without sleeping, for limits that a single sleep might pass.  (Sleeps of a given length, or a choice between the
+// two in every wait, cost 1024 tokens at 15001 positions 7 to 40 us of 438.)
+template <bool NAP = true>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* gone, unsigned* status, unsigned long long limit) {
+  bool ok = NAP ? bar_try(bar, parity) : bar_test(bar, parity);
   if (__builtin_expect(!ok, 0)) {
     const unsigned long long t0 = gtimer();
     while (true) {
 #pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = bar_try(bar, parity);
+      for (int i = 0; i < (NAP ? 64 : 1) && !ok; ++i) ok = NAP ? bar_try(bar, parity) : bar_test(bar, parity);
       if (ok || *gone) break;
-      if (gtimer() - t0 > WAIT_NS) {
+      if (gtimer() - t0 > limit) {
         atomicOr(status, KVQ_DEV_TIMEOUT);
         *gone = 1;
         break;
@@ -211,9 +214,9 @@ __device__ __forceinline__ float quad_max(const float (&x)[32]) {
   m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
   return fmaxf(m, __shfl_xor_sync(FULL, m, 2));
 }
-// log2 of a scale, its fraction to 2^-22 whatever its size; -inf of zero
+// log2 of a finite scale, its fraction to 2^-22 whatever its size; -inf of zero
 __device__ __forceinline__ float log2_of(float x) {
-  if (!(x > 0.f) || x == INFINITY) return x > 0.f ? x : x == 0.f ? -INFINITY : x;
+  if (!(x > 0.f)) return -INFINITY;
   int e = 0;
   if (x < FLT_MIN) {
     x *= 0x1p24f;
@@ -293,7 +296,7 @@ struct Kernel {
     lane = tid & 31;
     tmem = *const_cast<volatile uint32_t*>(&s.tmem);
   }
-  __device__ __forceinline__ bool held(uint64_t* bar, uint32_t parity) { return wait(bar, parity, &sh.gone, a.p.status); }
+  __device__ __forceinline__ bool held(uint64_t* bar, uint32_t parity) { return wait(bar, parity, &sh.gone, a.p.status, a.wait_ns); }
   __device__ __forceinline__ void sync_all() { part_sync(1, THREADS); }
 
   __device__ __forceinline__ List list() const {
@@ -564,8 +567,9 @@ struct Kernel {
       if (!held(&sh.rfull[rs], (gr / RS) & 1)) return;
       if (gt >= NS && !held(&sh.kempty[s], before)) return;
       if (dw == 0 && lane < 2) {
-        const float2 d = lane < sh.halves[rs] ? *reinterpret_cast<const float2*>(smem + PAGE_OFF + rs * PAGE_SLOT + lane * (PAGE_SLOT / 2) + 8192)
+        float2 d = lane < sh.halves[rs] ? *reinterpret_cast<const float2*>(smem + PAGE_OFF + rs * PAGE_SLOT + lane * (PAGE_SLOT / 2) + 8192)
                                               : make_float2(0.f, 0.f);
+        if (!(d.y < INFINITY)) d = make_float2(NAN, 1.f);  // (as for raw values that are not finite)
         const float e = log2_of(d.y);
         sh.blk[gt & 7][lane] = make_float4(d.x, e, d.x, e);
       }
@@ -692,9 +696,12 @@ struct Kernel {
       uint8_t* to = plane + (values ? (k >> 3) * V_LEAD + (k & 7) * 16 : (uint32_t)((t >> 3) * 128 + (t & 7) * 16));
       float inv;
       const float s2 = pow2_of(most[n], inv);
-      if (lane < 8)
-        reinterpret_cast<float*>(&sh.col[gt & 7][t])[values] =
-            sick >> n & 1 ? NAN : values ? (float)((int)(__float_as_uint(s2) >> 23) - 127) : s2;
+      if (lane < 8) {
+        float* col = reinterpret_cast<float*>(&sh.col[gt & 7][t]);
+        if (!values) col[0] = s2;
+        else col[1] = (float)((int)(__float_as_uint(s2) >> 23) - 127);
+        if (sick >> n & 1) col[0] = NAN;
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float x[8];
@@ -709,7 +716,7 @@ struct Kernel {
       }
     }
     // A vector that is not finite counts as zero in the products, where rows that do not attend to it meet it too; those that do
-    // get NaN by its power of two.
+    // get NaN by the keys' power of two.
     if (__any_sync(FULL, sick != 0)) {
 #pragma unroll 1
       for (int i = 0; i < 4 * ROUNDS; ++i) {
@@ -1016,11 +1023,13 @@ struct Kernel {
     for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     sh.M[row] = M;
   }
-  // rows to the output, or to a partial result: lane i & 15 knows of the warp's i-th row, then all write each row
+  // rows to the output, or to a partial result: lane i & 15 knows of the warp's i-th row, then all write each row.  NaN where the CTA
+  // has given up.
   __device__ void rows_out(const Stretch& u) {
     static_assert(ROWS == 16 * N_SOFT, "");
     const int g = a.g, nrows = u.tl.nq * g, lane = once(this->lane), warp = once(this->warp), row = warp + N_SOFT * (lane & 15);
     float* dst = a.parts + (size_t)max(u.rec, 0) * REC;
+    const bool gone = sh.gone;
     float f = 0.f;
     if (row < nrows) {
       const float M = sh.M[row], m0 = sh.m[0][row], m1 = sh.m[1][row];
@@ -1039,6 +1048,7 @@ struct Kernel {
         f = share_of(M - m, l);
         dst = a.out + (((size_t)u.unit * g + row % g) * a.T + u.tl.t0 + row / g) * D;
       }
+      if (gone) f = NAN;
     }
 #pragma unroll 4
     for (int i = 0; i < 16; ++i) {
@@ -1077,25 +1087,30 @@ struct Kernel {
     for (int k = 0;; ++k) {
       const Stretch& u = sh.at[k & 1];
       if (u.tb < 0) return;
-      if (ROLE == SOFTMAX) queries(u);
-      sync_all();
-      if (ROLE == SOFTMAX) queries_to_tmem();
-      if (k == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the call's tokens are appended, older ones copied
-      fence_before();
-      sync_all();
-      fence_after();
-      if (ROLE == SOFTMAX) softmax(u);
-      if (ROLE == SUMS) sums(u);
-      if (ROLE == OPERANDS) operands(u);
-      if (ROLE == LOGITS) issue_logits(u);
-      if (ROLE == VALUES) issue_values(u);
-      if (ROLE == PAGES) fetch(u);
+      // (all threads agree: a wait that sets it is behind the barrier that all come to next)
+      if (!*const_cast<volatile int*>(&sh.gone)) {
+        if (ROLE == SOFTMAX) queries(u);
+        sync_all();
+        if (ROLE == SOFTMAX) queries_to_tmem();
+        if (k == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the call's tokens are appended, older ones copied
+        fence_before();
+        sync_all();
+        fence_after();
+        if (ROLE == SOFTMAX) softmax(u);
+        if (ROLE == SUMS) sums(u);
+        if (ROLE == OPERANDS) operands(u);
+        if (ROLE == LOGITS) issue_logits(u);
+        if (ROLE == VALUES) issue_values(u);
+        if (ROLE == PAGES) fetch(u);
+        // (the warp that has time keeps a limit below a sleep, with the stretch's first product)
+        if (ROLE == AHEAD && a.wait_ns < NAP_NS) wait<false>(&sh.sfull[gt & 1], (gt >> 1) & 1, &sh.gone, a.p.status, a.wait_ns);
+        if (ROLE == AHEAD) gt += u.tb - u.ta;
+      }
       if (ROLE == AHEAD && lane == 0) {
         if (sh.whole) grab(-1, sh.at[(k + 1) & 1]);
         else follow_up(u, sh.at[(k + 1) & 1]);
       }
       sync_all();
-      if (sh.gone) return;
       if (ROLE == SOFTMAX) rows_out(u);
       sync_all();
     }
