@@ -476,7 +476,10 @@ int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq
  *                Anything else: flagged KVQ_DEV_BAD_PARENT, stays as it is
  *   seq_lens     device int32 [batch] (out of range: flagged KVQ_DEV_SEQLEN_RANGE, treated as 0)
  *   new_lens     device int32 [batch] (out): seq_lens[parents[b]]; must not overlap parents or seq_lens
- * Tokens appended next go to pages of the sequence's own once kv_pool_reserve has been called for them.
+ * Tokens appended next go to pages of the sequence's own once kv_pool_reserve has been called for them.  Where a wait
+ * for a ring's copy runs out (flagged KVQ_DEV_TIMEOUT, kv_set_wait_limit_ns), the table, the counts and new_lens are those
+ * of the whole fork, but the rings of the sequences that change hold their old and their parents' vectors in parts: such a
+ * sequence can only be released, or forked again from one that stayed as it is.
  *
  * kv_pool_release: give back the pages of each sequence that hold none of its first keep_lens[b] tokens (0: all of
  * them; < 0: none).
@@ -545,7 +548,7 @@ int kv_split_decode(int32_t hi_bits, uint64_t seed, const int16_t* outliers, int
 int kv_status(kvq_cache* cache, uint32_t* flags, void* stream);
 
 /* The stall limit, in nanoseconds, of every later kv_decode_attention / _noalloc, kv_tree_attention and
- * kv_attention_weights call of this process, and of kv_prefill_attention over KVQ_Q8B32 caches: a serving loop can
+ * kv_attention_weights call of this process, of kv_prefill_attention over KVQ_Q8B32 caches and of kv_pool_fork: a serving loop can
  * tighten the ~1 s default to detect a stalled call sooner.  ns must lie in [1, 1e10], else KVQ_ERR_INVALID_ARG and the limit is unchanged.
  *   decode    the copy pipeline's producer wait (a producer warp waiting for its consumers to release a stage): a
  *             producer whose wait runs out stops issuing copies and sets KVQ_DEV_TIMEOUT in the status word (the
@@ -557,6 +560,7 @@ int kv_status(kvq_cache* cache, uint32_t* flags, void* stream);
  *             their entries are the old ones, times decay or not
  *   prefill   (KVQ_Q8B32) as for trees: the rows that the block had a part of, or would have come to, are NaN.  The
  *             chunk is appended all the same
+ *   fork      a block's wait for the rings that it copies: one that runs out leaves the rest of its copies undone
  * The prefill of the other formats and the append kernels keep their own ~1 s limits.  A captured call keeps the limit of its capture. */
 int kv_set_wait_limit_ns(uint64_t ns);
 

@@ -181,7 +181,7 @@ static int check_device(const kvq_cache* c) {
   return dev == c->device ? KVQ_OK : KVQ_ERR_INVALID_ARG;
 }
 
-// give-up limit of the waits of the decode's pipeline, the trees, the weights and the prefill over 8-bit blocks (kv_set_wait_limit_ns)
+// give-up limit of the waits of the decode's pipeline, the trees, the weights, the prefill over 8-bit blocks and the forks (kv_set_wait_limit_ns)
 std::atomic<unsigned long long> g_decode_wait_ns{1000000000ull};
 unsigned long long decode_wait_ns() { return g_decode_wait_ns.load(); }
 
@@ -695,6 +695,7 @@ int kv_pool_fork(kvq_cache* cache, void* pool, size_t pool_bytes, const int32_t*
   a.pos = parents;
   a.counts = seq_lens;
   a.out = new_lens;
+  a.wait_ns = decode_wait_ns();
   a.batch = batch;
   return call_status(launch_pool_fork(a, static_cast<cudaStream_t>(stream)));
 }

@@ -207,6 +207,7 @@ struct PoolArgs {
   int32_t* out;           // reserve: positions granted; fork: new lengths; compact: pages in use
   int n_layers, max_batch, Hkv, W, max_seq_len, batch, n_tokens;
   int fork_smem;  // bytes of a fork block's stages
+  unsigned long long wait_ns;  // fork: give-up limit of a wait for the parents' slices
 };
 size_t pool_layout(void* pool, int n_pages, PoolArgs* a);  // the buffer's parts, where there is one; its bytes
 cudaError_t launch_pool_init(const PoolArgs& a, cudaStream_t s);

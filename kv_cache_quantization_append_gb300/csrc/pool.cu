@@ -377,7 +377,7 @@ __device__ void fork_rings(const PoolArgs& a, uint8_t* smem, int cta, int ctas) 
   int done = 0;
   for (long long task = cta; task < tasks; task += ctas, ++done) {
     const int st = done % n_stages;
-    tc::bar_wait(&full[st], (done / n_stages) & 1, &gone, a.p.status, tc::LAND_NS);
+    tc::bar_wait(&full[st], (done / n_stages) & 1, &gone, a.p.status, a.wait_ns);
     if (__any_sync(FULL, *const_cast<volatile int*>(&gone))) break;
     int off;
     uint8_t* base = place(task, off);
