@@ -90,3 +90,12 @@ def test_nothing_to_do(walk):
     assert len(out) == 0 and parts == 0
     out, _, parts = walk([100], 5, 2, 4, max_seq_len=104)
     assert len(out) == 0 and parts == 0
+
+
+def test_one_long_sequence_among_many(walk):
+    """Row tiles that are many are taken whole, but for one so long that its CTA would end after all others."""
+    for far, whole in ((0, True), (20000, True), (100000, False)):
+        for s in (0, 37, 63):
+            pos = [0] * 64
+            pos[s] = far
+            assert _check(walk, pos, 256, 4, 8, 128, True) == whole
