@@ -482,7 +482,9 @@ int kv_evict(kvq_cache* cache, int32_t layer, float* weights, const int32_t* seq
  * sequence can only be released, or forked again from one that stayed as it is.
  *
  * kv_pool_release: give back the pages of each sequence that hold none of its first keep_lens[b] tokens (0: all of
- * them; < 0: none).
+ * them; < 0: none).  This takes back what was reserved ahead, ends a sequence or follows an eviction; it does not take back
+ * tokens: the window ring goes on holding the newest ``window`` appended ones, so what is appended or decoded after a
+ * cut by n tokens finds n of the window's slots with later tokens in them.
  *   keep_lens    device int32 [batch]
  *
  * kv_pool_compact: move pages so that the U pages in use are pages 0 .. U - 1: the i-th page (in order) of those in use
