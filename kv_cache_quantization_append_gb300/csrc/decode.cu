@@ -1001,8 +1001,8 @@ struct Kernel {
     }
   }
 
-  // Q8B32: the reference stays 2^BOOST below the largest logit, so that the fp16 parts of weights keep their bits down
-  // to 2^-34 of the largest (weights up to 2^(BOOST + LAZY_RAISE) = 16384)
+  // Q8B32: the reference stays 2^BOOST below the largest logit (weights up to 2^(BOOST + LAZY_RAISE) = 16384): a weight's fp16
+  // parts have its 22 bits, or are within 2^-35 of the largest weight where it is small (half of fp16's smallest step)
   static constexpr float BOOST = QB ? 10.f : 0.f;
 
   __device__ void quant_step(uint8_t* stage, int ntok, QuantState& st) {

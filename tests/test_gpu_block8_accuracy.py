@@ -214,6 +214,21 @@ def test_an_earlier_token_that_is_not_finite(in_dtype):
     assert torch.isfinite(good).all()
 
 
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L,window", [(20, 32), (300, 100), (4000, 128)])
+def test_decode_row_by_row(in_dtype, L, window):
+    """Single tokens are held to the same bounds (the raw products are float sums of 128 and less: within them)."""
+    rng = np.random.default_rng(L)
+    gpu, ref = br.make(1, 2, 8, 2, L, window=window, in_dtype=in_dtype)
+    k, v = (_to(rng.standard_normal((2, 2, L, 128)), in_dtype) for _ in range(2))
+    gpu.append(0, k.cuda(), v.cuda(), _i32([0, 0]))
+    ref.append(0, harness.to_np(k), harness.to_np(v), [0, 0])
+    q = _to(3 * rng.standard_normal((2, 8, 128)), in_dtype)
+    out = gpu.decode(0, q.cuda(), _i32([L, L])).double().cpu().numpy()[:, :, None]
+    for b in range(2):
+        _check(out, ref, b, harness.to_np(q)[:, :, None], L - 1, [0], typical=2e-5)
+
+
 def _slots(gpu):
     """The rings of keys and values, [layers][batch][heads][window][128] each."""
     cfg = gpu.cfg
