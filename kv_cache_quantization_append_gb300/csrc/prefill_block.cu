@@ -32,10 +32,11 @@
 //  * Every wait is bounded (kv_set_wait_limit_ns); one that runs out flags the status word, and the CTA makes NaN of the row
 //    tiles, or parts of them, that it is at and that it would have come to.
 //
-// One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 435 us (two passes of the products over recorded
-// positions at the measured bf16 rate: 204 us, 47 %), a prompt of 2048 tokens of 32 heads 154 us, three float turns of 37
-// tokens of 8 heads at 1000 positions 35 us.  A tile of 64 positions takes 2300 cycles of which each of the products takes
-// 1100: bound by the weights (1500 cycles a tile and group of warps, two groups) and the rate at which instructions come.
+// One layer, bf16, window 128: 1024 tokens of 24 heads at position 15001 take 440 us (two passes of the products over recorded
+// positions at the measured bf16 rate: 204 us, 46 %), a prompt of 2048 tokens of 32 heads 164 us, three float turns of 37
+// tokens of 8 heads at 1000 positions 37 us.  A tile of 64 positions takes 2400 cycles of which both products would take 1024 (the
+// tensor pipe is busy 40 % of the time): bound by the weights (1500 cycles a tile and group of warps, two groups) and the rate at
+// which instructions come.
 #include <cfloat>
 
 #include "prefill_list.cuh"
@@ -759,7 +760,8 @@ struct Kernel {
     }
   }
   // ... of columns first .. last of any other tile of nt, whose scales of columns c, c + 1 are at[(c >> 5) half + (c / 2 mod 16) step]
-  __device__ __forceinline__ void top_of(uint32_t sa, const float4* at, int half, int step, int nt, float qs, int first, int last, float& mx, float& rx) {
+  __device__ __forceinline__ void top_of(uint32_t sa, const float4* at, int half, int step, int nt, float qs, int first, int last, float& mx,
+                                         float& rx) {
     mx = rx = -INFINITY;
 #pragma unroll 1
     for (int c0 = 0; c0 < nt; c0 += 32, at += half) {

@@ -172,9 +172,9 @@ struct List {
   // Whether CTAs take row tiles whole instead of equal stretches of the line, whose cuts cost most CTAs a row tile's fixed cost
   // more: when the sum of the longest of each round is below 1.15 of a share with that cost; where they are 16 a CTA or more, when
   // the longest of all (it may be taken last) is not above a share.  (far: the largest position.)
-  // Whole against cut: a prompt of 2048 tokens of 32 heads 152 against 209 us, 4096 tokens 400 / 498, 1024 tokens 78 / 98, 1500 of
-  // 24 heads 99 / 120; 2048 of 16 heads at position 6000 (256 long row tiles) 315 / 282, not taken.  64 prompts of 256 tokens 587 /
-  // 731, one of them at position 20000 1012 / 1057, at 60000 1701 / 1495 and at 100000 2380 / 1766, not taken.
+  // Whole against cut: a prompt of 2048 tokens of 32 heads 160 against 219 us, 4096 tokens 411 / 550, 1024 tokens 89 / 102, 1500 of
+  // 24 heads 110 / 129; 2048 of 16 heads at position 6000 (256 long row tiles) 322 / 304, not taken.  64 prompts of 256 tokens 585 /
+  // 737, one of them at position 20000 1012 / 1057, at 60000 1701 / 1495 and at 100000 2380 / 1766, not taken.
   KVQ_HD bool take_whole(int ctas, int far) const {
     const long long n = units(), each = (long long)n_act * HL, share = total() / ctas;
     if (n >= 16LL * ctas) return far + (long long)nx * qpt + K0 <= share;
