@@ -1,7 +1,7 @@
 """Prefill over KVQ_Q8B32 caches, row by row: what a query does not attend to, or hardly, costs its output no bits.
 
 The error of a row (one query of one head) is measured against S = sum_j p_j rms(v_j), p its weights: RMS over the 128
-channels, which a rotation keeps.  Bound, before any run, with A = max_j |q| |k_j| log2(e) / sqrt(128) over the attended j:
+channels, which a rotation keeps.  Bound, with A = max_j |q| |k_j| log2(e) / sqrt(128) over the attended j:
 
   a logit is off by A (2 * 2^-22 (operands of 22 bits) + 24 * 2^-23 (up to 24 truncated sums, each below A)) and by 2^-18
   (exponents of up to 64, rounded twice in float): dl; a weight by ln 2 dl, an average of values by twice that;
