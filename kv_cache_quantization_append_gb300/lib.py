@@ -575,7 +575,8 @@ def kv_status(cache: kvq_cache, stream=None) -> int:
 
 
 def kv_set_wait_limit_ns(ns: int) -> None:
-    """Stall limit (ns, 1..1e10) of later decode calls' producer waits; the default is 1e9."""
+    """Stall limit (ns, 1..1e10) of waits within later decode, tree, weights and fork calls and prefills over 8-bit blocks; the default
+    is 1e9 (see include/kvq.h)."""
     _check(load().kv_set_wait_limit_ns(int(ns)))
 
 
